@@ -343,6 +343,138 @@ O1_API int o1_set_wait_limit(int64_t cycles);
  * these sticky bits. */
 O1_API int o1_state_flags(void *state, const o1_geom *geom, uint32_t *flags, int32_t clear, void *stream);
 
+/* ------------------------------------------------------------------ heads
+ * What stands around a sealed layer in a hybrid model: the normalisation of
+ * query and key heads before attention, and the other attention with a state
+ * of constant size, linear attention with a decay per head. These entry
+ * points take rows of several element types and with a stride:
+ *  - a row tensor [rows][heads][width] has its heads and widths contiguous
+ *    and `*_stride` elements from one row to the next (a slice of a fused
+ *    projection's rows, say), heads * width <= stride, the base address and
+ *    the stride in bytes multiples of 16;
+ *  - weights, frequencies and decays are fp32;
+ *  - outputs may not overlap inputs except where stated (row tensors of the
+ *    same row stride whose columns are apart, as slices of one buffer, do not
+ *    overlap).
+ * Rows that an entry point is not told to compute are left as they were. */
+
+/* Element types of row tensors. */
+enum { O1_F32 = 0, O1_BF16 = 1, O1_F16 = 2 };
+
+/* Norms of o1_head_prep. */
+enum {
+    O1_NORM_NONE = 0,
+    O1_NORM_RMS = 1,   /* y = x / sqrt(mean(x^2) + eps) */
+    O1_NORM_UNIT = 2   /* y = x / sqrt(sum(x^2) + eps)  */
+};
+
+/* Limits: q_heads and k_heads in [0, 4096], at least one head; d in [8, 256]
+ * with d % 8 == 0; rot in [0, d] with rot % 8 == 0; eps finite, >= 0;
+ * out_dtype O1_F32 or equal to in_dtype. */
+typedef struct o1_prep_geom {
+    int32_t q_heads, k_heads;  /* heads of the two row tensors; 0 = absent     */
+    int32_t d;                 /* head width                                   */
+    int32_t rot;               /* leading values of a head that rotate         */
+    int32_t norm;              /* O1_NORM_*                                    */
+    int32_t in_dtype, out_dtype;
+    float eps;
+} o1_prep_geom;
+
+/* Norm of every query and key head and their rotation in one pass
+ * ("cortiq-engine 0.8.77 src/gpu_wgpu/dory.rs", dory_prep: rotate, unit-
+ * normalise each head, scale; here the norm comes first, as query / key norms
+ * of models in use do, and a per-value weight carries the scale). Per row r
+ * and head, x its d values:
+ *   y = norm(x) * weight            (weight NULL: 1; a zero head under
+ *                                    eps = 0 stays zero)
+ *   z_j          = y_j cos a - y_{j + rot/2} sin a,   a = p inv_freq[j],
+ *   z_{j + rot/2} = y_{j + rot/2} cos a + y_j sin a,  j < rot/2,
+ * and z = y past rot. p = pos[r], or pos0 + r when pos is NULL.
+ *   q, k           device row tensors [rows][q_heads][d], [rows][k_heads][d]
+ *   q_weight, k_weight  device [d] or NULL, 16-byte aligned
+ *   inv_freq       device [rot/2], 0 <= inv_freq < 2^24 (NULL if rot == 0)
+ *   pos            device int64 [rows] or NULL
+ *   q_out, k_out   device row tensors; either may be its own input exactly
+ *                  (same address, stride and type)
+ * Sums and the rotation are fp32; the angle is reduced exactly in fixed point
+ * (a turn is 2^64), so far positions keep fp32 accuracy. The sum of squares
+ * of a head must be finite in fp32. The result feeds o1_chunk_attend and its
+ * kin with rope_base = 0, or the linear layer. rows = 0 does nothing.
+ * Asynchronous; one launch. */
+O1_API int o1_head_prep(const o1_prep_geom *geom, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const float *q_weight, const float *k_weight, const float *inv_freq, const int64_t *pos,
+                        int64_t pos0, int32_t rows, void *q_out, int64_t q_out_stride, void *k_out,
+                        int64_t k_out_stride, void *stream);
+
+/* Geometry of a linear layer: limits groups in [1, 4096], heads_per_group in
+ * [1, 16], d and dv in [8, 256] with both % 8 == 0, scale finite. Heads of a
+ * group share its keys and values; each head has a decay and a state of its
+ * own. */
+typedef struct o1_lin_geom {
+    int32_t groups;           /* G: KV groups                                  */
+    int32_t heads_per_group;  /* query heads per group (nh = G * hpg)          */
+    int32_t d, dv;            /* key / query and value width                   */
+    int32_t dtype;            /* O1_F32, O1_BF16, O1_F16: q, k, v and out      */
+    float scale;              /* output scale, normally 1/sqrt(d)              */
+} o1_lin_geom;
+
+/* One sequence of a packed batch (host memory): rows row0 .. row0 + rows - 1
+ * of the row tensors, on state slot `slot`. */
+typedef struct o1_lin_seq {
+    int32_t row0, rows, slot;
+} o1_lin_seq;
+
+/* Bytes of `slots` states, fp32 [slots][nh][d][dv], 16-byte aligned, which
+ * the caller sets to zero (an empty sequence) or to any finite state before
+ * first use, copies and keeps as it likes: there is no header. 0 if the
+ * geometry is unsupported or slots < 1. Host-only. */
+O1_API size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots);
+
+/* Bytes of device scratch that lets o1_lin_chunk_attend run `rows` rows of at
+ * most `seqs` sequences in one pass. Any size from
+ * o1_lin_scratch_bytes(geom, 1, 1) on works: longer batches run as several
+ * passes. Host-only; 0 if unsupported or a count is below 1. */
+O1_API size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs);
+
+/* Linear attention with a decay per head over packed sequences: the state of
+ * each advanced past its rows. Per sequence, head h and row t,
+ *   S = e^{log_decay[h]} S + k_t v_t^T;   out_t = scale q_t S,
+ * up to rounding (the rows of a long sequence run in chunks: products inside
+ * a chunk, and one state a chunk). It is the chunk / one-row pair of a sealed
+ * layer ("cortiq-engine 0.8.51 src/gpu_wgpu/o1_batch.rs", module doc: a state
+ * of constant size, a chunk at once, the next chunk continuing from it) for
+ * the attention whose state is a plain sum; the pages have no such layer.
+ *   state      device fp32 [n_slots][nh][d][dv]
+ *   scratch    device, 256-byte aligned, see o1_lin_scratch_bytes
+ *   q, k, v    device row tensors [total_rows][nh][d], [..][G][d], [..][G][dv]
+ *   log_decay  device [nh], each in [-inf, 0] (0: no decay)
+ *   seqs       host [n_seq], read during the call; rows of a sequence may be
+ *              0; row ranges may not overlap, row0 + rows <= total_rows, and
+ *              slots are distinct and in [0, n_slots) (else O1_ERR_ARG)
+ *   out        device row tensor [total_rows][nh][dv]; rows of no sequence
+ *              are left as they were
+ * q, k, v and the state are finite; a non-finite value spoils rows of its own
+ * sequence only, from up to 127 rows before it. States and sums are fp32;
+ * operands of 16-bit and fp32 products alike are split into bf16 terms that
+ * hold them to fp32 accuracy in the state (to the output type's accuracy in
+ * the outputs). Asynchronous. */
+O1_API int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, void *scratch,
+                               size_t scratch_bytes, const void *q, int64_t q_stride, const void *k,
+                               int64_t k_stride, const void *v, int64_t v_stride, const float *log_decay,
+                               const o1_lin_seq *seqs, int32_t n_seq, void *out, int64_t out_stride,
+                               int32_t total_rows, void *stream);
+
+/* One row of each of `rows` sequences (a decode step of a batch): row r
+ * advances slot slots[r] (NULL: slot r) by the same recurrence. slots is a
+ * device array, so that a captured step can be replayed on other slots. A row
+ * whose slot is outside [0, n_slots) is padding: its output is left as it
+ * was. Of rows that name the same slot the first counts and the others are
+ * padding. No scratch; one launch; asynchronous. */
+O1_API int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, const void *q,
+                               int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                               const float *log_decay, const int32_t *slots, void *out, int64_t out_stride,
+                               int32_t rows, void *stream);
+
 /* A static, human-readable name for a status code. (The pages' geometry
  * gates refuse a shape instead of running it: "cortiq-engine 0.8.82
  * src/gpu_metal/o1c.rs", admits and tok_ok; this library returns

@@ -1,0 +1,37 @@
+// Internals of the linear layer (linear attention with a decay per head):
+// the argument block of its kernels and the launchers.
+#pragma once
+
+#include "o1_rows.cuh"
+
+// Sequences of one launch, passed by value.
+#define LIN_TABLE 128
+struct LinTable {
+    o1_lin_seq s[LIN_TABLE];
+};
+
+struct LinArgs {
+    float *state;              // [slots][nh][d][dv]
+    const void *q, *k, *v;
+    void *out;
+    size_t qs, ks, vs, os;     // row strides, elements
+    const float *decay;        // [nh] log decay
+    const int *slots;          // token batches: slot of each row, or null
+    int nslots, G, hpg, nh, d, dv;
+    float scale;
+    int cols;                  // value columns of a CTA of the row kernel (a power of two)
+};
+
+// e^{g n}, 1 at n = 0 whatever g (also -inf): the product g n keeps its
+// rounding error as a second term, so that the power of a slow decay over
+// many rows stays within a few roundings.
+__device__ __forceinline__ float lin_pow(float g, int n) {
+    if (n == 0) return 1.f;
+    const float fn = (float)n;                        // exact below 2^24
+    const float fl = (float)(n - (int)fn);
+    const float x = __fmul_rn(g, fn);
+    if (x <= -150.f) return 0.f;                      // below the smallest fp32 value
+    const float e = fmaf(g, fn, -x) + g * fl;
+    const float y = expf(x);
+    return fmaf(y, e, y);
+}

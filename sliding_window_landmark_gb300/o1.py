@@ -48,8 +48,28 @@ class o1_state_host(ctypes.Structure):
                 ("far_mass", ctypes.c_void_p), ("far_val", ctypes.c_void_p)]
 
 
+class o1_prep_geom(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("norm", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class o1_lin_geom(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("heads_per_group", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    @property
+    def nh(self) -> int:
+        return self.groups * self.heads_per_group
+
+
+class o1_lin_seq(ctypes.Structure):
+    _fields_ = [("row0", ctypes.c_int32), ("rows", ctypes.c_int32), ("slot", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _G = ctypes.POINTER(o1_geom)
+_LG = ctypes.POINTER(o1_lin_geom)
 
 
 def _load(path: str | None = None):
@@ -91,6 +111,19 @@ def _load(path: str | None = None):
     lib.o1_state_flags.restype = ctypes.c_int
     lib.o1_status_string.argtypes = [ctypes.c_int]
     lib.o1_status_string.restype = ctypes.c_char_p
+    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.o1_head_prep.argtypes = [ctypes.POINTER(o1_prep_geom), _VP, i64, _VP, i64, _VP, _VP, _VP, _VP, i64, i32, _VP,
+                                 i64, _VP, i64, _VP]
+    lib.o1_head_prep.restype = ctypes.c_int
+    lib.o1_lin_state_bytes.argtypes = [_LG, i32]
+    lib.o1_lin_state_bytes.restype = sz
+    lib.o1_lin_scratch_bytes.argtypes = [_LG, i32, i32]
+    lib.o1_lin_scratch_bytes.restype = sz
+    lib.o1_lin_chunk_attend.argtypes = [_VP, i32, _LG, _VP, sz, _VP, i64, _VP, i64, _VP, i64, _VP,
+                                        ctypes.POINTER(o1_lin_seq), i32, _VP, i64, i32, _VP]
+    lib.o1_lin_chunk_attend.restype = ctypes.c_int
+    lib.o1_lin_token_attend.argtypes = [_VP, i32, _LG, _VP, i64, _VP, i64, _VP, i64, _VP, _VP, _VP, i64, i32, _VP]
+    lib.o1_lin_token_attend.restype = ctypes.c_int
     lib.o1_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.o1_set_wait_limit.restype = ctypes.c_int
     return lib
@@ -319,6 +352,108 @@ def o1_state_flags(state, g: o1_geom, clear: bool = False, stream=None) -> int:
     check(LIB.o1_state_flags(_dev(state, o1_state_bytes(g), "state", dtype=None), ctypes.byref(g),
                              ctypes.byref(f), int(bool(clear)), _stream(stream)), "flags")
     return int(f.value)
+
+
+# Element types of row tensors (enum in include/o1.h).
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+NORMS = {"none": 0, "rms": 1, "unit": 2}
+
+
+def prep_geom(q_heads: int, k_heads: int, d: int, rot: int | None = None, norm: str = "rms",
+              in_dtype=torch.float32, out_dtype=None, eps: float = 1e-6) -> o1_prep_geom:
+    """An o1_prep_geom (rot defaults to d, out_dtype to in_dtype)."""
+    return o1_prep_geom(q_heads, k_heads, d, d if rot is None else rot, NORMS[norm], DTYPES[in_dtype],
+                        DTYPES[in_dtype if out_dtype is None else out_dtype], float(eps))
+
+
+def lin_geom(groups: int, heads_per_group: int, d: int, dv: int, dtype=torch.float32,
+             scale: float | None = None) -> o1_lin_geom:
+    """An o1_lin_geom (scale defaults to 1/sqrt(d), rounded to f32)."""
+    return o1_lin_geom(groups, heads_per_group, d, dv, DTYPES[dtype], float(1.0 / d ** 0.5 if scale is None else scale))
+
+
+def lin_seqs(seqs):
+    """(row0, rows, slot) triples as the array o1_lin_chunk_attend takes."""
+    return (o1_lin_seq * len(seqs))(*[tuple(int(x) for x in s) for s in seqs])
+
+
+def _here(t, name):
+    if t is not None and isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on device {t.device.index}, the current device is {torch.cuda.current_device()}")
+    return t
+
+
+def _rows(t, heads: int, width: int, dtype: int, rows: int, name: str):
+    """Pointer and row stride of a [rows, heads, width] CUDA tensor whose heads
+    and widths are contiguous (None where it has no heads -> NULL)."""
+    if t is None and heads == 0:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if DTYPES.get(t.dtype) != dtype:
+        raise TypeError(f"{name}: element type {t.dtype} is not the geometry's")
+    if tuple(t.shape) != (rows, heads, width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {(rows, heads, width)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != width)):
+        raise ValueError(f"{name}: heads and widths must be contiguous")
+    _here(t, name)
+    return _VP(t.data_ptr()), (t.stride(0) if rows > 1 else heads * width)
+
+
+def o1_head_prep(g: o1_prep_geom, q, k, q_weight, k_weight, inv_freq, q_out, k_out, pos=None, pos0: int = 0,
+                 stream=None) -> int:
+    """Per-head norm and rotation of q [rows, q_heads, d] and k [rows, k_heads,
+    d] into q_out and k_out (which may be q and k themselves)."""
+    rows = (q if g.q_heads else k).shape[0]
+    (qp, qs), (kp, ks) = _rows(q, g.q_heads, g.d, g.in_dtype, rows, "q"), _rows(k, g.k_heads, g.d, g.in_dtype, rows, "k")
+    (qo, qos), (ko, kos) = (_rows(q_out, g.q_heads, g.d, g.out_dtype, rows, "q_out"),
+                            _rows(k_out, g.k_heads, g.d, g.out_dtype, rows, "k_out"))
+    return LIB.o1_head_prep(
+        ctypes.byref(g), qp, qs, kp, ks, _dev(_here(q_weight, "q_weight"), g.d, "q_weight"),
+        _dev(_here(k_weight, "k_weight"), g.d, "k_weight"), _dev(_here(inv_freq, "inv_freq"), g.rot // 2, "inv_freq"),
+        _dev(_here(pos, "pos"), 2 * rows, "pos", dtype=torch.int64), int(pos0), rows, qo, qos, ko, kos, _stream(stream))
+
+
+def o1_lin_state_bytes(g: o1_lin_geom, slots: int) -> int:
+    return int(LIB.o1_lin_state_bytes(ctypes.byref(g), int(slots)))
+
+
+def o1_lin_scratch_bytes(g: o1_lin_geom, rows: int, seqs: int = 1) -> int:
+    return int(LIB.o1_lin_scratch_bytes(ctypes.byref(g), int(rows), int(seqs)))
+
+
+def _lin_state(state, g: o1_lin_geom):
+    """Pointer and slots of a linear layer's state [slots, nh, d, dv]."""
+    if not isinstance(state, torch.Tensor) or tuple(state.shape[1:]) != (g.nh, g.d, g.dv):
+        raise ValueError(f"state: need a [slots, {g.nh}, {g.d}, {g.dv}] tensor")
+    return _dev(_here(state, "state"), None, "state"), state.shape[0]
+
+
+def o1_lin_chunk_attend(state, g: o1_lin_geom, scratch, q, k, v, log_decay, seqs, out, stream=None) -> int:
+    """Linear attention over packed sequences; ``seqs``: (row0, rows, slot)
+    triples or what ``lin_seqs`` made of them."""
+    if not isinstance(seqs, ctypes.Array):
+        seqs = lin_seqs(seqs)
+    rows, nh = q.shape[0], g.nh
+    sp, slots = _lin_state(state, g)
+    (qp, qs), (kp, ks) = _rows(q, nh, g.d, g.dtype, rows, "q"), _rows(k, g.groups, g.d, g.dtype, rows, "k")
+    (vp, vs), (op, os_) = _rows(v, g.groups, g.dv, g.dtype, rows, "v"), _rows(out, nh, g.dv, g.dtype, rows, "out")
+    return LIB.o1_lin_chunk_attend(
+        sp, slots, ctypes.byref(g), _dev(_here(scratch, "scratch"), None, "scratch", dtype=None),
+        scratch.numel() * scratch.element_size(), qp, qs, kp, ks, vp, vs,
+        _dev(_here(log_decay, "log_decay"), nh, "log_decay"), seqs, len(seqs), op, os_, rows, _stream(stream))
+
+
+def o1_lin_token_attend(state, g: o1_lin_geom, q, k, v, log_decay, slots, out, stream=None) -> int:
+    """One row of each sequence: row r on state slot slots[r] (int32 tensor;
+    None: slot r; outside [0, slots): padding)."""
+    rows, nh = q.shape[0], g.nh
+    sp, n_slots = _lin_state(state, g)
+    (qp, qs), (kp, ks) = _rows(q, nh, g.d, g.dtype, rows, "q"), _rows(k, g.groups, g.d, g.dtype, rows, "k")
+    (vp, vs), (op, os_) = _rows(v, g.groups, g.dv, g.dtype, rows, "v"), _rows(out, nh, g.dv, g.dtype, rows, "out")
+    return LIB.o1_lin_token_attend(
+        sp, n_slots, ctypes.byref(g), qp, qs, kp, ks, vp, vs, _dev(_here(log_decay, "log_decay"), nh, "log_decay"),
+        _dev(_here(slots, "slots"), rows, "slots", dtype=torch.int32), op, os_, rows, _stream(stream))
 
 
 def empty_state_arrays(g: o1_geom) -> dict:
