@@ -407,7 +407,7 @@ O1_API int o1_head_prep(const o1_prep_geom *geom, const void *q, int64_t q_strid
                         int64_t k_out_stride, void *stream);
 
 /* Geometry of a linear layer: limits groups in [1, 4096], heads_per_group in
- * [1, 16], d and dv in [8, 256] with both % 8 == 0, scale finite. Heads of a
+ * [1, 16], at most 65535 heads, d and dv in [8, 256] with both % 8 == 0, scale finite. Heads of a
  * group share its keys and values; each head has a decay and a state of its
  * own. */
 typedef struct o1_lin_geom {
@@ -474,6 +474,13 @@ O1_API int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom 
                                int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                const float *log_decay, const int32_t *slots, void *out, int64_t out_stride,
                                int32_t rows, void *stream);
+
+/* Read the sticky flags that the chunk kernels of linear layers raised on the
+ * current device into *flags (host) and, if `clear` is non-zero, reset them:
+ * O1_FLAG_WAIT_EXPIRED (a bounded wait ran out, see o1_set_wait_limit; the
+ * outputs and states that the block was to write are NaN). The states have no
+ * header to hold them. Synchronises `stream`. */
+O1_API int o1_lin_flags(uint32_t *flags, int32_t clear, void *stream);
 
 /* A static, human-readable name for a status code. (The pages' geometry
  * gates refuse a shape instead of running it: "cortiq-engine 0.8.82

@@ -226,6 +226,8 @@ int noalloc_scratch(void **out) {
 
 }  // namespace
 
+long long o1_wait_limit() { return g_wait_cycles.load(std::memory_order_relaxed); }
+
 extern "C" {
 
 size_t o1_state_bytes(const o1_geom *geom) {

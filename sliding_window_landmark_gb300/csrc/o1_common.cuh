@@ -38,6 +38,8 @@
 // 2 s at the maximum SM clock). Drains of copies or MMAs already in flight
 // always use this limit; the first waits of a call use O1Args::wait_cycles.
 #define O1_WAIT_CYCLES_FULL 4000000000LL
+// The limit set by o1_set_wait_limit (o1_api.cu).
+long long o1_wait_limit();
 
 // First bytes of a state buffer.
 struct O1Header {

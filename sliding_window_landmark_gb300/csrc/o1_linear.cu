@@ -158,6 +158,7 @@ bool lin_geom_ok(const o1_lin_geom *g) {
     if (!g) return false;
     if (g->groups < 1 || g->groups > 4096) return false;
     if (g->heads_per_group < 1 || g->heads_per_group > O1_MAX_HPG) return false;
+    if (g->groups * g->heads_per_group > 65535) return false;   // heads are a grid's y
     if (g->d < 8 || g->d > O1_MAX_D || g->d % 8) return false;
     if (g->dv < 8 || g->dv > O1_MAX_DV || g->dv % 8) return false;
     return o1_dtype_ok(g->dtype) && isfinite(g->scale);
@@ -165,6 +166,20 @@ bool lin_geom_ok(const o1_lin_geom *g) {
 
 size_t slot_floats(const o1_lin_geom &g) {
     return (size_t)g.groups * g.heads_per_group * g.d * g.dv;
+}
+
+// Sequences of up to LIN_ROW_MAX rows take the row kernel, longer ones the
+// chunk kernels.
+constexpr int LIN_ROW_MAX = 32;
+// A pass's chunk states: written, read, rewritten and read again, so they are
+// kept to what stays in the L2.
+constexpr size_t LIN_PASS_BYTES = (size_t)64 << 20;
+
+// Chunk states of a pass that a scratch of `bytes` holds.
+size_t pass_chunks(const o1_lin_geom &g, size_t bytes) {
+    const size_t per = slot_floats(g) * 4;
+    const size_t lim = LIN_PASS_BYTES / per > 1 ? LIN_PASS_BYTES / per : 1, fit = bytes / per;
+    return fit < lim ? fit : lim;
 }
 
 // The sequences of a call: ranges and slots in bounds and apart. Sorted
@@ -230,7 +245,9 @@ size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots) {
 
 size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs) {
     if (!lin_geom_ok(geom) || rows < 1 || seqs < 1) return 0;
-    return 256;
+    const size_t per = slot_floats(*geom) * 4, most = (size_t)rows / LIN_CHUNK + (size_t)seqs;
+    const size_t lim = pass_chunks(*geom, SIZE_MAX);
+    return o1_al256((most < lim ? most : lim) * per);
 }
 
 int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, void *scratch, size_t scratch_bytes,
@@ -249,15 +266,39 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
                             total_rows, o1_span(scratch, scratch_bytes));
     if (rc != O1_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    LinTable t;
-    int n = 0;
+    a.wait_cycles = o1_wait_limit();
+    const int cap = (int)pass_chunks(g, scratch_bytes);
+    LinTable rows;
+    LinWorkTable work;
+    int n = 0, chunks = 0;
+    work.n = 0;
+    auto flush_rows = [&]() {
+        if (n) rows_launch(a, g.dtype, &rows, n, st);
+        n = 0;
+    };
+    auto flush_chunks = [&]() {
+        if (work.n) lin_launch_pass(a, g.dtype, work, chunks, (float *)scratch, st);
+        work.n = chunks = 0;
+    };
     for (int i = 0; i < n_seq; ++i) {
-        if (seqs[i].rows) t.s[n++] = seqs[i];
-        if (n == LIN_TABLE || (i == n_seq - 1 && n)) {
-            rows_launch(a, g.dtype, &t, n, st);
-            n = 0;
+        const o1_lin_seq &s = seqs[i];
+        if (s.rows == 0) continue;
+        if (s.rows <= LIN_ROW_MAX) {
+            rows.s[n++] = s;
+            if (n == LIN_TABLE) flush_rows();
+            continue;
+        }
+        for (int off = 0; off < s.rows;) {
+            if (chunks == cap || work.n == LIN_TABLE) flush_chunks();
+            const int64_t most = (int64_t)(cap - chunks) * LIN_CHUNK;
+            const int take = s.rows - off < most ? s.rows - off : (int)most;
+            work.w[work.n++] = {s.row0 + off, take, s.slot, chunks};
+            chunks += (take + LIN_CHUNK - 1) / LIN_CHUNK;
+            off += take;
         }
     }
+    flush_rows();
+    flush_chunks();
     return cudaGetLastError() == cudaSuccess ? O1_OK : O1_ERR_CUDA;
 }
 
@@ -276,6 +317,11 @@ int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     a.slots = slots;
     rows_launch(a, g.dtype, nullptr, rows, (cudaStream_t)stream);
     return cudaGetLastError() == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+}
+
+int o1_lin_flags(uint32_t *flags, int32_t clear, void *stream) {
+    if (!flags) return O1_ERR_ARG;
+    return lin_flags(flags, clear, (cudaStream_t)stream);
 }
 
 }  // extern "C"

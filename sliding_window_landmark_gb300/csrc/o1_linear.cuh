@@ -10,6 +10,17 @@ struct LinTable {
     o1_lin_seq s[LIN_TABLE];
 };
 
+// A piece of a sequence in a pass of the chunk kernels: its rows in chunks of
+// LIN_CHUNK, on the scratch's chunk states chunk0, chunk0 + 1, ...
+#define LIN_CHUNK 128
+struct LinWork {
+    int32_t row0, rows, slot, chunk0;
+};
+struct LinWorkTable {
+    int32_t n;
+    LinWork w[LIN_TABLE];
+};
+
 struct LinArgs {
     float *state;              // [slots][nh][d][dv]
     const void *q, *k, *v;
@@ -20,6 +31,7 @@ struct LinArgs {
     int nslots, G, hpg, nh, d, dv;
     float scale;
     int cols;                  // value columns of a CTA of the row kernel (a power of two)
+    long long wait_cycles;     // limit of the chunk kernels' waits (o1_set_wait_limit)
 };
 
 // e^{g n}, 1 at n = 0 whatever g (also -inf): the product g n keeps its
@@ -35,3 +47,11 @@ __device__ __forceinline__ float lin_pow(float g, int n) {
     const float y = expf(x);
     return fmaf(y, e, y);
 }
+
+// One pass of the chunk kernels (o1_linear_tc.cu) over the pieces of a table,
+// `chunks` chunks in all; inc: [chunks][nh][d][dv] fp32 scratch. Launches only.
+void lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int chunks, float *inc,
+                     cudaStream_t st);
+// Flags its kernels raised on the current device (O1_FLAG_WAIT_EXPIRED), and
+// their reset.
+int lin_flags(uint32_t *flags, int clear, cudaStream_t st);

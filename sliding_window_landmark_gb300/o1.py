@@ -124,6 +124,8 @@ def _load(path: str | None = None):
     lib.o1_lin_chunk_attend.restype = ctypes.c_int
     lib.o1_lin_token_attend.argtypes = [_VP, i32, _LG, _VP, i64, _VP, i64, _VP, i64, _VP, _VP, _VP, i64, i32, _VP]
     lib.o1_lin_token_attend.restype = ctypes.c_int
+    lib.o1_lin_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, _VP]
+    lib.o1_lin_flags.restype = ctypes.c_int
     lib.o1_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.o1_set_wait_limit.restype = ctypes.c_int
     return lib
@@ -454,6 +456,13 @@ def o1_lin_token_attend(state, g: o1_lin_geom, q, k, v, log_decay, slots, out, s
     return LIB.o1_lin_token_attend(
         sp, n_slots, ctypes.byref(g), qp, qs, kp, ks, vp, vs, _dev(_here(log_decay, "log_decay"), nh, "log_decay"),
         _dev(_here(slots, "slots"), rows, "slots", dtype=torch.int32), op, os_, rows, _stream(stream))
+
+
+def o1_lin_flags(clear: bool = False, stream=None) -> int:
+    """Sticky flags (O1_FLAG_*) of linear layers on the current device."""
+    f = ctypes.c_uint32(0)
+    check(LIB.o1_lin_flags(ctypes.byref(f), int(bool(clear)), _stream(stream)), "flags")
+    return int(f.value)
 
 
 def empty_state_arrays(g: o1_geom) -> dict:
