@@ -3,6 +3,7 @@
 //   S = e^{g_h} S + k_t v_t^T,   out_t = scale q_t S.
 #include <limits.h>
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -171,15 +172,20 @@ size_t slot_floats(const o1_lin_geom &g) {
 // Sequences of up to LIN_ROW_MAX rows take the row kernel, longer ones the
 // chunk kernels.
 constexpr int LIN_ROW_MAX = 32;
-// A pass's chunk states: written, read, rewritten and read again, so they are
+// A pass's states: written, read, rewritten and read again, so they are
 // kept to what stays in the L2.
 constexpr size_t LIN_PASS_BYTES = (size_t)64 << 20;
 
-// Chunk states of a pass that a scratch of `bytes` holds.
-size_t pass_chunks(const o1_lin_geom &g, size_t bytes) {
+// States of a pass that a scratch of `bytes` holds.
+size_t pass_states(const o1_lin_geom &g, size_t bytes) {
     const size_t per = slot_floats(g) * 4;
     const size_t lim = LIN_PASS_BYTES / per > 1 ? LIN_PASS_BYTES / per : 1, fit = bytes / per;
     return fit < lim ? fit : lim;
+}
+
+int seg_rows(const o1_lin_geom &g) {
+    const char *e = getenv("LIN_SEG");
+    return e ? atoi(e) : 256;
 }
 
 // The sequences of a call: ranges and slots in bounds and apart. Sorted
@@ -228,6 +234,7 @@ int lin_args(LinArgs &a, float *state, int32_t n_slots, const o1_lin_geom &g, co
     a.q = q; a.k = k; a.v = v; a.out = out;
     a.qs = (size_t)q_stride; a.ks = (size_t)k_stride; a.vs = (size_t)v_stride; a.os = (size_t)out_stride;
     a.decay = log_decay;
+    a.rows = rows;
     a.nslots = n_slots;
     a.G = g.groups; a.hpg = g.heads_per_group; a.nh = nh; a.d = g.d; a.dv = g.dv;
     a.scale = g.scale;
@@ -246,7 +253,7 @@ size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots) {
 size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs) {
     if (!lin_geom_ok(geom) || rows < 1 || seqs < 1) return 0;
     const size_t per = slot_floats(*geom) * 4, most = (size_t)rows / LIN_CHUNK + (size_t)seqs;
-    const size_t lim = pass_chunks(*geom, SIZE_MAX);
+    const size_t lim = pass_states(*geom, SIZE_MAX);
     return o1_al256((most < lim ? most : lim) * per);
 }
 
@@ -267,18 +274,20 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     if (rc != O1_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     a.wait_cycles = o1_wait_limit();
-    const int cap = (int)pass_chunks(g, scratch_bytes);
+    const int cap = (int)pass_states(g, scratch_bytes);
+    a.seg = seg_rows(g);
     LinTable rows;
     LinWorkTable work;
-    int n = 0, chunks = 0;
+    int n = 0, segs = 0, tiles = 0;
+    bool launched = true;
     work.n = 0;
     auto flush_rows = [&]() {
         if (n) rows_launch(a, g.dtype, &rows, n, st);
         n = 0;
     };
     auto flush_chunks = [&]() {
-        if (work.n) lin_launch_pass(a, g.dtype, work, chunks, (float *)scratch, st);
-        work.n = chunks = 0;
+        if (work.n && !lin_launch_pass(a, g.dtype, work, segs, tiles, (float *)scratch, st)) launched = false;
+        work.n = segs = tiles = 0;
     };
     for (int i = 0; i < n_seq; ++i) {
         const o1_lin_seq &s = seqs[i];
@@ -289,17 +298,18 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
             continue;
         }
         for (int off = 0; off < s.rows;) {
-            if (chunks == cap || work.n == LIN_TABLE) flush_chunks();
-            const int64_t most = (int64_t)(cap - chunks) * LIN_CHUNK;
+            if (segs == cap || work.n == LIN_TABLE) flush_chunks();
+            const int64_t most = (int64_t)(cap - segs) * a.seg;
             const int take = s.rows - off < most ? s.rows - off : (int)most;
-            work.w[work.n++] = {s.row0 + off, take, s.slot, chunks};
-            chunks += (take + LIN_CHUNK - 1) / LIN_CHUNK;
+            work.w[work.n++] = {s.row0 + off, take, s.slot, segs, tiles};
+            segs += (take + a.seg - 1) / a.seg;
+            tiles += (take + LIN_CHUNK - 1) / LIN_CHUNK;
             off += take;
         }
     }
     flush_rows();
     flush_chunks();
-    return cudaGetLastError() == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess && launched ? O1_OK : O1_ERR_CUDA;
 }
 
 int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, const void *q, int64_t q_stride,

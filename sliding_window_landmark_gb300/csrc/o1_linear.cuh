@@ -10,11 +10,15 @@ struct LinTable {
     o1_lin_seq s[LIN_TABLE];
 };
 
-// A piece of a sequence in a pass of the chunk kernels: its rows in chunks of
-// LIN_CHUNK, on the scratch's chunk states chunk0, chunk0 + 1, ...
+// Rows of a tile of the chunk kernels.
 #define LIN_CHUNK 128
+// CTAs of their persistent grids: one an SM.
+#define LIN_SMS 152
+// A piece of a sequence in a pass of the chunk kernels: its rows in segments
+// of LinArgs::seg (a multiple of LIN_CHUNK), on the scratch's states seg0,
+// seg0 + 1, ..., and in tiles tile0, tile0 + 1, ... of LIN_CHUNK rows.
 struct LinWork {
-    int32_t row0, rows, slot, chunk0;
+    int32_t row0, rows, slot, seg0, tile0;
 };
 struct LinWorkTable {
     int32_t n;
@@ -28,9 +32,11 @@ struct LinArgs {
     size_t qs, ks, vs, os;     // row strides, elements
     const float *decay;        // [nh] log decay
     const int *slots;          // token batches: slot of each row, or null
+    int rows;                  // of the row tensors
     int nslots, G, hpg, nh, d, dv;
     float scale;
     int cols;                  // value columns of a CTA of the row kernel (a power of two)
+    int seg;                   // rows of a segment of the chunk kernels
     long long wait_cycles;     // limit of the chunk kernels' waits (o1_set_wait_limit)
 };
 
@@ -49,8 +55,9 @@ __device__ __forceinline__ float lin_pow(float g, int n) {
 }
 
 // One pass of the chunk kernels (o1_linear_tc.cu) over the pieces of a table,
-// `chunks` chunks in all; inc: [chunks][nh][d][dv] fp32 scratch. Launches only.
-void lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int chunks, float *inc,
+// `segs` segments and `tiles` tiles in all; inc: [segs][nh][d][dv] fp32
+// scratch. Launches only; false where a tensor map cannot be made.
+bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, float *inc,
                      cudaStream_t st);
 // Flags its kernels raised on the current device (O1_FLAG_WAIT_EXPIRED), and
 // their reset.

@@ -39,176 +39,23 @@ static __device__ uint32_t lin_device_flags;
 
 namespace {
 
-constexpr int COLS = 128;   // columns of a panel: d or dv of one tile
+constexpr int TN = 128;   // columns of a tile of dv (and of d, for dS)
+constexpr int KV = 64;    // rows or columns of a staged panel's short side
+constexpr int PROD_WARPS = 8, PROD = 32 * PROD_WARPS;
+constexpr int LIST = 64;  // units of a CTA, decoded once at its start
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-struct Chunk {
-    int row0, nr;   // rows row0 .. row0 + nr - 1
-};
-__device__ __forceinline__ Chunk find_chunk(const LinWorkTable &t, int c) {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.w[mid].chunk0 <= c) lo = mid;
-        else hi = mid - 1;
-    }
-    const int off = (c - t.w[lo].chunk0) * LIN_CHUNK;
-    return {t.w[lo].row0 + off, min(LIN_CHUNK, t.w[lo].rows - off)};
-}
-
-// 8 consecutive values as loaded
-struct Raw32 {
-    float4 a, b;
-};
-template <typename T>
-struct RawOf {
-    using type = uint4;
-};
-template <>
-struct RawOf<float> {
-    using type = Raw32;
-};
-__device__ __forceinline__ void raw_zero(uint4 &r) { r = make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void raw_zero(Raw32 &r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
-__device__ __forceinline__ void raw_load(uint4 &r, const void *p) { r = *(const uint4 *)p; }
-__device__ __forceinline__ void raw_load(Raw32 &r, const void *p) {
-    r.a = ((const float4 *)p)[0];
-    r.b = ((const float4 *)p)[1];
-}
-__device__ __forceinline__ void raw_floats(const Raw32 &r, float (&x)[8], const float *) {
-    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-}
-__device__ __forceinline__ void raw_floats(const uint4 &r, float (&x)[8], const __nv_bfloat16 *) {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void raw_floats(const uint4 &r, float (&x)[8], const __half *) {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*(const __half2 *)&u[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
-// x[8] as NT bf16 terms, term t's 16 bytes at dst + t * panel
-template <int NT>
-__device__ __forceinline__ void store_terms(unsigned char *dst, size_t panel, float (&x)[8]) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *(const uint32_t *)&h;
-            if (t + 1 < NT) {
-                x[2 * i] -= __uint_as_float(w[i] << 16);
-                x[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
-            }
-        }
-        *(uint4 *)(dst + t * panel) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
-// Byte offset of the 8-column group cg of row r in a panel of `rows` rows.
-__device__ __forceinline__ uint32_t panel_off(int rows, int r, int cg) {
-    return (uint32_t)((cg >> 3) * rows * 128 + r * 128 + (((cg & 7) ^ (r & 7)) << 4));
-}
-
-// A tile of ROWS rows in flight from global memory to a panel: 8-column
-// groups in order along a row, NTHR threads. cgs: groups per row as a power of
-// two (8 or 16), so that narrow tiles keep all threads busy.
-template <typename T, int ROWS, int NTHR>
-struct Tile {
-    static constexpr int IT = ROWS * (COLS / 8) / NTHR;
-    typename RawOf<T>::type raw[IT];
-
-    // rows [0, nr) and columns [0, width) of src (row stride in values); the rest reads as zero
-    __device__ __forceinline__ void load(const T *src, size_t stride, int nr, int width, int cgs) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int item = threadIdx.x + NTHR * i, r = cgs == 8 ? item >> 3 : item >> 4, cg = item & (cgs - 1);
-            raw_zero(raw[i]);
-            if (r < min(nr, ROWS) && 8 * cg < width) raw_load(raw[i], src + (size_t)r * stride + 8 * cg);
-        }
-    }
-    // NT terms, each a panel of ROWS rows; w: weight of each row, or null
-    template <int NT>
-    __device__ __forceinline__ void store(unsigned char *dst, int cgs, const float *w) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int item = threadIdx.x + NTHR * i, r = cgs == 8 ? item >> 3 : item >> 4, cg = item & (cgs - 1);
-            if (r >= ROWS) break;
-            unsigned char *p = dst + panel_off(ROWS, r, cg);
-            put<NT>(p, raw[i], w ? w[r] : 1.f, w != nullptr);
-        }
-    }
-    template <int NT, typename R>
-    __device__ __forceinline__ void put(unsigned char *p, const R &r, float w, bool weighted) {
-        float x[8];
-        raw_floats(r, x, (const T *)nullptr);
-        if (weighted) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= w;
-        }
-        store_terms<NT>(p, (size_t)ROWS * COLS * 2, x);
-    }
-};
-
-// Waits of a block that moves in step: every thread polls; a wait that runs
-// out anywhere ends the block's work (uniformly) with the flag raised.
-struct Waits {
-    uint64_t *bar;
-    volatile int *abort;
-    long long limit;
-    uint32_t phase;   // completed phases of the one barrier, modulo 2
-    __device__ __forceinline__ bool wait() {
-        const bool ok = mbar_wait(bar, phase, abort, limit);
-        phase ^= 1;
-        return !__syncthreads_or(!ok);
-    }
-};
-
-// MMAs D[128][N] (+)= A B over `steps` steps of 16 of the contraction, for the
-// term pairs (ta, tb) with ta + tb <= MAXS, the smallest products first: an
-// accumulation is rounded at the size of the sum so far, so only the last
-// pair's steps round at the result's own size. A step moves `a_block` /
-// `b_block` or 32 bytes in a K-major panel, 16 rows in an MN-major one.
-template <int TA, int TB, int MAXS>
-__device__ __forceinline__ void issue(uint32_t d, uint32_t a, uint32_t a_panel, bool a_mn, uint32_t a_block, uint32_t b,
-                                      uint32_t b_panel, bool b_mn, uint32_t b_block, uint32_t id, int steps, bool acc) {
-#pragma unroll
-    for (int sum = MAXS; sum >= 0; --sum)
-#pragma unroll
-        for (int ta = 0; ta < TA; ++ta) {
-            const int tb = sum - ta;
-            if (tb < 0 || tb >= TB) continue;
-            for (int s = 0; s < steps; ++s) {
-                const uint32_t pa = a + ta * a_panel + (a_mn ? 2048u * s : (s >> 2) * a_block + 32u * (s & 3));
-                const uint32_t pb = b + tb * b_panel + (b_mn ? 2048u * s : (s >> 2) * b_block + 32u * (s & 3));
-                mma_ss(d, a_mn ? desc_sw128_mn(pa, a_block) : desc_sw128(pa),
-                       b_mn ? desc_sw128_mn(pb, b_block) : desc_sw128(pb), id, acc);
-                acc = true;
-            }
-        }
-}
-
-__device__ __forceinline__ void tmem_alloc(uint32_t *slot, int cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(slot)), "r"(cols)
+__device__ __forceinline__ void tmem_alloc512(uint32_t *slot) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_free(uint32_t addr, int cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+__device__ __forceinline__ void tmem_free512(uint32_t addr) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(512) : "memory");
 }
 
+// bf16 terms of the inputs (q, k, v) and of what is formed on the way (the
+// entering state, P).
 template <typename T>
 struct Terms {
     static constexpr int in = 1;    // bf16 terms of q, k, v
@@ -223,319 +70,1079 @@ struct Terms<float> {
     static constexpr int in = 3, mid = 3;
 };
 __host__ __device__ constexpr int max_sum(int a, int b) { return a > b ? a - 1 : b - 1; }
-
 __host__ __device__ inline int ceil16(int x) { return (x + 15) & ~15; }
+
+// ---------------------------------------------------------------- staging
+
+// 8 consecutive values of T as loaded: one 16-byte word, two for fp32.
+template <typename T>
+constexpr int WORDS = sizeof(T) == 4 ? 2 : 1;
+
+__device__ __forceinline__ void words_floats(const uint4 *r, float (&x)[8], const float *) {
+    const uint32_t u[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void words_floats(const uint4 *r, float (&x)[8], const __nv_bfloat16 *) {
+    const uint32_t u[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void words_floats(const uint4 *r, float (&x)[8], const __half *) {
+    const uint32_t u[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*(const __half2 *)&u[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+// x[2i], x[2i + 1] as bf16 pairs (the lower index in the low half), x left
+// with what the rounding dropped (exact)
+__device__ __forceinline__ uint32_t take_pair(float &x0, float &x1) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+    const uint32_t w = *(const uint32_t *)&h;
+    x0 -= __uint_as_float(w << 16);
+    x1 -= __uint_as_float(w & 0xffff0000u);
+    return w;
+}
+// x[8] as NT bf16 terms, term t's 16 bytes at dst + t * panel
+template <int NT>
+__device__ __forceinline__ void store_terms(unsigned char *dst, uint32_t panel, float (&x)[8]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = take_pair(x[2 * i], x[2 * i + 1]);
+        *(uint4 *)(dst + t * panel) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// A panel of bf16 in shared memory: `rows` rows in blocks of 64 columns
+// (rows * 128 bytes each), 128-byte swizzled. Byte offset of the 8-column
+// group cg of row r:
+__device__ __forceinline__ uint32_t panel_off(int rows, int r, int cg) {
+    return (uint32_t)((cg >> 3) * rows * 128 + r * 128 + (((cg & 7) ^ (r & 7)) << 4));
+}
+
+// What a producer stages into a slot of the ring: a panel of ROWS x COLS
+// values of a row tensor (rows past nr and columns past width read as zero),
+// as NT bf16 terms. Thread pt takes one 8-column group of every STEP-th row, so
+// that its addresses on both sides are one base and constant steps: a producer
+// has two warps a scheduler, and every dependent instruction shows.
+template <typename T, int ROWS, int COLS>
+struct Panel {
+    static constexpr int GPR = COLS / 8, STEP = PROD / GPR, IT = ROWS / STEP, W = WORDS<T>;
+    static_assert(ROWS % STEP == 0 && STEP % 8 == 0, "rows a thread");
+    static __device__ __forceinline__ uint32_t row(uint32_t pt) { return pt / GPR; }
+    static __device__ __forceinline__ uint32_t off(uint32_t pt) { return panel_off(ROWS, pt / GPR, pt % GPR); }
+    static __device__ __forceinline__ void load(uint4 *raw, const T *src, size_t stride, int nr, int width, uint32_t pt) {
+        const uint32_t r = pt / GPR, cg = pt % GPR;
+        const char *p = (const char *)(src + (size_t)r * stride + 8 * cg);
+        const size_t step = STEP * stride * sizeof(T);
+        nr = 8 * (int)cg < width ? nr - (int)r : 0;   // of this thread's rows
+#pragma unroll
+        for (int i = 0; i < IT; ++i, p += step)
+#pragma unroll
+            for (int j = 0; j < W; ++j) raw[i * W + j] = STEP * i < nr ? ((const uint4 *)p)[j] : make_uint4(0, 0, 0, 0);
+    }
+    // as they are (bf16 in one term); dst: the panel + off(pt)
+    static __device__ __forceinline__ void copy(const uint4 *raw, unsigned char *dst) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) *(uint4 *)(dst + i * STEP * 128) = raw[i];
+    }
+    // NT terms of w[i] * x, w the weights of this thread's rows
+    template <int NT>
+    static __device__ __forceinline__ void split(const uint4 *raw, unsigned char *dst, const float (&w)[IT]) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            float x[8];
+            words_floats(raw + i * W, x, (const T *)nullptr);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= w[i];
+            store_terms<NT>(dst + i * STEP * 128, ROWS * COLS * 2, x);
+        }
+    }
+    // NT terms of x
+    template <int NT>
+    static __device__ __forceinline__ void put(const uint4 *raw, unsigned char *dst) {
+        if constexpr (NT == 1) {
+            copy(raw, dst);
+        } else {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                float x[8];
+                words_floats(raw + i * W, x, (const T *)nullptr);
+                store_terms<NT>(dst + i * STEP * 128, ROWS * COLS * 2, x);
+            }
+        }
+    }
+};
+
+// MMAs over `steps` steps of 16 of the contraction for the term pairs
+// (ta, tb), ta + tb <= MAXS, into `d` for the pair (0, 0) and `dc` for the
+// others (dc may be d). An accumulation rounds at the size of the sum so far;
+// the corrections are 2^-8 of the whole, so that in an accumulator of their own
+// (where the result is fp32) they round at that much smaller a size. a, b:
+// descriptors (a: TMEM address where TS) of step 0 of term 0; AT, AS, BT, BS:
+// what a term and a step add. One thread issues, so a step is an addition or
+// two and the MMA: with descriptors built in place a step took 198 cycles.
+template <int TA, int TB, int MAXS, bool TS, int AT, int AS, int BT, int BS, typename A>
+__device__ __forceinline__ void issue(uint32_t d, uint32_t dc, uint32_t id, int steps, bool acc, A a, uint64_t b) {
+    bool accc = acc;
+#pragma unroll
+    for (int sum = MAXS; sum >= 0; --sum)
+#pragma unroll
+        for (int ta = 0; ta < TA; ++ta) {
+            const int tb = sum - ta;
+            if (tb < 0 || tb >= TB) continue;
+            const bool main = sum == 0 && dc != d;
+            const uint32_t dst = main ? d : dc;
+            auto one = [&](int s, uint32_t ac) {
+                if constexpr (TS) mma_ts(dst, a + (uint32_t)(ta * AT + s * AS), b + (uint64_t)(tb * BT + s * BS), id, ac);
+                else mma_ss(dst, a + (uint64_t)(ta * AT + s * AS), b + (uint64_t)(tb * BT + s * BS), id, ac);
+            };
+            one(0, main ? acc : accc);
+            if (!main) accc = true;
+            if (steps >= 4) {
+                one(1, 1u);
+                one(2, 1u);
+                one(3, 1u);
+                for (int s = 4; s < steps; ++s) one(s, 1u);
+            } else {
+                for (int s = 1; s < steps; ++s) one(s, 1u);
+            }
+        }
+}
+
+// A piece's rows: the table entry that owns index c of its numbering.
+template <typename F>
+__device__ __forceinline__ const LinWork &find_piece(const LinWorkTable &t, int c, F first) {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first(t.w[mid]) <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return t.w[lo];
+}
+
+// A warp's 32 x 32 block of TMEM values to memory rows: through shared memory
+// (36 floats a row), so that stores cover whole lines of a row.
+constexpr int STAGE_FLOATS = 32 * 36;
+template <typename T>
+__device__ __forceinline__ void store_block(float *stage, const float (&x)[32], T *dst, size_t stride, int nr, int width,
+                                            int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *(float4 *)(stage + lane * 36 + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    __syncwarp();
+    const int c = 4 * (lane & 7);
+    if (c < width) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            if (r < nr) o1_st4(dst + (size_t)r * stride + c, *(const float4 *)(stage + r * 36 + c));
+        }
+    }
+}
+
+// TMA warp, all lanes: `boxes` boxes of ROWS rows x 64 columns of a bf16 row
+// tensor into slot bytes dst (block after block), published on `full`. Rows
+// from nr on are another sequence's or padding: the MMAs take them up to the
+// next multiple of 16 under zero weights, which would still spread a NaN, so
+// where nr cuts a step of 16 the rows are zeroed after the copy has landed (the
+// slot is published then).
+template <int ROWS>
+__device__ __forceinline__ bool tma_rows(unsigned char *dst, const CUtensorMap *map, int col, int head, int row, int boxes,
+                                         int nr, uint64_t *full, uint64_t *tail, uint32_t &tail_phase, volatile int *abort,
+                                         long long limit, int lane) {
+    const bool cut = nr < ROWS && nr % 16;
+    uint64_t *bar = cut ? tail : full;
+    if (lane == 0) {
+        mbar_expect_tx(bar, boxes * ROWS * 128);
+        for (int i = 0; i < boxes; ++i) tma_3d(dst + i * ROWS * 128, map, col + 64 * i, head, row, bar);
+    }
+    __syncwarp();
+    if (!cut) return true;
+    // in flight: waited for with the full limit
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(tail, tail_phase, abort, O1_WAIT_CYCLES_FULL));
+    tail_phase ^= 1;
+    if (!ok) {
+        mbar_drain(tail, tail_phase ^ 1);
+        return false;
+    }
+    for (int i = lane; i < (ceil16(nr) - nr) * 8 * boxes; i += 32) {
+        const int r = nr + (i >> 3) % (ceil16(nr) - nr), b = (i >> 3) / (ceil16(nr) - nr);
+        *(uint4 *)(dst + b * ROWS * 128 + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
+    return true;
+}
 
 // ------------------------------------------------------------- increments
 
-constexpr int INC_ROWS = 64;   // keys staged at a time
-constexpr int INC_THREADS = 256;
-constexpr uint32_t INC_PANEL = INC_ROWS * COLS * 2, INC_BLOCK = INC_ROWS * 128;
+// One unit: dS[d0 .. +128][v0 .. +N] of (segment, head).
+struct IncUnit {
+    int row0, nr, seg, h, g, d0, v0;
+};
 
-template <typename T>
-constexpr size_t inc_smem() { return 1024 + (3 + Terms<T>::in) * (size_t)INC_PANEL; }
+// N columns of dv a unit: 256 for bf16 values (the weighted keys are then
+// staged once for all of dv), 128 where values take more terms.
+template <typename T, int N>
+struct IncCfg {
+    static constexpr int NT = Terms<T>::in;
+    static constexpr bool TMA = NT == 1;            // values by TMA, as they are
+    static constexpr int NB = N == 128 ? 2 : 1;     // accumulators: main and corrections, N columns each
+    static constexpr int KSLOT = 3 * KV * TN * 2, NK = 2;
+    static constexpr int VSLOT = NT * KV * N * 2, NV = NT == 3 ? 2 : 3;
+    static constexpr int THREADS = 32 * (4 + 2 + PROD_WARPS);
+    static constexpr size_t SMEM = 1024 + (size_t)NK * KSLOT + (size_t)NV * VSLOT + 4 * STAGE_FLOATS * 4;
+};
 
-// dS[d][dv] of one (chunk, head), a tile of 128 x 128 of it a CTA:
-// A = weighted keys (M = d), B = values (N = dv), both MN-major, contraction
-// over the keys, 64 staged at a time while the previous 64 multiply.
-template <typename T>
-__global__ __launch_bounds__(INC_THREADS, Terms<T>::in == 1 ? 3 : 2) void k_lin_inc(LinArgs a,
-                                                                                    const __grid_constant__ LinWorkTable t,
-                                                                                    float *inc) {
+// dS of every (segment, head): A = weighted keys (M = d), B = values (N = dv),
+// both MN-major, contraction over the rows, 64 of them a step. Persistent: a
+// CTA takes units in turn. Warps: 0-3 store a finished unit, 4 issues the
+// MMAs, 5 the values' TMA, 6-13 stage the weighted keys (and the values that
+// are split), running ahead over the rings.
+template <typename T, int N>
+__global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs a, const __grid_constant__ LinWorkTable t,
+                                                                      const __grid_constant__ CUtensorMap mv, int units,
+                                                                      float *inc) {
+    using C = IncCfg<T, N>;
+    constexpr int NT = C::NT, NK = C::NK, NV = C::NV;
     extern __shared__ unsigned char smraw[];
-    __shared__ uint64_t bar;
+    __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], done[2], freed[2], tail, fin;
     __shared__ uint32_t tslot;
-    __shared__ int abort;
-    __shared__ float pw[LIN_CHUNK];   // weight of each key
-    unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
-    unsigned char *sK = sm, *sV = sm + 3 * INC_PANEL;
-    constexpr int NT = Terms<T>::in;
+    __shared__ int abort_s;
+    __shared__ IncUnit list[LIST];
+    volatile int *abort = &abort_s;
+    unsigned char *sK = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023), *sV = sK + NK * C::KSLOT;
+    float *stage = (float *)(sV + NV * C::VSLOT);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c = blockIdx.x, h = blockIdx.y, g = h / a.hpg;
-    const int vt = (a.dv + COLS - 1) / COLS, d0 = (blockIdx.z / vt) * COLS, v0 = (blockIdx.z % vt) * COLS;
-    const int wd = min(COLS, a.d - d0), wv = min(COLS, a.dv - v0);
-    const int cgd = wd > 64 ? 16 : 8, cgv = wv > 64 ? 16 : 8;
-    const Chunk ch = find_chunk(t, c);
+    const int count = (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;   // <= LIST
     if (tid == 0) {
-        mbar_init(&bar, 1);
-        abort = 0;
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&kfull[i], PROD_WARPS);
+            mbar_init(&kempty[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&vfull[i], C::TMA ? 1 : PROD_WARPS);
+            mbar_init(&vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&freed[i], 4);
+        }
+        mbar_init(&tail, 1);
+        mbar_init(&fin, 1);
+        abort_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) tmem_alloc(&tslot, 128);
-    if (tid < LIN_CHUNK) pw[tid] = tid < ch.nr ? lin_pow(a.decay[h], ch.nr - 1 - tid) : 0.f;
+    if (warp == 0) tmem_alloc512(&tslot);
+    if (tid >= 64 && tid < 64 + count) {
+        const int vt = (a.dv + N - 1) / N, dt = (a.d + TN - 1) / TN;
+        int u = blockIdx.x + gridDim.x * (tid - 64);
+        IncUnit x;
+        x.v0 = (u % vt) * N;
+        u /= vt;
+        x.d0 = (u % dt) * TN;
+        u /= dt;
+        x.h = u % a.nh;
+        x.g = x.h / a.hpg;
+        x.seg = u / a.nh;
+        const LinWork &w = find_piece(t, x.seg, [](const LinWork &p) { return p.seg0; });
+        const int off = (x.seg - w.seg0) * a.seg;
+        x.row0 = w.row0 + off;
+        x.nr = min(a.seg, w.rows - off);
+        list[tid - 64] = x;
+    }
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = tslot;
-    Waits w{&bar, &abort, a.wait_cycles, 0};
-    const T *k = (const T *)a.k + (size_t)ch.row0 * a.ks + (size_t)g * a.d + d0;
-    const T *v = (const T *)a.v + (size_t)ch.row0 * a.vs + (size_t)g * a.dv + v0;
-    Tile<T, INC_ROWS, INC_THREADS> tk, tv;
-    tk.load(k, a.ks, ch.nr, wd, cgd);
-    tv.load(v, a.vs, ch.nr, wv, cgv);
-    bool ok = true;
-    for (int s = 0; s * INC_ROWS < ch.nr; ++s) {
-        if (s > 0) {
-            ok = w.wait();   // the panels are free
-            if (!ok) break;
-        }
-        tk.template store<3>(sK, cgd, pw + s * INC_ROWS);
-        tv.template store<NT>(sV, cgv, nullptr);
-        fence_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            tc_after();
-            const int left = ch.nr - s * INC_ROWS;
-            issue<3, NT, 2>(tmem, su32(sK), INC_PANEL, true, INC_BLOCK, su32(sV), INC_PANEL, true, INC_BLOCK,
-                            idesc_bf16(128, ceil16(wv), 1, 1), min(INC_ROWS, ceil16(left)) / 16, s > 0);
-            mma_commit(&bar);
-        }
-        const int nx = (s + 1) * INC_ROWS;
-        if (nx < ch.nr) {
-            tk.load(k + (size_t)nx * a.ks, a.ks, ch.nr - nx, wd, cgd);
-            tv.load(v + (size_t)nx * a.vs, a.vs, ch.nr - nx, wv, cgv);
-        }
-    }
-    if (ok) ok = w.wait();
-    tc_after();
-    // lane = state row: warps 0-3 columns 0-63, warps 4-7 columns 64-127
-    float *o = inc + ((size_t)c * a.nh + h) * a.d * a.dv;
-    const int row = 32 * (warp & 3) + lane, cb = 64 * (warp >> 2);
-    if (ok) {
-        for (int q = 0; q < 2; ++q) {
-            const int col = cb + 32 * q;
-            if (col >= wv) break;
-            uint32_t r[32];
-            TMEM_LD32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + col, r);
-            tmem_ld_wait();
-            if (row < wd) {
-                float *p = o + (size_t)(d0 + row) * a.dv + v0 + col;
+    const long long wl = a.wait_cycles;
+
+    if (warp >= 6) {
+        // ------------------------------------------------------- producers
+        // the next panel's loads are in flight while one is stored
+        using P = Panel<T, KV, TN>;
+        const uint32_t pt = tid - 192, off = P::off(pt), prow = P::row(pt);
+        uint4 ra[4 * WORDS<T>], rb[4 * WORDS<T>];
+        int ik = 0, iv = 0;
+        bool ok = true;
+        auto load_k = [&](uint4 *r, const IncUnit &x, int s) {
+            P::load(r, (const T *)a.k + (size_t)(x.row0 + KV * s) * a.ks + (size_t)x.g * a.d + x.d0, a.ks, x.nr - KV * s,
+                    a.d - x.d0, pt);
+        };
+        auto load_v = [&](uint4 *r, const IncUnit &x, int s) {
+            P::load(r, (const T *)a.v + (size_t)(x.row0 + KV * s) * a.vs + (size_t)x.g * a.dv + x.v0, a.vs, x.nr - KV * s,
+                    a.dv - x.v0, pt);
+        };
+        float g = 0.f, gstep = 0.f;
+        // weights e^{g (nr - 1 - row)} of the thread's rows, from the last
+        // back; rows past the end are zeros under any finite weight
+        auto store_k = [&](const uint4 *r, const IncUnit &x, int s) {
+            const int b = ik % NK;
+            ok = __all_sync(0xffffffffu, mbar_wait(&kempty[b], ((ik / NK) & 1) ^ 1, abort, wl));
+            if (!ok) return;
+            const int last = x.nr - 1 - KV * s - (int)prow;
+            float w[P::IT];
+            w[P::IT - 1] = lin_pow(g, max(last - P::STEP * (P::IT - 1), 0));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (col + 4 * i < wv)
-                        *(float4 *)(p + 4 * i) = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                                             __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+            for (int i = P::IT - 2; i >= 0; --i)
+                w[i] = last >= P::STEP * (i + 1) ? w[i + 1] * gstep : lin_pow(g, max(last - P::STEP * i, 0));
+            P::template split<3>(r, sK + b * C::KSLOT + off, w);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kfull[b]);
+            ++ik;
+        };
+        auto store_v = [&](const uint4 *r) {
+            const int b = iv % NV;
+            ok = __all_sync(0xffffffffu, mbar_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl));
+            if (!ok) return;
+            P::template put<NT>(r, sV + b * C::VSLOT + off);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[b]);
+            ++iv;
+        };
+        IncUnit x = list[0], y;
+        load_k(ra, x, 0);
+        for (int n = 0; n < count && ok; ++n, x = y) {
+            const int ns = (x.nr + KV - 1) / KV;
+            g = a.decay[x.h];
+            gstep = lin_pow(g, P::STEP);
+            y = list[n + 1 < count ? n + 1 : n];
+            if constexpr (C::TMA) {
+                for (int s = 0; s < ns; s += 2) {   // two buffers in turn
+                    if (s + 1 < ns) load_k(rb, x, s + 1);
+                    store_k(ra, x, s);
+                    if (!ok) break;
+                    if (s + 2 < ns) load_k(ra, x, s + 2);
+                    else if (n + 1 < count) load_k(ra, y, 0);
+                    if (s + 1 < ns) store_k(rb, x, s + 1);
+                    if (!ok) break;
+                }
+            } else {
+                for (int s = 0; s < ns; ++s) {
+                    load_v(rb, x, s);
+                    store_k(ra, x, s);
+                    if (!ok) break;
+                    if (s + 1 < ns) load_k(ra, x, s + 1);
+                    else if (n + 1 < count) load_k(ra, y, 0);
+                    store_v(rb);
+                    if (!ok) break;
+                }
             }
         }
-    } else if (row < wd) {
-        for (int col = cb; col < min(wv, cb + 64); ++col) o[(size_t)(d0 + row) * a.dv + v0 + col] = NAN;
-    }
-    if (!ok && tid == 0) {
-        mbar_drain(&bar, w.phase ^ 1);   // the commit whose wait ran out: the only one in flight
-        atomicOr(&lin_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
+    } else if (warp == 5) {
+        // ------------------------------------------------- TMA of the values
+        if constexpr (C::TMA) {
+            int iv = 0;
+            uint32_t tp = 0;
+            bool ok = true;
+            for (int n = 0; n < count && ok; ++n) {
+                const IncUnit x = list[n];
+                const int boxes = (min(N, a.dv - x.v0) + 63) / 64;
+                for (int s = 0; KV * s < x.nr && ok; ++s) {
+                    const int b = iv % NV;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl)) &&
+                         tma_rows<KV>(sV + b * C::VSLOT, &mv, x.v0, x.g, x.row0 + KV * s, boxes, x.nr - KV * s, &vfull[b],
+                                      &tail, tp, abort, wl, lane);
+                    if (ok) ++iv;
+                }
+            }
+            // after an abort: copies published on their slots may be in flight
+            if (!ok && lane == 0)
+                for (int i = max(0, iv - NV); i < iv; ++i) mbar_drain(&vfull[i % NV], (i / NV) & 1);
+        }
+    } else if (warp == 4) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            const uint32_t k0 = su32(sK), v0 = su32(sV);
+            constexpr int KTERM = KV * TN * 2 / 16, VTERM = KV * N * 2 / 16;
+            for (int n = 0; n < count && ok; ++n) {
+                const int nr = list[n].nr;
+                const uint32_t id = idesc_bf16(128, min(N, ceil16(a.dv - list[n].v0)), 1, 1);
+                const uint32_t d = tmem + (n % C::NB) * 2 * N;
+                ok = mbar_wait(&freed[n % C::NB], ((n / C::NB) & 1) ^ 1, abort, wl);
+                for (int s = 0; KV * s < nr && ok; ++s, ++it) {
+                    const int bk = it % NK, bv = it % NV;
+                    ok = mbar_wait(&kfull[bk], (it / NK) & 1, abort, wl) && mbar_wait(&vfull[bv], (it / NV) & 1, abort, wl);
+                    if (!ok) break;
+                    tc_after();
+                    issue<3, NT, 2, false, KTERM, 128, VTERM, 128>(d, d + N, id, min(KV, ceil16(nr - KV * s)) / 16, s > 0,
+                                                                   desc_sw128_mn(k0 + bk * C::KSLOT, KV * 128),
+                                                                   desc_sw128_mn(v0 + bv * C::VSLOT, KV * 128));
+                    mma_commit(&kempty[bk]);
+                    mma_commit(&vempty[bv]);
+                }
+                if (ok) mma_commit(&done[n % C::NB]);
+            }
+            mma_commit(&fin);   // tracks every MMA issued, also after an abort
+            mbar_drain(&fin, 0);
+        }
+    } else {
+        // -------------------------------------------------------- epilogue
+        bool ok = true;
+        for (int n = 0; n < count; ++n) {
+            const IncUnit x = list[n];
+            const uint32_t lanes = tmem + (n % C::NB) * 2 * N + ((uint32_t)(32 * warp) << 16);
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&done[n % C::NB], (n / C::NB) & 1, abort, wl));
+            tc_after();
+            float *o = inc + ((size_t)x.seg * a.nh + x.h) * a.d * a.dv + (size_t)(x.d0 + 32 * warp) * a.dv + x.v0;
+            const int nr = a.d - x.d0 - 32 * warp, wv = min(N, a.dv - x.v0);
+            for (int c = 0; c < wv; c += 32) {
+                float y[32];
+                if (ok) {
+                    uint32_t r0[32], r1[32];
+                    TMEM_LD32(lanes + c, r0);
+                    TMEM_LD32(lanes + N + c, r1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r0[i]) + __uint_as_float(r1[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = NAN;
+                }
+                store_block(stage + warp * STAGE_FLOATS, y, o + c, a.dv, nr, wv - c, lane);
+            }
+            tc_before();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&freed[n % C::NB]);
+        }
     }
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 0) tmem_free(tmem, 128);
+    if (warp == 0) tmem_free512(tmem);
+    if (tid == 0 && abort_s) atomicOr(&lin_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
 }
 
 // ------------------------------------------------------------------- scan
 
-// Per state element, over a piece's chunks: inc <- the state entering the
-// chunk, S <- l^n S + dS, the last S to its slot. Bound: the scratch's
-// bytes (read and written once, L2-resident for a pass); 4 chunks' loads
-// go out ahead of their use.
+// Per state element, over a piece's segments: the increment is replaced by
+// the state entering the segment, S <- l^n S + dS, the last S goes to its
+// slot. TERMS: the entering state is stored as the two bf16 terms that the
+// outputs multiply, in the same bytes: each row of dv values as dv first
+// terms, then dv second ones. A row is one warp's (a lane the columns 4 lane
+// and 128 + 4 lane), so that it is read before it is overwritten. Bound: the
+// scratch's bytes, read and written once; 4 segments' loads go out ahead of
+// their use.
+template <bool TERMS>
 __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_constant__ LinWorkTable t, float *inc) {
     const LinWork w = t.w[blockIdx.z];
-    const int h = blockIdx.y;
-    const size_t n = (size_t)a.d * a.dv;
-    const size_t e = 4 * ((size_t)blockIdx.x * 256 + threadIdx.x);
-    if (e >= n) return;
-    float4 *sp = (float4 *)(a.state + ((size_t)w.slot * a.nh + h) * n + e);
-    const size_t step = (size_t)a.nh * n / 4;
-    float4 *p = (float4 *)(inc + ((size_t)w.chunk0 * a.nh + h) * n + e);
-    const int nc = (w.rows + LIN_CHUNK - 1) / LIN_CHUNK;
-    const float gd = a.decay[h], full = lin_pow(gd, LIN_CHUNK), last = lin_pow(gd, w.rows - (nc - 1) * LIN_CHUNK);
-    float4 s = *sp;
+    const int h = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= a.d) return;
+    const size_t n = (size_t)a.d * a.dv, step = (size_t)a.nh * n;
+    const int nc = (w.rows + a.seg - 1) / a.seg;
+    const float gd = a.decay[h], full = lin_pow(gd, a.seg), last = lin_pow(gd, w.rows - (nc - 1) * a.seg);
+    float *sp = a.state + ((size_t)w.slot * a.nh + h) * n + (size_t)row * a.dv;
+    float *p = inc + ((size_t)w.seg0 * a.nh + h) * n + (size_t)row * a.dv;
+    float4 s[2];
+    bool in[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        in[j] = 4 * lane + 128 * j < a.dv;
+        if (in[j]) s[j] = *(const float4 *)(sp + 4 * lane + 128 * j);
+    }
     for (int c = 0; c < nc; c += 4) {
-        float4 x[4];
+        float4 x[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (c + i < nc) x[i] = p[(size_t)(c + i) * step];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (c + i < nc && in[j]) x[i][j] = *(const float4 *)(p + (size_t)(c + i) * step + 4 * lane + 128 * j);
+        if (TERMS) __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (c + i >= nc) break;
-            p[(size_t)(c + i) * step] = s;
             const float l = c + i == nc - 1 ? last : full;
-            s.x = fmaf(s.x, l, x[i].x);
-            s.y = fmaf(s.y, l, x[i].y);
-            s.z = fmaf(s.z, l, x[i].z);
-            s.w = fmaf(s.w, l, x[i].w);
+            float *q = p + (size_t)(c + i) * step;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (!in[j]) continue;
+                const int col = 4 * lane + 128 * j;
+                if (TERMS) {
+                    float4 y = s[j];
+                    const uint2 hi = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
+                    const uint2 lo = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
+                    *(uint2 *)((uint16_t *)q + col) = hi;
+                    *(uint2 *)((uint16_t *)q + a.dv + col) = lo;
+                } else {
+                    *(float4 *)(q + col) = s[j];
+                }
+                s[j].x = fmaf(s[j].x, l, x[i][j].x);
+                s[j].y = fmaf(s[j].y, l, x[i][j].y);
+                s[j].z = fmaf(s[j].z, l, x[i][j].z);
+                s[j].w = fmaf(s[j].w, l, x[i][j].w);
+            }
         }
     }
-    *sp = s;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (in[j]) *(float4 *)(sp + 4 * lane + 128 * j) = s[j];
 }
 
 // ---------------------------------------------------------------- outputs
 
-constexpr uint32_t OUT_PANEL = LIN_CHUNK * COLS * 2, OUT_BLOCK = LIN_CHUNK * 128;
-constexpr int OUT_ACC = 0, OUT_SC = 128;   // TMEM columns: Q S_in; scores, later P V
+// Warps: 0-3 P (a thread a row), 4-7 epilogue, 8 MMA issuer, 9 TMA (bf16) or
+// 9-16 producers (types that are split).
+template <typename T>
+struct OutCfg {
+    static constexpr int NT = Terms<T>::in, MT = Terms<T>::mid;
+    static constexpr bool TMA = NT == 1;       // panels by TMA, as they are; Q and K of a step share a slot
+    static constexpr int THREADS = 32 * (9 + (TMA ? 1 : PROD_WARPS));
+    static constexpr int SLOT = NT == 3 ? 49152 : 32768, NSLOT = NT == 3 ? 4 : 6;
+    static constexpr int VR = NT == 1 ? 128 : 64;   // value rows of a slot
+    static constexpr bool SPLIT = NT == 3;     // corrections in accumulators of their own
+    // TMEM: outputs ACC (two buffers; SPLIT: one, main and corrections), then
+    // scores X (two buffers; SPLIT: one, main and corrections). P overlays X.
+    static constexpr int XB = SPLIT ? 1 : 2, AB = SPLIT ? 1 : 2;
+    static constexpr size_t SMEM = 1024 + (size_t)NSLOT * SLOT + 4 * STAGE_FLOATS * 4;
+    static __device__ __forceinline__ uint32_t acc(int n) { return SPLIT ? 0u : 128u * (n & 1); }
+    static __device__ __forceinline__ uint32_t x(int u) { return 256u + (SPLIT ? 0u : 128u * (u & 1)); }
+    static constexpr uint32_t CORR = SPLIT ? 128u : 0u;
+};
 
-template <typename T>
-constexpr int out_threads() { return Terms<T>::in == 1 ? 256 : 512; }
-template <typename T>
-constexpr size_t out_smem() {
-    const int b = Terms<T>::in > Terms<T>::mid ? Terms<T>::in : Terms<T>::mid;
-    return 1024 + (size_t)(Terms<T>::in + b) * OUT_PANEL;
-}
+// One tile: 128 query rows x 128 value columns of a head; its units are the
+// key tiles kt = 0 .. nkt - 1 of the segment up to its own rows (the last).
+struct OutTile {
+    int row0, nr;        // query rows
+    int seg0row, seg;    // segment: first row, state
+    int h, g, v0, nkt;
+};
+struct Cursor {
+    int n, u, kt;        // tile of the list, units so far, key tile
+    OutTile x;
+    __device__ __forceinline__ void start(const OutTile *list) {
+        n = u = kt = 0;
+        x = list[0];
+    }
+    // the next unit: false after the last
+    __device__ __forceinline__ bool next(const OutTile *list, int count) {
+        ++u;
+        if (++kt < x.nkt) return true;
+        kt = 0;
+        if (++n >= count) return false;
+        x = list[n];
+        return true;
+    }
+    __device__ __forceinline__ bool diag() const { return kt == x.nkt - 1; }
+    __device__ __forceinline__ int keys() const { return diag() ? x.nr : LIN_CHUNK; }
+    __device__ __forceinline__ int key0() const { return x.seg0row + LIN_CHUNK * kt; }
+};
 
-// The outputs of one (chunk, head), a tile of 128 value columns a CTA. Two
-// shared-memory regions: A holds Q, then V; B holds K, then S_in, then P. d
-// above 128 runs Q, K and S_in in two rounds. Two CTAs an SM (bf16) hide each
-// other's staging.
+// Outputs. Weights: with i0 the tile's first row and s0 its segment's,
+//   o_i = l^{i-i0+1} ( l^{i0-s0} q_i S_in + sum_{j<i0} l^{i0-1-j} s_ij v_j )
+//         + sum_{i0<=j<=i} l^{i-j} s_ij v_j
+// so the accumulator is weighted once after q S_in (if earlier key tiles
+// follow) and once, by row, before the last (diagonal) tile, the earlier key
+// tiles' scores by column. The MMA thread issues the next unit's scores (and a
+// next tile's q S_in) ahead of this unit's P V where TMEM holds two score
+// buffers, so that P is formed under them.
 template <typename T>
-__global__ __launch_bounds__(out_threads<T>(), Terms<T>::in == 1 ? 2 : 1) void k_lin_out(
-    LinArgs a, const __grid_constant__ LinWorkTable t, const float *inc) {
+__global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, const __grid_constant__ LinWorkTable t,
+                                                                   const __grid_constant__ CUtensorMap mq,
+                                                                   const __grid_constant__ CUtensorMap mk,
+                                                                   const __grid_constant__ CUtensorMap mv,
+                                                                   const __grid_constant__ CUtensorMap ms, int tiles,
+                                                                   const float *inc) {
+    using C = OutCfg<T>;
+    constexpr int NT = C::NT, MT = C::MT;
     extern __shared__ unsigned char smraw[];
-    __shared__ uint64_t bar;
+    __shared__ uint64_t full[C::NSLOT], empty[C::NSLOT], sc_full[2], p_full[2], acc_ready[2], o_done[2], acc_free[2], tail,
+        fin;
     __shared__ uint32_t tslot;
-    __shared__ int abort;
-    __shared__ float pw[LIN_CHUNK + 1];   // powers of the decay
-    constexpr int NT = Terms<T>::in, MT = Terms<T>::mid, NTHR = out_threads<T>(), NW = NTHR / 32;
-    constexpr int WC = COLS / (NW / 4);   // columns a warp takes of its 32 TMEM lanes
+    __shared__ int abort_s;
+    __shared__ float powers[4][LIN_CHUNK + 1];   // of the decay, for each P warp
+    __shared__ OutTile list[LIST];
+    volatile int *abort = &abort_s;
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
-    unsigned char *sA = sm, *sB = sm + NT * OUT_PANEL;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c = blockIdx.x, h = blockIdx.y, g = h / a.hpg, v0 = blockIdx.z * COLS;
-    const int wv = min(COLS, a.dv - v0), cgv = wv > 64 ? 16 : 8;
-    const Chunk ch = find_chunk(t, c);
+    const int count = (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;   // <= LIST
     if (tid == 0) {
-        mbar_init(&bar, 1);
-        abort = 0;
+        for (int i = 0; i < C::NSLOT; ++i) {
+            mbar_init(&full[i], C::TMA ? 1 : PROD_WARPS);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&acc_ready[i], 1);
+            mbar_init(&o_done[i], 1);
+            mbar_init(&acc_free[i], 4);
+        }
+        mbar_init(&tail, 1);
+        mbar_init(&fin, 1);
+        abort_s = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) tmem_alloc(&tslot, 256);
-    if (tid <= LIN_CHUNK) pw[tid] = lin_pow(a.decay[h], tid);
+    if (warp == 0) tmem_alloc512(&tslot);
+    if (tid >= 64 && tid < 64 + count) {
+        const int vt = (a.dv + TN - 1) / TN;
+        int c = blockIdx.x + gridDim.x * (tid - 64);
+        OutTile x;
+        x.v0 = (c % vt) * TN;
+        c /= vt;
+        x.h = c % a.nh;
+        x.g = x.h / a.hpg;
+        c /= a.nh;
+        const LinWork &w = find_piece(t, c, [](const LinWork &p) { return p.tile0; });
+        const int off = (c - w.tile0) * LIN_CHUNK, sl = off / a.seg;
+        x.row0 = w.row0 + off;
+        x.nr = min(LIN_CHUNK, w.rows - off);
+        x.seg = w.seg0 + sl;
+        x.seg0row = w.row0 + sl * a.seg;
+        x.nkt = (off - sl * a.seg) / LIN_CHUNK + 1;
+        list[tid - 64] = x;
+    }
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = tslot;
-    Waits w{&bar, &abort, a.wait_cycles, 0};
-    const T *q = (const T *)a.q + (size_t)ch.row0 * a.qs + (size_t)h * a.d;
-    const T *k = (const T *)a.k + (size_t)ch.row0 * a.ks + (size_t)g * a.d;
-    const T *v = (const T *)a.v + (size_t)ch.row0 * a.vs + (size_t)g * a.dv + v0;
-    const float *S = inc + ((size_t)c * a.nh + h) * a.d * a.dv + v0;
-    const uint32_t A = su32(sA), B = su32(sB);
-    bool ok = true;
-    Tile<T, LIN_CHUNK, NTHR> tv;
-    for (int d0 = 0; d0 < a.d && ok; d0 += COLS) {
-        const int wd = min(COLS, a.d - d0), cgd = wd > 64 ? 16 : 8, ks = ceil16(wd) / 16;
-        {
-            Tile<T, LIN_CHUNK, NTHR> tq, tk;
-            tq.load(q + d0, a.qs, ch.nr, wd, cgd);
-            tk.load(k + d0, a.ks, ch.nr, wd, cgd);
-            tq.template store<NT>(sA, cgd, nullptr);
-            tk.template store<NT>(sB, cgd, nullptr);
-        }
-        fence_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            tc_after();
-            issue<NT, NT, NT - 1>(tmem + OUT_SC, A, OUT_PANEL, false, OUT_BLOCK, B, OUT_PANEL, false, OUT_BLOCK,
-                                  idesc_bf16(128, 128, 0, 0), ks, d0 > 0);
-            mma_commit(&bar);
-        }
-        Tile<float, LIN_CHUNK, NTHR> ts;   // S_in rows d0 ..: panel rows are d
-        ts.load(S + (size_t)d0 * a.dv, a.dv, wd, wv, cgv);
-        ok = w.wait();
-        if (!ok) break;
-        ts.template store<MT>(sB, cgv, nullptr);
-        fence_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            tc_after();
-            issue<NT, MT, max_sum(NT, MT)>(tmem + OUT_ACC, A, OUT_PANEL, false, OUT_BLOCK, B, OUT_PANEL, true, OUT_BLOCK,
-                                           idesc_bf16(128, ceil16(wv), 0, 1), ks, d0 > 0);
-            mma_commit(&bar);
-        }
-        if (d0 + COLS >= a.d) tv.load(v, a.vs, ch.nr, wv, cgv);
-        ok = w.wait();
-    }
-    const int row = 32 * (warp & 3) + lane, cw = WC * (warp >> 2);
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    if (ok) {
-        // P_ij = l^{i-j} s_ij for j <= i, else 0 (also for keys past the end)
-        tv.template store<NT>(sA, cgv, nullptr);
-        tc_after();
-        for (int cb = cw; cb < cw + WC; cb += 32) {
-            uint32_t r[32];
-            TMEM_LD32(lane_base + OUT_SC + cb, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = cb + 8 * i + e;
-                    x[e] = j <= row ? __uint_as_float(r[8 * i + e]) * pw[row - j] : 0.f;
+    const long long wl = a.wait_cycles;
+    const int nb = (a.d + KV - 1) / KV;   // steps of 64 of d
+
+    if (warp == 8) {
+        // ------------------------------------------------------ MMA issuer
+        // Ring items in order: per unit, for each step of d the Q and K
+        // panels and (first unit of a tile) the entering state's; the unit's
+        // values (a unit later where scores run ahead).
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true, vq = true, vv = true;
+            Cursor cq, cv;
+            cq.start(list);
+            cv.start(list);
+            const uint32_t base = su32(sm);
+            auto need = [&](int i) -> uint32_t {   // slot of ring item i, once filled
+                const int s = i % C::NSLOT;
+                ok = ok && mbar_wait(&full[s], (i / C::NSLOT) & 1, abort, wl);
+                return base + (uint32_t)s * C::SLOT;
+            };
+            auto done = [&](int i) { mma_commit(&empty[i % C::NSLOT]); };
+            // scores of a unit, and with a tile's first unit its q S_in
+            auto scores = [&]() {
+                const uint32_t x = tmem + C::x(cq.u), acc = tmem + C::acc(cq.n);
+                const uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cq.x.v0)), 0, 1);
+                for (int b = 0; b < nb; ++b) {
+                    const int steps = ceil16(min(KV, a.d - KV * b)) / 16, iq = it;
+                    const uint32_t q = need(it++), k = C::TMA ? q + 16384 : need(it++);
+                    if (!ok) return;
+                    tc_after();
+                    const uint64_t qd = desc_sw128(q);
+                    issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(x, x + C::CORR, id_x, steps, b > 0, qd, desc_sw128(k));
+                    if (!C::TMA) done(iq + 1);
+                    if (b == nb - 1) mma_commit(&sc_full[cq.u % C::XB]);
+                    if (cq.kt == 0) {
+                        if (b == 0) ok = mbar_wait(&acc_free[cq.n % C::AB], ((cq.n / C::AB) & 1) ^ 1, abort, wl);
+                        const int is = it++;
+                        const uint32_t s0 = need(is);
+                        if (!ok) return;
+                        tc_after();
+                        issue<NT, MT, max_sum(NT, MT), false, 1024, 2, KV * TN * 2 / 16, 128>(
+                            acc, acc + C::CORR, id_a, steps, b > 0, qd, desc_sw128_mn(s0, KV * 128));
+                        done(is);
+                    }
+                    done(iq);
                 }
-                store_terms<MT>(sB + panel_off(LIN_CHUNK, row, (cb >> 3) + i), OUT_PANEL, x);
+                if (cq.kt == 0) mma_commit(&acc_ready[cq.n % C::AB]);
+                vq = cq.next(list, count);
+            };
+            auto values = [&]() {
+                const uint32_t x = tmem + C::x(cv.u), acc = tmem + C::acc(cv.n);
+                const uint32_t id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cv.x.v0)), 0, 1);
+                const int nk = cv.keys();
+                ok = mbar_wait(&p_full[cv.u % C::XB], (cv.u / C::XB) & 1, abort, wl);
+                for (int i = 0; i < LIN_CHUNK / C::VR; ++i) {
+                    const uint32_t v = need(it);
+                    if (!ok) return;
+                    tc_after();
+                    const int steps = min(C::VR, ceil16(max(0, nk - C::VR * i))) / 16;
+                    const uint64_t vd = desc_sw128_mn(v, C::VR * 128);
+                    constexpr int TERM = C::VR * TN * 2 / 16;
+                    if (steps > 0) {
+                        // P's terms 0 and 1 of 16 keys are 16 columns; the third's 8 lie apart
+                        if constexpr (MT == 3)
+                            issue<1, 1, 0, true, 0, 8, 0, 128>(acc + C::CORR, acc + C::CORR, id_a, steps, true,
+                                                               x + 128 + C::VR * i / 2, vd);
+                        issue<2, NT, max_sum(MT, NT), true, 8, 16, TERM, 128>(acc, acc + C::CORR, id_a, steps, true,
+                                                                             x + C::VR * i, vd);
+                    }
+                    done(it++);
+                }
+                if (cv.diag()) mma_commit(&o_done[cv.n % C::AB]);
+                else if (cv.kt == cv.x.nkt - 2) mma_commit(&acc_ready[cv.n % C::AB]);
+                vv = cv.next(list, count);
+            };
+            scores();
+            while (vv && ok) {
+                if (C::XB == 2 && vq) scores();
+                if (ok) values();
+                if (C::XB == 1 && vq && ok) scores();
+            }
+            mma_commit(&fin);   // tracks every MMA issued, also after an abort
+            mbar_drain(&fin, 0);
+        }
+    } else if (warp > 8) {
+        int it = 0;
+        if constexpr (C::TMA) {
+            // -------------------------------------------------- TMA, one warp
+            bool ok = true, vq = true, vv = true;
+            uint32_t tp = 0;
+            Cursor cq, cv;
+            cq.start(list);
+            cv.start(list);
+            auto slot = [&]() -> unsigned char * {
+                const int s = it % C::NSLOT;
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl));
+                return sm + (size_t)s * C::SLOT;
+            };
+            auto scores = [&]() {
+                const int vb = (min(TN, a.dv - cq.x.v0) + 63) / 64;
+                for (int b = 0; b < nb; ++b) {
+                    unsigned char *d = slot();
+                    if (!ok) return;
+                    uint64_t *f = &full[it % C::NSLOT];
+                    if (lane == 0) {
+                        mbar_expect_tx(f, 32768);
+                        tma_3d(d, &mq, KV * b, cq.x.h, cq.x.row0, f);
+                        tma_3d(d + 16384, &mk, KV * b, cq.x.g, cq.key0(), f);
+                    }
+                    ++it;
+                    if (cq.kt == 0) {
+                        d = slot();
+                        if (!ok) return;
+                        f = &full[it % C::NSLOT];
+                        if (lane == 0) {
+                            mbar_expect_tx(f, MT * vb * 8192);
+                            for (int m = 0; m < MT; ++m)
+                                for (int i = 0; i < vb; ++i)
+                                    tma_4d(d + 16384 * m + 8192 * i, &ms, cq.x.v0 + 64 * i, m, KV * b,
+                                           cq.x.seg * a.nh + cq.x.h, f);
+                        }
+                        ++it;
+                    }
+                }
+                vq = cq.next(list, count);
+            };
+            auto values = [&]() {
+                unsigned char *d = slot();
+                if (!ok) return;
+                ok = tma_rows<C::VR>(d, &mv, cv.x.v0, cv.x.g, cv.key0(), (min(TN, a.dv - cv.x.v0) + 63) / 64, cv.keys(),
+                                     &full[it % C::NSLOT], &tail, tp, abort, wl, lane);
+                if (!ok) return;
+                ++it;
+                vv = cv.next(list, count);
+            };
+            scores();
+            while (vv && ok) {
+                if (vq) scores();
+                if (ok) values();
+            }
+            if (!ok && lane == 0)
+                for (int i = max(0, it - C::NSLOT); i < it; ++i) mbar_drain(&full[i % C::NSLOT], (i / C::NSLOT) & 1);
+        } else {
+            // ---------------------------------------------------- producers
+            // Two register buffers: an item is loaded while the one before is
+            // stored.
+            using PQ = Panel<T, 128, KV>;
+            using PS = Panel<float, KV, TN>;
+            using PV = Panel<T, C::VR, TN>;
+            const uint32_t pt = tid - 288, qoff = PQ::off(pt), soff = PS::off(pt), voff = PV::off(pt);
+            enum { IT_QK, IT_S, IT_V };
+            struct Item {
+                int kind, nr, width;
+                const void *p;
+                size_t stride;
+            };
+            Cursor cq, cv;
+            cq.start(list);
+            cv.start(list);
+            bool vq = true, vv = true, in_v = false, first = true;   // in_v: a values item comes next
+            int b = 0, j = 0, i = 0;   // step of d and item of it; value panel
+            auto gen = [&](Item &e) -> bool {
+                if (!in_v) {
+                    if (!vq) return false;
+                    if (j == 2) {
+                        e.kind = IT_S;
+                        e.p = inc + ((size_t)cq.x.seg * a.nh + cq.x.h) * a.d * a.dv + KV * b * a.dv + cq.x.v0;
+                        e.stride = a.dv;
+                        e.nr = a.d - KV * b;
+                        e.width = a.dv - cq.x.v0;
+                    } else {
+                        e.kind = IT_QK;
+                        e.p = j == 0 ? (const T *)a.q + (size_t)cq.x.row0 * a.qs + cq.x.h * a.d + KV * b
+                                     : (const T *)a.k + (size_t)cq.key0() * a.ks + cq.x.g * a.d + KV * b;
+                        e.stride = j == 0 ? a.qs : a.ks;
+                        e.nr = j == 0 ? cq.x.nr : cq.keys();
+                        e.width = a.d - KV * b;
+                    }
+                    if (++j == (cq.kt == 0 ? 3 : 2)) {
+                        j = 0;
+                        if (++b == nb) {
+                            b = 0;
+                            vq = cq.next(list, count);
+                            // scores run one unit ahead with two score buffers
+                            in_v = C::XB == 1 || !first || !vq;
+                            first = false;
+                        }
+                    }
+                    return true;
+                }
+                if (!vv) return false;
+                e.kind = IT_V;
+                e.p = (const T *)a.v + (size_t)(cv.key0() + C::VR * i) * a.vs + cv.x.g * a.dv + cv.x.v0;
+                e.stride = a.vs;
+                e.nr = cv.keys() - C::VR * i;
+                e.width = a.dv - cv.x.v0;
+                if (++i == LIN_CHUNK / C::VR) {
+                    i = 0;
+                    vv = cv.next(list, count);
+                    in_v = !vq;
+                }
+                return true;
+            };
+            auto load = [&](uint4 *r, const Item &e) {
+                if (e.kind == IT_QK) PQ::load(r, (const T *)e.p, e.stride, e.nr, e.width, pt);
+                else if (e.kind == IT_S) PS::load(r, (const float *)e.p, e.stride, e.nr, e.width, pt);
+                else PV::load(r, (const T *)e.p, e.stride, e.nr, e.width, pt);
+            };
+            auto store = [&](const uint4 *r, const Item &e) -> bool {
+                const int s = it % C::NSLOT;
+                if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl))) return false;
+                unsigned char *d = sm + (size_t)s * C::SLOT;
+                if (e.kind == IT_QK) PQ::template put<NT>(r, d + qoff);
+                else if (e.kind == IT_S) PS::template put<MT>(r, d + soff);
+                else PV::template put<NT>(r, d + voff);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+                ++it;
+                return true;
+            };
+            uint4 ra[8], rb[8];
+            Item ea, eb;
+            bool ha = gen(ea), hb;
+            load(ra, ea);
+            while (ha) {
+                hb = gen(eb);
+                if (hb) load(rb, eb);
+                if (!store(ra, ea) || !hb) break;
+                ha = gen(ea);
+                if (ha) load(ra, ea);
+                if (!store(rb, eb)) break;
             }
         }
-        tc_before();
-        fence_async_smem();
-        __syncthreads();
-        if (tid == 0) {
+    } else if (warp < 4) {
+        // --------------------------------------------------------------- P
+        Cursor c;
+        c.start(list);
+        bool have = true, ok = true;
+        const int row = tid;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        int table = -1;   // head of the power table
+        float *pw = powers[warp];
+        float g = 0.f;
+        uint32_t rp[2] = {0, 0};   // phases of acc_ready
+        // the accumulator times f, once what it holds so far is complete
+        auto weight = [&](float f) -> bool {
+            const int i = c.n % C::AB;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_ready[i], i ? rp[1] : rp[0], abort, wl))) return false;
+            if (i) rp[1] ^= 1;
+            else rp[0] ^= 1;
             tc_after();
-            issue<MT, NT, max_sum(MT, NT)>(tmem + OUT_SC, B, OUT_PANEL, false, OUT_BLOCK, A, OUT_PANEL, true, OUT_BLOCK,
-                                           idesc_bf16(128, ceil16(wv), 0, 1), ceil16(ch.nr) / 16, false);
-            mma_commit(&bar);
-        }
-        ok = w.wait();
-    }
-    tc_after();
-    const float lr = pw[row + 1];
-    for (int cb = cw; cb < cw + WC; cb += 32) {
-        if (cb >= wv) break;
-        uint32_t r0[32], r1[32];
-        TMEM_LD32(lane_base + OUT_ACC + cb, r0);
-        TMEM_LD32(lane_base + OUT_SC + cb, r1);
-        tmem_ld_wait();
-        if (row < ch.nr) {
-            T *o = (T *)a.out + (size_t)(ch.row0 + row) * a.os + (size_t)h * a.dv + v0 + cb;
+            const int wv = min(TN, a.dv - c.x.v0);
+            for (int half = 0; half <= (C::SPLIT ? 1 : 0); ++half)
+                for (int cb = 0; cb < wv; cb += 32) {
+                    const uint32_t ad = lanes + C::acc(c.n) + 128 * half + cb;
+                    uint32_t r[32];
+                    TMEM_LD32(ad, r);
+                    tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (cb + 4 * i >= wv) continue;
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[e] = ok ? a.scale * fmaf(lr, __uint_as_float(r0[4 * i + e]), __uint_as_float(r1[4 * i + e])) : NAN;
-                o1_st4(o + 4 * i, make_float4(y[0], y[1], y[2], y[3]));
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                    TMEM_ST32(ad, r);
+                }
+            return true;
+        };
+        while (have && ok) {
+            if (table != c.x.h) {
+                __syncwarp();
+                g = a.decay[c.x.h];
+                for (int i = lane; i <= LIN_CHUNK; i += 32) pw[i] = lin_pow(g, i);
+                table = c.x.h;
+                __syncwarp();
             }
+            ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[c.u % C::XB], (c.u / C::XB) & 1, abort, wl));
+            if (!ok) break;
+            tc_after();
+            const bool diag = c.diag();
+            const float tf = diag ? 0.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt));
+            const uint32_t x = lanes + C::x(c.u);
+            // P over the scores of the same keys; a third term of 32 keys
+            // takes 16 columns of the corrections, of keys already read
+#pragma unroll
+            for (int cb = 0; cb < LIN_CHUNK; cb += 32) {
+                uint32_t r[32], third[16];
+                float s[32];
+                TMEM_LD32(x + cb, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
+                if (C::SPLIT) {
+                    TMEM_LD32(x + C::CORR + cb, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(r[i]);
+                }
+                if (diag) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] = cb + i <= row ? s[i] * pw[max(row - cb - i, 0)] : 0.f;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] *= pw[LIN_CHUNK - 1 - cb - i] * tf;
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float &x0 = s[16 * q + 2 * e], &x1 = s[16 * q + 2 * e + 1];
+                        r[16 * q + e] = take_pair(x0, x1);
+                        r[16 * q + 8 + e] = take_pair(x0, x1);
+                        if (C::SPLIT) third[8 * q + e] = take_pair(x0, x1);
+                    }
+                TMEM_ST32(x + cb, r);
+                if (C::SPLIT) TMEM_ST16(x + 128 + cb / 2, third);
+            }
+            if (c.kt == 0 && !diag) ok = weight(lin_pow(g, c.x.row0 - c.x.seg0row));
+            if (diag && ok) ok = weight(pw[row + 1]);
+            if (!ok) break;
+            tmem_st_wait();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[c.u % C::XB]);
+            have = c.next(list, count);
         }
-    }
-    if (!ok && tid == 0) {
-        mbar_drain(&bar, w.phase ^ 1);   // the commit whose wait ran out: the only one in flight
-        atomicOr(&lin_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
+    } else {
+        // -------------------------------------------------------- epilogue
+        float *stage = (float *)(sm + (size_t)C::NSLOT * C::SLOT) + (warp & 3) * STAGE_FLOATS;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        bool ok = true;
+        for (int n = 0; n < count; ++n) {
+            const OutTile x = list[n];
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[n % C::AB], (n / C::AB) & 1, abort, wl));
+            tc_after();
+            T *o = (T *)a.out + (size_t)(x.row0 + 32 * (warp & 3)) * a.os + (size_t)x.h * a.dv + x.v0;
+            const int nr = x.nr - 32 * (warp & 3), wv = min(TN, a.dv - x.v0);
+            for (int cb = 0; cb < wv; cb += 32) {
+                float y[32];
+                if (ok) {
+                    uint32_t r[32];
+                    TMEM_LD32(lanes + C::acc(n) + cb, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r[i]);
+                    if (C::SPLIT) {
+                        TMEM_LD32(lanes + C::acc(n) + C::CORR + cb, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] += __uint_as_float(r[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] *= a.scale;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = NAN;
+                }
+                store_block(stage, y, o + cb, a.os, nr, wv - cb, lane);
+            }
+            tc_before();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&acc_free[n % C::AB]);
+        }
     }
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 0) tmem_free(tmem, 256);
+    if (warp == 0) tmem_free512(tmem);
+    if (tid == 0 && abort_s) atomicOr(&lin_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
 }
 
-template <typename T>
-void pass_t(const LinArgs &a, const LinWorkTable &t, int chunks, float *inc, cudaStream_t st) {
+// ----------------------------------------------------------------- launch
+
+// A bf16 row tensor [rows][heads][width] in boxes of 64 columns of `box` rows.
+bool rows_map(CUtensorMap *m, const void *base, int width, int heads, int rows, size_t stride, int box) {
+    const auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
+    cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)base, dims, strides, boxes, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The entering states as the scan leaves them: [states][d][2 terms][dv].
+bool states_map(CUtensorMap *m, const void *base, const LinArgs &a, int states) {
+    const auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)a.dv, 2, (cuuint64_t)a.d, (cuuint64_t)states};
+    cuuint64_t strides[3] = {(cuuint64_t)a.dv * 2, (cuuint64_t)a.dv * 4, (cuuint64_t)a.d * a.dv * 4};
+    cuuint32_t boxes[4] = {64, 1, KV, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void *)base, dims, strides, boxes, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of a persistent grid: one an SM, more where a CTA's list would overflow.
+int grid_of(int units) {
+    const int ctas = units < LIN_SMS ? units : LIN_SMS, need = (units + LIST - 1) / LIST;
+    return ctas > need ? ctas : need;
+}
+
+template <typename T, int N>
+bool pass_t(const LinArgs &a, const LinWorkTable &t, int segs, int tiles, float *inc, cudaStream_t st) {
+    using CI = IncCfg<T, N>;
+    using CO = OutCfg<T>;
     static unsigned long long done = 0;
     unsigned long long bit = 0;
     if (o1_attrs_needed(&done, &bit)) {
-        cudaFuncSetAttribute(k_lin_inc<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)inc_smem<T>());
-        cudaFuncSetAttribute(k_lin_out<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)out_smem<T>());
+        cudaFuncSetAttribute(k_lin_inc<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CI::SMEM);
+        cudaFuncSetAttribute(k_lin_out<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CO::SMEM);
         o1_attrs_done(&done, bit);
     }
-    const int dt = (a.d + COLS - 1) / COLS, vt = (a.dv + COLS - 1) / COLS;
-    k_lin_inc<T><<<dim3(chunks, a.nh, dt * vt), INC_THREADS, inc_smem<T>(), st>>>(a, t, inc);
-    k_lin_scan<<<dim3((a.d * a.dv / 4 + 255) / 256, a.nh, t.n), 256, 0, st>>>(a, t, inc);
-    k_lin_out<T><<<dim3(chunks, a.nh, vt), out_threads<T>(), out_smem<T>(), st>>>(a, t, inc);
+    CUtensorMap mq = {}, mk = {}, mv = {}, mvi = {}, ms = {};
+    if (CO::TMA && !(rows_map(&mq, a.q, a.d, a.nh, a.rows, a.qs, LIN_CHUNK) &&
+                     rows_map(&mk, a.k, a.d, a.G, a.rows, a.ks, LIN_CHUNK) &&
+                     rows_map(&mv, a.v, a.dv, a.G, a.rows, a.vs, CO::VR) &&
+                     rows_map(&mvi, a.v, a.dv, a.G, a.rows, a.vs, KV) && states_map(&ms, inc, a, segs * a.nh)))
+        return false;
+    const int dt = (a.d + TN - 1) / TN, units = segs * a.nh * dt * ((a.dv + N - 1) / N);
+    const int ot = tiles * a.nh * ((a.dv + TN - 1) / TN);
+    k_lin_inc<T, N><<<grid_of(units), CI::THREADS, CI::SMEM, st>>>(a, t, mvi, units, inc);
+    k_lin_scan<CO::TMA><<<dim3((a.d + 7) / 8, a.nh, t.n), 256, 0, st>>>(a, t, inc);
+    k_lin_out<T><<<grid_of(ot), CO::THREADS, CO::SMEM, st>>>(a, t, mq, mk, mv, ms, ot, inc);
+    return true;
 }
 
 }  // namespace
 
-void lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int chunks, float *inc, cudaStream_t st) {
-    if (dtype == O1_F32) pass_t<float>(a, t, chunks, inc, st);
-    else if (dtype == O1_BF16) pass_t<__nv_bfloat16>(a, t, chunks, inc, st);
-    else pass_t<__half>(a, t, chunks, inc, st);
+bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, float *inc, cudaStream_t st) {
+    if (dtype == O1_F32) return pass_t<float, 128>(a, t, segs, tiles, inc, st);
+    if (dtype == O1_F16) return pass_t<__half, 128>(a, t, segs, tiles, inc, st);
+    return a.dv > 128 ? pass_t<__nv_bfloat16, 256>(a, t, segs, tiles, inc, st)
+                      : pass_t<__nv_bfloat16, 128>(a, t, segs, tiles, inc, st);
 }
 
 int lin_flags(uint32_t *flags, int clear, cudaStream_t st) {

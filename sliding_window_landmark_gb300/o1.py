@@ -193,6 +193,14 @@ def _stream(stream):
     return _VP(int(stream))
 
 
+def _raw_stream(stream, dev: int):
+    """The handle of a stream; None: device `dev`'s current one, read without
+    making a Stream object (a few microseconds of a small call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def o1_status_string(status: int) -> str:
     return LIB.o1_status_string(int(status)).decode()
 
@@ -379,41 +387,55 @@ def lin_seqs(seqs):
     return (o1_lin_seq * len(seqs))(*[tuple(int(x) for x in s) for s in seqs])
 
 
-def _here(t, name):
-    if t is not None and isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on device {t.device.index}, the current device is {torch.cuda.current_device()}")
-    return t
-
-
-def _rows(t, heads: int, width: int, dtype: int, rows: int, name: str):
-    """Pointer and row stride of a [rows, heads, width] CUDA tensor whose heads
-    and widths are contiguous (None where it has no heads -> NULL)."""
+def _rows(t, heads: int, width: int, dtype: int, rows: int, name: str, dev: int):
+    """Pointer and row stride of a [rows, heads, width] tensor on device `dev`
+    whose heads and widths are contiguous (None where it has no heads -> NULL)."""
     if t is None and heads == 0:
         return None, 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
     if DTYPES.get(t.dtype) != dtype:
         raise TypeError(f"{name}: element type {t.dtype} is not the geometry's")
-    if tuple(t.shape) != (rows, heads, width):
+    if t.shape != (rows, heads, width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need {(rows, heads, width)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != width)):
+    row, head, one = t.stride()
+    if (one != 1 or (head != width and heads > 1)) and t.numel():
         raise ValueError(f"{name}: heads and widths must be contiguous")
-    _here(t, name)
-    return _VP(t.data_ptr()), (t.stride(0) if rows > 1 else heads * width)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+    return t.data_ptr(), row if rows > 1 else heads * width
+
+
+def _flat(t, n: int, dtype, name: str, dev: int):
+    """Pointer of a contiguous tensor of at least n elements on device `dev`."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous tensor of {n} elements")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
+    return t.data_ptr()
 
 
 def o1_head_prep(g: o1_prep_geom, q, k, q_weight, k_weight, inv_freq, q_out, k_out, pos=None, pos0: int = 0,
                  stream=None) -> int:
     """Per-head norm and rotation of q [rows, q_heads, d] and k [rows, k_heads,
     d] into q_out and k_out (which may be q and k themselves)."""
-    rows = (q if g.q_heads else k).shape[0]
-    (qp, qs), (kp, ks) = _rows(q, g.q_heads, g.d, g.in_dtype, rows, "q"), _rows(k, g.k_heads, g.d, g.in_dtype, rows, "k")
-    (qo, qos), (ko, kos) = (_rows(q_out, g.q_heads, g.d, g.out_dtype, rows, "q_out"),
-                            _rows(k_out, g.k_heads, g.d, g.out_dtype, rows, "k_out"))
+    dev, hq, hk, d = torch.cuda.current_device(), g.q_heads, g.k_heads, g.d
+    rows = (q if hq else k).shape[0]
+    qp, qs = _rows(q, hq, d, g.in_dtype, rows, "q", dev)
+    kp, ks = _rows(k, hk, d, g.in_dtype, rows, "k", dev)
+    qo, qos = _rows(q_out, hq, d, g.out_dtype, rows, "q_out", dev)
+    ko, kos = _rows(k_out, hk, d, g.out_dtype, rows, "k_out", dev)
+    f32 = torch.float32
     return LIB.o1_head_prep(
-        ctypes.byref(g), qp, qs, kp, ks, _dev(_here(q_weight, "q_weight"), g.d, "q_weight"),
-        _dev(_here(k_weight, "k_weight"), g.d, "k_weight"), _dev(_here(inv_freq, "inv_freq"), g.rot // 2, "inv_freq"),
-        _dev(_here(pos, "pos"), 2 * rows, "pos", dtype=torch.int64), int(pos0), rows, qo, qos, ko, kos, _stream(stream))
+        ctypes.byref(g), qp, qs, kp, ks, _flat(q_weight, d, f32, "q_weight", dev), _flat(k_weight, d, f32, "k_weight", dev),
+        _flat(inv_freq, g.rot // 2, f32, "inv_freq", dev), _flat(pos, rows, torch.int64, "pos", dev), pos0, rows, qo, qos,
+        ko, kos, _raw_stream(stream, dev))
 
 
 def o1_lin_state_bytes(g: o1_lin_geom, slots: int) -> int:
@@ -424,11 +446,17 @@ def o1_lin_scratch_bytes(g: o1_lin_geom, rows: int, seqs: int = 1) -> int:
     return int(LIB.o1_lin_scratch_bytes(ctypes.byref(g), int(rows), int(seqs)))
 
 
-def _lin_state(state, g: o1_lin_geom):
-    """Pointer and slots of a linear layer's state [slots, nh, d, dv]."""
-    if not isinstance(state, torch.Tensor) or tuple(state.shape[1:]) != (g.nh, g.d, g.dv):
-        raise ValueError(f"state: need a [slots, {g.nh}, {g.d}, {g.dv}] tensor")
-    return _dev(_here(state, "state"), None, "state"), state.shape[0]
+def _lin_tensors(state, g: o1_lin_geom, q, k, v, out, log_decay, dev: int):
+    """The C arguments of a linear layer's tensors: state and slots; q, k, v
+    with their strides; the decays; out with its stride; rows."""
+    G, nh, d, dv, dt = g.groups, g.nh, g.d, g.dv, g.dtype
+    if not isinstance(state, torch.Tensor) or state.shape[1:] != (nh, d, dv):
+        raise ValueError(f"state: need a [slots, {nh}, {d}, {dv}] tensor")
+    rows = q.shape[0]
+    return ((_flat(state, 1, torch.float32, "state", dev), state.shape[0]),
+            (*_rows(q, nh, d, dt, rows, "q", dev), *_rows(k, G, d, dt, rows, "k", dev), *_rows(v, G, dv, dt, rows, "v", dev),
+             _flat(log_decay, nh, torch.float32, "log_decay", dev)),
+            _rows(out, nh, dv, dt, rows, "out", dev), rows)
 
 
 def o1_lin_chunk_attend(state, g: o1_lin_geom, scratch, q, k, v, log_decay, seqs, out, stream=None) -> int:
@@ -436,26 +464,19 @@ def o1_lin_chunk_attend(state, g: o1_lin_geom, scratch, q, k, v, log_decay, seqs
     triples or what ``lin_seqs`` made of them."""
     if not isinstance(seqs, ctypes.Array):
         seqs = lin_seqs(seqs)
-    rows, nh = q.shape[0], g.nh
-    sp, slots = _lin_state(state, g)
-    (qp, qs), (kp, ks) = _rows(q, nh, g.d, g.dtype, rows, "q"), _rows(k, g.groups, g.d, g.dtype, rows, "k")
-    (vp, vs), (op, os_) = _rows(v, g.groups, g.dv, g.dtype, rows, "v"), _rows(out, nh, g.dv, g.dtype, rows, "out")
-    return LIB.o1_lin_chunk_attend(
-        sp, slots, ctypes.byref(g), _dev(_here(scratch, "scratch"), None, "scratch", dtype=None),
-        scratch.numel() * scratch.element_size(), qp, qs, kp, ks, vp, vs,
-        _dev(_here(log_decay, "log_decay"), nh, "log_decay"), seqs, len(seqs), op, os_, rows, _stream(stream))
+    dev = torch.cuda.current_device()
+    st, ins, o, rows = _lin_tensors(state, g, q, k, v, out, log_decay, dev)
+    return LIB.o1_lin_chunk_attend(*st, ctypes.byref(g), _flat(scratch, 1, scratch.dtype, "scratch", dev), scratch.nbytes,
+                                   *ins, seqs, len(seqs), *o, rows, _raw_stream(stream, dev))
 
 
 def o1_lin_token_attend(state, g: o1_lin_geom, q, k, v, log_decay, slots, out, stream=None) -> int:
     """One row of each sequence: row r on state slot slots[r] (int32 tensor;
     None: slot r; outside [0, slots): padding)."""
-    rows, nh = q.shape[0], g.nh
-    sp, n_slots = _lin_state(state, g)
-    (qp, qs), (kp, ks) = _rows(q, nh, g.d, g.dtype, rows, "q"), _rows(k, g.groups, g.d, g.dtype, rows, "k")
-    (vp, vs), (op, os_) = _rows(v, g.groups, g.dv, g.dtype, rows, "v"), _rows(out, nh, g.dv, g.dtype, rows, "out")
-    return LIB.o1_lin_token_attend(
-        sp, n_slots, ctypes.byref(g), qp, qs, kp, ks, vp, vs, _dev(_here(log_decay, "log_decay"), nh, "log_decay"),
-        _dev(_here(slots, "slots"), rows, "slots", dtype=torch.int32), op, os_, rows, _stream(stream))
+    dev = torch.cuda.current_device()
+    st, ins, o, rows = _lin_tensors(state, g, q, k, v, out, log_decay, dev)
+    return LIB.o1_lin_token_attend(*st, ctypes.byref(g), *ins, _flat(slots, rows, torch.int32, "slots", dev), *o, rows,
+                                   _raw_stream(stream, dev))
 
 
 def o1_lin_flags(clear: bool = False, stream=None) -> int:
