@@ -172,16 +172,10 @@ size_t slot_floats(const o1_lin_geom &g) {
 // Sequences of up to LIN_ROW_MAX rows take the row kernel, longer ones the
 // chunk kernels.
 constexpr int LIN_ROW_MAX = 32;
-// A pass's states: written, read, rewritten and read again, so they are
+// A pass's scratch is written, read, rewritten and read again, so passes are
 // kept to what stays in the L2.
-constexpr size_t LIN_PASS_BYTES = (size_t)64 << 20;
-
-// States of a pass that a scratch of `bytes` holds.
-size_t pass_states(const o1_lin_geom &g, size_t bytes) {
-    const size_t per = slot_floats(g) * 4;
-    const size_t lim = LIN_PASS_BYTES / per > 1 ? LIN_PASS_BYTES / per : 1, fit = bytes / per;
-    return fit < lim ? fit : lim;
-}
+const size_t LIN_PASS_BYTES = (size_t)(getenv("LIN_MB") ? atoi(getenv("LIN_MB")) : 64) << 20;
+constexpr int64_t LIN_PASS_ROWS = 1 << 24;   // and their counts to 32 bits
 
 int seg_rows(const o1_lin_geom &g) {
     const char *e = getenv("LIN_SEG");
@@ -252,9 +246,12 @@ size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots) {
 
 size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs) {
     if (!lin_geom_ok(geom) || rows < 1 || seqs < 1) return 0;
-    const size_t per = slot_floats(*geom) * 4, most = (size_t)rows / LIN_CHUNK + (size_t)seqs;
-    const size_t lim = pass_states(*geom, SIZE_MAX);
-    return o1_al256((most < lim ? most : lim) * per);
+    // segments of LIN_CHUNK rows are the most states any split into segments takes
+    const int64_t segs = (int64_t)rows / LIN_CHUNK + seqs, prows = (int64_t)rows + 16 * (int64_t)seqs;
+    const size_t one = lin_pass_bytes(*geom, 1, LIN_CHUNK);
+    const size_t lim = one > LIN_PASS_BYTES ? one : LIN_PASS_BYTES;
+    const size_t all = lin_pass_bytes(*geom, segs < INT_MAX ? (int)segs : INT_MAX, prows);
+    return all < lim ? all : lim;
 }
 
 int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, void *scratch, size_t scratch_bytes,
@@ -274,11 +271,12 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     if (rc != O1_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     a.wait_cycles = o1_wait_limit();
-    const int cap = (int)pass_states(g, scratch_bytes);
     a.seg = seg_rows(g);
+    const size_t one = lin_pass_bytes(g, 1, LIN_CHUNK), lim = one > LIN_PASS_BYTES ? one : LIN_PASS_BYTES;
+    const size_t cap = scratch_bytes < lim ? scratch_bytes : lim;
     LinTable rows;
     LinWorkTable work;
-    int n = 0, segs = 0, tiles = 0;
+    int n = 0, segs = 0, tiles = 0, prows = 0;
     bool launched = true;
     work.n = 0;
     auto flush_rows = [&]() {
@@ -286,8 +284,14 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
         n = 0;
     };
     auto flush_chunks = [&]() {
-        if (work.n && !lin_launch_pass(a, g.dtype, work, segs, tiles, (float *)scratch, st)) launched = false;
-        work.n = segs = tiles = 0;
+        if (work.n && !lin_launch_pass(a, g.dtype, work, segs, tiles, prows, scratch, st)) launched = false;
+        work.n = segs = tiles = prows = 0;
+    };
+    auto up = [](int64_t x, int m) { return (int)((x + m - 1) / m); };
+    // whether the pass takes r more rows of a sequence
+    auto fits = [&](int64_t r) {
+        const int64_t p = prows + 16 * (int64_t)up(r, 16);
+        return p <= LIN_PASS_ROWS && lin_pass_bytes(g, segs + up(r, a.seg), p) <= cap;
     };
     for (int i = 0; i < n_seq; ++i) {
         const o1_lin_seq &s = seqs[i];
@@ -298,12 +302,31 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
             continue;
         }
         for (int off = 0; off < s.rows;) {
-            if (segs == cap || work.n == LIN_TABLE) flush_chunks();
-            const int64_t most = (int64_t)(cap - segs) * a.seg;
-            const int take = s.rows - off < most ? s.rows - off : (int)most;
-            work.w[work.n++] = {s.row0 + off, take, s.slot, segs, tiles};
-            segs += (take + a.seg - 1) / a.seg;
-            tiles += (take + LIN_CHUNK - 1) / LIN_CHUNK;
+            // the rest of the sequence, or as many whole segments, tiles, or
+            // (in an empty pass) steps of 16 rows as fit
+            int take = s.rows - off;
+            for (const int m : {a.seg, LIN_CHUNK, 16}) {
+                if (work.n == LIN_TABLE) break;
+                if (fits(take)) break;
+                int lo = 0, hi = take / m;
+                while (lo < hi) {
+                    const int mid = lo + (hi - lo + 1) / 2;
+                    if (fits((int64_t)mid * m)) lo = mid;
+                    else hi = mid - 1;
+                }
+                take = lo * m;
+                if (take || work.n) break;
+                if (m != 16) take = s.rows - off;
+            }
+            if (!take || work.n == LIN_TABLE) {
+                if (!work.n) return O1_ERR_ARG;   // not reached: the least scratch holds 16 rows
+                flush_chunks();
+                continue;
+            }
+            work.w[work.n++] = {s.row0 + off, take, s.slot, segs, tiles, prows};
+            segs += up(take, a.seg);
+            tiles += up(take, LIN_CHUNK);
+            prows += 16 * up(take, 16);
             off += take;
         }
     }

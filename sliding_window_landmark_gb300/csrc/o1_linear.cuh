@@ -16,9 +16,10 @@ struct LinTable {
 #define LIN_SMS 152
 // A piece of a sequence in a pass of the chunk kernels: its rows in segments
 // of LinArgs::seg (a multiple of LIN_CHUNK), on the scratch's states seg0,
-// seg0 + 1, ..., and in tiles tile0, tile0 + 1, ... of LIN_CHUNK rows.
+// seg0 + 1, ..., in tiles tile0, tile0 + 1, ... of LIN_CHUNK rows, and, for
+// types that are split, in the panels' rows from prow0 on (a multiple of 16).
 struct LinWork {
-    int32_t row0, rows, slot, seg0, tile0;
+    int32_t row0, rows, slot, seg0, tile0, prow0;
 };
 struct LinWorkTable {
     int32_t n;
@@ -54,10 +55,28 @@ __device__ __forceinline__ float lin_pow(float g, int n) {
     return fmaf(y, e, y);
 }
 
-// One pass of the chunk kernels (o1_linear_tc.cu) over the pieces of a table,
-// `segs` segments and `tiles` tiles in all; inc: [segs][nh][d][dv] fp32
-// scratch. Launches only; false where a tensor map cannot be made.
-bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, float *inc,
+// Scratch of a pass: per segment, the increments (fp32, overwritten by two bf16
+// terms of the entering states) and, for fp32, their third terms; then, for
+// types of more than one bf16 term, the rows' term panels (per row).
+static inline int lin_terms(int dtype) { return dtype == O1_BF16 ? 1 : dtype == O1_F16 ? 2 : 3; }
+struct LinStates {
+    size_t inc, third;
+};
+static inline LinStates lin_pass_states(int nh, int d, int dv, int dtype, int segs) {
+    const size_t n = (size_t)segs * nh * d * dv;
+    return {o1_al256(4 * n), dtype == O1_F32 ? o1_al256(2 * n) : 0};
+}
+static inline size_t lin_pass_bytes(const o1_lin_geom &g, int segs, int64_t prows) {
+    const int nt = lin_terms(g.dtype), nh = g.groups * g.heads_per_group;
+    const LinStates s = lin_pass_states(nh, g.d, g.dv, g.dtype, segs);
+    const size_t row = (size_t)(nh + g.groups) * g.d + (size_t)g.groups * g.dv;
+    return s.inc + s.third + (nt > 1 ? o1_al256((size_t)prows * row * 2 * nt) : 0);
+}
+
+// One pass of the chunk kernels (o1_linear_tc.cu) over the pieces of a table:
+// `segs` segments, `tiles` tiles and `prows` panel rows in all, in a scratch of
+// lin_pass_bytes. Launches only; false where a tensor map cannot be made.
+bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, int prows, void *scratch,
                      cudaStream_t st);
 // Flags its kernels raised on the current device (O1_FLAG_WAIT_EXPIRED), and
 // their reset.

@@ -45,6 +45,12 @@ constexpr int PROD_WARPS = 8, PROD = 32 * PROD_WARPS;
 constexpr int LIST = 64;  // units of a CTA, decoded once at its start
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void tmem_alloc512(uint32_t *slot) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(slot)), "r"(512)
                  : "memory");
@@ -150,12 +156,7 @@ struct Panel {
 #pragma unroll
             for (int j = 0; j < W; ++j) raw[i * W + j] = STEP * i < nr ? ((const uint4 *)p)[j] : make_uint4(0, 0, 0, 0);
     }
-    // as they are (bf16 in one term); dst: the panel + off(pt)
-    static __device__ __forceinline__ void copy(const uint4 *raw, unsigned char *dst) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) *(uint4 *)(dst + i * STEP * 128) = raw[i];
-    }
-    // NT terms of w[i] * x, w the weights of this thread's rows
+    // NT terms of w[i] * x, w the weights of this thread's rows; dst: the panel + off(pt)
     template <int NT>
     static __device__ __forceinline__ void split(const uint4 *raw, unsigned char *dst, const float (&w)[IT]) {
 #pragma unroll
@@ -167,20 +168,6 @@ struct Panel {
             store_terms<NT>(dst + i * STEP * 128, ROWS * COLS * 2, x);
         }
     }
-    // NT terms of x
-    template <int NT>
-    static __device__ __forceinline__ void put(const uint4 *raw, unsigned char *dst) {
-        if constexpr (NT == 1) {
-            copy(raw, dst);
-        } else {
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                float x[8];
-                words_floats(raw + i * W, x, (const T *)nullptr);
-                store_terms<NT>(dst + i * STEP * 128, ROWS * COLS * 2, x);
-            }
-        }
-    }
 };
 
 // MMAs over `steps` steps of 16 of the contraction for the term pairs
@@ -189,10 +176,12 @@ struct Panel {
 // the corrections are 2^-8 of the whole, so that in an accumulator of their own
 // (where the result is fp32) they round at that much smaller a size. a, b:
 // descriptors (a: TMEM address where TS) of step 0 of term 0; AT, AS, BT, BS:
-// what a term and a step add. One thread issues, so a step is an addition or
-// two and the MMA: with descriptors built in place a step took 198 cycles.
+// what a term and a step add. The whole warp takes the loop and the elected
+// lane (`e`) the MMA: warp-uniform control flow keeps the operands in uniform
+// registers, and a 128 x 128 x 16 MMA issues every 64 cycles, its rate; from
+// one lane's branch it took 86 (and with descriptors built in place 198).
 template <int TA, int TB, int MAXS, bool TS, int AT, int AS, int BT, int BS, typename A>
-__device__ __forceinline__ void issue(uint32_t d, uint32_t dc, uint32_t id, int steps, bool acc, A a, uint64_t b) {
+__device__ __forceinline__ void issue(bool e, uint32_t d, uint32_t dc, uint32_t id, int steps, bool acc, A a, uint64_t b) {
     bool accc = acc;
 #pragma unroll
     for (int sum = MAXS; sum >= 0; --sum)
@@ -202,20 +191,20 @@ __device__ __forceinline__ void issue(uint32_t d, uint32_t dc, uint32_t id, int 
             if (tb < 0 || tb >= TB) continue;
             const bool main = sum == 0 && dc != d;
             const uint32_t dst = main ? d : dc;
-            auto one = [&](int s, uint32_t ac) {
-                if constexpr (TS) mma_ts(dst, a + (uint32_t)(ta * AT + s * AS), b + (uint64_t)(tb * BT + s * BS), id, ac);
-                else mma_ss(dst, a + (uint64_t)(ta * AT + s * AS), b + (uint64_t)(tb * BT + s * BS), id, ac);
-            };
-            one(0, main ? acc : accc);
-            if (!main) accc = true;
-            if (steps >= 4) {
-                one(1, 1u);
-                one(2, 1u);
-                one(3, 1u);
-                for (int s = 4; s < steps; ++s) one(s, 1u);
-            } else {
-                for (int s = 1; s < steps; ++s) one(s, 1u);
+            A pa = a + (A)(ta * AT);
+            uint64_t pb = b + (uint64_t)(tb * BT);
+            uint32_t ac = main ? acc : accc;
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k) {
+                if (e) {
+                    if constexpr (TS) mma_ts(dst, pa, pb, id, ac);
+                    else mma_ss(dst, pa, pb, id, ac);
+                }
+                pa += AS;
+                pb += BS;
+                ac = 1;
             }
+            if (!main) accc = true;
         }
 }
 
@@ -252,46 +241,99 @@ __device__ __forceinline__ void store_block(float *stage, const float (&x)[32], 
     }
 }
 
-// TMA warp, all lanes: `boxes` boxes of ROWS rows x 64 columns of a bf16 row
-// tensor into slot bytes dst (block after block), published on `full`. Rows
-// from nr on are another sequence's or padding: the MMAs take them up to the
-// next multiple of 16 under zero weights, which would still spread a NaN, so
-// where nr cuts a step of 16 the rows are zeroed after the copy has landed (the
-// slot is published then).
-template <int ROWS>
-__device__ __forceinline__ bool tma_rows(unsigned char *dst, const CUtensorMap *map, int col, int head, int row, int boxes,
-                                         int nr, uint64_t *full, uint64_t *tail, uint32_t &tail_phase, volatile int *abort,
-                                         long long limit, int lane) {
-    const bool cut = nr < ROWS && nr % 16;
+// Panels by TMA (one warp, all lanes): rows row .. row + ROWS - 1 and `boxes`
+// blocks of 64 columns of each of NT terms of a row panel, term t to dst + t *
+// PANEL, published on `full`. The MMAs take value rows up to the next multiple
+// of 16 past nr under zero weights. A split panel holds zeros there; a bf16
+// tensor is read in place, and its rows from nr on are another sequence's or
+// padding, which under a zero weight would still spread a NaN: where nr cuts
+// a step of 16 the rows are zeroed after the copy has landed, and the slot is
+// published then.
+template <int NT, int ROWS, int PANEL>
+__device__ __forceinline__ void tma_panel(unsigned char *dst, const CUtensorMap *map, int col, int head, int row, int boxes,
+                                          uint64_t *bar, int lane) {
+    if (lane == 0)
+        for (int t = 0; t < NT; ++t)
+            for (int i = 0; i < boxes; ++i)
+                tma_4d(dst + t * PANEL + i * ROWS * 128, map, col + 64 * i, head, row, t, bar);
+}
+template <int NT, int ROWS, int PANEL>
+__device__ __forceinline__ bool tma_values(unsigned char *dst, const CUtensorMap *map, int col, int head, int row, int boxes,
+                                           int nr, uint64_t *full, uint64_t *tail, uint32_t &tail_phase,
+                                           volatile int *abort, int lane) {
+    const bool cut = NT == 1 && nr < ROWS && nr % 16;
     uint64_t *bar = cut ? tail : full;
-    if (lane == 0) {
-        mbar_expect_tx(bar, boxes * ROWS * 128);
-        for (int i = 0; i < boxes; ++i) tma_3d(dst + i * ROWS * 128, map, col + 64 * i, head, row, bar);
-    }
-    __syncwarp();
+    if (lane == 0) mbar_expect_tx(bar, NT * boxes * ROWS * 128);
+    tma_panel<NT, ROWS, PANEL>(dst, map, col, head, row, boxes, bar, lane);
     if (!cut) return true;
+    __syncwarp();
     // in flight: waited for with the full limit
     const bool ok = __all_sync(0xffffffffu, mbar_wait(tail, tail_phase, abort, O1_WAIT_CYCLES_FULL));
+    if (!ok) mbar_drain(tail, tail_phase);
     tail_phase ^= 1;
-    if (!ok) {
-        mbar_drain(tail, tail_phase ^ 1);
-        return false;
-    }
-    for (int i = lane; i < (ceil16(nr) - nr) * 8 * boxes; i += 32) {
-        const int r = nr + (i >> 3) % (ceil16(nr) - nr), b = (i >> 3) / (ceil16(nr) - nr);
+    const int z = ceil16(nr) - nr;   // rows of zeros
+    for (int i = lane; i < z * 8 * boxes; i += 32) {
+        const int r = nr + (i >> 3) % z, b = (i >> 3) / z;
         *(uint4 *)(dst + b * ROWS * 128 + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(full);
-    return true;
+    return ok;
+}
+
+// ------------------------------------------------------------------ split
+
+// Rows of q, k and v as the bf16 terms the MMAs take (types of more than one
+// term): panels [NT][prows][heads][width], a piece's rows from prow0 on, padded
+// with zeros to a multiple of 16. A block a row. Done once, where each
+// key would otherwise be split again by every tile, head and column block that
+// reads it (12 times for 4 heads a group of 256 columns).
+struct SplitArgs {
+    uint16_t *q, *k, *v;
+    int prows;
+};
+template <typename T>
+__global__ __launch_bounds__(256) void k_lin_split(LinArgs a, const __grid_constant__ LinWorkTable t, SplitArgs s) {
+    constexpr int NT = Terms<T>::in;
+    const int pr = blockIdx.x;
+    const LinWork &w = find_piece(t, pr, [](const LinWork &p) { return p.prow0; });
+    const int r = pr - w.prow0;
+    const bool in = r < w.rows;
+    const size_t row = (size_t)w.row0 + r;
+    const int nq = a.nh * a.d / 8, nk = a.G * a.d / 8, nv = a.G * a.dv / 8;
+    for (int i = threadIdx.x; i < nq + nk + nv; i += 256) {
+        const T *src;
+        uint16_t *dst;
+        int n, c = i;
+        if (c < nq) {
+            src = (const T *)a.q + row * a.qs, dst = s.q, n = nq;
+        } else if ((c -= nq) < nk) {
+            src = (const T *)a.k + row * a.ks, dst = s.k, n = nk;
+        } else {
+            c -= nk;
+            src = (const T *)a.v + row * a.vs, dst = s.v, n = nv;
+        }
+        uint4 raw[WORDS<T>];
+#pragma unroll
+        for (int j = 0; j < WORDS<T>; ++j) raw[j] = in ? ((const uint4 *)(src + 8 * c))[j] : make_uint4(0, 0, 0, 0);
+        float x[8];
+        words_floats(raw, x, (const T *)nullptr);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = take_pair(x[2 * e], x[2 * e + 1]);
+            *(uint4 *)(dst + ((size_t)m * s.prows + pr) * n * 8 + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+    }
 }
 
 // ------------------------------------------------------------- increments
 
 // One unit: dS[d0 .. +128][v0 .. +N] of (segment, head).
 struct IncUnit {
-    int row0, nr, seg, h, g, d0, v0;
+    int row0, prow, nr, seg, h, g, d0, v0;   // prow: first row in the panels
 };
 
 // N columns of dv a unit: 256 for bf16 values (the weighted keys are then
@@ -299,7 +341,6 @@ struct IncUnit {
 template <typename T, int N>
 struct IncCfg {
     static constexpr int NT = Terms<T>::in;
-    static constexpr bool TMA = NT == 1;            // values by TMA, as they are
     static constexpr int NB = N == 128 ? 2 : 1;     // accumulators: main and corrections, N columns each
     static constexpr int KSLOT = 3 * KV * TN * 2, NK = 2;
     static constexpr int VSLOT = NT * KV * N * 2, NV = NT == 3 ? 2 : 3;
@@ -310,8 +351,8 @@ struct IncCfg {
 // dS of every (segment, head): A = weighted keys (M = d), B = values (N = dv),
 // both MN-major, contraction over the rows, 64 of them a step. Persistent: a
 // CTA takes units in turn. Warps: 0-3 store a finished unit, 4 issues the
-// MMAs, 5 the values' TMA, 6-13 stage the weighted keys (and the values that
-// are split), running ahead over the rings.
+// MMAs, 5 the values' TMA, 6-13 stage the weighted keys, running ahead over
+// the rings.
 template <typename T, int N>
 __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs a, const __grid_constant__ LinWorkTable t,
                                                                       const __grid_constant__ CUtensorMap mv, int units,
@@ -334,7 +375,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             mbar_init(&kempty[i], 1);
         }
         for (int i = 0; i < NV; ++i) {
-            mbar_init(&vfull[i], C::TMA ? 1 : PROD_WARPS);
+            mbar_init(&vfull[i], 1);
             mbar_init(&vempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -361,6 +402,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         const LinWork &w = find_piece(t, x.seg, [](const LinWork &p) { return p.seg0; });
         const int off = (x.seg - w.seg0) * a.seg;
         x.row0 = w.row0 + off;
+        x.prow = (NT == 1 ? w.row0 : w.prow0) + off;
         x.nr = min(a.seg, w.rows - off);
         list[tid - 64] = x;
     }
@@ -376,15 +418,11 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         using P = Panel<T, KV, TN>;
         const uint32_t pt = tid - 192, off = P::off(pt), prow = P::row(pt);
         uint4 ra[4 * WORDS<T>], rb[4 * WORDS<T>];
-        int ik = 0, iv = 0;
+        int ik = 0;
         bool ok = true;
         auto load_k = [&](uint4 *r, const IncUnit &x, int s) {
             P::load(r, (const T *)a.k + (size_t)(x.row0 + KV * s) * a.ks + (size_t)x.g * a.d + x.d0, a.ks, x.nr - KV * s,
                     a.d - x.d0, pt);
-        };
-        auto load_v = [&](uint4 *r, const IncUnit &x, int s) {
-            P::load(r, (const T *)a.v + (size_t)(x.row0 + KV * s) * a.vs + (size_t)x.g * a.dv + x.v0, a.vs, x.nr - KV * s,
-                    a.dv - x.v0, pt);
         };
         float g = 0.f, gstep = 0.f;
         // weights e^{g (nr - 1 - row)} of the thread's rows, from the last
@@ -405,16 +443,6 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             if (lane == 0) mbar_arrive(&kfull[b]);
             ++ik;
         };
-        auto store_v = [&](const uint4 *r) {
-            const int b = iv % NV;
-            ok = __all_sync(0xffffffffu, mbar_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl));
-            if (!ok) return;
-            P::template put<NT>(r, sV + b * C::VSLOT + off);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&vfull[b]);
-            ++iv;
-        };
         IncUnit x = list[0], y;
         load_k(ra, x, 0);
         for (int n = 0; n < count && ok; ++n, x = y) {
@@ -422,77 +450,69 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             g = a.decay[x.h];
             gstep = lin_pow(g, P::STEP);
             y = list[n + 1 < count ? n + 1 : n];
-            if constexpr (C::TMA) {
-                for (int s = 0; s < ns; s += 2) {   // two buffers in turn
-                    if (s + 1 < ns) load_k(rb, x, s + 1);
-                    store_k(ra, x, s);
-                    if (!ok) break;
-                    if (s + 2 < ns) load_k(ra, x, s + 2);
-                    else if (n + 1 < count) load_k(ra, y, 0);
-                    if (s + 1 < ns) store_k(rb, x, s + 1);
-                    if (!ok) break;
-                }
-            } else {
-                for (int s = 0; s < ns; ++s) {
-                    load_v(rb, x, s);
-                    store_k(ra, x, s);
-                    if (!ok) break;
-                    if (s + 1 < ns) load_k(ra, x, s + 1);
-                    else if (n + 1 < count) load_k(ra, y, 0);
-                    store_v(rb);
-                    if (!ok) break;
-                }
+            // two buffers in turn, a unit's first panel in ra
+            for (int s = 0; s < ns; s += 2) {
+                if (s + 1 < ns) load_k(rb, x, s + 1);
+                store_k(ra, x, s);
+                if (!ok) break;
+                if (s + 2 < ns) load_k(ra, x, s + 2);
+                else if (n + 1 < count) load_k(ra, y, 0);
+                if (s + 1 < ns) store_k(rb, x, s + 1);
+                if (!ok) break;
             }
         }
     } else if (warp == 5) {
         // ------------------------------------------------- TMA of the values
-        if constexpr (C::TMA) {
-            int iv = 0;
-            uint32_t tp = 0;
-            bool ok = true;
-            for (int n = 0; n < count && ok; ++n) {
-                const IncUnit x = list[n];
-                const int boxes = (min(N, a.dv - x.v0) + 63) / 64;
-                for (int s = 0; KV * s < x.nr && ok; ++s) {
-                    const int b = iv % NV;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl)) &&
-                         tma_rows<KV>(sV + b * C::VSLOT, &mv, x.v0, x.g, x.row0 + KV * s, boxes, x.nr - KV * s, &vfull[b],
-                                      &tail, tp, abort, wl, lane);
-                    if (ok) ++iv;
-                }
+        int iv = 0;
+        uint32_t tp = 0;
+        bool ok = true;
+        for (int n = 0; n < count && ok; ++n) {
+            const IncUnit x = list[n];
+            const int boxes = (min(N, a.dv - x.v0) + 63) / 64;
+            for (int s = 0; KV * s < x.nr && ok; ++s, ++iv) {
+                const int b = iv % NV;
+                ok = __all_sync(0xffffffffu, mbar_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl));
+                if (!ok) break;
+                ok = tma_values<NT, KV, KV * N * 2>(sV + b * C::VSLOT, &mv, x.v0, x.g, x.prow + KV * s, boxes, x.nr - KV * s,
+                                                    &vfull[b], &tail, tp, abort, lane);
             }
-            // after an abort: copies published on their slots may be in flight
-            if (!ok && lane == 0)
-                for (int i = max(0, iv - NV); i < iv; ++i) mbar_drain(&vfull[i % NV], (i / NV) & 1);
         }
+        // copies published on their slots are over before the block ends
+        if (lane == 0)
+            for (int i = max(0, iv - NV); i < iv; ++i) mbar_drain(&vfull[i % NV], (i / NV) & 1);
     } else if (warp == 4) {
         // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            const uint32_t k0 = su32(sK), v0 = su32(sV);
-            constexpr int KTERM = KV * TN * 2 / 16, VTERM = KV * N * 2 / 16;
-            for (int n = 0; n < count && ok; ++n) {
-                const int nr = list[n].nr;
-                const uint32_t id = idesc_bf16(128, min(N, ceil16(a.dv - list[n].v0)), 1, 1);
-                const uint32_t d = tmem + (n % C::NB) * 2 * N;
-                ok = mbar_wait(&freed[n % C::NB], ((n / C::NB) & 1) ^ 1, abort, wl);
-                for (int s = 0; KV * s < nr && ok; ++s, ++it) {
-                    const int bk = it % NK, bv = it % NV;
-                    ok = mbar_wait(&kfull[bk], (it / NK) & 1, abort, wl) && mbar_wait(&vfull[bv], (it / NV) & 1, abort, wl);
-                    if (!ok) break;
-                    tc_after();
-                    issue<3, NT, 2, false, KTERM, 128, VTERM, 128>(d, d + N, id, min(KV, ceil16(nr - KV * s)) / 16, s > 0,
-                                                                   desc_sw128_mn(k0 + bk * C::KSLOT, KV * 128),
-                                                                   desc_sw128_mn(v0 + bv * C::VSLOT, KV * 128));
+        const bool e = elect_one();
+        int it = 0;
+        bool ok = true;
+        const uint32_t k0 = su32(sK), v0 = su32(sV);
+        constexpr int KTERM = KV * TN * 2 / 16, VTERM = KV * N * 2 / 16;
+        for (int n = 0; n < count && ok; ++n) {
+            const int nr = list[n].nr;
+            const uint32_t id = idesc_bf16(128, min(N, ceil16(a.dv - list[n].v0)), 1, 1);
+            const uint32_t d = tmem + (n % C::NB) * 2 * N;
+            ok = __all_sync(0xffffffffu, mbar_wait(&freed[n % C::NB], ((n / C::NB) & 1) ^ 1, abort, wl));
+            for (int s = 0; KV * s < nr && ok; ++s, ++it) {
+                const int bk = it % NK, bv = it % NV;
+                ok = __all_sync(0xffffffffu, mbar_wait(&kfull[bk], (it / NK) & 1, abort, wl) &&
+                                                 mbar_wait(&vfull[bv], (it / NV) & 1, abort, wl));
+                if (!ok) break;
+                tc_after();
+                issue<3, NT, 2, false, KTERM, 128, VTERM, 128>(e, d, d + N, id, min(KV, ceil16(nr - KV * s)) / 16, s > 0,
+                                                               desc_sw128_mn(k0 + bk * C::KSLOT, KV * 128),
+                                                               desc_sw128_mn(v0 + bv * C::VSLOT, KV * 128));
+                if (e) {
                     mma_commit(&kempty[bk]);
                     mma_commit(&vempty[bv]);
                 }
-                if (ok) mma_commit(&done[n % C::NB]);
             }
+            if (ok && e) mma_commit(&done[n % C::NB]);
+        }
+        if (e) {
             mma_commit(&fin);   // tracks every MMA issued, also after an abort
             mbar_drain(&fin, 0);
         }
+        __syncwarp();
     } else {
         // -------------------------------------------------------- epilogue
         bool ok = true;
@@ -503,6 +523,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             tc_after();
             float *o = inc + ((size_t)x.seg * a.nh + x.h) * a.d * a.dv + (size_t)(x.d0 + 32 * warp) * a.dv + x.v0;
             const int nr = a.d - x.d0 - 32 * warp, wv = min(N, a.dv - x.v0);
+#pragma unroll 1
             for (int c = 0; c < wv; c += 32) {
                 float y[32];
                 if (ok) {
@@ -534,14 +555,15 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
 
 // Per state element, over a piece's segments: the increment is replaced by
 // the state entering the segment, S <- l^n S + dS, the last S goes to its
-// slot. TERMS: the entering state is stored as the two bf16 terms that the
-// outputs multiply, in the same bytes: each row of dv values as dv first
-// terms, then dv second ones. A row is one warp's (a lane the columns 4 lane
-// and 128 + 4 lane), so that it is read before it is overwritten. Bound: the
-// scratch's bytes, read and written once; 4 segments' loads go out ahead of
-// their use.
-template <bool TERMS>
-__global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_constant__ LinWorkTable t, float *inc) {
+// slot. The entering state is stored as the bf16 terms that the outputs
+// multiply: two in the increment's own bytes, each row of dv values as dv
+// first terms, then dv second ones (a row is one warp's, a lane the columns 4
+// lane and 128 + 4 lane, so that it is read before it is overwritten), a
+// third in `third` [states][d][dv]. Bound: the scratch's bytes, read and
+// written once; 4 segments' loads go out ahead of their use.
+template <int MT>
+__global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_constant__ LinWorkTable t, float *inc,
+                                                  uint16_t *third) {
     const LinWork w = t.w[blockIdx.z];
     const int h = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= a.d) return;
@@ -564,7 +586,7 @@ __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_consta
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 if (c + i < nc && in[j]) x[i][j] = *(const float4 *)(p + (size_t)(c + i) * step + 4 * lane + 128 * j);
-        if (TERMS) __syncwarp();
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (c + i >= nc) break;
@@ -574,15 +596,14 @@ __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_consta
             for (int j = 0; j < 2; ++j) {
                 if (!in[j]) continue;
                 const int col = 4 * lane + 128 * j;
-                if (TERMS) {
-                    float4 y = s[j];
-                    const uint2 hi = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
-                    const uint2 lo = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
-                    *(uint2 *)((uint16_t *)q + col) = hi;
-                    *(uint2 *)((uint16_t *)q + a.dv + col) = lo;
-                } else {
-                    *(float4 *)(q + col) = s[j];
-                }
+                float4 y = s[j];
+                const uint2 t0 = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
+                const uint2 t1 = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
+                *(uint2 *)((uint16_t *)q + col) = t0;
+                *(uint2 *)((uint16_t *)q + a.dv + col) = t1;
+                if (MT == 3)
+                    *(uint2 *)(third + ((size_t)w.seg0 * a.nh + h) * n + (size_t)(c + i) * step + (size_t)row * a.dv + col) =
+                        make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
                 s[j].x = fmaf(s[j].x, l, x[i][j].x);
                 s[j].y = fmaf(s[j].y, l, x[i][j].y);
                 s[j].z = fmaf(s[j].z, l, x[i][j].z);
@@ -597,13 +618,12 @@ __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_consta
 
 // ---------------------------------------------------------------- outputs
 
-// Warps: 0-3 P (a thread a row), 4-7 epilogue, 8 MMA issuer, 9 TMA (bf16) or
-// 9-16 producers (types that are split).
+// Warps: 0-3 P (a thread a row), 4-7 epilogue, 8 MMA issuer, 9 TMA.
+constexpr int OUT_THREADS = 320;
 template <typename T>
 struct OutCfg {
     static constexpr int NT = Terms<T>::in, MT = Terms<T>::mid;
-    static constexpr bool TMA = NT == 1;       // panels by TMA, as they are; Q and K of a step share a slot
-    static constexpr int THREADS = 32 * (9 + (TMA ? 1 : PROD_WARPS));
+    static constexpr bool PAIR = NT == 1;      // Q and K of a step share a slot
     static constexpr int SLOT = NT == 3 ? 49152 : 32768, NSLOT = NT == 3 ? 4 : 6;
     static constexpr int VR = NT == 1 ? 128 : 64;   // value rows of a slot
     static constexpr bool SPLIT = NT == 3;     // corrections in accumulators of their own
@@ -620,7 +640,8 @@ struct OutCfg {
 // key tiles kt = 0 .. nkt - 1 of the segment up to its own rows (the last).
 struct OutTile {
     int row0, nr;        // query rows
-    int seg0row, seg;    // segment: first row, state
+    int prow, kprow;     // in the panels: the tile's and its segment's first row
+    int i0, seg;         // row in the segment; the segment's state
     int h, g, v0, nkt;
 };
 struct Cursor {
@@ -641,7 +662,7 @@ struct Cursor {
     }
     __device__ __forceinline__ bool diag() const { return kt == x.nkt - 1; }
     __device__ __forceinline__ int keys() const { return diag() ? x.nr : LIN_CHUNK; }
-    __device__ __forceinline__ int key0() const { return x.seg0row + LIN_CHUNK * kt; }
+    __device__ __forceinline__ int key0() const { return x.kprow + LIN_CHUNK * kt; }
 };
 
 // Outputs. Weights: with i0 the tile's first row and s0 its segment's,
@@ -653,12 +674,12 @@ struct Cursor {
 // next tile's q S_in) ahead of this unit's P V where TMEM holds two score
 // buffers, so that P is formed under them.
 template <typename T>
-__global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, const __grid_constant__ LinWorkTable t,
+__global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __grid_constant__ LinWorkTable t,
                                                                    const __grid_constant__ CUtensorMap mq,
                                                                    const __grid_constant__ CUtensorMap mk,
                                                                    const __grid_constant__ CUtensorMap mv,
-                                                                   const __grid_constant__ CUtensorMap ms, int tiles,
-                                                                   const float *inc) {
+                                                                   const __grid_constant__ CUtensorMap ms,
+                                                                   const __grid_constant__ CUtensorMap ms3, int tiles) {
     using C = OutCfg<T>;
     constexpr int NT = C::NT, MT = C::MT;
     extern __shared__ unsigned char smraw[];
@@ -674,7 +695,7 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
     const int count = (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;   // <= LIST
     if (tid == 0) {
         for (int i = 0; i < C::NSLOT; ++i) {
-            mbar_init(&full[i], C::TMA ? 1 : PROD_WARPS);
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -704,8 +725,10 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
         x.row0 = w.row0 + off;
         x.nr = min(LIN_CHUNK, w.rows - off);
         x.seg = w.seg0 + sl;
-        x.seg0row = w.row0 + sl * a.seg;
-        x.nkt = (off - sl * a.seg) / LIN_CHUNK + 1;
+        x.i0 = off - sl * a.seg;
+        x.prow = (NT == 1 ? w.row0 : w.prow0) + off;
+        x.kprow = x.prow - x.i0;
+        x.nkt = x.i0 / LIN_CHUNK + 1;
         list[tid - 64] = x;
     }
     tc_before();
@@ -720,232 +743,160 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
         // Ring items in order: per unit, for each step of d the Q and K
         // panels and (first unit of a tile) the entering state's; the unit's
         // values (a unit later where scores run ahead).
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true, vq = true, vv = true;
-            Cursor cq, cv;
-            cq.start(list);
-            cv.start(list);
-            const uint32_t base = su32(sm);
-            auto need = [&](int i) -> uint32_t {   // slot of ring item i, once filled
-                const int s = i % C::NSLOT;
-                ok = ok && mbar_wait(&full[s], (i / C::NSLOT) & 1, abort, wl);
-                return base + (uint32_t)s * C::SLOT;
-            };
-            auto done = [&](int i) { mma_commit(&empty[i % C::NSLOT]); };
-            // scores of a unit, and with a tile's first unit its q S_in
-            auto scores = [&]() {
-                const uint32_t x = tmem + C::x(cq.u), acc = tmem + C::acc(cq.n);
-                const uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cq.x.v0)), 0, 1);
-                for (int b = 0; b < nb; ++b) {
-                    const int steps = ceil16(min(KV, a.d - KV * b)) / 16, iq = it;
-                    const uint32_t q = need(it++), k = C::TMA ? q + 16384 : need(it++);
+        const bool e = elect_one();
+        int it = 0;
+        bool ok = true, vq = true, vv = true;
+        Cursor cq, cv;
+        cq.start(list);
+        cv.start(list);
+        const uint32_t base = su32(sm);
+        auto need = [&](int i) -> uint32_t {   // slot of ring item i, once filled
+            const int s = i % C::NSLOT;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s], (i / C::NSLOT) & 1, abort, wl));
+            return base + (uint32_t)s * C::SLOT;
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (e) mma_commit(bar);
+        };
+        auto done = [&](int i) { commit(&empty[i % C::NSLOT]); };
+        // scores of a unit, and with a tile's first unit its q S_in
+        auto scores = [&]() {
+            const uint32_t x = tmem + C::x(cq.u), acc = tmem + C::acc(cq.n);
+            const uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cq.x.v0)), 0, 1);
+            for (int b = 0; b < nb; ++b) {
+                const int steps = ceil16(min(KV, a.d - KV * b)) / 16, iq = it;
+                const uint32_t q = need(it++), k = C::PAIR ? q + 16384 : need(it++);
+                if (!ok) return;
+                tc_after();
+                const uint64_t qd = desc_sw128(q);
+                issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(e, x, x + C::CORR, id_x, steps, b > 0, qd, desc_sw128(k));
+                if (!C::PAIR) done(iq + 1);
+                if (b == nb - 1) commit(&sc_full[cq.u % C::XB]);
+                if (cq.kt == 0) {
+                    if (b == 0) ok = __all_sync(0xffffffffu, mbar_wait(&acc_free[cq.n % C::AB], ((cq.n / C::AB) & 1) ^ 1, abort, wl));
+                    const int is = it++;
+                    const uint32_t s0 = need(is);
                     if (!ok) return;
                     tc_after();
-                    const uint64_t qd = desc_sw128(q);
-                    issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(x, x + C::CORR, id_x, steps, b > 0, qd, desc_sw128(k));
-                    if (!C::TMA) done(iq + 1);
-                    if (b == nb - 1) mma_commit(&sc_full[cq.u % C::XB]);
-                    if (cq.kt == 0) {
-                        if (b == 0) ok = mbar_wait(&acc_free[cq.n % C::AB], ((cq.n / C::AB) & 1) ^ 1, abort, wl);
-                        const int is = it++;
-                        const uint32_t s0 = need(is);
-                        if (!ok) return;
-                        tc_after();
-                        issue<NT, MT, max_sum(NT, MT), false, 1024, 2, KV * TN * 2 / 16, 128>(
-                            acc, acc + C::CORR, id_a, steps, b > 0, qd, desc_sw128_mn(s0, KV * 128));
-                        done(is);
-                    }
-                    done(iq);
+                    issue<NT, MT, max_sum(NT, MT), false, 1024, 2, KV * TN * 2 / 16, 128>(
+                        e, acc, acc + C::CORR, id_a, steps, b > 0, qd, desc_sw128_mn(s0, KV * 128));
+                    done(is);
                 }
-                if (cq.kt == 0) mma_commit(&acc_ready[cq.n % C::AB]);
-                vq = cq.next(list, count);
-            };
-            auto values = [&]() {
-                const uint32_t x = tmem + C::x(cv.u), acc = tmem + C::acc(cv.n);
-                const uint32_t id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cv.x.v0)), 0, 1);
-                const int nk = cv.keys();
-                ok = mbar_wait(&p_full[cv.u % C::XB], (cv.u / C::XB) & 1, abort, wl);
-                for (int i = 0; i < LIN_CHUNK / C::VR; ++i) {
-                    const uint32_t v = need(it);
-                    if (!ok) return;
-                    tc_after();
-                    const int steps = min(C::VR, ceil16(max(0, nk - C::VR * i))) / 16;
-                    const uint64_t vd = desc_sw128_mn(v, C::VR * 128);
-                    constexpr int TERM = C::VR * TN * 2 / 16;
-                    if (steps > 0) {
-                        // P's terms 0 and 1 of 16 keys are 16 columns; the third's 8 lie apart
-                        if constexpr (MT == 3)
-                            issue<1, 1, 0, true, 0, 8, 0, 128>(acc + C::CORR, acc + C::CORR, id_a, steps, true,
-                                                               x + 128 + C::VR * i / 2, vd);
-                        issue<2, NT, max_sum(MT, NT), true, 8, 16, TERM, 128>(acc, acc + C::CORR, id_a, steps, true,
-                                                                             x + C::VR * i, vd);
-                    }
-                    done(it++);
-                }
-                if (cv.diag()) mma_commit(&o_done[cv.n % C::AB]);
-                else if (cv.kt == cv.x.nkt - 2) mma_commit(&acc_ready[cv.n % C::AB]);
-                vv = cv.next(list, count);
-            };
-            scores();
-            while (vv && ok) {
-                if (C::XB == 2 && vq) scores();
-                if (ok) values();
-                if (C::XB == 1 && vq && ok) scores();
+                done(iq);
             }
+            if (cq.kt == 0) commit(&acc_ready[cq.n % C::AB]);
+            vq = cq.next(list, count);
+        };
+        auto values = [&]() {
+            const uint32_t x = tmem + C::x(cv.u), acc = tmem + C::acc(cv.n);
+            const uint32_t id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cv.x.v0)), 0, 1);
+            const int nk = cv.keys();
+            ok = __all_sync(0xffffffffu, mbar_wait(&p_full[cv.u % C::XB], (cv.u / C::XB) & 1, abort, wl));
+            for (int i = 0; i < LIN_CHUNK / C::VR; ++i) {
+                const uint32_t v = need(it);
+                if (!ok) return;
+                tc_after();
+                const int steps = min(C::VR, ceil16(max(0, nk - C::VR * i))) / 16;
+                const uint64_t vd = desc_sw128_mn(v, C::VR * 128);
+                constexpr int TERM = C::VR * TN * 2 / 16;
+                if (steps > 0) {
+                    // P's terms 0 and 1 of 16 keys are 16 columns; the third's 8 lie apart
+                    if constexpr (MT == 3)
+                        issue<1, 1, 0, true, 0, 8, 0, 128>(e, acc + C::CORR, acc + C::CORR, id_a, steps, true,
+                                                           x + 128 + C::VR * i / 2, vd);
+                    issue<2, NT, max_sum(MT, NT), true, 8, 16, TERM, 128>(e, acc, acc + C::CORR, id_a, steps, true,
+                                                                         x + C::VR * i, vd);
+                }
+                done(it++);
+            }
+            if (cv.diag()) commit(&o_done[cv.n % C::AB]);
+            else if (cv.kt == cv.x.nkt - 2) commit(&acc_ready[cv.n % C::AB]);
+            vv = cv.next(list, count);
+        };
+        for (int ahead = 0; vv && ok;) {   // units scored, their P V not issued
+            if (vq && ahead < C::XB) {
+                scores();
+                ++ahead;
+            } else {
+                values();
+                --ahead;
+            }
+        }
+        if (e) {
             mma_commit(&fin);   // tracks every MMA issued, also after an abort
             mbar_drain(&fin, 0);
         }
-    } else if (warp > 8) {
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------------------- TMA
         int it = 0;
-        if constexpr (C::TMA) {
-            // -------------------------------------------------- TMA, one warp
-            bool ok = true, vq = true, vv = true;
-            uint32_t tp = 0;
-            Cursor cq, cv;
-            cq.start(list);
-            cv.start(list);
-            auto slot = [&]() -> unsigned char * {
-                const int s = it % C::NSLOT;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl));
-                return sm + (size_t)s * C::SLOT;
-            };
-            auto scores = [&]() {
-                const int vb = (min(TN, a.dv - cq.x.v0) + 63) / 64;
-                for (int b = 0; b < nb; ++b) {
-                    unsigned char *d = slot();
-                    if (!ok) return;
-                    uint64_t *f = &full[it % C::NSLOT];
-                    if (lane == 0) {
-                        mbar_expect_tx(f, 32768);
-                        tma_3d(d, &mq, KV * b, cq.x.h, cq.x.row0, f);
-                        tma_3d(d + 16384, &mk, KV * b, cq.x.g, cq.key0(), f);
-                    }
-                    ++it;
-                    if (cq.kt == 0) {
-                        d = slot();
-                        if (!ok) return;
-                        f = &full[it % C::NSLOT];
-                        if (lane == 0) {
-                            mbar_expect_tx(f, MT * vb * 8192);
-                            for (int m = 0; m < MT; ++m)
-                                for (int i = 0; i < vb; ++i)
-                                    tma_4d(d + 16384 * m + 8192 * i, &ms, cq.x.v0 + 64 * i, m, KV * b,
-                                           cq.x.seg * a.nh + cq.x.h, f);
-                        }
-                        ++it;
-                    }
-                }
-                vq = cq.next(list, count);
-            };
-            auto values = [&]() {
+        bool ok = true, vq = true, vv = true;
+        uint32_t tp = 0;
+        Cursor cq, cv;
+        cq.start(list);
+        cv.start(list);
+        uint64_t *f = full;
+        auto slot = [&]() -> unsigned char * {   // the next item's, once free
+            const int s = it % C::NSLOT;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl));
+            f = &full[s];
+            if (ok) ++it;
+            return sm + (size_t)s * C::SLOT;
+        };
+        auto expect = [&](int bytes) {
+            if (lane == 0) mbar_expect_tx(f, bytes);
+        };
+        auto scores = [&]() {
+            const int vb = (min(TN, a.dv - cq.x.v0) + 63) / 64, state = cq.x.seg * a.nh + cq.x.h;
+            for (int b = 0; b < nb; ++b) {
                 unsigned char *d = slot();
                 if (!ok) return;
-                ok = tma_rows<C::VR>(d, &mv, cv.x.v0, cv.x.g, cv.key0(), (min(TN, a.dv - cv.x.v0) + 63) / 64, cv.keys(),
-                                     &full[it % C::NSLOT], &tail, tp, abort, wl, lane);
-                if (!ok) return;
-                ++it;
-                vv = cv.next(list, count);
-            };
-            scores();
-            while (vv && ok) {
-                if (vq) scores();
-                if (ok) values();
+                expect(16384 * (C::PAIR ? 2 : NT));
+                tma_panel<NT, 128, 16384>(d, &mq, KV * b, cq.x.h, cq.x.prow, 1, f, lane);
+                if (C::PAIR) {
+                    d += 16384;
+                } else {
+                    d = slot();
+                    if (!ok) return;
+                    expect(16384 * NT);
+                }
+                tma_panel<NT, 128, 16384>(d, &mk, KV * b, cq.x.g, cq.key0(), 1, f, lane);
+                if (cq.kt == 0) {
+                    d = slot();
+                    if (!ok) return;
+                    expect(MT * vb * 8192);
+                    if (lane == 0)
+                        for (int m = 0; m < MT; ++m)
+                            for (int i = 0; i < vb; ++i)
+                                tma_4d(d + 16384 * m + 8192 * i, m < 2 ? &ms : &ms3, cq.x.v0 + 64 * i, m < 2 ? m : 0, KV * b,
+                                       state, f);
+                }
             }
-            if (!ok && lane == 0)
-                for (int i = max(0, it - C::NSLOT); i < it; ++i) mbar_drain(&full[i % C::NSLOT], (i / C::NSLOT) & 1);
-        } else {
-            // ---------------------------------------------------- producers
-            // Two register buffers: an item is loaded while the one before is
-            // stored.
-            using PQ = Panel<T, 128, KV>;
-            using PS = Panel<float, KV, TN>;
-            using PV = Panel<T, C::VR, TN>;
-            const uint32_t pt = tid - 288, qoff = PQ::off(pt), soff = PS::off(pt), voff = PV::off(pt);
-            enum { IT_QK, IT_S, IT_V };
-            struct Item {
-                int kind, nr, width;
-                const void *p;
-                size_t stride;
-            };
-            Cursor cq, cv;
-            cq.start(list);
-            cv.start(list);
-            bool vq = true, vv = true, in_v = false, first = true;   // in_v: a values item comes next
-            int b = 0, j = 0, i = 0;   // step of d and item of it; value panel
-            auto gen = [&](Item &e) -> bool {
-                if (!in_v) {
-                    if (!vq) return false;
-                    if (j == 2) {
-                        e.kind = IT_S;
-                        e.p = inc + ((size_t)cq.x.seg * a.nh + cq.x.h) * a.d * a.dv + KV * b * a.dv + cq.x.v0;
-                        e.stride = a.dv;
-                        e.nr = a.d - KV * b;
-                        e.width = a.dv - cq.x.v0;
-                    } else {
-                        e.kind = IT_QK;
-                        e.p = j == 0 ? (const T *)a.q + (size_t)cq.x.row0 * a.qs + cq.x.h * a.d + KV * b
-                                     : (const T *)a.k + (size_t)cq.key0() * a.ks + cq.x.g * a.d + KV * b;
-                        e.stride = j == 0 ? a.qs : a.ks;
-                        e.nr = j == 0 ? cq.x.nr : cq.keys();
-                        e.width = a.d - KV * b;
-                    }
-                    if (++j == (cq.kt == 0 ? 3 : 2)) {
-                        j = 0;
-                        if (++b == nb) {
-                            b = 0;
-                            vq = cq.next(list, count);
-                            // scores run one unit ahead with two score buffers
-                            in_v = C::XB == 1 || !first || !vq;
-                            first = false;
-                        }
-                    }
-                    return true;
-                }
-                if (!vv) return false;
-                e.kind = IT_V;
-                e.p = (const T *)a.v + (size_t)(cv.key0() + C::VR * i) * a.vs + cv.x.g * a.dv + cv.x.v0;
-                e.stride = a.vs;
-                e.nr = cv.keys() - C::VR * i;
-                e.width = a.dv - cv.x.v0;
-                if (++i == LIN_CHUNK / C::VR) {
-                    i = 0;
-                    vv = cv.next(list, count);
-                    in_v = !vq;
-                }
-                return true;
-            };
-            auto load = [&](uint4 *r, const Item &e) {
-                if (e.kind == IT_QK) PQ::load(r, (const T *)e.p, e.stride, e.nr, e.width, pt);
-                else if (e.kind == IT_S) PS::load(r, (const float *)e.p, e.stride, e.nr, e.width, pt);
-                else PV::load(r, (const T *)e.p, e.stride, e.nr, e.width, pt);
-            };
-            auto store = [&](const uint4 *r, const Item &e) -> bool {
-                const int s = it % C::NSLOT;
-                if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl))) return false;
-                unsigned char *d = sm + (size_t)s * C::SLOT;
-                if (e.kind == IT_QK) PQ::template put<NT>(r, d + qoff);
-                else if (e.kind == IT_S) PS::template put<MT>(r, d + soff);
-                else PV::template put<NT>(r, d + voff);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
-                ++it;
-                return true;
-            };
-            uint4 ra[8], rb[8];
-            Item ea, eb;
-            bool ha = gen(ea), hb;
-            load(ra, ea);
-            while (ha) {
-                hb = gen(eb);
-                if (hb) load(rb, eb);
-                if (!store(ra, ea) || !hb) break;
-                ha = gen(ea);
-                if (ha) load(ra, ea);
-                if (!store(rb, eb)) break;
+            vq = cq.next(list, count);
+        };
+        auto values = [&]() {
+            for (int i = 0; i < LIN_CHUNK / C::VR; ++i) {
+                unsigned char *d = slot();
+                if (!ok) return;
+                ok = tma_values<NT, C::VR, C::VR * TN * 2>(d, &mv, cv.x.v0, cv.x.g, cv.key0() + C::VR * i,
+                                                           (min(TN, a.dv - cv.x.v0) + 63) / 64, cv.keys() - C::VR * i, f, &tail,
+                                                           tp, abort, lane);
+                if (!ok) return;
+            }
+            vv = cv.next(list, count);
+        };
+        for (int ahead = 0; vv && ok;) {   // in the MMA issuer's order
+            if (vq && ahead < C::XB) {
+                scores();
+                ++ahead;
+            } else {
+                values();
+                --ahead;
             }
         }
+        // copies are over before the block ends
+        if (lane == 0)
+            for (int i = max(0, it - C::NSLOT); i < it; ++i) mbar_drain(&full[i % C::NSLOT], (i / C::NSLOT) & 1);
     } else if (warp < 4) {
         // --------------------------------------------------------------- P
         Cursor c;
@@ -966,6 +917,7 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
             tc_after();
             const int wv = min(TN, a.dv - c.x.v0);
             for (int half = 0; half <= (C::SPLIT ? 1 : 0); ++half)
+#pragma unroll 1
                 for (int cb = 0; cb < wv; cb += 32) {
                     const uint32_t ad = lanes + C::acc(c.n) + 128 * half + cb;
                     uint32_t r[32];
@@ -993,7 +945,7 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
             const uint32_t x = lanes + C::x(c.u);
             // P over the scores of the same keys; a third term of 32 keys
             // takes 16 columns of the corrections, of keys already read
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < LIN_CHUNK; cb += 32) {
                 uint32_t r[32], third[16];
                 float s[32];
@@ -1026,7 +978,7 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
                 TMEM_ST32(x + cb, r);
                 if (C::SPLIT) TMEM_ST16(x + 128 + cb / 2, third);
             }
-            if (c.kt == 0 && !diag) ok = weight(lin_pow(g, c.x.row0 - c.x.seg0row));
+            if (c.kt == 0 && !diag) ok = weight(lin_pow(g, c.x.i0));
             if (diag && ok) ok = weight(pw[row + 1]);
             if (!ok) break;
             tmem_st_wait();
@@ -1046,6 +998,7 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
             tc_after();
             T *o = (T *)a.out + (size_t)(x.row0 + 32 * (warp & 3)) * a.os + (size_t)x.h * a.dv + x.v0;
             const int nr = x.nr - 32 * (warp & 3), wv = min(TN, a.dv - x.v0);
+#pragma unroll 1
             for (int cb = 0; cb < wv; cb += 32) {
                 float y[32];
                 if (ok) {
@@ -1082,27 +1035,26 @@ __global__ __launch_bounds__(OutCfg<T>::THREADS, 1) void k_lin_out(LinArgs a, co
 
 // ----------------------------------------------------------------- launch
 
-// A bf16 row tensor [rows][heads][width] in boxes of 64 columns of `box` rows.
-bool rows_map(CUtensorMap *m, const void *base, int width, int heads, int rows, size_t stride, int box) {
+bool encode(CUtensorMap *m, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, int rows_dim, int rows) {
     const auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
-    cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
-    cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box}, es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void *)base, dims, strides, boxes, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    cuuint32_t boxes[4] = {64, 1, 1, 1}, es[4] = {1, 1, 1, 1};
+    boxes[rows_dim] = (cuuint32_t)rows;
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void *)base, dims, strides, boxes, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The entering states as the scan leaves them: [states][d][2 terms][dv].
-bool states_map(CUtensorMap *m, const void *base, const LinArgs &a, int states) {
-    const auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)a.dv, 2, (cuuint64_t)a.d, (cuuint64_t)states};
-    cuuint64_t strides[3] = {(cuuint64_t)a.dv * 2, (cuuint64_t)a.dv * 4, (cuuint64_t)a.d * a.dv * 4};
-    cuuint32_t boxes[4] = {64, 1, KV, 1}, es[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void *)base, dims, strides, boxes, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// A row panel [terms][rows][heads][width] in boxes of 64 columns of `box` rows.
+bool rows_map(CUtensorMap *m, const void *base, int width, int heads, int rows, size_t stride, int terms, int box) {
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)terms};
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2, (cuuint64_t)rows * stride * 2};
+    return encode(m, base, dims, strides, 2, box);
+}
+// Entering states as the scan leaves them: [states][d][terms][dv].
+bool states_map(CUtensorMap *m, const void *base, const LinArgs &a, int states, int terms) {
+    const cuuint64_t dims[4] = {(cuuint64_t)a.dv, (cuuint64_t)terms, (cuuint64_t)a.d, (cuuint64_t)states};
+    const cuuint64_t row = (cuuint64_t)a.dv * 2 * terms;
+    const cuuint64_t strides[3] = {(cuuint64_t)a.dv * 2, row, a.d * row};
+    return encode(m, base, dims, strides, 2, KV);
 }
 
 // CTAs of a persistent grid: one an SM, more where a CTA's list would overflow.
@@ -1112,7 +1064,8 @@ int grid_of(int units) {
 }
 
 template <typename T, int N>
-bool pass_t(const LinArgs &a, const LinWorkTable &t, int segs, int tiles, float *inc, cudaStream_t st) {
+bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int tiles, int prows, void *scratch,
+            cudaStream_t st) {
     using CI = IncCfg<T, N>;
     using CO = OutCfg<T>;
     static unsigned long long done = 0;
@@ -1122,27 +1075,51 @@ bool pass_t(const LinArgs &a, const LinWorkTable &t, int segs, int tiles, float 
         cudaFuncSetAttribute(k_lin_out<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CO::SMEM);
         o1_attrs_done(&done, bit);
     }
-    CUtensorMap mq = {}, mk = {}, mv = {}, mvi = {}, ms = {};
-    if (CO::TMA && !(rows_map(&mq, a.q, a.d, a.nh, a.rows, a.qs, LIN_CHUNK) &&
-                     rows_map(&mk, a.k, a.d, a.G, a.rows, a.ks, LIN_CHUNK) &&
-                     rows_map(&mv, a.v, a.dv, a.G, a.rows, a.vs, CO::VR) &&
-                     rows_map(&mvi, a.v, a.dv, a.G, a.rows, a.vs, KV) && states_map(&ms, inc, a, segs * a.nh)))
+    // the pass's scratch: increments and entering states, third terms, panels
+    char *at = (char *)scratch;
+    float *inc = (float *)at;
+    at += lin_pass_states(a.nh, a.d, a.dv, dtype, segs).inc;
+    uint16_t *third = (uint16_t *)at;
+    at += lin_pass_states(a.nh, a.d, a.dv, dtype, segs).third;
+    SplitArgs sp = {};
+    const void *q = a.q, *k = a.k, *v = a.v;
+    size_t qs = a.qs, ks = a.ks, vs = a.vs;
+    int rows = a.rows;
+    if (CO::NT > 1) {
+        rows = prows;
+        qs = (size_t)a.nh * a.d;
+        ks = (size_t)a.G * a.d;
+        vs = (size_t)a.G * a.dv;
+        const size_t n = (size_t)prows * CO::NT;
+        q = sp.q = (uint16_t *)at;
+        k = sp.k = sp.q + n * qs;
+        v = sp.v = sp.k + n * ks;
+        sp.prows = prows;
+    }
+    CUtensorMap mq, mk, mv, mvi, ms, ms3;
+    if (!rows_map(&mq, q, a.d, a.nh, rows, qs, CO::NT, LIN_CHUNK) || !rows_map(&mk, k, a.d, a.G, rows, ks, CO::NT, LIN_CHUNK) ||
+        !rows_map(&mv, v, a.dv, a.G, rows, vs, CO::NT, CO::VR) || !rows_map(&mvi, v, a.dv, a.G, rows, vs, CO::NT, KV) ||
+        !states_map(&ms, inc, a, segs * a.nh, 2))
         return false;
+    ms3 = ms;
+    if (CO::MT == 3 && !states_map(&ms3, third, a, segs * a.nh, 1)) return false;
     const int dt = (a.d + TN - 1) / TN, units = segs * a.nh * dt * ((a.dv + N - 1) / N);
     const int ot = tiles * a.nh * ((a.dv + TN - 1) / TN);
+    if (CO::NT > 1) k_lin_split<T><<<prows, 256, 0, st>>>(a, t, sp);
     k_lin_inc<T, N><<<grid_of(units), CI::THREADS, CI::SMEM, st>>>(a, t, mvi, units, inc);
-    k_lin_scan<CO::TMA><<<dim3((a.d + 7) / 8, a.nh, t.n), 256, 0, st>>>(a, t, inc);
-    k_lin_out<T><<<grid_of(ot), CO::THREADS, CO::SMEM, st>>>(a, t, mq, mk, mv, ms, ot, inc);
+    k_lin_scan<CO::MT><<<dim3((a.d + 7) / 8, a.nh, t.n), 256, 0, st>>>(a, t, inc, third);
+    k_lin_out<T><<<grid_of(ot), OUT_THREADS, CO::SMEM, st>>>(a, t, mq, mk, mv, ms, ms3, ot);
     return true;
 }
 
 }  // namespace
 
-bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, float *inc, cudaStream_t st) {
-    if (dtype == O1_F32) return pass_t<float, 128>(a, t, segs, tiles, inc, st);
-    if (dtype == O1_F16) return pass_t<__half, 128>(a, t, segs, tiles, inc, st);
-    return a.dv > 128 ? pass_t<__nv_bfloat16, 256>(a, t, segs, tiles, inc, st)
-                      : pass_t<__nv_bfloat16, 128>(a, t, segs, tiles, inc, st);
+bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, int prows, void *scratch,
+                     cudaStream_t st) {
+    if (dtype == O1_F32) return pass_t<float, 128>(a, t, dtype, segs, tiles, prows, scratch, st);
+    if (dtype == O1_F16) return pass_t<__half, 128>(a, t, dtype, segs, tiles, prows, scratch, st);
+    return a.dv > 128 ? pass_t<__nv_bfloat16, 256>(a, t, dtype, segs, tiles, prows, scratch, st)
+                      : pass_t<__nv_bfloat16, 128>(a, t, dtype, segs, tiles, prows, scratch, st);
 }
 
 int lin_flags(uint32_t *flags, int clear, cudaStream_t st) {
