@@ -3,7 +3,6 @@
 //   S = e^{g_h} S + k_t v_t^T,   out_t = scale q_t S.
 #include <limits.h>
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 
@@ -172,15 +171,29 @@ size_t slot_floats(const o1_lin_geom &g) {
 // Sequences of up to LIN_ROW_MAX rows take the row kernel, longer ones the
 // chunk kernels.
 constexpr int LIN_ROW_MAX = 32;
-// A pass's scratch is written, read, rewritten and read again, so passes are
-// kept to what stays in the L2.
-const size_t LIN_PASS_BYTES = (size_t)(getenv("LIN_MB") ? atoi(getenv("LIN_MB")) : 64) << 20;
-constexpr int64_t LIN_PASS_ROWS = 1 << 24;   // and their counts to 32 bits
+// Limits of a pass: its states are written, read, rewritten and read again and
+// are kept to what stays in the L2 (a 32768-row prompt of 2 MB a state: 412 us
+// in passes of 64 MB, 469 of 96, 472 of 128); its scratch as a whole, and its
+// rows, so that counts fit 32 bits.
+constexpr size_t LIN_PASS_STATES = (size_t)64 << 20, LIN_PASS_BYTES = (size_t)256 << 20;
+constexpr int64_t LIN_PASS_ROWS = 1 << 24;
 
-int seg_rows(const o1_lin_geom &g) {
-    const char *e = getenv("LIN_SEG");
-    return e ? atoi(e) : 256;
+// Whether a pass of that many segments and panel rows is within the limits
+// (a single segment of one tile always is).
+bool pass_within(const o1_lin_geom &g, int64_t segs, int64_t prows) {
+    if (segs <= 1 && prows <= LIN_CHUNK) return true;
+    return (size_t)segs * slot_floats(g) * 4 <= LIN_PASS_STATES && prows <= LIN_PASS_ROWS &&
+           lin_pass_bytes(g, segs, prows) <= LIN_PASS_BYTES;
 }
+
+// Rows of a segment for a call of `tiles` tiles (LIN_CHUNK rows of a head, 128
+// value columns). Longer segments write and read fewer states (4 d dv bytes a
+// head each, several times over) and pay with scores against the earlier
+// tiles of the segment: a 4096-row fp32 prompt of 8 heads of 256 took 141 us
+// with 256 rows, 152 with 128, 178 with 512. A call that does not fill the SMs
+// is bound by the longest chain instead: 1077 fp16 rows of 3 heads 19.7 us with
+// 128 rows, 22.1 with 256.
+int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : 2 * LIN_CHUNK; }
 
 // The sequences of a call: ranges and slots in bounds and apart. Sorted
 // copies on the stack (nothing is allocated for a call).
@@ -247,10 +260,10 @@ size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots) {
 size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs) {
     if (!lin_geom_ok(geom) || rows < 1 || seqs < 1) return 0;
     // segments of LIN_CHUNK rows are the most states any split into segments takes
-    const int64_t segs = (int64_t)rows / LIN_CHUNK + seqs, prows = (int64_t)rows + 16 * (int64_t)seqs;
+    const size_t all = lin_pass_bytes(*geom, (int64_t)rows / LIN_CHUNK + seqs, (int64_t)rows + 16 * (int64_t)seqs);
     const size_t one = lin_pass_bytes(*geom, 1, LIN_CHUNK);
-    const size_t lim = one > LIN_PASS_BYTES ? one : LIN_PASS_BYTES;
-    const size_t all = lin_pass_bytes(*geom, segs < INT_MAX ? (int)segs : INT_MAX, prows);
+    size_t lim = lin_terms(geom->dtype) == 1 ? LIN_PASS_STATES : LIN_PASS_BYTES;
+    lim = one > lim ? one : lim;
     return all < lim ? all : lim;
 }
 
@@ -271,9 +284,10 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     if (rc != O1_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     a.wait_cycles = o1_wait_limit();
-    a.seg = seg_rows(g);
-    const size_t one = lin_pass_bytes(g, 1, LIN_CHUNK), lim = one > LIN_PASS_BYTES ? one : LIN_PASS_BYTES;
-    const size_t cap = scratch_bytes < lim ? scratch_bytes : lim;
+    int64_t tiles_all = 0;
+    for (int i = 0; i < n_seq; ++i)
+        if (seqs[i].rows > LIN_ROW_MAX) tiles_all += (seqs[i].rows - 1) / LIN_CHUNK + 1;
+    a.seg = seg_rows(tiles_all * a.nh * ((g.dv + 127) / 128));
     LinTable rows;
     LinWorkTable work;
     int n = 0, segs = 0, tiles = 0, prows = 0;
@@ -290,8 +304,8 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     auto up = [](int64_t x, int m) { return (int)((x + m - 1) / m); };
     // whether the pass takes r more rows of a sequence
     auto fits = [&](int64_t r) {
-        const int64_t p = prows + 16 * (int64_t)up(r, 16);
-        return p <= LIN_PASS_ROWS && lin_pass_bytes(g, segs + up(r, a.seg), p) <= cap;
+        const int64_t p = prows + 16 * (int64_t)up(r, 16), n = segs + up(r, a.seg);
+        return pass_within(g, n, p) && lin_pass_bytes(g, n, p) <= scratch_bytes;
     };
     for (int i = 0; i < n_seq; ++i) {
         const o1_lin_seq &s = seqs[i];

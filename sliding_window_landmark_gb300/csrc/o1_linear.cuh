@@ -62,11 +62,11 @@ static inline int lin_terms(int dtype) { return dtype == O1_BF16 ? 1 : dtype == 
 struct LinStates {
     size_t inc, third;
 };
-static inline LinStates lin_pass_states(int nh, int d, int dv, int dtype, int segs) {
+static inline LinStates lin_pass_states(int nh, int d, int dv, int dtype, int64_t segs) {
     const size_t n = (size_t)segs * nh * d * dv;
     return {o1_al256(4 * n), dtype == O1_F32 ? o1_al256(2 * n) : 0};
 }
-static inline size_t lin_pass_bytes(const o1_lin_geom &g, int segs, int64_t prows) {
+static inline size_t lin_pass_bytes(const o1_lin_geom &g, int64_t segs, int64_t prows) {
     const int nt = lin_terms(g.dtype), nh = g.groups * g.heads_per_group;
     const LinStates s = lin_pass_states(nh, g.d, g.dv, g.dtype, segs);
     const size_t row = (size_t)(nh + g.groups) * g.d + (size_t)g.groups * g.dv;

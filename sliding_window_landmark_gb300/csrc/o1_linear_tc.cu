@@ -41,10 +41,35 @@ namespace {
 
 constexpr int TN = 128;   // columns of a tile of dv (and of d, for dS)
 constexpr int KV = 64;    // rows or columns of a staged panel's short side
-constexpr int PROD_WARPS = 8, PROD = 32 * PROD_WARPS;
+constexpr int PROD_WARPS = 16, PROD = 32 * PROD_WARPS;
 constexpr int LIST = 64;  // units of a CTA, decoded once at its start
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// A warp's bounded wait, as mbar_wait, with a hint to suspend between polls:
+// ten waiting warps that poll at full rate take the shared-memory pipe from the
+// barrier operations of the others.
+__device__ __forceinline__ bool mbar_try_hint(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(su32(bar)), "r"(parity), "r"(2000)
+        : "memory");
+    return ok != 0;
+}
+// (Every decision is a warp vote: the .aligned instructions that follow a wait
+// need the warp together. With one lane polling and the rest at a shuffle
+// they raised an illegal instruction.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long limit) {
+    if (__all_sync(0xffffffffu, mbar_try_hint(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try_hint(bar, parity)))
+        if (__any_sync(0xffffffffu, *abort || clock64() - t0 > limit)) {
+            *abort = 1;
+            return false;
+        }
+    return true;
+}
 // One lane of the (whole) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -138,8 +163,8 @@ __device__ __forceinline__ uint32_t panel_off(int rows, int r, int cg) {
 // What a producer stages into a slot of the ring: a panel of ROWS x COLS
 // values of a row tensor (rows past nr and columns past width read as zero),
 // as NT bf16 terms. Thread pt takes one 8-column group of every STEP-th row, so
-// that its addresses on both sides are one base and constant steps: a producer
-// has two warps a scheduler, and every dependent instruction shows.
+// that its addresses on both sides are one base and constant steps: producers
+// are few warps a scheduler, and every dependent instruction shows.
 template <typename T, int ROWS, int COLS>
 struct Panel {
     static constexpr int GPR = COLS / 8, STEP = PROD / GPR, IT = ROWS / STEP, W = WORDS<T>;
@@ -268,7 +293,7 @@ __device__ __forceinline__ bool tma_values(unsigned char *dst, const CUtensorMap
     if (!cut) return true;
     __syncwarp();
     // in flight: waited for with the full limit
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(tail, tail_phase, abort, O1_WAIT_CYCLES_FULL));
+    const bool ok = warp_wait(tail, tail_phase, abort, O1_WAIT_CYCLES_FULL);
     if (!ok) mbar_drain(tail, tail_phase);
     tail_phase ^= 1;
     const int z = ceil16(nr) - nr;   // rows of zeros
@@ -351,7 +376,7 @@ struct IncCfg {
 // dS of every (segment, head): A = weighted keys (M = d), B = values (N = dv),
 // both MN-major, contraction over the rows, 64 of them a step. Persistent: a
 // CTA takes units in turn. Warps: 0-3 store a finished unit, 4 issues the
-// MMAs, 5 the values' TMA, 6-13 stage the weighted keys, running ahead over
+// MMAs, 5 the values' TMA, 6-21 stage the weighted keys, running ahead over
 // the rings.
 template <typename T, int N>
 __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs a, const __grid_constant__ LinWorkTable t,
@@ -417,7 +442,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         // the next panel's loads are in flight while one is stored
         using P = Panel<T, KV, TN>;
         const uint32_t pt = tid - 192, off = P::off(pt), prow = P::row(pt);
-        uint4 ra[4 * WORDS<T>], rb[4 * WORDS<T>];
+        uint4 ra[P::IT * WORDS<T>], rb[P::IT * WORDS<T>];
         int ik = 0;
         bool ok = true;
         auto load_k = [&](uint4 *r, const IncUnit &x, int s) {
@@ -429,7 +454,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         // back; rows past the end are zeros under any finite weight
         auto store_k = [&](const uint4 *r, const IncUnit &x, int s) {
             const int b = ik % NK;
-            ok = __all_sync(0xffffffffu, mbar_wait(&kempty[b], ((ik / NK) & 1) ^ 1, abort, wl));
+            ok = warp_wait(&kempty[b], ((ik / NK) & 1) ^ 1, abort, wl);
             if (!ok) return;
             const int last = x.nr - 1 - KV * s - (int)prow;
             float w[P::IT];
@@ -471,7 +496,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             const int boxes = (min(N, a.dv - x.v0) + 63) / 64;
             for (int s = 0; KV * s < x.nr && ok; ++s, ++iv) {
                 const int b = iv % NV;
-                ok = __all_sync(0xffffffffu, mbar_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl));
+                ok = warp_wait(&vempty[b], ((iv / NV) & 1) ^ 1, abort, wl);
                 if (!ok) break;
                 ok = tma_values<NT, KV, KV * N * 2>(sV + b * C::VSLOT, &mv, x.v0, x.g, x.prow + KV * s, boxes, x.nr - KV * s,
                                                     &vfull[b], &tail, tp, abort, lane);
@@ -491,11 +516,10 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             const int nr = list[n].nr;
             const uint32_t id = idesc_bf16(128, min(N, ceil16(a.dv - list[n].v0)), 1, 1);
             const uint32_t d = tmem + (n % C::NB) * 2 * N;
-            ok = __all_sync(0xffffffffu, mbar_wait(&freed[n % C::NB], ((n / C::NB) & 1) ^ 1, abort, wl));
+            ok = warp_wait(&freed[n % C::NB], ((n / C::NB) & 1) ^ 1, abort, wl);
             for (int s = 0; KV * s < nr && ok; ++s, ++it) {
                 const int bk = it % NK, bv = it % NV;
-                ok = __all_sync(0xffffffffu, mbar_wait(&kfull[bk], (it / NK) & 1, abort, wl) &&
-                                                 mbar_wait(&vfull[bv], (it / NV) & 1, abort, wl));
+                ok = warp_wait(&kfull[bk], (it / NK) & 1, abort, wl) && warp_wait(&vfull[bv], (it / NV) & 1, abort, wl);
                 if (!ok) break;
                 tc_after();
                 issue<3, NT, 2, false, KTERM, 128, VTERM, 128>(e, d, d + N, id, min(KV, ceil16(nr - KV * s)) / 16, s > 0,
@@ -519,7 +543,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         for (int n = 0; n < count; ++n) {
             const IncUnit x = list[n];
             const uint32_t lanes = tmem + (n % C::NB) * 2 * N + ((uint32_t)(32 * warp) << 16);
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&done[n % C::NB], (n / C::NB) & 1, abort, wl));
+            if (ok) ok = warp_wait(&done[n % C::NB], (n / C::NB) & 1, abort, wl);
             tc_after();
             float *o = inc + ((size_t)x.seg * a.nh + x.h) * a.d * a.dv + (size_t)(x.d0 + 32 * warp) * a.dv + x.v0;
             const int nr = a.d - x.d0 - 32 * warp, wv = min(N, a.dv - x.v0);
@@ -624,7 +648,8 @@ template <typename T>
 struct OutCfg {
     static constexpr int NT = Terms<T>::in, MT = Terms<T>::mid;
     static constexpr bool PAIR = NT == 1;      // Q and K of a step share a slot
-    static constexpr int SLOT = NT == 3 ? 49152 : 32768, NSLOT = NT == 3 ? 4 : 6;
+    static constexpr int DK = NT == 1 ? 128 : 64;   // values of d a step
+    static constexpr int SLOT = NT == 1 ? 65536 : NT == 2 ? 32768 : 49152, NSLOT = NT == 1 ? 3 : NT == 2 ? 6 : 4;
     static constexpr int VR = NT == 1 ? 128 : 64;   // value rows of a slot
     static constexpr bool SPLIT = NT == 3;     // corrections in accumulators of their own
     // TMEM: outputs ACC (two buffers; SPLIT: one, main and corrections), then
@@ -643,6 +668,7 @@ struct OutTile {
     int prow, kprow;     // in the panels: the tile's and its segment's first row
     int i0, seg;         // row in the segment; the segment's state
     int h, g, v0, nkt;
+    int nv;              // value columns, rounded to 16
 };
 struct Cursor {
     int n, u, kt;        // tile of the list, units so far, key tile
@@ -729,6 +755,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         x.prow = (NT == 1 ? w.row0 : w.prow0) + off;
         x.kprow = x.prow - x.i0;
         x.nkt = x.i0 / LIN_CHUNK + 1;
+        x.nv = min(TN, ceil16(a.dv - x.v0));
         list[tid - 64] = x;
     }
     tc_before();
@@ -736,68 +763,81 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
     tc_after();
     const uint32_t tmem = tslot;
     const long long wl = a.wait_cycles;
-    const int nb = (a.d + KV - 1) / KV;   // steps of 64 of d
+    const int nb = (a.d + C::DK - 1) / C::DK;   // steps of d
 
     if (warp == 8) {
         // ------------------------------------------------------ MMA issuer
         // Ring items in order: per unit, for each step of d the Q and K
         // panels and (first unit of a tile) the entering state's; the unit's
-        // values (a unit later where scores run ahead).
+        // values (a unit later where scores run ahead). The tensor pipe holds
+        // an MMA or two, so what this warp does between them shows: positions
+        // are carried, not computed.
         const bool e = elect_one();
-        int it = 0;
         bool ok = true, vq = true, vv = true;
         Cursor cq, cv;
         cq.start(list);
         cv.start(list);
         const uint32_t base = su32(sm);
-        auto need = [&](int i) -> uint32_t {   // slot of ring item i, once filled
-            const int s = i % C::NSLOT;
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[s], (i / C::NSLOT) & 1, abort, wl));
-            return base + (uint32_t)s * C::SLOT;
+        const uint64_t dk = desc_sw128(base), ds = desc_sw128_mn(base, C::DK * 128), dv = desc_sw128_mn(base, C::VR * 128);
+        const uint32_t id_x = idesc_bf16(128, 128, 0, 0);
+        int slot = 0;              // of the next ring item
+        uint32_t phase = 0;
+        auto take = [&]() -> int {   // the next item's slot, once filled
+            const int s = slot;
+            ok = ok && warp_wait(&full[s], phase, abort, wl);
+            if (++slot == C::NSLOT) slot = 0, phase ^= 1;
+            return s;
         };
         auto commit = [&](uint64_t *bar) {
             if (e) mma_commit(bar);
         };
-        auto done = [&](int i) { commit(&empty[i % C::NSLOT]); };
-        // scores of a unit, and with a tile's first unit its q S_in
+        // scores of a unit, and with a tile's first unit its q S_in; 64
+        // columns of Q and K (a block of their panels) at a time
         auto scores = [&]() {
-            const uint32_t x = tmem + C::x(cq.u), acc = tmem + C::acc(cq.n);
-            const uint32_t id_x = idesc_bf16(128, 128, 0, 0), id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cq.x.v0)), 0, 1);
+            const int n = cq.n % C::AB;
+            const uint32_t x = tmem + C::x(cq.u), acc = tmem + C::acc(cq.n), id_a = idesc_bf16(128, cq.x.nv, 0, 1);
+            const bool state = cq.kt == 0;
+#pragma unroll 1
             for (int b = 0; b < nb; ++b) {
-                const int steps = ceil16(min(KV, a.d - KV * b)) / 16, iq = it;
-                const uint32_t q = need(it++), k = C::PAIR ? q + 16384 : need(it++);
+                const int steps = (min(C::DK, a.d - C::DK * b) + 15) / 16, sq = take(), sk = C::PAIR ? sq : take();
                 if (!ok) return;
                 tc_after();
-                const uint64_t qd = desc_sw128(q);
-                issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(e, x, x + C::CORR, id_x, steps, b > 0, qd, desc_sw128(k));
-                if (!C::PAIR) done(iq + 1);
+                const uint64_t qd = dk + (uint64_t)(sq * (C::SLOT / 16));
+                const uint64_t kd = C::PAIR ? qd + C::DK * 16 : dk + (uint64_t)(sk * (C::SLOT / 16));
+#pragma unroll 1
+                for (int i = 0; 4 * i < steps; ++i)
+                    issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(e, x, x + C::CORR, id_x, min(4, steps - 4 * i), b + i > 0,
+                                                                   qd + 1024 * i, kd + 1024 * i);
+                if (!C::PAIR) commit(&empty[sk]);
                 if (b == nb - 1) commit(&sc_full[cq.u % C::XB]);
-                if (cq.kt == 0) {
-                    if (b == 0) ok = __all_sync(0xffffffffu, mbar_wait(&acc_free[cq.n % C::AB], ((cq.n / C::AB) & 1) ^ 1, abort, wl));
-                    const int is = it++;
-                    const uint32_t s0 = need(is);
+                if (state) {
+                    if (b == 0) ok = warp_wait(&acc_free[n], ((cq.n / C::AB) & 1) ^ 1, abort, wl);
+                    const int ss = take();
                     if (!ok) return;
                     tc_after();
-                    issue<NT, MT, max_sum(NT, MT), false, 1024, 2, KV * TN * 2 / 16, 128>(
-                        e, acc, acc + C::CORR, id_a, steps, b > 0, qd, desc_sw128_mn(s0, KV * 128));
-                    done(is);
+                    const uint64_t sd = ds + (uint64_t)(ss * (C::SLOT / 16));
+#pragma unroll 1
+                    for (int i = 0; 4 * i < steps; ++i)
+                        issue<NT, MT, max_sum(NT, MT), false, 1024, 2, C::DK * TN * 2 / 16, 128>(
+                            e, acc, acc + C::CORR, id_a, min(4, steps - 4 * i), b + i > 0, qd + 1024 * i, sd + 512 * i);
+                    commit(&empty[ss]);
                 }
-                done(iq);
+                commit(&empty[sq]);
             }
-            if (cq.kt == 0) commit(&acc_ready[cq.n % C::AB]);
+            if (state) commit(&acc_ready[n]);
             vq = cq.next(list, count);
         };
         auto values = [&]() {
-            const uint32_t x = tmem + C::x(cv.u), acc = tmem + C::acc(cv.n);
-            const uint32_t id_a = idesc_bf16(128, min(TN, ceil16(a.dv - cv.x.v0)), 0, 1);
-            const int nk = cv.keys();
-            ok = __all_sync(0xffffffffu, mbar_wait(&p_full[cv.u % C::XB], (cv.u / C::XB) & 1, abort, wl));
+            const uint32_t x = tmem + C::x(cv.u), acc = tmem + C::acc(cv.n), id_a = idesc_bf16(128, cv.x.nv, 0, 1);
+            const int keys = (cv.keys() + 15) / 16;   // steps
+            ok = warp_wait(&p_full[cv.u % C::XB], (cv.u / C::XB) & 1, abort, wl);
+#pragma unroll 1
             for (int i = 0; i < LIN_CHUNK / C::VR; ++i) {
-                const uint32_t v = need(it);
+                const int sv = take();
                 if (!ok) return;
                 tc_after();
-                const int steps = min(C::VR, ceil16(max(0, nk - C::VR * i))) / 16;
-                const uint64_t vd = desc_sw128_mn(v, C::VR * 128);
+                const int steps = min(C::VR / 16, keys - C::VR / 16 * i);
+                const uint64_t vd = dv + (uint64_t)(sv * (C::SLOT / 16));
                 constexpr int TERM = C::VR * TN * 2 / 16;
                 if (steps > 0) {
                     // P's terms 0 and 1 of 16 keys are 16 columns; the third's 8 lie apart
@@ -807,7 +847,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                     issue<2, NT, max_sum(MT, NT), true, 8, 16, TERM, 128>(e, acc, acc + C::CORR, id_a, steps, true,
                                                                          x + C::VR * i, vd);
                 }
-                done(it++);
+                commit(&empty[sv]);
             }
             if (cv.diag()) commit(&o_done[cv.n % C::AB]);
             else if (cv.kt == cv.x.nkt - 2) commit(&acc_ready[cv.n % C::AB]);
@@ -838,7 +878,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         uint64_t *f = full;
         auto slot = [&]() -> unsigned char * {   // the next item's, once free
             const int s = it % C::NSLOT;
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl));
+            ok = ok && warp_wait(&empty[s], ((it / C::NSLOT) & 1) ^ 1, abort, wl);
             f = &full[s];
             if (ok) ++it;
             return sm + (size_t)s * C::SLOT;
@@ -847,29 +887,30 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             if (lane == 0) mbar_expect_tx(f, bytes);
         };
         auto scores = [&]() {
-            const int vb = (min(TN, a.dv - cq.x.v0) + 63) / 64, state = cq.x.seg * a.nh + cq.x.h;
+            const int vb = (cq.x.nv + 63) / 64, state = cq.x.seg * a.nh + cq.x.h;
             for (int b = 0; b < nb; ++b) {
                 unsigned char *d = slot();
                 if (!ok) return;
-                expect(16384 * (C::PAIR ? 2 : NT));
-                tma_panel<NT, 128, 16384>(d, &mq, KV * b, cq.x.h, cq.x.prow, 1, f, lane);
+                const int db = (min(C::DK, a.d - C::DK * b) + 63) / 64;   // blocks of 64 columns
+                expect(16384 * db * (C::PAIR ? 2 : NT));
+                tma_panel<NT, 128, 16384>(d, &mq, C::DK * b, cq.x.h, cq.x.prow, db, f, lane);
                 if (C::PAIR) {
-                    d += 16384;
+                    d += C::DK * 256;
                 } else {
                     d = slot();
                     if (!ok) return;
                     expect(16384 * NT);
                 }
-                tma_panel<NT, 128, 16384>(d, &mk, KV * b, cq.x.g, cq.key0(), 1, f, lane);
+                tma_panel<NT, 128, 16384>(d, &mk, C::DK * b, cq.x.g, cq.key0(), db, f, lane);
                 if (cq.kt == 0) {
                     d = slot();
                     if (!ok) return;
-                    expect(MT * vb * 8192);
+                    expect(MT * vb * C::DK * 128);
                     if (lane == 0)
                         for (int m = 0; m < MT; ++m)
                             for (int i = 0; i < vb; ++i)
-                                tma_4d(d + 16384 * m + 8192 * i, m < 2 ? &ms : &ms3, cq.x.v0 + 64 * i, m < 2 ? m : 0, KV * b,
-                                       state, f);
+                                tma_4d(d + C::DK * (256 * m + 128 * i), m < 2 ? &ms : &ms3, cq.x.v0 + 64 * i, m < 2 ? m : 0,
+                                       C::DK * b, state, f);
                 }
             }
             vq = cq.next(list, count);
@@ -879,7 +920,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                 unsigned char *d = slot();
                 if (!ok) return;
                 ok = tma_values<NT, C::VR, C::VR * TN * 2>(d, &mv, cv.x.v0, cv.x.g, cv.key0() + C::VR * i,
-                                                           (min(TN, a.dv - cv.x.v0) + 63) / 64, cv.keys() - C::VR * i, f, &tail,
+                                                           (cv.x.nv + 63) / 64, cv.keys() - C::VR * i, f, &tail,
                                                            tp, abort, lane);
                 if (!ok) return;
             }
@@ -911,7 +952,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         // the accumulator times f, once what it holds so far is complete
         auto weight = [&](float f) -> bool {
             const int i = c.n % C::AB;
-            if (!__all_sync(0xffffffffu, mbar_wait(&acc_ready[i], i ? rp[1] : rp[0], abort, wl))) return false;
+            if (!warp_wait(&acc_ready[i], i ? rp[1] : rp[0], abort, wl)) return false;
             if (i) rp[1] ^= 1;
             else rp[0] ^= 1;
             tc_after();
@@ -937,11 +978,14 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                 table = c.x.h;
                 __syncwarp();
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[c.u % C::XB], (c.u / C::XB) & 1, abort, wl));
+            ok = warp_wait(&sc_full[c.u % C::XB], (c.u / C::XB) & 1, abort, wl);
             if (!ok) break;
             tc_after();
             const bool diag = c.diag();
-            const float tf = diag ? 0.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt));
+            // weights: l^{row - j} up to the diagonal; for an earlier tile
+            // l^{127 - j} for all its keys, and the tiles in between
+            const int lim = diag ? row : LIN_CHUNK - 1;
+            const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt));
             const uint32_t x = lanes + C::x(c.u);
             // P over the scores of the same keys; a third term of 32 keys
             // takes 16 columns of the corrections, of keys already read
@@ -959,13 +1003,8 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
 #pragma unroll
                     for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(r[i]);
                 }
-                if (diag) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] = cb + i <= row ? s[i] * pw[max(row - cb - i, 0)] : 0.f;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[i] *= pw[LIN_CHUNK - 1 - cb - i] * tf;
-                }
+                for (int i = 0; i < 32; ++i) s[i] = cb + i <= lim ? s[i] * (pw[max(lim - cb - i, 0)] * tf) : 0.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -994,7 +1033,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         bool ok = true;
         for (int n = 0; n < count; ++n) {
             const OutTile x = list[n];
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[n % C::AB], (n / C::AB) & 1, abort, wl));
+            if (ok) ok = warp_wait(&o_done[n % C::AB], (n / C::AB) & 1, abort, wl);
             tc_after();
             T *o = (T *)a.out + (size_t)(x.row0 + 32 * (warp & 3)) * a.os + (size_t)x.h * a.dv + x.v0;
             const int nr = x.nr - 32 * (warp & 3), wv = min(TN, a.dv - x.v0);
@@ -1050,11 +1089,11 @@ bool rows_map(CUtensorMap *m, const void *base, int width, int heads, int rows, 
     return encode(m, base, dims, strides, 2, box);
 }
 // Entering states as the scan leaves them: [states][d][terms][dv].
-bool states_map(CUtensorMap *m, const void *base, const LinArgs &a, int states, int terms) {
+bool states_map(CUtensorMap *m, const void *base, const LinArgs &a, int states, int terms, int box) {
     const cuuint64_t dims[4] = {(cuuint64_t)a.dv, (cuuint64_t)terms, (cuuint64_t)a.d, (cuuint64_t)states};
     const cuuint64_t row = (cuuint64_t)a.dv * 2 * terms;
     const cuuint64_t strides[3] = {(cuuint64_t)a.dv * 2, row, a.d * row};
-    return encode(m, base, dims, strides, 2, KV);
+    return encode(m, base, dims, strides, 2, box);
 }
 
 // CTAs of a persistent grid: one an SM, more where a CTA's list would overflow.
@@ -1099,10 +1138,10 @@ bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int ti
     CUtensorMap mq, mk, mv, mvi, ms, ms3;
     if (!rows_map(&mq, q, a.d, a.nh, rows, qs, CO::NT, LIN_CHUNK) || !rows_map(&mk, k, a.d, a.G, rows, ks, CO::NT, LIN_CHUNK) ||
         !rows_map(&mv, v, a.dv, a.G, rows, vs, CO::NT, CO::VR) || !rows_map(&mvi, v, a.dv, a.G, rows, vs, CO::NT, KV) ||
-        !states_map(&ms, inc, a, segs * a.nh, 2))
+        !states_map(&ms, inc, a, segs * a.nh, 2, CO::DK))
         return false;
     ms3 = ms;
-    if (CO::MT == 3 && !states_map(&ms3, third, a, segs * a.nh, 1)) return false;
+    if (CO::MT == 3 && !states_map(&ms3, third, a, segs * a.nh, 1, CO::DK)) return false;
     const int dt = (a.d + TN - 1) / TN, units = segs * a.nh * dt * ((a.dv + N - 1) / N);
     const int ot = tiles * a.nh * ((a.dv + TN - 1) / TN);
     if (CO::NT > 1) k_lin_split<T><<<prows, 256, 0, st>>>(a, t, sp);
