@@ -245,25 +245,37 @@ __device__ __forceinline__ const LinWork &find_piece(const LinWorkTable &t, int 
     return t.w[lo];
 }
 
-// A warp's 32 x 32 block of TMEM values to memory rows: through shared memory
-// (36 floats a row), so that stores cover whole lines of a row.
-constexpr int STAGE_FLOATS = 32 * 36;
-template <typename T>
-__device__ __forceinline__ void store_block(float *stage, const float (&x)[32], T *dst, size_t stride, int nr, int width,
-                                            int lane) {
+// A warp's 32 rows (a lane a row) of W 4-byte words to memory rows: through
+// shared memory (W + 4 words a row), so that stores cover whole lines of a row.
+constexpr int STAGE_WORDS = 32 * 36;
+template <int W>
+__device__ __forceinline__ void store_rows(uint32_t *stage, const uint32_t *x, void *dst, size_t stride, int nr, int width,
+                                           int lane) {
+    constexpr int LANES = W / 4, ROWS = 32 / LANES;   // 16-byte lanes of a row, rows of a store
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        *(float4 *)(stage + lane * 36 + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < LANES; ++i)
+        *(uint4 *)(stage + lane * (W + 4) + 4 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     __syncwarp();
-    const int c = 4 * (lane & 7);
-    if (c < width) {
+    const int c = lane % LANES;
+    if (16 * c < width) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            if (r < nr) o1_st4(dst + (size_t)r * stride + c, *(const float4 *)(stage + r * 36 + c));
+        for (int i = 0; i < 32 / ROWS; ++i) {
+            const int r = ROWS * i + lane / LANES;
+            if (r < nr) *(uint4 *)((char *)dst + r * stride + 16 * c) = *(const uint4 *)(stage + r * (W + 4) + 4 * c);
         }
     }
+}
+
+// Word i of a row of outputs y.
+__device__ __forceinline__ uint32_t out_word(const float *, const float *y, int i) { return __float_as_uint(y[i]); }
+__device__ __forceinline__ uint32_t out_word(const __nv_bfloat16 *, const float *y, int i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ uint32_t out_word(const __half *, const float *y, int i) {
+    const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+    return *(const uint32_t *)&h;
 }
 
 // Panels by TMA (one warp, all lanes): rows row .. row + ROWS - 1 and `boxes`
@@ -370,7 +382,7 @@ struct IncCfg {
     static constexpr int KSLOT = 3 * KV * TN * 2, NK = 2;
     static constexpr int VSLOT = NT * KV * N * 2, NV = NT == 3 ? 2 : 3;
     static constexpr int THREADS = 32 * (4 + 2 + PROD_WARPS);
-    static constexpr size_t SMEM = 1024 + (size_t)NK * KSLOT + (size_t)NV * VSLOT + 4 * STAGE_FLOATS * 4;
+    static constexpr size_t SMEM = 1024 + (size_t)NK * KSLOT + (size_t)NV * VSLOT + 4 * STAGE_WORDS * 4;
 };
 
 // dS of every (segment, head): A = weighted keys (M = d), B = values (N = dv),
@@ -391,7 +403,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
     __shared__ IncUnit list[LIST];
     volatile int *abort = &abort_s;
     unsigned char *sK = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023), *sV = sK + NK * C::KSLOT;
-    float *stage = (float *)(sV + NV * C::VSLOT);
+    uint32_t *stage = (uint32_t *)(sV + NV * C::VSLOT);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int count = (units - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;   // <= LIST
     if (tid == 0) {
@@ -549,19 +561,14 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             const int nr = a.d - x.d0 - 32 * warp, wv = min(N, a.dv - x.v0);
 #pragma unroll 1
             for (int c = 0; c < wv; c += 32) {
-                float y[32];
-                if (ok) {
-                    uint32_t r0[32], r1[32];
-                    TMEM_LD32(lanes + c, r0);
-                    TMEM_LD32(lanes + N + c, r1);
-                    tmem_ld_wait();
+                uint32_t r0[32], r1[32];
+                TMEM_LD32(lanes + c, r0);
+                TMEM_LD32(lanes + N + c, r1);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r0[i]) + __uint_as_float(r1[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = NAN;
-                }
-                store_block(stage + warp * STAGE_FLOATS, y, o + c, a.dv, nr, wv - c, lane);
+                for (int i = 0; i < 32; ++i)
+                    r0[i] = __float_as_uint(ok ? __uint_as_float(r0[i]) + __uint_as_float(r1[i]) : NAN);
+                store_rows<32>(stage + warp * STAGE_WORDS, r0, o + c, a.dv * 4, nr, 4 * (wv - c), lane);
             }
             tc_before();
             __syncwarp();
@@ -642,20 +649,21 @@ __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_consta
 
 // ---------------------------------------------------------------- outputs
 
-// Warps: 0-3 P (a thread a row), 4-7 epilogue, 8 MMA issuer, 9 TMA.
-constexpr int OUT_THREADS = 320;
+// Warps: 0-7 P (a thread a row and half of its columns), 8-11 epilogue, 12 MMA
+// issuer, 13 TMA.
+constexpr int P_WARPS = 8, OUT_THREADS = 32 * (P_WARPS + 6);
 template <typename T>
 struct OutCfg {
     static constexpr int NT = Terms<T>::in, MT = Terms<T>::mid;
     static constexpr bool PAIR = NT == 1;      // Q and K of a step share a slot
-    static constexpr int DK = NT == 1 ? 128 : 64;   // values of d a step
-    static constexpr int SLOT = NT == 1 ? 65536 : NT == 2 ? 32768 : 49152, NSLOT = NT == 1 ? 3 : NT == 2 ? 6 : 4;
+    static constexpr int DK = 64;              // values of d a step
+    static constexpr int SLOT = NT == 3 ? 49152 : 32768, NSLOT = NT == 3 ? 4 : 6;
     static constexpr int VR = NT == 1 ? 128 : 64;   // value rows of a slot
     static constexpr bool SPLIT = NT == 3;     // corrections in accumulators of their own
     // TMEM: outputs ACC (two buffers; SPLIT: one, main and corrections), then
     // scores X (two buffers; SPLIT: one, main and corrections). P overlays X.
     static constexpr int XB = SPLIT ? 1 : 2, AB = SPLIT ? 1 : 2;
-    static constexpr size_t SMEM = 1024 + (size_t)NSLOT * SLOT + 4 * STAGE_FLOATS * 4;
+    static constexpr size_t SMEM = 1024 + (size_t)NSLOT * SLOT + 4 * STAGE_WORDS * 4;
     static __device__ __forceinline__ uint32_t acc(int n) { return SPLIT ? 0u : 128u * (n & 1); }
     static __device__ __forceinline__ uint32_t x(int u) { return 256u + (SPLIT ? 0u : 128u * (u & 1)); }
     static constexpr uint32_t CORR = SPLIT ? 128u : 0u;
@@ -713,7 +721,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         fin;
     __shared__ uint32_t tslot;
     __shared__ int abort_s;
-    __shared__ float powers[4][LIN_CHUNK + 1];   // of the decay, for each P warp
+    __shared__ float powers[P_WARPS][LIN_CHUNK + 1];   // of the decay, for each P warp
     __shared__ OutTile list[LIST];
     volatile int *abort = &abort_s;
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
@@ -726,7 +734,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sc_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], P_WARPS);
             mbar_init(&acc_ready[i], 1);
             mbar_init(&o_done[i], 1);
             mbar_init(&acc_free[i], 4);
@@ -765,7 +773,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
     const long long wl = a.wait_cycles;
     const int nb = (a.d + C::DK - 1) / C::DK;   // steps of d
 
-    if (warp == 8) {
+    if (warp == P_WARPS + 4) {
         // ------------------------------------------------------ MMA issuer
         // Ring items in order: per unit, for each step of d the Q and K
         // panels and (first unit of a tile) the entering state's; the unit's
@@ -843,7 +851,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                     // P's terms 0 and 1 of 16 keys are 16 columns; the third's 8 lie apart
                     if constexpr (MT == 3)
                         issue<1, 1, 0, true, 0, 8, 0, 128>(e, acc + C::CORR, acc + C::CORR, id_a, steps, true,
-                                                           x + 128 + C::VR * i / 2, vd);
+                                                           x + 128 + C::VR * i, vd);
                     issue<2, NT, max_sum(MT, NT), true, 8, 16, TERM, 128>(e, acc, acc + C::CORR, id_a, steps, true,
                                                                          x + C::VR * i, vd);
                 }
@@ -867,7 +875,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             mbar_drain(&fin, 0);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp > P_WARPS + 4) {
         // ------------------------------------------------------------- TMA
         int it = 0;
         bool ok = true, vq = true, vv = true;
@@ -938,13 +946,13 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         // copies are over before the block ends
         if (lane == 0)
             for (int i = max(0, it - C::NSLOT); i < it; ++i) mbar_drain(&full[i % C::NSLOT], (i / C::NSLOT) & 1);
-    } else if (warp < 4) {
+    } else if (warp < P_WARPS) {
         // --------------------------------------------------------------- P
         Cursor c;
         c.start(list);
         bool have = true, ok = true;
-        const int row = tid;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+        const int row = 32 * (warp & 3) + lane, c0 = 64 * (warp >> 2);   // this warp's columns from c0
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         int table = -1;   // head of the power table
         float *pw = powers[warp];
         float g = 0.f;
@@ -956,10 +964,10 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             if (i) rp[1] ^= 1;
             else rp[0] ^= 1;
             tc_after();
-            const int wv = min(TN, a.dv - c.x.v0);
+            const int wv = min(c0 + 64, c.x.nv);
             for (int half = 0; half <= (C::SPLIT ? 1 : 0); ++half)
 #pragma unroll 1
-                for (int cb = 0; cb < wv; cb += 32) {
+                for (int cb = c0; cb < wv; cb += 32) {
                     const uint32_t ad = lanes + C::acc(c.n) + 128 * half + cb;
                     uint32_t r[32];
                     TMEM_LD32(ad, r);
@@ -988,9 +996,9 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt));
             const uint32_t x = lanes + C::x(c.u);
             // P over the scores of the same keys; a third term of 32 keys
-            // takes 16 columns of the corrections, of keys already read
+            // takes 16 columns of the corrections, of keys this warp has read
 #pragma unroll 1
-            for (int cb = 0; cb < LIN_CHUNK; cb += 32) {
+            for (int cb = c0; cb < c0 + 64; cb += 32) {
                 uint32_t r[32], third[16];
                 float s[32];
                 TMEM_LD32(x + cb, r);
@@ -1015,7 +1023,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                         if (C::SPLIT) third[8 * q + e] = take_pair(x0, x1);
                     }
                 TMEM_ST32(x + cb, r);
-                if (C::SPLIT) TMEM_ST16(x + 128 + cb / 2, third);
+                if (C::SPLIT) TMEM_ST16(x + 128 + c0 + (cb - c0) / 2, third);
             }
             if (c.kt == 0 && !diag) ok = weight(lin_pow(g, c.x.i0));
             if (diag && ok) ok = weight(pw[row + 1]);
@@ -1028,7 +1036,10 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         }
     } else {
         // -------------------------------------------------------- epilogue
-        float *stage = (float *)(sm + (size_t)C::NSLOT * C::SLOT) + (warp & 3) * STAGE_FLOATS;
+        // The accumulator is read into registers, as output words, and given
+        // back before the stores (fp32: half of it at a time).
+        constexpr int W = 8 * sizeof(T), B = sizeof(T) == 2 ? 4 : 2;   // words of 32 columns; such blocks held
+        uint32_t *stage = (uint32_t *)(sm + (size_t)C::NSLOT * C::SLOT) + (warp & 3) * STAGE_WORDS;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         bool ok = true;
         for (int n = 0; n < count; ++n) {
@@ -1038,31 +1049,40 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             T *o = (T *)a.out + (size_t)(x.row0 + 32 * (warp & 3)) * a.os + (size_t)x.h * a.dv + x.v0;
             const int nr = x.nr - 32 * (warp & 3), wv = min(TN, a.dv - x.v0);
 #pragma unroll 1
-            for (int cb = 0; cb < wv; cb += 32) {
-                float y[32];
-                if (ok) {
+            for (int c0 = 0; c0 < TN; c0 += 32 * B) {
+                uint32_t w[B * W];
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const uint32_t ad = lanes + C::acc(n) + c0 + 32 * b;
                     uint32_t r[32];
-                    TMEM_LD32(lanes + C::acc(n) + cb, r);
+                    float y[32];
+                    TMEM_LD32(ad, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r[i]);
                     if (C::SPLIT) {
-                        TMEM_LD32(lanes + C::acc(n) + C::CORR + cb, r);
+                        TMEM_LD32(ad + C::CORR, r);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) y[i] += __uint_as_float(r[i]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] *= a.scale;
-                } else {
+                    for (int i = 0; i < 32; ++i) y[i] = ok ? y[i] * a.scale : NAN;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = NAN;
+                    for (int i = 0; i < W; ++i) w[b * W + i] = out_word((const T *)nullptr, y, i);
                 }
-                store_block(stage, y, o + cb, a.os, nr, wv - cb, lane);
+                if (c0 + 32 * B == TN) {
+                    tc_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&acc_free[n % C::AB]);
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const int c = c0 + 32 * b;
+                    if (c < wv)
+                        store_rows<W>(stage, w + b * W, o + c, a.os * sizeof(T), nr, (wv - c) * (int)sizeof(T), lane);
+                }
             }
-            tc_before();
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&acc_free[n % C::AB]);
         }
     }
     tc_before();
