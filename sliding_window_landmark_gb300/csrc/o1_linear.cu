@@ -18,106 +18,167 @@ constexpr int ROW_THREADS = 256;
 // the sequence's rows, and written once. A row's output is a sum over the
 // state rows: lanes by shuffles, warps through shared memory.
 //
-// Bound: HBM, by the state (8 d dv bytes a head and step). The columns
-// of a CTA are chosen by the launcher so that a batch of one still spreads
-// over the SMs.
-template <typename T, int NI>
-__device__ __forceinline__ void lin_rows(const LinArgs &a, int slot, int row0, int rows, int h, int col0) {
-    __shared__ float4 red[2][ROW_THREADS / 32][32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int vl = a.cols >> 2;                      // lanes along the columns (a power of two, <= 32)
-    const int c = tid & (vl - 1), dg = tid / vl, DG = ROW_THREADS / vl;
-    const int col = col0 + 4 * c;
-    const bool in = col < a.dv;
-    const int g = h / a.hpg;
-    // One step's decay as near + dec: 0 + e^g, or 1 + (e^g - 1) for slow
-    // decays. e^g rounded to fp32 is off by up to 2^-25 every step, the same
-    // way each time; over the 1 / |g| steps a slow state remembers that adds
-    // up to 2^-25 / |g|, while expm1f's error is 2^-24 |g| a step.
-    const float gd = a.decay[h];
-    const float near = gd > -0.35f ? 1.f : 0.f, dec = gd > -0.35f ? expm1f(gd) : expf(gd);
-    float *S = a.state + ((size_t)slot * a.nh + h) * a.d * a.dv;
-    const T *q = (const T *)a.q + (size_t)row0 * a.qs + (size_t)h * a.d;
-    const T *k = (const T *)a.k + (size_t)row0 * a.ks + (size_t)g * a.d;
-    const T *v = (const T *)a.v + (size_t)row0 * a.vs + (size_t)g * a.dv;
-    T *o = (T *)a.out + (size_t)row0 * a.os + (size_t)h * a.dv;
-    float4 s[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int di = dg + DG * i;
-        s[i] = in && di < a.d ? *(const float4 *)(S + (size_t)di * a.dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+// One step's decay is near + dec: 0 + e^g, or 1 + (e^g - 1) for slow decays.
+// e^g rounded to fp32 is off by up to 2^-25 every step, the same way each
+// time; over the 1 / |g| steps a slow state remembers that adds up to
+// 2^-25 / |g|, while expm1f's error is 2^-24 |g| a step.
+struct RowThread {
+    int c, dg, DG, vl, col;   // column group, first state row, their step, lanes along the columns, column
+    bool in;
+    float near, dec;
+    __device__ __forceinline__ RowThread(const LinArgs &a, int h, int col0) {
+        vl = a.cols >> 2;   // a power of two, at most 32
+        c = threadIdx.x & (vl - 1);
+        dg = threadIdx.x / vl;
+        DG = ROW_THREADS / vl;
+        col = col0 + 4 * c;
+        in = col < a.dv;
+        const float g = a.decay[h];
+        near = g > -0.35f ? 1.f : 0.f;
+        dec = g > -0.35f ? expm1f(g) : expf(g);
     }
-    for (int r = 0; r < rows; ++r) {
-        const float4 vv = in ? o1_ld4(v + (size_t)r * a.vs + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int di = dg + DG * i;
-            const float kk = di < a.d ? o1_ld1(k + (size_t)r * a.ks + di) : 0.f;
-            const float qq = di < a.d ? o1_ld1(q + (size_t)r * a.qs + di) : 0.f;
-            s[i].x = fmaf(s[i].x, near, fmaf(s[i].x, dec, kk * vv.x));
-            s[i].y = fmaf(s[i].y, near, fmaf(s[i].y, dec, kk * vv.y));
-            s[i].z = fmaf(s[i].z, near, fmaf(s[i].z, dec, kk * vv.z));
-            s[i].w = fmaf(s[i].w, near, fmaf(s[i].w, dec, kk * vv.w));
-            acc.x = fmaf(qq, s[i].x, acc.x);
-            acc.y = fmaf(qq, s[i].y, acc.y);
-            acc.z = fmaf(qq, s[i].z, acc.z);
-            acc.w = fmaf(qq, s[i].w, acc.w);
-        }
+    __device__ __forceinline__ void step(float4 &s, float4 &acc, float k, float q, const float4 &v) const {
+        s.x = fmaf(s.x, near, fmaf(s.x, dec, k * v.x));
+        s.y = fmaf(s.y, near, fmaf(s.y, dec, k * v.y));
+        s.z = fmaf(s.z, near, fmaf(s.z, dec, k * v.z));
+        s.w = fmaf(s.w, near, fmaf(s.w, dec, k * v.w));
+        acc.x = fmaf(q, s.x, acc.x);
+        acc.y = fmaf(q, s.y, acc.y);
+        acc.z = fmaf(q, s.z, acc.z);
+        acc.w = fmaf(q, s.w, acc.w);
+    }
+    // the block's sum over the state rows, at the threads below vl; `red`
+    // holds one row, read before the barrier of the next row on it
+    __device__ __forceinline__ float4 sum(float4 acc, float4 (*red)[32]) const {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         for (int m = vl; m < 32; m <<= 1) {
             acc.x += __shfl_xor_sync(0xffffffffu, acc.x, m);
             acc.y += __shfl_xor_sync(0xffffffffu, acc.y, m);
             acc.z += __shfl_xor_sync(0xffffffffu, acc.z, m);
             acc.w += __shfl_xor_sync(0xffffffffu, acc.w, m);
         }
-        // two buffers: row r + 2 writes this one after the barrier of row
-        // r + 1, which its readers reach only when done
-        if (lane < vl) red[r & 1][warp][lane] = acc;
+        if (lane < vl) red[warp][lane] = acc;
         __syncthreads();
-        if (tid < vl && in) {
-            float4 t = red[r & 1][0][tid];
+        if (threadIdx.x < vl) {
+            acc = red[0][threadIdx.x];
 #pragma unroll
             for (int w = 1; w < ROW_THREADS / 32; ++w) {
-                const float4 x = red[r & 1][w][tid];
-                t.x += x.x;
-                t.y += x.y;
-                t.z += x.z;
-                t.w += x.w;
+                const float4 x = red[w][threadIdx.x];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
             }
-            o1_st4(o + (size_t)r * a.os + col,
-                   make_float4(t.x * a.scale, t.y * a.scale, t.z * a.scale, t.w * a.scale));
+        }
+        return acc;
+    }
+};
+__device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
+
+// Token batch: row r on slot slots[r]. A row whose slot an earlier row names
+// is padding (two CTAs on one state would race), so every CTA looks through
+// the earlier rows' slots, under the state's loads. The state goes back before
+// the output's sum. Bound: HBM, by the state (8 d dv bytes a head and step).
+template <typename T, int NI>
+__global__ __launch_bounds__(ROW_THREADS, 3) void k_lin_token(LinArgs a) {
+    __shared__ float4 red[ROW_THREADS / 32][32];
+    __shared__ float sq[O1_MAX_D], sk[O1_MAX_D];
+    const int ns = (a.dv + a.cols - 1) / a.cols, h = blockIdx.y, g = h / a.hpg;
+    const int r = blockIdx.x / ns, col0 = (blockIdx.x - r * ns) * a.cols;
+    const int slot = a.slots ? a.slots[r] : r;
+    if (slot < 0 || slot >= a.nslots) return;
+    const RowThread t(a, h, col0);
+    float *S = a.state + ((size_t)slot * a.nh + h) * a.d * a.dv + t.col;
+    float4 s[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int di = t.dg + t.DG * i;
+        s[i] = t.in && di < a.d ? *(const float4 *)(S + (size_t)di * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const T *q = (const T *)a.q + (size_t)r * a.qs + (size_t)h * a.d;
+    const T *k = (const T *)a.k + (size_t)r * a.ks + (size_t)g * a.d;
+    const T *v = (const T *)a.v + (size_t)r * a.vs + (size_t)g * a.dv;
+    const float4 vv = t.in ? o1_ld4(v + t.col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (threadIdx.x < a.d) {
+        sq[threadIdx.x] = o1_ld1(q + threadIdx.x);
+        sk[threadIdx.x] = o1_ld1(k + threadIdx.x);
+    }
+    int dup = 0;
+    if (a.slots)
+        for (int i = threadIdx.x; i < r; i += ROW_THREADS) dup |= a.slots[i] == slot;
+    if (__syncthreads_or(dup)) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int di = t.dg + t.DG * i;
+        if (di >= a.d) break;
+        t.step(s[i], acc, sk[di], sq[di], vv);
+        if (t.in) *(float4 *)(S + (size_t)di * a.dv) = s[i];
+    }
+    acc = t.sum(acc, red);
+    if (threadIdx.x < t.vl && t.in)
+        o1_st4((T *)a.out + (size_t)r * a.os + (size_t)h * a.dv + t.col, scaled(acc, a.scale));
+}
+
+// Sequences of a table, a few rows each. ROW_STEP rows of q, k and v at a time
+// come into shared memory: loaded row by row, a row took the memory's latency
+// (0.9 us).
+constexpr int ROW_STEP = 16;
+template <typename T, int NI>
+__global__ __launch_bounds__(ROW_THREADS) void k_lin_rows(LinArgs a, const __grid_constant__ LinTable tab) {
+    __shared__ float4 red[2][ROW_THREADS / 32][32];
+    __shared__ float sq[ROW_STEP][O1_MAX_D], sk[ROW_STEP][O1_MAX_D];
+    const int ns = (a.dv + a.cols - 1) / a.cols, h = blockIdx.y, g = h / a.hpg, tid = threadIdx.x;
+    const int n = blockIdx.x / ns, col0 = (blockIdx.x - n * ns) * a.cols;
+    const o1_lin_seq seq = tab.s[n];
+    const RowThread t(a, h, col0);
+    float *S = a.state + ((size_t)seq.slot * a.nh + h) * a.d * a.dv + t.col;
+    const T *q = (const T *)a.q + (size_t)seq.row0 * a.qs + (size_t)h * a.d;
+    const T *k = (const T *)a.k + (size_t)seq.row0 * a.ks + (size_t)g * a.d;
+    const T *v = (const T *)a.v + (size_t)seq.row0 * a.vs + (size_t)g * a.dv + t.col;
+    T *o = (T *)a.out + (size_t)seq.row0 * a.os + (size_t)h * a.dv + t.col;
+    float4 s[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int di = t.dg + t.DG * i;
+        s[i] = t.in && di < a.d ? *(const float4 *)(S + (size_t)di * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int d4 = a.d / 4;
+    for (int r0 = 0; r0 < seq.rows; r0 += ROW_STEP) {
+        const int nr = min(ROW_STEP, seq.rows - r0);
+        __syncthreads();
+        for (int i = tid; i < nr * d4; i += ROW_THREADS) {
+            const int r = i / d4, c = 4 * (i - r * d4);
+            *(float4 *)&sq[r][c] = o1_ld4(q + (size_t)(r0 + r) * a.qs + c);
+            *(float4 *)&sk[r][c] = o1_ld4(k + (size_t)(r0 + r) * a.ks + c);
+        }
+        __syncthreads();
+        // values a few rows ahead of their use
+        constexpr int AHEAD = 4;
+        float4 vv[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            vv[j] = t.in && j < nr ? o1_ld4(v + (size_t)(r0 + j) * a.vs) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < ROW_STEP; ++r) {
+            if (r >= nr) break;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int di = t.dg + t.DG * i;
+                const bool on = di < a.d;
+                t.step(s[i], acc, on ? sk[r][on ? di : 0] : 0.f, on ? sq[r][on ? di : 0] : 0.f, vv[r % AHEAD]);
+            }
+            if (t.in && r + AHEAD < nr) vv[r % AHEAD] = o1_ld4(v + (size_t)(r0 + r + AHEAD) * a.vs);
+            acc = t.sum(acc, red[r & 1]);
+            if (tid < t.vl && t.in) o1_st4(o + (size_t)(r0 + r) * a.os, scaled(acc, a.scale));
         }
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int di = dg + DG * i;
-        if (in && di < a.d) *(float4 *)(S + (size_t)di * a.dv + col) = s[i];
+        const int di = t.dg + t.DG * i;
+        if (t.in && di < a.d) *(float4 *)(S + (size_t)di * a.dv) = s[i];
     }
-}
-
-// Token batch: row r on slot slots[r]. A row whose slot an earlier row names
-// is padding (two CTAs on one state would race), so every CTA looks through
-// the earlier rows' slots.
-template <typename T, int NI>
-__global__ __launch_bounds__(ROW_THREADS) void k_lin_token(LinArgs a) {
-    const int ns = (a.dv + a.cols - 1) / a.cols;
-    const int r = blockIdx.x / ns, col0 = (blockIdx.x - r * ns) * a.cols;
-    const int slot = a.slots ? a.slots[r] : r;
-    if (slot < 0 || slot >= a.nslots) return;
-    if (a.slots) {
-        int dup = 0;
-        for (int i = threadIdx.x; i < r; i += ROW_THREADS) dup |= a.slots[i] == slot;
-        if (__syncthreads_or(dup)) return;
-    }
-    lin_rows<T, NI>(a, slot, r, 1, blockIdx.y, col0);
-}
-
-// Sequences of a table, a few rows each.
-template <typename T, int NI>
-__global__ __launch_bounds__(ROW_THREADS) void k_lin_rows(LinArgs a, const __grid_constant__ LinTable t) {
-    const int ns = (a.dv + a.cols - 1) / a.cols;
-    const int i = blockIdx.x / ns, col0 = (blockIdx.x - i * ns) * a.cols;
-    lin_rows<T, NI>(a, t.s[i].slot, t.s[i].row0, t.s[i].rows, blockIdx.y, col0);
 }
 
 // Columns of a CTA: as many as fill a warp's width in memory, fewer while the
@@ -168,9 +229,18 @@ size_t slot_floats(const o1_lin_geom &g) {
     return (size_t)g.groups * g.heads_per_group * g.d * g.dv;
 }
 
-// Sequences of up to LIN_ROW_MAX rows take the row kernel, longer ones the
-// chunk kernels.
-constexpr int LIN_ROW_MAX = 32;
+// Sequences of up to that many rows take the row kernel (about 0.4 us a row
+// and 2 to start), longer ones the chunk kernels, which take 14 us a call of
+// few rows in bf16 and 20 in fp32 (16 heads of 128): even at 32 and 52 rows.
+// Where a call has longer sequences too, a short one costs those kernels only
+// its tiles, and the row kernel would stand before them: a batch of the lengths
+// 700, 1, 2047, 130, 1500, 17, 64 and 333 took 66 us with 17 rows row by row.
+int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
+    const int most = lin_terms(g.dtype) == 1 ? 32 : 48;
+    for (int i = 0; i < n; ++i)
+        if (s[i].rows > most) return 4;
+    return most;
+}
 // Limits of a pass: its states are written, read, rewritten and read again and
 // are kept to what stays in the L2 (a 32768-row prompt of 2 MB a state: 412 us
 // in passes of 64 MB, 469 of 96, 472 of 128); its scratch as a whole, and its
@@ -284,9 +354,10 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     if (rc != O1_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     a.wait_cycles = o1_wait_limit();
+    const int short_rows = row_max(g, seqs, n_seq);
     int64_t tiles_all = 0;
     for (int i = 0; i < n_seq; ++i)
-        if (seqs[i].rows > LIN_ROW_MAX) tiles_all += (seqs[i].rows - 1) / LIN_CHUNK + 1;
+        if (seqs[i].rows > short_rows) tiles_all += (seqs[i].rows - 1) / LIN_CHUNK + 1;
     a.seg = seg_rows(tiles_all * a.nh * ((g.dv + 127) / 128));
     LinTable rows;
     LinWorkTable work;
@@ -310,7 +381,7 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     for (int i = 0; i < n_seq; ++i) {
         const o1_lin_seq &s = seqs[i];
         if (s.rows == 0) continue;
-        if (s.rows <= LIN_ROW_MAX) {
+        if (s.rows <= short_rows) {
             rows.s[n++] = s;
             if (n == LIN_TABLE) flush_rows();
             continue;

@@ -333,6 +333,7 @@ struct SplitArgs {
 template <typename T>
 __global__ __launch_bounds__(256) void k_lin_split(LinArgs a, const __grid_constant__ LinWorkTable t, SplitArgs s) {
     constexpr int NT = Terms<T>::in;
+    o1_chain_wait();
     const int pr = blockIdx.x;
     const LinWork &w = find_piece(t, pr, [](const LinWork &p) { return p.prow0; });
     const int r = pr - w.prow0;
@@ -364,6 +365,7 @@ __global__ __launch_bounds__(256) void k_lin_split(LinArgs a, const __grid_const
             *(uint4 *)(dst + ((size_t)m * s.prows + pr) * n * 8 + 8 * c) = make_uint4(y[0], y[1], y[2], y[3]);
         }
     }
+    o1_chain_release();   // here, not at the top: the next kernel's CTAs, one an SM, would take this one's room
 }
 
 // ------------------------------------------------------------- increments
@@ -378,7 +380,10 @@ struct IncUnit {
 template <typename T, int N>
 struct IncCfg {
     static constexpr int NT = Terms<T>::in;
-    static constexpr int NB = N == 128 ? 2 : 1;     // accumulators: main and corrections, N columns each
+    // accumulators: two, so that one is stored while the other is summed; with
+    // 128 columns main and corrections apart (the state's relative error over
+    // a 600-row bf16 prompt 2.2e-7; 3.3e-7 in one)
+    static constexpr int NB = 2, CORR = N == 128 ? 128 : 0, COLS = N + CORR;
     static constexpr int KSLOT = 3 * KV * TN * 2, NK = 2;
     static constexpr int VSLOT = NT * KV * N * 2, NV = NT == 3 ? 2 : 3;
     static constexpr int THREADS = 32 * (4 + 2 + PROD_WARPS);
@@ -447,6 +452,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
     __syncthreads();
     tc_after();
     const uint32_t tmem = tslot;
+    o1_chain_wait();   // the set-up above overlaps the kernel before
     const long long wl = a.wait_cycles;
 
     if (warp >= 6) {
@@ -527,14 +533,14 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         for (int n = 0; n < count && ok; ++n) {
             const int nr = list[n].nr;
             const uint32_t id = idesc_bf16(128, min(N, ceil16(a.dv - list[n].v0)), 1, 1);
-            const uint32_t d = tmem + (n % C::NB) * 2 * N;
+            const uint32_t d = tmem + (n % C::NB) * C::COLS;
             ok = warp_wait(&freed[n % C::NB], ((n / C::NB) & 1) ^ 1, abort, wl);
             for (int s = 0; KV * s < nr && ok; ++s, ++it) {
                 const int bk = it % NK, bv = it % NV;
                 ok = warp_wait(&kfull[bk], (it / NK) & 1, abort, wl) && warp_wait(&vfull[bv], (it / NV) & 1, abort, wl);
                 if (!ok) break;
                 tc_after();
-                issue<3, NT, 2, false, KTERM, 128, VTERM, 128>(e, d, d + N, id, min(KV, ceil16(nr - KV * s)) / 16, s > 0,
+                issue<3, NT, 2, false, KTERM, 128, VTERM, 128>(e, d, d + C::CORR, id, min(KV, ceil16(nr - KV * s)) / 16, s > 0,
                                                                desc_sw128_mn(k0 + bk * C::KSLOT, KV * 128),
                                                                desc_sw128_mn(v0 + bv * C::VSLOT, KV * 128));
                 if (e) {
@@ -554,7 +560,7 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
         bool ok = true;
         for (int n = 0; n < count; ++n) {
             const IncUnit x = list[n];
-            const uint32_t lanes = tmem + (n % C::NB) * 2 * N + ((uint32_t)(32 * warp) << 16);
+            const uint32_t lanes = tmem + (n % C::NB) * C::COLS + ((uint32_t)(32 * warp) << 16);
             if (ok) ok = warp_wait(&done[n % C::NB], (n / C::NB) & 1, abort, wl);
             tc_after();
             float *o = inc + ((size_t)x.seg * a.nh + x.h) * a.d * a.dv + (size_t)(x.d0 + 32 * warp) * a.dv + x.v0;
@@ -563,11 +569,16 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
             for (int c = 0; c < wv; c += 32) {
                 uint32_t r0[32], r1[32];
                 TMEM_LD32(lanes + c, r0);
-                TMEM_LD32(lanes + N + c, r1);
+                if (C::CORR) TMEM_LD32(lanes + C::CORR + c, r1);
                 tmem_ld_wait();
+                if (C::CORR) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    r0[i] = __float_as_uint(ok ? __uint_as_float(r0[i]) + __uint_as_float(r1[i]) : NAN);
+                    for (int i = 0; i < 32; ++i) r0[i] = __float_as_uint(__uint_as_float(r0[i]) + __uint_as_float(r1[i]));
+                }
+                if (!ok) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r0[i] = __float_as_uint(NAN);
+                }
                 store_rows<32>(stage + warp * STAGE_WORDS, r0, o + c, a.dv * 4, nr, 4 * (wv - c), lane);
             }
             tc_before();
@@ -645,6 +656,7 @@ __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_consta
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         if (in[j]) *(float4 *)(sp + 4 * lane + 128 * j) = s[j];
+    o1_chain_release();   // as in the split
 }
 
 // ---------------------------------------------------------------- outputs
@@ -770,6 +782,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
     __syncthreads();
     tc_after();
     const uint32_t tmem = tslot;
+    o1_chain_wait();   // the set-up above overlaps the scan
     const long long wl = a.wait_cycles;
     const int nb = (a.d + C::DK - 1) / C::DK;   // steps of d
 
@@ -1164,10 +1177,14 @@ bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int ti
     if (CO::MT == 3 && !states_map(&ms3, third, a, segs * a.nh, 1, CO::DK)) return false;
     const int dt = (a.d + TN - 1) / TN, units = segs * a.nh * dt * ((a.dv + N - 1) / N);
     const int ot = tiles * a.nh * ((a.dv + TN - 1) / TN);
-    if (CO::NT > 1) k_lin_split<T><<<prows, 256, 0, st>>>(a, t, sp);
-    k_lin_inc<T, N><<<grid_of(units), CI::THREADS, CI::SMEM, st>>>(a, t, mvi, units, inc);
+    // Chained launches: a kernel's set-up runs under the end of the one before
+    // (1024 fp32 rows 45.5 -> 43 us). Not the scan: its blocks, small and many,
+    // would pile up on the SMs that finish first (1024 bf16 rows of 256 columns
+    // 24.6 -> 27 us).
+    if (CO::NT > 1) o1_launch_chained(true, k_lin_split<T>, dim3(prows), dim3(256), 0, st, a, t, sp);
+    o1_launch_chained(true, k_lin_inc<T, N>, dim3(grid_of(units)), dim3(CI::THREADS), CI::SMEM, st, a, t, mvi, units, inc);
     k_lin_scan<CO::MT><<<dim3((a.d + 7) / 8, a.nh, t.n), 256, 0, st>>>(a, t, inc, third);
-    k_lin_out<T><<<grid_of(ot), OUT_THREADS, CO::SMEM, st>>>(a, t, mq, mk, mv, ms, ms3, ot);
+    o1_launch_chained(true, k_lin_out<T>, dim3(grid_of(ot)), dim3(OUT_THREADS), CO::SMEM, st, a, t, mq, mk, mv, ms, ms3, ot);
     return true;
 }
 
