@@ -3,9 +3,15 @@
 // dory_prep). Per head vector: sum of squares, one factor, the weight, the
 // half-split rotation of its first `rot` values.
 //
-// Bound: HBM. Each value is read once and written once; the cosine and sine
-// of a row's rot/2 angles are shared by all its heads, so a block takes
-// whole rows and makes their table in shared memory first.
+// Bound: HBM; each value is read once and written once. What stands against it
+// is the instruction count (a kernel with a lane on 8 consecutive values and
+// rotation partners read again took 176 us for 32749 bf16 rows of 20 heads of
+// 128, whose bytes take 50), so a lane holds both values of four rotation
+// pairs: 4 values from the head's lower half and the 4 half a rotation further
+// on (past the rotated part: 8 in a row). 32 / lanes heads run side by side. A
+// warp walks over rows with its weights and frequencies in registers, and over
+// the heads of a row with the row's cosines times the weights; the loads of
+// several heads go out before the cosines are made.
 //
 // Angles. p inv_j has to be known modulo 2 pi to fp32 accuracy for positions
 // in the millions, and FP64 runs at a small fraction of the fp32 rate on this
@@ -19,8 +25,7 @@
 
 namespace {
 
-constexpr int PREP_THREADS = 256;
-constexpr int PREP_ROWS = 4;   // rows of a block
+constexpr int PREP_WARPS = 8;
 
 struct PrepArgs {
     const void *q, *k;
@@ -30,6 +35,7 @@ struct PrepArgs {
     int64_t pos0;
     size_t qs, ks, qos, kos;   // row strides, elements
     int rows, hq, hk, d, rot, norm;
+    int parts, per;   // warps of a row, and heads of one
     float eps;
 };
 
@@ -51,75 +57,151 @@ __device__ __forceinline__ uint64_t turns_of(float inv) {
     return s < 128 ? t2 >> (s - 64) : 0;
 }
 
-template <typename Tin, typename Tout>
-__global__ __launch_bounds__(PREP_THREADS) void k_prep(PrepArgs a) {
-    __shared__ float2 cs[PREP_ROWS][O1_MAX_D / 2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r0 = blockIdx.x * PREP_ROWS, nr = min(PREP_ROWS, a.rows - r0);
-    const int half = a.rot >> 1, nh = a.hq + a.hk;
-    for (int i = tid; i < nr * half; i += PREP_THREADS) {
-        const int r = i / half, j = i - r * half;
-        const int64_t p = a.pos ? a.pos[r0 + r] : a.pos0 + r0 + r;
-        const int64_t frac = (int64_t)(turns_of(a.inv[j]) * (uint64_t)p);   // in [-1/2, 1/2) turn
-        float s, c;
-        sincospif((float)frac * 0x1p-63f, &s, &c);
-        cs[r][j] = make_float2(c, s);
+template <typename T>
+struct Raw4 {
+    using type = uint2;
+};
+template <>
+struct Raw4<float> {
+    using type = float4;
+};
+
+// LPV lanes of 8 values a head (a power of two, 8 LPV >= d)
+template <typename Tin, typename Tout, int LPV>
+__global__ __launch_bounds__(32 * PREP_WARPS, 3) void k_prep(PrepArgs a) {
+    using R = typename Raw4<Tin>::type;
+    constexpr int SIDE = 32 / LPV, U = sizeof(Tin) == 4 ? 2 : 4;   // heads side by side, and rounds of them in flight
+    constexpr int NJ = LPV / 8 > 1 ? LPV / 8 : 1;                  // frequencies of a lane
+    __shared__ float2 table[PREP_WARPS][O1_MAX_D / 2];
+    __shared__ __align__(16) float sw[2][O1_MAX_D];   // weights of q and k
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = lane % LPV, side = lane / LPV;
+    const int half = a.rot >> 1, pairs = a.rot >> 3;
+    const bool on = 8 * slot < a.d, rotates = slot < pairs;
+    const int lo = on ? rotates ? 4 * slot : 8 * slot : 0, hi = on ? rotates ? lo + half : lo + 4 : 0;
+    float2 *cs = table[warp];
+    uint64_t turns[NJ];
+#pragma unroll
+    for (int i = 0; i < NJ; ++i) turns[i] = lane + 32 * i < half ? turns_of(a.inv[lane + 32 * i]) : 0;
+    for (int i = threadIdx.x; i < 2 * a.d; i += 32 * PREP_WARPS) {
+        const int t = i >= a.d, c = i - t * a.d;
+        const float *p = t ? a.kw : a.qw;
+        sw[t][c] = p ? p[c] : 1.f;
     }
     __syncthreads();
-    for (int it = warp; it < nr * nh; it += PREP_THREADS / 32) {
-        const int r = it / nh, h = it - r * nh;
-        const bool isq = h < a.hq;
-        const Tin *x = isq ? (const Tin *)a.q + (size_t)(r0 + r) * a.qs + (size_t)h * a.d
-                           : (const Tin *)a.k + (size_t)(r0 + r) * a.ks + (size_t)(h - a.hq) * a.d;
-        Tout *o = isq ? (Tout *)a.qo + (size_t)(r0 + r) * a.qos + (size_t)h * a.d
-                      : (Tout *)a.ko + (size_t)(r0 + r) * a.kos + (size_t)(h - a.hq) * a.d;
-        const float *w = isq ? a.qw : a.kw;
-        float4 v[2], u[2];   // values 4 lane + 128 i and their rotation partners
-        float ss = 0.f;
+    const float inv_d = a.norm == O1_NORM_RMS ? 1.f / (float)a.d : 1.f;
+    const int64_t items = (int64_t)a.rows * a.parts;
+    for (int64_t it = (int64_t)blockIdx.x * PREP_WARPS + warp; it < items; it += (int64_t)gridDim.x * PREP_WARPS) {
+        const int r = (int)(it / a.parts), part = (int)(it - (int64_t)r * a.parts);
+        const int64_t pos = a.pos ? a.pos[r] : a.pos0 + r;
+        const int h_end = min(a.hq + a.hk, (part + 1) * a.per);
+        bool made = false;
+        for (int h0 = part * a.per; h0 < h_end;) {
+            // the part's heads of q, then those of k
+            const bool isq = h0 < a.hq;
+            const int h1 = isq ? min(h_end, a.hq) : h_end;
+            const Tin *x = isq ? (const Tin *)a.q + (size_t)r * a.qs : (const Tin *)a.k + (size_t)r * a.ks - (size_t)a.hq * a.d;
+            Tout *o = isq ? (Tout *)a.qo + (size_t)r * a.qos : (Tout *)a.ko + (size_t)r * a.kos - (size_t)a.hq * a.d;
+            float c0[4], c1[4], s0[4], s1[4];   // z_lo = c0 x_lo + s0 x_hi, z_hi = c1 x_hi + s1 x_lo
+            bool have = false;
+            for (int h = h0; h < h1; h += SIDE * U) {
+                R vl[U], vh[U];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = 4 * lane + 128 * i;
-            v[i] = u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e >= a.d) continue;
-            v[i] = o1_ld4(x + e);
-            if (e < a.rot) u[i] = o1_ld4(x + (e < half ? e + half : e - half));
-            ss += v[i].x * v[i].x + v[i].y * v[i].y + v[i].z * v[i].z + v[i].w * v[i].w;
-        }
-        float f = 1.f;
-        if (a.norm != O1_NORM_NONE) {
-            ss = warp_sum(ss);
-            if (a.norm == O1_NORM_RMS) ss /= (float)a.d;
-            ss += a.eps;
-            f = ss > 0.f ? rsqrtf(ss) : 0.f;
-        }
-        __syncwarp();   // in place: every lane's loads of this head come before any store
+                for (int k = 0; k < U; ++k) {
+                    const int hh = h + SIDE * k + side;
+                    const Tin *p = x + (size_t)(hh < h1 ? hh : h) * a.d;
+                    vl[k] = *(const R *)(p + lo);
+                    vh[k] = *(const R *)(p + hi);
+                }
+                if (!made) {
+                    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = 4 * lane + 128 * i;
-            if (e >= a.d) continue;
-            float4 wv = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (w) wv = *(const float4 *)(w + e);
-            float4 y = make_float4(v[i].x * f * wv.x, v[i].y * f * wv.y, v[i].z * f * wv.z, v[i].w * f * wv.w);
-            if (e < a.rot) {
-                const bool lo = e < half;
-                const int pe = lo ? e + half : e - half, j = lo ? e : pe;
-                float4 pw = make_float4(1.f, 1.f, 1.f, 1.f);
-                if (w) pw = *(const float4 *)(w + pe);
-                const float sg = lo ? -1.f : 1.f;
-                const float2 c0 = cs[r][j], c1 = cs[r][j + 1], c2 = cs[r][j + 2], c3 = cs[r][j + 3];
-                y.x = y.x * c0.x + sg * (u[i].x * f * pw.x) * c0.y;
-                y.y = y.y * c1.x + sg * (u[i].y * f * pw.y) * c1.y;
-                y.z = y.z * c2.x + sg * (u[i].z * f * pw.z) * c2.y;
-                y.w = y.w * c3.x + sg * (u[i].w * f * pw.w) * c3.y;
+                    for (int i = 0; i < NJ; ++i)
+                        if (lane + 32 * i < half) {
+                            // the angle's fraction of a turn, [-1/2, 1/2), to 2^-32
+                            const int frac = (int)(uint32_t)((turns[i] * (uint64_t)pos) >> 32);
+                            float s, c;
+                            sincospif((float)frac * 0x1p-31f, &s, &c);
+                            cs[lane + 32 * i] = make_float2(c, s);
+                        }
+                    __syncwarp();
+                    made = true;
+                }
+                if (!have) {
+                    const float4 wl = *(const float4 *)&sw[isq ? 0 : 1][lo], wh = *(const float4 *)&sw[isq ? 0 : 1][hi];
+                    const float l4[4] = {wl.x, wl.y, wl.z, wl.w}, h4[4] = {wh.x, wh.y, wh.z, wh.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 t = rotates ? cs[lo + i] : make_float2(1.f, 0.f);
+                        c0[i] = l4[i] * t.x;
+                        s0[i] = -h4[i] * t.y;
+                        c1[i] = h4[i] * t.x;
+                        s1[i] = l4[i] * t.y;
+                    }
+                    have = true;
+                }
+                __syncwarp();   // in place: every lane's loads of these heads come before any store
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int hh = h + SIDE * k + side;
+                    const float4 l = o1_ld4((const Tin *)&vl[k]), g = o1_ld4((const Tin *)&vh[k]);
+                    const float xl[4] = {l.x, l.y, l.z, l.w}, xh[4] = {g.x, g.y, g.z, g.w};
+                    float f = 1.f;
+                    if (a.norm != O1_NORM_NONE) {
+                        float ss = 0.f;
+                        if (on) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) ss = fmaf(xl[i], xl[i], fmaf(xh[i], xh[i], ss));
+                        }
+#pragma unroll
+                        for (int m = 1; m < LPV; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                        ss = fmaf(ss, inv_d, a.eps);
+                        f = ss > 0.f ? rsqrtf(ss) : 0.f;
+                    }
+                    float yl[4], yh[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        yl[i] = c0[i] * (f * xl[i]);
+                        yh[i] = c1[i] * (f * xh[i]);
+                    }
+                    if (rotates) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            yl[i] = fmaf(s0[i], f * xh[i], yl[i]);
+                            yh[i] = fmaf(s1[i], f * xl[i], yh[i]);
+                        }
+                    }
+                    if (on && hh < h1) {
+                        Tout *p = o + (size_t)hh * a.d;
+                        o1_st4(p + lo, make_float4(yl[0], yl[1], yl[2], yl[3]));
+                        o1_st4(p + hi, make_float4(yh[0], yh[1], yh[2], yh[3]));
+                    }
+                }
             }
-            o1_st4(o + e, y);
+            h0 = h1;
         }
     }
 }
 
+template <typename Tin, typename Tout, int LPV>
+void prep_launch_l(PrepArgs a, cudaStream_t st) {
+    // Warps of a row: one, or more while the rows leave SMs idle (down to the
+    // heads that a warp has in flight).
+    constexpr int UNIT = (32 / LPV) * (sizeof(Tin) == 4 ? 2 : 4), SMS = 152;
+    const int nh = a.hq + a.hk, most = (nh + UNIT - 1) / UNIT, want = (SMS * 16 - 1) / a.rows + 1;
+    a.parts = want < most ? want : most;
+    a.per = (most + a.parts - 1) / a.parts * UNIT;
+    a.parts = (nh + a.per - 1) / a.per;
+    // a warp takes several rows where there are many
+    const int64_t blocks = ((int64_t)a.rows * a.parts + PREP_WARPS - 1) / PREP_WARPS, few = 6 * SMS;
+    const int64_t grid = blocks <= few ? blocks : blocks / 4 > few ? blocks / 4 : few;
+    k_prep<Tin, Tout, LPV><<<(unsigned)(grid < (1 << 20) ? grid : 1 << 20), 32 * PREP_WARPS, 0, st>>>(a);
+}
 template <typename Tin, typename Tout>
 void prep_launch(const PrepArgs &a, cudaStream_t st) {
-    k_prep<Tin, Tout><<<(a.rows - 1) / PREP_ROWS + 1, PREP_THREADS, 0, st>>>(a);
+    if (a.d <= 32) prep_launch_l<Tin, Tout, 4>(a, st);
+    else if (a.d <= 64) prep_launch_l<Tin, Tout, 8>(a, st);
+    else if (a.d <= 128) prep_launch_l<Tin, Tout, 16>(a, st);
+    else prep_launch_l<Tin, Tout, 32>(a, st);
 }
 
 bool prep_geom_ok(const o1_prep_geom *g) {
@@ -165,7 +247,7 @@ extern "C" int o1_head_prep(const o1_prep_geom *geom, const void *q, int64_t q_s
             if (o1_spans_overlap(s, out[i])) return O1_ERR_ARG;
     }
     if (o1_spans_overlap(out[0], out[1])) return O1_ERR_ARG;
-    PrepArgs a;
+    PrepArgs a = {};
     a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
     a.qw = q_weight; a.kw = k_weight; a.inv = inv_freq; a.pos = pos; a.pos0 = pos0;
     a.qs = (size_t)q_stride; a.ks = (size_t)k_stride; a.qos = (size_t)q_out_stride; a.kos = (size_t)k_out_stride;
