@@ -57,6 +57,28 @@ __device__ __forceinline__ uint64_t turns_of(float inv) {
     return s < 128 ? t2 >> (s - 64) : 0;
 }
 
+// Two fp32 values in one register pair: the packed operations take one issue
+// for both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 template <typename T>
 struct Raw4 {
     using type = uint2;
@@ -68,20 +90,18 @@ struct Raw4<float> {
 
 // LPV lanes of 8 values a head (a power of two, 8 LPV >= d)
 template <typename Tin, typename Tout, int LPV>
-__global__ __launch_bounds__(32 * PREP_WARPS, 3) void k_prep(PrepArgs a) {
+__global__ __launch_bounds__(32 * PREP_WARPS, 4) void k_prep(PrepArgs a) {
     using R = typename Raw4<Tin>::type;
     constexpr int SIDE = 32 / LPV, U = sizeof(Tin) == 4 ? 2 : 4;   // heads side by side, and rounds of them in flight
-    constexpr int NJ = LPV / 8 > 1 ? LPV / 8 : 1;                  // frequencies of a lane
     __shared__ float2 table[PREP_WARPS][O1_MAX_D / 2];
     __shared__ __align__(16) float sw[2][O1_MAX_D];   // weights of q and k
+    __shared__ uint64_t turns[O1_MAX_D / 2];          // of one position step
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = lane % LPV, side = lane / LPV;
     const int half = a.rot >> 1, pairs = a.rot >> 3;
     const bool on = 8 * slot < a.d, rotates = slot < pairs;
     const int lo = on ? rotates ? 4 * slot : 8 * slot : 0, hi = on ? rotates ? lo + half : lo + 4 : 0;
     float2 *cs = table[warp];
-    uint64_t turns[NJ];
-#pragma unroll
-    for (int i = 0; i < NJ; ++i) turns[i] = lane + 32 * i < half ? turns_of(a.inv[lane + 32 * i]) : 0;
+    for (int j = threadIdx.x; j < half; j += 32 * PREP_WARPS) turns[j] = turns_of(a.inv[j]);
     for (int i = threadIdx.x; i < 2 * a.d; i += 32 * PREP_WARPS) {
         const int t = i >= a.d, c = i - t * a.d;
         const float *p = t ? a.kw : a.qw;
@@ -101,7 +121,7 @@ __global__ __launch_bounds__(32 * PREP_WARPS, 3) void k_prep(PrepArgs a) {
             const int h1 = isq ? min(h_end, a.hq) : h_end;
             const Tin *x = isq ? (const Tin *)a.q + (size_t)r * a.qs : (const Tin *)a.k + (size_t)r * a.ks - (size_t)a.hq * a.d;
             Tout *o = isq ? (Tout *)a.qo + (size_t)r * a.qos : (Tout *)a.ko + (size_t)r * a.kos - (size_t)a.hq * a.d;
-            float c0[4], c1[4], s0[4], s1[4];   // z_lo = c0 x_lo + s0 x_hi, z_hi = c1 x_hi + s1 x_lo
+            F2 c0[2], c1[2], s0[2], s1[2];   // z_lo = c0 x_lo + s0 x_hi, z_hi = c1 x_hi + s1 x_lo
             bool have = false;
             for (int h = h0; h < h1; h += SIDE * U) {
                 R vl[U], vh[U];
@@ -114,29 +134,29 @@ __global__ __launch_bounds__(32 * PREP_WARPS, 3) void k_prep(PrepArgs a) {
                 }
                 if (!made) {
                     __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < NJ; ++i)
-                        if (lane + 32 * i < half) {
-                            // the angle's fraction of a turn, [-1/2, 1/2), to 2^-32
-                            const int frac = (int)(uint32_t)((turns[i] * (uint64_t)pos) >> 32);
-                            float s, c;
-                            sincospif((float)frac * 0x1p-31f, &s, &c);
-                            cs[lane + 32 * i] = make_float2(c, s);
-                        }
+                    for (int j = lane; j < half; j += 32) {
+                        // the angle's fraction of a turn, [-1/2, 1/2), to 2^-32
+                        const int frac = (int)(uint32_t)((turns[j] * (uint64_t)pos) >> 32);
+                        float s, c;
+                        sincospif((float)frac * 0x1p-31f, &s, &c);
+                        cs[j] = make_float2(c, s);
+                    }
                     __syncwarp();
                     made = true;
                 }
                 if (!have) {
                     const float4 wl = *(const float4 *)&sw[isq ? 0 : 1][lo], wh = *(const float4 *)&sw[isq ? 0 : 1][hi];
-                    const float l4[4] = {wl.x, wl.y, wl.z, wl.w}, h4[4] = {wh.x, wh.y, wh.z, wh.w};
+                    float2 t[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 t = rotates ? cs[lo + i] : make_float2(1.f, 0.f);
-                        c0[i] = l4[i] * t.x;
-                        s0[i] = -h4[i] * t.y;
-                        c1[i] = h4[i] * t.x;
-                        s1[i] = l4[i] * t.y;
-                    }
+                    for (int i = 0; i < 4; ++i) t[i] = rotates ? cs[lo + i] : make_float2(1.f, 0.f);
+                    c0[0] = f2(wl.x * t[0].x, wl.y * t[1].x);
+                    c0[1] = f2(wl.z * t[2].x, wl.w * t[3].x);
+                    s0[0] = f2(-wh.x * t[0].y, -wh.y * t[1].y);
+                    s0[1] = f2(-wh.z * t[2].y, -wh.w * t[3].y);
+                    c1[0] = f2(wh.x * t[0].x, wh.y * t[1].x);
+                    c1[1] = f2(wh.z * t[2].x, wh.w * t[3].x);
+                    s1[0] = f2(wl.x * t[0].y, wl.y * t[1].y);
+                    s1[1] = f2(wl.z * t[2].y, wl.w * t[3].y);
                     have = true;
                 }
                 __syncwarp();   // in place: every lane's loads of these heads come before any store
@@ -144,31 +164,30 @@ __global__ __launch_bounds__(32 * PREP_WARPS, 3) void k_prep(PrepArgs a) {
                 for (int k = 0; k < U; ++k) {
                     const int hh = h + SIDE * k + side;
                     const float4 l = o1_ld4((const Tin *)&vl[k]), g = o1_ld4((const Tin *)&vh[k]);
-                    const float xl[4] = {l.x, l.y, l.z, l.w}, xh[4] = {g.x, g.y, g.z, g.w};
+                    const F2 xl[2] = {f2(l.x, l.y), f2(l.z, l.w)}, xh[2] = {f2(g.x, g.y), f2(g.z, g.w)};
                     float f = 1.f;
                     if (a.norm != O1_NORM_NONE) {
-                        float ss = 0.f;
-                        if (on) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) ss = fmaf(xl[i], xl[i], fmaf(xh[i], xh[i], ss));
-                        }
+                        const F2 s2 = f2_fma(xh[1], xh[1], f2_fma(xh[0], xh[0], f2_fma(xl[1], xl[1], f2_mul(xl[0], xl[0]))));
+                        float ss, s_odd;
+                        f2_get(s2, ss, s_odd);
+                        ss = on ? ss + s_odd : 0.f;
 #pragma unroll
                         for (int m = 1; m < LPV; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
                         ss = fmaf(ss, inv_d, a.eps);
                         f = ss > 0.f ? rsqrtf(ss) : 0.f;
                     }
+                    const F2 ff = f2(f, f);
                     float yl[4], yh[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        yl[i] = c0[i] * (f * xl[i]);
-                        yh[i] = c1[i] * (f * xh[i]);
-                    }
-                    if (rotates) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            yl[i] = fmaf(s0[i], f * xh[i], yl[i]);
-                            yh[i] = fmaf(s1[i], f * xl[i], yh[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const F2 ul = f2_mul(ff, xl[i]), uh = f2_mul(ff, xh[i]);
+                        F2 zl = f2_mul(c0[i], ul), zh = f2_mul(c1[i], uh);
+                        if (rotates) {
+                            zl = f2_fma(s0[i], uh, zl);
+                            zh = f2_fma(s1[i], ul, zh);
                         }
+                        f2_get(zl, yl[2 * i], yl[2 * i + 1]);
+                        f2_get(zh, yh[2 * i], yh[2 * i + 1]);
                     }
                     if (on && hh < h1) {
                         Tout *p = o + (size_t)hh * a.d;
