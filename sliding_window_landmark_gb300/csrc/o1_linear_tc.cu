@@ -45,29 +45,28 @@ constexpr int PROD_WARPS = 16, PROD = 32 * PROD_WARPS;
 constexpr int LIST = 64;  // units of a CTA, decoded once at its start
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// A warp's bounded wait, as mbar_wait, with a hint to suspend between polls:
-// ten waiting warps that poll at full rate take the shared-memory pipe from the
-// barrier operations of the others.
-__device__ __forceinline__ bool mbar_try_hint(uint64_t *bar, uint32_t parity) {
+// A warp's bounded wait, as mbar_wait, but every decision is a warp vote: the
+// .aligned instructions that follow a wait need the warp together. (With one
+// lane polling and the rest at a shuffle they raised an illegal instruction.)
+// The first look does not suspend, so that a tiny limit does run out.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(su32(bar)), "r"(parity), "r"(2000)
+        : "r"(su32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
 }
-// (Every decision is a warp vote: the .aligned instructions that follow a wait
-// need the warp together. With one lane polling and the rest at a shuffle
-// they raised an illegal instruction.)
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long limit) {
-    if (__all_sync(0xffffffffu, mbar_try_hint(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
     const long long t0 = clock64();
-    while (!__all_sync(0xffffffffu, mbar_try_hint(bar, parity)))
+    do {
         if (__any_sync(0xffffffffu, *abort || clock64() - t0 > limit)) {
             *abort = 1;
             return false;
         }
+    } while (!__all_sync(0xffffffffu, mbar_try(bar, parity)));
     return true;
 }
 // One lane of the (whole) warp.

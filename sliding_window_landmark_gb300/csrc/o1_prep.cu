@@ -92,7 +92,7 @@ struct Raw4<float> {
 template <typename Tin, typename Tout, int LPV>
 __global__ __launch_bounds__(32 * PREP_WARPS, 4) void k_prep(PrepArgs a) {
     using R = typename Raw4<Tin>::type;
-    constexpr int SIDE = 32 / LPV, U = sizeof(Tin) == 4 ? 2 : 4;   // heads side by side, and rounds of them in flight
+    constexpr int SIDE = 32 / LPV, U = 2;   // heads side by side, and rounds of them in flight
     __shared__ float2 table[PREP_WARPS][O1_MAX_D / 2];
     __shared__ __align__(16) float sw[2][O1_MAX_D];   // weights of q and k
     __shared__ uint64_t turns[O1_MAX_D / 2];          // of one position step
@@ -205,7 +205,7 @@ template <typename Tin, typename Tout, int LPV>
 void prep_launch_l(PrepArgs a, cudaStream_t st) {
     // Warps of a row: one, or more while the rows leave SMs idle (down to the
     // heads that a warp has in flight).
-    constexpr int UNIT = (32 / LPV) * (sizeof(Tin) == 4 ? 2 : 4), SMS = 152;
+    constexpr int UNIT = (32 / LPV) * 2, SMS = 152;
     const int nh = a.hq + a.hk, most = (nh + UNIT - 1) / UNIT, want = (SMS * 16 - 1) / a.rows + 1;
     a.parts = want < most ? want : most;
     a.per = (most + a.parts - 1) / a.parts * UNIT;

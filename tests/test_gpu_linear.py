@@ -326,3 +326,28 @@ def test_prep_prompt_and_tokens_together(o1):
         z, mag = ref.prep(src, w, inv, pos, d, "rms", 1e-6)
         ref.assert_within(got, z, ref.prep_bound(z, mag, d, F32), "prep")
     check(o1, {**x, "q": pq, "k": pk}, s0, [(0, rows, 0)], out, geom.scale, "together")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_expired_waits_raise_the_flag(o1, dt):
+    """Waits cut to a clock cycle run out: the call ends, the flag is raised, what its
+    blocks would have written is NaN, and with the limit restored the next
+    call is right again."""
+    x = make(2, 2, 128, 128, 600, 1, dt, 59)
+    geom, s0 = o1.lin_geom(2, 2, 128, 128, dtype=dt), x["state"].clone()
+    assert o1.o1_lin_flags() == 0
+    out = torch.zeros(600, 4, 128, dtype=dt, device="cuda")
+    o1.o1_set_wait_limit(1)
+    try:
+        chunk(o1, x, geom, [(0, 600, 0)], out)
+        torch.cuda.synchronize()
+    finally:
+        o1.o1_set_wait_limit(0)
+    assert o1.o1_lin_flags(clear=True) == o1.O1_FLAG_WAIT_EXPIRED
+    assert o1.o1_lin_flags() == 0
+    assert torch.isnan(out).any()
+    x["state"].copy_(s0)
+    out.fill_(float("nan"))
+    chunk(o1, x, geom, [(0, 600, 0)], out)
+    torch.cuda.synchronize()
+    check(o1, x, s0, [(0, 600, 0)], out, geom.scale, "after expiry")
