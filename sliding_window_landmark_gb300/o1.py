@@ -387,38 +387,45 @@ def lin_seqs(seqs):
     return (o1_lin_seq * len(seqs))(*[tuple(int(x) for x in s) for s in seqs])
 
 
-def _rows(t, heads: int, width: int, dtype: int, rows: int, name: str, dev: int):
+_TYPES = {n: t for t, n in DTYPES.items()}
+
+
+def _rows(t, heads: int, width: int, dtype, rows: int, name: str, dev: int):
     """Pointer and row stride of a [rows, heads, width] tensor on device `dev`
-    whose heads and widths are contiguous (None where it has no heads -> NULL)."""
+    whose heads and widths are contiguous (None where it has no heads -> NULL).
+    One look where all is right; the reason is sought where it is not."""
     if t is None and heads == 0:
         return None, 0
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == (rows, heads, width):
+        row, head, one = t.stride()
+        if one == 1 and (head == width or heads == 1):
+            return t.data_ptr(), row if rows > 1 else heads * width
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    if DTYPES.get(t.dtype) != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: element type {t.dtype} is not the geometry's")
     if t.shape != (rows, heads, width):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need {(rows, heads, width)}")
-    row, head, one = t.stride()
-    if (one != 1 or (head != width and heads > 1)) and t.numel():
-        raise ValueError(f"{name}: heads and widths must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
-    return t.data_ptr(), row if rows > 1 else heads * width
+    if not t.numel():
+        return None, heads * width
+    raise ValueError(f"{name}: heads and widths must be contiguous")
 
 
 def _flat(t, n: int, dtype, name: str, dev: int):
     """Pointer of a contiguous tensor of at least n elements on device `dev`."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous tensor of {n} elements")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on device {t.get_device()}, the current device is {dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: need a contiguous tensor of {n} elements")
 
 
 def o1_head_prep(g: o1_prep_geom, q, k, q_weight, k_weight, inv_freq, q_out, k_out, pos=None, pos0: int = 0,
@@ -426,11 +433,11 @@ def o1_head_prep(g: o1_prep_geom, q, k, q_weight, k_weight, inv_freq, q_out, k_o
     """Per-head norm and rotation of q [rows, q_heads, d] and k [rows, k_heads,
     d] into q_out and k_out (which may be q and k themselves)."""
     dev, hq, hk, d = torch.cuda.current_device(), g.q_heads, g.k_heads, g.d
-    rows = (q if hq else k).shape[0]
-    qp, qs = _rows(q, hq, d, g.in_dtype, rows, "q", dev)
-    kp, ks = _rows(k, hk, d, g.in_dtype, rows, "k", dev)
-    qo, qos = _rows(q_out, hq, d, g.out_dtype, rows, "q_out", dev)
-    ko, kos = _rows(k_out, hk, d, g.out_dtype, rows, "k_out", dev)
+    rows, tin, tout = (q if hq else k).shape[0], _TYPES[g.in_dtype], _TYPES[g.out_dtype]
+    qp, qs = _rows(q, hq, d, tin, rows, "q", dev)
+    kp, ks = _rows(k, hk, d, tin, rows, "k", dev)
+    qo, qos = _rows(q_out, hq, d, tout, rows, "q_out", dev)
+    ko, kos = _rows(k_out, hk, d, tout, rows, "k_out", dev)
     f32 = torch.float32
     return LIB.o1_head_prep(
         ctypes.byref(g), qp, qs, kp, ks, _flat(q_weight, d, f32, "q_weight", dev), _flat(k_weight, d, f32, "k_weight", dev),
@@ -449,11 +456,13 @@ def o1_lin_scratch_bytes(g: o1_lin_geom, rows: int, seqs: int = 1) -> int:
 def _lin_tensors(state, g: o1_lin_geom, q, k, v, out, log_decay, dev: int):
     """The C arguments of a linear layer's tensors: state and slots; q, k, v
     with their strides; the decays; out with its stride; rows."""
-    G, nh, d, dv, dt = g.groups, g.nh, g.d, g.dv, g.dtype
-    if not isinstance(state, torch.Tensor) or state.shape[1:] != (nh, d, dv):
+    G, d, dv, dt = g.groups, g.d, g.dv, _TYPES[g.dtype]
+    nh = G * g.heads_per_group
+    shape = state.shape
+    if shape[1:] != (nh, d, dv):
         raise ValueError(f"state: need a [slots, {nh}, {d}, {dv}] tensor")
     rows = q.shape[0]
-    return ((_flat(state, 1, torch.float32, "state", dev), state.shape[0]),
+    return ((_flat(state, 1, torch.float32, "state", dev), shape[0]),
             (*_rows(q, nh, d, dt, rows, "q", dev), *_rows(k, G, d, dt, rows, "k", dev), *_rows(v, G, dv, dt, rows, "v", dev),
              _flat(log_decay, nh, torch.float32, "log_decay", dev)),
             _rows(out, nh, dv, dt, rows, "out", dev), rows)
