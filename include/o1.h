@@ -448,16 +448,20 @@ O1_API size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_
  *   scratch    device, 256-byte aligned, see o1_lin_scratch_bytes
  *   q, k, v    device row tensors [total_rows][nh][d], [..][G][d], [..][G][dv]
  *   log_decay  device [nh], each in [-inf, 0] (0: no decay)
- *   seqs       host [n_seq], read during the call; rows of a sequence may be
- *              0; row ranges may not overlap, row0 + rows <= total_rows, and
- *              slots are distinct and in [0, n_slots) (else O1_ERR_ARG)
+ *   seqs       host [n_seq], n_seq <= 4096, read during the call; rows of a
+ *              sequence may be 0; row ranges may not overlap, row0 + rows <=
+ *              total_rows, and slots are distinct and in [0, n_slots) (else
+ *              O1_ERR_ARG)
  *   out        device row tensor [total_rows][nh][dv]; rows of no sequence
  *              are left as they were
- * q, k, v and the state are finite; a non-finite value spoils rows of its own
- * sequence only, from up to 127 rows before it. States and sums are fp32;
- * operands of 16-bit and fp32 products alike are split into bf16 terms that
- * hold them to fp32 accuracy in the state (to the output type's accuracy in
- * the outputs). Asynchronous. */
+ * q, k, v and the state are finite, in fp32 at most 3.38e38 (the largest bf16
+ * value). A non-finite one spoils rows and the state of its own sequence only:
+ * from its row on, and up to 127 rows before it. Rows of no sequence may hold
+ * anything. States and sums are fp32. Longer sequences run on the tensor cores:
+ * operands are split into bf16 terms that hold fp32 and fp16 values and the
+ * decayed keys to fp32 accuracy; for 16-bit outputs the entering state and
+ * the scores are taken to 2^-16. Calls that may overlap on the GPU (other
+ * streams, captured graphs) need a scratch each. Asynchronous. */
 O1_API int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, void *scratch,
                                size_t scratch_bytes, const void *q, int64_t q_stride, const void *k,
                                int64_t k_stride, const void *v, int64_t v_stride, const float *log_decay,
@@ -469,7 +473,7 @@ O1_API int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom 
  * device array, so that a captured step can be replayed on other slots. A row
  * whose slot is outside [0, n_slots) is padding: its output is left as it
  * was. Of rows that name the same slot the first counts and the others are
- * padding. No scratch; one launch; asynchronous. */
+ * padding. At most 65536 rows. No scratch; one launch; asynchronous. */
 O1_API int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, const void *q,
                                int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                const float *log_decay, const int32_t *slots, void *out, int64_t out_stride,

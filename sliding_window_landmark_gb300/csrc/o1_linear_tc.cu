@@ -1,35 +1,44 @@
 // Linear attention with a decay per head over prompts, on the tensor cores.
 //
-// The recurrence S = l S + k v^T, o = q S over a chunk of C = 128 rows with
-// entering state S_in (l = e^{log_decay}):
+// The recurrence S = l S + k v^T, o = q S over the n rows of a segment (128 or
+// 256) with entering state S_in (l = e^{log_decay}):
 //   o_i   = l^{i+1} q_i S_in + sum_{j <= i} l^{i-j} (q_i . k_j) v_j
-//   S_out = l^n S_in + dS,   dS = sum_j (l^{n-1-j} k_j) v_j^T   (n rows)
-// so that only the chunk states are sequential:
-//   k_lin_inc   dS of every (chunk, head): one product of depth n
-//   k_lin_scan  per state element, over the chunks of a sequence: dS is
-//               replaced by the state entering the chunk, and the last state
-//               goes to its slot
-//   k_lin_out   every (chunk, head)'s outputs: scores Q K^T, weighted and
-//               masked into P; acc = Q S_in, then P V; o joins the two with
-//               the row's decay in fp32
+//   S_out = l^n S_in + dS,   dS = sum_j (l^{n-1-j} k_j) v_j^T
+// so that only the segments' states are sequential:
+//   k_lin_split  fp16 and fp32 rows: q, k, v as bf16 terms, once
+//   k_lin_inc    dS of every (segment, head): one product of depth n
+//   k_lin_scan   per state element, over the segments of a sequence: dS is
+//                replaced by the state entering the segment (as bf16 terms),
+//                and the last state goes to its slot
+//   k_lin_out    every (128-row tile, head)'s outputs: q S_in, scores against
+//                the segment's tiles so far, weighted and masked into P, P V
 // No step carries a weight above 1 (every power of l has an exponent >= 0), so
 // nothing overflows whatever the decay.
 //
 // Precision. The MMAs take bf16 operands with fp32 accumulation. An fp32
-// value is split into three bf16 terms (x = x0 + x1 + x2 exactly but for
-// 2^-24, each the bf16 of what the earlier leave; the subtractions are exact), an fp16
+// value is split into three bf16 terms (each the bf16 of what the earlier ones
+// leave, the subtractions exact; what is left is below 2^-24 of it), an fp16
 // value into two (exactly), a bf16 value is one; of a product's term pairs
 // those down to 2^-16 (two terms) or 2^-24 (three) are taken. bf16 terms have
 // fp32's exponent range, so no scaling is needed. States are fp32 sums: the
 // weighted keys l^{n-1-j} k_j are always three terms. The entering state and P
 // only reach the outputs: two terms where those are 16-bit, three for fp32.
+// An accumulation rounds at the size of the sum so far, so smaller products
+// come first, or have accumulators of their own: summed as they come, 600 fp32
+// rows were 1.5e-6 off in the 2-norm instead of 2.4e-7 (plain fp32: 3e-7).
 //
-// Layout. All panels are [rows][128 columns] of bf16 in two blocks of 64
-// columns, 128-byte swizzled, and serve as K-major or MN-major operands as
-// they lie: the keys are K-major for the scores and (weighted) MN-major for
-// dS, values and S_in are MN-major. Threads stage them, since every operand but a bf16 one
-// is split or weighted on the way. A chunk's rows past its sequence's end are
-// staged as zeros: what lies there is never multiplied.
+// Layout. All panels are rows of 64-column blocks of bf16, 128-byte swizzled,
+// and serve as K-major or MN-major operands as they lie: keys are K-major
+// for the scores and (weighted) MN-major for dS, values and S_in are MN-major.
+// Both kernels of MMAs are persistent and split by warp: TMA (or, for weighted
+// keys, staging warps), an MMA issuer, P warps, and warps that store.
+//
+// Bound, measured at 32768 bf16 rows of 8 heads of 256 (362 us, 4 passes): the
+// outputs (47 us a pass) by the L2-to-shared-memory ingest, 46 bytes a clock
+// and SM at best, 31 on average; the increments (28) by the keys' weighting and
+// splitting beside MMAs that read 96 of the 128 bytes a clock shared memory
+// gives; the scan (17) by its bytes, 7.3 TB/s. fp32 (4096 rows: 132 us) reads
+// three terms: its 128 x 128 MMAs alone take the whole shared-memory bandwidth.
 #include <math.h>
 
 #include "o1_linear.cuh"
@@ -379,9 +388,10 @@ struct IncUnit {
 template <typename T, int N>
 struct IncCfg {
     static constexpr int NT = Terms<T>::in;
-    // accumulators: two, so that one is stored while the other is summed; with
-    // 128 columns main and corrections apart (the state's relative error over
-    // a 600-row bf16 prompt 2.2e-7; 3.3e-7 in one)
+    // accumulators: two, so that one is stored (7500 cycles for 256 columns)
+    // while the other is summed: 36 -> 28 us a pass of 8192 bf16 rows of 8 heads
+    // of 256. With 128 columns main and corrections apart (the state's
+    // relative error over 600 rows 1.2e-7; in one, 256 columns, 1.6e-7)
     static constexpr int NB = 2, CORR = N == 128 ? 128 : 0, COLS = N + CORR;
     static constexpr int KSLOT = 3 * KV * TN * 2, NK = 2;
     static constexpr int VSLOT = NT * KV * N * 2, NV = NT == 3 ? 2 : 3;
@@ -661,7 +671,8 @@ __global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_consta
 // ---------------------------------------------------------------- outputs
 
 // Warps: 0-7 P (a thread a row and half of its columns), 8-11 epilogue, 12 MMA
-// issuer, 13 TMA.
+// issuer, 13 TMA. One CTA an SM: two with half the ring and TMEM each took 57
+// us a pass instead of 48.
 constexpr int P_WARPS = 8, OUT_THREADS = 32 * (P_WARPS + 6);
 template <typename T>
 struct OutCfg {
@@ -720,11 +731,11 @@ struct Cursor {
 // buffers, so that P is formed under them.
 template <typename T>
 __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __grid_constant__ LinWorkTable t,
-                                                                   const __grid_constant__ CUtensorMap mq,
-                                                                   const __grid_constant__ CUtensorMap mk,
-                                                                   const __grid_constant__ CUtensorMap mv,
-                                                                   const __grid_constant__ CUtensorMap ms,
-                                                                   const __grid_constant__ CUtensorMap ms3, int tiles) {
+                                                            const __grid_constant__ CUtensorMap mq,
+                                                            const __grid_constant__ CUtensorMap mk,
+                                                            const __grid_constant__ CUtensorMap mv,
+                                                            const __grid_constant__ CUtensorMap ms,
+                                                            const __grid_constant__ CUtensorMap ms3, int tiles) {
     using C = OutCfg<T>;
     constexpr int NT = C::NT, MT = C::MT;
     extern __shared__ unsigned char smraw[];

@@ -8,10 +8,12 @@
 // rotation partners read again took 176 us for 32749 bf16 rows of 20 heads of
 // 128, whose bytes take 50), so a lane holds both values of four rotation
 // pairs: 4 values from the head's lower half and the 4 half a rotation further
-// on (past the rotated part: 8 in a row). 32 / lanes heads run side by side. A
-// warp walks over rows with its weights and frequencies in registers, and over
-// the heads of a row with the row's cosines times the weights; the loads of
-// several heads go out before the cosines are made.
+// on (past the rotated part: 8 in a row), and works on pairs in packed fp32.
+// 32 / lanes heads run side by side. A warp takes rows, or parts of a row's
+// heads, with the row's cosines times the weights in registers; the loads of
+// two rounds of heads go out before the cosines are made. The batch above: 69
+// us, 4.9 TB/s (four rounds in flight 72, three blocks an SM 82); 4096 fp32
+// rows of 10 heads of 256: 17 us.
 //
 // Angles. p inv_j has to be known modulo 2 pi to fp32 accuracy for positions
 // in the millions, and FP64 runs at a small fraction of the fp32 rate on this

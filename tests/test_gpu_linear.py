@@ -351,3 +351,68 @@ def test_expired_waits_raise_the_flag(o1, dt):
     chunk(o1, x, geom, [(0, 600, 0)], out)
     torch.cuda.synchronize()
     check(o1, x, s0, [(0, 600, 0)], out, geom.scale, "after expiry")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+def test_a_sequence_of_nans_spoils_no_neighbour(o1, dt):
+    """Three sequences end to end, the middle one NaN and infinities throughout."""
+    lens = [150, 70, 140]
+    x = make(2, 2, 64, 72, sum(lens), 3, dt, 61)
+    for n, bad in (("q", float("nan")), ("k", float("inf")), ("v", float("nan"))):
+        x[n][lens[0]:lens[0] + lens[1]] = bad
+    geom, s0 = o1.lin_geom(2, 2, 64, 72, dtype=dt), x["state"].clone()
+    seqs = [(sum(lens[:i]), n, i) for i, n in enumerate(lens)]
+    out = torch.zeros(sum(lens), 4, 72, dtype=dt, device="cuda")
+    chunk(o1, x, geom, seqs, out)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[lens[0]:lens[0] + lens[1]]).all()
+    keep = [seqs[0], seqs[2]]
+    y = {**x, "state": torch.stack([x["state"][0], s0[1], x["state"][2]])}
+    for r0, n, _ in [seqs[1]]:
+        out[r0:r0 + n] = float("nan")
+    check(o1, {**y, **{n: torch.nan_to_num(x[n], 0, 0, 0) for n in "qkv"}}, s0, keep, out, geom.scale, "neighbours")
+
+
+def test_rows_past_32_bit_offsets(o1):
+    """A row stride of 2^27 values: rows past 2^31 values from the first."""
+    rows, d = 40, 64
+    x = make(1, 1, d, d, rows, 1, BF16, 67)
+    geom, s0 = o1.lin_geom(1, 1, d, d, dtype=BF16), x["state"].clone()
+    far = torch.empty(rows << 27, dtype=BF16, device="cuda")
+    q = far.as_strided((rows, 1, d), (1 << 27, d, 1))
+    k = far[4096:].as_strided((rows, 1, d), (1 << 27, d, 1))
+    out = far[8192:].as_strided((rows, 1, d), (1 << 27, d, 1))
+    q.copy_(x["q"])
+    k.copy_(x["k"])
+    chunk(o1, {**x, "q": q, "k": k}, geom, [(0, rows, 0)], out)
+    torch.cuda.synchronize()
+    got = out.clone()
+    del far, q, k, out
+    check(o1, x, s0, [(0, rows, 0)], got, geom.scale, "far rows")
+
+
+def test_two_streams_with_a_scratch_each(o1):
+    xs = [make(2, 2, 128, 128, 900, 1, F32, 71 + i) for i in range(2)]
+    geom = o1.lin_geom(2, 2, 128, 128)
+    s0 = [x["state"].clone() for x in xs]
+    outs = [torch.full((900, 4, 128), float("nan"), device="cuda") for _ in xs]
+    scr = [torch.empty(o1.o1_lin_scratch_bytes(geom, 900), dtype=torch.uint8, device="cuda") for _ in xs]
+    st = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for i, x in enumerate(xs):
+        o1.check(o1.o1_lin_chunk_attend(x["state"], geom, scr[i], x["q"], x["k"], x["v"], x["g"], [(0, 900, 0)], outs[i],
+                                        stream=st[i]))
+    torch.cuda.synchronize()
+    for i, x in enumerate(xs):
+        check(o1, x, s0[i], [(0, 900, 0)], outs[i], geom.scale, f"stream {i}")
+
+
+def test_a_scratch_of_one_step_serves_every_type(o1):
+    """The least scratch holds one state and a few rows: steps of 16 rows."""
+    for dt in (F32, BF16, F16):
+        x = make(1, 2, 136, 72, 210, 1, dt, 73)
+        geom, s0 = o1.lin_geom(1, 2, 136, 72, dtype=dt), x["state"].clone()
+        out = torch.full((210, 2, 72), float("nan"), dtype=dt, device="cuda")
+        chunk(o1, x, geom, [(0, 210, 0)], out, scratch_rows=1)
+        torch.cuda.synchronize()
+        check(o1, x, s0, [(0, 210, 0)], out, geom.scale, f"least scratch {dt}")
