@@ -101,6 +101,23 @@ def test_chunk(o1, case):
     check(o1, x, state0, seqs, out, geom.scale, f"case {case}")
 
 
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+def test_many_tiles(o1, dt):
+    """More tiles than SMs: segments of 256 rows, of which sequences leave 1 to
+    256, and several of them, long and short in turn, for a block of threads."""
+    G, hpg, d, dv = 4, 2, 72, 136
+    lens = [700, 129, 130, 256, 64, 255, 257, 300, 128, 513, 49, 1025, 384, 100]
+    rows = sum(lens) + 2
+    x = make(G, hpg, d, dv, rows, len(lens), dt, 61)
+    seqs = [(sum(lens[:i]), n, len(lens) - 1 - i) for i, n in enumerate(lens)]
+    x["q"][-2:], x["k"][-2:], x["v"][-2:] = float("inf"), float("nan"), float("nan")
+    geom, s0 = o1.lin_geom(G, hpg, d, dv, dtype=dt), x["state"].clone()
+    out = torch.full((rows, G * hpg, dv), float("nan"), dtype=dt, device="cuda")
+    chunk(o1, x, geom, seqs, out)
+    torch.cuda.synchronize()
+    check(o1, x, s0, seqs, out, geom.scale, f"many tiles {dt}")
+
+
 @pytest.mark.parametrize("width", [128, 256])
 @pytest.mark.parametrize("dt", [F32, BF16, F16])
 def test_chunk_relative_error(o1, dt, width):
