@@ -11,9 +11,11 @@
 // on (past the rotated part: 8 in a row), and works on pairs in packed fp32.
 // 32 / lanes heads run side by side. A warp takes rows, or parts of a row's
 // heads, with the row's cosines times the weights in registers; the loads of
-// two rounds of heads go out before the cosines are made. The batch above: 69
-// us, 4.9 TB/s (four rounds in flight 72, three blocks an SM 82); 4096 fp32
-// rows of 10 heads of 256: 17 us.
+// two rounds of heads go out before the cosines are made. The batch above: 65
+// us, 5.2 TB/s, with 1450 instructions a row issued at 0.6 of the rate (four
+// rounds in flight, or the next row's loads ahead of the stores, at 64
+// registers 72 to 76; three blocks an SM with more registers 65 to 72); 4096
+// fp32 rows of 10 heads of 256: 17 us, where the pipelined form takes 20.
 //
 // Angles. p inv_j has to be known modulo 2 pi to fp32 accuracy for positions
 // in the millions, and FP64 runs at a small fraction of the fp32 rate on this
@@ -212,10 +214,12 @@ void prep_launch_l(PrepArgs a, cudaStream_t st) {
     a.parts = want < most ? want : most;
     a.per = (most + a.parts - 1) / a.parts * UNIT;
     a.parts = (nh + a.per - 1) / a.per;
-    // a warp takes several rows where there are many
-    const int64_t blocks = ((int64_t)a.rows * a.parts + PREP_WARPS - 1) / PREP_WARPS, few = 6 * SMS;
-    const int64_t grid = blocks <= few ? blocks : blocks / 4 > few ? blocks / 4 : few;
-    k_prep<Tin, Tout, LPV><<<(unsigned)(grid < (1 << 20) ? grid : 1 << 20), 32 * PREP_WARPS, 0, st>>>(a);
+    // At most the blocks that run at once (four an SM): a warp then takes rows
+    // in turn, and none of a second wave's SMs idle (the batch above: 65 us;
+    // 1.7 waves 68, a block for every 8 rows 69, 1.25 waves 80).
+    const int64_t blocks = ((int64_t)a.rows * a.parts + PREP_WARPS - 1) / PREP_WARPS, most_blocks = 4 * SMS;
+    const int64_t grid = blocks < most_blocks ? blocks : most_blocks;
+    k_prep<Tin, Tout, LPV><<<(unsigned)grid, 32 * PREP_WARPS, 0, st>>>(a);
 }
 template <typename Tin, typename Tout>
 void prep_launch(const PrepArgs &a, cudaStream_t st) {
