@@ -33,11 +33,11 @@
 // Both kernels of MMAs are persistent and split by warp: TMA (or, for weighted
 // keys, staging warps), an MMA issuer, P warps, and warps that store.
 //
-// Bound, measured at 32768 bf16 rows of 8 heads of 256 (362 us, 4 passes): the
+// Bound, measured at 32768 bf16 rows of 8 heads of 256 (358 us, 4 passes): the
 // outputs (47 us a pass) by the L2-to-shared-memory ingest, 46 bytes a clock
 // and SM at best, 31 on average; the increments (28) by the keys' weighting and
 // splitting beside MMAs that read 96 of the 128 bytes a clock shared memory
-// gives; the scan (17) by its bytes, 7.3 TB/s. fp32 (4096 rows: 132 us) reads
+// gives; the scan (17) by its bytes, 7.3 TB/s. fp32 (4096 rows: 131 us) reads
 // three terms: its 128 x 128 MMAs alone take the whole shared-memory bandwidth.
 #include <math.h>
 
@@ -722,11 +722,10 @@ struct Cursor {
 };
 
 // Outputs. Weights: with i0 the tile's first row and s0 its segment's,
-//   o_i = l^{i-i0+1} ( l^{i0-s0} q_i S_in + sum_{j<i0} l^{i0-1-j} s_ij v_j )
+//   o_i = l^{i-s0+1} q_i S_in + sum_{j<i0} l^{i-i0+1} l^{i0-1-j} s_ij v_j
 //         + sum_{i0<=j<=i} l^{i-j} s_ij v_j
-// so the accumulator is weighted once after q S_in (if earlier key tiles
-// follow) and once, by row, before the last (diagonal) tile, the earlier key
-// tiles' scores by column. The MMA thread issues the next unit's scores (and a
+// so the accumulator is weighted once, by row, after q S_in, the earlier key
+// tiles' scores by row and column. The MMA thread issues the next unit's scores (and a
 // next tile's q S_in) ahead of this unit's P V where TMEM holds two score
 // buffers, so that P is formed under them.
 template <typename T>
@@ -743,7 +742,9 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         fin;
     __shared__ uint32_t tslot;
     __shared__ int abort_s;
-    __shared__ float powers[P_WARPS][LIN_CHUNK + 1];   // of the decay, for each P warp
+    // of the decay, for each P warp: zeros for the exponents -128 .. -1 (keys
+    // past the diagonal, discarded), then l^0 .. l^128
+    __shared__ float powers[P_WARPS][2 * LIN_CHUNK + 1];
     __shared__ OutTile list[LIST];
     volatile int *abort = &abort_s;
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
@@ -881,7 +882,6 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                 commit(&empty[sv]);
             }
             if (cv.diag()) commit(&o_done[cv.n % C::AB]);
-            else if (cv.kt == cv.x.nkt - 2) commit(&acc_ready[cv.n % C::AB]);
             vv = cv.next(list, count);
         };
         for (int ahead = 0; vv && ok;) {   // units scored, their P V not issued
@@ -977,9 +977,9 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         const int row = 32 * (warp & 3) + lane, c0 = 64 * (warp >> 2);   // this warp's columns from c0
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         int table = -1;   // head of the power table
-        float *pw = powers[warp];
+        float *pw = powers[warp] + LIN_CHUNK;
         float g = 0.f;
-        uint32_t rp[2] = {0, 0};   // phases of acc_ready
+        uint32_t rp[2] = {0, 0};   // phases of acc_ready, one a tile
         // the accumulator times f, once what it holds so far is complete
         auto weight = [&](float f) -> bool {
             const int i = c.n % C::AB;
@@ -1005,7 +1005,10 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             if (table != c.x.h) {
                 __syncwarp();
                 g = a.decay[c.x.h];
-                for (int i = lane; i <= LIN_CHUNK; i += 32) pw[i] = lin_pow(g, i);
+                for (int i = lane; i <= LIN_CHUNK; i += 32) {
+                    pw[i] = lin_pow(g, i);
+                    if (i) pw[-i] = 0.f;
+                }
                 table = c.x.h;
                 __syncwarp();
             }
@@ -1014,14 +1017,15 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             tc_after();
             const bool diag = c.diag();
             // weights: l^{row - j} up to the diagonal; for an earlier tile
-            // l^{127 - j} for all its keys, and the tiles in between
+            // l^{127 - j} for all its keys, the tiles in between, and l^{row + 1}
             const int lim = diag ? row : LIN_CHUNK - 1;
-            const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt));
+            const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt)) * pw[row + 1];
             const uint32_t x = lanes + C::x(c.u);
             // P over the scores of the same keys; a third term of 32 keys
             // takes 16 columns of the corrections, of keys this warp has read
 #pragma unroll 1
             for (int cb = c0; cb < c0 + 64; cb += 32) {
+                const float *w = pw + lim - cb;
                 uint32_t r[32], third[16];
                 float s[32];
                 TMEM_LD32(x + cb, r);
@@ -1035,7 +1039,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                     for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(r[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = cb + i <= lim ? s[i] * (pw[max(lim - cb - i, 0)] * tf) : 0.f;
+                for (int i = 0; i < 32; ++i) s[i] = cb + i <= lim ? s[i] * (w[-i] * tf) : 0.f;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -1048,8 +1052,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                 TMEM_ST32(x + cb, r);
                 if (C::SPLIT) TMEM_ST16(x + 128 + c0 + (cb - c0) / 2, third);
             }
-            if (c.kt == 0 && !diag) ok = weight(lin_pow(g, c.x.i0));
-            if (diag && ok) ok = weight(pw[row + 1]);
+            if (c.kt == 0) ok = weight(lin_pow(g, c.x.i0) * pw[row + 1]);
             if (!ok) break;
             tmem_st_wait();
             tc_before();
