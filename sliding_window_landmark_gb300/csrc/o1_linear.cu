@@ -229,18 +229,6 @@ size_t slot_floats(const o1_lin_geom &g) {
     return (size_t)g.groups * g.heads_per_group * g.d * g.dv;
 }
 
-// Sequences of up to that many rows take the row kernel (about 0.4 us a row
-// and 2 to start), longer ones the chunk kernels, which take 14 us a call of
-// few rows in bf16 and 20 in fp32 (16 heads of 128): even at 32 and 52 rows.
-// Where a call has longer sequences too, a short one costs those kernels only
-// its tiles, and the row kernel would stand before them: a batch of the lengths
-// 700, 1, 2047, 130, 1500, 17, 64 and 333 took 66 us with 17 rows row by row.
-int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
-    const int most = lin_terms(g.dtype) == 1 ? 32 : 48;
-    for (int i = 0; i < n; ++i)
-        if (s[i].rows > most) return 4;
-    return most;
-}
 // Limits of a pass: its states are written, read, rewritten and read again and
 // are kept to what stays in the L2 (a 32768-row prompt of 2 MB a state: 412 us
 // in passes of 64 MB, 469 of 96, 472 of 128); its scratch as a whole, and its
@@ -265,6 +253,58 @@ bool pass_within(const o1_lin_geom &g, int64_t segs, int64_t prows) {
 // 128 rows, 22.1 with 256.
 int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : 2 * LIN_CHUNK; }
 
+// Sequences of up to that many rows take the row kernel, longer ones the chunk
+// kernels. Their times in us, E = nh d dv the elements of a sequence's states,
+// from batches of 1 to 64 sequences of 1 to 32 rows alone and beside prompts of
+// 100, 2047 and 4096 rows (16 heads of 128 bf16 and fp32, 8 of 256, 8 of 64):
+//   row kernel    2.5, 0.36 a row of the longest sequence or 2.9e-7 E a row of
+//                 them all, and the states' bytes, 1.2e-6 E a sequence
+//   chunk kernels 14 (fp32 20) a call, 0.06 (0.07) a tile of 128 rows, a head
+//                 and 128 value columns, and 1.6 a MB of the pass's states as
+//                 those outgrow the L2 (a quarter of that at half of 64 MB)
+// so few short sequences beside a prompt go with its tiles, and many apart:
+// 16 heads of 128, bf16, 2047 rows beside 2 of 16 rows 29.6 us as tiles and
+// 35.4 by rows, beside 64 of 16 rows 214 and 129.
+int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
+    constexpr int TH = 6;
+    const bool f32 = g.dtype == O1_F32;
+    const int th[TH] = {0, 1, 4, 8, 16, lin_terms(g.dtype) == 1 ? 32 : 48};
+    struct {
+        int64_t seqs, rows, longest;
+    } at[TH + 1] = {};   // of th[i - 1] + 1 .. th[i] rows; at[TH]: longer, in tiles
+    for (int i = 0; i < n; ++i) {
+        const int r = s[i].rows;
+        int b = 0;
+        while (b < TH && r > th[b]) ++b;
+        at[b].seqs += b < TH ? 1 : (r - 1) / LIN_CHUNK + 1;
+        at[b].rows += r;
+        if (r > at[b].longest) at[b].longest = r;
+    }
+    const double E = (double)slot_floats(g), units = (double)(g.groups * g.heads_per_group) * ((g.dv + 127) / 128);
+    const bool halves = at[TH].seqs * units > LIN_SMS;   // long sequences' segments are of two tiles
+    int best = 0;
+    double best_us = 0.;
+    for (int t = 0; t < TH; ++t) {   // th[t] the longest by rows
+        double seqs = 0., rows = 0., longest = 0., tiles = (double)at[TH].seqs, segs = halves ? tiles / 2 : tiles, us = 0.;
+        for (int b = 1; b < TH; ++b) {
+            if (b <= t) {
+                seqs += (double)at[b].seqs;
+                rows += (double)at[b].rows;
+                if (at[b].seqs) longest = (double)at[b].longest;
+            } else {
+                tiles += (double)at[b].seqs;
+                segs += (double)at[b].seqs;
+            }
+        }
+        if (seqs) us += 2.5 + fmax(0.36 * longest, 2.9e-7 * E * rows) + 1.2e-6 * E * seqs;
+        if (tiles) {
+            const double mb = (f32 ? 6e-6 : 4e-6) * E * segs, full = fmin(1., mb / 64.);
+            us += (f32 ? 20. : 14.) + (f32 ? 0.07 : 0.06) * units * tiles + 1.6 * mb * full * full;
+        }
+        if (t == 0 || us < best_us) best = th[t], best_us = us;
+    }
+    return best;
+}
 // The sequences of a call: ranges and slots in bounds and apart. Sorted
 // copies on the stack (nothing is allocated for a call).
 constexpr int LIN_MAX_SEQ = 4096;

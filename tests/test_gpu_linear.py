@@ -118,6 +118,21 @@ def test_many_tiles(o1, dt):
     check(o1, x, s0, seqs, out, geom.scale, f"many tiles {dt}")
 
 
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+@pytest.mark.parametrize("lens", [[300] + 40 * [1] + 3 * [16] + [0, 31, 49], 3 * [2] + [260], 2 * [33] + 30 * [5]])
+def test_short_sequences_beside_long_ones(o1, dt, lens):
+    """Short sequences by rows or with the tiles, whichever the call takes."""
+    G, hpg, d, dv = 2, 4, 64, 128
+    rows = sum(lens)
+    x = make(G, hpg, d, dv, rows, len(lens), dt, 67)
+    seqs = [(sum(lens[:i]), n, len(lens) - 1 - i) for i, n in enumerate(lens)]
+    geom, s0 = o1.lin_geom(G, hpg, d, dv, dtype=dt), x["state"].clone()
+    out = torch.full((rows, G * hpg, dv), float("nan"), dtype=dt, device="cuda")
+    chunk(o1, x, geom, seqs, out)
+    torch.cuda.synchronize()
+    check(o1, x, s0, seqs, out, geom.scale, f"{len(lens)} sequences {dt}")
+
+
 @pytest.mark.parametrize("width", [128, 256])
 @pytest.mark.parametrize("dt", [F32, BF16, F16])
 def test_chunk_relative_error(o1, dt, width):
