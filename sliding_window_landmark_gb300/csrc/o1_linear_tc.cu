@@ -609,63 +609,95 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
 // slot. The entering state is stored as the bf16 terms that the outputs
 // multiply: two in the increment's own bytes, each row of dv values as dv
 // first terms, then dv second ones (a row is one warp's, a lane the columns 4
-// lane and 128 + 4 lane, so that it is read before it is overwritten), a
-// third in `third` [states][d][dv]. Bound: the scratch's bytes, read and
-// written once; 4 segments' loads go out ahead of their use.
-template <int MT>
-__global__ __launch_bounds__(256) void k_lin_scan(LinArgs a, const __grid_constant__ LinWorkTable t, float *inc,
-                                                  uint16_t *third) {
+// lane and, J = 2, 128 + 4 lane, so that it is read before it is overwritten),
+// a third in `third` [states][d][dv]. Bound: the scratch's bytes, read and
+// written once, as long as enough loads are out: a warp takes R rows and U
+// segments at a time, and the next U are on their way while these are stored.
+template <int MT, int R, int J>
+__global__ __launch_bounds__(256, 2) void k_lin_scan(LinArgs a, const __grid_constant__ LinWorkTable t, float *inc,
+                                                     uint16_t *third) {
+    constexpr int U = 8 / (R * J);
     const LinWork w = t.w[blockIdx.z];
-    const int h = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= a.d) return;
+    const int h = blockIdx.y, row = (blockIdx.x * 8 + (threadIdx.x >> 5)) * R, lane = threadIdx.x & 31;
+    if (row >= a.d) return;   // d is a multiple of R
     const size_t n = (size_t)a.d * a.dv, step = (size_t)a.nh * n;
     const int nc = (w.rows + a.seg - 1) / a.seg;
     const float gd = a.decay[h], full = lin_pow(gd, a.seg), last = lin_pow(gd, w.rows - (nc - 1) * a.seg);
     float *sp = a.state + ((size_t)w.slot * a.nh + h) * n + (size_t)row * a.dv;
-    float *p = inc + ((size_t)w.seg0 * a.nh + h) * n + (size_t)row * a.dv;
-    float4 s[2];
-    bool in[2];
+    const size_t first = ((size_t)w.seg0 * a.nh + h) * n + (size_t)row * a.dv;
+    float *p = inc + first;
+    float4 s[R][J], x[U][R][J], y[U][R][J];
+    bool in[J];
+    auto load = [&](float4 (&z)[U][R][J], int c) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        in[j] = 4 * lane + 128 * j < a.dv;
-        if (in[j]) s[j] = *(const float4 *)(sp + 4 * lane + 128 * j);
-    }
-    for (int c = 0; c < nc; c += 4) {
-        float4 x[4][2];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (c + i < nc && in[j]) x[i][j] = *(const float4 *)(p + (size_t)(c + i) * step + 4 * lane + 128 * j);
+                for (int j = 0; j < J; ++j)
+                    if (c + u < nc && in[j]) z[u][r][j] = *(const float4 *)(p + (size_t)(c + u) * step + r * a.dv + 4 * lane + 128 * j);
+    };
+#pragma unroll
+    for (int j = 0; j < J; ++j) in[j] = 4 * lane + 128 * j < a.dv;
+    load(x, 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (in[j]) s[r][j] = *(const float4 *)(sp + r * a.dv + 4 * lane + 128 * j);
+    for (int c = 0; c < nc; c += U) {
+        load(y, c + U);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (c + i >= nc) break;
-            const float l = c + i == nc - 1 ? last : full;
-            float *q = p + (size_t)(c + i) * step;
+        for (int u = 0; u < U; ++u) {
+            if (c + u >= nc) break;
+            const float l = c + u == nc - 1 ? last : full;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (!in[j]) continue;
-                const int col = 4 * lane + 128 * j;
-                float4 y = s[j];
-                const uint2 t0 = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
-                const uint2 t1 = make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
-                *(uint2 *)((uint16_t *)q + col) = t0;
-                *(uint2 *)((uint16_t *)q + a.dv + col) = t1;
-                if (MT == 3)
-                    *(uint2 *)(third + ((size_t)w.seg0 * a.nh + h) * n + (size_t)(c + i) * step + (size_t)row * a.dv + col) =
-                        make_uint2(take_pair(y.x, y.y), take_pair(y.z, y.w));
-                s[j].x = fmaf(s[j].x, l, x[i][j].x);
-                s[j].y = fmaf(s[j].y, l, x[i][j].y);
-                s[j].z = fmaf(s[j].z, l, x[i][j].z);
-                s[j].w = fmaf(s[j].w, l, x[i][j].w);
-            }
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (!in[j]) continue;
+                    const int col = 4 * lane + 128 * j;
+                    float4 &e = s[r][j];
+                    const float4 d = x[u][r][j];
+                    float4 m = e;
+                    const uint2 t0 = make_uint2(take_pair(m.x, m.y), take_pair(m.z, m.w));
+                    const uint2 t1 = make_uint2(take_pair(m.x, m.y), take_pair(m.z, m.w));
+                    const size_t at = (size_t)(c + u) * step + r * a.dv;
+                    *(uint2 *)((uint16_t *)(p + at) + col) = t0;
+                    *(uint2 *)((uint16_t *)(p + at) + a.dv + col) = t1;
+                    if (MT == 3) *(uint2 *)(third + first + at + col) = make_uint2(take_pair(m.x, m.y), take_pair(m.z, m.w));
+                    e = make_float4(fmaf(e.x, l, d.x), fmaf(e.y, l, d.y), fmaf(e.z, l, d.z), fmaf(e.w, l, d.w));
+                }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int j = 0; j < J; ++j) x[u][r][j] = y[u][r][j];
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (in[j]) *(float4 *)(sp + 4 * lane + 128 * j) = s[j];
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (in[j]) *(float4 *)(sp + r * a.dv + 4 * lane + 128 * j) = s[r][j];
     o1_chain_release();   // as in the split
+}
+
+template <int MT, int R, int J>
+void scan_launch_r(const LinArgs &a, const LinWorkTable &t, float *inc, uint16_t *third, cudaStream_t st) {
+    k_lin_scan<MT, R, J><<<dim3((a.d + 8 * R - 1) / (8 * R), a.nh, t.n), 256, 0, st>>>(a, t, inc, third);
+}
+// Rows of a warp: several where pieces have few segments to load ahead and the
+// rows are many.
+template <int MT, int J>
+void scan_launch(const LinArgs &a, const LinWorkTable &t, int segs, float *inc, uint16_t *third, cudaStream_t st) {
+    int R = segs <= 2 * t.n ? 4 / J : segs <= 4 * t.n ? 2 : 1;
+    while (R > 1 && (int64_t)a.d * a.nh * t.n < (int64_t)R * LIN_SMS * 16) R /= 2;
+    if (R == 1) scan_launch_r<MT, 1, J>(a, t, inc, third, st);
+    else if (R == 2) scan_launch_r<MT, 2, J>(a, t, inc, third, st);
+    else if constexpr (J == 1) scan_launch_r<MT, 4, J>(a, t, inc, third, st);
 }
 
 // ---------------------------------------------------------------- outputs
@@ -1196,7 +1228,8 @@ bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int ti
     // 24.6 -> 27 us).
     if (CO::NT > 1) o1_launch_chained(true, k_lin_split<T>, dim3(prows), dim3(256), 0, st, a, t, sp);
     o1_launch_chained(true, k_lin_inc<T, N>, dim3(grid_of(units)), dim3(CI::THREADS), CI::SMEM, st, a, t, mvi, units, inc);
-    k_lin_scan<CO::MT><<<dim3((a.d + 7) / 8, a.nh, t.n), 256, 0, st>>>(a, t, inc, third);
+    if (a.dv > 128) scan_launch<CO::MT, 2>(a, t, segs, inc, third, st);
+    else scan_launch<CO::MT, 1>(a, t, segs, inc, third, st);
     o1_launch_chained(true, k_lin_out<T>, dim3(grid_of(ot)), dim3(OUT_THREADS), CO::SMEM, st, a, t, mq, mk, mv, ms, ms3, ot);
     return true;
 }
