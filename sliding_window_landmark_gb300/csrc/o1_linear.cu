@@ -259,12 +259,13 @@ int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : 2 * LIN_CHUN
 // 100, 2047 and 4096 rows (16 heads of 128 bf16 and fp32, 8 of 256, 8 of 64):
 //   row kernel    2.5, 0.36 a row of the longest sequence or 2.9e-7 E a row of
 //                 them all, and the states' bytes, 1.2e-6 E a sequence
-//   chunk kernels 14 (fp32 20) a call, 0.06 (0.07) a tile of 128 rows, a head
-//                 and 128 value columns, and 1.6 a MB of the pass's states as
-//                 those outgrow the L2 (a quarter of that at half of 64 MB)
+//   chunk kernels 14 (fp32 20) a call, 5 + d / 32 (a third more) a further wave
+//                 of tiles (of 128 rows, a head and 128 value columns), and 0.5
+//                 a MB of the pass's states once those outgrow the L2 (a
+//                 quarter of that at half of 64 MB)
 // so few short sequences beside a prompt go with its tiles, and many apart:
-// 16 heads of 128, bf16, 2047 rows beside 2 of 16 rows 29.6 us as tiles and
-// 35.4 by rows, beside 64 of 16 rows 214 and 129.
+// 16 heads of 128, bf16, 2047 rows beside 4 of 16 rows 31 us as tiles and 39 by
+// rows, beside 64 of 4 rows 114 and 67.
 int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
     constexpr int TH = 6;
     const bool f32 = g.dtype == O1_F32;
@@ -281,6 +282,7 @@ int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
         if (r > at[b].longest) at[b].longest = r;
     }
     const double E = (double)slot_floats(g), units = (double)(g.groups * g.heads_per_group) * ((g.dv + 127) / 128);
+    const double wave = (5. + g.d / 32.) * (f32 ? 1.33 : 1.);
     const bool halves = at[TH].seqs * units > LIN_SMS;   // long sequences' segments are of two tiles
     int best = 0;
     double best_us = 0.;
@@ -299,7 +301,7 @@ int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
         if (seqs) us += 2.5 + fmax(0.36 * longest, 2.9e-7 * E * rows) + 1.2e-6 * E * seqs;
         if (tiles) {
             const double mb = (f32 ? 6e-6 : 4e-6) * E * segs, full = fmin(1., mb / 64.);
-            us += (f32 ? 20. : 14.) + (f32 ? 0.07 : 0.06) * units * tiles + 1.6 * mb * full * full;
+            us += (f32 ? 20. : 14.) + (ceil(units * tiles / LIN_SMS) - 1.) * wave + 0.5 * mb * full * full;
         }
         if (t == 0 || us < best_us) best = th[t], best_us = us;
     }
