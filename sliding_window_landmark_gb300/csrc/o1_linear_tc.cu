@@ -723,6 +723,20 @@ struct OutCfg {
     static constexpr uint32_t CORR = SPLIT ? 128u : 0u;
 };
 
+// One P warp's powers of a head's decay l.
+struct alignas(16) Powers {
+    float col[32];                    // l^{31 - i}
+    float pow[32 + LIN_CHUNK + 1];    // l^i from 32 on; zeros before, read by lanes left of the diagonal
+    __device__ __forceinline__ float at(int i) const { return pow[32 + i]; }
+    __device__ __forceinline__ void fill(float g, int lane) {
+        __syncwarp();
+        col[lane] = lin_pow(g, 31 - lane);
+        pow[lane] = 0.f;
+        for (int i = lane; i <= LIN_CHUNK; i += 32) pow[32 + i] = lin_pow(g, i);
+        __syncwarp();
+    }
+};
+
 // One tile: 128 query rows x 128 value columns of a head; its units are the
 // key tiles kt = 0 .. nkt - 1 of the segment up to its own rows (the last).
 struct OutTile {
@@ -774,9 +788,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         fin;
     __shared__ uint32_t tslot;
     __shared__ int abort_s;
-    // of the decay, for each P warp: zeros for the exponents -128 .. -1 (keys
-    // past the diagonal, discarded), then l^0 .. l^128
-    __shared__ float powers[P_WARPS][2 * LIN_CHUNK + 1];
+    __shared__ Powers powers[P_WARPS];
     __shared__ OutTile list[LIST];
     volatile int *abort = &abort_s;
     unsigned char *sm = (unsigned char *)(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
@@ -1006,10 +1018,10 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         Cursor c;
         c.start(list);
         bool have = true, ok = true;
-        const int row = 32 * (warp & 3) + lane, c0 = 64 * (warp >> 2);   // this warp's columns from c0
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int r0 = 32 * (warp & 3), row = r0 + lane, c0 = 64 * (warp >> 2);   // this warp's rows and columns
+        const uint32_t lanes = tmem + ((uint32_t)r0 << 16);
         int table = -1;   // head of the power table
-        float *pw = powers[warp] + LIN_CHUNK;
+        Powers &pw = powers[warp];
         float g = 0.f;
         uint32_t rp[2] = {0, 0};   // phases of acc_ready, one a tile
         // the accumulator times f, once what it holds so far is complete
@@ -1035,14 +1047,9 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
         };
         while (have && ok) {
             if (table != c.x.h) {
-                __syncwarp();
-                g = a.decay[c.x.h];
-                for (int i = lane; i <= LIN_CHUNK; i += 32) {
-                    pw[i] = lin_pow(g, i);
-                    if (i) pw[-i] = 0.f;
-                }
                 table = c.x.h;
-                __syncwarp();
+                g = a.decay[table];
+                pw.fill(g, lane);
             }
             ok = warp_wait(&sc_full[c.u % C::XB], (c.u / C::XB) & 1, abort, wl);
             if (!ok) break;
@@ -1050,14 +1057,15 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             const bool diag = c.diag();
             // weights: l^{row - j} up to the diagonal; for an earlier tile
             // l^{127 - j} for all its keys, the tiles in between, and l^{row + 1}
-            const int lim = diag ? row : LIN_CHUNK - 1;
-            const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt)) * pw[row + 1];
+            const int base = diag ? row : LIN_CHUNK - 1;
+            const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt)) * pw.at(row + 1);
             const uint32_t x = lanes + C::x(c.u);
             // P over the scores of the same keys; a third term of 32 keys
-            // takes 16 columns of the corrections, of keys this warp has read
+            // takes 16 columns of the corrections, of keys this warp has read.
+            // Left of the diagonal a block's weights are a power of the column
+            // (one for all lanes, four a load) times one of the row.
 #pragma unroll 1
             for (int cb = c0; cb < c0 + 64; cb += 32) {
-                const float *w = pw + lim - cb;
                 uint32_t r[32], third[16];
                 float s[32];
                 TMEM_LD32(x + cb, r);
@@ -1070,8 +1078,24 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
 #pragma unroll
                     for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(r[i]);
                 }
+                if (!diag || cb < r0) {
+                    const float f = pw.at(base - cb - 31) * tf;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = cb + i <= lim ? s[i] * (w[-i] * tf) : 0.f;
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 w = *(const float4 *)(pw.col + i);
+                        s[i] *= w.x * f;
+                        s[i + 1] *= w.y * f;
+                        s[i + 2] *= w.z * f;
+                        s[i + 3] *= w.w * f;
+                    }
+                } else if (cb == r0) {
+                    const float *w = pw.pow + 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] = i <= lane ? s[i] * w[-i] : 0.f;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] = 0.f;
+                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -1081,10 +1105,11 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                         r[16 * q + 8 + e] = take_pair(x0, x1);
                         if (C::SPLIT) third[8 * q + e] = take_pair(x0, x1);
                     }
+                __syncwarp();   // the warp is together for the stores
                 TMEM_ST32(x + cb, r);
                 if (C::SPLIT) TMEM_ST16(x + 128 + c0 + (cb - c0) / 2, third);
             }
-            if (c.kt == 0) ok = weight(lin_pow(g, c.x.i0) * pw[row + 1]);
+            if (c.kt == 0) ok = weight(lin_pow(g, c.x.i0) * pw.at(row + 1));
             if (!ok) break;
             tmem_st_wait();
             tc_before();
