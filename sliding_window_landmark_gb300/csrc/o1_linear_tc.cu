@@ -33,11 +33,11 @@
 // Both kernels of MMAs are persistent and split by warp: TMA (or, for weighted
 // keys, staging warps), an MMA issuer, P warps, and warps that store.
 //
-// Bound, measured at 32768 bf16 rows of 8 heads of 256 (358 us, 4 passes): the
-// outputs (47 us a pass) by the L2-to-shared-memory ingest, 46 bytes a clock
+// Bound, measured at 32768 bf16 rows of 8 heads of 256 (338 us, 4 passes): the
+// outputs (45 us a pass) by the L2-to-shared-memory ingest, 46 bytes a clock
 // and SM at best, 31 on average; the increments (28) by the keys' weighting and
 // splitting beside MMAs that read 96 of the 128 bytes a clock shared memory
-// gives; the scan (17) by its bytes, 7.3 TB/s. fp32 (4096 rows: 131 us) reads
+// gives; the scan (14) by its bytes, 9 TB/s in the L2. fp32 (4096 rows: 128 us) reads
 // three terms: its 128 x 128 MMAs alone take the whole shared-memory bandwidth.
 #include <math.h>
 
@@ -612,7 +612,10 @@ __global__ __launch_bounds__((IncCfg<T, N>::THREADS), 1) void k_lin_inc(LinArgs 
 // lane and, J = 2, 128 + 4 lane, so that it is read before it is overwritten),
 // a third in `third` [states][d][dv]. Bound: the scratch's bytes, read and
 // written once, as long as enough loads are out: a warp takes R rows and U
-// segments at a time, and the next U are on their way while these are stored.
+// segments at a time, and the next U are on their way while these are stored
+// (one row and four segments a warp, loaded when the last four were stored: 17
+// us instead of 14 for 32 segments of 2 MB, 189 instead of 40 for 64 sequences
+// of one segment of 1 MB).
 template <int MT, int R, int J>
 __global__ __launch_bounds__(256, 2) void k_lin_scan(LinArgs a, const __grid_constant__ LinWorkTable t, float *inc,
                                                      uint16_t *third) {
