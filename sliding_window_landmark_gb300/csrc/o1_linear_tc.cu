@@ -1120,6 +1120,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             if (lane == 0) mbar_arrive(&p_full[c.u % C::XB]);
             have = c.next(list, count);
         }
+        if (!ok) tmem_st_wait();   // stores issued before a wait ran out are over before the TMEM is given back
     } else {
         // -------------------------------------------------------- epilogue
         // The accumulator is read into registers, as output words, and given

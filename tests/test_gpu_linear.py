@@ -448,3 +448,33 @@ def test_a_scratch_of_one_step_serves_every_type(o1):
         chunk(o1, x, geom, [(0, 210, 0)], out, scratch_rows=1)
         torch.cuda.synchronize()
         check(o1, x, s0, [(0, 210, 0)], out, geom.scale, f"least scratch {dt}")
+
+
+@pytest.mark.parametrize("limit", [1, 2000])
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+def test_expired_waits_spoil_values_with_nan_only(o1, dt, limit):
+    """Waits that run out at once, or some of them: every value is NaN or right,
+    and a NaN that is not raised by the flag does not occur."""
+    G, hpg, d, dv = 4, 2, 72, 136
+    lens = [700, 129, 256, 64, 513]
+    x = make(G, hpg, d, dv, sum(lens), len(lens), dt, 101)
+    seqs = [(sum(lens[:i]), n, i) for i, n in enumerate(lens)]
+    geom, s0 = o1.lin_geom(G, hpg, d, dv, dtype=dt), x["state"].clone()
+    want, Ao, S, As = ref.linear(x["q"], x["k"], x["v"], x["g"], s0, seqs, geom.scale)
+    bo, bs = ref.linear_bounds(want, Ao, As, seqs, dt)
+    for _ in range(3):
+        x["state"].copy_(s0)
+        out = torch.zeros(sum(lens), G * hpg, dv, dtype=dt, device="cuda")
+        o1.o1_set_wait_limit(limit)
+        try:
+            chunk(o1, x, geom, seqs, out)
+            torch.cuda.synchronize()
+        finally:
+            o1.o1_set_wait_limit(0)
+        expired = o1.o1_lin_flags(clear=True) == o1.O1_FLAG_WAIT_EXPIRED
+        assert expired or limit > 1
+        for got, w, b in ((out, want, bo), (x["state"], S, bs)):
+            got = got.cpu().double()
+            bad = torch.isnan(got)
+            assert expired or not bad.any()
+            assert ((got - w).abs() <= b)[~bad].all()
