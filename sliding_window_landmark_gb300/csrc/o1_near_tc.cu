@@ -445,6 +445,15 @@ __global__ __launch_bounds__(TC_THREADS, 1) void k_near_tc(O1Args a, const __gri
         }
         ok = __all_sync(0xffffffffu, ok && mbar_wait(o_done, 0, abort, wl));
         tc_after();
+        // The four warps decide together: the MMA thread commits o_done after an
+        // abort too, so that one warp's wait may have run out where another's is
+        // met, and a warp that skipped the barrier below would leave the others
+        // at it.
+        int all = ok;
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.ne.s32 p, %0, 0;\nbar.red.and.pred p, 1, 128, p;\nselp.s32 %0, 1, 0, p;\n}\n"
+            : "+r"(all)::"memory");
+        ok = all != 0;
         if (ok) {
             // the window part of each row: its header (reference, mass, true
             // max, natural units) and its numerator O, which goes to `out`

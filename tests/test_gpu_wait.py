@@ -78,3 +78,24 @@ def test_token_wait_runs_out_and_output_stays_valid():
           "one-row steps under the tiny limit: every copy landed before the first look")
     harness.assert_outputs(got, want, diag, "one-row steps under a tiny wait limit")
     harness.assert_state(gpu.read(), orc, "after the steps")
+
+
+@pytest.mark.parametrize("limit", [1, 60, 300, 1000, 2500])
+def test_window_kernel_ends_whichever_waits_run_out(limit):
+    """Limits at which some warps' waits run out and others' are met: every call
+    ends, and says so by the flag; one without the flag is right."""
+    from sliding_window_landmark_gb300 import o1
+    sh = synth.Shape(groups=2, heads_per_group=4, d=64, dv=128, sinks=4, window=512, landmarks=4)
+    c = synth.layer_constants(sh, 43)
+    q, k, v, g = synth.layer_rows(sh, 43, 0, 700)
+    orc = harness.oracle_layer(sh, c)
+    want, diag = orc.rows(q, k, v, g, diag=True)
+    for _ in range(4):
+        gpu = harness.GpuLayer(sh, c, max_rows=700)
+        try:
+            o1.o1_set_wait_limit(limit)
+            got = gpu.rows(q, k, v, g)
+        finally:
+            o1.o1_set_wait_limit(0)
+        if not o1.o1_state_flags(gpu.state, gpu.g) & o1.O1_FLAG_WAIT_EXPIRED:
+            harness.assert_outputs(got, want, diag, f"limit {limit}")
