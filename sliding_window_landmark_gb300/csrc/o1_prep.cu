@@ -178,7 +178,7 @@ __global__ __launch_bounds__(32 * PREP_WARPS, 4) void k_prep(PrepArgs a) {
 #pragma unroll
                         for (int m = 1; m < LPV; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
                         ss = fmaf(ss, inv_d, a.eps);
-                        f = ss > 0.f ? rsqrtf(ss) : 0.f;
+                        f = ss == 0.f ? 0.f : rsqrtf(ss);   // a NaN stays one
                     }
                     const F2 ff = f2(f, f);
                     float yl[4], yh[4];

@@ -172,3 +172,24 @@ def test_prepared_rows_feed_a_sealed_layer(o1):
     want, diag = orc.rows(nq.astype("f4"), nk.astype("f4"), v, gate, diag=True)
     got = harness.GpuLayer(flat, c, max_rows=130).rows(qo.cpu().numpy(), ko.cpu().numpy(), v, gate)
     harness.assert_outputs(got, want, diag, "prepared rows")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+@pytest.mark.parametrize("norm", ["rms", "unit"])
+@pytest.mark.parametrize("d,rot", [(72, 24), (256, 256), (16, 0)])
+def test_a_nan_spoils_its_whole_head(o1, dt, norm, d, rot):
+    """A norm with a NaN in it is NaN: every value of that head, and no other head's."""
+    gen = torch.Generator().manual_seed(13)
+    q, k = (torch.randn(6, h, d, generator=gen).to(dt) for h in (3, 2))
+    q[1, 2, 5] = k[3, 0, d - 1] = float("nan")
+    q[5, 0] = float("nan")
+    inv, pos = freqs(rot), torch.arange(100, 106)
+    qo, ko = torch.zeros(6, 3, d, dtype=dt, device="cuda"), torch.zeros(6, 2, d, dtype=dt, device="cuda")
+    g = o1.prep_geom(3, 2, d, rot=rot, norm=norm, in_dtype=dt)
+    o1.check(o1.o1_head_prep(g, q.cuda(), k.cuda(), None, None, inv.cuda() if rot else None, qo, ko, pos0=100))
+    torch.cuda.synchronize()
+    for x, got in ((q, qo.cpu()), (k, ko.cpu())):
+        bad = torch.isnan(x).any(-1)
+        assert torch.isnan(got[bad]).all()
+        z, mag = ref.prep(x, None, inv, pos, rot, norm, g.eps)
+        ref.assert_within(got[~bad], z[~bad], ref.prep_bound(z, mag, d, dt)[~bad], "other heads")
