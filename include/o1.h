@@ -398,7 +398,8 @@ typedef struct o1_prep_geom {
  *                  (same address, stride and type)
  * Sums and the rotation are fp32; the angle is reduced exactly in fixed point
  * (a turn is 2^64), so far positions keep fp32 accuracy. The sum of squares
- * of a head must be finite in fp32. The result feeds o1_chunk_attend and its
+ * of a head must be finite in fp32; it may be as small as it likes, and a NaN
+ * in a head makes the head NaN under a norm. The result feeds o1_chunk_attend and its
  * kin with rope_base = 0, or the linear layer. rows = 0 does nothing.
  * Asynchronous; one launch. */
 O1_API int o1_head_prep(const o1_prep_geom *geom, const void *q, int64_t q_stride, const void *k, int64_t k_stride,

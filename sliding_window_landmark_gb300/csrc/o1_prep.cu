@@ -92,8 +92,27 @@ struct Raw4<float> {
     using type = float4;
 };
 
-// LPV lanes of 8 values a head (a power of two, 8 LPV >= d)
-template <typename Tin, typename Tout, int LPV>
+// Sum of a head's squares over its LPV lanes.
+template <int LPV>
+__device__ __forceinline__ float head_squares(const F2 (&xl)[2], const F2 (&xh)[2], bool on) {
+    const F2 s2 = f2_fma(xh[1], xh[1], f2_fma(xh[0], xh[0], f2_fma(xl[1], xl[1], f2_mul(xl[0], xl[0]))));
+    float ss, s_odd;
+    f2_get(s2, ss, s_odd);
+    ss = on ? ss + s_odd : 0.f;
+#pragma unroll
+    for (int m = 1; m < LPV; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    return ss;
+}
+// A mean or sum of squares from here on has lost at most d 2^-150, 2^-52 of it,
+// to squares below fp32's range; with an epsilon that large none can fall
+// below. Below it (values under 2^-41) a head is squared times 2^100: the
+// smallest fp32 value becomes 2^-49, and the sum of 256 stays under 2^118.
+constexpr float TINY = 0x1p-90f;
+
+// LPV lanes of 8 values a head (a power of two, 8 LPV >= d); SMALL: the epsilon
+// is below TINY (a kernel of its own: the batch above 65.4 us, 65.9 with the
+// question in every head)
+template <typename Tin, typename Tout, int LPV, bool SMALL>
 __global__ __launch_bounds__(32 * PREP_WARPS, 4) void k_prep(PrepArgs a) {
     using R = typename Raw4<Tin>::type;
     constexpr int SIDE = 32 / LPV, U = 2;   // heads side by side, and rounds of them in flight
@@ -168,16 +187,21 @@ __global__ __launch_bounds__(32 * PREP_WARPS, 4) void k_prep(PrepArgs a) {
                 for (int k = 0; k < U; ++k) {
                     const int hh = h + SIDE * k + side;
                     const float4 l = o1_ld4((const Tin *)&vl[k]), g = o1_ld4((const Tin *)&vh[k]);
-                    const F2 xl[2] = {f2(l.x, l.y), f2(l.z, l.w)}, xh[2] = {f2(g.x, g.y), f2(g.z, g.w)};
+                    F2 xl[2] = {f2(l.x, l.y), f2(l.z, l.w)}, xh[2] = {f2(g.x, g.y), f2(g.z, g.w)};
                     float f = 1.f;
                     if (a.norm != O1_NORM_NONE) {
-                        const F2 s2 = f2_fma(xh[1], xh[1], f2_fma(xh[0], xh[0], f2_fma(xl[1], xl[1], f2_mul(xl[0], xl[0]))));
-                        float ss, s_odd;
-                        f2_get(s2, ss, s_odd);
-                        ss = on ? ss + s_odd : 0.f;
+                        float ss = fmaf(head_squares<LPV>(xl, xh, on), inv_d, a.eps);
+                        if (SMALL && __any_sync(0xffffffffu, ss < TINY)) {
+                            // squares that leave fp32's range at the bottom: such heads times 2^100
+                            const float up = ss < TINY ? 0x1p100f : 1.f;
+                            const F2 u2 = f2(up, up);
 #pragma unroll
-                        for (int m = 1; m < LPV; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                        ss = fmaf(ss, inv_d, a.eps);
+                            for (int i = 0; i < 2; ++i) {
+                                xl[i] = f2_mul(u2, xl[i]);
+                                xh[i] = f2_mul(u2, xh[i]);
+                            }
+                            ss = fmaf(head_squares<LPV>(xl, xh, on), inv_d, a.eps * up * up);
+                        }
                         f = ss == 0.f ? 0.f : rsqrtf(ss);   // a NaN stays one
                     }
                     const F2 ff = f2(f, f);
@@ -219,7 +243,8 @@ void prep_launch_l(PrepArgs a, cudaStream_t st) {
     // 1.7 waves 68, a block for every 8 rows 69, 1.25 waves 80).
     const int64_t blocks = ((int64_t)a.rows * a.parts + PREP_WARPS - 1) / PREP_WARPS, most_blocks = 4 * SMS;
     const int64_t grid = blocks < most_blocks ? blocks : most_blocks;
-    k_prep<Tin, Tout, LPV><<<(unsigned)grid, 32 * PREP_WARPS, 0, st>>>(a);
+    if (a.eps < TINY && a.norm != O1_NORM_NONE) k_prep<Tin, Tout, LPV, true><<<(unsigned)grid, 32 * PREP_WARPS, 0, st>>>(a);
+    else k_prep<Tin, Tout, LPV, false><<<(unsigned)grid, 32 * PREP_WARPS, 0, st>>>(a);
 }
 template <typename Tin, typename Tout>
 void prep_launch(const PrepArgs &a, cudaStream_t st) {

@@ -193,3 +193,22 @@ def test_a_nan_spoils_its_whole_head(o1, dt, norm, d, rot):
         assert torch.isnan(got[bad]).all()
         z, mag = ref.prep(x, None, inv, pos, rot, norm, g.eps)
         ref.assert_within(got[~bad], z[~bad], ref.prep_bound(z, mag, d, dt)[~bad], "other heads")
+
+
+# 2^-149 is the smallest fp32 value: heads of one or two steps of it too
+@pytest.mark.parametrize("size", [1e-13, 1e-19, 1e-22, 1e-30, 1e-38, 2.0 ** -148])
+@pytest.mark.parametrize("eps", [0.0, 1e-37, 1e-44])
+@pytest.mark.parametrize("norm,d,rot", [("unit", 64, 64), ("rms", 256, 128), ("rms", 200, 56), ("unit", 8, 0)])
+def test_tiny_heads_with_little_or_no_epsilon(o1, size, eps, norm, d, rot):
+    """Heads whose squares leave fp32's range, beside heads of common size and zero heads."""
+    gen = torch.Generator().manual_seed(17)
+    q = torch.randn(5, 7, d, generator=gen)
+    q[1:] *= size
+    q[2, 3], q[3] = 0.0, q[0] * 1e3
+    inv = freqs(rot)
+    g = o1.prep_geom(7, 0, d, rot=rot, norm=norm, eps=eps)
+    out = torch.full((5, 7, d), float("nan"), device="cuda")
+    o1.check(o1.o1_head_prep(g, q.cuda(), None, None, None, inv.cuda() if rot else None, out, None, pos0=3))
+    torch.cuda.synchronize()
+    z, mag = ref.prep(q, None, inv, torch.arange(3, 8), rot, norm, g.eps)
+    ref.assert_within(out, z, ref.prep_bound(z, mag, d, F32), f"{norm} of {size} with {eps}")
