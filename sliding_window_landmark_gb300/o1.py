@@ -10,6 +10,7 @@ to, and importing this module fails if the library is not built.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -384,10 +385,18 @@ def lin_geom(groups: int, heads_per_group: int, d: int, dv: int, dtype=torch.flo
 
 def lin_seqs(seqs):
     """(row0, rows, slot) triples as the array o1_lin_chunk_attend takes."""
-    return (o1_lin_seq * len(seqs))(*[tuple(int(x) for x in s) for s in seqs])
+    flat = array.array("i", [int(x) for row0, rows, slot in seqs for x in (row0, rows, slot)])   # OverflowError past 32 bits
+    return (o1_lin_seq * len(seqs)).from_buffer(flat) if flat else (o1_lin_seq * 0)()
 
 
 _TYPES = {n: t for t, n in DTYPES.items()}
+
+
+def _count(n, name: str) -> int:
+    """A count as the 32 bits that the C call takes (ctypes would drop the rest)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: {n} does not fit 32 bits")
+    return int(n)
 
 
 def _rows(t, heads: int, width: int, dtype, rows: int, name: str, dev: int):
@@ -433,7 +442,7 @@ def o1_head_prep(g: o1_prep_geom, q, k, q_weight, k_weight, inv_freq, q_out, k_o
     """Per-head norm and rotation of q [rows, q_heads, d] and k [rows, k_heads,
     d] into q_out and k_out (which may be q and k themselves)."""
     dev, hq, hk, d = torch.cuda.current_device(), g.q_heads, g.k_heads, g.d
-    rows, tin, tout = (q if hq else k).shape[0], _TYPES[g.in_dtype], _TYPES[g.out_dtype]
+    rows, tin, tout = _count((q if hq else k).shape[0], "rows"), _TYPES[g.in_dtype], _TYPES[g.out_dtype]
     qp, qs = _rows(q, hq, d, tin, rows, "q", dev)
     kp, ks = _rows(k, hk, d, tin, rows, "k", dev)
     qo, qos = _rows(q_out, hq, d, tout, rows, "q_out", dev)
@@ -446,11 +455,11 @@ def o1_head_prep(g: o1_prep_geom, q, k, q_weight, k_weight, inv_freq, q_out, k_o
 
 
 def o1_lin_state_bytes(g: o1_lin_geom, slots: int) -> int:
-    return int(LIB.o1_lin_state_bytes(ctypes.byref(g), int(slots)))
+    return int(LIB.o1_lin_state_bytes(ctypes.byref(g), _count(slots, "slots")))
 
 
 def o1_lin_scratch_bytes(g: o1_lin_geom, rows: int, seqs: int = 1) -> int:
-    return int(LIB.o1_lin_scratch_bytes(ctypes.byref(g), int(rows), int(seqs)))
+    return int(LIB.o1_lin_scratch_bytes(ctypes.byref(g), _count(rows, "rows"), _count(seqs, "seqs")))
 
 
 def _lin_tensors(state, g: o1_lin_geom, q, k, v, out, log_decay, dev: int):
@@ -461,8 +470,8 @@ def _lin_tensors(state, g: o1_lin_geom, q, k, v, out, log_decay, dev: int):
     shape = state.shape
     if shape[1:] != (nh, d, dv):
         raise ValueError(f"state: need a [slots, {nh}, {d}, {dv}] tensor")
-    rows = q.shape[0]
-    return ((_flat(state, 1, torch.float32, "state", dev), shape[0]),
+    rows = _count(q.shape[0], "rows")
+    return ((_flat(state, 1, torch.float32, "state", dev), _count(shape[0], "slots")),
             (*_rows(q, nh, d, dt, rows, "q", dev), *_rows(k, G, d, dt, rows, "k", dev), *_rows(v, G, dv, dt, rows, "v", dev),
              _flat(log_decay, nh, torch.float32, "log_decay", dev)),
             _rows(out, nh, dv, dt, rows, "out", dev), rows)

@@ -478,3 +478,14 @@ def test_expired_waits_spoil_values_with_nan_only(o1, dt, limit):
             bad = torch.isnan(got)
             assert expired or not bad.any()
             assert ((got - w).abs() <= b)[~bad].all()
+
+
+def test_more_rows_than_a_call_counts(o1):
+    """A row count past 32 bits is refused, not taken modulo 2^32."""
+    geom = o1.lin_geom(1, 1, 8, 8)
+    t = torch.zeros(1, 1, 8, device="cuda").expand(2 ** 32 + 1, 1, 8)
+    state, g = torch.zeros(1, 1, 8, 8, device="cuda"), torch.zeros(1, device="cuda")
+    with pytest.raises(ValueError):
+        o1.o1_lin_token_attend(state, geom, t, t, t, g, None, t)
+    with pytest.raises(ValueError):
+        o1.o1_lin_chunk_attend(state, geom, torch.empty(4096, dtype=torch.uint8, device="cuda"), t, t, t, g, [(0, 1, 0)], t)

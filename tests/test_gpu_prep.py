@@ -212,3 +212,11 @@ def test_tiny_heads_with_little_or_no_epsilon(o1, size, eps, norm, d, rot):
     torch.cuda.synchronize()
     z, mag = ref.prep(q, None, inv, torch.arange(3, 8), rot, norm, g.eps)
     ref.assert_within(out, z, ref.prep_bound(z, mag, d, F32), f"{norm} of {size} with {eps}")
+
+
+def test_more_rows_than_a_call_counts(o1):
+    """A row count past 32 bits is refused, not taken modulo 2^32."""
+    g = o1.prep_geom(1, 0, 8, rot=0)
+    q = torch.zeros(1, 1, 8, device="cuda").expand(2 ** 32 + 5, 1, 8)
+    with pytest.raises(ValueError):
+        o1.o1_head_prep(g, q, None, None, None, None, q, None)

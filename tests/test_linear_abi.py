@@ -147,3 +147,19 @@ def test_reference_state_is_the_closed_form():
         torch.testing.assert_close(S[1, h], want, rtol=1e-6, atol=1e-6)
     assert (out[:2] == 0).all() and (out[8:] == 0).all() and torch.equal(S[0], S0[0].double())
     assert (Ao >= out.abs()).all() and (As >= S.abs() - 1e-12).all()
+
+
+def test_binding_counts_past_32_bits(o1):
+    """Refused, where ctypes would take them modulo 2^32."""
+    g = o1.lin_geom(2, 2, 64, 64)
+    for bad in ((2 ** 32, 4, 0), (0, 2 ** 32 + 4, 0), (0, 4, 2 ** 32), (0, 4, -2 ** 31 - 1)):
+        with pytest.raises(OverflowError):
+            o1.lin_seqs([(0, 4, 1), bad])
+    with pytest.raises(ValueError):
+        o1.lin_seqs([(0, 4)])
+    for call in (lambda n: o1.o1_lin_state_bytes(g, n), lambda n: o1.o1_lin_scratch_bytes(g, n),
+                 lambda n: o1.o1_lin_scratch_bytes(g, 5, n)):
+        with pytest.raises(ValueError):
+            call(2 ** 32 + 1)
+    s = o1.lin_seqs([(7, 2 ** 31 - 1, 3), (torch.tensor(5), 4.0, -1)])
+    assert [(x.row0, x.rows, x.slot) for x in s] == [(7, 2 ** 31 - 1, 3), (5, 4, -1)] and len(o1.lin_seqs([])) == 0
