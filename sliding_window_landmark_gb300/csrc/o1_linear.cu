@@ -1,8 +1,8 @@
 // Linear attention with a decay per head: the row kernel (token batches,
 // short sequences) and the C ABI of the linear layer. Per head h and row t
 //   S = e^{g_h} S + k_t v_t^T,   out_t = scale q_t S.
-#include <limits.h>
 #include <math.h>
+#include <stdint.h>
 
 #include <algorithm>
 
@@ -229,6 +229,9 @@ size_t slot_floats(const o1_lin_geom &g) {
     return (size_t)g.groups * g.heads_per_group * g.d * g.dv;
 }
 
+// Whether the states of that many slots have a size in bytes (64 bits).
+bool slots_ok(const o1_lin_geom &g, int32_t slots) { return (size_t)slots <= SIZE_MAX / 4 / slot_floats(g); }
+
 // Limits of a pass: its states are written, read, rewritten and read again and
 // are kept to what stays in the L2 (a 32768-row prompt of 2 MB a state: 412 us
 // in passes of 64 MB, 469 of 96, 472 of 128); its scratch as a whole, and its
@@ -333,7 +336,8 @@ bool seqs_ok(const o1_lin_seq *s, int n, int n_slots, int total_rows) {
 int lin_args(LinArgs &a, float *state, int32_t n_slots, const o1_lin_geom &g, const void *q, int64_t q_stride,
              const void *k, int64_t k_stride, const void *v, int64_t v_stride, const float *log_decay, void *out,
              int64_t out_stride, int32_t rows, const O1Span &extra) {
-    if (!state || (uintptr_t)state % 16 || n_slots < 1 || !log_decay || (uintptr_t)log_decay % 4) return O1_ERR_ARG;
+    if (!state || (uintptr_t)state % 16 || n_slots < 1 || !slots_ok(g, n_slots) || !log_decay || (uintptr_t)log_decay % 4)
+        return O1_ERR_ARG;
     const int nh = g.groups * g.heads_per_group;
     const O1Span sp[6] = {o1_row_span(out, g.dtype, nh, g.dv, out_stride, rows),
                           o1_span(state, slot_floats(g) * n_slots * 4),
@@ -365,14 +369,17 @@ int lin_args(LinArgs &a, float *state, int32_t n_slots, const o1_lin_geom &g, co
 extern "C" {
 
 size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots) {
-    if (!lin_geom_ok(geom) || slots < 1) return 0;
+    if (!lin_geom_ok(geom) || slots < 1 || !slots_ok(*geom, slots)) return 0;
     return slot_floats(*geom) * slots * 4;
 }
 
 size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs) {
     if (!lin_geom_ok(geom) || rows < 1 || seqs < 1) return 0;
-    // segments of LIN_CHUNK rows are the most states any split into segments takes
-    const size_t all = lin_pass_bytes(*geom, (int64_t)rows / LIN_CHUNK + seqs, (int64_t)rows + 16 * (int64_t)seqs);
+    // segments of LIN_CHUNK rows are the most states any split into segments
+    // takes; a count past the limit of a pass is cut there, before it is
+    // multiplied by a state (of at most 2^34 bytes)
+    const int64_t segs = std::min((int64_t)rows / LIN_CHUNK + seqs, (int64_t)1 << 24);
+    const size_t all = lin_pass_bytes(*geom, segs, (int64_t)rows + 16 * (int64_t)seqs);
     const size_t one = lin_pass_bytes(*geom, 1, LIN_CHUNK);
     size_t lim = lin_terms(geom->dtype) == 1 ? LIN_PASS_STATES : LIN_PASS_BYTES;
     lim = one > lim ? one : lim;

@@ -163,3 +163,19 @@ def test_binding_counts_past_32_bits(o1):
             call(2 ** 32 + 1)
     s = o1.lin_seqs([(7, 2 ** 31 - 1, 3), (torch.tensor(5), 4.0, -1)])
     assert [(x.row0, x.rows, x.slot) for x in s] == [(7, 2 ** 31 - 1, 3), (5, 4, -1)] and len(o1.lin_seqs([])) == 0
+
+
+def test_sizes_past_64_bits(o1):
+    """The largest states: their bytes, or 0 where 64 bits do not hold them; a
+    scratch for any counts is no smaller than one for fewer."""
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        big = o1.lin_geom(4095, 16, 256, 256, dtype=dt)
+        one = 4095 * 16 * 256 * 256 * 4
+        most = (2 ** 64 - 1) // one
+        assert o1.o1_lin_state_bytes(big, most) == most * one
+        for n in (most + 1, 2 ** 30 + 2 ** 20, 2 ** 31 - 1):
+            assert n > most and o1.o1_lin_state_bytes(big, n) == 0
+        for g in (big, o1.lin_geom(2, 2, 64, 64, dtype=dt), o1.lin_geom(1, 1, 8, 8, dtype=dt)):
+            sizes = [o1.o1_lin_scratch_bytes(g, r, n) for r, n in
+                     ((1, 1), (4096, 1), (2 ** 20, 4096), (2 ** 31 - 1, 2 ** 24), (2 ** 31 - 1, 2 ** 30), (2 ** 31 - 1, 2 ** 31 - 1))]
+            assert 0 < sizes[0] and sizes == sorted(sizes), sizes
