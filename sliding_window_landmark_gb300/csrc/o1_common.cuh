@@ -557,21 +557,23 @@ static inline void o1_attrs_done(unsigned long long *mask, unsigned long long bi
     __atomic_fetch_or(mask, bit, __ATOMIC_RELEASE);
 }
 
-// Chained launches (programmatic dependent launch), used in short passes
-// (at most O1_SHORT_ROWS rows: the key-slice window kernels, the short
-// commit pass; O1Args::chain_early). A kernel launched by o1_launch_chained
+// Chained launches (programmatic dependent launch), used in short passes of
+// sealed layers (at most O1_SHORT_ROWS rows: the key-slice window kernels, the
+// short commit pass; O1Args::chain_early) and in linear layers' passes. A kernel launched by o1_launch_chained
 // with `chained` set may be scheduled while the previous kernel of its
 // stream is still running, so every kernel that can be launched that way
 // calls o1_chain_wait() before it touches global memory; the wait returns
 // once that kernel has completed and its writes are visible (and at once
 // after a plain launch). Since every chained kernel waits, a chain completes
 // in order. The first kernel of a pass on a stream, and every kernel behind
-// an event wait, is launched plainly. o1_chain_release() lets the next
-// chained kernel be scheduled before this one ends; the kernels that can
-// end a pass never call it, because a one-row step launched after them reads
-// the state ahead of its own wait. Longer passes launch plainly: chaining
-// them measured slower (a 24-layer stack of 64-row chunks 40.7 -> 48.9 ms,
-// a 4096-row prompt with early release 0.370 -> 0.396 ms).
+// an event wait, is launched plainly (linear layers: the first kernel of a
+// call; later passes follow the call's own kernels). o1_chain_release() lets
+// the next chained kernel be scheduled before this one ends; the kernels that
+// can end a pass never call it, because a one-row step launched after them
+// reads the state ahead of its own wait. Longer passes of sealed layers launch
+// plainly: chaining them measured slower (a 24-layer stack of 64-row chunks
+// 40.7 -> 48.9 ms, a 4096-row prompt with early release 0.370 -> 0.396 ms);
+// passes of linear layers are chained whatever their length (o1_linear_tc.cu).
 __device__ __forceinline__ void o1_chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void o1_chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

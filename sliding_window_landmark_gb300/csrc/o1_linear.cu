@@ -411,14 +411,15 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     LinTable rows;
     LinWorkTable work;
     int n = 0, segs = 0, tiles = 0, prows = 0;
-    bool launched = true;
+    bool launched = true, first = true;
     work.n = 0;
     auto flush_rows = [&]() {
-        if (n) rows_launch(a, g.dtype, &rows, n, st);
+        if (n) rows_launch(a, g.dtype, &rows, n, st), first = false;
         n = 0;
     };
     auto flush_chunks = [&]() {
-        if (work.n && !lin_launch_pass(a, g.dtype, work, segs, tiles, prows, scratch, st)) launched = false;
+        if (work.n && !lin_launch_pass(a, g.dtype, work, segs, tiles, prows, scratch, first, st)) launched = false;
+        first = first && !work.n;
         work.n = segs = tiles = prows = 0;
     };
     auto up = [](int64_t x, int m) { return (int)((x + m - 1) / m); };

@@ -76,8 +76,9 @@ static inline size_t lin_pass_bytes(const o1_lin_geom &g, int64_t segs, int64_t 
 // One pass of the chunk kernels (o1_linear_tc.cu) over the pieces of a table:
 // `segs` segments, `tiles` tiles and `prows` panel rows in all, in a scratch of
 // lin_pass_bytes. Launches only; false where a tensor map cannot be made.
+// first: no kernel of this call stands before it in the stream.
 bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, int prows, void *scratch,
-                     cudaStream_t st);
+                     bool first, cudaStream_t st);
 // Flags its kernels raised on the current device (O1_FLAG_WAIT_EXPIRED), and
 // their reset.
 int lin_flags(uint32_t *flags, int clear, cudaStream_t st);

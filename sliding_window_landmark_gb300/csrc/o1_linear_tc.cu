@@ -1210,7 +1210,7 @@ int grid_of(int units) {
 }
 
 template <typename T, int N>
-bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int tiles, int prows, void *scratch,
+bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int tiles, int prows, void *scratch, bool first,
             cudaStream_t st) {
     using CI = IncCfg<T, N>;
     using CO = OutCfg<T>;
@@ -1252,11 +1252,16 @@ bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int ti
     const int dt = (a.d + TN - 1) / TN, units = segs * a.nh * dt * ((a.dv + N - 1) / N);
     const int ot = tiles * a.nh * ((a.dv + TN - 1) / TN);
     // Chained launches: a kernel's set-up runs under the end of the one before
-    // (1024 fp32 rows 45.5 -> 43 us). Not the scan: its blocks, small and many,
-    // would pile up on the SMs that finish first (1024 bf16 rows of 256 columns
-    // 24.6 -> 27 us).
-    if (CO::NT > 1) o1_launch_chained(true, k_lin_split<T>, dim3(prows), dim3(256), 0, st, a, t, sp);
-    o1_launch_chained(true, k_lin_inc<T, N>, dim3(grid_of(units)), dim3(CI::THREADS), CI::SMEM, st, a, t, mvi, units, inc);
+    // (1024 fp32 rows 45.5 -> 43 us). Not the first of a call (64 fp32 rows in a
+    // loop 23.3 -> 27.2 us, in a graph 21.3 -> 21.6), since what ran before it is
+    // unknown: a chained kernel waits for the one kernel before it, which may
+    // itself have been chained and not have waited; and one that lets its
+    // successor start and takes tensor memory only then would wait for ever on
+    // an SM whose tensor memory k_lin_inc already holds. Not the scan: its
+    // blocks, small and many, would pile up on the SMs that finish first (1024
+    // bf16 rows of 256 columns 24.6 -> 27 us).
+    if constexpr (CO::NT > 1) o1_launch_chained(!first, k_lin_split<T>, dim3(prows), dim3(256), 0, st, a, t, sp);
+    o1_launch_chained(CO::NT > 1 || !first, k_lin_inc<T, N>, dim3(grid_of(units)), dim3(CI::THREADS), CI::SMEM, st, a, t, mvi, units, inc);
     if (a.dv > 128) scan_launch<CO::MT, 2>(a, t, segs, inc, third, st);
     else scan_launch<CO::MT, 1>(a, t, segs, inc, third, st);
     o1_launch_chained(true, k_lin_out<T>, dim3(grid_of(ot)), dim3(OUT_THREADS), CO::SMEM, st, a, t, mq, mk, mv, ms, ms3, ot);
@@ -1266,11 +1271,11 @@ bool pass_t(const LinArgs &a, const LinWorkTable &t, int dtype, int segs, int ti
 }  // namespace
 
 bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int segs, int tiles, int prows, void *scratch,
-                     cudaStream_t st) {
-    if (dtype == O1_F32) return pass_t<float, 128>(a, t, dtype, segs, tiles, prows, scratch, st);
-    if (dtype == O1_F16) return pass_t<__half, 128>(a, t, dtype, segs, tiles, prows, scratch, st);
-    return a.dv > 128 ? pass_t<__nv_bfloat16, 256>(a, t, dtype, segs, tiles, prows, scratch, st)
-                      : pass_t<__nv_bfloat16, 128>(a, t, dtype, segs, tiles, prows, scratch, st);
+                     bool first, cudaStream_t st) {
+    if (dtype == O1_F32) return pass_t<float, 128>(a, t, dtype, segs, tiles, prows, scratch, first, st);
+    if (dtype == O1_F16) return pass_t<__half, 128>(a, t, dtype, segs, tiles, prows, scratch, first, st);
+    return a.dv > 128 ? pass_t<__nv_bfloat16, 256>(a, t, dtype, segs, tiles, prows, scratch, first, st)
+                      : pass_t<__nv_bfloat16, 128>(a, t, dtype, segs, tiles, prows, scratch, first, st);
 }
 
 int lin_flags(uint32_t *flags, int clear, cudaStream_t st) {

@@ -489,3 +489,49 @@ def test_more_rows_than_a_call_counts(o1):
         o1.o1_lin_token_attend(state, geom, t, t, t, g, None, t)
     with pytest.raises(ValueError):
         o1.o1_lin_chunk_attend(state, geom, torch.empty(4096, dtype=torch.uint8, device="cuda"), t, t, t, g, [(0, 1, 0)], t)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+@pytest.mark.parametrize("before", ["kernel", "copy", "join", "prep"])
+def test_captured_behind_other_work(o1, dt, before):
+    """A captured prompt whose queries come from a foreign kernel, a copy, another
+    stream, or the head prep just before it: every replay takes the new ones."""
+    G, hpg, d, dv, rows = 2, 2, 64, 64, 420
+    x = make(G, hpg, d, dv, rows, 2, dt, 83)
+    geom, s0 = o1.lin_geom(G, hpg, d, dv, dtype=dt), x["state"].clone()
+    seqs = o1.lin_seqs([(0, 300, 1), (300, 120, 0)])
+    out = torch.full((rows, G * hpg, dv), float("nan"), dtype=dt, device="cuda")
+    scratch = torch.empty(o1.o1_lin_scratch_bytes(geom, rows, 2), dtype=torch.uint8, device="cuda")
+    src, side = torch.empty_like(x["q"]), torch.cuda.Stream()
+    copy_of = lambda: x["q"].copy_(src)
+    gp = o1.prep_geom(G * hpg, 0, d, rot=0, norm="none", in_dtype=dt)
+
+    def run():
+        here = torch.cuda.current_stream()
+        if before == "kernel":
+            torch.mul(src, 1.0, out=x["q"])
+        elif before == "copy":
+            copy_of()
+        elif before == "prep":
+            o1.check(o1.o1_head_prep(gp, src, None, None, None, None, x["q"], None))
+        else:
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                copy_of()
+            torch.add(x["v"], 0.0, out=x["v"])
+            here.wait_stream(side)
+        o1.check(o1.o1_lin_chunk_attend(x["state"], geom, scratch, x["q"], x["k"], x["v"], x["g"], seqs, out))
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (1, 2):
+        src.copy_(torch.randn(src.shape, generator=torch.Generator().manual_seed(seed)).to(dt))
+        x["q"].fill_(float("nan"))
+        out.fill_(float("nan"))
+        x["state"].copy_(s0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(o1, {**x, "q": src}, s0, [(0, 300, 1), (300, 120, 0)], out, geom.scale, f"behind a {before}")
