@@ -262,35 +262,47 @@ int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : 2 * LIN_CHUN
 // 100, 2047 and 4096 rows (16 heads of 128 bf16 and fp32, 8 of 256, 8 of 64):
 //   row kernel    2.5, 0.36 a row of the longest sequence or 2.9e-7 E a row of
 //                 them all, and the states' bytes, 1.2e-6 E a sequence
-//   chunk kernels 14 (fp32 20) a call, 5 + d / 32 (a third more) a further wave
-//                 of tiles (of 128 rows, a head and 128 value columns), and 0.5
-//                 a MB of the pass's states once those outgrow the L2 (a
-//                 quarter of that at half of 64 MB)
+//   chunk kernels 14 (fp16 17, fp32 20) a pass, 5 + d / 32 (fp32 a third more)
+//                 a further wave of tiles (of 128 rows, a head and 128 value
+//                 columns), and 0.5 a MB of the pass's states once those
+//                 outgrow the L2 (a quarter of that at half of 64 MB)
 // so few short sequences beside a prompt go with its tiles, and many apart:
 // 16 heads of 128, bf16, 2047 rows beside 4 of 16 rows 31 us as tiles and 39 by
-// rows, beside 64 of 4 rows 114 and 67.
-int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
+// rows, beside 64 of 4 rows 114 and 67. fp16's waves are charged as bf16's: a
+// third more sent 4 of 16 rows beside 2047 by rows, 49 us, where tiles take 41.
+// Passes are what the limits and the scratch let into one, in parts (whole ones
+// moved sequences apart that fill a prompt's last pass: 8 of 4 rows beside
+// 32768 237 us, 228 with the tiles): with a scratch of one state every short
+// sequence among the tiles is a pass, 32 bf16 ones of 24 rows 96 launches.
+int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n, size_t scratch_bytes) {
     constexpr int TH = 6;
     const bool f32 = g.dtype == O1_F32;
     const int th[TH] = {0, 1, 4, 8, 16, lin_terms(g.dtype) == 1 ? 32 : 48};
     struct {
         int64_t seqs, rows, longest;
     } at[TH + 1] = {};   // of th[i - 1] + 1 .. th[i] rows; at[TH]: longer, in tiles
+    int n_long = 0;
     for (int i = 0; i < n; ++i) {
         const int r = s[i].rows;
         int b = 0;
         while (b < TH && r > th[b]) ++b;
         at[b].seqs += b < TH ? 1 : (r - 1) / LIN_CHUNK + 1;
         at[b].rows += r;
+        n_long += b == TH;
         if (r > at[b].longest) at[b].longest = r;
     }
     const double E = (double)slot_floats(g), units = (double)(g.groups * g.heads_per_group) * ((g.dv + 127) / 128);
+    const double fixed = f32 ? 20. : g.dtype == O1_F16 ? 17. : 14.;
     const double wave = (5. + g.d / 32.) * (f32 ? 1.33 : 1.);
+    const double most = fmin((double)scratch_bytes, (double)LIN_PASS_BYTES);
+    const double per_row = (double)lin_terms(g.dtype) * (lin_terms(g.dtype) > 1 ? 2. : 0.) *
+                           ((double)(g.groups * g.heads_per_group + g.groups) * g.d + (double)g.groups * g.dv);
     const bool halves = at[TH].seqs * units > LIN_SMS;   // long sequences' segments are of two tiles
     int best = 0;
     double best_us = 0.;
     for (int t = 0; t < TH; ++t) {   // th[t] the longest by rows
         double seqs = 0., rows = 0., longest = 0., tiles = (double)at[TH].seqs, segs = halves ? tiles / 2 : tiles, us = 0.;
+        double trows = (double)at[TH].rows, pieces = n_long;
         for (int b = 1; b < TH; ++b) {
             if (b <= t) {
                 seqs += (double)at[b].seqs;
@@ -299,12 +311,17 @@ int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n) {
             } else {
                 tiles += (double)at[b].seqs;
                 segs += (double)at[b].seqs;
+                pieces += (double)at[b].seqs;
+                trows += (double)at[b].rows;
             }
         }
         if (seqs) us += 2.5 + fmax(0.36 * longest, 2.9e-7 * E * rows) + 1.2e-6 * E * seqs;
         if (tiles) {
-            const double mb = (f32 ? 6e-6 : 4e-6) * E * segs, full = fmin(1., mb / 64.);
-            us += (f32 ? 20. : 14.) + (ceil(units * tiles / LIN_SMS) - 1.) * wave + 0.5 * mb * full * full;
+            const double state = (f32 ? 6. : 4.) * E;   // bytes of a segment, beside its panels
+            const double hold = fmin(LIN_PASS_STATES / (4. * E), most / (state + per_row * trows / segs));
+            const double passes = fmax(1., fmax(segs / fmax(1., floor(hold)), pieces / LIN_TABLE));
+            const double mb = 1e-6 * state * segs, full = fmin(1., mb / passes / 64.);
+            us += fixed * passes + fmax(0., ceil(units * tiles / LIN_SMS) - passes) * wave + 0.5 * mb * full * full;
         }
         if (t == 0 || us < best_us) best = th[t], best_us = us;
     }
@@ -403,7 +420,7 @@ int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, 
     if (rc != O1_OK) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     a.wait_cycles = o1_wait_limit();
-    const int short_rows = row_max(g, seqs, n_seq);
+    const int short_rows = row_max(g, seqs, n_seq, scratch_bytes);
     int64_t tiles_all = 0;
     for (int i = 0; i < n_seq; ++i)
         if (seqs[i].rows > short_rows) tiles_all += (seqs[i].rows - 1) / LIN_CHUNK + 1;

@@ -535,3 +535,30 @@ def test_captured_behind_other_work(o1, dt, before):
         graph.replay()
         torch.cuda.synchronize()
         check(o1, {**x, "q": src}, s0, [(0, 300, 1), (300, 120, 0)], out, geom.scale, f"behind a {before}")
+
+
+def kernels(run):
+    """Names of the kernels that a call launches, one a launch."""
+    from torch.profiler import ProfilerActivity, profile
+    for _ in range(2):   # the process's first profile may miss launches
+        with profile(activities=[ProfilerActivity.CUDA]) as p:
+            run()
+            torch.cuda.synchronize()
+    return [e.name for e in p.events() if "k_lin_" in e.name]
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+def test_short_sequences_of_a_small_scratch(o1, dt):
+    """With a scratch of one state each sequence sent to the tiles is a pass of
+    its own: 32 short ones go by rows, in one launch."""
+    G, hpg, d, n, r = 2, 2, 128, 32, 24
+    x = make(G, hpg, d, d, n * r, n, dt, 97)
+    geom, s0 = o1.lin_geom(G, hpg, d, d, dtype=dt), x["state"].clone()
+    seqs = [(r * i, r, i) for i in range(n)]
+    out = torch.full((n * r, G * hpg, d), float("nan"), dtype=dt, device="cuda")
+    names = kernels(lambda: chunk(o1, x, geom, seqs, out, scratch_rows=1))
+    assert len(names) == 1 and "k_lin_rows" in names[0], names
+    x["state"].copy_(s0)
+    chunk(o1, x, geom, seqs, out, scratch_rows=1)
+    torch.cuda.synchronize()
+    check(o1, x, s0, seqs, out, geom.scale, "small scratch by rows")
