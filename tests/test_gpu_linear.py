@@ -562,3 +562,26 @@ def test_short_sequences_of_a_small_scratch(o1, dt):
     chunk(o1, x, geom, seqs, out, scratch_rows=1)
     torch.cuda.synchronize()
     check(o1, x, s0, seqs, out, geom.scale, "small scratch by rows")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16])
+def test_passes_of_long_segments(o1, dt):
+    """More tiles than SMs (segments of 256 rows) in many passes: the least
+    scratch (steps of 16 rows, of a segment for bf16), one that takes 128 rows
+    but not a segment's panels, one of several segments. Sequences are cut at
+    each and carry on from their slots."""
+    G, hpg, d, dv = 4, 2, 72, 136
+    lens = [700, 129, 130, 256, 64, 255, 257, 300, 128, 513, 49, 1025, 384, 100]
+    rows = sum(lens)
+    x = make(G, hpg, d, dv, rows, len(lens), dt, 89)
+    seqs = [(sum(lens[:i]), n, len(lens) - 1 - i) for i, n in enumerate(lens)]
+    geom, s0 = o1.lin_geom(G, hpg, d, dv, dtype=dt), x["state"].clone()
+    want, Ao, S, As = ref.linear(x["q"], x["k"], x["v"], x["g"], s0, seqs, geom.scale)
+    bo, bs = ref.linear_bounds(want, Ao, As, seqs, dt)
+    for scratch_rows in (1, 128, 512, 900):
+        x["state"].copy_(s0)
+        out = torch.full((rows, G * hpg, dv), float("nan"), dtype=dt, device="cuda")
+        chunk(o1, x, geom, seqs, out, scratch_rows=scratch_rows)
+        torch.cuda.synchronize()
+        ref.assert_within(out, want, bo, f"scratch of {scratch_rows} rows, out")
+        ref.assert_within(x["state"], S, bs, f"scratch of {scratch_rows} rows, state")
