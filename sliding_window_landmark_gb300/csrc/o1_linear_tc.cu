@@ -1278,12 +1278,16 @@ bool lin_launch_pass(const LinArgs &a, int dtype, const LinWorkTable &t, int seg
                       : pass_t<__nv_bfloat16, 128>(a, t, dtype, segs, tiles, prows, scratch, first, st);
 }
 
+// The word is reset only where it was read as raised, after the read is over: a
+// flag that a kernel on another stream raises in between is then the one that
+// is reported, and none is dropped unread.
 int lin_flags(uint32_t *flags, int clear, cudaStream_t st) {
-    if (cudaMemcpyFromSymbolAsync(flags, lin_device_flags, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess)
+    if (cudaMemcpyFromSymbolAsync(flags, lin_device_flags, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
         return O1_ERR_CUDA;
+    if (!clear || !*flags) return O1_OK;
     static const uint32_t zero = 0;
-    if (clear &&
-        cudaMemcpyToSymbolAsync(lin_device_flags, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
+    if (cudaMemcpyToSymbolAsync(lin_device_flags, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
         return O1_ERR_CUDA;
     return cudaStreamSynchronize(st) == cudaSuccess ? O1_OK : O1_ERR_CUDA;
 }

@@ -585,3 +585,25 @@ def test_passes_of_long_segments(o1, dt):
         torch.cuda.synchronize()
         ref.assert_within(out, want, bo, f"scratch of {scratch_rows} rows, out")
         ref.assert_within(x["state"], S, bs, f"scratch of {scratch_rows} rows, state")
+
+
+def test_flags_of_two_streams(o1):
+    """A flag raised on one stream stays until it is read as raised, whichever
+    stream reads, with or without a reset; reads that find none drop none."""
+    x = make(2, 2, 128, 128, 600, 1, BF16, 103)
+    geom = o1.lin_geom(2, 2, 128, 128, dtype=BF16)
+    out, st = torch.zeros(600, 4, 128, dtype=BF16, device="cuda"), torch.cuda.Stream()
+    assert o1.o1_lin_flags(clear=True) == 0
+    torch.cuda.synchronize()
+    o1.o1_set_wait_limit(1)
+    try:
+        keep = chunk(o1, x, geom, [(0, 600, 0)], out, stream=st)
+        seen = [o1.o1_lin_flags(clear=True) for _ in range(50)]   # beside the running call
+    finally:
+        o1.o1_set_wait_limit(0)
+    torch.cuda.synchronize()
+    del keep
+    seen += [o1.o1_lin_flags(), o1.o1_lin_flags(clear=True, stream=st)]
+    assert o1.O1_FLAG_WAIT_EXPIRED in seen and set(seen) <= {0, o1.O1_FLAG_WAIT_EXPIRED}
+    o1.o1_lin_flags(clear=True)
+    assert o1.o1_lin_flags() == 0
