@@ -254,7 +254,7 @@ bool pass_within(const o1_lin_geom &g, int64_t segs, int64_t prows) {
 // with 256 rows, 152 with 128, 178 with 512. A call that does not fill the SMs
 // is bound by the longest chain instead: 1077 fp16 rows of 3 heads 19.7 us with
 // 128 rows, 22.1 with 256.
-int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : 2 * LIN_CHUNK; }
+int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : LIN_SEG; }
 
 // Sequences of up to that many rows take the row kernel, longer ones the chunk
 // kernels. Their times in us, E = nh d dv the elements of a sequence's states,

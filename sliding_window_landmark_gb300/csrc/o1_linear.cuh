@@ -12,10 +12,13 @@ struct LinTable {
 
 // Rows of a tile of the chunk kernels.
 #define LIN_CHUNK 128
+// Rows of a segment at most: two tiles (k_lin_out weights the scores against
+// one earlier tile).
+#define LIN_SEG (2 * LIN_CHUNK)
 // CTAs of their persistent grids: one an SM.
 #define LIN_SMS 152
 // A piece of a sequence in a pass of the chunk kernels: its rows in segments
-// of LinArgs::seg (a multiple of LIN_CHUNK), on the scratch's states seg0,
+// of LinArgs::seg (LIN_CHUNK or LIN_SEG), on the scratch's states seg0,
 // seg0 + 1, ..., in tiles tile0, tile0 + 1, ... of LIN_CHUNK rows, and, for
 // types that are split, in the panels' rows from prow0 on (a multiple of 16).
 struct LinWork {

@@ -713,7 +713,7 @@ template <typename T>
 struct OutCfg {
     static constexpr int NT = Terms<T>::in, MT = Terms<T>::mid;
     static constexpr bool PAIR = NT == 1;      // Q and K of a step share a slot
-    static constexpr int DK = 64;              // values of d a step
+    static constexpr int DK = 64;              // values of d a step: a block of the panels
     static constexpr int SLOT = NT == 3 ? 49152 : 32768, NSLOT = NT == 3 ? 4 : 6;
     static constexpr int VR = NT == 1 ? 128 : 64;   // value rows of a slot
     static constexpr bool SPLIT = NT == 3;     // corrections in accumulators of their own
@@ -746,7 +746,7 @@ struct OutTile {
     int row0, nr;        // query rows
     int prow, kprow;     // in the panels: the tile's and its segment's first row
     int i0, seg;         // row in the segment; the segment's state
-    int h, g, v0, nkt;
+    int h, g, v0, nkt;   // nkt: 1 or 2 (LIN_SEG rows a segment at most)
     int nv;              // value columns, rounded to 16
 };
 struct Cursor {
@@ -883,10 +883,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                 tc_after();
                 const uint64_t qd = dk + (uint64_t)(sq * (C::SLOT / 16));
                 const uint64_t kd = C::PAIR ? qd + C::DK * 16 : dk + (uint64_t)(sk * (C::SLOT / 16));
-#pragma unroll 1
-                for (int i = 0; 4 * i < steps; ++i)
-                    issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(e, x, x + C::CORR, id_x, min(4, steps - 4 * i), b + i > 0,
-                                                                   qd + 1024 * i, kd + 1024 * i);
+                issue<NT, NT, NT - 1, false, 1024, 2, 1024, 2>(e, x, x + C::CORR, id_x, steps, b > 0, qd, kd);
                 if (!C::PAIR) commit(&empty[sk]);
                 if (b == nb - 1) commit(&sc_full[cq.u % C::XB]);
                 if (state) {
@@ -895,10 +892,8 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                     if (!ok) return;
                     tc_after();
                     const uint64_t sd = ds + (uint64_t)(ss * (C::SLOT / 16));
-#pragma unroll 1
-                    for (int i = 0; 4 * i < steps; ++i)
-                        issue<NT, MT, max_sum(NT, MT), false, 1024, 2, C::DK * TN * 2 / 16, 128>(
-                            e, acc, acc + C::CORR, id_a, min(4, steps - 4 * i), b + i > 0, qd + 1024 * i, sd + 512 * i);
+                    issue<NT, MT, max_sum(NT, MT), false, 1024, 2, C::DK * TN * 2 / 16, 128>(e, acc, acc + C::CORR, id_a, steps,
+                                                                                             b > 0, qd, sd);
                     commit(&empty[ss]);
                 }
                 commit(&empty[sq]);
@@ -969,9 +964,8 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             for (int b = 0; b < nb; ++b) {
                 unsigned char *d = slot();
                 if (!ok) return;
-                const int db = (min(C::DK, a.d - C::DK * b) + 63) / 64;   // blocks of 64 columns
-                expect(16384 * db * (C::PAIR ? 2 : NT));
-                tma_panel<NT, 128, 16384>(d, &mq, C::DK * b, cq.x.h, cq.x.prow, db, f, lane);
+                expect(16384 * (C::PAIR ? 2 : NT));
+                tma_panel<NT, 128, 16384>(d, &mq, C::DK * b, cq.x.h, cq.x.prow, 1, f, lane);
                 if (C::PAIR) {
                     d += C::DK * 256;
                 } else {
@@ -979,7 +973,7 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
                     if (!ok) return;
                     expect(16384 * NT);
                 }
-                tma_panel<NT, 128, 16384>(d, &mk, C::DK * b, cq.x.g, cq.key0(), db, f, lane);
+                tma_panel<NT, 128, 16384>(d, &mk, C::DK * b, cq.x.g, cq.key0(), 1, f, lane);
                 if (cq.kt == 0) {
                     d = slot();
                     if (!ok) return;
@@ -1058,10 +1052,10 @@ __global__ __launch_bounds__(OUT_THREADS, 1) void k_lin_out(LinArgs a, const __g
             if (!ok) break;
             tc_after();
             const bool diag = c.diag();
-            // weights: l^{row - j} up to the diagonal; for an earlier tile
-            // l^{127 - j} for all its keys, the tiles in between, and l^{row + 1}
+            // weights: l^{row - j} up to the diagonal; for the tile before
+            // l^{127 - j} for all its keys, and l^{row + 1}
             const int base = diag ? row : LIN_CHUNK - 1;
-            const float tf = diag ? 1.f : lin_pow(g, LIN_CHUNK * (c.x.nkt - 2 - c.kt)) * pw.at(row + 1);
+            const float tf = diag ? 1.f : pw.at(row + 1);
             const uint32_t x = lanes + C::x(c.u);
             // P over the scores of the same keys; a third term of 32 keys
             // takes 16 columns of the corrections, of keys this warp has read.
