@@ -153,13 +153,12 @@ def _own(s, case):
     if "geom" not in s:
         s["geom"] = o1.lin_geom(case["groups"], case["hpg"], case["d"], case["dv"], dtype=s["q"].dtype)
         if case["op"] == "chunk":
-            s["plan"] = o1.lin_seqs(s["seqs"])
             # the scratch as a user's program sizes it: by the library's own function
             s["scratch"] = torch.empty(o1.o1_lin_scratch_bytes(s["geom"], s["q"].shape[0], len(s["seqs"])),
                                        dtype=torch.uint8, device="cuda")
     if case["op"] == "chunk":
         o1.check(o1.o1_lin_chunk_attend(s["state"], s["geom"], s["scratch"], s["q"], s["k"], s["v"], s["g"],
-                                        s["plan"], s["out"]), "chunk")
+                                        s["seqs"], s["out"]), "chunk")
     else:
         o1.check(o1.o1_lin_token_attend(s["state"], s["geom"], s["q"], s["k"], s["v"], s["g"], s["slots"],
                                         s["out"]), "token")
