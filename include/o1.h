@@ -399,8 +399,8 @@ typedef struct o1_prep_geom {
  * Sums and the rotation are fp32; the angle is reduced exactly in fixed point
  * (a turn is 2^64), so far positions keep fp32 accuracy. The sum of squares
  * of a head must be finite in fp32; it may be as small as it likes, and a NaN
- * in a head makes the head NaN under a norm. The result feeds o1_chunk_attend and its
- * kin with rope_base = 0, or the linear layer. rows = 0 does nothing.
+ * in a head makes the head NaN under a norm. The result feeds o1_chunk_attend
+ * and its kin with rope_base = 0, or the linear layer. rows = 0 does nothing.
  * Asynchronous; one launch. */
 O1_API int o1_head_prep(const o1_prep_geom *geom, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                         const float *q_weight, const float *k_weight, const float *inv_freq, const int64_t *pos,
@@ -428,13 +428,17 @@ typedef struct o1_lin_seq {
 /* Bytes of `slots` states, fp32 [slots][nh][d][dv], 16-byte aligned, which
  * the caller sets to zero (an empty sequence) or to any finite state before
  * first use, copies and keeps as it likes: there is no header. 0 if the
- * geometry is unsupported or slots < 1. Host-only. */
+ * geometry is unsupported, slots < 1, or the size does not fit 64 bits.
+ * Host-only. */
 O1_API size_t o1_lin_state_bytes(const o1_lin_geom *geom, int32_t slots);
 
-/* Bytes of device scratch that lets o1_lin_chunk_attend run `rows` rows of at
- * most `seqs` sequences in one pass. Any size from
- * o1_lin_scratch_bytes(geom, 1, 1) on works: longer batches run as several
- * passes. Host-only; 0 if unsupported or a count is below 1. */
+/* Bytes of device scratch that o1_lin_chunk_attend has a use for in a call of
+ * `rows` rows of at most `seqs` sequences. A call runs in one pass over what
+ * the scratch holds, or in several: large calls in passes of about 64 MB of
+ * states (256 MB with the rows of fp16 and fp32) and 128 sequences, whatever
+ * the scratch, and the size returned is no larger than such a pass. Any size
+ * from o1_lin_scratch_bytes(geom, 1, 1) on works, in passes as small as it is.
+ * Host-only; 0 if unsupported or a count is below 1. */
 O1_API size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_t seqs);
 
 /* Linear attention with a decay per head over packed sequences: the state of
@@ -456,9 +460,10 @@ O1_API size_t o1_lin_scratch_bytes(const o1_lin_geom *geom, int32_t rows, int32_
  *   out        device row tensor [total_rows][nh][dv]; rows of no sequence
  *              are left as they were
  * q, k, v and the state are finite, in fp32 at most 3.38e38 (the largest bf16
- * value). A non-finite one spoils rows and the state of its own sequence only:
- * from its row on, and up to 127 rows before it. Rows of no sequence may hold
- * anything. States and sums are fp32. Longer sequences run on the tensor cores:
+ * value), and so are the sums q_i . k_j of a row and the rows up to 255 before
+ * it in its sequence, which longer sequences form. A non-finite one spoils
+ * rows and the state of its own sequence only: from its row on, and up to 127
+ * rows before it. Rows of no sequence may hold anything. States and sums are fp32. Longer sequences run on the tensor cores:
  * operands are split into bf16 terms that hold fp32 and fp16 values and the
  * decayed keys to fp32 accuracy; for 16-bit outputs the entering state and
  * the scores are taken to 2^-16. Calls that may overlap on the GPU (other
@@ -474,7 +479,9 @@ O1_API int o1_lin_chunk_attend(float *state, int32_t n_slots, const o1_lin_geom 
  * device array, so that a captured step can be replayed on other slots. A row
  * whose slot is outside [0, n_slots) is padding: its output is left as it
  * was. Of rows that name the same slot the first counts and the others are
- * padding. At most 65536 rows. No scratch; one launch; asynchronous. */
+ * padding (with slots, every row looks at those of the rows before it: a time
+ * that grows with the square of the rows and shows from some thousands on).
+ * At most 65536 rows. No scratch; one launch; asynchronous. */
 O1_API int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom *geom, const void *q,
                                int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                const float *log_decay, const int32_t *slots, void *out, int64_t out_stride,

@@ -77,7 +77,9 @@ __device__ __forceinline__ float4 scaled(float4 x, float f) { return make_float4
 
 // Token batch: row r on slot slots[r]. A row whose slot an earlier row names
 // is padding (two CTAs on one state would race), so every CTA looks through
-// the earlier rows' slots, under the state's loads. The state goes back before
+// the earlier rows' slots, under the state's loads: 1024 bf16 rows of 16 heads
+// of 64 take 110 us, 103 without slots; 4096 of 16 heads of 128 1421 and 1264;
+// 65536 fp32 rows of one head of 64 754 and 375. The state goes back before
 // the output's sum. Bound: HBM, by the state (8 d dv bytes a head and step).
 template <typename T, int NI>
 __global__ __launch_bounds__(ROW_THREADS, 3) void k_lin_token(LinArgs a) {
@@ -233,9 +235,12 @@ size_t slot_floats(const o1_lin_geom &g) {
 bool slots_ok(const o1_lin_geom &g, int32_t slots) { return (size_t)slots <= SIZE_MAX / 4 / slot_floats(g); }
 
 // Limits of a pass: its states are written, read, rewritten and read again and
-// are kept to what stays in the L2 (a 32768-row prompt of 2 MB a state: 412 us
-// in passes of 64 MB, 469 of 96, 472 of 128); its scratch as a whole, and its
-// rows, so that counts fit 32 bits.
+// are kept to what stays in the L2; its scratch as a whole, and its rows, so
+// that counts fit 32 bits. In passes of 32 / 48 / 64 / 96 / 128 MB of states a
+// bf16 prompt of 32768 rows of 8 heads of 256 took 401 / 379 / 340 / 353 / 344
+// us (fp16 647 / 622 / 562 / 580 / 571), of 16 heads of 128 253 / 238 / 218 /
+// 232 / 218, 16384 rows of 64 heads of 128 with a key head each 548 / 517 / 475
+// / 466 / 450; 16384 fp32 rows of 8 heads of 256 508 / 493 / 453 / 480 / 452.
 constexpr size_t LIN_PASS_STATES = (size_t)64 << 20, LIN_PASS_BYTES = (size_t)256 << 20;
 constexpr int64_t LIN_PASS_ROWS = 1 << 24;
 
@@ -250,10 +255,18 @@ bool pass_within(const o1_lin_geom &g, int64_t segs, int64_t prows) {
 // Rows of a segment for a call of `tiles` tiles (LIN_CHUNK rows of a head, 128
 // value columns). Longer segments write and read fewer states (4 d dv bytes a
 // head each, several times over) and pay with scores against the earlier
-// tiles of the segment: a 4096-row fp32 prompt of 8 heads of 256 took 141 us
-// with 256 rows, 152 with 128, 178 with 512. A call that does not fill the SMs
-// is bound by the longest chain instead: 1077 fp16 rows of 3 heads 19.7 us with
-// 128 rows, 22.1 with 256.
+// tiles of the segment. Prompts in us with 128 / 256 / 512 rows (512 from a
+// build with any number of tiles a segment):
+//                            bf16                fp16                fp32
+//    4096, 8 heads of 256     58 /  49 /  58      88 /  82 / 101     132 / 128 / 161
+//   32768, 8 heads of 256    461 / 340 / 343     697 / 564 / 617    1042 / 907 / 1069
+//    4096, 16 heads of 128    41 /  37 /  45      61 /  58 /  72      92 /  92 / 116
+//   32768, 16 heads of 128   273 / 217 / 231     422 / 375 / 430     644 / 633 / 737
+//    4096, 64 heads of 128,  157 / 120 / 138     300 / 277 / 305     509 / 483 / 535
+//   32768, a key head each  1250 / 947 / 962    2390 /2217 /2438    3946 /3795 /4221
+// A call that does not fill the SMs is bound by the longest chain instead: 1077
+// fp16 rows of 3 heads 19.7 us with 128 rows, 22.1 with 256 (before the scan
+// took several rows a warp; 17.8 now).
 int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : LIN_SEG; }
 
 // Sequences of up to that many rows take the row kernel, longer ones the chunk

@@ -33,12 +33,14 @@
 // Both kernels of MMAs are persistent and split by warp: TMA (or, for weighted
 // keys, staging warps), an MMA issuer, P warps, and warps that store.
 //
-// Bound, measured at 32768 bf16 rows of 8 heads of 256 (338 us, 4 passes): the
-// outputs (45 us a pass) by the L2-to-shared-memory ingest, 46 bytes a clock
-// and SM at best, 31 on average; the increments (28) by the keys' weighting and
-// splitting beside MMAs that read 96 of the 128 bytes a clock shared memory
-// gives; the scan (14) by its bytes, 9 TB/s in the L2. fp32 (4096 rows: 128 us) reads
-// three terms: its 128 x 128 MMAs alone take the whole shared-memory bandwidth.
+// Bound, measured at 32768 bf16 rows of 8 heads of 256 (341 us, 4 passes; a
+// pass's kernels alone, under the profiler, take 45, 29 and 14 us, 351 in all:
+// in the call a kernel's set-up runs under the one before): the outputs by the
+// L2-to-shared-memory ingest, 46 bytes a clock and SM at best, 31 on average;
+// the increments by the keys' weighting and splitting beside MMAs that read 96
+// of the 128 bytes a clock shared memory gives; the scan by its bytes, 9 TB/s
+// in the L2. fp32 (4096 rows: 128 us) reads three terms: its 128 x 128 MMAs
+// alone take the whole shared-memory bandwidth.
 #include <math.h>
 
 #include "o1_linear.cuh"
