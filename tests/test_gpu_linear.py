@@ -537,14 +537,16 @@ def test_captured_behind_other_work(o1, dt, before):
         check(o1, {**x, "q": src}, s0, [(0, 300, 1), (300, 120, 0)], out, geom.scale, f"behind a {before}")
 
 
-def kernels(run):
-    """Names of the kernels that a call launches, one a launch."""
-    from torch.profiler import ProfilerActivity, profile
-    for _ in range(2):   # the process's first profile may miss launches
-        with profile(activities=[ProfilerActivity.CUDA]) as p:
-            run()
-            torch.cuda.synchronize()
-    return [e.name for e in p.events() if "k_lin_" in e.name]
+def launches(run):
+    """How many nodes a call leaves in a captured graph: its launches."""
+    import ctypes
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        run()
+    n = ctypes.c_size_t(0)
+    cudart = ctypes.CDLL(next(line.split()[-1] for line in open("/proc/self/maps") if "libcudart.so" in line))
+    assert cudart.cudaGraphGetNodes(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+    return n.value
 
 
 @pytest.mark.parametrize("dt", [F32, BF16, F16])
@@ -556,8 +558,11 @@ def test_short_sequences_of_a_small_scratch(o1, dt):
     geom, s0 = o1.lin_geom(G, hpg, d, d, dtype=dt), x["state"].clone()
     seqs = [(r * i, r, i) for i in range(n)]
     out = torch.full((n * r, G * hpg, d), float("nan"), dtype=dt, device="cuda")
-    names = kernels(lambda: chunk(o1, x, geom, seqs, out, scratch_rows=1))
-    assert len(names) == 1 and "k_lin_rows" in names[0], names
+    scratch = torch.empty(o1.o1_lin_scratch_bytes(geom, 1), dtype=torch.uint8, device="cuda")
+    call = lambda: o1.check(o1.o1_lin_chunk_attend(x["state"], geom, scratch, x["q"], x["k"], x["v"], x["g"], seqs, out))
+    call()
+    torch.cuda.synchronize()
+    assert launches(call) == 1
     x["state"].copy_(s0)
     chunk(o1, x, geom, seqs, out, scratch_rows=1)
     torch.cuda.synchronize()
