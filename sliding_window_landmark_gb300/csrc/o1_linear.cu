@@ -283,10 +283,11 @@ int seg_rows(int64_t tiles) { return tiles <= LIN_SMS ? LIN_CHUNK : LIN_SEG; }
 // 16 heads of 128, bf16, 2047 rows beside 4 of 16 rows 31 us as tiles and 39 by
 // rows, beside 64 of 4 rows 114 and 67. fp16's waves are charged as bf16's: a
 // third more sent 4 of 16 rows beside 2047 by rows, 49 us, where tiles take 41.
-// Passes are what the limits and the scratch let into one, in parts (whole ones
-// moved sequences apart that fill a prompt's last pass: 8 of 4 rows beside
-// 32768 237 us, 228 with the tiles): with a scratch of one state every short
+// A pass beyond the first is charged where what the limits and the scratch let
+// into one does not fill the SMs: with a scratch of one state every short
 // sequence among the tiles is a pass, 32 bf16 ones of 24 rows 96 launches.
+// (Charged for all of them, 64 of 16 rows beside 32768 of 16 heads of 128 went
+// by rows: bf16 318 us, 304 with the tiles.)
 int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n, size_t scratch_bytes) {
     constexpr int TH = 6;
     const bool f32 = g.dtype == O1_F32;
@@ -294,14 +295,12 @@ int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n, size_t scratch_byt
     struct {
         int64_t seqs, rows, longest;
     } at[TH + 1] = {};   // of th[i - 1] + 1 .. th[i] rows; at[TH]: longer, in tiles
-    int n_long = 0;
     for (int i = 0; i < n; ++i) {
         const int r = s[i].rows;
         int b = 0;
         while (b < TH && r > th[b]) ++b;
         at[b].seqs += b < TH ? 1 : (r - 1) / LIN_CHUNK + 1;
         at[b].rows += r;
-        n_long += b == TH;
         if (r > at[b].longest) at[b].longest = r;
     }
     const double E = (double)slot_floats(g), units = (double)(g.groups * g.heads_per_group) * ((g.dv + 127) / 128);
@@ -315,7 +314,7 @@ int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n, size_t scratch_byt
     double best_us = 0.;
     for (int t = 0; t < TH; ++t) {   // th[t] the longest by rows
         double seqs = 0., rows = 0., longest = 0., tiles = (double)at[TH].seqs, segs = halves ? tiles / 2 : tiles, us = 0.;
-        double trows = (double)at[TH].rows, pieces = n_long;
+        double trows = (double)at[TH].rows;
         for (int b = 1; b < TH; ++b) {
             if (b <= t) {
                 seqs += (double)at[b].seqs;
@@ -324,15 +323,14 @@ int row_max(const o1_lin_geom &g, const o1_lin_seq *s, int n, size_t scratch_byt
             } else {
                 tiles += (double)at[b].seqs;
                 segs += (double)at[b].seqs;
-                pieces += (double)at[b].seqs;
                 trows += (double)at[b].rows;
             }
         }
         if (seqs) us += 2.5 + fmax(0.36 * longest, 2.9e-7 * E * rows) + 1.2e-6 * E * seqs;
         if (tiles) {
             const double state = (f32 ? 6. : 4.) * E;   // bytes of a segment, beside its panels
-            const double hold = fmin(LIN_PASS_STATES / (4. * E), most / (state + per_row * trows / segs));
-            const double passes = fmax(1., fmax(segs / fmax(1., floor(hold)), pieces / LIN_TABLE));
+            const double hold = floor(fmin(LIN_PASS_STATES / (4. * E), most / (state + per_row * trows / segs)));
+            const double passes = hold * units < LIN_SMS ? fmax(1., segs / fmax(1., hold)) : 1.;   // that do not fill the SMs
             const double mb = 1e-6 * state * segs, full = fmin(1., mb / passes / 64.);
             us += fixed * passes + fmax(0., ceil(units * tiles / LIN_SMS) - passes) * wave + 0.5 * mb * full * full;
         }
