@@ -1,0 +1,365 @@
+"""Measured cases of the paged cache of exact attention layers, each operator in its plain form (elementary torch
+operations) and, with ``own`` set, as the calls a user makes of the binding.
+
+  write  o1_pg_write, o1_pg_token_write     rows of keys and values into a cache of 16 or 8 bits
+  read   o1_pg_read                         the cached rows of sequences back as rows
+  chunk  o1_pg_chunk_attend                 attention of new rows of packed sequences over the cache
+  token  o1_pg_token_attend                 the same, one row per sequence
+
+The cache holds pages [group][page rows][width]; a table names the pages of each sequence. Position p of a sequence
+attends its positions max(0, p - window + 1) .. p: out = sum_j w_j v_j / sum_j w_j, w_j = e^{scale q . k_j}. In 8 bits a
+head's row x is stored as e4m3 values x / 2^e, rounded to nearest even, 2^e the smallest power of two with
+max |x| <= 448 2^e (e >= -126), and as the byte e + 127.
+"""
+import math
+
+import torch
+
+own = False
+
+F32, BF16, F16, E4M3 = "f32", "bf16", "f16", "e4m3"
+_TYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16, E4M3: torch.float8_e4m3fn}
+_BYTES = {F32: 4, BF16: 2, F16: 2, E4M3: 1}
+
+
+def listed():
+    return [
+        # one decode row of the Qwen3.5-0.8B-shaped layer (8 query and 2 key heads of 256) into its cache: latency
+        dict(name="write one row", op="write", form="rows", rows=1, slots=1, pos_max=8192, groups=2, hpg=4, d=256, dv=256,
+             page=64, t=F32, cache=BF16),
+        # a long prompt of the stack layer's fp32 rows, quantised on the way into the cache
+        dict(name="write prompt", op="write", form="seqs", lens="32000,749", slots=4, pos_max=500, groups=4, hpg=4, d=128,
+             dv=128, page=64, t=F32, cache=E4M3),
+        # two odd sequences with narrow odd heads taken out of a cache
+        dict(name="read odd widths", op="read", lens="1000,77", slots=3, pos_max=300, groups=3, hpg=1, d=72, dv=40, page=32,
+             t=F16, cache=F16),
+        # a long sequence read back as fp32 rows, as a sealed layer's commit takes them
+        dict(name="read long", op="read", lens="32768", slots=1, pos_max=1, groups=2, hpg=4, d=256, dv=256, page=64, t=F32,
+             cache=E4M3),
+        # one decode step of one sequence, fp32 rows
+        dict(name="token one", op="token", rows=1, pad=0, slots=1, pos_min=8191, pos_max=8192, groups=2, hpg=4, d=256, dv=256,
+             page=64, window=0, t=F32, cache=BF16),
+        # a ragged decode batch of the stack layer, lengths of 1 to 32768, small pages of 8 bits, some rows padding
+        dict(name="token ragged", op="token", rows=61, pad=3, slots=80, pos_min=0, pos_max=32768, groups=4, hpg=4, d=128, dv=128,
+             page=16, window=0, t=BF16, cache=E4M3),
+        # a large decode batch: 4 GB of cache
+        dict(name="token large", op="token", rows=256, pad=0, slots=256, pos_min=4096, pos_max=14000, groups=4, hpg=4, d=128,
+             dv=128, page=64, window=0, t=BF16, cache=BF16),
+        # one 64-row chunk of the stack layer behind a long prefix: the pages' calling pattern
+        dict(name="chunk 64 rows", op="chunk", lens="64", pasts="16000", slots=1, groups=4, hpg=4, d=128, dv=128, page=64,
+             window=0, t=F32, cache=BF16),
+        # odd widths and heads, half precision, a sliding window that ends inside pages and tiles
+        dict(name="chunk odd widths", op="chunk", lens="300,77", pasts="0,1001", slots=3, groups=3, hpg=3, d=72, dv=40, page=32,
+             window=200, t=F16, cache=F16),
+        # a ragged batch of prompts and later chunks, 8-bit cache, one empty and one of a single row among them
+        dict(name="chunk ragged", op="chunk", lens="700,1,2047,0,130,1500,17,64,333", pasts="0,2000,0,5,1000,33,4090,3000,777",
+             slots=12, groups=4, hpg=4, d=128, dv=128, page=16, window=0, t=BF16, cache=E4M3),
+        # a prompt from an empty cache
+        dict(name="chunk prompt", op="chunk", lens="8192", pasts="0", slots=1, groups=4, hpg=4, d=128, dv=128, page=64, window=0,
+             t=BF16, cache=BF16),
+        # the last 4096 rows of a 16384-row prompt of the Qwen3.5-0.8B-shaped layer
+        dict(name="chunk long", op="chunk", lens="4096", pasts="12288", slots=1, groups=2, hpg=4, d=256, dv=256, page=128,
+             window=0, t=BF16, cache=BF16),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "read", "chunk", "chunk", "token", "token"])
+    t, small = rng.choice([F32, BF16, F16]), rng.random() < 0.5
+    cache = E4M3 if small else F16 if t == F16 else BF16
+    unit = 16 if small else 8
+    d, dv = rng.choice([(64, 64), (128, 128), (256, 256), tuple(unit * rng.randint(1, 256 // unit) for _ in "kv")])
+    groups = rng.randint(1, 4)
+    case = dict(op=op, groups=groups, hpg=rng.choice([1, 2, 3, 4] if groups > 2 else [1, 3, 4, 8]), d=d, dv=dv,
+                page=rng.choice([16, 32, 64, 128, 256]), t=t, cache=cache)
+    n = rng.randint(1, 6)
+    if op == "write" and rng.random() < 0.3:
+        rows = _log(rng, 1, 512)
+        return dict(case, form="rows", rows=rows, slots=rows + rng.randint(0, 9), pos_max=_log(rng, 1, 2000))
+    if op in ("write", "read"):
+        lens = [rng.choice([0, 1, _log(rng, 2, 8192), _log(rng, 2, 8192)]) for _ in range(n)] + [_log(rng, 2, 8192)]
+        form = dict(form="seqs") if op == "write" else {}
+        return dict(case, **form, lens=",".join(map(str, lens)), slots=len(lens) + rng.randint(0, 3), pos_max=_log(rng, 1, 2000))
+    case["window"] = rng.choice([0, 0, _log(rng, 1, 4096)])
+    if op == "token":
+        rows, lo = _log(rng, 1, 96), rng.choice([0, 0, 1000])
+        return dict(case, rows=rows, pad=rng.randint(0, rows // 4), slots=rows + rng.randint(0, 9), pos_min=lo,
+                    pos_max=lo + _log(rng, 1, 16384))
+    lens = [rng.choice([0, 1, _log(rng, 2, 2048), _log(rng, 2, 2048)]) for _ in range(n)] + [_log(rng, 2, 2048)]
+    pasts = [rng.choice([0, _log(rng, 1, 8192)]) for _ in lens]
+    return dict(case, lens=",".join(map(str, lens)), pasts=",".join(map(str, pasts)), slots=len(lens) + rng.randint(0, 3))
+
+
+def _ints(text):
+    return [int(x) for x in text.split(",")]
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(int(seed))
+    host = torch.Generator().manual_seed(int(seed))
+    G, d, dv, page, slots, t = case["groups"], case["d"], case["dv"], case["page"], case["slots"], _TYPES[case["t"]]
+    nh = G * case["hpg"]
+
+    def randn(*shape, dtype=torch.float32):
+        return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
+
+    s = dict(case=case)
+    order = torch.randperm(slots, generator=host)
+    if case.get("form") == "rows" or case["op"] == "token":
+        # one row of each sequence, at its position; a slot of -1 is a padding row
+        rows, lo = case["rows"], case.get("pos_min", 0)
+        if lo == 0 and case["pos_max"] >= 1024:   # lengths spread over their logarithm
+            pos = torch.exp(torch.rand(rows, generator=host, dtype=torch.float64) * math.log(case["pos_max"])).long() - 1
+        else:
+            pos = torch.randint(lo, case["pos_max"], (rows,), generator=host)
+        slot = order[:rows].clone()
+        ends = torch.zeros(slots, dtype=torch.long)
+        ends[slot] = pos + 1
+        slot[torch.randperm(rows, generator=host)[:case.get("pad", 0)]] = -1
+        s["slots"], s["pos"] = slot.to(torch.int32).cuda(), pos.cuda()
+    else:
+        # packed sequences (first row, rows, slot, first position), a few rows of no sequence at the end
+        lens = _ints(case["lens"])
+        pasts = _ints(case["pasts"]) if "pasts" in case else torch.randint(0, case["pos_max"], (len(lens),), generator=host).tolist()
+        rows = sum(lens) + 5 * (len(lens) > 1)
+        s["seqs"] = [(sum(lens[:i]), n, int(order[i]), pasts[i]) for i, n in enumerate(lens)]
+        ends = torch.zeros(slots, dtype=torch.long)
+        ends[order[:len(lens)]] = torch.tensor(lens) + torch.tensor(pasts)
+    # pages in an order of their own; what lies past a sequence's end in the table is not a page
+    used = (ends + page - 1) // page
+    n_pages = int(used.sum()) + 3
+    if case["op"] == "write":   # a pool is an output there: of one size whatever the positions
+        lens = _ints(case["lens"]) if "lens" in case else [1] * case["rows"]
+        n_pages = sum((n + case["pos_max"] - 1) // page + 1 for n in lens) + 3
+    ids = torch.randperm(n_pages, generator=host)
+    table = torch.full((slots, int(used.max()) + 1), n_pages + 7, dtype=torch.int32)
+    live = torch.arange(table.shape[1]) < used[:, None]
+    table[live] = ids[:int(used.sum())].to(torch.int32)
+    s["table"] = table.cuda()
+    if case["cache"] == E4M3:
+        s["k"], s["v"] = ((randn(n_pages, G, page, w) * 128).clamp(-448, 448).to(torch.float8_e4m3fn) for w in (d, dv))
+        s["k_exp"], s["v_exp"] = (torch.randint(119, 122, (n_pages, G, page), generator=gen, device="cuda", dtype=torch.uint8)
+                                  for _ in "kv")
+    else:
+        s["k"], s["v"] = (randn(n_pages, G, page, w, dtype=_TYPES[case["cache"]]) for w in (d, dv))
+    if case["op"] == "write":
+        # heads of different sizes, as projections give them
+        s["k_rows"], s["v_rows"] = ((randn(rows, G, w) * torch.exp2(randn(rows, G, 1))).to(t) for w in (d, dv))
+    elif case["op"] == "read":
+        s["k_rows"], s["v_rows"] = (torch.zeros(rows, G, w, dtype=t, device="cuda") for w in (d, dv))
+    else:
+        s["q"], s["out"] = randn(rows, nh, d, dtype=t), torch.zeros(rows, nh, dv, dtype=t, device="cuda")
+    return s
+
+
+def run(s):
+    case = s["case"]
+    if own:
+        return _own(s, case)
+    return {"write": _write, "read": _read, "chunk": _attend, "token": _attend}[case["op"]](s, case)
+
+
+def _pools(s):
+    return {n: s[n] for n in ("k", "v", "k_exp", "v_exp") if n in s}
+
+
+def _own(s, case):
+    from sliding_window_landmark_gb300 import o1
+    if "geom" not in s:
+        # what a program keeps: the geometry, the cache's description and a scratch, sized by the library's own function
+        s["geom"] = o1.pg_geom(case["groups"], case["hpg"], case["d"], case["dv"], case["page"], dtype=_TYPES[case["t"]],
+                               cache_dtype=_TYPES[case["cache"]], window=case.get("window", 0))
+        s["cache"] = o1.pg_cache(s["geom"], s["k"], s["v"], s["table"], s.get("k_exp"), s.get("v_exp"))
+        if "q" in s:
+            s["scratch"] = torch.empty(o1.o1_pg_scratch_bytes(s["geom"], s["q"].shape[0]), dtype=torch.uint8, device="cuda")
+    g, c = s["geom"], s["cache"]
+    if case["op"] == "write":
+        if case["form"] == "rows":
+            o1.check(o1.o1_pg_token_write(g, c, s["k_rows"], s["v_rows"], s["slots"], s["pos"]), "write")
+        else:
+            o1.check(o1.o1_pg_write(g, c, s["k_rows"], s["v_rows"], s["seqs"]), "write")
+        return _pools(s)
+    if case["op"] == "read":
+        o1.check(o1.o1_pg_read(g, c, s["seqs"], s["k_rows"], s["v_rows"]), "read")
+        return s["k_rows"], s["v_rows"]
+    if case["op"] == "chunk":
+        o1.check(o1.o1_pg_chunk_attend(g, c, s["scratch"], s["q"], s["seqs"], s["out"]), "chunk")
+    else:
+        o1.check(o1.o1_pg_token_attend(g, c, s["scratch"], s["q"], s["slots"], s["pos"], s["out"]), "token")
+    return s["out"]
+
+
+# ------------------------------------------------------------ plain forms
+
+def _sequences(s):
+    """First row, rows, slot and first position of every live sequence, on the GPU."""
+    if "seqs" in s:
+        return torch.tensor(s["seqs"], device="cuda").T
+    live = (s["slots"] >= 0).nonzero()[:, 0]
+    return live, torch.ones_like(live), s["slots"][live].long(), s["pos"][live]
+
+
+def _rows_of(s):
+    """Every row of a sequence: its index in the row tensors, its page and its row in that page."""
+    row0, rows, slot, past = _sequences(s)
+    i = torch.arange(int(rows.max()), device="cuda")
+    valid = i < rows[:, None]
+    p = (past[:, None] + i)[valid]
+    page = s["case"]["page"]
+    return (row0[:, None] + i)[valid], s["table"][slot.repeat_interleave(rows), p // page].long(), p % page
+
+
+def _write(s, case):
+    row, page, at = _rows_of(s)
+    for name in ("k", "v"):
+        x = s[name + "_rows"][row].float()
+        if case["cache"] == E4M3:
+            top = x.abs().amax(-1)
+            m, e = torch.frexp(top)                      # top = m 2^e, m in [1/2, 1); 448 = 0.875 2^9
+            e = (torch.where(top > 0, torch.where(m <= 0.875, e - 9, e - 8), -126)).clamp(min=-126)
+            s[name + "_exp"][page, :, at] = (e + 127).to(torch.uint8)
+            x = torch.ldexp(x, -e[..., None]).to(torch.float8_e4m3fn)
+            s[name].view(torch.uint8)[page, :, at] = x.view(torch.uint8)
+        else:
+            s[name][page, :, at] = x.to(s[name].dtype)
+    return _pools(s)
+
+
+def _cached(s, name, page, at):
+    """Cached rows [..., groups, width] in 32 bits."""
+    if name + "_exp" not in s:
+        return s[name][page, :, at].float()
+    x = s[name].view(torch.uint8)[page, :, at].view(torch.float8_e4m3fn).float()
+    return torch.ldexp(x, s[name + "_exp"][page, :, at].int()[..., None] - 127)
+
+
+def _read(s, case):
+    row, page, at = _rows_of(s)
+    s["k_rows"][row] = _cached(s, "k", page, at).to(s["k_rows"].dtype)
+    s["v_rows"][row] = _cached(s, "v", page, at).to(s["v_rows"].dtype)
+    return s["k_rows"], s["v_rows"]
+
+
+def _attend(s, case):
+    """All sequences padded to one count of rows and one of keys."""
+    G, hpg, page, window = case["groups"], case["hpg"], case["page"], case["window"]
+    row0, rows, slot, past = _sequences(s)
+    i = torch.arange(int(rows.max()), device="cuda")
+    j = torch.arange(int(((past + rows) * (rows > 0)).max()), device="cuda")
+    valid = i < rows[:, None]                                                          # [B, Lq]
+    at = torch.where(valid, row0[:, None] + i, 0)
+    held = j < (past + rows)[:, None]                                                  # [B, Lk]
+    pages = torch.where(held, s["table"][slot][:, (j // page).clamp(max=s["table"].shape[1] - 1)].long(), 0)
+    k, v = (torch.where(held[..., None, None], _cached(s, n, pages, j % page), 0.0).transpose(1, 2) for n in "kv")
+    q = torch.where(valid[..., None, None], s["q"][at].float(), 0.0).unflatten(2, (G, hpg)).permute(0, 2, 1, 3, 4)
+    w = (q.flatten(2, 3) @ k.transpose(-1, -2)).unflatten(2, (-1, hpg))                # [B, G, Lq, hpg, Lk]
+    p = past[:, None] + i
+    mask = (j <= p[..., None]) & valid[..., None]
+    if window:
+        mask &= j > p[..., None] - window
+    w = (w * (1.0 / math.sqrt(case["d"]))).masked_fill_(~mask[:, None, :, None], -math.inf)
+    top = w.amax(-1, keepdim=True)
+    w = w.sub_(torch.where(top > -math.inf, top, 0.0)).exp_()
+    o = (w.flatten(2, 3) @ v).unflatten(2, (-1, hpg)) / w.sum(-1, keepdim=True)
+    s["out"][at[valid]] = o.permute(0, 2, 1, 3, 4).flatten(2, 3)[valid].to(s["out"].dtype)
+    return s["out"]
+
+
+# ------------------------------------------------------------ cost and truth
+
+def _spans(case, s=None):
+    """(rows, first position) of every live sequence."""
+    if "lens" in case:
+        lens = _ints(case["lens"])
+        return list(zip(lens, _ints(case["pasts"]) if "pasts" in case else [0] * len(lens)))
+    n, lo, hi = case["rows"] - case.get("pad", 0), case.get("pos_min", 0), case["pos_max"]
+    if lo == 0 and hi >= 1024:   # positions e^{u log hi} - 1, u in (i + 1/2) / n
+        return [(1, int(math.exp((i + 0.5) / n * math.log(hi))) - 1) for i in range(n)]
+    return [(1, lo + int((i + 0.5) / n * (hi - lo))) for i in range(n)]
+
+
+def work(case):
+    G, d, dv, b, cb = case["groups"], case["d"], case["dv"], _BYTES[case["t"]], _BYTES[case["cache"]]
+    nh, spans = G * case["hpg"], _spans(case)
+    rows = sum(n for n, _ in spans)
+    cached = G * ((d + dv) * cb + 2 * (case["cache"] == E4M3))   # bytes of a position
+    if case["op"] in ("write", "read"):
+        return {"bytes": rows * (G * (d + dv) * b + cached), "flops": rows * G * (d + dv)}
+    # every row's query and output once, every position that some row attends once; the products of the pairs
+    window = case["window"] or 1 << 40
+    pairs = sum(_pairs(p0, n, window) for n, p0 in spans)
+    keys = sum(p0 + n - max(0, p0 - window + 1) for n, p0 in spans if n)
+    return {"bytes": rows * nh * (d + dv) * b + keys * cached, "flops": 2 * pairs * nh * (d + dv)}
+
+
+def _pairs(p0, n, window):
+    full = max(0, min(n, window - 1 - p0))   # rows that attend every position up to their own: p + 1 of them
+    return full * p0 + full * (full + 1) // 2 + (n - full) * window
+
+
+def _e4m3(x):
+    """The nearest e4m3 value (ties to even) of |x| <= 448, in 64 bits."""
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6))) - 3)
+    return torch.round(x / step) * step
+
+
+def exact(case, seed):
+    """The definitions in 64 bits, one sequence after the other."""
+    s = prepare(case, seed)
+    page, G, hpg = case["page"], case["groups"], case["hpg"]
+    if "seqs" in s:
+        seqs = s["seqs"]
+    else:
+        seqs = [(r, 1, i, p) for r, (i, p) in enumerate(zip(s["slots"].tolist(), s["pos"].tolist())) if i >= 0]
+
+    def places(slot, a, b):
+        p = torch.arange(a, b, device="cuda")
+        return s["table"][slot, p // page].long(), p % page
+
+    def value(name, ids, at):
+        x = s[name].view(torch.uint8)[ids, :, at].view(torch.float8_e4m3fn) if name + "_exp" in s else s[name][ids, :, at]
+        x = x.double()
+        return x * torch.exp2(s[name + "_exp"][ids, :, at].double() - 127)[..., None] if name + "_exp" in s else x
+
+    if case["op"] == "write":
+        res = {}
+        for name in "kv":
+            pool = s[name].double()
+            for row0, rows, slot, past in seqs:
+                if not rows:
+                    continue
+                ids, at = places(slot, past, past + rows)
+                x = s[name + "_rows"][row0:row0 + rows].double()
+                if case["cache"] == E4M3:
+                    top = x.abs().amax(-1, keepdim=True)
+                    x = _e4m3(x / torch.exp2(torch.ceil(torch.log2(top.clamp(min=2.0 ** -110) / 448)).clamp(min=-126)))
+                pool[ids, :, at] = x
+            res[name] = pool
+        return {n: res.get(n) for n in _pools(s)}
+    if case["op"] == "read":
+        res = [s["k_rows"].double(), s["v_rows"].double()]
+        for row0, rows, slot, past in seqs:
+            ids, at = places(slot, past, past + rows)
+            for x, name in zip(res, "kv"):
+                x[row0:row0 + rows] = value(name, ids, at)
+        return tuple(res)
+    out = s["out"].double()
+    for row0, rows, slot, past in seqs:
+        for r in range(0, rows, 1024):
+            n = min(1024, rows - r)
+            p = torch.arange(past + r, past + r + n, device="cuda")
+            a = max(0, past + r - case["window"] + 1) if case["window"] else 0
+            ids, at = places(slot, a, past + r + n)
+            j = torch.arange(a, past + r + n, device="cuda")
+            k, v = value("k", ids, at), value("v", ids, at)
+            q = s["q"][row0 + r:row0 + r + n].double().unflatten(1, (G, hpg))
+            sc = torch.einsum("nghd,jgd->ghnj", q, k) / math.sqrt(case["d"])
+            see = (j <= p[:, None]) & ((j > p[:, None] - case["window"]) if case["window"] else True)
+            sc = torch.where(see, sc, -math.inf)
+            w = torch.exp(sc - torch.logsumexp(sc, -1, keepdim=True))
+            out[row0 + r:row0 + r + n] = torch.einsum("ghnj,jgd->nghd", w, v).flatten(1, 2)
+    return out
