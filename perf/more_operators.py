@@ -213,6 +213,11 @@ def _rows_of(s):
     return (row0[:, None] + i)[valid], s["table"][slot.repeat_interleave(rows), p // page].long(), p % page
 
 
+def _pow2(e):
+    """2^e in 32 bits, from its bits: powers and exponentials need not be exact."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
 def _write(s, case):
     row, page, at = _rows_of(s)
     for name in ("k", "v"):
@@ -222,7 +227,7 @@ def _write(s, case):
             m, e = torch.frexp(top)                      # top = m 2^e, m in [1/2, 1); 448 = 0.875 2^9
             e = (torch.where(top > 0, torch.where(m <= 0.875, e - 9, e - 8), -126)).clamp(min=-126)
             s[name + "_exp"][page, :, at] = (e + 127).to(torch.uint8)
-            x = torch.ldexp(x, -e[..., None]).to(torch.float8_e4m3fn)
+            x = (x * _pow2(-e[..., None])).to(torch.float8_e4m3fn)
             s[name].view(torch.uint8)[page, :, at] = x.view(torch.uint8)
         else:
             s[name][page, :, at] = x.to(s[name].dtype)
@@ -234,7 +239,7 @@ def _cached(s, name, page, at):
     if name + "_exp" not in s:
         return s[name][page, :, at].float()
     x = s[name].view(torch.uint8)[page, :, at].view(torch.float8_e4m3fn).float()
-    return torch.ldexp(x, s[name + "_exp"][page, :, at].int()[..., None] - 127)
+    return x * _pow2(s[name + "_exp"][page, :, at].int()[..., None] - 127)
 
 
 def _read(s, case):
@@ -301,9 +306,14 @@ def _pairs(p0, n, window):
     return full * p0 + full * (full + 1) // 2 + (n - full) * window
 
 
+def _two(n):
+    """2^n of whole n, in 64 bits."""
+    return ((n.long() + 1023) << 52).view(torch.float64)
+
+
 def _e4m3(x):
     """The nearest e4m3 value (ties to even) of |x| <= 448, in 64 bits."""
-    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6))) - 3)
+    step = _two(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6))) - 3)
     return torch.round(x / step) * step
 
 
@@ -323,7 +333,7 @@ def exact(case, seed):
     def value(name, ids, at):
         x = s[name].view(torch.uint8)[ids, :, at].view(torch.float8_e4m3fn) if name + "_exp" in s else s[name][ids, :, at]
         x = x.double()
-        return x * torch.exp2(s[name + "_exp"][ids, :, at].double() - 127)[..., None] if name + "_exp" in s else x
+        return x * _two(s[name + "_exp"][ids, :, at].long() - 127)[..., None] if name + "_exp" in s else x
 
     if case["op"] == "write":
         res = {}
@@ -336,7 +346,8 @@ def exact(case, seed):
                 x = s[name + "_rows"][row0:row0 + rows].double()
                 if case["cache"] == E4M3:
                     top = x.abs().amax(-1, keepdim=True)
-                    x = _e4m3(x / torch.exp2(torch.ceil(torch.log2(top.clamp(min=2.0 ** -110) / 448)).clamp(min=-126)))
+                    m, e = torch.frexp(top.clamp(min=2.0 ** -110) / 448)
+                    x = _e4m3(x / _two((e - (m == 0.5).int()).clamp(min=-126)))   # ceil(log2(top / 448))
                 pool[ids, :, at] = x
             res[name] = pool
         return {n: res.get(n) for n in _pools(s)}
