@@ -494,6 +494,135 @@ O1_API int o1_lin_token_attend(float *state, int32_t n_slots, const o1_lin_geom 
  * header to hold them. Synchronises `stream`. */
 O1_API int o1_lin_flags(uint32_t *flags, int32_t clear, void *stream);
 
+/* ------------------------------------------------------------ paged cache
+ * The layers of a hybrid model that are not sealed attend to every key kept
+ * ("cortiq-engine 0.8.77 src/gpu_wgpu/dory.rs", dory_score, dory_soft and
+ * dory_sum: exact attention over the cached rows of a layer). Their cache
+ * grows with the sequences, so it is held in pages that a table assigns, in 16
+ * bits or in 8: written as rows come (o1_pg_write, o1_pg_token_write), attended
+ * by chunks of new rows or by one row of each sequence (o1_pg_chunk_attend,
+ * o1_pg_token_attend), and read back as rows (o1_pg_read), say for o1_spec_commit
+ * to move a sealed layer over them. Row tensors are those of the section
+ * above. The caller owns pages and table; the library keeps nothing. */
+
+/* Element type of a cache of 8 bits: e4m3 values under a power of two a head's
+ * row. A row x of d values is held as x / 2^e, rounded to nearest (ties to
+ * even), with 2^e the smallest power of two for which max |x| <= 448 * 2^e
+ * (e >= -126), and the byte e + 127. The division is exact, so what is held
+ * has one rounding (2^-4 of a value, or 2^-10 * 2^e if that is more). Infinities and NaN are held as NaN and do not count in the max.
+ * Only a cache_dtype. */
+enum { O1_E4M3 = 3 };
+
+/* Geometry of a paged cache and the attention over it. Limits: groups in
+ * [1, 4096], heads_per_group in [1, 16], at most 65535 heads, d and dv in
+ * [8, 256], both % 8 == 0 (O1_E4M3: % 16 == 0), page in {16, 32, 64, 128, 256},
+ * window >= 0, scale finite; cache_dtype O1_E4M3, or O1_F16 for dtype O1_F16 and
+ * O1_BF16 for the others. */
+typedef struct o1_pg_geom {
+    int32_t groups;           /* G: KV groups                                  */
+    int32_t heads_per_group;  /* query heads per group (nh = G * hpg)          */
+    int32_t d, dv;            /* key / query and value width                   */
+    int32_t page;             /* positions of a page                           */
+    int32_t window;           /* positions a row attends, its own included; 0: all */
+    int32_t dtype;            /* O1_F32, O1_BF16, O1_F16: q, k, v and out      */
+    int32_t cache_dtype;      /* O1_BF16, O1_F16, O1_E4M3                      */
+    float scale;              /* score scale, normally 1/sqrt(d)               */
+} o1_pg_geom;
+
+/* A cache (device pointers, 16-byte aligned; this struct is host memory).
+ * Position p of the sequence in slot s is row p % page of page
+ * table[s][p / page]. Limits: n_pages, n_slots, width >= 1, n_pages * G * page
+ * and width * page < 2^31. A table entry outside [0, n_pages) is an absent
+ * page: nothing is written to it or read from it, and its positions are left
+ * out of the attention. Sequences may share pages that no call writes. */
+typedef struct o1_pg_cache {
+    void *k, *v;              /* [n_pages][G][page][d] and [..][dv], cache_dtype */
+    uint8_t *k_exp, *v_exp;   /* [n_pages][G][page], e + 127 (1 to 254); NULL unless O1_E4M3 */
+    const int32_t *table;     /* [n_slots][width]                              */
+    int32_t n_pages, n_slots, width;
+} o1_pg_cache;
+
+/* One sequence of a packed batch (host memory): rows row0 .. row0 + rows - 1 of
+ * the row tensors are positions pos0 .. pos0 + rows - 1 of slot `slot`. */
+typedef struct o1_pg_seq {
+    int32_t row0, rows, slot, pos0;
+} o1_pg_seq;
+
+/* Write rows of keys and values into the cache, rounded to nearest or quantised
+ * on the way. Sequences: host [n_seq], n_seq <= 4096, read during the call; row
+ * ranges in [0, total_rows) and apart, positions in [0, width * page), slots in
+ * [0, n_slots), no position of a slot twice (else O1_ERR_ARG). Rows of no
+ * sequence are not read. Two positions that the table puts in one place (a page
+ * named twice) leave a mixture there.
+ *   k, v  device row tensors [total_rows][G][d], [total_rows][G][dv]
+ * Asynchronous; a launch every 128 sequences. */
+O1_API int o1_pg_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const void *k, int64_t k_stride,
+                       const void *v, int64_t v_stride, const o1_pg_seq *seqs, int32_t n_seq, int32_t total_rows,
+                       void *stream);
+
+/* The same for one row of each of `rows` sequences (a decode step): row r is
+ * position pos[r] (device int64, also o1_head_prep's) of slot slots[r] (device
+ * int32; NULL: slot r). A row whose slot or position is out of range is padding
+ * and written nowhere. Of rows that name the same position of a slot the first
+ * counts (with the slots' look of o1_lin_token_attend). At most 65536 rows. One
+ * launch; asynchronous. */
+O1_API int o1_pg_token_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, const int32_t *slots, const int64_t *pos, int32_t rows,
+                             void *stream);
+
+/* Read cached rows back: row row0 + i of a sequence is what position pos0 + i of
+ * its slot holds, rounded to the row tensors' type (exact for all but e4m3 values
+ * beyond fp16's range). Sequences as for o1_pg_write, except that positions may
+ * be read more than once. Rows of no sequence, and those of absent pages, are
+ * left as they were.
+ *   k, v  device row tensors [total_rows][G][d], [total_rows][G][dv], written
+ * Asynchronous; a launch every 128 sequences. */
+O1_API int o1_pg_read(const o1_pg_geom *geom, const o1_pg_cache *cache, const o1_pg_seq *seqs, int32_t n_seq, void *k,
+                      int64_t k_stride, void *v, int64_t v_stride, int32_t total_rows, void *stream);
+
+/* Bytes of device scratch of the two attend calls for up to `rows` rows (the
+ * partial results of heads whose keys are split over several blocks); it does
+ * not grow with the cache. Host-only; 0 if the geometry is unsupported or rows <
+ * 1. */
+O1_API size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows);
+
+/* Attention of the rows of packed sequences over the cache: the row at position
+ * p of a slot attends its positions max(0, p - window + 1) .. p (window 0: from
+ * 0) on present pages,
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = e^{scale q . k_j},
+ * per query head, with the keys and values of its group. The rows' own keys and
+ * values are in the cache before (o1_pg_write). A row with no position left is 0.
+ *   scratch  device, 256-byte aligned, o1_pg_scratch_bytes(geom, total_rows) at least
+ *   q        device row tensor [total_rows][nh][d]
+ *   seqs     as for o1_pg_read
+ *   out      device row tensor [total_rows][nh][dv]; rows of no sequence are
+ *            left as they were
+ * q and what is attended are finite, and scores below 2^127 in fp32. A
+ * non-finite key or value spoils rows of its own sequence only: from its
+ * position on, and up to 127 before it. Positions that no row of the sequence
+ * attends (past its end, before its window) may hold anything.
+ * Scores, the softmax's maxima and sums and the outputs' sums are fp32. The
+ * products run on the tensor cores with the cached values as they are; of the
+ * other operand, q is exact, and the softmax's weights are rounded to 2^-8 (bf16
+ * rows), 2^-11 (fp16 rows over fp16), 2^-16 (fp16 rows over e4m3) or 2^-24 (fp32
+ * rows) of their value. Calls that
+ * may overlap on the GPU (other streams, captured graphs) need a scratch each.
+ * Asynchronous. */
+O1_API int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
+                              const void *q, int64_t q_stride, const o1_pg_seq *seqs, int32_t n_seq, void *out,
+                              int64_t out_stride, int32_t total_rows, void *stream);
+
+/* The same for one row of each of `rows` sequences (a decode step of a batch):
+ * row r is position pos[r] (device int64) of slot slots[r] (device int32; NULL:
+ * slot r), whatever lengths the arrays hold when it runs, so that a captured
+ * step can be replayed as the sequences grow. A row whose slot or position is
+ * out of range is padding: its output is left as it was. A slot may be named by
+ * several rows (draft rows at successive positions). At most 65536 rows. The
+ * keys of all rows are split evenly over the GPU. Two launches; asynchronous. */
+O1_API int o1_pg_token_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
+                              const void *q, int64_t q_stride, const int32_t *slots, const int64_t *pos, void *out,
+                              int64_t out_stride, int32_t rows, void *stream);
+
 /* A static, human-readable name for a status code. (The pages' geometry
  * gates refuse a shape instead of running it: "cortiq-engine 0.8.82
  * src/gpu_metal/o1c.rs", admits and tok_ok; this library returns

@@ -1,0 +1,500 @@
+// The paged cache: rows of keys and values written into it, quantised on the
+// way, and read back; and the C ABI of the cache and of the attention over it.
+//
+// Bound of both copies: HBM, each value read once and written once. A group of
+// lanes takes a head's row, 8 values a lane, four rows a group of lanes in
+// flight.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "o1_page.cuh"
+
+namespace {
+
+constexpr int CP_THREADS = 256;
+
+struct Vec8 {
+    float x[8];
+};
+__device__ __forceinline__ Vec8 ld8(const float *p) {
+    const float4 a = o1_ld4(p), b = o1_ld4(p + 4);
+    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+template <typename T>
+__device__ __forceinline__ Vec8 ld8_16(const T *p) {
+    const uint4 u = *(const uint4 *)p;
+    const uint2 h[2] = {make_uint2(u.x, u.y), make_uint2(u.z, u.w)};
+    const float4 a = o1_ld4((const T *)&h[0]), b = o1_ld4((const T *)&h[1]);
+    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ Vec8 ld8(const __nv_bfloat16 *p) { return ld8_16(p); }
+__device__ __forceinline__ Vec8 ld8(const __half *p) { return ld8_16(p); }
+// e4m3 codes
+__device__ __forceinline__ Vec8 ld8(const uint8_t *p) {
+    const uint2 u = *(const uint2 *)p;
+    Vec8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t two = (uint16_t)((i < 2 ? u.x : u.y) >> (16 * (i & 1)));
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        const float2 f = __half22float2(*(const __half2 *)&h);
+        r.x[2 * i] = f.x;
+        r.x[2 * i + 1] = f.y;
+    }
+    return r;
+}
+__device__ __forceinline__ void st8(float *p, const Vec8 &v) {
+    o1_st4(p, make_float4(v.x[0], v.x[1], v.x[2], v.x[3]));
+    o1_st4(p + 4, make_float4(v.x[4], v.x[5], v.x[6], v.x[7]));
+}
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 *, float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ uint32_t pack2(__half *, float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+template <typename T>
+__device__ __forceinline__ void st8(T *p, const Vec8 &v) {
+    *(uint4 *)p = make_uint4(pack2(p, v.x[0], v.x[1]), pack2(p, v.x[2], v.x[3]), pack2(p, v.x[4], v.x[5]),
+                             pack2(p, v.x[6], v.x[7]));
+}
+
+// A head's row, LPV lanes of 8 values, as e4m3 codes under a power of two:
+// returns the byte e + 127. With max |x| = 1.m 2^(E - 127) the least e has
+// 1.m 2^(E - 127) <= 1.75 2^8 2^e, so e + 127 = E - 8, one more where 1.m > 1.75
+// (fraction above 0x600000), and at least 1, which also takes rows of zeros and
+// subnormals. The factor 2^-e is a normal number and x 2^-e exact unless it
+// falls below fp32's range, far below e4m3's.
+template <int LPV>
+__device__ __forceinline__ uint32_t quantise8(const Vec8 &v, uint2 &codes) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = fabsf(v.x[i]);
+        top = fmaxf(top, x < INFINITY ? x : 0.f);
+    }
+#pragma unroll
+    for (int m = 1; m < LPV; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    const uint32_t bits = __float_as_uint(top);
+    const int e = max(1, (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+    const float f = __uint_as_float((uint32_t)(254 - e) << 23);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = v.x[2 * i] * f, b = v.x[2 * i + 1] * f;
+        if (!(fabsf(v.x[2 * i]) < INFINITY)) a = NAN;   // infinities would saturate
+        if (!(fabsf(v.x[2 * i + 1]) < INFINITY)) b = NAN;
+        uint16_t two;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+        h[i] = two;
+    }
+    codes = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    return (uint32_t)e;
+}
+
+// A head's row into the cache at `at`; every lane of the group calls it.
+template <typename C, int LPV>
+struct Store {
+    static __device__ __forceinline__ void row(C *at, uint8_t *, const Vec8 &v, int lane, bool on) {
+        if (on) st8(at + 8 * lane, v);
+    }
+};
+template <int LPV>
+struct Store<uint8_t, LPV> {
+    static __device__ __forceinline__ void row(uint8_t *at, uint8_t *exp, const Vec8 &v, int lane, bool on) {
+        uint2 codes;
+        const uint32_t e = quantise8<LPV>(v, codes);
+        if (on) *(uint2 *)(at + 8 * lane) = codes;
+        if (on && lane == 0) *exp = (uint8_t)e;
+    }
+};
+template <typename C>
+__device__ __forceinline__ Vec8 cached8(const C *at, const uint8_t *, int lane) { return ld8(at + 8 * lane); }
+template <>
+__device__ __forceinline__ Vec8 cached8<uint8_t>(const uint8_t *at, const uint8_t *exp, int lane) {
+    Vec8 v = ld8(at + 8 * lane);
+    const float f = pg_scale(*exp);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.x[i] *= f;
+    return v;
+}
+
+// One side (keys or values) of a copy.
+template <typename T, typename C>
+struct Side {
+    T *rows;
+    C *pool;
+    uint8_t *exp;
+    size_t stride;
+    int width;
+};
+template <typename T, typename C>
+__device__ __forceinline__ Side<T, C> side_of(const PgArgs &a, bool keys, bool write) {
+    if (keys) return {(T *)(write ? a.k_in : a.k_out), (C *)a.k, a.ke, a.ks, a.d};
+    return {(T *)(write ? a.v_in : a.v_out), (C *)a.v, a.ve, a.vs, a.dv};
+}
+
+// Rows of the table's sequences to their places or back. Head rows are counted
+// i G + g over the live rows i; a block takes a run of them, a group of LPV
+// lanes every GROUPS-th of the run.
+template <typename T, typename C, int LPV, bool WRITE>
+__device__ __forceinline__ void copy_run(const PgArgs &a, const PgTable &tab, bool keys) {
+    constexpr int GROUPS = CP_THREADS / LPV, U = 4;
+    const Side<T, C> s = side_of<T, C>(a, keys, WRITE);
+    const int lane = threadIdx.x % LPV, grp = threadIdx.x / LPV;
+    const bool on = 8 * lane < s.width;
+    const int64_t all = (int64_t)tab.total * a.G, per = (all + gridDim.x - 1) / gridDim.x;
+    const int64_t run = (per + GROUPS * U - 1) / (GROUPS * U) * (GROUPS * U);
+    const int64_t v0 = run * blockIdx.x, v1 = min(all, v0 + run);
+    if (v0 >= v1) return;
+    int i = (int)((v0 + grp) / a.G), g = (int)(v0 + grp - (int64_t)i * a.G);
+    const int step_i = GROUPS / a.G, step_g = GROUPS - step_i * a.G;
+    int n = 0;
+    for (int hi = tab.n - 1; n < hi;) {   // the last sequence that starts at or before row i
+        const int mid = (n + hi + 1) >> 1;
+        if (tab.s[mid].before <= i) n = mid;
+        else hi = mid - 1;
+    }
+    for (int64_t v = v0; v < v1; v += GROUPS * U) {
+        Vec8 x[U];
+        C *at[U];
+        uint8_t *ex[U];
+        T *row[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            at[u] = nullptr;
+            if (v + grp + GROUPS * u < v1) {
+                while (n + 1 < tab.n && tab.s[n + 1].before <= i) ++n;
+                const int r = i - tab.s[n].before, p = tab.s[n].pos0 + r;
+                const int page = pg_page(a, tab.s[n].slot, p), w = p & ((1 << a.lpage) - 1);
+                row[u] = s.rows + (size_t)(tab.s[n].row0 + r) * s.stride + (size_t)g * s.width;
+                if (page >= 0) {
+                    at[u] = pg_at(s.pool, a, page, g, w, s.width);
+                    if (sizeof(C) == 1) ex[u] = pg_at(s.exp, a, page, g, w, 1);
+                }
+                if (WRITE && on) x[u] = ld8((const T *)row[u] + 8 * lane);
+            }
+            g += step_g;
+            i += step_i;
+            if (g >= a.G) g -= a.G, ++i;
+        }
+        if (WRITE) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!on || !at[u]) x[u] = {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
+                Store<C, LPV>::row(at[u], ex[u], x[u], lane, on && at[u]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (on && at[u]) x[u] = cached8(at[u], ex[u], lane);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (on && at[u]) st8(row[u] + 8 * lane, x[u]);
+        }
+    }
+}
+
+template <typename T, typename C, int LPV, bool WRITE>
+__global__ __launch_bounds__(CP_THREADS) void k_pg_copy(PgArgs a, const __grid_constant__ PgTable tab) {
+    copy_run<T, C, LPV, WRITE>(a, tab, blockIdx.y == 0);
+}
+
+// A decode step's rows, a block a row: the look for an earlier row of the same
+// place, then its head rows.
+template <typename T, typename C, int LPV>
+__device__ __forceinline__ void token_side(const PgArgs &a, const PgRow &pr, int page, bool keys) {
+    constexpr int GROUPS = CP_THREADS / LPV;
+    const Side<T, C> s = side_of<T, C>(a, keys, true);
+    const int lane = threadIdx.x % LPV, grp = threadIdx.x / LPV, w = pr.pos & ((1 << a.lpage) - 1);
+    const bool on = 8 * lane < s.width;
+    for (int g0 = 0; g0 < a.G; g0 += GROUPS) {   // the same number of turns for every lane: shuffles inside
+        const int g = min(g0 + grp, a.G - 1);
+        const bool live = on && g0 + grp < a.G;
+        Vec8 x = {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
+        if (live) x = ld8((const T *)s.rows + (size_t)blockIdx.x * s.stride + (size_t)g * s.width + 8 * lane);
+        Store<C, LPV>::row(pg_at(s.pool, a, page, g, w, s.width), sizeof(C) == 1 ? pg_at(s.exp, a, page, g, w, 1) : nullptr,
+                           x, lane, live);
+    }
+}
+template <typename T, typename C, int LPV>
+__global__ __launch_bounds__(CP_THREADS) void k_pg_token_write(PgArgs a) {
+    const int r = blockIdx.x;
+    const PgRow pr = pg_token_row(a, r);
+    if (pr.slot < 0) return;
+    const int page = pg_page(a, pr.slot, pr.pos);
+    int dup = 0;
+    for (int i = threadIdx.x; i < r; i += CP_THREADS) {
+        const PgRow o = pg_token_row(a, i);
+        dup |= o.slot == pr.slot && o.pos == pr.pos;
+    }
+    if (__syncthreads_or(dup) || page < 0) return;
+    token_side<T, C, LPV>(a, pr, page, true);
+    token_side<T, C, LPV>(a, pr, page, false);
+}
+
+// LPV lanes of 8 values a head's row (a power of two that holds the wider side).
+template <typename T, typename C, bool WRITE, int LPV>
+void copy_launch_l(const PgArgs &a, const PgTable *tab, cudaStream_t st) {
+    if (!tab) {
+        if (WRITE) k_pg_token_write<T, C, LPV><<<a.rows, CP_THREADS, 0, st>>>(a);
+        return;
+    }
+    // at most three blocks an SM and side, fewer where the rows do not fill them
+    const int64_t vecs = (int64_t)tab->total * a.G, turn = CP_THREADS / LPV * 4, want = (vecs + turn - 1) / turn, most = 152 * 3;
+    k_pg_copy<T, C, LPV, WRITE><<<dim3((unsigned)(want < most ? want : most), 2), CP_THREADS, 0, st>>>(a, *tab);
+}
+template <typename T, typename C, bool WRITE>
+void copy_launch_c(const PgArgs &a, const PgTable *tab, cudaStream_t st) {
+    const int w = a.d > a.dv ? a.d : a.dv;
+    if (w <= 64) copy_launch_l<T, C, WRITE, 8>(a, tab, st);
+    else if (w <= 128) copy_launch_l<T, C, WRITE, 16>(a, tab, st);
+    else copy_launch_l<T, C, WRITE, 32>(a, tab, st);
+}
+// tab null: a token batch
+template <bool WRITE>
+void copy_launch(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, cudaStream_t st) {
+    if (dtype == O1_F32 && cache_dtype == O1_BF16) copy_launch_c<float, __nv_bfloat16, WRITE>(a, tab, st);
+    else if (dtype == O1_F32) copy_launch_c<float, uint8_t, WRITE>(a, tab, st);
+    else if (dtype == O1_BF16 && cache_dtype == O1_BF16) copy_launch_c<__nv_bfloat16, __nv_bfloat16, WRITE>(a, tab, st);
+    else if (dtype == O1_BF16) copy_launch_c<__nv_bfloat16, uint8_t, WRITE>(a, tab, st);
+    else if (cache_dtype == O1_F16) copy_launch_c<__half, __half, WRITE>(a, tab, st);
+    else copy_launch_c<__half, uint8_t, WRITE>(a, tab, st);
+}
+
+// ------------------------------------------------------------ host checks
+
+bool pg_geom_ok(const o1_pg_geom *g) {
+    if (!g) return false;
+    if (g->groups < 1 || g->groups > 4096) return false;
+    if (g->heads_per_group < 1 || g->heads_per_group > O1_MAX_HPG) return false;
+    if (g->groups * g->heads_per_group > 65535) return false;
+    const int unit = g->cache_dtype == O1_E4M3 ? 16 : 8;   // 16 bytes of a cached row
+    if (g->d < 8 || g->d > O1_MAX_D || g->d % unit || g->dv < 8 || g->dv > O1_MAX_DV || g->dv % unit) return false;
+    if (g->page < 16 || g->page > 256 || (g->page & (g->page - 1))) return false;
+    if (g->window < 0 || !o1_dtype_ok(g->dtype) || !isfinite(g->scale)) return false;
+    return g->cache_dtype == O1_E4M3 || g->cache_dtype == (g->dtype == O1_F16 ? O1_F16 : O1_BF16);
+}
+
+// The parts of a cache as spans: keys, values, their exponents, the table.
+struct PgSpans {
+    O1Span s[5];
+};
+bool cache_ok(const o1_pg_geom &g, const o1_pg_cache *c, PgSpans &sp) {
+    if (!c || !c->k || !c->v || !c->table) return false;
+    if ((uintptr_t)c->k % 16 || (uintptr_t)c->v % 16 || (uintptr_t)c->k_exp % 16 || (uintptr_t)c->v_exp % 16 ||
+        (uintptr_t)c->table % 16)
+        return false;
+    if (g.cache_dtype == O1_E4M3 && (!c->k_exp || !c->v_exp)) return false;
+    if (c->n_pages < 1 || c->n_slots < 1 || c->width < 1) return false;
+    const int64_t lim = (int64_t)1 << 31;
+    if ((int64_t)c->width * g.page >= lim || (int64_t)g.groups * g.page * c->n_pages >= lim) return false;
+    const size_t rows = (size_t)c->n_pages * g.groups * g.page, e = pg_cache_bytes(g.cache_dtype);
+    const bool q = g.cache_dtype == O1_E4M3;
+    sp = {{o1_span(c->k, rows * g.d * e), o1_span(c->v, rows * g.dv * e), o1_span(q ? c->k_exp : nullptr, rows),
+           o1_span(q ? c->v_exp : nullptr, rows), o1_span(c->table, (size_t)c->n_slots * c->width * 4)}};
+    return true;
+}
+bool meets(const PgSpans &sp, const O1Span &x) {
+    for (const O1Span &s : sp.s)
+        if (o1_spans_overlap(s, x)) return true;
+    return false;
+}
+// Whether the parts that a write touches are apart from each other and the table.
+bool apart(const PgSpans &sp) {
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 5; ++j)
+            if (o1_spans_overlap(sp.s[i], sp.s[j])) return false;
+    return true;
+}
+
+// The sequences of a call: ranges in bounds, rows apart and, for writes,
+// positions of a slot apart. Sorted copies on the stack.
+constexpr int PG_MAX_SEQ = 4096;
+bool seqs_ok(const o1_pg_seq *s, int n, const o1_pg_geom &g, const o1_pg_cache &c, int total_rows, bool write) {
+    struct Range {
+        int64_t key;   // slot 2^32 + first position, or the first row
+        int32_t n;
+    } r[PG_MAX_SEQ];
+    const auto apart = [&](int m) {
+        std::sort(r, r + m, [](const Range &a, const Range &b) { return a.key < b.key; });
+        for (int i = 1; i < m; ++i)
+            if (r[i - 1].key + r[i - 1].n > r[i].key) return false;
+        return true;
+    };
+    const int64_t len = (int64_t)c.width * g.page;
+    int m = 0;
+    for (int i = 0; i < n; ++i) {
+        if (s[i].row0 < 0 || s[i].rows < 0 || s[i].slot < 0 || s[i].slot >= c.n_slots || s[i].pos0 < 0) return false;
+        if ((int64_t)s[i].row0 + s[i].rows > total_rows || (int64_t)s[i].pos0 + s[i].rows > len) return false;
+        if (s[i].rows) r[m++] = {s[i].row0, s[i].rows};
+    }
+    if (!apart(m)) return false;
+    if (!write) return true;
+    m = 0;
+    for (int i = 0; i < n; ++i)
+        if (s[i].rows) r[m++] = {((int64_t)s[i].slot << 32) + s[i].pos0, s[i].rows};
+    return apart(m);
+}
+
+void fill(PgArgs &a, const o1_pg_geom &g, const o1_pg_cache &c) {
+    a = PgArgs();
+    a.k = c.k; a.v = c.v; a.ke = c.k_exp; a.ve = c.v_exp; a.table = c.table;
+    a.n_pages = c.n_pages; a.n_slots = c.n_slots; a.width = c.width;
+    a.G = g.groups; a.hpg = g.heads_per_group; a.d = g.d; a.dv = g.dv; a.window = g.window; a.scale = g.scale;
+    for (a.lpage = 4; 1 << a.lpage < g.page;) ++a.lpage;
+    a.wait_cycles = o1_wait_limit();
+}
+
+// Sequences of some rows in tables of PG_TABLE, counted by `count` of their rows.
+template <typename Count, typename Launch>
+void for_tables(const o1_pg_seq *seqs, int n_seq, Count count, Launch launch) {
+    PgTable t;
+    t.n = t.total = 0;
+    for (int i = 0; i < n_seq; ++i) {
+        if (!seqs[i].rows) continue;
+        const int64_t c = count(seqs[i].rows);
+        if (t.n == PG_TABLE || t.total + c > INT32_MAX) {
+            launch(t);
+            t.n = t.total = 0;
+        }
+        t.s[t.n++] = {seqs[i].row0, seqs[i].rows, seqs[i].slot, seqs[i].pos0, t.total};
+        t.total += (int32_t)c;
+    }
+    if (t.n) launch(t);
+}
+
+int copy_seqs(const o1_pg_geom *geom, const o1_pg_cache *cache, const void *k, int64_t ks, const void *v, int64_t vs,
+              const o1_pg_seq *seqs, int32_t n_seq, int32_t total_rows, bool write, cudaStream_t st) {
+    if (!pg_geom_ok(geom)) return O1_ERR_UNSUPPORTED;
+    const o1_pg_geom &g = *geom;
+    PgSpans sp;
+    if (!cache_ok(g, cache, sp) || (write && !apart(sp))) return O1_ERR_ARG;
+    if (n_seq < 0 || n_seq > PG_MAX_SEQ || total_rows < 0) return O1_ERR_ARG;
+    if (n_seq == 0) return O1_OK;
+    if (!seqs || !seqs_ok(seqs, n_seq, g, *cache, total_rows, write)) return O1_ERR_ARG;
+    if (total_rows == 0) return O1_OK;
+    const O1Span kk = o1_row_span(k, g.dtype, g.groups, g.d, ks, total_rows),
+                 vv = o1_row_span(v, g.dtype, g.groups, g.dv, vs, total_rows);
+    if (!o1_rows_ok(kk) || !o1_rows_ok(vv) || meets(sp, kk) || meets(sp, vv)) return O1_ERR_ARG;
+    if (!write && o1_spans_overlap(kk, vv)) return O1_ERR_ARG;
+    PgArgs a;
+    fill(a, g, *cache);
+    if (write) a.k_in = k, a.v_in = v;
+    else a.k_out = (void *)k, a.v_out = (void *)v;
+    a.ks = (size_t)ks; a.vs = (size_t)vs;
+    for_tables(seqs, n_seq, [](int rows) { return (int64_t)rows; }, [&](const PgTable &t) {
+        if (write) copy_launch<true>(a, g.dtype, g.cache_dtype, &t, st);
+        else copy_launch<false>(a, g.dtype, g.cache_dtype, &t, st);
+    });
+    return cudaGetLastError() == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+}
+
+// Checks of the two attend calls; fills the kernels' arguments.
+int attend_args(PgArgs &a, const o1_pg_geom &g, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
+                const void *q, int64_t qs, void *out, int64_t os, int32_t rows, const O1Span &slots, const O1Span &pos) {
+    PgSpans sp;
+    if (!cache_ok(g, cache, sp)) return O1_ERR_ARG;
+    if (!scratch || (uintptr_t)scratch % 256 || scratch_bytes < o1_pg_scratch_bytes(&g, rows)) return O1_ERR_ARG;
+    const int nh = g.groups * g.heads_per_group;
+    const O1Span o = o1_row_span(out, g.dtype, nh, g.dv, os, rows), x = o1_row_span(q, g.dtype, nh, g.d, qs, rows),
+                 sc = o1_span(scratch, scratch_bytes);
+    if (!o1_rows_ok(o) || !o1_rows_ok(x)) return O1_ERR_ARG;
+    for (const O1Span &w : {o, sc})   // what is written, against everything else
+        if (meets(sp, w) || o1_spans_overlap(w, x) || o1_spans_overlap(w, slots) || o1_spans_overlap(w, pos)) return O1_ERR_ARG;
+    if (o1_spans_overlap(o, sc)) return O1_ERR_ARG;
+    fill(a, g, *cache);
+    a.q = q; a.out = out; a.qs = (size_t)qs; a.os = (size_t)os;
+    a.part = (float *)scratch;
+    return O1_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int o1_pg_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const void *k, int64_t k_stride, const void *v,
+                int64_t v_stride, const o1_pg_seq *seqs, int32_t n_seq, int32_t total_rows, void *stream) {
+    return copy_seqs(geom, cache, k, k_stride, v, v_stride, seqs, n_seq, total_rows, true, (cudaStream_t)stream);
+}
+
+int o1_pg_read(const o1_pg_geom *geom, const o1_pg_cache *cache, const o1_pg_seq *seqs, int32_t n_seq, void *k,
+               int64_t k_stride, void *v, int64_t v_stride, int32_t total_rows, void *stream) {
+    return copy_seqs(geom, cache, k, k_stride, v, v_stride, seqs, n_seq, total_rows, false, (cudaStream_t)stream);
+}
+
+int o1_pg_token_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const int32_t *slots, const int64_t *pos, int32_t rows, void *stream) {
+    if (!pg_geom_ok(geom)) return O1_ERR_UNSUPPORTED;
+    const o1_pg_geom &g = *geom;
+    PgSpans sp;
+    if (!cache_ok(g, cache, sp) || !apart(sp)) return O1_ERR_ARG;
+    if (rows < 0 || rows > 65536 || (uintptr_t)slots % 4 || (uintptr_t)pos % 8) return O1_ERR_ARG;
+    if (rows == 0) return O1_OK;
+    if (!pos || (!slots && rows > cache->n_slots)) return O1_ERR_ARG;
+    const O1Span kk = o1_row_span(k, g.dtype, g.groups, g.d, k_stride, rows),
+                 vv = o1_row_span(v, g.dtype, g.groups, g.dv, v_stride, rows);
+    if (!o1_rows_ok(kk) || !o1_rows_ok(vv)) return O1_ERR_ARG;
+    for (const O1Span &x : {kk, vv, o1_span(slots, (size_t)rows * 4), o1_span(pos, (size_t)rows * 8)})
+        if (meets(sp, x)) return O1_ERR_ARG;
+    PgArgs a;
+    fill(a, g, *cache);
+    a.k_in = k; a.v_in = v;
+    a.ks = (size_t)k_stride; a.vs = (size_t)v_stride;
+    a.slots = slots; a.pos = pos; a.rows = rows;
+    copy_launch<true>(a, g.dtype, g.cache_dtype, nullptr, (cudaStream_t)stream);
+    return cudaGetLastError() == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+}
+
+size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows) {
+    if (!pg_geom_ok(geom) || rows < 1) return 0;
+    return pg_rows_scratch(geom->dv, geom->groups, (int64_t)rows * geom->heads_per_group);
+}
+
+int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
+                       const void *q, int64_t q_stride, const o1_pg_seq *seqs, int32_t n_seq, void *out,
+                       int64_t out_stride, int32_t total_rows, void *stream) {
+    if (!pg_geom_ok(geom)) return O1_ERR_UNSUPPORTED;
+    const o1_pg_geom &g = *geom;
+    PgSpans sp;
+    if (!cache_ok(g, cache, sp)) return O1_ERR_ARG;
+    if (n_seq < 0 || n_seq > PG_MAX_SEQ || total_rows < 0) return O1_ERR_ARG;
+    if (n_seq == 0) return O1_OK;
+    if (!seqs || !seqs_ok(seqs, n_seq, g, *cache, total_rows, false)) return O1_ERR_ARG;
+    if (total_rows == 0) return O1_OK;
+    PgArgs a;
+    const int rc = attend_args(a, g, cache, scratch, scratch_bytes, q, q_stride, out, out_stride, total_rows,
+                               o1_span(nullptr, 0), o1_span(nullptr, 0));
+    if (rc != O1_OK) return rc;
+    bool first = true, ok = true;
+    for_tables(seqs, n_seq, [&](int rows) { return ((int64_t)rows * g.heads_per_group + 15) / 16; }, [&](const PgTable &t) {
+        ok = pg_launch_rows(a, g.dtype, g.cache_dtype, &t, first, (cudaStream_t)stream) == cudaSuccess && ok;
+        first = false;
+    });
+    return ok ? O1_OK : O1_ERR_CUDA;
+}
+
+int o1_pg_token_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
+                       const void *q, int64_t q_stride, const int32_t *slots, const int64_t *pos, void *out,
+                       int64_t out_stride, int32_t rows, void *stream) {
+    if (!pg_geom_ok(geom)) return O1_ERR_UNSUPPORTED;
+    const o1_pg_geom &g = *geom;
+    PgSpans sp;
+    if (!cache_ok(g, cache, sp)) return O1_ERR_ARG;
+    if (rows < 0 || rows > 65536 || (uintptr_t)slots % 4 || (uintptr_t)pos % 8) return O1_ERR_ARG;
+    if (rows == 0) return O1_OK;
+    if (!pos || (!slots && rows > cache->n_slots)) return O1_ERR_ARG;
+    PgArgs a;
+    const int rc = attend_args(a, g, cache, scratch, scratch_bytes, q, q_stride, out, out_stride, rows,
+                               o1_span(slots, (size_t)rows * 4), o1_span(pos, (size_t)rows * 8));
+    if (rc != O1_OK) return rc;
+    a.slots = slots; a.pos = pos; a.rows = rows;
+    return pg_launch_rows(a, g.dtype, g.cache_dtype, nullptr, true, (cudaStream_t)stream) == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+}
+
+}  // extern "C"

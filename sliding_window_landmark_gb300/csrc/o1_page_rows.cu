@@ -1,0 +1,670 @@
+// Attention over the paged cache for few rows a group: decode rows, and chunks
+// of few query vectors. The query heads of a group share its keys, so up to 16
+// query vectors (rows of the sequence times heads of the group) go against each
+// key with one mma.sync m16n8k16: the keys and values are read once, and the
+// bound is HBM.
+//
+// Work. A unit is (16 query vectors, group); its keys are tiles of 64. The
+// tiles of all units, one behind the other, are split evenly over the blocks of
+// one wave, whatever the lengths; a unit cut by such a border leaves partial
+// results (maximum, sum, weighted values), which k_pg_join adds up.
+//
+// A warp takes 16 of a tile's keys and keeps a softmax and an accumulator of
+// its own, so that nothing waits for another warp until the segment's end. Its
+// keys and values come by 16-byte asynchronous copies into a ring of items (16
+// keys, or 16 values); a lane copies exactly the bytes that it will use, so the
+// ring needs no barrier and no swizzle. That works since the order of a
+// contraction is free: the lane that holds key n's contraction indices 2q, 2q+1,
+// 2q + 8, 2q + 9 of every k16 step (q = lane % 4) takes them from 16 consecutive
+// bytes of the row, and the queries are laid out to match; likewise a lane takes
+// 16 consecutive bytes of the value columns, column j of it belonging to the
+// j-th n8 tile.
+#include <math.h>
+
+#include "o1_page.cuh"
+
+namespace {
+
+constexpr int RW = 4, RT = 32 * RW;   // warps and threads of a block
+constexpr int RV = 16;                // query vectors of a unit
+constexpr int TILE = 16 * RW;         // keys of a tile
+constexpr int PER_SM = 2, BLOCKS = 152 * PER_SM;
+
+// Rows of type T over a cache of type C: the MMA's type M, and the terms that q
+// and the weights are split into (a weight in [0, 2^8]): 16-bit rows over their
+// own type need one; bf16 rows over e4m3 one (the codes are bf16 values); fp16
+// rows over e4m3 two (bf16 keeps the range of value times scale); fp32 rows
+// three, which hold fp32.
+template <typename T, typename C>
+struct Types;
+template <>
+struct Types<float, __nv_bfloat16> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 3;
+};
+template <>
+struct Types<float, uint8_t> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 3;
+};
+template <>
+struct Types<__nv_bfloat16, __nv_bfloat16> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 1;
+};
+template <>
+struct Types<__nv_bfloat16, uint8_t> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 1;
+};
+template <>
+struct Types<__half, __half> {
+    using M = __half;
+    static constexpr int TERMS = 1;
+};
+template <>
+struct Types<__half, uint8_t> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 2;
+};
+
+// Sizes for widths of up to 64 N values.
+template <typename C, int N, int TERMS>
+struct Sizes {
+    static constexpr int CB = sizeof(C), VL = 16 / CB;   // values of a lane's 16 bytes
+    static constexpr int KB = N * CB;                    // 64-byte blocks of a key
+    static constexpr int VB = (N * CB + 1) / 2;          // 128-byte blocks of a value row
+    static constexpr int STEPS = N * 4;                  // k16 steps of a key
+    static constexpr int ITEM = (2 * KB > 4 * VB ? 2 * KB : 4 * VB) * 512;
+    // items of a warp's ring: what two blocks an SM hold beside the queries
+    static constexpr int RING = N == 4 ? (CB == 2 ? 3 : 6) : N == 2 && CB == 2 ? 6 : 8;
+};
+
+__device__ __forceinline__ uint32_t pack_m(const __nv_bfloat16 *, float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ uint32_t pack_m(const __half *, float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ float2 unpack_m(const __nv_bfloat16 *, uint32_t w) {
+    return __bfloat1622float2(*(const __nv_bfloat162 *)&w);
+}
+__device__ __forceinline__ float2 unpack_m(const __half *, uint32_t w) { return __half22float2(*(const __half2 *)&w); }
+
+// (a, b) as TERMS packed pairs, the first the nearest, each next the nearest to
+// what is left (the subtractions are exact)
+template <typename M, int TERMS>
+__device__ __forceinline__ void split_m(float a, float b, uint32_t (&w)[TERMS]) {
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+        w[t] = pack_m((const M *)nullptr, a, b);
+        if (t + 1 < TERMS) {
+            const float2 f = unpack_m((const M *)nullptr, w[t]);
+            a -= f.x;
+            b -= f.y;
+        }
+    }
+}
+
+__device__ __forceinline__ void mma16(const __nv_bfloat16 *, float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16(const __half *, float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// two e4m3 codes (low half of w, or its high half) as a bf16 pair: exact
+__device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t w, int half) {
+    const uint16_t two = (uint16_t)(half ? w >> 16 : w);
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    const float2 f = __half22float2(*(const __half2 *)&h);
+    return pack_m((const __nv_bfloat16 *)nullptr, f.x, f.y);
+}
+
+// 16 bytes, or zeros where !on
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
+    const int n = on ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 query vectors of a sequence: vector i is row i / hpg of its rows, head i % hpg.
+struct Unit {
+    int slot;      // -1: padding, no tiles
+    int row0;      // first row of the sequence in the row tensors
+    int pos0;      // its position
+    int vec0, nv;  // first vector, and vectors
+    int lo, hi;    // positions attended by some vector: lo .. hi
+    __device__ __forceinline__ int tiles() const { return slot < 0 ? 0 : (hi / TILE) - (lo / TILE) + 1; }
+};
+__device__ __forceinline__ Unit unit_of(const PgArgs &a, const PgTable &tab, int u) {
+    Unit x;
+    int rows;
+    if (a.pos) {
+        const PgRow r = pg_token_row(a, u);
+        x = {r.slot, u, r.pos, 0, a.hpg, 0, 0};
+    } else {
+        int n = 0;
+        for (int hi = tab.n - 1; n < hi;) {
+            const int mid = (n + hi + 1) >> 1;
+            if (tab.s[mid].before <= u) n = mid;
+            else hi = mid - 1;
+        }
+        rows = tab.s[n].rows;
+        x = {tab.s[n].slot, tab.s[n].row0, tab.s[n].pos0, (u - tab.s[n].before) * RV, 0, 0, 0};
+        x.nv = (int)min((int64_t)RV, (int64_t)rows * a.hpg - x.vec0);
+    }
+    x.hi = x.pos0 + (x.vec0 + x.nv - 1) / a.hpg;
+    x.lo = a.window ? max(0, x.pos0 + x.vec0 / a.hpg - a.window + 1) : 0;
+    return x;
+}
+
+// What a block leaves of the units that its borders cut: the values [RV][dv]
+// and the statistics [RV][2] of its first segment (slot 0) and its last (slot 1),
+// and in its header the units.
+struct Head {
+    int unit;       // of slot 0: the one that a block before began; -1: none
+    int goes_on;    // whether it goes on in the next block
+    int row0, vec0, nv, g;   // that unit's vectors
+};
+struct Scratch {
+    Head *head;
+    float *stat, *val;
+};
+__device__ __forceinline__ Scratch scratch_of(float *p) {
+    return {(Head *)p, p + BLOCKS * 8, p + BLOCKS * 8 + BLOCKS * 2 * RV * 2};
+}
+
+// The row and head of a unit's vector in the row tensors.
+__device__ __forceinline__ size_t vec_at(const PgArgs &a, int row0, int vec, int g, size_t stride, int width) {
+    const int r = vec / a.hpg, h = g * a.hpg + (vec - r * a.hpg);
+    return (size_t)(row0 + r) * stride + (size_t)h * width;
+}
+
+template <typename T, typename C, int N>
+__global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_constant__ PgTable tab, int units) {
+    using Ty = Types<T, C>;
+    using M = typename Ty::M;
+    constexpr int TERMS = Ty::TERMS;
+    using Z = Sizes<C, N, TERMS>;
+    constexpr int CB = Z::CB, VL = Z::VL, KB = Z::KB, VB = Z::VB, STEPS = Z::STEPS, RING = Z::RING, ITEM = Z::ITEM;
+    constexpr bool E4 = CB == 1;
+    extern __shared__ __align__(16) unsigned char sm[];
+    __shared__ long long s_sum[RW];
+    __shared__ long long s_from;
+    __shared__ int s_unit;
+    __shared__ float s_m[RW][RV], s_l[RW][RV];
+    __shared__ __align__(16) uint8_t s_exp[E4 ? RW * RING * 16 : 16];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qd = lane & 3, row = lane >> 2;
+    unsigned char *ring = sm + (size_t)warp * RING * ITEM;
+    uint32_t *sq = (uint32_t *)(sm + (size_t)RW * RING * ITEM);   // [term][step][lane][4]
+    const C *pk = (const C *)a.k, *pv = (const C *)a.v;
+
+    // ---- this block's share of the tiles
+    int64_t total, from, to;
+    {
+        const int per = (units + RT - 1) / RT, u0 = min(units, tid * per), u1 = min(units, u0 + per);
+        long long own = 0;
+        for (int u = u0; u < u1; ++u) own += unit_of(a, tab, u).tiles();
+        long long before = own;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, before, m);
+            if (lane >= m) before += o;
+        }
+        if (lane == 31) s_sum[warp] = before;
+        __syncthreads();
+        total = 0;
+        long long base = 0;
+        for (int w = 0; w < RW; ++w) {
+            if (w < warp) base += s_sum[w];
+            total += s_sum[w];
+        }
+        total *= a.G;
+        // blocks that get a tile at least (a block without one inside a unit
+        // would break the chain of its partial results)
+        const int64_t nblk = min((int64_t)gridDim.x, total);
+        from = blockIdx.x < nblk ? total * blockIdx.x / nblk : 0;
+        to = blockIdx.x < nblk ? total * (blockIdx.x + 1) / nblk : 0;
+        before = (base + before - own) * a.G;   // tiles before this thread's units
+        if (from < to && from >= before && from < before + own * a.G) {
+            int u = u0;
+            for (; u + 1 < u1; ++u) {
+                const int64_t n = (int64_t)unit_of(a, tab, u).tiles() * a.G;
+                if (from < before + n) break;
+                before += n;
+            }
+            s_unit = u;
+            s_from = from - before;
+        }
+        __syncthreads();
+    }
+    const Scratch sc = scratch_of(a.part);
+    if (tid == 0) sc.head[blockIdx.x].unit = -1;
+    if (from >= to) return;
+
+    const float sc2 = a.scale * 1.4426950408889634f;
+    int u = s_unit;
+    int64_t left = to - from, skip = s_from;   // tiles to go, and those before the first in its unit's groups
+    bool first_seg = true;
+    while (left > 0 && u < units) {
+        const Unit x = unit_of(a, tab, u);
+        const int nt = x.tiles();
+        if (nt == 0) {
+            ++u;
+            continue;
+        }
+        const int g = (int)(skip / nt), t0 = (int)(skip - (int64_t)g * nt);
+        const int t1 = (int)min((int64_t)nt, t0 + left);
+        left -= t1 - t0;
+        // ---- queries, in the MMA's A layout of this lane order
+        __syncthreads();   // the segment before is done with shared memory
+        const int kb_n = (a.d * CB + 63) >> 6, vb_n = (a.dv * CB + 127) >> 7;
+        for (int i = tid; i < kb_n * (VL / 4) * 32; i += RT) {
+            const int st = i >> 5, ln = i & 31, b = st / (VL / 4), s = st - b * (VL / 4);
+            const int c = 4 * VL * b + VL * (ln & 3) + 4 * s;   // 4 consecutive values: k indices 2q, 2q + 1, 2q + 8, 2q + 9
+            uint32_t w[4][TERMS];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int v = (ln >> 2) + 8 * h;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (v < x.nv && c < a.d) f = o1_ld4((const T *)a.q + vec_at(a, x.row0, x.vec0 + v, g, a.qs, a.d) + c);
+                split_m<M, TERMS>(f.x, f.y, w[h]);
+                split_m<M, TERMS>(f.z, f.w, w[2 + h]);
+            }
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) *(uint4 *)(sq + ((t * STEPS + st) * 32 + ln) * 4) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
+        }
+        __syncthreads();
+
+        // ---- this warp's blocks of 16 keys: blk0, blk0 + RW, ...
+        const int blk0 = (x.lo / TILE + t0) * RW + warp, nb = t1 - t0;
+        int pos[2], low[2];   // of this lane's two vectors: last and first position attended
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            pos[h] = x.pos0 + (x.vec0 + min(row + 8 * h, x.nv - 1)) / a.hpg;   // past the last: zeros, not written
+            low[h] = a.window ? pos[h] - a.window + 1 : 0;
+        }
+        const int plain_lo = a.window ? max(0, x.hi - a.window + 1) : 0, plain_hi = x.pos0 + x.vec0 / a.hpg;
+        float acc[VB * VL][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < VB * VL; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        // pages of the next 32 blocks, a lane each, and of the 32 after them
+        auto page_of = [&](int i) {
+            const int p = (blk0 + RW * i) * 16;
+            return i < nb && p <= x.hi ? pg_page(a, x.slot, p) : -1;
+        };
+        int pages = page_of(lane), pages_next = page_of(32 + lane);
+        uint32_t present = 0;   // bit i % 32: block i has a page
+        int put = 0, put_slot = 0, get_slot = 0;   // next item to issue: block put / 2, keys then values
+        auto issue = [&]() {
+            const int i = put >> 1;
+            if (i < nb) {
+                const int p0 = (blk0 + RW * i) * 16;
+                const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+                unsigned char *dst = ring + put_slot * ITEM + 16 * lane;
+                const int in = p0 & ((1 << a.lpage) - 1);
+                if (!(put & 1)) {
+                    present = (present & ~(1u << (i & 31))) | (page >= 0 ? 1u : 0u) << (i & 31);
+                    const C *src = pg_at(pk, a, max(page, 0), g, in, a.d);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int key = 8 * n + row;
+                        const bool in_range = page >= 0 && p0 + key >= x.lo && p0 + key <= x.hi;
+#pragma unroll
+                        for (int b = 0; b < KB; ++b)
+                            if (b < kb_n) {
+                                const int c = 4 * VL * b + VL * qd;
+                                const bool on = in_range && c < a.d;
+                                copy16(dst + (n * KB + b) * 512, on ? src + (size_t)key * a.d + c : pk, on);
+                            }
+                    }
+                } else {
+                    const C *src = pg_at(pv, a, max(page, 0), g, in, a.dv);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int key = 2 * qd + (r & 1) + 8 * (r >> 1);
+                        const bool in_range = page >= 0 && p0 + key >= x.lo && p0 + key <= x.hi;
+#pragma unroll
+                        for (int b = 0; b < VB; ++b)
+                            if (b < vb_n) {
+                                const int c = 8 * VL * b + VL * row;
+                                const bool on = in_range && c < a.dv;
+                                copy16(dst + (b * 4 + r) * 512, on ? src + (size_t)key * a.dv + c : pv, on);
+                            }
+                    }
+                }
+                if (E4 && lane == 0) {
+                    const uint8_t *e = put & 1 ? a.ve : a.ke;
+                    copy16(&s_exp[(warp * RING + put_slot) * 16], page >= 0 ? pg_at(e, a, page, g, in, 1) : e, page >= 0);
+                }
+                if ((put & 1) && (i & 31) == 31) {
+                    pages = pages_next;
+                    pages_next = page_of(i + 33 + lane);
+                }
+            }
+            copy_commit();
+            ++put;
+            put_slot = put_slot + 1 == RING ? 0 : put_slot + 1;
+        };
+        // the item to use next: all but the last RING - 1 groups are here (for
+        // the exponents, which one lane copied, at every lane)
+        auto item = [&]() -> const unsigned char * {
+            copy_wait<RING - 1>();
+            if (E4) __syncwarp();
+            return ring + get_slot * ITEM + 16 * lane;
+        };
+        auto done = [&]() {
+            if (E4) __syncwarp();
+            get_slot = get_slot + 1 == RING ? 0 : get_slot + 1;
+        };
+#pragma unroll 1
+        for (int i = 0; i < RING - 1; ++i) issue();
+#pragma unroll 1
+        for (int i = 0; i < nb; ++i) {
+            issue();
+            const unsigned char *it = item();
+            // ---- scores
+            // the lower terms of q in a sum of their own: the MMA truncates at each
+            // accumulation, and three times as many of the full sum showed (d = 256:
+            // fp32 outputs 1.2e-6 off in the 2-norm)
+            float s[2][4] = {}, low_s[2][4] = {};
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+                if (b < kb_n) {
+                    uint4 kw[2];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) kw[n] = *(const uint4 *)(it + (n * KB + b) * 512);
+#pragma unroll
+                    for (int st = 0; st < VL / 4; ++st) {
+                        uint32_t b0[2], b1[2];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            if (E4) {
+                                const uint32_t w = st == 0 ? kw[n].x : st == 1 ? kw[n].y : st == 2 ? kw[n].z : kw[n].w;
+                                b0[n] = bf16_of_e4m3(w, 0);
+                                b1[n] = bf16_of_e4m3(w, 1);
+                            } else {
+                                b0[n] = st == 0 ? kw[n].x : kw[n].z;
+                                b1[n] = st == 0 ? kw[n].y : kw[n].w;
+                            }
+                        }
+#pragma unroll
+                        for (int t = TERMS - 1; t >= 0; --t) {
+                            const uint4 qa = *(const uint4 *)(sq + ((t * STEPS + b * (VL / 4) + st) * 32 + lane) * 4);
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) mma16((const M *)nullptr, t ? low_s[n] : s[n], qa, b0[n], b1[n]);
+                        }
+                    }
+                }
+            const int p0 = (blk0 + RW * i) * 16;
+            const uint8_t *ek = &s_exp[(warp * RING + get_slot) * 16];
+            float f[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) f[n][c] = E4 ? sc2 * pg_scale(ek[8 * n + 2 * qd + c]) : sc2;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[n][j] = (TERMS > 1 ? s[n][j] + low_s[n][j] : s[n][j]) * f[n][j & 1];
+            const bool there = present >> (i & 31) & 1;
+            if (!(there && p0 >= plain_lo && p0 + 15 <= plain_hi)) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int p = p0 + 8 * n + 2 * qd + (j & 1);
+                        if (!there || p > pos[j >> 1] || p < low[j >> 1]) s[n][j] = -INFINITY;
+                    }
+            }
+            done();
+            issue();
+            // ---- softmax: a reference within 2^8 of the running maximum
+            float top[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+            }
+            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float mn = fmaxf(m[h], top[h]), r = m[h] > -INFINITY ? ex2(m[h] - mn) : 0.f;
+                    m[h] = mn;
+                    l[h] *= r;
+#pragma unroll
+                    for (int j = 0; j < VB * VL; ++j) {
+                        acc[j][2 * h] *= r;
+                        acc[j][2 * h + 1] *= r;
+                    }
+                }
+            }
+            const float ref[2] = {m[0] > -INFINITY ? m[0] : 0.f, m[1] > -INFINITY ? m[1] : 0.f};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[n][j] = ex2(s[n][j] - ref[j >> 1]);
+                    l[j >> 1] += s[n][j];
+                }
+            // ---- weighted values
+            it = item();
+            if (E4) {
+                const uint8_t *ev = &s_exp[(warp * RING + get_slot) * 16];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[n][j] = s[n][j] > 0.f ? s[n][j] * pg_scale(ev[8 * n + 2 * qd + (j & 1)]) : 0.f;   // a masked position's byte may be any
+            }
+            uint32_t w[4][TERMS];
+            split_m<M, TERMS>(s[0][0], s[0][1], w[0]);
+            split_m<M, TERMS>(s[0][2], s[0][3], w[1]);
+            split_m<M, TERMS>(s[1][0], s[1][1], w[2]);
+            split_m<M, TERMS>(s[1][2], s[1][3], w[3]);
+#pragma unroll
+            for (int b = 0; b < VB; ++b)
+                if (b < vb_n) {
+                    uint32_t vw[4][4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) *(uint4 *)vw[r] = *(const uint4 *)(it + (b * 4 + r) * 512);
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; ++j4) {
+                        uint32_t b0[VL / 4], b1[VL / 4];   // of the columns in word j4
+                        if (E4) {
+                            const uint32_t lo = __byte_perm(vw[0][j4], vw[1][j4], 0x5140), hi = __byte_perm(vw[0][j4], vw[1][j4], 0x7362);
+                            const uint32_t lo8 = __byte_perm(vw[2][j4], vw[3][j4], 0x5140), hi8 = __byte_perm(vw[2][j4], vw[3][j4], 0x7362);
+#pragma unroll
+                            for (int c = 0; c < VL / 4; ++c) {
+                                b0[c] = bf16_of_e4m3(c < 2 ? lo : hi, c & 1);
+                                b1[c] = bf16_of_e4m3(c < 2 ? lo8 : hi8, c & 1);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < VL / 4; ++c) {
+                                b0[c] = __byte_perm(vw[0][j4], vw[1][j4], c ? 0x7632 : 0x5410);
+                                b1[c] = __byte_perm(vw[2][j4], vw[3][j4], c ? 0x7632 : 0x5410);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < VL / 4; ++c) {
+                            float (&o)[4] = acc[b * VL + j4 * (VL / 4) + c];
+                            if (TERMS == 3) {
+                                // a sum of its own, added with rounding: the MMA's own accumulation truncates
+                                // each time, the same way, which over a long cache adds up
+                                float y[4] = {};
+#pragma unroll
+                                for (int t = TERMS - 1; t >= 0; --t)
+                                    mma16((const M *)nullptr, y, make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]), b0[c], b1[c]);
+#pragma unroll
+                                for (int i2 = 0; i2 < 4; ++i2) o[i2] += y[i2];
+                            } else {
+#pragma unroll
+                                for (int t = TERMS - 1; t >= 0; --t)
+                                    mma16((const M *)nullptr, o, make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]), b0[c], b1[c]);
+                            }
+                        }
+                    }
+                }
+            done();
+        }
+        copy_wait<0>();
+
+        // ---- the four warps' results under one reference
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            if (qd == 0) s_m[warp][row + 8 * h] = m[h], s_l[warp][row + 8 * h] = l[h];
+        }
+        __syncthreads();
+        float big[2], fac[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            big[h] = -INFINITY;
+            for (int w = 0; w < RW; ++w) big[h] = fmaxf(big[h], s_m[w][row + 8 * h]);
+            fac[h] = m[h] > -INFINITY ? ex2(m[h] - big[h]) : 0.f;
+        }
+        const int ld = a.dv + 4;
+        float *so = (float *)ring;   // [RV][ld]: within this warp's ring
+#pragma unroll
+        for (int b = 0; b < VB; ++b)
+            if (b < vb_n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {   // C column 2 qd + (j & 1) of vector row + 8 (j / 2)
+                    const int c0 = 8 * VL * b + VL * (2 * qd + (j & 1));
+                    if (c0 >= a.dv) continue;
+#pragma unroll
+                    for (int i = 0; i < VL; i += 4)
+                        *(float4 *)(so + (row + 8 * (j >> 1)) * ld + c0 + i) =
+                            make_float4(acc[b * VL + i][j] * fac[j >> 1], acc[b * VL + i + 1][j] * fac[j >> 1],
+                                        acc[b * VL + i + 2][j] * fac[j >> 1], acc[b * VL + i + 3][j] * fac[j >> 1]);
+                }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == nt;
+        // a segment that begins inside its unit is the block's first (slot 0),
+        // one that ends inside its unit the block's last (slot 1 if it begins it)
+        const int slot = t0 > 0 ? 0 : 1;
+        const size_t ps = (size_t)blockIdx.x * 2 + slot;
+        for (int i = tid; i < x.nv * (a.dv >> 2); i += RT) {
+            const int v = i / (a.dv >> 2), c = 4 * (i - v * (a.dv >> 2));
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f, mx = -INFINITY;
+            for (int w = 0; w < RW; ++w) mx = fmaxf(mx, s_m[w][v]);
+            for (int w = 0; w < RW; ++w) {
+                const float4 y = *(const float4 *)((const float *)(sm + (size_t)w * RING * ITEM) + v * ld + c);
+                o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+                sum += s_m[w][v] > -INFINITY ? s_l[w][v] * ex2(s_m[w][v] - mx) : 0.f;
+            }
+            if (whole) {
+                const float r = sum > 0.f ? 1.f / sum : 0.f;
+                o1_st4((T *)a.out + vec_at(a, x.row0, x.vec0 + v, g, a.os, a.dv) + c, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+            } else {
+                *(float4 *)(sc.val + (ps * RV + v) * a.dv + c) = o;
+                if (c == 0) *(float2 *)(sc.stat + (ps * RV + v) * 2) = make_float2(mx, sum);
+            }
+        }
+        if (tid == 0 && first_seg && t0 > 0) sc.head[blockIdx.x] = {u * a.G + g, t1 < nt, x.row0, x.vec0, x.nv, g};
+        first_seg = false;
+        skip = 0;
+        if (t1 == nt && g + 1 < a.G) skip = (int64_t)(g + 1) * nt;
+        else if (t1 == nt) ++u;
+    }
+}
+
+// The partial results of a unit that borders cut, added up by the block of the
+// first border inside it: (border, slice of vectors).
+template <typename T>
+__global__ __launch_bounds__(128) void k_pg_join(PgArgs a, int blocks) {
+    o1_chain_wait();
+    const int c = blockIdx.x + 1;
+    const Scratch sc = scratch_of(a.part);
+    const Head h = sc.head[c];
+    if (h.unit < 0 || (int)blockIdx.y >= h.nv) return;
+    if (sc.head[c - 1].unit == h.unit && sc.head[c - 1].goes_on) return;   // the border before is in it too
+    int last = c;
+    while (sc.head[last].goes_on) ++last;
+    const int v = blockIdx.y;
+    auto at = [&](int i) { return (size_t)(i == c - 1 ? 2 * i + 1 : 2 * i) * RV + v; };
+    float mx = -INFINITY;
+    for (int i = c - 1; i <= last; ++i) mx = fmaxf(mx, sc.stat[at(i) * 2]);
+    for (int col = 4 * threadIdx.x; col < a.dv; col += 4 * 128) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int i = c - 1; i <= last; ++i) {
+            const float2 st = *(const float2 *)(sc.stat + at(i) * 2);
+            const float f = st.x > -INFINITY ? ex2(st.x - mx) : 0.f;
+            const float4 y = *(const float4 *)(sc.val + at(i) * a.dv + col);
+            sum = fmaf(f, st.y, sum);
+            o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+        }
+        const float r = sum > 0.f ? 1.f / sum : 0.f;
+        o1_st4((T *)a.out + vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + col, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+    }
+}
+
+template <typename T, typename C, int N>
+cudaError_t rows_launch_n(const PgArgs &a, const PgTable *tab, int units, cudaStream_t st) {
+    constexpr int TERMS = Types<T, C>::TERMS;
+    using Z = Sizes<C, N, TERMS>;
+    const size_t smem = (size_t)RW * Z::RING * Z::ITEM + (size_t)TERMS * Z::STEPS * 512;
+    static_assert((size_t)Z::RING * Z::ITEM >= RV * (64 * N + 4) * 4, "a warp's results in its ring");
+    static_assert(sizeof(Head) <= 32, "headers of 8 words");
+    static unsigned long long done = 0;
+    unsigned long long bit = 0;
+    auto *k = k_pg_rows<T, C, N>;
+    if (o1_attrs_needed(&done, &bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        o1_attrs_done(&done, bit);
+    }
+    PgTable none;
+    none.n = 0;
+    k<<<BLOCKS, RT, smem, st>>>(a, tab ? *tab : none, units);
+    const int nv = tab ? RV : a.hpg;
+    o1_launch_chained(true, k_pg_join<T>, dim3(BLOCKS - 1, nv), dim3(128), 0, st, a, BLOCKS);
+    return cudaGetLastError();
+}
+template <typename T, typename C>
+cudaError_t rows_launch_c(const PgArgs &a, const PgTable *tab, int units, cudaStream_t st) {
+    const int w = a.d > a.dv ? a.d : a.dv;
+    if (w <= 64) return rows_launch_n<T, C, 1>(a, tab, units, st);
+    if (w <= 128) return rows_launch_n<T, C, 2>(a, tab, units, st);
+    return rows_launch_n<T, C, 4>(a, tab, units, st);
+}
+
+}  // namespace
+
+size_t pg_rows_scratch(int dv, int, int64_t) {
+    return o1_al256(((size_t)BLOCKS * 8 + (size_t)BLOCKS * 2 * RV * (2 + dv)) * 4);
+}
+
+cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, bool, cudaStream_t st) {
+    const int units = tab ? tab->total : a.rows;
+    if (dtype == O1_F32 && cache_dtype == O1_BF16) return rows_launch_c<float, __nv_bfloat16>(a, tab, units, st);
+    if (dtype == O1_F32) return rows_launch_c<float, uint8_t>(a, tab, units, st);
+    if (dtype == O1_BF16 && cache_dtype == O1_BF16) return rows_launch_c<__nv_bfloat16, __nv_bfloat16>(a, tab, units, st);
+    if (dtype == O1_BF16) return rows_launch_c<__nv_bfloat16, uint8_t>(a, tab, units, st);
+    if (cache_dtype == O1_F16) return rows_launch_c<__half, __half>(a, tab, units, st);
+    return rows_launch_c<__half, uint8_t>(a, tab, units, st);
+}

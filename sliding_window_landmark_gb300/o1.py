@@ -68,9 +68,33 @@ class o1_lin_seq(ctypes.Structure):
     _fields_ = [("row0", ctypes.c_int32), ("rows", ctypes.c_int32), ("slot", ctypes.c_int32)]
 
 
+class o1_pg_geom(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("heads_per_group", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("page", ctypes.c_int32), ("window", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    @property
+    def nh(self) -> int:
+        return self.groups * self.heads_per_group
+
+
+class o1_pg_cache(ctypes.Structure):
+    """Pointers of a paged cache; ``pg_cache`` makes one of tensors, which it
+    keeps alive and whose device it remembers."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("width", ctypes.c_int32)]
+
+
+class o1_pg_seq(ctypes.Structure):
+    _fields_ = [("row0", ctypes.c_int32), ("rows", ctypes.c_int32), ("slot", ctypes.c_int32), ("pos0", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _G = ctypes.POINTER(o1_geom)
 _LG = ctypes.POINTER(o1_lin_geom)
+_PG = ctypes.POINTER(o1_pg_geom)
+_PC = ctypes.POINTER(o1_pg_cache)
 
 
 def _load(path: str | None = None):
@@ -127,6 +151,19 @@ def _load(path: str | None = None):
     lib.o1_lin_token_attend.restype = ctypes.c_int
     lib.o1_lin_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, _VP]
     lib.o1_lin_flags.restype = ctypes.c_int
+    ps = ctypes.POINTER(o1_pg_seq)
+    lib.o1_pg_write.argtypes = [_PG, _PC, _VP, i64, _VP, i64, ps, i32, i32, _VP]
+    lib.o1_pg_write.restype = ctypes.c_int
+    lib.o1_pg_token_write.argtypes = [_PG, _PC, _VP, i64, _VP, i64, _VP, _VP, i32, _VP]
+    lib.o1_pg_token_write.restype = ctypes.c_int
+    lib.o1_pg_read.argtypes = [_PG, _PC, ps, i32, _VP, i64, _VP, i64, i32, _VP]
+    lib.o1_pg_read.restype = ctypes.c_int
+    lib.o1_pg_scratch_bytes.argtypes = [_PG, i32]
+    lib.o1_pg_scratch_bytes.restype = sz
+    lib.o1_pg_chunk_attend.argtypes = [_PG, _PC, _VP, sz, _VP, i64, ps, i32, _VP, i64, i32, _VP]
+    lib.o1_pg_chunk_attend.restype = ctypes.c_int
+    lib.o1_pg_token_attend.argtypes = [_PG, _PC, _VP, sz, _VP, i64, _VP, _VP, _VP, i64, i32, _VP]
+    lib.o1_pg_token_attend.restype = ctypes.c_int
     lib.o1_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.o1_set_wait_limit.restype = ctypes.c_int
     return lib
@@ -502,6 +539,128 @@ def o1_lin_flags(clear: bool = False, stream=None) -> int:
     f = ctypes.c_uint32(0)
     check(LIB.o1_lin_flags(ctypes.byref(f), int(bool(clear)), _stream(stream)), "flags")
     return int(f.value)
+
+
+# Element types of a paged cache (O1_E4M3 in include/o1.h beside the row types).
+CACHE_DTYPES = {torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3}
+_CACHE_TYPES = {n: t for t, n in CACHE_DTYPES.items()}
+
+
+def pg_geom(groups: int, heads_per_group: int, d: int, dv: int, page: int = 64, dtype=torch.float32, cache_dtype=None,
+            window: int = 0, scale: float | None = None) -> o1_pg_geom:
+    """An o1_pg_geom (cache_dtype defaults to dtype, bf16 for f32; scale to
+    1/sqrt(d), rounded to f32)."""
+    if cache_dtype is None:
+        cache_dtype = torch.bfloat16 if dtype is torch.float32 else dtype
+    return o1_pg_geom(groups, heads_per_group, d, dv, page, _count(window, "window"), DTYPES[dtype], CACHE_DTYPES[cache_dtype],
+                      float(1.0 / d ** 0.5 if scale is None else scale))
+
+
+def pg_cache(g: o1_pg_geom, k, v, table, k_exp=None, v_exp=None) -> o1_pg_cache:
+    """An o1_pg_cache over tensors on one CUDA device: k [pages, groups, page, d]
+    and v [.., dv] of the geometry's cache type, table [slots, width] int32, and
+    for e4m3 k_exp and v_exp [pages, groups, page] uint8."""
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4:
+        raise TypeError("k: expected a CUDA tensor [pages, groups, page, d]")
+    dev, n, G, page = k.get_device(), k.shape[0], g.groups, g.page
+    ct = _CACHE_TYPES[g.cache_dtype]
+    parts = [("k", k, (n, G, page, g.d), ct), ("v", v, (n, G, page, g.dv), ct)]
+    if ct is torch.float8_e4m3fn:
+        parts += [("k_exp", k_exp, (n, G, page), torch.uint8), ("v_exp", v_exp, (n, G, page), torch.uint8)]
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("k_exp, v_exp: only for an e4m3 cache")
+    for name, t, shape, dt in parts + [("table", table, None, torch.int32)]:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.dtype is not dt:
+            raise TypeError(f"{name}: expected {dt}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on device {t.get_device()}, k is on {dev}")
+        if (t.dim() != 2 if shape is None else t.shape != shape) or not t.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous {'[slots, width]' if shape is None else list(shape)} tensor")
+    c = o1_pg_cache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if k_exp is not None else None,
+                    v_exp.data_ptr() if v_exp is not None else None, table.data_ptr(), _count(n, "pages"),
+                    _count(table.shape[0], "slots"), _count(table.shape[1], "width"))
+    c.device, c.tensors, c.made_for = dev, (k, v, k_exp, v_exp, table), (G, g.d, g.dv, page, g.cache_dtype)
+    return c
+
+
+def pg_seqs(seqs):
+    """(row0, rows, slot, pos0) quadruples as the array the o1_pg calls take."""
+    flat = array.array("i", [int(x) for row0, rows, slot, pos0 in seqs for x in (row0, rows, slot, pos0)])
+    return (o1_pg_seq * len(seqs)).from_buffer(flat) if flat else (o1_pg_seq * 0)()
+
+
+def _pg_args(g: o1_pg_geom, cache: o1_pg_cache):
+    """The current device and the C arguments of a geometry and its cache."""
+    dev = torch.cuda.current_device()
+    if cache.device != dev:
+        raise ValueError(f"cache: on device {cache.device}, the current device is {dev}")
+    if cache.made_for != (g.groups, g.d, g.dv, g.page, g.cache_dtype):
+        raise ValueError("cache: made for another geometry")
+    return dev, (ctypes.byref(g), ctypes.byref(cache))
+
+
+def _pg_kv(g: o1_pg_geom, k, v, dev: int):
+    rows, dt = _count(k.shape[0], "rows"), _TYPES[g.dtype]
+    return (*_rows(k, g.groups, g.d, dt, rows, "k", dev), *_rows(v, g.groups, g.dv, dt, rows, "v", dev)), rows
+
+
+def o1_pg_write(g: o1_pg_geom, cache: o1_pg_cache, k, v, seqs, stream=None) -> int:
+    """Rows of k [rows, groups, d] and v [rows, groups, dv] into the cache;
+    ``seqs``: (row0, rows, slot, pos0) or what ``pg_seqs`` made of them."""
+    if not isinstance(seqs, ctypes.Array):
+        seqs = pg_seqs(seqs)
+    dev, head = _pg_args(g, cache)
+    kv, rows = _pg_kv(g, k, v, dev)
+    return LIB.o1_pg_write(*head, *kv, seqs, len(seqs), rows, _raw_stream(stream, dev))
+
+
+def o1_pg_token_write(g: o1_pg_geom, cache: o1_pg_cache, k, v, slots, pos, stream=None) -> int:
+    """Row r of k and v at position pos[r] (int64 tensor) of slot slots[r] (int32
+    tensor; None: slot r); out of range: padding."""
+    dev, head = _pg_args(g, cache)
+    kv, rows = _pg_kv(g, k, v, dev)
+    return LIB.o1_pg_token_write(*head, *kv, _flat(slots, rows, torch.int32, "slots", dev),
+                                 _flat(pos, rows, torch.int64, "pos", dev), rows, _raw_stream(stream, dev))
+
+
+def o1_pg_read(g: o1_pg_geom, cache: o1_pg_cache, seqs, k, v, stream=None) -> int:
+    """Cached rows of sequences into k [rows, groups, d] and v [rows, groups, dv]."""
+    if not isinstance(seqs, ctypes.Array):
+        seqs = pg_seqs(seqs)
+    dev, head = _pg_args(g, cache)
+    kv, rows = _pg_kv(g, k, v, dev)
+    return LIB.o1_pg_read(*head, seqs, len(seqs), *kv, rows, _raw_stream(stream, dev))
+
+
+def o1_pg_scratch_bytes(g: o1_pg_geom, rows: int) -> int:
+    return int(LIB.o1_pg_scratch_bytes(ctypes.byref(g), _count(rows, "rows")))
+
+
+def _pg_attend(g: o1_pg_geom, scratch, q, out, dev: int):
+    rows, dt = _count(q.shape[0], "rows"), _TYPES[g.dtype]
+    return ((_flat(scratch, 1, scratch.dtype, "scratch", dev), scratch.nbytes, *_rows(q, g.nh, g.d, dt, rows, "q", dev)),
+            _rows(out, g.nh, g.dv, dt, rows, "out", dev), rows)
+
+
+def o1_pg_chunk_attend(g: o1_pg_geom, cache: o1_pg_cache, scratch, q, seqs, out, stream=None) -> int:
+    """Attention of packed sequences' rows q [rows, heads, d] over the cache into
+    out [rows, heads, dv]; ``seqs`` as for o1_pg_write."""
+    if not isinstance(seqs, ctypes.Array):
+        seqs = pg_seqs(seqs)
+    dev, head = _pg_args(g, cache)
+    ins, o, rows = _pg_attend(g, scratch, q, out, dev)
+    return LIB.o1_pg_chunk_attend(*head, *ins, seqs, len(seqs), *o, rows, _raw_stream(stream, dev))
+
+
+def o1_pg_token_attend(g: o1_pg_geom, cache: o1_pg_cache, scratch, q, slots, pos, out, stream=None) -> int:
+    """Attention of one row of each sequence: row r at position pos[r] of slot
+    slots[r] (as for o1_pg_token_write)."""
+    dev, head = _pg_args(g, cache)
+    ins, o, rows = _pg_attend(g, scratch, q, out, dev)
+    return LIB.o1_pg_token_attend(*head, *ins, _flat(slots, rows, torch.int32, "slots", dev),
+                                  _flat(pos, rows, torch.int64, "pos", dev), *o, rows, _raw_stream(stream, dev))
 
 
 def empty_state_arrays(g: o1_geom) -> dict:
