@@ -516,7 +516,7 @@ enum { O1_E4M3 = 3 };
 /* Geometry of a paged cache and the attention over it. Limits: groups in
  * [1, 4096], heads_per_group in [1, 16], at most 65535 heads, d and dv in
  * [8, 256], both % 8 == 0 (O1_E4M3: % 16 == 0), page in {16, 32, 64, 128, 256},
- * window >= 0, scale finite; cache_dtype O1_E4M3, or O1_F16 for dtype O1_F16 and
+ * window >= 0, scale finite and above 0; cache_dtype O1_E4M3, or O1_F16 for dtype O1_F16 and
  * O1_BF16 for the others. */
 typedef struct o1_pg_geom {
     int32_t groups;           /* G: KV groups                                  */
@@ -622,6 +622,12 @@ O1_API int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, 
 O1_API int o1_pg_token_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
                               const void *q, int64_t q_stride, const int32_t *slots, const int64_t *pos, void *out,
                               int64_t out_stride, int32_t rows, void *stream);
+
+/* Read the sticky flags that o1_pg_chunk_attend's kernels raised on the current
+ * device into *flags (host) and, if `clear` is non-zero, reset them:
+ * O1_FLAG_WAIT_EXPIRED (a bounded wait ran out, see o1_set_wait_limit; the
+ * outputs that the block was to write are NaN). Synchronises `stream`. */
+O1_API int o1_pg_flags(uint32_t *flags, int32_t clear, void *stream);
 
 /* A static, human-readable name for a status code. (The pages' geometry
  * gates refuse a shape instead of running it: "cortiq-engine 0.8.82

@@ -277,7 +277,7 @@ bool pg_geom_ok(const o1_pg_geom *g) {
     const int unit = g->cache_dtype == O1_E4M3 ? 16 : 8;   // 16 bytes of a cached row
     if (g->d < 8 || g->d > O1_MAX_D || g->d % unit || g->dv < 8 || g->dv > O1_MAX_DV || g->dv % unit) return false;
     if (g->page < 16 || g->page > 256 || (g->page & (g->page - 1))) return false;
-    if (g->window < 0 || !o1_dtype_ok(g->dtype) || !isfinite(g->scale)) return false;
+    if (g->window < 0 || !o1_dtype_ok(g->dtype) || !isfinite(g->scale) || !(g->scale > 0.f)) return false;
     return g->cache_dtype == O1_E4M3 || g->cache_dtype == (g->dtype == O1_F16 ? O1_F16 : O1_BF16);
 }
 
@@ -453,7 +453,7 @@ int o1_pg_token_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const vo
 
 size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows) {
     if (!pg_geom_ok(geom) || rows < 1) return 0;
-    return pg_rows_scratch(geom->dv, geom->groups, (int64_t)rows * geom->heads_per_group);
+    return std::max(pg_rows_scratch(geom->dv), pg_tc_scratch(*geom, (int64_t)rows * geom->heads_per_group));
 }
 
 int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
@@ -471,10 +471,17 @@ int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *s
     const int rc = attend_args(a, g, cache, scratch, scratch_bytes, q, q_stride, out, out_stride, total_rows,
                                o1_span(nullptr, 0), o1_span(nullptr, 0));
     if (rc != O1_OK) return rc;
-    bool first = true, ok = true;
-    for_tables(seqs, n_seq, [&](int rows) { return ((int64_t)rows * g.heads_per_group + 15) / 16; }, [&](const PgTable &t) {
-        ok = pg_launch_rows(a, g.dtype, g.cache_dtype, &t, first, (cudaStream_t)stream) == cudaSuccess && ok;
-        first = false;
+    // one kernel for all the sequences: the one for few vectors where a group's
+    // fit into its units, the tensor cores' where they do not
+    int64_t most = 0;
+    for (int i = 0; i < n_seq; ++i) most = std::max(most, (int64_t)seqs[i].rows * g.heads_per_group);
+    const int tc = most > PG_ROWS_V ? pg_tc_vectors(g) : 0, unit = tc ? tc : PG_ROWS_V;
+    cudaStream_t st = (cudaStream_t)stream;
+    bool ok = true;
+    for_tables(seqs, n_seq, [&](int rows) { return ((int64_t)rows * g.heads_per_group + unit - 1) / unit; }, [&](const PgTable &t) {
+        const cudaError_t e = tc ? pg_launch_tc(a, g, t, (int64_t)total_rows * g.heads_per_group, st)
+                                 : pg_launch_rows(a, g.dtype, g.cache_dtype, &t, st);
+        ok = ok && e == cudaSuccess;
     });
     return ok ? O1_OK : O1_ERR_CUDA;
 }
@@ -494,7 +501,12 @@ int o1_pg_token_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *s
                                o1_span(slots, (size_t)rows * 4), o1_span(pos, (size_t)rows * 8));
     if (rc != O1_OK) return rc;
     a.slots = slots; a.pos = pos; a.rows = rows;
-    return pg_launch_rows(a, g.dtype, g.cache_dtype, nullptr, true, (cudaStream_t)stream) == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+    return pg_launch_rows(a, g.dtype, g.cache_dtype, nullptr, (cudaStream_t)stream) == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+}
+
+int o1_pg_flags(uint32_t *flags, int32_t clear, void *stream) {
+    if (!flags) return O1_ERR_ARG;
+    return pg_flags(flags, clear, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -61,8 +61,164 @@ __device__ __forceinline__ PgRow pg_token_row(const PgArgs &a, int r) {
     return {ok ? slot : -1, ok ? (int)p : 0};
 }
 
-// Attention of a few rows a group (o1_page_rows.cu): launches over the rows of
-// a token batch (tab null) or the sequences of a table, and the scratch it takes
-// for calls of up to `vectors` query vectors a group.
-cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, bool first, cudaStream_t st);
-size_t pg_rows_scratch(int dv, int groups, int64_t vectors);
+// ---------------------------------------------------------------- attention
+// Work, for both kernels. A unit is up to V query vectors of a sequence (vector
+// i: row i / hpg of its rows, head i % hpg of a group) and a group; its keys are
+// tiles of K positions. The tiles of all units, one unit behind the other, are
+// split evenly over the blocks of one wave, whatever the lengths; a unit cut by
+// such a border leaves partial results (maximum, sum, weighted values), which
+// k_pg_join adds up.
+struct PgUnit {
+    int slot;      // -1: padding, no tiles
+    int row0;      // first row of the sequence in the row tensors
+    int pos0;      // its position
+    int vec0, nv;  // first vector, and vectors
+    int lo, hi;    // positions attended by some vector: lo .. hi
+    template <int K>
+    __device__ __forceinline__ int tiles() const {
+        return slot < 0 ? 0 : hi / K - lo / K + 1;
+    }
+    __device__ __forceinline__ int pos(const PgArgs &a, int v) const { return pos0 + (vec0 + v) / a.hpg; }   // of vector v
+};
+// Unit u of a table (counted by units in `before`), or row u of a token batch.
+template <int V>
+__device__ __forceinline__ PgUnit pg_unit(const PgArgs &a, const PgTable &tab, int u) {
+    PgUnit x;
+    if (a.pos) {
+        const PgRow r = pg_token_row(a, u);
+        x = {r.slot, u, r.pos, 0, a.hpg, 0, 0};
+    } else {
+        int n = 0;
+        for (int hi = tab.n - 1; n < hi;) {
+            const int mid = (n + hi + 1) >> 1;
+            if (tab.s[mid].before <= u) n = mid;
+            else hi = mid - 1;
+        }
+        x = {tab.s[n].slot, tab.s[n].row0, tab.s[n].pos0, (u - tab.s[n].before) * V, 0, 0, 0};
+        x.nv = (int)min((int64_t)V, (int64_t)tab.s[n].rows * a.hpg - x.vec0);
+    }
+    x.hi = x.pos(a, x.nv - 1);
+    x.lo = a.window ? max(0, x.pos(a, 0) - a.window + 1) : 0;
+    return x;
+}
+
+// A block's share of the tiles: `left` of them from tile `skip` of unit u's
+// groups on (group skip / tiles, tile skip % tiles of it). All threads of the
+// block call it; shared: THREADS / 32 + 2 words.
+struct PgShare {
+    int u;
+    int64_t skip, left;
+};
+template <int V, int K, int THREADS>
+__device__ __forceinline__ PgShare pg_share(const PgArgs &a, const PgTable &tab, int units, long long *shared) {
+    constexpr int W = THREADS / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (units + THREADS - 1) / THREADS, u0 = min(units, tid * per), u1 = min(units, u0 + per);
+    long long own = 0;
+    for (int u = u0; u < u1; ++u) own += pg_unit<V>(a, tab, u).template tiles<K>();
+    long long before = own;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, before, m);
+        if (lane >= m) before += o;
+    }
+    if (lane == 31) shared[warp] = before;
+    if (tid == 0) shared[W] = units, shared[W + 1] = 0;
+    __syncthreads();
+    long long total = 0, base = 0;
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) base += shared[w];
+        total += shared[w];
+    }
+    total *= a.G;
+    // blocks that get a tile at least (a block without one inside a unit would
+    // break the chain of its partial results)
+    const int64_t nblk = min((long long)gridDim.x, total);
+    const int64_t from = blockIdx.x < nblk ? total * blockIdx.x / nblk : 0;
+    const int64_t to = blockIdx.x < nblk ? total * (blockIdx.x + 1) / nblk : 0;
+    before = (base + before - own) * a.G;   // tiles before this thread's units
+    if (from < to && from >= before && from < before + own * a.G) {
+        int u = u0;
+        for (; u + 1 < u1; ++u) {
+            const int64_t n = (int64_t)pg_unit<V>(a, tab, u).template tiles<K>() * a.G;
+            if (from < before + n) break;
+            before += n;
+        }
+        shared[W] = u;
+        shared[W + 1] = from - before;
+    }
+    __syncthreads();
+    return {(int)shared[W], shared[W + 1], to - from};
+}
+// The next segment of a share: tiles t0 .. t1 - 1 of unit u and group g, nt in all.
+struct PgSegment {
+    int u, g, t0, t1, nt;
+    PgUnit x;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    // where its partial result goes: a segment that begins inside its unit is
+    // its block's first, one that only ends inside it the block's last
+    __device__ __forceinline__ int part() const { return blockIdx.x * 2 + (t0 > 0 ? 0 : 1); }
+};
+template <int V, int K>
+__device__ __forceinline__ bool pg_next(const PgArgs &a, const PgTable &tab, int units, PgShare &s, PgSegment &o) {
+    while (s.left > 0 && s.u < units) {
+        o.x = pg_unit<V>(a, tab, s.u);
+        o.nt = o.x.template tiles<K>();
+        if (o.nt == 0) {
+            ++s.u;
+            continue;
+        }
+        o.u = s.u;
+        o.g = (int)(s.skip / o.nt);
+        o.t0 = (int)(s.skip - (int64_t)o.g * o.nt);
+        o.t1 = (int)min((int64_t)o.nt, o.t0 + s.left);
+        s.left -= o.t1 - o.t0;
+        s.skip += o.t1 - o.t0;
+        if (s.skip == (int64_t)a.G * o.nt) ++s.u, s.skip = 0;
+        return true;
+    }
+    return false;
+}
+
+// What a block leaves of the units that its borders cut: the values [V][dv] and
+// the statistics [V][2] (maximum in log2 units, sum) of its first segment and of
+// its last, and in its header the first one's unit.
+struct PgHead {
+    int unit;       // u G + g of a unit that a block before began; -1: none
+    int goes_on;    // whether it goes on in the next block
+    int row0, vec0, nv, g;
+    int pad[2];
+};
+struct PgParts {
+    PgHead *head;
+    float *stat, *val;
+};
+__host__ __device__ inline PgParts pg_parts(float *p, int blocks, int vecs) {
+    return {(PgHead *)p, p + (size_t)blocks * 8, p + (size_t)blocks * 8 + (size_t)blocks * 2 * vecs * 2};
+}
+static inline size_t pg_parts_bytes(int blocks, int vecs, int dv) {
+    return o1_al256(((size_t)blocks * 8 + (size_t)blocks * 2 * vecs * (2 + dv)) * 4);
+}
+__device__ __forceinline__ void pg_head(PgHead *head, const PgArgs &a, const PgSegment &s) {
+    *head = {s.u * a.G + s.g, s.t1 < s.nt, s.x.row0, s.x.vec0, s.x.nv, s.g, {0, 0}};
+}
+// A unit's vector in the row tensors.
+__device__ __forceinline__ size_t pg_vec_at(const PgArgs &a, int row0, int vec, int g, size_t stride, int width) {
+    const int r = vec / a.hpg, h = g * a.hpg + (vec - r * a.hpg);
+    return (size_t)(row0 + r) * stride + (size_t)h * width;
+}
+
+// Launches over the rows of a token batch (tab null) or the sequences of a
+// table, counted in units of the launched kernel's vectors.
+// o1_page_rows.cu: few query vectors a group, any geometry.
+constexpr int PG_ROWS_V = 16;
+cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, cudaStream_t st);
+size_t pg_rows_scratch(int dv);
+// The partial results of a launch of `blocks` blocks, joined (chained behind it).
+cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, cudaStream_t st);
+// o1_page_tc.cu: many query vectors, on tcgen05. pg_tc_vectors: a unit's, 0
+// where it does not take the geometry.
+int pg_tc_vectors(const o1_pg_geom &g);
+size_t pg_tc_scratch(const o1_pg_geom &g, int64_t vectors);
+cudaError_t pg_launch_tc(const PgArgs &a, const o1_pg_geom &g, const PgTable &tab, int64_t vectors, cudaStream_t st);
+int pg_flags(uint32_t *flags, int clear, cudaStream_t st);

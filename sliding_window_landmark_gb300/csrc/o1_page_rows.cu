@@ -4,11 +4,6 @@
 // key with one mma.sync m16n8k16: the keys and values are read once, and the
 // bound is HBM.
 //
-// Work. A unit is (16 query vectors, group); its keys are tiles of 64. The
-// tiles of all units, one behind the other, are split evenly over the blocks of
-// one wave, whatever the lengths; a unit cut by such a border leaves partial
-// results (maximum, sum, weighted values), which k_pg_join adds up.
-//
 // A warp takes 16 of a tile's keys and keeps a softmax and an accumulator of
 // its own, so that nothing waits for another warp until the segment's end. Its
 // keys and values come by 16-byte asynchronous copies into a ring of items (16
@@ -26,7 +21,7 @@
 namespace {
 
 constexpr int RW = 4, RT = 32 * RW;   // warps and threads of a block
-constexpr int RV = 16;                // query vectors of a unit
+constexpr int RV = PG_ROWS_V;         // query vectors of a unit
 constexpr int TILE = 16 * RW;         // keys of a tile
 constexpr int PER_SM = 2, BLOCKS = 152 * PER_SM;
 
@@ -145,59 +140,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 16 query vectors of a sequence: vector i is row i / hpg of its rows, head i % hpg.
-struct Unit {
-    int slot;      // -1: padding, no tiles
-    int row0;      // first row of the sequence in the row tensors
-    int pos0;      // its position
-    int vec0, nv;  // first vector, and vectors
-    int lo, hi;    // positions attended by some vector: lo .. hi
-    __device__ __forceinline__ int tiles() const { return slot < 0 ? 0 : (hi / TILE) - (lo / TILE) + 1; }
-};
-__device__ __forceinline__ Unit unit_of(const PgArgs &a, const PgTable &tab, int u) {
-    Unit x;
-    int rows;
-    if (a.pos) {
-        const PgRow r = pg_token_row(a, u);
-        x = {r.slot, u, r.pos, 0, a.hpg, 0, 0};
-    } else {
-        int n = 0;
-        for (int hi = tab.n - 1; n < hi;) {
-            const int mid = (n + hi + 1) >> 1;
-            if (tab.s[mid].before <= u) n = mid;
-            else hi = mid - 1;
-        }
-        rows = tab.s[n].rows;
-        x = {tab.s[n].slot, tab.s[n].row0, tab.s[n].pos0, (u - tab.s[n].before) * RV, 0, 0, 0};
-        x.nv = (int)min((int64_t)RV, (int64_t)rows * a.hpg - x.vec0);
-    }
-    x.hi = x.pos0 + (x.vec0 + x.nv - 1) / a.hpg;
-    x.lo = a.window ? max(0, x.pos0 + x.vec0 / a.hpg - a.window + 1) : 0;
-    return x;
-}
-
-// What a block leaves of the units that its borders cut: the values [RV][dv]
-// and the statistics [RV][2] of its first segment (slot 0) and its last (slot 1),
-// and in its header the units.
-struct Head {
-    int unit;       // of slot 0: the one that a block before began; -1: none
-    int goes_on;    // whether it goes on in the next block
-    int row0, vec0, nv, g;   // that unit's vectors
-};
-struct Scratch {
-    Head *head;
-    float *stat, *val;
-};
-__device__ __forceinline__ Scratch scratch_of(float *p) {
-    return {(Head *)p, p + BLOCKS * 8, p + BLOCKS * 8 + BLOCKS * 2 * RV * 2};
-}
-
-// The row and head of a unit's vector in the row tensors.
-__device__ __forceinline__ size_t vec_at(const PgArgs &a, int row0, int vec, int g, size_t stride, int width) {
-    const int r = vec / a.hpg, h = g * a.hpg + (vec - r * a.hpg);
-    return (size_t)(row0 + r) * stride + (size_t)h * width;
-}
-
 template <typename T, typename C, int N>
 __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_constant__ PgTable tab, int units) {
     using Ty = Types<T, C>;
@@ -207,9 +149,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     constexpr int CB = Z::CB, VL = Z::VL, KB = Z::KB, VB = Z::VB, STEPS = Z::STEPS, RING = Z::RING, ITEM = Z::ITEM;
     constexpr bool E4 = CB == 1;
     extern __shared__ __align__(16) unsigned char sm[];
-    __shared__ long long s_sum[RW];
-    __shared__ long long s_from;
-    __shared__ int s_unit;
+    __shared__ long long s_share[RW + 2];
     __shared__ float s_m[RW][RV], s_l[RW][RV];
     __shared__ __align__(16) uint8_t s_exp[E4 ? RW * RING * 16 : 16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qd = lane & 3, row = lane >> 2;
@@ -217,63 +157,15 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     uint32_t *sq = (uint32_t *)(sm + (size_t)RW * RING * ITEM);   // [term][step][lane][4]
     const C *pk = (const C *)a.k, *pv = (const C *)a.v;
 
-    // ---- this block's share of the tiles
-    int64_t total, from, to;
-    {
-        const int per = (units + RT - 1) / RT, u0 = min(units, tid * per), u1 = min(units, u0 + per);
-        long long own = 0;
-        for (int u = u0; u < u1; ++u) own += unit_of(a, tab, u).tiles();
-        long long before = own;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, before, m);
-            if (lane >= m) before += o;
-        }
-        if (lane == 31) s_sum[warp] = before;
-        __syncthreads();
-        total = 0;
-        long long base = 0;
-        for (int w = 0; w < RW; ++w) {
-            if (w < warp) base += s_sum[w];
-            total += s_sum[w];
-        }
-        total *= a.G;
-        // blocks that get a tile at least (a block without one inside a unit
-        // would break the chain of its partial results)
-        const int64_t nblk = min((int64_t)gridDim.x, total);
-        from = blockIdx.x < nblk ? total * blockIdx.x / nblk : 0;
-        to = blockIdx.x < nblk ? total * (blockIdx.x + 1) / nblk : 0;
-        before = (base + before - own) * a.G;   // tiles before this thread's units
-        if (from < to && from >= before && from < before + own * a.G) {
-            int u = u0;
-            for (; u + 1 < u1; ++u) {
-                const int64_t n = (int64_t)unit_of(a, tab, u).tiles() * a.G;
-                if (from < before + n) break;
-                before += n;
-            }
-            s_unit = u;
-            s_from = from - before;
-        }
-        __syncthreads();
-    }
-    const Scratch sc = scratch_of(a.part);
-    if (tid == 0) sc.head[blockIdx.x].unit = -1;
-    if (from >= to) return;
-
+    PgShare share = pg_share<RV, TILE, RT>(a, tab, units, s_share);
+    const PgParts parts = pg_parts(a.part, BLOCKS, RV);
+    if (tid == 0) parts.head[blockIdx.x].unit = -1;
     const float sc2 = a.scale * 1.4426950408889634f;
-    int u = s_unit;
-    int64_t left = to - from, skip = s_from;   // tiles to go, and those before the first in its unit's groups
     bool first_seg = true;
-    while (left > 0 && u < units) {
-        const Unit x = unit_of(a, tab, u);
-        const int nt = x.tiles();
-        if (nt == 0) {
-            ++u;
-            continue;
-        }
-        const int g = (int)(skip / nt), t0 = (int)(skip - (int64_t)g * nt);
-        const int t1 = (int)min((int64_t)nt, t0 + left);
-        left -= t1 - t0;
+    PgSegment seg;
+    while (pg_next<RV, TILE>(a, tab, units, share, seg)) {
+        const PgUnit &x = seg.x;
+        const int g = seg.g;
         // ---- queries, in the MMA's A layout of this lane order
         __syncthreads();   // the segment before is done with shared memory
         const int kb_n = (a.d * CB + 63) >> 6, vb_n = (a.dv * CB + 127) >> 7;
@@ -285,7 +177,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             for (int h = 0; h < 2; ++h) {
                 const int v = (ln >> 2) + 8 * h;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (v < x.nv && c < a.d) f = o1_ld4((const T *)a.q + vec_at(a, x.row0, x.vec0 + v, g, a.qs, a.d) + c);
+                if (v < x.nv && c < a.d) f = o1_ld4((const T *)a.q + pg_vec_at(a, x.row0, x.vec0 + v, g, a.qs, a.d) + c);
                 split_m<M, TERMS>(f.x, f.y, w[h]);
                 split_m<M, TERMS>(f.z, f.w, w[2 + h]);
             }
@@ -295,14 +187,14 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
         __syncthreads();
 
         // ---- this warp's blocks of 16 keys: blk0, blk0 + RW, ...
-        const int blk0 = (x.lo / TILE + t0) * RW + warp, nb = t1 - t0;
+        const int blk0 = (x.lo / TILE + seg.t0) * RW + warp, nb = seg.t1 - seg.t0;
         int pos[2], low[2];   // of this lane's two vectors: last and first position attended
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            pos[h] = x.pos0 + (x.vec0 + min(row + 8 * h, x.nv - 1)) / a.hpg;   // past the last: zeros, not written
+            pos[h] = x.pos(a, min(row + 8 * h, x.nv - 1));   // past the last: zeros, not written
             low[h] = a.window ? pos[h] - a.window + 1 : 0;
         }
-        const int plain_lo = a.window ? max(0, x.hi - a.window + 1) : 0, plain_hi = x.pos0 + x.vec0 / a.hpg;
+        const int plain_lo = a.window ? max(0, x.hi - a.window + 1) : 0, plain_hi = x.pos(a, 0);
         float acc[VB * VL][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < VB * VL; ++i)
@@ -561,11 +453,8 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                                         acc[b * VL + i + 2][j] * fac[j >> 1], acc[b * VL + i + 3][j] * fac[j >> 1]);
                 }
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == nt;
-        // a segment that begins inside its unit is the block's first (slot 0),
-        // one that ends inside its unit the block's last (slot 1 if it begins it)
-        const int slot = t0 > 0 ? 0 : 1;
-        const size_t ps = (size_t)blockIdx.x * 2 + slot;
+        const bool whole = seg.whole();
+        const size_t ps = seg.part();
         for (int i = tid; i < x.nv * (a.dv >> 2); i += RT) {
             const int v = i / (a.dv >> 2), c = 4 * (i - v * (a.dv >> 2));
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -577,49 +466,51 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 sum += s_m[w][v] > -INFINITY ? s_l[w][v] * ex2(s_m[w][v] - mx) : 0.f;
             }
             if (whole) {
-                const float r = sum > 0.f ? 1.f / sum : 0.f;
-                o1_st4((T *)a.out + vec_at(a, x.row0, x.vec0 + v, g, a.os, a.dv) + c, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+                const float r = sum == 0.f ? 0.f : 1.f / sum;   // a NaN stays one
+                o1_st4((T *)a.out + pg_vec_at(a, x.row0, x.vec0 + v, g, a.os, a.dv) + c, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
             } else {
-                *(float4 *)(sc.val + (ps * RV + v) * a.dv + c) = o;
-                if (c == 0) *(float2 *)(sc.stat + (ps * RV + v) * 2) = make_float2(mx, sum);
+                *(float4 *)(parts.val + (ps * RV + v) * a.dv + c) = o;
+                if (c == 0) *(float2 *)(parts.stat + (ps * RV + v) * 2) = make_float2(mx, sum);
             }
         }
-        if (tid == 0 && first_seg && t0 > 0) sc.head[blockIdx.x] = {u * a.G + g, t1 < nt, x.row0, x.vec0, x.nv, g};
+        if (tid == 0 && first_seg && seg.t0 > 0) pg_head(&parts.head[blockIdx.x], a, seg);
         first_seg = false;
-        skip = 0;
-        if (t1 == nt && g + 1 < a.G) skip = (int64_t)(g + 1) * nt;
-        else if (t1 == nt) ++u;
     }
 }
 
-// The partial results of a unit that borders cut, added up by the block of the
-// first border inside it: (border, slice of vectors).
+// The partial results of a unit that borders cut, added up by the blocks of the
+// first border inside it, a warp a vector.
+constexpr int JOIN_WARPS = 4;
 template <typename T>
-__global__ __launch_bounds__(128) void k_pg_join(PgArgs a, int blocks) {
+__global__ __launch_bounds__(32 * JOIN_WARPS) void k_pg_join(PgArgs a, int blocks, int vecs) {
     o1_chain_wait();
-    const int c = blockIdx.x + 1;
-    const Scratch sc = scratch_of(a.part);
-    const Head h = sc.head[c];
-    if (h.unit < 0 || (int)blockIdx.y >= h.nv) return;
-    if (sc.head[c - 1].unit == h.unit && sc.head[c - 1].goes_on) return;   // the border before is in it too
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const PgParts parts = pg_parts(a.part, blocks, vecs);
+    const PgHead h = parts.head[c];
+    if (h.unit < 0) return;
+    if (parts.head[c - 1].unit == h.unit && parts.head[c - 1].goes_on) return;   // the border before is in it too
     int last = c;
-    while (sc.head[last].goes_on) ++last;
-    const int v = blockIdx.y;
-    auto at = [&](int i) { return (size_t)(i == c - 1 ? 2 * i + 1 : 2 * i) * RV + v; };
-    float mx = -INFINITY;
-    for (int i = c - 1; i <= last; ++i) mx = fmaxf(mx, sc.stat[at(i) * 2]);
-    for (int col = 4 * threadIdx.x; col < a.dv; col += 4 * 128) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        for (int i = c - 1; i <= last; ++i) {
-            const float2 st = *(const float2 *)(sc.stat + at(i) * 2);
-            const float f = st.x > -INFINITY ? ex2(st.x - mx) : 0.f;
-            const float4 y = *(const float4 *)(sc.val + at(i) * a.dv + col);
-            sum = fmaf(f, st.y, sum);
-            o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+    while (last + 1 < blocks && parts.head[last].goes_on) ++last;
+    for (int v = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); v < h.nv; v += gridDim.y * JOIN_WARPS) {
+        auto at = [&](int i) { return (size_t)(i == c - 1 ? 2 * i + 1 : 2 * i) * vecs + v; };
+        float mx = -INFINITY;
+        for (int i = c - 1 + lane; i <= last; i += 32) mx = fmaxf(mx, parts.stat[at(i) * 2]);
+        mx = warp_max(mx);
+        for (int col = 4 * lane; col < a.dv; col += 128) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll 4
+            for (int i = c - 1; i <= last; ++i) {
+                const float2 st = *(const float2 *)(parts.stat + at(i) * 2);
+                const float f = st.x > -INFINITY ? exp2f(st.x - mx) : 0.f;
+                const float4 y = *(const float4 *)(parts.val + at(i) * a.dv + col);
+                sum = fmaf(f, st.y, sum);
+                o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+            }
+            const float r = sum == 0.f ? 0.f : 1.f / sum;   // a NaN stays one
+            o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + col,
+                   make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
         }
-        const float r = sum > 0.f ? 1.f / sum : 0.f;
-        o1_st4((T *)a.out + vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + col, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
     }
 }
 
@@ -629,7 +520,7 @@ cudaError_t rows_launch_n(const PgArgs &a, const PgTable *tab, int units, cudaSt
     using Z = Sizes<C, N, TERMS>;
     const size_t smem = (size_t)RW * Z::RING * Z::ITEM + (size_t)TERMS * Z::STEPS * 512;
     static_assert((size_t)Z::RING * Z::ITEM >= RV * (64 * N + 4) * 4, "a warp's results in its ring");
-    static_assert(sizeof(Head) <= 32, "headers of 8 words");
+    static_assert(sizeof(PgHead) == 32, "headers of 8 words");
     static unsigned long long done = 0;
     unsigned long long bit = 0;
     auto *k = k_pg_rows<T, C, N>;
@@ -641,8 +532,6 @@ cudaError_t rows_launch_n(const PgArgs &a, const PgTable *tab, int units, cudaSt
     PgTable none;
     none.n = 0;
     k<<<BLOCKS, RT, smem, st>>>(a, tab ? *tab : none, units);
-    const int nv = tab ? RV : a.hpg;
-    o1_launch_chained(true, k_pg_join<T>, dim3(BLOCKS - 1, nv), dim3(128), 0, st, a, BLOCKS);
     return cudaGetLastError();
 }
 template <typename T, typename C>
@@ -655,16 +544,26 @@ cudaError_t rows_launch_c(const PgArgs &a, const PgTable *tab, int units, cudaSt
 
 }  // namespace
 
-size_t pg_rows_scratch(int dv, int, int64_t) {
-    return o1_al256(((size_t)BLOCKS * 8 + (size_t)BLOCKS * 2 * RV * (2 + dv)) * 4);
+size_t pg_rows_scratch(int dv) { return pg_parts_bytes(BLOCKS, RV, dv); }
+
+cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, cudaStream_t st) {
+    // a warp a vector for narrow units; wide ones in a few turns
+    const int most = (vecs + JOIN_WARPS - 1) / JOIN_WARPS;
+    const dim3 grid(blocks - 1, most < 8 ? most : 8);
+    if (dtype == O1_F32) o1_launch_chained(true, k_pg_join<float>, grid, dim3(32 * JOIN_WARPS), 0, st, a, blocks, vecs);
+    else if (dtype == O1_BF16) o1_launch_chained(true, k_pg_join<__nv_bfloat16>, grid, dim3(32 * JOIN_WARPS), 0, st, a, blocks, vecs);
+    else o1_launch_chained(true, k_pg_join<__half>, grid, dim3(32 * JOIN_WARPS), 0, st, a, blocks, vecs);
+    return cudaGetLastError();
 }
 
-cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, bool, cudaStream_t st) {
+cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, cudaStream_t st) {
     const int units = tab ? tab->total : a.rows;
-    if (dtype == O1_F32 && cache_dtype == O1_BF16) return rows_launch_c<float, __nv_bfloat16>(a, tab, units, st);
-    if (dtype == O1_F32) return rows_launch_c<float, uint8_t>(a, tab, units, st);
-    if (dtype == O1_BF16 && cache_dtype == O1_BF16) return rows_launch_c<__nv_bfloat16, __nv_bfloat16>(a, tab, units, st);
-    if (dtype == O1_BF16) return rows_launch_c<__nv_bfloat16, uint8_t>(a, tab, units, st);
-    if (cache_dtype == O1_F16) return rows_launch_c<__half, __half>(a, tab, units, st);
-    return rows_launch_c<__half, uint8_t>(a, tab, units, st);
+    cudaError_t e;
+    if (dtype == O1_F32 && cache_dtype == O1_BF16) e = rows_launch_c<float, __nv_bfloat16>(a, tab, units, st);
+    else if (dtype == O1_F32) e = rows_launch_c<float, uint8_t>(a, tab, units, st);
+    else if (dtype == O1_BF16 && cache_dtype == O1_BF16) e = rows_launch_c<__nv_bfloat16, __nv_bfloat16>(a, tab, units, st);
+    else if (dtype == O1_BF16) e = rows_launch_c<__nv_bfloat16, uint8_t>(a, tab, units, st);
+    else if (cache_dtype == O1_F16) e = rows_launch_c<__half, __half>(a, tab, units, st);
+    else e = rows_launch_c<__half, uint8_t>(a, tab, units, st);
+    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, RV, st) : e;
 }

@@ -1,0 +1,940 @@
+// Attention of many query vectors over the paged cache, on the tensor cores
+// (tcgen05, accumulators in TMEM). The query heads of a group share its keys, so
+// a tile is 128 query vectors (rows times heads of the group) against 128 keys:
+//   S = Q K^T, P = e^{S - m}, O += P V
+// with a running reference m a row within 2^8 of the row's maximum (O is
+// rescaled only when the maximum passes it), P written over S in TMEM.
+//
+// A block takes segments of units (o1_page.cuh), one block an SM:
+//   warps 0-7   softmax: a thread a row; two query tiles (QT = 2: rows of up to
+//               128 values), a warpgroup each, in turn on the tensor cores, or
+//               one tile with two score buffers and a warpgroup on either half
+//               of its keys (QT = 1)
+//   warps 8-11  producers: queries, keys and values into shared memory, 128-byte
+//               swizzled, by 16-byte asynchronous copies (16-bit caches) or
+//               through registers, where e4m3 codes become bf16 values under
+//               their row's power of two (exact). Pages end anywhere on 16
+//               positions; a producer's 16 rows lie in one page. What no row
+//               attends is zero-filled, not read.
+//   warp 12     issues the MMAs
+// Keys come as items of 128 keys x 128 columns, values as 128 keys x 128 columns
+// or 64 x 256: 32 KB slots of one ring, in the order of use.
+//
+// Terms. As in o1_page_rows.cu: one for 16-bit rows over their own type and bf16
+// over e4m3, two bf16 for fp16 over e4m3, three for fp32. For fp32 rows a tile's
+// P V is an accumulation of its own, added to sums in registers with rounding:
+// the MMA's accumulation truncates, the same way each time.
+//
+// Every wait is bounded; where one runs out the block raises a flag, writes NaN
+// for what is left of its share, and ends once its copies and MMAs are over.
+#include <math.h>
+
+#include <type_traits>
+
+#include "o1_page.cuh"
+#include "o1_tc.cuh"
+
+static __device__ uint32_t pg_device_flags;
+
+namespace {
+
+constexpr int KT = 128;                        // keys of a tile
+constexpr int SM_WARPS = 8, PR_WARPS = 4;      // softmax and producer warps
+constexpr int THREADS = 32 * (SM_WARPS + PR_WARPS + 4), SM_THREADS = 32 * SM_WARPS;   // the issuer's warpgroup has three idle warps
+constexpr int SLOT = 32768, MAX_SLOTS = 6;
+constexpr int BLOCKS = 152;
+constexpr int LAG = 2;                         // items that a producer has in flight beyond the one it issues
+constexpr float HEADROOM = 8.f;                // log2 units above the reference before it moves
+constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside it
+
+template <typename T, typename C>
+struct Types {   // 16-bit rows over their own type
+    using M = T;
+    static constexpr int TERMS = 1;
+};
+template <>
+struct Types<float, __nv_bfloat16> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 3;
+};
+template <>
+struct Types<float, uint8_t> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 3;
+};
+template <>
+struct Types<__nv_bfloat16, uint8_t> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 1;
+};
+template <>
+struct Types<__half, uint8_t> {
+    using M = __nv_bfloat16;
+    static constexpr int TERMS = 2;
+};
+
+// Registers a thread. The block starts with 128, all of the SM's; each role's
+// warpgroups then trade them: softmax (two warpgroups), producers, issuer.
+constexpr int REGS = 128;
+template <bool E4>
+struct Regs {
+    static constexpr int PRODUCER = E4 ? 104 : 72, ISSUER = 72, SOFTMAX = E4 ? 168 : 184;
+    static_assert(2 * SOFTMAX + PRODUCER + ISSUER <= 4 * REGS, "no more than the block has");
+};
+template <int N>
+__device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_less() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// TMEM columns. QT = 2: scores of the two tiles at 0 and 128, outputs at 256 and
+// 384. QT = 1: two score buffers, outputs behind them; a third term of P has 64
+// columns more a buffer.
+template <int TERMS>
+struct Cols {
+    static constexpr uint32_t STRIDE = TERMS == 3 ? 192 : 128, OUT = 2 * STRIDE;
+    static __device__ __forceinline__ uint32_t score(int b) { return STRIDE * b; }
+    static __device__ __forceinline__ uint32_t out(int tile) { return OUT + 128 * tile; }
+    // A operand of 16 keys (step k of 8), term t: 64 keys' first and second
+    // terms lie over the scores of those keys
+    static __device__ __forceinline__ uint32_t p(int k, int t) {
+        return t < 2 ? 64 * (k >> 2) + 32 * t + 8 * (k & 3) : 128 + 8 * k;
+    }
+};
+
+template <typename M>
+__device__ __forceinline__ uint32_t idesc(int m, int n, int mn_b) {
+    return (1u << 4) | (std::is_same<M, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)mn_b << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t pack_m(const __nv_bfloat16 *, float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ uint32_t pack_m(const __half *, float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ float2 unpack_m(const __nv_bfloat16 *, uint32_t w) {
+    return __bfloat1622float2(*(const __nv_bfloat162 *)&w);
+}
+// (a, b) as packed M pair, and what it leaves of them
+template <typename M>
+__device__ __forceinline__ uint32_t take_m(float &a, float &b) {
+    const uint32_t w = pack_m((const M *)nullptr, a, b);
+    const float2 f = unpack_m((const M *)nullptr, w);
+    a -= f.x;
+    b -= f.y;
+    return w;
+}
+
+// 16 bytes into shared memory, zeros where !on
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
+    const int n = on ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t dst, const uint4 &v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Byte of 16-byte piece p (0 to 7) of row r in a panel of 128-byte rows.
+__device__ __forceinline__ uint32_t piece(int r, int p) { return (uint32_t)(128 * r + 16 * (p ^ (r & 7))); }
+
+// 8 e4m3 codes as bf16 pairs times a power of two (a bf16 pair)
+__device__ __forceinline__ uint4 bf16_of_e4m3(uint2 c, __nv_bfloat162 f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t two = (uint16_t)((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        const float2 x = __half22float2(*(const __half2 *)&h);
+        const __nv_bfloat162 y = __hmul2(__floats2bfloat162_rn(x.x, x.y), f);
+        w[i] = *(const uint32_t *)&y;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct Shared {
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    uint64_t q_full, q_free;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], fin;
+    long long share[THREADS / 32 + 2];
+    uint32_t tslot;
+    int abort;
+    float half[2][128];   // QT = 1: the warpgroups' maxima, then sums
+};
+static_assert(sizeof(Shared) <= 2048, "static and dynamic shared memory in 227 KB");
+
+// Sizes of a call, the same in every role.
+struct Shape {
+    int nqc;       // 64-column blocks of Q and K
+    int ksteps;    // k16 steps of a score
+    int k_items;   // items of a key tile (128 columns each)
+    int v_keys;    // keys of a value item
+    int v_items;
+    int nv;        // value columns, rounded to 16
+    int nslot;
+};
+template <int QT, int TERMS>
+__device__ __forceinline__ Shape shape_of(int d, int dv) {
+    Shape s;
+    s.nqc = (d + 63) / 64;
+    s.ksteps = (d + 15) / 16;
+    s.k_items = (d + 127) / 128;
+    s.v_keys = dv > 128 ? 64 : 128;
+    s.v_items = dv > 128 ? 2 : 1;
+    s.nv = (dv + 15) / 16 * 16;
+    s.nslot = min(MAX_SLOTS, (int)((SMEM - 1024 - (size_t)TERMS * QT * s.nqc * 16384) / SLOT));   // 3 at least
+    return s;
+}
+
+// A ring position.
+struct Ring {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) slot = 0, phase ^= 1;
+    }
+};
+
+__device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SM_THREADS) : "memory"); }
+// the softmax warps' barrier that says whether any thread had `p`
+__device__ __forceinline__ bool sm_or(bool p) {
+    int r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\nbar.red.or.pred q, 1, %2, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((int)p), "n"(SM_THREADS)
+        : "memory");
+    return r != 0;
+}
+
+// ---------------------------------------------------------------- producers
+
+template <typename T, typename C, int QT>
+struct Producer {
+    using M = typename Types<T, C>::M;
+    static constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    static constexpr bool E4 = sizeof(C) == 1, Q_COPY = TERMS == 1 && sizeof(T) == 2;
+    const PgArgs &a;
+    Shared &sh;
+    const Shape &z;
+    uint32_t q0, ring0;   // shared addresses
+    int lane, r4, l8;     // r4: this thread's row of each 16, l8: its place among the 8 threads of a row
+    Ring put;             // slot of the next item
+    Ring tell;            // of the next to be announced
+    int out;              // items issued and not announced
+    bool ok;
+
+    __device__ __forceinline__ void announce() {   // the oldest item is in shared memory
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[tell.slot]);
+        tell.next(z.nslot);
+        --out;
+    }
+    __device__ __forceinline__ bool take() {
+        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles);
+        return ok;
+    }
+    __device__ __forceinline__ void issued() {
+        put.next(z.nslot);
+        ++out;
+        if (E4) {
+            announce();
+        } else {
+            copy_commit();
+            if (out > LAG) {
+                copy_wait<LAG>();
+                announce();
+            }
+        }
+    }
+    __device__ __forceinline__ void flush() {
+        if (!E4) copy_wait<0>();
+        while (out) announce();
+    }
+
+    // The query tiles: row v of the unit's vectors, its values as terms.
+    __device__ __forceinline__ void queries(const PgSegment &s) {
+        const int tiles = QT == 2 && s.x.nv > 128 ? 2 : 1, pieces = 2 * z.ksteps;   // 16-byte pieces of a row
+#pragma unroll 1
+        for (int r0 = 0; r0 < 128 * tiles; r0 += 16) {
+            const int v = r0 + r4, row = v & 127;
+            const bool in = v < s.x.nv;
+            const T *src = (const T *)a.q + (in ? pg_vec_at(a, s.x.row0, s.x.vec0 + v, s.g, a.qs, a.d) : 0);
+            const uint32_t dst = q0 + (uint32_t)((v >> 7) * z.nqc) * 16384;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int p = 8 * c + l8;
+                if (p >= pieces) continue;
+                const bool on = in && 8 * p < a.d;
+                const uint32_t at = dst + c * 16384 + piece(row, l8);
+                if constexpr (Q_COPY) {
+                    copy16(at, on ? (const void *)(src + 8 * p) : a.q, on);
+                } else {
+                    float x[8];
+                    if (on) {
+                        const float4 f0 = o1_ld4(src + 8 * p), f1 = o1_ld4(src + 8 * p + 4);
+                        x[0] = f0.x; x[1] = f0.y; x[2] = f0.z; x[3] = f0.w;
+                        x[4] = f1.x; x[5] = f1.y; x[6] = f1.z; x[7] = f1.w;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int t = 0; t < TERMS; ++t) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = take_m<M>(x[2 * i], x[2 * i + 1]);
+                        st16(at + (uint32_t)(t * QT * z.nqc) * 16384, make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                }
+            }
+        }
+        if (Q_COPY) {
+            copy_commit();
+            copy_wait<0>();
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+    }
+
+    // The pages of a tile's eight runs of 16 positions, run i in lanes i, i + 8, ...
+    __device__ __forceinline__ int pages(const PgSegment &s, int j) const {
+        const int p = (s.x.lo / KT + j) * KT + 16 * (lane & 7);
+        return j < s.t1 && p <= s.x.hi && p + 15 >= s.x.lo ? pg_page(a, s.x.slot, p) : -1;
+    }
+
+    // An item of the tile: keys (128 columns) or values (v_keys rows). 16 rows
+    // at a time; a thread has the same row of each 16.
+    template <bool KEYS>
+    __device__ __forceinline__ void item(const PgSegment &s, int j, int ids, int part) {
+        if (!take()) return;
+        const int width = KEYS ? a.d : a.dv, col0 = KEYS ? 128 * part : 0, key0 = KEYS ? 0 : z.v_keys * part;
+        const int rows = KEYS ? 128 : z.v_keys, runs = rows / 16;
+        const int cols = min(KEYS ? 128 : 256, (width + 15) / 16 * 16 - col0);   // to be filled
+        const int p0 = (s.x.lo / KT + j) * KT + key0;
+        const uint32_t dst = ring0 + put.slot * SLOT;
+        const C *pool = (const C *)(KEYS ? a.k : a.v);
+        if constexpr (!E4) {
+            const int blocks = (cols + 63) / 64;
+#pragma unroll 1
+            for (int i = 0; i < runs; ++i) {
+                const int page = __shfl_sync(0xffffffffu, ids, key0 / 16 + i), p = p0 + 16 * i + r4;
+                const bool in = page >= 0 && p >= s.x.lo && p <= s.x.hi;
+                const C *src = pg_at(pool, a, max(page, 0), s.g, p & ((1 << a.lpage) - 1), width) + col0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int c = 64 * b + 8 * l8;
+                    if (b >= blocks || c >= cols) continue;
+                    const bool on = in && col0 + c < width;
+                    copy16(dst + b * (rows * 128) + piece(16 * i + r4, l8), on ? src + c : pool, on);
+                }
+            }
+        } else {
+            // 16 codes a thread, two pieces of a 64-column block; four threads
+            // cover a block, and the 8 of a row write their two pieces in
+            // opposite orders, so that no bank is hit twice
+            const uint8_t *exps = KEYS ? a.ke : a.ve;
+            const int halves = cols > 128 ? 2 : 1;
+#pragma unroll 1
+            for (int i0 = 0; i0 < runs; i0 += 4) {
+                uint4 w[4][2];
+                uint32_t e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int page = __shfl_sync(0xffffffffu, ids, key0 / 16 + i0 + i), p = p0 + 16 * (i0 + i) + r4;
+                    const bool in = page >= 0 && p >= s.x.lo && p <= s.x.hi;
+                    const int at = p & ((1 << a.lpage) - 1);
+                    const C *src = pg_at(pool, a, max(page, 0), s.g, at, width) + col0;
+                    e[i] = in ? *pg_at(exps, a, page, s.g, at, 1) : 0u;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = 128 * h + 16 * l8;
+                        w[i][h] = make_uint4(0u, 0u, 0u, 0u);
+                        if (h < halves && in && col0 + c < width) w[i][h] = *(const uint4 *)(src + c);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t f2 = e[i] * 0x00800080u;   // 2^(byte - 127) twice
+                    const __nv_bfloat162 f = *(const __nv_bfloat162 *)&f2;
+                    const int row = 16 * (i0 + i) + r4;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = 128 * h + 16 * l8;
+                        if (h >= halves || c >= cols) continue;
+                        const uint32_t at = dst + (c >> 6) * (rows * 128);
+                        const int p = (c & 63) >> 3, odd = (l8 >> 2) & 1;
+                        const uint4 lo = bf16_of_e4m3(make_uint2(w[i][h].x, w[i][h].y), f);
+                        const uint4 hi = bf16_of_e4m3(make_uint2(w[i][h].z, w[i][h].w), f);
+                        st16(at + piece(row, p + odd), odd ? hi : lo);
+                        st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
+                    }
+                }
+            }
+        }
+        issued();
+    }
+
+    __device__ __forceinline__ void run(const PgTable &tab, int units, PgShare share) {
+        PgSegment s;
+        uint32_t qp = 1;
+        while (ok && pg_next<V, KT>(a, tab, units, share, s)) {
+            int ids = pages(s, s.t0), ids1 = pages(s, s.t0 + 1);
+            flush();   // the scores that free the queries may need an item not announced yet
+            ok = warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
+            if (!ok) break;
+            qp ^= 1;
+            queries(s);
+            // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
+            auto keys = [&](int j, int id) {
+                for (int p = 0; ok && p < z.k_items; ++p) item<true>(s, j, id, p);
+            };
+            auto values = [&](int j, int id) {
+                for (int p = 0; ok && p < z.v_items; ++p) item<false>(s, j, id, p);
+            };
+            keys(s.t0, ids);
+            for (int j = s.t0; ok && j < s.t1; ++j) {
+                const int ids2 = pages(s, j + 2);
+                if (QT == 1 && j + 1 < s.t1) keys(j + 1, ids1);
+                values(j, ids);
+                if (QT == 2 && j + 1 < s.t1) keys(j + 1, ids1);
+                ids = ids1;
+                ids1 = ids2;
+            }
+        }
+        flush();
+    }
+};
+
+// ------------------------------------------------------------- MMA issuer
+
+template <typename T, typename C, int QT>
+__device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape &z, uint32_t q0, uint32_t ring0, uint32_t tmem,
+                                       const PgTable &tab, int units, PgShare share) {
+    using M = typename Types<T, C>::M;
+    constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    using Col = Cols<TERMS>;
+    const bool e = elect_one();
+    const uint64_t dq = desc_sw128(q0), dk = desc_sw128(ring0), dv = desc_sw128_mn(ring0, z.v_keys * 128);
+    const uint32_t id_s = idesc<M>(128, KT, 0), id_o = idesc<M>(128, z.nv, 1);
+    const long long wl = a.wait_cycles;
+    bool ok = true;
+    Ring get = {0, 0};
+    uint32_t qp = 0;                 // phase of q_full
+    uint32_t npv[2] = {0, 0};        // P V issued: of either tile (QT = 2), or in all
+    uint32_t nseg[2] = {0, 0};       // segments of either tile
+    uint32_t nsc = 0;                // QT = 1: scores issued
+    PgSegment s;
+    auto commit = [&](uint64_t *bar) {
+        if (e) mma_commit(bar);
+    };
+    auto filled = [&](const Ring &r) -> bool {
+        ok = ok && warp_wait(&sh.full[r.slot], r.phase, &sh.abort, wl);
+        return ok;
+    };
+    // scores of query tile t from the key items at `r` on (QT = 1: released once used)
+    auto scores = [&](int t, int buf, Ring r) {
+        const uint32_t col = tmem + Col::score(buf);
+        if constexpr (TERMS == 1) {
+            for (int i = 0; i < z.k_items; ++i) {
+                if (!filled(r)) return;
+                tc_after();
+                const uint64_t kd = dk + (uint64_t)(r.slot * (SLOT / 16)), qd = dq + (uint64_t)((t * z.nqc + 2 * i) * 1024);
+                const int n = min(8, z.ksteps - 8 * i);
+                for (int x = 0; x < n; ++x)
+                    if (e) mma_ss(col, qd + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s, i + x > 0);
+                if (QT == 1) commit(&sh.empty[r.slot]);
+                r.next(z.nslot);
+            }
+        } else {
+            // lower terms first: an accumulation rounds at the size of the sum so far
+            Ring q = r;
+            for (int i = 0; i < z.k_items; ++i, q.next(z.nslot))
+                if (!filled(q)) return;
+            tc_after();
+            for (int m = TERMS - 1; m >= 0; --m) {
+                q = r;
+                for (int i = 0; i < z.k_items; ++i, q.next(z.nslot)) {
+                    const uint64_t kd = dk + (uint64_t)(q.slot * (SLOT / 16));
+                    const uint64_t qd = dq + (uint64_t)(((m * QT + t) * z.nqc + 2 * i) * 1024);
+                    const int n = min(8, z.ksteps - 8 * i);
+                    for (int x = 0; x < n; ++x)
+                        if (e) mma_ss(col, qd + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s, m < TERMS - 1 || i + x > 0);
+                }
+            }
+            q = r;
+            for (int i = 0; i < z.k_items; ++i, q.next(z.nslot)) commit(&sh.empty[q.slot]);
+        }
+        commit(&sh.s_full[buf]);
+    };
+    // P V of query tile t from the value items at `r` on
+    auto values = [&](int t, int buf, Ring r, bool acc, bool release) {
+        const uint32_t out = tmem + Col::out(t), p = tmem + Col::score(buf);
+        if constexpr (TERMS == 3) {   // one item; a sum of its own
+            if (!filled(r)) return;
+            tc_after();
+            const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
+            for (int m = 2; m >= 0; --m)
+                for (int k = 0; k < 8; ++k)
+                    if (e) mma_ts(out, p + Col::p(k, m), vd + 128 * k, id_o, m < 2 || k > 0);
+            commit(&sh.empty[r.slot]);
+        } else {
+            const int steps = z.v_keys / 16;
+            for (int i = 0; i < z.v_items; ++i) {
+                if (!filled(r)) return;
+                tc_after();
+                const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
+                for (int x = 0; x < steps; ++x)
+#pragma unroll
+                    for (int m = TERMS - 1; m >= 0; --m)
+                        if (e) mma_ts(out, p + Col::p(i * steps + x, m), vd + 128 * x, id_o, acc || i + x > 0 || m < TERMS - 1);
+                if (release) commit(&sh.empty[r.slot]);
+                r.next(z.nslot);
+            }
+        }
+        commit(&sh.pv_done[t]);
+    };
+    auto advance = [&](int n) {
+        for (int i = 0; i < n; ++i) get.next(z.nslot);
+    };
+    while (ok && pg_next<V, KT>(a, tab, units, share, s)) {
+        ok = warp_wait(&sh.q_full, qp, &sh.abort, wl);
+        if (!ok) break;
+        qp ^= 1;
+        tc_after();
+        const int nt = s.t1 - s.t0;
+        if (QT == 2) {
+            // S0 S1 | PV0 S0' PV1 S1' | ...: a tile's softmax runs under the other's MMAs
+            const int lt = s.x.nv > 128 ? 1 : 0;   // last tile
+            scores(0, 0, get);
+            if (lt && ok) scores(1, 1, get);
+            commit(&sh.empty[get.slot]);
+            get.next(z.nslot);
+            for (int j = 0; ok && j < nt; ++j) {
+                Ring kr = get;
+                kr.next(z.nslot);
+                if (j == nt - 1) commit(&sh.q_free);   // the last scores are issued
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t > lt || !ok) break;
+                    ok = warp_wait(&sh.p_full[t], npv[t] & 1, &sh.abort, wl);
+                    if (ok && j == 0) ok = warp_wait(&sh.o_free[t], (nseg[t] & 1) ^ 1, &sh.abort, wl);
+                    if (!ok) break;
+                    tc_after();
+                    values(t, t, get, j > 0, t == lt);
+                    ++npv[t];
+                    if (ok && j + 1 < nt) {
+                        scores(t, t, kr);
+                        if (t == lt) commit(&sh.empty[kr.slot]);
+                    }
+                }
+                advance(j + 1 < nt ? 2 : 1);
+            }
+            ++nseg[0];
+            if (lt) ++nseg[1];
+        } else {
+            scores(0, nsc & 1, get);
+            ++nsc;
+            advance(z.k_items);
+            for (int j = 0; ok && j < nt; ++j) {
+                if (j + 1 < nt) {
+                    scores(0, nsc & 1, get);
+                    if (!ok) break;
+                    ++nsc;
+                    advance(z.k_items);
+                }
+                if (j == nt - 1) commit(&sh.q_free);
+                const uint32_t n = npv[0];
+                ok = warp_wait(&sh.p_full[n & 1], (n >> 1) & 1, &sh.abort, wl);
+                // outputs given back: of the segment before, or (sums in registers) of the tile before
+                if (ok && (TERMS == 3 || j == 0)) ok = warp_wait(&sh.o_free[0], ((TERMS == 3 ? n : nseg[0]) & 1) ^ 1, &sh.abort, wl);
+                if (!ok) break;
+                tc_after();
+                values(0, n & 1, get, j > 0, true);
+                ++npv[0];
+                advance(z.v_items);
+            }
+            ++nseg[0];
+        }
+    }
+    if (e) {
+        mma_commit(&sh.fin);   // tracks every MMA issued, also after an abort
+        mbar_drain(&sh.fin, 0);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- softmax
+
+// 8 floats to 8 values of T
+__device__ __forceinline__ void st8(float *p, const float *x) {
+    o1_st4(p, make_float4(x[0], x[1], x[2], x[3]));
+    o1_st4(p + 4, make_float4(x[4], x[5], x[6], x[7]));
+}
+template <typename T>
+__device__ __forceinline__ void st8(T *p, const float *x) {
+    *(uint4 *)p = make_uint4(pack_m(p, x[0], x[1]), pack_m(p, x[2], x[3]), pack_m(p, x[4], x[5]), pack_m(p, x[6], x[7]));
+}
+
+template <typename T, typename C, int QT>
+__device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape &z, uint32_t tmem, const PgTable &tab, int units,
+                                        PgShare share, int vecs) {
+    using M = typename Types<T, C>::M;
+    constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    constexpr bool REG = TERMS == 3;   // sums in registers
+    using Col = Cols<TERMS>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const float sc2 = a.scale * 1.4426950408889634f;   // scores in log2 units; scale > 0
+    const long long wl = a.wait_cycles;
+    const PgParts parts = pg_parts(a.part, BLOCKS, vecs);
+    if (tid == 0) parts.head[blockIdx.x].unit = -1;
+    bool ok = true, first = true;
+    uint32_t n = 0;   // tiles so far, of this warpgroup's query tile
+    PgSegment s;
+    while (pg_next<V, KT>(a, tab, units, share, s)) {
+        if (tid == 0 && first && s.t0 > 0) pg_head(&parts.head[blockIdx.x], a, s);
+        first = false;
+        const int tile = QT == 2 ? wg : 0, v0 = 128 * tile, v = v0 + row;
+        if (QT == 2 && s.x.nv <= v0) continue;
+        const int pos = s.x.pos(a, min(v, s.x.nv - 1)), low = a.window ? pos - a.window + 1 : 0;
+        // positions that every row of the tile attends
+        const int plain_hi = s.x.pos(a, v0), last = s.x.pos(a, min(v0 + 127, s.x.nv - 1));
+        const int plain_lo = a.window ? last - a.window + 1 : 0;
+        const bool idle = v0 + 32 * (warp & 3) >= s.x.nv;   // no row of this warp's
+        float m = -INFINITY, l = 0.f;
+        float o[REG ? 64 : 1];
+        if (REG) {
+#pragma unroll
+            for (int i = 0; i < (REG ? 64 : 1); ++i) o[i] = 0.f;
+        }
+        auto ids = [&](int j) {   // whether a run of 16 positions has a page
+            const int p = (s.x.lo / KT + j) * KT + 16 * (lane & 7);
+            return j >= s.t1 || p > s.x.hi || p + 15 < s.x.lo || pg_page(a, s.x.slot, p) >= 0;
+        };
+        bool next_there = ids(s.t0);
+        // P V of the tile before (number t), added to this warpgroup's columns
+        auto add_values = [&](uint32_t t) {
+            ok = ok && warp_wait(&sh.pv_done[0], t & 1, &sh.abort, wl);
+            if (!ok) return;
+            tc_after();
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t r[32];
+                TMEM_LD32(lanes + Col::out(0) + 64 * wg + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[REG ? c + i : 0] += __uint_as_float(r[i]);
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_free[0]);
+        };
+        for (int j = s.t0; ok && j < s.t1; ++j, ++n) {
+            const uint32_t there = __ballot_sync(0xffffffffu, next_there) & 0xffu;
+            next_there = ids(j + 1);
+            const int x0 = (s.x.lo / KT + j) * KT, buf = QT == 2 ? tile : n & 1;
+            const bool plain = x0 >= plain_lo && x0 + KT - 1 <= plain_hi && there == 0xffu;
+            ok = warp_wait(&sh.s_full[buf], QT == 2 ? n & 1 : (n >> 1) & 1, &sh.abort, wl);
+            if (QT == 2 && !ok) break;
+            tc_after();
+            if (REG && j > s.t0) add_values(n - 1);
+            const uint32_t scol = lanes + Col::score(buf);
+            uint32_t r[64];
+            // raw scores of 64 keys, those not attended -inf
+            auto load = [&](int h) {
+                TMEM_LD32(scol + 64 * h, (&r[0]));
+                TMEM_LD32(scol + 64 * h + 32, (&r[32]));
+                tmem_ld_wait();
+                if (!plain) {
+                    const int b0 = low - x0 - 64 * h, b1 = pos - x0 - 64 * h;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c < b0 || c > b1 || !(there >> (4 * h + c / 16) & 1)) r[c] = 0xff800000u;
+                }
+            };
+            auto top_of = [&]() {
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 64; ++c) t[c & 3] = fmaxf(t[c & 3], __uint_as_float(r[c]));
+                return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            };
+            float top = -INFINITY;
+            if (ok && !idle) {
+                if (QT == 2) {
+                    load(0);
+                    top = top_of();
+                    load(1);
+                } else {
+                    load(wg);
+                }
+                top = fmaxf(top, top_of()) * sc2;
+            }
+            // The reference moves where the maximum has passed it by 2^8. QT = 1:
+            // the two halves of a row decide together, also to give up (a
+            // barrier that one of them left would never be met).
+            bool move = top > m + HEADROOM;
+            if (QT == 2) {
+                move = __any_sync(0xffffffffu, move);
+            } else {
+                move = sm_or(move || !ok);
+                if (move) {
+                    sh.half[wg][row] = top;
+                    ok = !sm_or(!ok);
+                    if (!ok) break;
+                    top = fmaxf(top, sh.half[wg ^ 1][row]);
+                }
+            }
+            if (move) {
+                const float mn = fmaxf(m, top), f = m > -INFINITY ? ex2(m - mn) : 0.f;
+                m = mn;
+                l *= f;
+                if (REG) {
+#pragma unroll
+                    for (int i = 0; i < (REG ? 64 : 1); ++i) o[i] *= f;
+                } else if (j > s.t0) {
+                    ok = warp_wait(&sh.pv_done[QT == 2 ? tile : 0], (n - 1) & 1, &sh.abort, wl);
+                    if (QT == 1) ok = !sm_or(!ok);
+                    if (!ok) break;
+                    tc_after();
+                    // this warpgroup's columns: all of its tile's (QT = 2), or every other 32
+                    for (int c = QT == 2 ? 0 : 32 * wg; c < z.nv; c += QT == 2 ? 32 : 64) {
+                        uint32_t y[32];
+                        TMEM_LD32(lanes + Col::out(tile) + c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                        TMEM_ST32(lanes + Col::out(tile) + c, y);
+                    }
+                }
+                if (QT == 1) sm_sync();   // the maxima are read before they are written again
+            }
+            // P over the scores it comes from
+            if (!idle) {
+                const float ref = m > -INFINITY ? m : 0.f;
+                auto store = [&](int h) {
+                    float sum[2] = {0.f, 0.f};
+                    constexpr int W = TERMS == 1 ? 32 : 16;   // words at a time, 2 keys each
+#pragma unroll
+                    for (int i = 0; i < 32; i += W) {
+                        uint32_t w[W], w1[W], w2[W];
+#pragma unroll
+                        for (int c = 0; c < W; ++c) {
+                            float x = ex2(fmaf(__uint_as_float(r[2 * (i + c)]), sc2, -ref));
+                            float y = ex2(fmaf(__uint_as_float(r[2 * (i + c) + 1]), sc2, -ref));
+                            sum[0] += x;
+                            sum[1] += y;
+                            if constexpr (TERMS == 1) {
+                                w[c] = pack_m((const M *)nullptr, x, y);
+                            } else {
+                                w[c] = take_m<M>(x, y);
+                                w1[c] = take_m<M>(x, y);
+                                if constexpr (TERMS > 2) w2[c] = pack_m((const M *)nullptr, x, y);
+                            }
+                        }
+                        __syncwarp();   // the warp is together for the stores
+                        if constexpr (TERMS == 1) {
+                            TMEM_ST32(scol + 64 * h, w);
+                        } else {
+                            TMEM_ST16(scol + 64 * h + i, w);
+                            TMEM_ST16(scol + 64 * h + 32 + i, w1);
+                            if constexpr (TERMS > 2) TMEM_ST16(scol + 128 + 32 * h + i, w2);
+                        }
+                    }
+                    l += sum[0] + sum[1];
+                };
+                if (QT == 2) {
+                    store(1);
+                    load(0);
+                    store(0);
+                } else {
+                    store(wg);
+                }
+            }
+            tmem_st_wait();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+        }
+        // ---- the segment's end: its rows, or their partial results
+        if (REG) {
+            add_values(n - 1);
+        } else {
+            // a parity tells two phases apart: with scores a tile ahead (QT = 1) the
+            // last scores do not say that the P V before the last is done
+            if (QT == 1 && s.t1 - s.t0 > 1) ok = ok && warp_wait(&sh.pv_done[0], n & 1, &sh.abort, wl);
+            ok = ok && warp_wait(&sh.pv_done[QT == 2 ? tile : 0], (n - 1) & 1, &sh.abort, wl);
+            tc_after();
+        }
+        if (QT == 1) {
+            sh.half[wg][row] = l;
+            ok = !sm_or(!ok);   // both halves write, or none
+            l += sh.half[wg ^ 1][row];
+            sm_sync();
+        }
+        const bool whole = s.whole(), in = v < s.x.nv;
+        const float f = !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const size_t ps = (size_t)s.part() * vecs + v;
+        T *out = (T *)a.out + (in ? pg_vec_at(a, s.x.row0, s.x.vec0 + v, s.g, a.os, a.dv) : 0);
+        if (in && !whole && (QT == 2 || wg == 0)) *(float2 *)(parts.stat + ps * 2) = ok ? make_float2(m, l) : make_float2(0.f, NAN);
+        auto write = [&](int c, float *y) {   // 32 columns
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = ok ? y[i] * f : NAN;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                if (in && c + i < a.dv) {
+                    if (whole) st8(out + c + i, y + i);
+                    else st8(parts.val + ps * a.dv + c + i, y + i);
+                }
+        };
+        if constexpr (REG) {
+            write(64 * wg, o);
+            write(64 * wg + 32, o + 32);
+        } else {
+#pragma unroll 1
+            for (int c = QT == 2 ? 0 : 32 * wg; c < a.dv; c += QT == 2 ? 32 : 64) {
+                uint32_t y[32];
+                float x[32];
+                TMEM_LD32(lanes + Col::out(tile) + c, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(y[i]);
+                write(c, x);
+                __syncwarp();
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_free[QT == 2 ? tile : 0]);
+        }
+        __syncwarp();
+    }
+    if (!ok) tmem_st_wait();   // stores issued before a wait ran out are over before the TMEM is given back
+}
+
+template <typename T, typename C, int QT>
+__global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_constant__ PgTable tab, int units, int vecs) {
+    constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    extern __shared__ unsigned char smraw[];
+    __shared__ Shared sh;
+    const Shape z = shape_of<QT, TERMS>(a.d, a.dv);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t q0 = (su32(smraw) + 1023) & ~1023u, ring0 = q0 + (uint32_t)(TERMS * QT * z.nqc) * 16384;
+    if (tid == 0) {
+        for (int i = 0; i < MAX_SLOTS; ++i) {
+            mbar_init(&sh.full[i], PR_WARPS);
+            mbar_init(&sh.empty[i], 1);
+        }
+        mbar_init(&sh.q_full, PR_WARPS);
+        mbar_init(&sh.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], QT == 2 ? SM_WARPS / 2 : SM_WARPS);
+            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.o_free[i], QT == 2 ? SM_WARPS / 2 : SM_WARPS);
+        }
+        mbar_init(&sh.fin, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    if (warp == SM_WARPS + PR_WARPS) tmem_alloc512(&sh.tslot);
+    tc_before();
+    const PgShare share = pg_share<V, KT, THREADS>(a, tab, units, sh.share);
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sh.tslot;
+    using R = Regs<sizeof(C) == 1>;
+    if (warp < SM_WARPS) {
+        regs_more<R::SOFTMAX>();
+        softmax<T, C, QT>(a, sh, z, tmem, tab, units, share, vecs);
+    } else if (warp < SM_WARPS + PR_WARPS) {
+        regs_less<R::PRODUCER>();
+        Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * (warp - SM_WARPS) + (lane >> 3), lane & 7, {0, 0}, {0, 0}, 0, true};
+        p.run(tab, units, share);
+    } else {
+        regs_less<R::ISSUER>();
+        if (warp == SM_WARPS + PR_WARPS) issuer<T, C, QT>(a, sh, z, q0, ring0, tmem, tab, units, share);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == SM_WARPS + PR_WARPS) tmem_free512(tmem);
+    if (tid == 0 && sh.abort) atomicOr(&pg_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
+}
+
+template <typename T, typename C, int QT>
+cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vectors, cudaStream_t st) {
+    static unsigned long long done = 0;
+    unsigned long long bit = 0;
+    auto *k = k_pg_tc<T, C, QT>;
+    if (o1_attrs_needed(&done, &bit)) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+        if (e != cudaSuccess) return e;
+        // a trade of more registers than the block starts with would wait for ever
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, k)) != cudaSuccess) return e;
+        if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;
+        o1_attrs_done(&done, bit);
+    }
+    const int vecs = (int)(vectors < 128 * QT ? vectors : 128 * QT);
+    k<<<BLOCKS, THREADS, SMEM, st>>>(a, tab, tab.total, vecs);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, vecs, st) : e;
+}
+// Two query tiles a block where both fit beside a ring of five slots: one term
+// and rows of up to 128 values.
+template <typename T, typename C>
+cudaError_t launch_t(const PgArgs &a, int dtype, const PgTable &tab, int64_t vectors, cudaStream_t st) {
+    if constexpr (Types<T, C>::TERMS == 1)
+        if (a.d <= 128 && a.dv <= 128) return launch_q<T, C, 2>(a, dtype, tab, vectors, st);
+    return launch_q<T, C, 1>(a, dtype, tab, vectors, st);
+}
+
+}  // namespace
+
+int pg_tc_vectors(const o1_pg_geom &g) {
+    const bool wide = g.d > 128 || g.dv > 128;
+    if (g.dtype == O1_F32) return wide ? 0 : 128;   // three terms of Q, and P's third
+    if (g.dtype == O1_F16 && g.cache_dtype == O1_E4M3) return 128;
+    return wide ? 128 : 256;
+}
+
+size_t pg_tc_scratch(const o1_pg_geom &g, int64_t vectors) {
+    const int v = pg_tc_vectors(g);
+    return v ? pg_parts_bytes(BLOCKS, (int)(vectors < v ? vectors : v), g.dv) : 0;
+}
+
+cudaError_t pg_launch_tc(const PgArgs &a, const o1_pg_geom &g, const PgTable &tab, int64_t vectors, cudaStream_t st) {
+    if (g.dtype == O1_F32)
+        return g.cache_dtype == O1_E4M3 ? launch_t<float, uint8_t>(a, g.dtype, tab, vectors, st)
+                                        : launch_t<float, __nv_bfloat16>(a, g.dtype, tab, vectors, st);
+    if (g.dtype == O1_BF16)
+        return g.cache_dtype == O1_E4M3 ? launch_t<__nv_bfloat16, uint8_t>(a, g.dtype, tab, vectors, st)
+                                        : launch_t<__nv_bfloat16, __nv_bfloat16>(a, g.dtype, tab, vectors, st);
+    return g.cache_dtype == O1_E4M3 ? launch_t<__half, uint8_t>(a, g.dtype, tab, vectors, st)
+                                    : launch_t<__half, __half>(a, g.dtype, tab, vectors, st);
+}
+
+// As lin_flags: reset only where it was read as raised.
+int pg_flags(uint32_t *flags, int clear, cudaStream_t st) {
+    if (cudaMemcpyFromSymbolAsync(flags, pg_device_flags, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return O1_ERR_CUDA;
+    if (!clear || !*flags) return O1_OK;
+    static const uint32_t zero = 0;
+    if (cudaMemcpyToSymbolAsync(pg_device_flags, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
+        return O1_ERR_CUDA;
+    return cudaStreamSynchronize(st) == cudaSuccess ? O1_OK : O1_ERR_CUDA;
+}

@@ -164,6 +164,8 @@ def _load(path: str | None = None):
     lib.o1_pg_chunk_attend.restype = ctypes.c_int
     lib.o1_pg_token_attend.argtypes = [_PG, _PC, _VP, sz, _VP, i64, _VP, _VP, _VP, i64, i32, _VP]
     lib.o1_pg_token_attend.restype = ctypes.c_int
+    lib.o1_pg_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32, _VP]
+    lib.o1_pg_flags.restype = ctypes.c_int
     lib.o1_set_wait_limit.argtypes = [ctypes.c_int64]
     lib.o1_set_wait_limit.restype = ctypes.c_int
     return lib
@@ -661,6 +663,13 @@ def o1_pg_token_attend(g: o1_pg_geom, cache: o1_pg_cache, scratch, q, slots, pos
     ins, o, rows = _pg_attend(g, scratch, q, out, dev)
     return LIB.o1_pg_token_attend(*head, *ins, _flat(slots, rows, torch.int32, "slots", dev),
                                   _flat(pos, rows, torch.int64, "pos", dev), *o, rows, _raw_stream(stream, dev))
+
+
+def o1_pg_flags(clear: bool = False, stream=None) -> int:
+    """Sticky flags (O1_FLAG_*) of o1_pg_chunk_attend on the current device."""
+    f = ctypes.c_uint32(0)
+    check(LIB.o1_pg_flags(ctypes.byref(f), int(bool(clear)), _stream(stream)), "flags")
+    return int(f.value)
 
 
 def empty_state_arrays(g: o1_geom) -> dict:

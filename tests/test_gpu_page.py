@@ -263,6 +263,9 @@ CHUNKS = [
     (1, 2, 96, 96, 16, 0, [129], [4000]),
     (1, 8, 64, 64, 64, 0, [16] * 140, [5 * i for i in range(140)]),
     (2, 1, 192, 192, 64, 0, [384, 256], [0, 128]),
+    (2, 4, 256, 256, 64, 0, [700, 33], [3000, 5000]),
+    (3, 2, 136, 200, 16, 300, [900, 260], [1000, 0]),
+    (4, 8, 128, 128, 32, 0, [513], [4000]),
 ]
 
 
@@ -569,3 +572,34 @@ def test_sealing_from_the_cache(o1):
         states.append(lay.read())
     for name in states[0]:
         assert (states[0][name] == states[1][name]).all(), name
+
+
+@pytest.mark.parametrize("dt,ct,d", [(BF16, BF16, 128), (BF16, E4, 256), (F32, BF16, 64), (F16, E4, 128)])
+def test_expired_waits_leave_nan_or_right_values(o1, dt, ct, d):
+    """The waits of the tensor-core kernel run out on purpose, early and at
+    several points: a flag, every value NaN or right, and the next call is right."""
+    g = o1.pg_geom(2, 4, d, d, 64, dtype=dt, cache_dtype=ct)
+    seqs = [(0, 300, 0, 600), (300, 100, 1, 0)]
+    cache = Cache(o1, g, [900, 100], 27)
+    q = randn(torch.Generator().manual_seed(13), 400, 8, d, dtype=dt)
+    k, v = cache.held()
+    want, bound = ref.attend(q, k, v, cache.table, 64, cache.n, seqs, g.scale, 0, dt, *ref.precision(dt, ct))
+    assert o1.o1_pg_flags(clear=True) == 0
+    raised = 0
+    for limit in (1, 300, 1000, 2000, 3000, 5000, 8000, 20000):
+        out = torch.full((400, 8, d), 77.0, dtype=dt, device="cuda")
+        try:
+            o1.o1_set_wait_limit(limit)
+            attend(o1, cache, q, seqs, out)
+        finally:
+            o1.o1_set_wait_limit(0)
+        flags = o1.o1_pg_flags(clear=True)
+        raised += flags == o1.O1_FLAG_WAIT_EXPIRED
+        bad = ~torch.isnan(out) & ((out.double() - want).abs() > bound)
+        assert not bad.any(), f"limit {limit}: {int(bad.sum())} values neither NaN nor right"
+        assert flags or torch.isfinite(out).all()
+    assert raised and o1.o1_pg_flags() == 0
+    out = torch.full((400, 8, d), NAN, dtype=dt, device="cuda")
+    attend(o1, cache, q, seqs, out)
+    check(o1, cache, q, seqs, out, "after expiry")
+    assert o1.o1_pg_flags() == 0

@@ -68,7 +68,8 @@ def bad_geoms(o1):
     bad = [geom(o1, G=0), geom(o1, G=4097), geom(o1, hpg=0), geom(o1, hpg=17), geom(o1, G=4096, hpg=16), geom(o1, d=4),
            geom(o1, d=60), geom(o1, d=264), geom(o1, dv=0), geom(o1, dv=264), geom(o1, d=72, **e4), geom(o1, dv=40, **e4),
            geom(o1, page=8), geom(o1, page=48), geom(o1, page=512), geom(o1, page=0), geom(o1, window=-1),
-           geom(o1, scale=float("nan")), geom(o1, scale=float("inf")), geom(o1, cache_dtype=HF), geom(o1, dtype=BF, cache_dtype=HF),
+           geom(o1, scale=float("nan")), geom(o1, scale=float("inf")), geom(o1, scale=0.0),
+           geom(o1, scale=-1.0), geom(o1, cache_dtype=HF), geom(o1, dtype=BF, cache_dtype=HF),
            geom(o1, dtype=HF, cache_dtype=BF)]
     for n in (-1, 3, 4):
         g = geom(o1)
