@@ -62,18 +62,21 @@ __device__ __forceinline__ PgRow pg_token_row(const PgArgs &a, int r) {
 }
 
 // ---------------------------------------------------------------- attention
-// Work, for both kernels. A unit is up to V query vectors of a sequence (vector
-// i: row i / hpg of its rows, head i % hpg of a group) and a group; its keys are
-// tiles of K positions. The tiles of all units, one unit behind the other, are
-// split evenly over the blocks of one wave, whatever the lengths; a unit cut by
-// such a border leaves partial results (maximum, sum, weighted values), which
-// k_pg_join adds up.
+// Work, for both kernels (a plan P: constants V, K, START, LEAST). A unit is up
+// to V query vectors of a sequence (vector i: row i / hpg of its rows, head i %
+// hpg of a group) and a group; its keys are tiles of K positions, and it costs
+// its tiles and START more (queries, filling the pipeline, outputs). The costs of
+// all units, one behind the other, are split evenly over the blocks of one wave
+// (fewer where a block would get less than LEAST), whatever the lengths; a unit
+// whose tiles such a border cuts leaves partial results (maximum, sum, weighted
+// values), which k_pg_join adds up.
 struct PgUnit {
     int slot;      // -1: padding, no tiles
     int row0;      // first row of the sequence in the row tensors
     int pos0;      // its position
     int vec0, nv;  // first vector, and vectors
     int lo, hi;    // positions attended by some vector: lo .. hi
+    int first, last;   // the same of all of the sequence's rows
     template <int K>
     __device__ __forceinline__ int tiles() const {
         return slot < 0 ? 0 : hi / K - lo / K + 1;
@@ -86,7 +89,7 @@ __device__ __forceinline__ PgUnit pg_unit(const PgArgs &a, const PgTable &tab, i
     PgUnit x;
     if (a.pos) {
         const PgRow r = pg_token_row(a, u);
-        x = {r.slot, u, r.pos, 0, a.hpg, 0, 0};
+        x = {r.slot, u, r.pos, 0, a.hpg, 0, 0, 0, r.pos};
     } else {
         int n = 0;
         for (int hi = tab.n - 1; n < hi;) {
@@ -94,28 +97,34 @@ __device__ __forceinline__ PgUnit pg_unit(const PgArgs &a, const PgTable &tab, i
             if (tab.s[mid].before <= u) n = mid;
             else hi = mid - 1;
         }
-        x = {tab.s[n].slot, tab.s[n].row0, tab.s[n].pos0, (u - tab.s[n].before) * V, 0, 0, 0};
+        x = {tab.s[n].slot, tab.s[n].row0, tab.s[n].pos0, (u - tab.s[n].before) * V, 0, 0, 0, 0, tab.s[n].pos0 + tab.s[n].rows - 1};
         x.nv = (int)min((int64_t)V, (int64_t)tab.s[n].rows * a.hpg - x.vec0);
     }
     x.hi = x.pos(a, x.nv - 1);
     x.lo = a.window ? max(0, x.pos(a, 0) - a.window + 1) : 0;
+    x.first = a.window ? max(0, x.pos0 - a.window + 1) : 0;
     return x;
 }
 
-// A block's share of the tiles: `left` of them from tile `skip` of unit u's
-// groups on (group skip / tiles, tile skip % tiles of it). All threads of the
-// block call it; shared: THREADS / 32 + 2 words.
+// A block's share: costs `at` to `to` of all, the next in unit u, whose groups
+// begin at `start`.
 struct PgShare {
-    int u;
-    int64_t skip, left;
+    int64_t at, to, start, total;
+    int u, blocks;   // blocks that get a share
+    __device__ __forceinline__ int64_t border(int b) const { return total * b / blocks; }   // first cost of block b
 };
-template <int V, int K, int THREADS>
+// All threads of the block call it; shared: THREADS / 32 + 2 words.
+template <typename P, int THREADS>
 __device__ __forceinline__ PgShare pg_share(const PgArgs &a, const PgTable &tab, int units, long long *shared) {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = (units + THREADS - 1) / THREADS, u0 = min(units, tid * per), u1 = min(units, u0 + per);
+    auto cost = [&](int u) -> int64_t {
+        const int n = pg_unit<P::V>(a, tab, u).template tiles<P::K>();
+        return n ? (int64_t)(n + P::START) * a.G : 0;
+    };
     long long own = 0;
-    for (int u = u0; u < u1; ++u) own += pg_unit<V>(a, tab, u).template tiles<K>();
+    for (int u = u0; u < u1; ++u) own += cost(u);
     long long before = own;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -130,52 +139,57 @@ __device__ __forceinline__ PgShare pg_share(const PgArgs &a, const PgTable &tab,
         if (w < warp) base += shared[w];
         total += shared[w];
     }
-    total *= a.G;
-    // blocks that get a tile at least (a block without one inside a unit would
-    // break the chain of its partial results)
-    const int64_t nblk = min((long long)gridDim.x, total);
-    const int64_t from = blockIdx.x < nblk ? total * blockIdx.x / nblk : 0;
-    const int64_t to = blockIdx.x < nblk ? total * (blockIdx.x + 1) / nblk : 0;
-    before = (base + before - own) * a.G;   // tiles before this thread's units
-    if (from < to && from >= before && from < before + own * a.G) {
+    PgShare s;
+    s.total = total;
+    s.blocks = (int)min((long long)gridDim.x, max(1ll, total / P::LEAST));
+    s.at = (int)blockIdx.x < s.blocks ? s.border(blockIdx.x) : 0;
+    s.to = (int)blockIdx.x < s.blocks ? s.border(blockIdx.x + 1) : 0;
+    before += base - own;   // costs before this thread's units
+    if (s.at < s.to && s.at >= before && s.at < before + own) {
         int u = u0;
         for (; u + 1 < u1; ++u) {
-            const int64_t n = (int64_t)pg_unit<V>(a, tab, u).template tiles<K>() * a.G;
-            if (from < before + n) break;
+            const int64_t n = cost(u);
+            if (s.at < before + n) break;
             before += n;
         }
         shared[W] = u;
-        shared[W + 1] = from - before;
+        shared[W + 1] = before;
     }
     __syncthreads();
-    return {(int)shared[W], shared[W + 1], to - from};
+    s.u = (int)shared[W];
+    s.start = shared[W + 1];
+    return s;
 }
-// The next segment of a share: tiles t0 .. t1 - 1 of unit u and group g, nt in all.
+// The next segment of a share: tiles t0 .. t1 - 1 of unit u and group g, nt in
+// all; `start`, the cost where the unit begins.
 struct PgSegment {
     int u, g, t0, t1, nt;
+    int64_t start;
     PgUnit x;
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
     // where its partial result goes: a segment that begins inside its unit is
     // its block's first, one that only ends inside it the block's last
     __device__ __forceinline__ int part() const { return blockIdx.x * 2 + (t0 > 0 ? 0 : 1); }
 };
-template <int V, int K>
+template <typename P>
 __device__ __forceinline__ bool pg_next(const PgArgs &a, const PgTable &tab, int units, PgShare &s, PgSegment &o) {
-    while (s.left > 0 && s.u < units) {
-        o.x = pg_unit<V>(a, tab, s.u);
-        o.nt = o.x.template tiles<K>();
-        if (o.nt == 0) {
+    while (s.at < s.to && s.u < units) {
+        o.x = pg_unit<P::V>(a, tab, s.u);
+        o.nt = o.x.template tiles<P::K>();
+        const int64_t each = o.nt ? o.nt + P::START : 0, end = s.start + each * a.G;
+        if (s.at >= end) {   // no tiles, or all of its groups done
             ++s.u;
+            s.start = end;
             continue;
         }
         o.u = s.u;
-        o.g = (int)(s.skip / o.nt);
-        o.t0 = (int)(s.skip - (int64_t)o.g * o.nt);
-        o.t1 = (int)min((int64_t)o.nt, o.t0 + s.left);
-        s.left -= o.t1 - o.t0;
-        s.skip += o.t1 - o.t0;
-        if (s.skip == (int64_t)a.G * o.nt) ++s.u, s.skip = 0;
-        return true;
+        o.g = (int)((s.at - s.start) / each);
+        o.start = s.start + o.g * each;
+        const int64_t to = min(s.to, o.start + each);
+        o.t0 = (int)max((int64_t)0, s.at - o.start - P::START);
+        o.t1 = (int)max((int64_t)0, to - o.start - P::START);
+        s.at = to;
+        if (o.t0 < o.t1) return true;
     }
     return false;
 }
@@ -184,10 +198,9 @@ __device__ __forceinline__ bool pg_next(const PgArgs &a, const PgTable &tab, int
 // the statistics [V][2] (maximum in log2 units, sum) of its first segment and of
 // its last, and in its header the first one's unit.
 struct PgHead {
-    int unit;       // u G + g of a unit that a block before began; -1: none
-    int goes_on;    // whether it goes on in the next block
+    int last;       // the last block with a part of the unit; -1: none begins its tiles in the block before
     int row0, vec0, nv, g;
-    int pad[2];
+    int pad[3];
 };
 struct PgParts {
     PgHead *head;
@@ -199,8 +212,13 @@ __host__ __device__ inline PgParts pg_parts(float *p, int blocks, int vecs) {
 static inline size_t pg_parts_bytes(int blocks, int vecs, int dv) {
     return o1_al256(((size_t)blocks * 8 + (size_t)blocks * 2 * vecs * (2 + dv)) * 4);
 }
-__device__ __forceinline__ void pg_head(PgHead *head, const PgArgs &a, const PgSegment &s) {
-    *head = {s.u * a.G + s.g, s.t1 < s.nt, s.x.row0, s.x.vec0, s.x.nv, s.g, {0, 0}};
+// The header of a block whose first segment is s: it holds the unit where the
+// block's own border is the first inside its tiles.
+template <typename P>
+__device__ __forceinline__ void pg_head(PgHead *head, const PgShare &sh, const PgSegment &s) {
+    if (s.t0 == 0 || sh.border(blockIdx.x - 1) > s.start + P::START) return;
+    const int64_t end = s.start + P::START + s.nt;   // last: border(last + 1) >= end
+    *head = {(int)((end * sh.blocks + sh.total - 1) / sh.total) - 1, s.x.row0, s.x.vec0, s.x.nv, s.g, {0, 0, 0}};
 }
 // A unit's vector in the row tensors.
 __device__ __forceinline__ size_t pg_vec_at(const PgArgs &a, int row0, int vec, int g, size_t stride, int width) {

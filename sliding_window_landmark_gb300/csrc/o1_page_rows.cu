@@ -24,6 +24,9 @@ constexpr int RW = 4, RT = 32 * RW;   // warps and threads of a block
 constexpr int RV = PG_ROWS_V;         // query vectors of a unit
 constexpr int TILE = 16 * RW;         // keys of a tile
 constexpr int PER_SM = 2, BLOCKS = 152 * PER_SM;
+struct Plan {
+    static constexpr int V = RV, K = TILE, START = 2, LEAST = 4;
+};
 
 // Rows of type T over a cache of type C: the MMA's type M, and the terms that q
 // and the weights are split into (a weight in [0, 2^8]): 16-bit rows over their
@@ -157,13 +160,13 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     uint32_t *sq = (uint32_t *)(sm + (size_t)RW * RING * ITEM);   // [term][step][lane][4]
     const C *pk = (const C *)a.k, *pv = (const C *)a.v;
 
-    PgShare share = pg_share<RV, TILE, RT>(a, tab, units, s_share);
+    PgShare share = pg_share<Plan, RT>(a, tab, units, s_share);
     const PgParts parts = pg_parts(a.part, BLOCKS, RV);
-    if (tid == 0) parts.head[blockIdx.x].unit = -1;
+    if (tid == 0) parts.head[blockIdx.x].last = -1;
     const float sc2 = a.scale * 1.4426950408889634f;
     bool first_seg = true;
     PgSegment seg;
-    while (pg_next<RV, TILE>(a, tab, units, share, seg)) {
+    while (pg_next<Plan>(a, tab, units, share, seg)) {
         const PgUnit &x = seg.x;
         const int g = seg.g;
         // ---- queries, in the MMA's A layout of this lane order
@@ -473,45 +476,81 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 if (c == 0) *(float2 *)(parts.stat + (ps * RV + v) * 2) = make_float2(mx, sum);
             }
         }
-        if (tid == 0 && first_seg && seg.t0 > 0) pg_head(&parts.head[blockIdx.x], a, seg);
+        if (tid == 0 && first_seg) pg_head<Plan>(&parts.head[blockIdx.x], share, seg);
         first_seg = false;
     }
 }
 
 // The partial results of a unit that borders cut, added up by the blocks of the
-// first border inside it, a warp a vector.
-constexpr int JOIN_WARPS = 4;
-template <typename T>
-__global__ __launch_bounds__(32 * JOIN_WARPS) void k_pg_join(PgArgs a, int blocks, int vecs) {
+// first border inside it. TPV threads a vector, 4 columns each, and eight parts
+// in flight: what it takes is the latency of three loads one behind the other.
+// SPLIT: one vector a block, its parts dealt to JOIN / TPV groups of threads
+// (few vectors, many parts); otherwise JOIN / TPV vectors a block.
+constexpr int JOIN = 256;
+struct Sum {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void add(float2 st, float4 y) {
+        const float mn = fmaxf(m, st.x);
+        const float f = m > -INFINITY ? exp2f(m - mn) : 0.f, h = st.x > -INFINITY ? exp2f(st.x - mn) : 0.f;
+        m = mn;
+        l = l * f + st.y * h;
+        o.x = o.x * f + y.x * h;
+        o.y = o.y * f + y.y * h;
+        o.z = o.z * f + y.z * h;
+        o.w = o.w * f + y.w * h;
+    }
+};
+template <typename T, int TPV, bool SPLIT>
+__global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs) {
+    constexpr int GROUPS = JOIN / TPV, U = 8;
+    __shared__ Sum part[SPLIT ? JOIN : 1];
     o1_chain_wait();
-    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1, grp = threadIdx.x / TPV, col = 4 * (threadIdx.x % TPV);
     const PgParts parts = pg_parts(a.part, blocks, vecs);
     const PgHead h = parts.head[c];
-    if (h.unit < 0) return;
-    if (parts.head[c - 1].unit == h.unit && parts.head[c - 1].goes_on) return;   // the border before is in it too
-    int last = c;
-    while (last + 1 < blocks && parts.head[last].goes_on) ++last;
-    for (int v = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); v < h.nv; v += gridDim.y * JOIN_WARPS) {
-        auto at = [&](int i) { return (size_t)(i == c - 1 ? 2 * i + 1 : 2 * i) * vecs + v; };
-        float mx = -INFINITY;
-        for (int i = c - 1 + lane; i <= last; i += 32) mx = fmaxf(mx, parts.stat[at(i) * 2]);
-        mx = warp_max(mx);
-        for (int col = 4 * lane; col < a.dv; col += 128) {
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-#pragma unroll 4
-            for (int i = c - 1; i <= last; ++i) {
-                const float2 st = *(const float2 *)(parts.stat + at(i) * 2);
-                const float f = st.x > -INFINITY ? exp2f(st.x - mx) : 0.f;
-                const float4 y = *(const float4 *)(parts.val + at(i) * a.dv + col);
-                sum = fmaf(f, st.y, sum);
-                o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+    const int v = SPLIT ? blockIdx.y : blockIdx.y * GROUPS + grp;
+    if (h.last < 0 || (SPLIT && v >= h.nv)) return;
+    const bool in = v < h.nv && col < a.dv;
+    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    constexpr int STEP = SPLIT ? GROUPS : 1;
+    if (in)
+        for (int i0 = c - 1 + (SPLIT ? grp : 0); i0 <= h.last; i0 += U * STEP) {
+            float2 st[U];
+            float4 y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * STEP;
+                const size_t at = (size_t)(i == c - 1 ? 2 * i + 1 : 2 * i) * vecs + v;
+                if (i <= h.last) st[u] = *(const float2 *)(parts.stat + at * 2), y[u] = *(const float4 *)(parts.val + at * a.dv + col);
             }
-            const float r = sum == 0.f ? 0.f : 1.f / sum;   // a NaN stays one
-            o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + col,
-                   make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * STEP <= h.last) s.add(st[u], y[u]);
+        }
+    if (SPLIT) {
+        part[threadIdx.x] = s;
+        __syncthreads();
+        if (grp) return;
+        for (int g = 1; g < GROUPS; ++g) {
+            const Sum &o = part[g * TPV + threadIdx.x];
+            s.add(make_float2(o.m, o.l), o.o);
         }
     }
+    if (!in) return;
+    const float r = s.l == 0.f ? 0.f : 1.f / s.l;   // a NaN stays one
+    o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + col, make_float4(s.o.x * r, s.o.y * r, s.o.z * r, s.o.w * r));
+}
+template <typename T, int TPV>
+void join_launch(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
+    if (vecs <= PG_ROWS_V) o1_launch_chained(true, k_pg_join<T, TPV, true>, dim3(blocks - 1, vecs), dim3(JOIN), 0, st, a, blocks, vecs);
+    else o1_launch_chained(true, k_pg_join<T, TPV, false>, dim3(blocks - 1, (vecs + JOIN / TPV - 1) / (JOIN / TPV)), dim3(JOIN), 0, st, a, blocks, vecs);
+}
+template <typename T>
+void join_launch_t(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
+    if (a.dv <= 64) join_launch<T, 16>(a, blocks, vecs, st);
+    else if (a.dv <= 128) join_launch<T, 32>(a, blocks, vecs, st);
+    else join_launch<T, 64>(a, blocks, vecs, st);
 }
 
 template <typename T, typename C, int N>
@@ -547,12 +586,9 @@ cudaError_t rows_launch_c(const PgArgs &a, const PgTable *tab, int units, cudaSt
 size_t pg_rows_scratch(int dv) { return pg_parts_bytes(BLOCKS, RV, dv); }
 
 cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, cudaStream_t st) {
-    // a warp a vector for narrow units; wide ones in a few turns
-    const int most = (vecs + JOIN_WARPS - 1) / JOIN_WARPS;
-    const dim3 grid(blocks - 1, most < 8 ? most : 8);
-    if (dtype == O1_F32) o1_launch_chained(true, k_pg_join<float>, grid, dim3(32 * JOIN_WARPS), 0, st, a, blocks, vecs);
-    else if (dtype == O1_BF16) o1_launch_chained(true, k_pg_join<__nv_bfloat16>, grid, dim3(32 * JOIN_WARPS), 0, st, a, blocks, vecs);
-    else o1_launch_chained(true, k_pg_join<__half>, grid, dim3(32 * JOIN_WARPS), 0, st, a, blocks, vecs);
+    if (dtype == O1_F32) join_launch_t<float>(a, blocks, vecs, st);
+    else if (dtype == O1_BF16) join_launch_t<__nv_bfloat16>(a, blocks, vecs, st);
+    else join_launch_t<__half>(a, blocks, vecs, st);
     return cudaGetLastError();
 }
 
@@ -565,5 +601,5 @@ cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const Pg
     else if (dtype == O1_BF16) e = rows_launch_c<__nv_bfloat16, uint8_t>(a, tab, units, st);
     else if (cache_dtype == O1_F16) e = rows_launch_c<__half, __half>(a, tab, units, st);
     else e = rows_launch_c<__half, uint8_t>(a, tab, units, st);
-    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, RV, st) : e;
+    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, RV, st) : e;   // partial results of RV vectors' room
 }

@@ -43,9 +43,13 @@ constexpr int SM_WARPS = 8, PR_WARPS = 4;      // softmax and producer warps
 constexpr int THREADS = 32 * (SM_WARPS + PR_WARPS + 4), SM_THREADS = 32 * SM_WARPS;   // the issuer's warpgroup has three idle warps
 constexpr int SLOT = 32768, MAX_SLOTS = 6;
 constexpr int BLOCKS = 152;
-constexpr int LAG = 2;                         // items that a producer has in flight beyond the one it issues
 constexpr float HEADROOM = 8.f;                // log2 units above the reference before it moves
 constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside it
+
+template <int QT>
+struct Plan {
+    static constexpr int V = 128 * QT, K = KT, START = 2, LEAST = 4;
+};
 
 template <typename T, typename C>
 struct Types {   // 16-bit rows over their own type
@@ -78,7 +82,7 @@ struct Types<__half, uint8_t> {
 constexpr int REGS = 128;
 template <bool E4>
 struct Regs {
-    static constexpr int PRODUCER = E4 ? 104 : 72, ISSUER = 72, SOFTMAX = E4 ? 168 : 184;
+    static constexpr int PRODUCER = E4 ? 104 : 88, ISSUER = 72, SOFTMAX = E4 ? 168 : 176;
     static_assert(2 * SOFTMAX + PRODUCER + ISSUER <= 4 * REGS, "no more than the block has");
 };
 template <int N>
@@ -144,6 +148,18 @@ __device__ __forceinline__ void copy_wait() {
 __device__ __forceinline__ void st16(uint32_t dst, const uint4 &v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ void tma_2d_at(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(x), "r"(y), "r"(su32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d_at(uint32_t dst, const CUtensorMap *map, int x, int y, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(x), "r"(y), "r"(w), "r"(su32(bar))
+        : "memory");
+}
 // Byte of 16-byte piece p (0 to 7) of row r in a panel of 128-byte rows.
 __device__ __forceinline__ uint32_t piece(int r, int p) { return (uint32_t)(128 * r + 16 * (p ^ (r & 7))); }
 
@@ -160,6 +176,32 @@ __device__ __forceinline__ uint4 bf16_of_e4m3(uint2 c, __nv_bfloat162 f) {
         w[i] = *(const uint32_t *)&y;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two fp32 values in a register pair: packed operations take one issue for both.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
 }
 
 struct Shared {
@@ -222,123 +264,191 @@ __device__ __forceinline__ bool sm_or(bool p) {
 template <typename T, typename C, int QT>
 struct Producer {
     using M = typename Types<T, C>::M;
-    static constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    static constexpr int TERMS = Types<T, C>::TERMS;
     static constexpr bool E4 = sizeof(C) == 1, Q_COPY = TERMS == 1 && sizeof(T) == 2;
     const PgArgs &a;
     Shared &sh;
     const Shape &z;
     uint32_t q0, ring0;   // shared addresses
     int lane, r4, l8;     // r4: this thread's row of each 16, l8: its place among the 8 threads of a row
+    const CUtensorMap *mq, *mk, *mv;   // for TMA: queries (null: not in boxes), and the pools of a 16-bit cache
+    int qrows;            // rows of a query box
+    int wid;              // this warp among the producers
     Ring put;             // slot of the next item
-    Ring tell;            // of the next to be announced
-    int out;              // items issued and not announced
     bool ok;
 
-    __device__ __forceinline__ void announce() {   // the oldest item is in shared memory
+    // 16-bit caches: the first warp alone waits and issues boxes; where all four
+    // copy, a barrier before says whether its wait was met, and one after lets it
+    // announce. Its wait may run out between two such places, so it goes on to
+    // the next one, where all learn of it (`ok`). e4m3: every warp waits and
+    // arrives for itself.
+    bool met;             // the first warp: its waits were met so far
+    int sent;             // its items
+    uint32_t qp;          // phase of q_free
+    bool q_sent;
+    __device__ __forceinline__ bool master() const { return wid == 0; }
+    __device__ __forceinline__ void sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * PR_WARPS) : "memory"); }
+    __device__ __forceinline__ bool any_of(bool p) {   // of the producers' threads
+        int r;
+        asm volatile(
+            "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\nbar.red.or.pred q, 2, %2, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+            : "=r"(r)
+            : "r"((int)p), "n"(32 * PR_WARPS)
+            : "memory");
+        return r != 0;
+    }
+    __device__ __forceinline__ void agree() { ok = !any_of(master() && !met); }
+    __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity) {
+        if (E4) ok = ok && warp_wait(bar, parity, &sh.abort, a.wait_cycles);
+        else if (master()) met = met && warp_wait(bar, parity, &sh.abort, a.wait_cycles);
+    }
+    // all warps' copies are in shared memory
+    __device__ __forceinline__ void announce(uint64_t *bar) {
+        copy_commit();
+        copy_wait<0>();
         fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[tell.slot]);
-        tell.next(z.nslot);
-        --out;
-    }
-    __device__ __forceinline__ bool take() {
-        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles);
-        return ok;
-    }
-    __device__ __forceinline__ void issued() {
-        put.next(z.nslot);
-        ++out;
-        if (E4) {
-            announce();
-        } else {
-            copy_commit();
-            if (out > LAG) {
-                copy_wait<LAG>();
-                announce();
-            }
-        }
-    }
-    __device__ __forceinline__ void flush() {
-        if (!E4) copy_wait<0>();
-        while (out) announce();
+        if (E4) __syncwarp();
+        else sync();
+        if (lane == 0 && (E4 || master())) mbar_arrive(bar);
     }
 
-    // The query tiles: row v of the unit's vectors, its values as terms.
+    // The query tiles: row v of the unit's vectors, its values as terms. Where
+    // a group's heads are a power of two, a tile's vectors are whole rows of heads
+    // and come as boxes (rows past the sequence's are not used).
     __device__ __forceinline__ void queries(const PgSegment &s) {
         const int tiles = QT == 2 && s.x.nv > 128 ? 2 : 1, pieces = 2 * z.ksteps;   // 16-byte pieces of a row
+        if (Q_COPY && mq) {
+            const int n = z.nqc * tiles;
+            if (master() && met) {
+                if (lane == 0) mbar_expect_tx(&sh.q_full, 16384 * n);
+                __syncwarp();
+                if (lane < n) {
+                    const int tile = lane / z.nqc, c = lane - tile * z.nqc;
+                    tma_3d_at(q0 + 16384 * lane, mq, 64 * c, s.g * a.hpg, s.x.row0 + s.x.vec0 / a.hpg + tile * qrows, &sh.q_full);
+                }
+                __syncwarp();
+                q_sent = true;
+            }
+            return;
+        }
+        if (!E4) {
+            agree();
+            if (!ok) return;
+        }
+        constexpr int U = TERMS == 1 ? 4 : 2;   // rows in flight
 #pragma unroll 1
-        for (int r0 = 0; r0 < 128 * tiles; r0 += 16) {
-            const int v = r0 + r4, row = v & 127;
-            const bool in = v < s.x.nv;
-            const T *src = (const T *)a.q + (in ? pg_vec_at(a, s.x.row0, s.x.vec0 + v, s.g, a.qs, a.d) : 0);
-            const uint32_t dst = q0 + (uint32_t)((v >> 7) * z.nqc) * 16384;
+        for (int r0 = 0; r0 < 128 * tiles; r0 += 16 * U) {
+            const T *src[U];
+            bool in[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = r0 + 16 * u + r4;
+                in[u] = v < s.x.nv;
+                src[u] = (const T *)a.q + (in[u] ? pg_vec_at(a, s.x.row0, s.x.vec0 + v, s.g, a.qs, a.d) : 0) + 8 * l8;
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int p = 8 * c + l8;
-                if (p >= pieces) continue;
-                const bool on = in && 8 * p < a.d;
-                const uint32_t at = dst + c * 16384 + piece(row, l8);
+                if (8 * c >= pieces) break;
                 if constexpr (Q_COPY) {
-                    copy16(at, on ? (const void *)(src + 8 * p) : a.q, on);
-                } else {
-                    float x[8];
-                    if (on) {
-                        const float4 f0 = o1_ld4(src + 8 * p), f1 = o1_ld4(src + 8 * p + 4);
-                        x[0] = f0.x; x[1] = f0.y; x[2] = f0.z; x[3] = f0.w;
-                        x[4] = f1.x; x[5] = f1.y; x[6] = f1.z; x[7] = f1.w;
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                    for (int u = 0; u < U; ++u) {
+                        const int v = r0 + 16 * u + r4;
+                        const bool on = in[u] && 8 * p < a.d;
+                        if (p < pieces)
+                            copy16(q0 + (uint32_t)((v >> 7) * z.nqc + c) * 16384 + piece(v & 127, l8), on ? (const void *)(src[u] + 64 * c) : a.q, on);
+                    }
+                } else {
+                    float4 f[U][2];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        f[u][0] = f[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (in[u] && 8 * p < a.d) f[u][0] = o1_ld4(src[u] + 64 * c), f[u][1] = o1_ld4(src[u] + 64 * c + 4);
                     }
 #pragma unroll
-                    for (int t = 0; t < TERMS; ++t) {
-                        uint32_t w[4];
+                    for (int u = 0; u < U; ++u) {
+                        const int v = r0 + 16 * u + r4;
+                        float x[8] = {f[u][0].x, f[u][0].y, f[u][0].z, f[u][0].w, f[u][1].x, f[u][1].y, f[u][1].z, f[u][1].w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = take_m<M>(x[2 * i], x[2 * i + 1]);
-                        st16(at + (uint32_t)(t * QT * z.nqc) * 16384, make_uint4(w[0], w[1], w[2], w[3]));
+                        for (int t = 0; t < TERMS; ++t) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = take_m<M>(x[2 * i], x[2 * i + 1]);
+                            if (p < pieces)
+                                st16(q0 + (uint32_t)((t * QT + (v >> 7)) * z.nqc + c) * 16384 + piece(v & 127, l8),
+                                     make_uint4(w[0], w[1], w[2], w[3]));
+                        }
                     }
                 }
             }
         }
-        if (Q_COPY) {
-            copy_commit();
-            copy_wait<0>();
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full);
+        announce(&sh.q_full);
     }
 
     // The pages of a tile's eight runs of 16 positions, run i in lanes i, i + 8, ...
     __device__ __forceinline__ int pages(const PgSegment &s, int j) const {
         const int p = (s.x.lo / KT + j) * KT + 16 * (lane & 7);
-        return j < s.t1 && p <= s.x.hi && p + 15 >= s.x.lo ? pg_page(a, s.x.slot, p) : -1;
+        return j < s.t1 && p <= s.x.last && p + 15 >= s.x.first ? pg_page(a, s.x.slot, p) : -1;
     }
 
     // An item of the tile: keys (128 columns) or values (v_keys rows). 16 rows
     // at a time; a thread has the same row of each 16.
+    // By TMA where every position of it is in the sequence and on a page: a lane
+    // a box of the item's rows on one page and 64 columns (at most 16).
     template <bool KEYS>
-    __device__ __forceinline__ void item(const PgSegment &s, int j, int ids, int part) {
-        if (!take()) return;
+    __device__ __forceinline__ void item(const PgSegment &s, int j, int ids, int part, bool boxes) {
+        if (!ok) return;
+        wait_for(&sh.empty[put.slot], put.phase ^ 1);
+        if (E4 && !ok) return;
         const int width = KEYS ? a.d : a.dv, col0 = KEYS ? 128 * part : 0, key0 = KEYS ? 0 : z.v_keys * part;
         const int rows = KEYS ? 128 : z.v_keys, runs = rows / 16;
         const int cols = min(KEYS ? 128 : 256, (width + 15) / 16 * 16 - col0);   // to be filled
         const int p0 = (s.x.lo / KT + j) * KT + key0;
         const uint32_t dst = ring0 + put.slot * SLOT;
         const C *pool = (const C *)(KEYS ? a.k : a.v);
+        uint64_t *full = &sh.full[put.slot];
         if constexpr (!E4) {
             const int blocks = (cols + 63) / 64;
+            if (boxes) {
+                if (master() && met) {
+                    const int lrows = min(a.lpage, KEYS || z.v_keys == 128 ? 7 : 6), brows = 1 << lrows;   // rows of a box
+                    const int n = blocks * (rows >> lrows), run = lane / blocks, b = lane - run * blocks;
+                    const int page = __shfl_sync(0xffffffffu, ids, (key0 + (run << lrows)) / 16 & 7);
+                    if (lane == 0) mbar_expect_tx(full, n * brows * 128);
+                    __syncwarp();
+                    if (lane < n) {
+                        const int p = p0 + (run << lrows);
+                        tma_2d_at(dst + b * (rows * 128) + (run << lrows) * 128, KEYS ? mk : mv, col0 + 64 * b,
+                                  ((page * a.G + s.g) << a.lpage) + (p & ((1 << a.lpage) - 1)), full);
+                    }
+                    __syncwarp();
+                    ++sent;
+                }
+                if (met) put.next(z.nslot);   // the first warp stays at the item it could not send
+                return;
+            }
+            agree();
+            if (!ok) return;
+            constexpr int U = 4;   // runs in flight
 #pragma unroll 1
-            for (int i = 0; i < runs; ++i) {
-                const int page = __shfl_sync(0xffffffffu, ids, key0 / 16 + i), p = p0 + 16 * i + r4;
-                const bool in = page >= 0 && p >= s.x.lo && p <= s.x.hi;
-                const C *src = pg_at(pool, a, max(page, 0), s.g, p & ((1 << a.lpage) - 1), width) + col0;
+            for (int i0 = 0; i0 < runs; i0 += U) {
+                const C *src[U];
+                bool in[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int page = __shfl_sync(0xffffffffu, ids, key0 / 16 + i0 + u), p = p0 + 16 * (i0 + u) + r4;
+                    in[u] = page >= 0 && p >= s.x.lo && p <= s.x.hi;
+                    src[u] = pg_at(pool, a, max(page, 0), s.g, p & ((1 << a.lpage) - 1), width) + col0 + 8 * l8;
+                }
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const int c = 64 * b + 8 * l8;
-                    if (b >= blocks || c >= cols) continue;
-                    const bool on = in && col0 + c < width;
-                    copy16(dst + b * (rows * 128) + piece(16 * i + r4, l8), on ? src + c : pool, on);
+                    if (64 * b >= cols) break;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool on = in[u] && col0 + c < width;
+                        if (c < cols) copy16(dst + b * (rows * 128) + piece(16 * (i0 + u) + r4, l8), on ? src[u] + 64 * b : pool, on);
+                    }
                 }
             }
         } else {
@@ -384,47 +494,100 @@ struct Producer {
                 }
             }
         }
-        issued();
+        announce(full);
+        put.next(z.nslot);
+        ++sent;
     }
 
     __device__ __forceinline__ void run(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
-        uint32_t qp = 1;
-        while (ok && pg_next<V, KT>(a, tab, units, share, s)) {
+        while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
+            // a tile of a 16-bit cache comes in boxes where some row of the
+            // sequence attends every position of it (outside, memory may hold
+            // anything); the warps decide together, whatever each read of the table
+            auto boxes = [&](int j, int id) -> bool {
+                if (E4 || j >= s.t1) return false;
+                const int x0 = (s.x.lo / KT + j) * KT;
+                return !any_of(!(x0 >= s.x.first && x0 + KT - 1 <= s.x.last && __all_sync(0xffffffffu, id >= 0)));
+            };
+            // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
+            auto keys = [&](int j, int id, bool bx) {
+                for (int p = 0; ok && p < z.k_items; ++p) item<true>(s, j, id, p, bx);
+            };
+            auto values = [&](int j, int id, bool bx) {
+                for (int p = 0; ok && p < z.v_items; ++p) item<false>(s, j, id, p, bx);
+            };
             int ids = pages(s, s.t0), ids1 = pages(s, s.t0 + 1);
-            flush();   // the scores that free the queries may need an item not announced yet
-            ok = warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
+            bool bx = boxes(s.t0, ids), bx1;
+            keys(s.t0, ids, bx);   // before the queries, whose place the segment before may still hold
+            wait_for(&sh.q_free, qp);
             if (!ok) break;
             qp ^= 1;
             queries(s);
-            // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
-            auto keys = [&](int j, int id) {
-                for (int p = 0; ok && p < z.k_items; ++p) item<true>(s, j, id, p);
-            };
-            auto values = [&](int j, int id) {
-                for (int p = 0; ok && p < z.v_items; ++p) item<false>(s, j, id, p);
-            };
-            keys(s.t0, ids);
             for (int j = s.t0; ok && j < s.t1; ++j) {
                 const int ids2 = pages(s, j + 2);
-                if (QT == 1 && j + 1 < s.t1) keys(j + 1, ids1);
-                values(j, ids);
-                if (QT == 2 && j + 1 < s.t1) keys(j + 1, ids1);
+                bx1 = boxes(j + 1, ids1);
+                if (QT == 1 && j + 1 < s.t1) keys(j + 1, ids1, bx1);
+                values(j, ids, bx);
+                if (QT == 2 && j + 1 < s.t1) keys(j + 1, ids1, bx1);
                 ids = ids1;
                 ids1 = ids2;
+                bx = bx1;
             }
         }
-        flush();
+        if (E4 || !master() || (ok && met)) return;
+        // after a wait that ran out: what TMA still writes lands before the block ends
+        if (lane == 0) {
+            if (q_sent) mbar_drain(&sh.q_full, qp);
+            Ring r = put;
+            const int back = min(sent, z.nslot);
+            for (int i = 0; i < back; ++i) {
+                if (--r.slot < 0) r.slot = z.nslot - 1, r.phase ^= 1;
+                mbar_drain(&sh.full[r.slot], r.phase);
+            }
+        }
+        __syncwarp();
     }
 };
 
 // ------------------------------------------------------------- MMA issuer
 
+// The MMAs of n k16 steps of a score, and of 64 keys of P V. The whole warp takes
+// the loops and the elected lane (`e`) the MMAs, with carried operands: warp-
+// uniform control flow keeps them in uniform registers, and an MMA issues at
+// its rate (from one lane's unrolled branch a step of 32 took 3700 cycles).
+__device__ __forceinline__ void run_ss(bool e, uint32_t col, uint64_t qd, uint64_t kd, uint32_t id, int n, uint32_t acc) {
+#pragma unroll 1
+    for (; n > 0; n -= 4, qd += 1024, kd += 1024) {   // a 64-column block
+        uint64_t q = qd, k = kd;
+#pragma unroll 1
+        for (int x = min(4, n); x > 0; --x) {
+            if (e) mma_ss(col, q, k, id, acc);
+            q += 2;
+            k += 2;
+            acc = 1;
+        }
+    }
+}
+template <int TERMS>
+__device__ __forceinline__ void run_ts(bool e, uint32_t out, uint32_t p, uint64_t vd, uint32_t id, uint32_t acc) {
+#pragma unroll 1
+    for (int x = 4; x > 0; --x) {
+#pragma unroll
+        for (int m = TERMS - 1; m >= 0; --m) {
+            if (e) mma_ts(out, p + 32 * m, vd, id, acc);
+            acc = 1;
+        }
+        p += 8;
+        vd += 128;
+    }
+}
+
 template <typename T, typename C, int QT>
 __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape &z, uint32_t q0, uint32_t ring0, uint32_t tmem,
                                        const PgTable &tab, int units, PgShare share) {
     using M = typename Types<T, C>::M;
-    constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    constexpr int TERMS = Types<T, C>::TERMS;
     using Col = Cols<TERMS>;
     const bool e = elect_one();
     const uint64_t dq = desc_sw128(q0), dk = desc_sw128(ring0), dv = desc_sw128_mn(ring0, z.v_keys * 128);
@@ -452,9 +615,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 if (!filled(r)) return;
                 tc_after();
                 const uint64_t kd = dk + (uint64_t)(r.slot * (SLOT / 16)), qd = dq + (uint64_t)((t * z.nqc + 2 * i) * 1024);
-                const int n = min(8, z.ksteps - 8 * i);
-                for (int x = 0; x < n; ++x)
-                    if (e) mma_ss(col, qd + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s, i + x > 0);
+                run_ss(e, col, qd, kd, id_s, min(8, z.ksteps - 8 * i), i > 0);
                 if (QT == 1) commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
@@ -469,9 +630,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 for (int i = 0; i < z.k_items; ++i, q.next(z.nslot)) {
                     const uint64_t kd = dk + (uint64_t)(q.slot * (SLOT / 16));
                     const uint64_t qd = dq + (uint64_t)(((m * QT + t) * z.nqc + 2 * i) * 1024);
-                    const int n = min(8, z.ksteps - 8 * i);
-                    for (int x = 0; x < n; ++x)
-                        if (e) mma_ss(col, qd + (x >> 2) * 1024 + 2 * (x & 3), kd + (x >> 2) * 1024 + 2 * (x & 3), id_s, m < TERMS - 1 || i + x > 0);
+                    run_ss(e, col, qd, kd, id_s, min(8, z.ksteps - 8 * i), m < TERMS - 1 || i > 0);
                 }
             }
             q = r;
@@ -486,20 +645,17 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
             if (!filled(r)) return;
             tc_after();
             const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
+            // lower terms first
             for (int m = 2; m >= 0; --m)
-                for (int k = 0; k < 8; ++k)
-                    if (e) mma_ts(out, p + Col::p(k, m), vd + 128 * k, id_o, m < 2 || k > 0);
+                for (int h = 0; h < 2; ++h) run_ts<1>(e, out, p + Col::p(4 * h, m), vd + 512 * h, id_o, m < 2 || h > 0);
             commit(&sh.empty[r.slot]);
         } else {
-            const int steps = z.v_keys / 16;
             for (int i = 0; i < z.v_items; ++i) {
                 if (!filled(r)) return;
                 tc_after();
                 const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
-                for (int x = 0; x < steps; ++x)
-#pragma unroll
-                    for (int m = TERMS - 1; m >= 0; --m)
-                        if (e) mma_ts(out, p + Col::p(i * steps + x, m), vd + 128 * x, id_o, acc || i + x > 0 || m < TERMS - 1);
+                run_ts<TERMS>(e, out, p + 64 * i, vd, id_o, acc || i > 0);
+                if (z.v_items == 1) run_ts<TERMS>(e, out, p + 64, vd + 512, id_o, 1);
                 if (release) commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
@@ -509,7 +665,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
     auto advance = [&](int n) {
         for (int i = 0; i < n; ++i) get.next(z.nslot);
     };
-    while (ok && pg_next<V, KT>(a, tab, units, share, s)) {
+    while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
         ok = warp_wait(&sh.q_full, qp, &sh.abort, wl);
         if (!ok) break;
         qp ^= 1;
@@ -592,24 +748,28 @@ template <typename T, typename C, int QT>
 __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape &z, uint32_t tmem, const PgTable &tab, int units,
                                         PgShare share, int vecs) {
     using M = typename Types<T, C>::M;
-    constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+    constexpr int TERMS = Types<T, C>::TERMS;
     constexpr bool REG = TERMS == 3;   // sums in registers
     using Col = Cols<TERMS>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float sc2 = a.scale * 1.4426950408889634f;   // scores in log2 units; scale > 0
     const long long wl = a.wait_cycles;
-    const PgParts parts = pg_parts(a.part, BLOCKS, vecs);
-    if (tid == 0) parts.head[blockIdx.x].unit = -1;
-    bool ok = true, first = true;
+    if (tid == 0) {
+        PgHead *head = &pg_parts(a.part, BLOCKS, vecs).head[blockIdx.x];
+        head->last = -1;
+        PgShare first = share;
+        PgSegment f;
+        if (pg_next<Plan<QT>>(a, tab, units, first, f)) pg_head<Plan<QT>>(head, share, f);
+    }
+    __syncwarp();
+    bool ok = true;
     uint32_t n = 0;   // tiles so far, of this warpgroup's query tile
     PgSegment s;
-    while (pg_next<V, KT>(a, tab, units, share, s)) {
-        if (tid == 0 && first && s.t0 > 0) pg_head(&parts.head[blockIdx.x], a, s);
-        first = false;
-        const int tile = QT == 2 ? wg : 0, v0 = 128 * tile, v = v0 + row;
+    while (pg_next<Plan<QT>>(a, tab, units, share, s)) {
+        const int tile = QT == 2 ? wg : 0, v0 = 128 * tile;
         if (QT == 2 && s.x.nv <= v0) continue;
-        const int pos = s.x.pos(a, min(v, s.x.nv - 1)), low = a.window ? pos - a.window + 1 : 0;
+        const int pos = s.x.pos(a, min(v0 + row, s.x.nv - 1)), low = a.window ? pos - a.window + 1 : 0;
         // positions that every row of the tile attends
         const int plain_hi = s.x.pos(a, v0), last = s.x.pos(a, min(v0 + 127, s.x.nv - 1));
         const int plain_lo = a.window ? last - a.window + 1 : 0;
@@ -620,11 +780,13 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
 #pragma unroll
             for (int i = 0; i < (REG ? 64 : 1); ++i) o[i] = 0.f;
         }
-        auto ids = [&](int j) {   // whether a run of 16 positions has a page
-            const int p = (s.x.lo / KT + j) * KT + 16 * (lane & 7);
-            return j >= s.t1 || p > s.x.hi || p + 15 < s.x.lo || pg_page(a, s.x.slot, p) >= 0;
+        // which runs of 16 positions have a page: four tiles a look, a lane a run
+        auto look = [&](int j) {
+            const int p = (s.x.lo / KT + j) * KT + 16 * lane;
+            return j + (lane >> 3) >= s.t1 || p > s.x.hi || p + 15 < s.x.lo || pg_page(a, s.x.slot, p) >= 0;
         };
-        bool next_there = ids(s.t0);
+        bool next_runs = look(s.t0);
+        uint32_t runs = 0;
         // P V of the tile before (number t), added to this warpgroup's columns
         auto add_values = [&](uint32_t t) {
             ok = ok && warp_wait(&sh.pv_done[0], t & 1, &sh.abort, wl);
@@ -643,8 +805,12 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             if (lane == 0) mbar_arrive(&sh.o_free[0]);
         };
         for (int j = s.t0; ok && j < s.t1; ++j, ++n) {
-            const uint32_t there = __ballot_sync(0xffffffffu, next_there) & 0xffu;
-            next_there = ids(j + 1);
+            if (((j - s.t0) & 3) == 0) {
+                runs = __ballot_sync(0xffffffffu, next_runs);
+                next_runs = look(j + 4);
+            }
+            const uint32_t there = runs & 0xffu;
+            runs >>= 8;
             const int x0 = (s.x.lo / KT + j) * KT, buf = QT == 2 ? tile : n & 1;
             const bool plain = x0 >= plain_lo && x0 + KT - 1 <= plain_hi && there == 0xffu;
             ok = warp_wait(&sh.s_full[buf], QT == 2 ? n & 1 : (n >> 1) & 1, &sh.abort, wl);
@@ -652,23 +818,25 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             tc_after();
             if (REG && j > s.t0) add_values(n - 1);
             const uint32_t scol = lanes + Col::score(buf);
+            // raw scores of 64 keys, those not attended -inf (all 128 of QT = 2
+            // at once did not fit the registers: the first half is loaded twice)
             uint32_t r[64];
-            // raw scores of 64 keys, those not attended -inf
             auto load = [&](int h) {
                 TMEM_LD32(scol + 64 * h, (&r[0]));
                 TMEM_LD32(scol + 64 * h + 32, (&r[32]));
                 tmem_ld_wait();
                 if (!plain) {
                     const int b0 = low - x0 - 64 * h, b1 = pos - x0 - 64 * h;
+                    const uint32_t on = there >> (4 * h);
 #pragma unroll
                     for (int c = 0; c < 64; ++c)
-                        if (c < b0 || c > b1 || !(there >> (4 * h + c / 16) & 1)) r[c] = 0xff800000u;
+                        if (c < b0 || c > b1 || !(on >> (c / 16) & 1)) r[c] = 0xff800000u;
                 }
             };
             auto top_of = [&]() {
                 float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 64; ++c) t[c & 3] = fmaxf(t[c & 3], __uint_as_float(r[c]));
+                for (int c = 0; c < 64; c += 2) t[(c / 2) & 3] = max3(t[(c / 2) & 3], r[c], r[c + 1]);
                 return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
             };
             float top = -INFINITY;
@@ -724,18 +892,20 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             // P over the scores it comes from
             if (!idle) {
                 const float ref = m > -INFINITY ? m : 0.f;
+                const F2 f2s = f2(sc2, sc2), f2r = f2(-ref, -ref);
+                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                constexpr int W = TERMS == 1 ? 32 : 16;   // words at a time, 2 keys each
                 auto store = [&](int h) {
-                    float sum[2] = {0.f, 0.f};
-                    constexpr int W = TERMS == 1 ? 32 : 16;   // words at a time, 2 keys each
 #pragma unroll
                     for (int i = 0; i < 32; i += W) {
                         uint32_t w[W], w1[W], w2[W];
 #pragma unroll
                         for (int c = 0; c < W; ++c) {
-                            float x = ex2(fmaf(__uint_as_float(r[2 * (i + c)]), sc2, -ref));
-                            float y = ex2(fmaf(__uint_as_float(r[2 * (i + c) + 1]), sc2, -ref));
-                            sum[0] += x;
-                            sum[1] += y;
+                            float x, y;
+                            f2_get(f2_fma(f2(__uint_as_float(r[2 * (i + c)]), __uint_as_float(r[2 * (i + c) + 1])), f2s, f2r), x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            sum[c & 1] = f2_add(sum[c & 1], f2(x, y));
                             if constexpr (TERMS == 1) {
                                 w[c] = pack_m((const M *)nullptr, x, y);
                             } else {
@@ -753,7 +923,6 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                             if constexpr (TERMS > 2) TMEM_ST16(scol + 128 + 32 * h + i, w2);
                         }
                     }
-                    l += sum[0] + sum[1];
                 };
                 if (QT == 2) {
                     store(1);
@@ -762,6 +931,10 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                 } else {
                     store(wg);
                 }
+                float a0, a1, b0, b1;
+                f2_get(sum[0], a0, a1);
+                f2_get(sum[1], b0, b1);
+                l += (a0 + a1) + (b0 + b1);
             }
             tmem_st_wait();
             tc_before();
@@ -784,10 +957,16 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             l += sh.half[wg ^ 1][row];
             sm_sync();
         }
-        const bool whole = s.whole(), in = v < s.x.nv;
+        // the unit again, not held in registers meanwhile
+        int u = s.u;
+        asm volatile("" : "+r"(u));
+        const PgUnit x = pg_unit<128 * QT>(a, tab, u);
+        const PgParts parts = pg_parts(a.part, BLOCKS, vecs);
+        const int v = v0 + row;
+        const bool whole = s.whole(), in = v < x.nv;
         const float f = !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
         const size_t ps = (size_t)s.part() * vecs + v;
-        T *out = (T *)a.out + (in ? pg_vec_at(a, s.x.row0, s.x.vec0 + v, s.g, a.os, a.dv) : 0);
+        T *out = (T *)a.out + (in ? pg_vec_at(a, x.row0, x.vec0 + v, s.g, a.os, a.dv) : 0);
         if (in && !whole && (QT == 2 || wg == 0)) *(float2 *)(parts.stat + ps * 2) = ok ? make_float2(m, l) : make_float2(0.f, NAN);
         auto write = [&](int c, float *y) {   // 32 columns
 #pragma unroll
@@ -806,12 +985,12 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
 #pragma unroll 1
             for (int c = QT == 2 ? 0 : 32 * wg; c < a.dv; c += QT == 2 ? 32 : 64) {
                 uint32_t y[32];
-                float x[32];
+                float w[32];
                 TMEM_LD32(lanes + Col::out(tile) + c, y);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(y[i]);
-                write(c, x);
+                for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(y[i]);
+                write(c, w);
                 __syncwarp();
             }
             tc_before();
@@ -824,8 +1003,10 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
 }
 
 template <typename T, typename C, int QT>
-__global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_constant__ PgTable tab, int units, int vecs) {
-    constexpr int TERMS = Types<T, C>::TERMS, V = 128 * QT;
+__global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_constant__ PgTable tab,
+                                                      const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                                                      const __grid_constant__ CUtensorMap mv, int qrows, int units, int vecs) {
+    constexpr int TERMS = Types<T, C>::TERMS;
     extern __shared__ unsigned char smraw[];
     __shared__ Shared sh;
     const Shape z = shape_of<QT, TERMS>(a.d, a.dv);
@@ -833,10 +1014,10 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     const uint32_t q0 = (su32(smraw) + 1023) & ~1023u, ring0 = q0 + (uint32_t)(TERMS * QT * z.nqc) * 16384;
     if (tid == 0) {
         for (int i = 0; i < MAX_SLOTS; ++i) {
-            mbar_init(&sh.full[i], PR_WARPS);
+            mbar_init(&sh.full[i], sizeof(C) == 1 ? PR_WARPS : 1);
             mbar_init(&sh.empty[i], 1);
         }
-        mbar_init(&sh.q_full, PR_WARPS);
+        mbar_init(&sh.q_full, sizeof(C) == 1 ? PR_WARPS : 1);
         mbar_init(&sh.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -851,7 +1032,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     __syncwarp();
     if (warp == SM_WARPS + PR_WARPS) tmem_alloc512(&sh.tslot);
     tc_before();
-    const PgShare share = pg_share<V, KT, THREADS>(a, tab, units, sh.share);
+    const PgShare share = pg_share<Plan<QT>, THREADS>(a, tab, units, sh.share);
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tslot;
@@ -861,7 +1042,9 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
         softmax<T, C, QT>(a, sh, z, tmem, tab, units, share, vecs);
     } else if (warp < SM_WARPS + PR_WARPS) {
         regs_less<R::PRODUCER>();
-        Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * (warp - SM_WARPS) + (lane >> 3), lane & 7, {0, 0}, {0, 0}, 0, true};
+        const int wid = warp - SM_WARPS;
+        Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * wid + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
+                                wid, {0, 0}, true, true, 0, 1, false};
         p.run(tab, units, share);
     } else {
         regs_less<R::ISSUER>();
@@ -872,6 +1055,22 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     tc_after();
     if (warp == SM_WARPS + PR_WARPS) tmem_free512(tmem);
     if (tid == 0 && sh.abort) atomicOr(&pg_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
+}
+
+template <typename M>
+bool encode(CUtensorMap *m, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    const auto enc = tensor_map_encoder();
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc && enc(m, std::is_same<M, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                      (void *)base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A pool as rows of `width` values, in boxes of 64 columns and `box` rows of a page.
+template <typename M>
+bool pool_map(CUtensorMap *m, const void *base, int width, uint64_t rows, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    return encode<M>(m, 2, base, dims, strides, box);
 }
 
 template <typename T, typename C, int QT>
@@ -889,7 +1088,22 @@ cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vec
         o1_attrs_done(&done, bit);
     }
     const int vecs = (int)(vectors < 128 * QT ? vectors : 128 * QT);
-    k<<<BLOCKS, THREADS, SMEM, st>>>(a, tab, tab.total, vecs);
+    CUtensorMap mq = {}, mk = {}, mv = {};
+    int qrows = 0;
+    if constexpr (sizeof(C) == 2) {
+        const uint64_t rows = ((uint64_t)a.n_pages * a.G) << a.lpage;
+        const uint32_t page = 1u << a.lpage, most = a.dv > 128 ? 64 : 128;
+        if (!pool_map<C>(&mk, a.k, a.d, rows, page < 128 ? page : 128) || !pool_map<C>(&mv, a.v, a.dv, rows, page < most ? page : most))
+            return cudaErrorInvalidValue;
+        if (sizeof(T) == 2 && 128 % a.hpg == 0) {
+            qrows = 128 / a.hpg;
+            const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.G * a.hpg, (cuuint64_t)vectors / a.hpg};
+            const cuuint64_t strides[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.qs * 2};
+            const cuuint32_t box[3] = {64, (cuuint32_t)a.hpg, (cuuint32_t)qrows};
+            if (!encode<T>(&mq, 3, a.q, dims, strides, box)) return cudaErrorInvalidValue;
+        }
+    }
+    k<<<BLOCKS, THREADS, SMEM, st>>>(a, tab, mq, mk, mv, qrows, tab.total, vecs);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, vecs, st) : e;
 }
