@@ -16,7 +16,7 @@
 //               their row's power of two (exact). Pages end anywhere on 16
 //               positions; a producer's 16 rows lie in one page. What no row
 //               attends is zero-filled, not read.
-//   warp 12     issues the MMAs
+//   warp 12     issues the MMAs (QT = 2: warps 12 and 13, a query tile each)
 // Keys come as items of 128 keys x 128 columns, values as 128 keys x 128 columns
 // or 64 x 256: 32 KB slots of one ring, in the order of use.
 //
@@ -207,7 +207,7 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
 struct Shared {
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
     uint64_t q_full, q_free;
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], fin;
+    uint64_t s_full[2], p_full[4], pv_half[2], pv_done[2], o_free[2], fin;   // p_full: QT = 2, halves of keys of either tile
     long long share[THREADS / 32 + 2];
     uint32_t tslot;
     int abort;
@@ -583,7 +583,81 @@ __device__ __forceinline__ void run_ts(bool e, uint32_t out, uint32_t p, uint64_
     }
 }
 
-template <typename T, typename C, int QT>
+// QT = 2: a warp for either query tile, so that what stands between one's MMAs
+// (waits, fences, commits) runs under the other's. A tile: S | PV S' | PV' S'' ...
+// A ring slot is free once both have used it.
+template <typename T, typename C>
+__device__ __forceinline__ void issuer_of(int tile, const PgArgs &a, Shared &sh, const Shape &z, uint32_t q0, uint32_t ring0,
+                                          uint32_t tmem, const PgTable &tab, int units, PgShare share) {
+    using M = typename Types<T, C>::M;
+    using Col = Cols<1>;
+    const bool e = elect_one();
+    const uint64_t dq = desc_sw128(q0) + (uint64_t)(tile * z.nqc * 1024), dk = desc_sw128(ring0), dv = desc_sw128_mn(ring0, KT * 128);
+    const uint32_t id_s = idesc<M>(128, KT, 0), id_o = idesc<M>(128, z.nv, 1);
+    const uint32_t sc = tmem + Col::score(tile), out = tmem + Col::out(tile);
+    const long long wl = a.wait_cycles;
+    bool ok = true;
+    Ring get = {0, 0};
+    uint32_t qp = 0, n = 0, nseg = 0;   // phase of q_full; tiles; segments of this query tile
+    PgSegment s;
+    auto commit = [&](uint64_t *bar) {
+        if (e) mma_commit(bar);
+    };
+    auto item = [&]() -> bool {   // the next one is here
+        ok = ok && warp_wait(&sh.full[get.slot], get.phase, &sh.abort, wl);
+        tc_after();
+        return ok;
+    };
+    auto scores = [&]() {
+        if (!item()) return;
+        run_ss(e, sc, dq, dk + (uint64_t)(get.slot * (SLOT / 16)), id_s, z.ksteps, 0);
+        commit(&sh.s_full[tile]);
+        commit(&sh.empty[get.slot]);
+        get.next(z.nslot);
+    };
+    while (ok && pg_next<Plan<2>>(a, tab, units, share, s)) {
+        ok = warp_wait(&sh.q_full, qp, &sh.abort, wl);
+        if (!ok) break;
+        qp ^= 1;
+        const int nt = s.t1 - s.t0;
+        if (s.x.nv <= 128 * tile) {   // no vector of this tile's
+            for (int i = 0; i < 2 * nt && item(); ++i) {
+                if (e) mbar_arrive(&sh.empty[get.slot]);
+                if (e && i == 2 * nt - 1) mbar_arrive(&sh.q_free);
+                get.next(z.nslot);
+            }
+            continue;
+        }
+        scores();
+        for (int j = 0; ok && j < nt; ++j) {
+            if (j == nt - 1) commit(&sh.q_free);   // the last scores are issued
+            if (j == 0) ok = warp_wait(&sh.o_free[tile], (nseg & 1) ^ 1, &sh.abort, wl);
+            // the later half of the keys first, as the softmax forms it
+            ok = ok && warp_wait(&sh.p_full[2 * tile + 1], n & 1, &sh.abort, wl);
+            if (!ok || !item()) break;
+            const uint64_t vd = dv + (uint64_t)(get.slot * (SLOT / 16));
+            run_ts<1>(e, out, sc + 64, vd + 512, id_o, j > 0);
+            commit(&sh.pv_half[tile]);
+            ok = warp_wait(&sh.p_full[2 * tile], n & 1, &sh.abort, wl);
+            if (!ok) break;
+            tc_after();
+            run_ts<1>(e, out, sc, vd, id_o, 1);
+            commit(&sh.pv_done[tile]);
+            commit(&sh.empty[get.slot]);
+            get.next(z.nslot);
+            ++n;
+            if (j + 1 < nt) scores();
+        }
+        ++nseg;
+    }
+    if (e) {
+        mma_commit(&sh.fin);   // tracks every MMA issued, also after an abort
+        mbar_drain(&sh.fin, 0);
+    }
+    __syncwarp();
+}
+
+template <typename T, typename C>
 __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape &z, uint32_t q0, uint32_t ring0, uint32_t tmem,
                                        const PgTable &tab, int units, PgShare share) {
     using M = typename Types<T, C>::M;
@@ -596,9 +670,8 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
     bool ok = true;
     Ring get = {0, 0};
     uint32_t qp = 0;                 // phase of q_full
-    uint32_t npv[2] = {0, 0};        // P V issued: of either tile (QT = 2), or in all
-    uint32_t nseg[2] = {0, 0};       // segments of either tile
-    uint32_t nsc = 0;                // QT = 1: scores issued
+    uint32_t npv = 0, nseg = 0;      // P V issued, segments
+    uint32_t nsc = 0;                // scores issued
     PgSegment s;
     auto commit = [&](uint64_t *bar) {
         if (e) mma_commit(bar);
@@ -607,16 +680,16 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
         ok = ok && warp_wait(&sh.full[r.slot], r.phase, &sh.abort, wl);
         return ok;
     };
-    // scores of query tile t from the key items at `r` on (QT = 1: released once used)
-    auto scores = [&](int t, int buf, Ring r) {
+    // scores from the key items at `r` on, released once used
+    auto scores = [&](int buf, Ring r) {
         const uint32_t col = tmem + Col::score(buf);
         if constexpr (TERMS == 1) {
             for (int i = 0; i < z.k_items; ++i) {
                 if (!filled(r)) return;
                 tc_after();
-                const uint64_t kd = dk + (uint64_t)(r.slot * (SLOT / 16)), qd = dq + (uint64_t)((t * z.nqc + 2 * i) * 1024);
+                const uint64_t kd = dk + (uint64_t)(r.slot * (SLOT / 16)), qd = dq + (uint64_t)(2 * i * 1024);
                 run_ss(e, col, qd, kd, id_s, min(8, z.ksteps - 8 * i), i > 0);
-                if (QT == 1) commit(&sh.empty[r.slot]);
+                commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
         } else {
@@ -629,7 +702,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 q = r;
                 for (int i = 0; i < z.k_items; ++i, q.next(z.nslot)) {
                     const uint64_t kd = dk + (uint64_t)(q.slot * (SLOT / 16));
-                    const uint64_t qd = dq + (uint64_t)(((m * QT + t) * z.nqc + 2 * i) * 1024);
+                    const uint64_t qd = dq + (uint64_t)((m * z.nqc + 2 * i) * 1024);
                     run_ss(e, col, qd, kd, id_s, min(8, z.ksteps - 8 * i), m < TERMS - 1 || i > 0);
                 }
             }
@@ -638,9 +711,9 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
         }
         commit(&sh.s_full[buf]);
     };
-    // P V of query tile t from the value items at `r` on
-    auto values = [&](int t, int buf, Ring r, bool acc, bool release) {
-        const uint32_t out = tmem + Col::out(t), p = tmem + Col::score(buf);
+    // P V from the value items at `r` on
+    auto values = [&](int buf, Ring r, bool acc) {
+        const uint32_t out = tmem + Col::out(0), p = tmem + Col::score(buf);
         if constexpr (TERMS == 3) {   // one item; a sum of its own
             if (!filled(r)) return;
             tc_after();
@@ -656,74 +729,42 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
                 run_ts<TERMS>(e, out, p + 64 * i, vd, id_o, acc || i > 0);
                 if (z.v_items == 1) run_ts<TERMS>(e, out, p + 64, vd + 512, id_o, 1);
-                if (release) commit(&sh.empty[r.slot]);
+                commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
         }
-        commit(&sh.pv_done[t]);
+        commit(&sh.pv_done[0]);
     };
     auto advance = [&](int n) {
         for (int i = 0; i < n; ++i) get.next(z.nslot);
     };
-    while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
+    while (ok && pg_next<Plan<1>>(a, tab, units, share, s)) {
         ok = warp_wait(&sh.q_full, qp, &sh.abort, wl);
         if (!ok) break;
         qp ^= 1;
         tc_after();
         const int nt = s.t1 - s.t0;
-        if (QT == 2) {
-            // S0 S1 | PV0 S0' PV1 S1' | ...: a tile's softmax runs under the other's MMAs
-            const int lt = s.x.nv > 128 ? 1 : 0;   // last tile
-            scores(0, 0, get);
-            if (lt && ok) scores(1, 1, get);
-            commit(&sh.empty[get.slot]);
-            get.next(z.nslot);
-            for (int j = 0; ok && j < nt; ++j) {
-                Ring kr = get;
-                kr.next(z.nslot);
-                if (j == nt - 1) commit(&sh.q_free);   // the last scores are issued
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t > lt || !ok) break;
-                    ok = warp_wait(&sh.p_full[t], npv[t] & 1, &sh.abort, wl);
-                    if (ok && j == 0) ok = warp_wait(&sh.o_free[t], (nseg[t] & 1) ^ 1, &sh.abort, wl);
-                    if (!ok) break;
-                    tc_after();
-                    values(t, t, get, j > 0, t == lt);
-                    ++npv[t];
-                    if (ok && j + 1 < nt) {
-                        scores(t, t, kr);
-                        if (t == lt) commit(&sh.empty[kr.slot]);
-                    }
-                }
-                advance(j + 1 < nt ? 2 : 1);
-            }
-            ++nseg[0];
-            if (lt) ++nseg[1];
-        } else {
-            scores(0, nsc & 1, get);
-            ++nsc;
-            advance(z.k_items);
-            for (int j = 0; ok && j < nt; ++j) {
-                if (j + 1 < nt) {
-                    scores(0, nsc & 1, get);
-                    if (!ok) break;
-                    ++nsc;
-                    advance(z.k_items);
-                }
-                if (j == nt - 1) commit(&sh.q_free);
-                const uint32_t n = npv[0];
-                ok = warp_wait(&sh.p_full[n & 1], (n >> 1) & 1, &sh.abort, wl);
-                // outputs given back: of the segment before, or (sums in registers) of the tile before
-                if (ok && (TERMS == 3 || j == 0)) ok = warp_wait(&sh.o_free[0], ((TERMS == 3 ? n : nseg[0]) & 1) ^ 1, &sh.abort, wl);
+        scores(nsc & 1, get);
+        ++nsc;
+        advance(z.k_items);
+        for (int j = 0; ok && j < nt; ++j) {
+            if (j + 1 < nt) {
+                scores(nsc & 1, get);
                 if (!ok) break;
-                tc_after();
-                values(0, n & 1, get, j > 0, true);
-                ++npv[0];
-                advance(z.v_items);
+                ++nsc;
+                advance(z.k_items);
             }
-            ++nseg[0];
+            if (j == nt - 1) commit(&sh.q_free);
+            ok = warp_wait(&sh.p_full[npv & 1], (npv >> 1) & 1, &sh.abort, wl);
+            // outputs given back: of the segment before, or (sums in registers) of the tile before
+            if (ok && (TERMS == 3 || j == 0)) ok = warp_wait(&sh.o_free[0], ((TERMS == 3 ? npv : nseg) & 1) ^ 1, &sh.abort, wl);
+            if (!ok) break;
+            tc_after();
+            values(npv & 1, get, j > 0);
+            ++npv;
+            advance(z.v_items);
         }
+        ++nseg;
     }
     if (e) {
         mma_commit(&sh.fin);   // tracks every MMA issued, also after an abort
@@ -804,7 +845,8 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.o_free[0]);
         };
-        for (int j = s.t0; ok && j < s.t1; ++j, ++n) {
+        // (QT = 1: a warp whose wait ran out goes on to the next decision)
+        for (int j = s.t0; j < s.t1 && (ok || (QT == 1 && j > s.t0)); ++j, ++n) {
             if (((j - s.t0) & 3) == 0) {
                 runs = __ballot_sync(0xffffffffu, next_runs);
                 next_runs = look(j + 4);
@@ -813,133 +855,135 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             runs >>= 8;
             const int x0 = (s.x.lo / KT + j) * KT, buf = QT == 2 ? tile : n & 1;
             const bool plain = x0 >= plain_lo && x0 + KT - 1 <= plain_hi && there == 0xffu;
-            ok = warp_wait(&sh.s_full[buf], QT == 2 ? n & 1 : (n >> 1) & 1, &sh.abort, wl);
+            ok = ok && warp_wait(&sh.s_full[buf], QT == 2 ? n & 1 : (n >> 1) & 1, &sh.abort, wl);
             if (QT == 2 && !ok) break;
             tc_after();
-            if (REG && j > s.t0) add_values(n - 1);
             const uint32_t scol = lanes + Col::score(buf);
-            // raw scores of 64 keys, those not attended -inf (all 128 of QT = 2
-            // at once did not fit the registers: the first half is loaded twice)
-            uint32_t r[64];
-            auto load = [&](int h) {
-                TMEM_LD32(scol + 64 * h, (&r[0]));
-                TMEM_LD32(scol + 64 * h + 32, (&r[32]));
-                tmem_ld_wait();
-                if (!plain) {
-                    const int b0 = low - x0 - 64 * h, b1 = pos - x0 - 64 * h;
-                    const uint32_t on = there >> (4 * h);
+            bool added = !REG || j == s.t0;   // the tile before's values
+            // 64 keys at a time (QT = 2: the later ones first; QT = 1: this
+            // warpgroup's half), each a step of the running softmax. Weights are
+            // taken from the reference as it stands, which the maximum, formed
+            // beside them, only rarely passes by 2^8: then the reference moves and
+            // they are formed again.
+#pragma unroll 1
+            for (int i = 0; i < QT; ++i) {
+                const int h = QT == 2 ? 1 - i : wg;
+                uint32_t r[64], w[TERMS == 1 ? 32 : 1];
+                float sum = 0.f;
+                if (ok && !idle) {   // raw scores, those not attended -inf
+                    TMEM_LD32(scol + 64 * h, (&r[0]));
+                    TMEM_LD32(scol + 64 * h + 32, (&r[32]));
+                    tmem_ld_wait();
+                    if (!plain) {
+                        const int b0 = low - x0 - 64 * h, b1 = pos - x0 - 64 * h;
+                        const uint32_t on = there >> (4 * h);
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c < b0 || c > b1 || !(on >> (c / 16) & 1)) r[c] = 0xff800000u;
-                }
-            };
-            auto top_of = [&]() {
-                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) t[(c / 2) & 3] = max3(t[(c / 2) & 3], r[c], r[c + 1]);
-                return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-            };
-            float top = -INFINITY;
-            if (ok && !idle) {
-                if (QT == 2) {
-                    load(0);
-                    top = top_of();
-                    load(1);
-                } else {
-                    load(wg);
-                }
-                top = fmaxf(top, top_of()) * sc2;
-            }
-            // The reference moves where the maximum has passed it by 2^8. QT = 1:
-            // the two halves of a row decide together, also to give up (a
-            // barrier that one of them left would never be met).
-            bool move = top > m + HEADROOM;
-            if (QT == 2) {
-                move = __any_sync(0xffffffffu, move);
-            } else {
-                move = sm_or(move || !ok);
-                if (move) {
-                    sh.half[wg][row] = top;
-                    ok = !sm_or(!ok);
-                    if (!ok) break;
-                    top = fmaxf(top, sh.half[wg ^ 1][row]);
-                }
-            }
-            if (move) {
-                const float mn = fmaxf(m, top), f = m > -INFINITY ? ex2(m - mn) : 0.f;
-                m = mn;
-                l *= f;
-                if (REG) {
-#pragma unroll
-                    for (int i = 0; i < (REG ? 64 : 1); ++i) o[i] *= f;
-                } else if (j > s.t0) {
-                    ok = warp_wait(&sh.pv_done[QT == 2 ? tile : 0], (n - 1) & 1, &sh.abort, wl);
-                    if (QT == 1) ok = !sm_or(!ok);
-                    if (!ok) break;
-                    tc_after();
-                    // this warpgroup's columns: all of its tile's (QT = 2), or every other 32
-                    for (int c = QT == 2 ? 0 : 32 * wg; c < z.nv; c += QT == 2 ? 32 : 64) {
-                        uint32_t y[32];
-                        TMEM_LD32(lanes + Col::out(tile) + c, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                        TMEM_ST32(lanes + Col::out(tile) + c, y);
+                        for (int c = 0; c < 64; ++c)
+                            if (c < b0 || c > b1 || !(on >> (c / 16) & 1)) r[c] = 0xff800000u;
                     }
                 }
-                if (QT == 1) sm_sync();   // the maxima are read before they are written again
-            }
-            // P over the scores it comes from
-            if (!idle) {
-                const float ref = m > -INFINITY ? m : 0.f;
-                const F2 f2s = f2(sc2, sc2), f2r = f2(-ref, -ref);
-                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-                constexpr int W = TERMS == 1 ? 32 : 16;   // words at a time, 2 keys each
-                auto store = [&](int h) {
+#pragma unroll 1
+                while (true) {
+                    float top = -INFINITY;
+                    const float ref = m > -INFINITY ? m : 0.f;
+                    const F2 f2s = f2(sc2, sc2), f2r = f2(-ref, -ref);
+                    if (ok && !idle) {
+                        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        F2 part[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-                    for (int i = 0; i < 32; i += W) {
-                        uint32_t w[W], w1[W], w2[W];
-#pragma unroll
-                        for (int c = 0; c < W; ++c) {
-                            float x, y;
-                            f2_get(f2_fma(f2(__uint_as_float(r[2 * (i + c)]), __uint_as_float(r[2 * (i + c) + 1])), f2s, f2r), x, y);
-                            x = ex2(x);
-                            y = ex2(y);
-                            sum[c & 1] = f2_add(sum[c & 1], f2(x, y));
+                        for (int c = 0; c < 32; ++c) {
+                            t[c & 3] = max3(t[c & 3], r[2 * c], r[2 * c + 1]);
                             if constexpr (TERMS == 1) {
+                                float x, y;
+                                f2_get(f2_fma(f2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), f2s, f2r), x, y);
+                                x = ex2(x);
+                                y = ex2(y);
+                                part[c & 1] = f2_add(part[c & 1], f2(x, y));
                                 w[c] = pack_m((const M *)nullptr, x, y);
-                            } else {
-                                w[c] = take_m<M>(x, y);
+                            }
+                        }
+                        top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * sc2;
+                        if constexpr (TERMS == 1) {
+                            float a0, a1;
+                            f2_get(f2_add(part[0], part[1]), a0, a1);
+                            sum = a0 + a1;
+                        }
+                    }
+                    // QT = 1: the two halves of a row decide together, also to give
+                    // up (a barrier that one of them left would never be met)
+                    bool move = top > m + HEADROOM;
+                    if (QT == 2) move = __any_sync(0xffffffffu, move);
+                    else move = sm_or(move || !ok);
+                    if (!move) break;
+                    if (QT == 1) {
+                        sh.half[wg][row] = top;
+                        ok = !sm_or(!ok);
+                        if (!ok) break;
+                        top = fmaxf(top, sh.half[wg ^ 1][row]);
+                    }
+                    const float mn = fmaxf(m, top), f = m > -INFINITY ? ex2(m - mn) : 0.f;
+                    m = mn;
+                    l *= f;
+                    if (REG) {
+                        if (!added) add_values(n - 1);
+                        added = true;
+#pragma unroll
+                        for (int c = 0; c < (REG ? 64 : 1); ++c) o[c] *= f;
+                    } else if (j > s.t0 || i > 0) {
+                        // all P V so far, of the tile before or of this one's first half
+                        if (QT == 2 && i > 0) ok = warp_wait(&sh.pv_half[tile], n & 1, &sh.abort, wl);
+                        else ok = warp_wait(&sh.pv_done[tile], (n - 1) & 1, &sh.abort, wl);
+                        if (QT == 1) ok = !sm_or(!ok);
+                        if (!ok) break;
+                        tc_after();
+                        // this warpgroup's columns: all of its tile's (QT = 2), or every other 32
+#pragma unroll 1
+                        for (int c = QT == 2 ? 0 : 32 * wg; c < z.nv; c += QT == 2 ? 32 : 64) {
+                            uint32_t y[32];
+                            TMEM_LD32(lanes + Col::out(tile) + c, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                            TMEM_ST32(lanes + Col::out(tile) + c, y);
+                        }
+                    }
+                    if (QT == 1) sm_sync();   // the maxima are read before they are written again
+                }
+                if (!ok) break;
+                // P over the scores it comes from
+                if (!idle) {
+                    __syncwarp();   // the warp is together for the stores
+                    if constexpr (TERMS == 1) {
+                        l += sum;
+                        TMEM_ST32(scol + 64 * h, w);
+                    } else {
+                        const float ref = m > -INFINITY ? m : 0.f;
+#pragma unroll
+                        for (int c0 = 0; c0 < 32; c0 += 16) {
+                            uint32_t w0[16], w1[16], w2[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                float x = ex2(fmaf(__uint_as_float(r[2 * (c0 + c)]), sc2, -ref));
+                                float y = ex2(fmaf(__uint_as_float(r[2 * (c0 + c) + 1]), sc2, -ref));
+                                l += x + y;
+                                w0[c] = take_m<M>(x, y);
                                 w1[c] = take_m<M>(x, y);
                                 if constexpr (TERMS > 2) w2[c] = pack_m((const M *)nullptr, x, y);
                             }
-                        }
-                        __syncwarp();   // the warp is together for the stores
-                        if constexpr (TERMS == 1) {
-                            TMEM_ST32(scol + 64 * h, w);
-                        } else {
-                            TMEM_ST16(scol + 64 * h + i, w);
-                            TMEM_ST16(scol + 64 * h + 32 + i, w1);
-                            if constexpr (TERMS > 2) TMEM_ST16(scol + 128 + 32 * h + i, w2);
+                            __syncwarp();
+                            TMEM_ST16(scol + 64 * h + c0, w0);
+                            TMEM_ST16(scol + 64 * h + 32 + c0, w1);
+                            if constexpr (TERMS > 2) TMEM_ST16(scol + 128 + 32 * h + c0, w2);
                         }
                     }
-                };
-                if (QT == 2) {
-                    store(1);
-                    load(0);
-                    store(0);
-                } else {
-                    store(wg);
                 }
-                float a0, a1, b0, b1;
-                f2_get(sum[0], a0, a1);
-                f2_get(sum[1], b0, b1);
-                l += (a0 + a1) + (b0 + b1);
+                tmem_st_wait();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[QT == 2 ? 2 * tile + h : buf]);
             }
-            tmem_st_wait();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+            if (ok && !added) add_values(n - 1);
+            if (QT == 2 && !ok) break;
         }
         // ---- the segment's end: its rows, or their partial results
         if (REG) {
@@ -1015,17 +1059,19 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     if (tid == 0) {
         for (int i = 0; i < MAX_SLOTS; ++i) {
             mbar_init(&sh.full[i], sizeof(C) == 1 ? PR_WARPS : 1);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.empty[i], QT);   // QT issuers
         }
         mbar_init(&sh.q_full, sizeof(C) == 1 ? PR_WARPS : 1);
-        mbar_init(&sh.q_free, 1);
+        mbar_init(&sh.q_free, QT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], QT == 2 ? SM_WARPS / 2 : SM_WARPS);
+            mbar_init(&sh.p_full[2 + i], SM_WARPS / 2);
             mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.pv_half[i], 1);
             mbar_init(&sh.o_free[i], QT == 2 ? SM_WARPS / 2 : SM_WARPS);
         }
-        mbar_init(&sh.fin, 1);
+        mbar_init(&sh.fin, QT);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1048,7 +1094,12 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
         p.run(tab, units, share);
     } else {
         regs_less<R::ISSUER>();
-        if (warp == SM_WARPS + PR_WARPS) issuer<T, C, QT>(a, sh, z, q0, ring0, tmem, tab, units, share);
+        const int w = warp - SM_WARPS - PR_WARPS;
+        if constexpr (QT == 2) {
+            if (w < 2) issuer_of<T, C>(w, a, sh, z, q0, ring0, tmem, tab, units, share);
+        } else {
+            if (w == 0) issuer<T, C>(a, sh, z, q0, ring0, tmem, tab, units, share);
+        }
     }
     tc_before();
     __syncthreads();
