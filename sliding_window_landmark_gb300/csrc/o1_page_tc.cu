@@ -209,6 +209,7 @@ struct Shared {
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_full[4], pv_half[2], pv_done[2], o_free[2], fin;   // p_full: QT = 2, halves of keys of either tile
     long long share[THREADS / 32 + 2];
+    uint64_t turn[2][4];   // QT = 2: the two tiles' warps of a scheduler form weights in turn
     uint32_t tslot;
     int abort;
     float half[2][128];   // QT = 1: the warpgroups' maxima, then sums
@@ -805,7 +806,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
     }
     __syncwarp();
     bool ok = true;
-    uint32_t n = 0;   // tiles so far, of this warpgroup's query tile
+    uint32_t n = 0, turns = 0;   // tiles so far, of this warpgroup's query tile, and in turn with the other's
     PgSegment s;
     while (pg_next<Plan<QT>>(a, tab, units, share, s)) {
         const int tile = QT == 2 ? wg : 0, v0 = 128 * tile;
@@ -814,6 +815,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
         // positions that every row of the tile attends
         const int plain_hi = s.x.pos(a, v0), last = s.x.pos(a, min(v0 + 127, s.x.nv - 1));
         const int plain_lo = a.window ? last - a.window + 1 : 0;
+        const bool paired = s.x.nv > 128;   // both query tiles have vectors
         const bool idle = v0 + 32 * (warp & 3) >= s.x.nv;   // no row of this warp's
         float m = -INFINITY, l = 0.f;
         float o[REG ? 64 : 1];
@@ -859,6 +861,11 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
             if (QT == 2 && !ok) break;
             tc_after();
             const uint32_t scol = lanes + Col::score(buf);
+            if (QT == 2 && paired) {   // after the other tile's warp: one forms weights while the other's MMAs run
+                ok = warp_wait(&sh.turn[wg][warp & 3], (turns & 1) ^ (wg == 0), &sh.abort, wl);
+                if (!ok) break;
+                ++turns;
+            }
             bool added = !REG || j == s.t0;   // the tile before's values
             // 64 keys at a time (QT = 2: the later ones first; QT = 1: this
             // warpgroup's half), each a step of the running softmax. Weights are
@@ -950,6 +957,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                     if (QT == 1) sm_sync();   // the maxima are read before they are written again
                 }
                 if (!ok) break;
+                if (QT == 2 && paired && i == 1 && lane == 0) mbar_arrive(&sh.turn[wg ^ 1][warp & 3]);
                 // P over the scores it comes from
                 if (!idle) {
                     __syncwarp();   // the warp is together for the stores
@@ -1072,6 +1080,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
             mbar_init(&sh.o_free[i], QT == 2 ? SM_WARPS / 2 : SM_WARPS);
         }
         mbar_init(&sh.fin, QT);
+        for (int i = 0; i < 8; ++i) mbar_init(&sh.turn[i >> 2][i & 3], 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
