@@ -603,9 +603,9 @@ O1_API size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows);
  * attends (past its end, before its window) may hold anything.
  * Scores, the softmax's maxima and sums and the outputs' sums are fp32. The
  * products run on the tensor cores with the cached values as they are; of the
- * other operand, q is exact, and the softmax's weights are rounded to 2^-8 (bf16
- * rows), 2^-11 (fp16 rows over fp16), 2^-16 (fp16 rows over e4m3) or 2^-24 (fp32
- * rows) of their value. Calls that
+ * other operand, q is exact (16-bit rows over e4m3: to 2^-25 of its largest
+ * value), and the softmax's weights are rounded to 2^-8 (bf16 rows), 2^-11 (fp16
+ * rows) or 2^-24 (fp32 rows) of their value. Calls that
  * may overlap on the GPU (other streams, captured graphs) need a scratch each.
  * Asynchronous. */
 O1_API int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,

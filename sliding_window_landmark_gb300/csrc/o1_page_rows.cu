@@ -16,6 +16,8 @@
 // j-th n8 tile.
 #include <math.h>
 
+#include <type_traits>
+
 #include "o1_page.cuh"
 
 namespace {
@@ -30,40 +32,35 @@ struct Plan {
 
 // Rows of type T over a cache of type C: the MMA's type M, and the terms that q
 // and the weights are split into (a weight in [0, 2^8]): 16-bit rows over their
-// own type need one; bf16 rows over e4m3 one (the codes are bf16 values); fp16
-// rows over e4m3 two (bf16 keeps the range of value times scale); fp32 rows
-// three, which hold fp32.
+// own type need one, fp32 rows three, which hold fp32.
+// 16-bit rows over e4m3 run in fp16, which holds the codes: a pair of codes is
+// one conversion (bf16 takes four). fp16's short range is met by powers of two:
+// a query vector is taken times the one that brings its largest value into [1,
+// 2), and the weights of the values, which carry the values' powers of two, from
+// a reference of their own, the maximum of score and power together.
 template <typename T, typename C>
-struct Types;
+struct Types {
+    using M = T;
+    static constexpr int TERMS = 1;
+    static constexpr bool CODES = false;   // codes under powers of two in fp16
+};
 template <>
 struct Types<float, __nv_bfloat16> {
     using M = __nv_bfloat16;
     static constexpr int TERMS = 3;
+    static constexpr bool CODES = false;
 };
 template <>
 struct Types<float, uint8_t> {
     using M = __nv_bfloat16;
     static constexpr int TERMS = 3;
+    static constexpr bool CODES = false;
 };
-template <>
-struct Types<__nv_bfloat16, __nv_bfloat16> {
-    using M = __nv_bfloat16;
-    static constexpr int TERMS = 1;
-};
-template <>
-struct Types<__nv_bfloat16, uint8_t> {
-    using M = __nv_bfloat16;
-    static constexpr int TERMS = 1;
-};
-template <>
-struct Types<__half, __half> {
+template <typename T>
+struct Types<T, uint8_t> {
     using M = __half;
     static constexpr int TERMS = 1;
-};
-template <>
-struct Types<__half, uint8_t> {
-    using M = __nv_bfloat16;
-    static constexpr int TERMS = 2;
+    static constexpr bool CODES = true;
 };
 
 // Sizes for widths of up to 64 N values.
@@ -117,20 +114,35 @@ __device__ __forceinline__ void mma16(const __half *, float (&c)[4], const uint4
                  : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// two e4m3 codes (low half of w, or its high half) as a bf16 pair: exact
-__device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t w, int half) {
+// two e4m3 codes (low half of w, or its high half) as a pair of M: exact
+__device__ __forceinline__ uint32_t of_e4m3(const __half *, uint32_t w, int half) {
     const uint16_t two = (uint16_t)(half ? w >> 16 : w);
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    return h;
+}
+__device__ __forceinline__ uint32_t of_e4m3(const __nv_bfloat16 *m, uint32_t w, int half) {
+    const uint32_t h = of_e4m3((const __half *)nullptr, w, half);
     const float2 f = __half22float2(*(const __half2 *)&h);
-    return pack_m((const __nv_bfloat16 *)nullptr, f.x, f.y);
+    return pack_m(m, f.x, f.y);
 }
 
 // 16 bytes, or zeros where !on
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool on) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
     const int n = on ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(n)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+template <int D, int S>
+__device__ __forceinline__ void copy16_at(uint32_t dst, const void *src) {   // dst + D, src + S
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(D), "n"(S) : "memory");
+}
+// A loop of constants 0 .. N - 1.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>());
+    }
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -148,30 +160,50 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     using Ty = Types<T, C>;
     using M = typename Ty::M;
     constexpr int TERMS = Ty::TERMS;
+    constexpr bool CODES = Ty::CODES;
     using Z = Sizes<C, N, TERMS>;
     constexpr int CB = Z::CB, VL = Z::VL, KB = Z::KB, VB = Z::VB, STEPS = Z::STEPS, RING = Z::RING, ITEM = Z::ITEM;
     constexpr bool E4 = CB == 1;
+    constexpr bool Q_REGS = TERMS == 1 && N <= 2;   // the queries in registers
     extern __shared__ __align__(16) unsigned char sm[];
     __shared__ long long s_share[RW + 2];
     __shared__ float s_m[RW][RV], s_l[RW][RV];
-    __shared__ __align__(16) uint8_t s_exp[E4 ? RW * RING * 16 : 16];
+    __shared__ int s_qe[RV];
+    __shared__ __align__(16) uint8_t s_exp[E4 ? RW * RING * 32 : 16];   // of an item of keys: theirs, then the values'
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qd = lane & 3, row = lane >> 2;
     unsigned char *ring = sm + (size_t)warp * RING * ITEM;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring) + 16 * lane;
     uint32_t *sq = (uint32_t *)(sm + (size_t)RW * RING * ITEM);   // [term][step][lane][4]
-    const C *pk = (const C *)a.k, *pv = (const C *)a.v;
 
     PgShare share = pg_share<Plan, RT>(a, tab, units, s_share);
     const PgParts parts = pg_parts(a.part, BLOCKS, RV);
     if (tid == 0) parts.head[blockIdx.x].last = -1;
     const float sc2 = a.scale * 1.4426950408889634f;
+    const int kb_n = (a.d * CB + 63) >> 6, vb_n = (a.dv * CB + 127) >> 7;
+    const bool k_whole = (a.d * CB & 63) == 0;
     bool first_seg = true;
     PgSegment seg;
     while (pg_next<Plan>(a, tab, units, share, seg)) {
         const PgUnit &x = seg.x;
         const int g = seg.g;
-        // ---- queries, in the MMA's A layout of this lane order
         __syncthreads();   // the segment before is done with shared memory
-        const int kb_n = (a.d * CB + 63) >> 6, vb_n = (a.dv * CB + 127) >> 7;
+        if (CODES) {   // the exponents of the query vectors' largest values, eight threads a vector
+            const int v = tid >> 3;
+            float top = 0.f;
+            if (v < x.nv) {
+                const T *q = (const T *)a.q + pg_vec_at(a, x.row0, x.vec0 + v, g, a.qs, a.d);
+                for (int c = 4 * (tid & 7); c < a.d; c += 32) {
+                    const float4 f = o1_ld4(q + c);
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
+                }
+            }
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+            // 2^-e and 2^e are normal numbers; an exponent below that range loses nothing but zeros
+            if ((tid & 7) == 0) s_qe[v] = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
+            __syncthreads();
+        }
+        // ---- queries, in the MMA's A layout of this lane order
         for (int i = tid; i < kb_n * (VL / 4) * 32; i += RT) {
             const int st = i >> 5, ln = i & 31, b = st / (VL / 4), s = st - b * (VL / 4);
             const int c = 4 * VL * b + VL * (ln & 3) + 4 * s;   // 4 consecutive values: k indices 2q, 2q + 1, 2q + 8, 2q + 9
@@ -181,6 +213,10 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 const int v = (ln >> 2) + 8 * h;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (v < x.nv && c < a.d) f = o1_ld4((const T *)a.q + pg_vec_at(a, x.row0, x.vec0 + v, g, a.qs, a.d) + c);
+                if (CODES) {
+                    const float e = pg_scale((uint32_t)(127 - s_qe[v]));
+                    f = make_float4(f.x * e, f.y * e, f.z * e, f.w * e);
+                }
                 split_m<M, TERMS>(f.x, f.y, w[h]);
                 split_m<M, TERMS>(f.z, f.w, w[2 + h]);
             }
@@ -188,17 +224,25 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             for (int t = 0; t < TERMS; ++t) *(uint4 *)(sq + ((t * STEPS + st) * 32 + ln) * 4) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
         }
         __syncthreads();
+        uint4 qr[Q_REGS ? STEPS : 1];
+        if (Q_REGS) {
+#pragma unroll
+            for (int st = 0; st < (Q_REGS ? STEPS : 1); ++st) qr[st] = *(const uint4 *)(sq + (st * 32 + lane) * 4);
+        }
 
         // ---- this warp's blocks of 16 keys: blk0, blk0 + RW, ...
         const int blk0 = (x.lo / TILE + seg.t0) * RW + warp, nb = seg.t1 - seg.t0;
         int pos[2], low[2];   // of this lane's two vectors: last and first position attended
+        float sc[2];          // what a score of theirs is taken times
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             pos[h] = x.pos(a, min(row + 8 * h, x.nv - 1));   // past the last: zeros, not written
             low[h] = a.window ? pos[h] - a.window + 1 : 0;
+            sc[h] = CODES ? sc2 * pg_scale((uint32_t)(s_qe[row + 8 * h] + 127)) : sc2;
         }
         const int plain_lo = a.window ? max(0, x.hi - a.window + 1) : 0, plain_hi = x.pos(a, 0);
-        float acc[VB * VL][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        // m, l: the softmax's reference and sum; mv: the reference of the values' weights
+        float acc[VB * VL][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < VB * VL; ++i)
 #pragma unroll
@@ -211,48 +255,83 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
         int pages = page_of(lane), pages_next = page_of(32 + lane);
         uint32_t present = 0;   // bit i % 32: block i has a page
         int put = 0, put_slot = 0, get_slot = 0;   // next item to issue: block put / 2, keys then values
-        auto issue = [&]() {
+        const unsigned char *kbase = (const unsigned char *)a.k + (size_t)(row * a.d + VL * qd) * CB;
+        const unsigned char *vbase = (const unsigned char *)a.v + (size_t)(2 * qd * a.dv + VL * row) * CB;
+        const int kw = a.d * CB, vw = a.dv * CB;   // bytes of a cached row
+        int rowid = 0;          // of the block's first position in the pools
+        bool inside = false;    // all of the block's positions are attended by some vector, and on a page
+        auto issue_keys = [&]() {
             const int i = put >> 1;
             if (i < nb) {
                 const int p0 = (blk0 + RW * i) * 16;
                 const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-                unsigned char *dst = ring + put_slot * ITEM + 16 * lane;
-                const int in = p0 & ((1 << a.lpage) - 1);
-                if (!(put & 1)) {
-                    present = (present & ~(1u << (i & 31))) | (page >= 0 ? 1u : 0u) << (i & 31);
-                    const C *src = pg_at(pk, a, max(page, 0), g, in, a.d);
+                present = (present & ~(1u << (i & 31))) | (page >= 0 ? 1u : 0u) << (i & 31);
+                rowid = ((max(page, 0) * a.G + g) << a.lpage) + (p0 & ((1 << a.lpage) - 1));
+                inside = page >= 0 && p0 >= x.lo && p0 + 15 <= x.hi;
+                const uint32_t dst = ring_at + put_slot * ITEM;
+                const unsigned char *src = kbase + (size_t)(uint32_t)rowid * kw;
+                if (inside && k_whole) {
+                    each<KB>([&](auto b) {
+                        if (b < kb_n) copy16_at<b * 512, b * 64>(dst, src);
+                    });
+                    src += 8 * kw;
+                    each<KB>([&](auto b) {
+                        if (b < kb_n) copy16_at<(KB + b) * 512, b * 64>(dst, src);
+                    });
+                } else {
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const int key = 8 * n + row;
-                        const bool in_range = page >= 0 && p0 + key >= x.lo && p0 + key <= x.hi;
+                        const int p = p0 + 8 * n + row;
+                        const bool in = page >= 0 && p >= x.lo && p <= x.hi;
 #pragma unroll
                         for (int b = 0; b < KB; ++b)
                             if (b < kb_n) {
-                                const int c = 4 * VL * b + VL * qd;
-                                const bool on = in_range && c < a.d;
-                                copy16(dst + (n * KB + b) * 512, on ? src + (size_t)key * a.d + c : pk, on);
+                                const bool on = in && 4 * VL * b + VL * qd < a.d;
+                                copy16(dst + (n * KB + b) * 512, on ? src + 8 * n * kw + 64 * b : a.k, on);
                             }
                     }
+                }
+                if (E4 && lane < 2) {   // the 16 exponents of the keys, and of the values
+                    const uint8_t *e = lane ? a.ve : a.ke;
+                    copy16((uint32_t)__cvta_generic_to_shared(&s_exp[(warp * RING + put_slot) * 32 + 16 * lane]),
+                           page >= 0 ? e + (size_t)(uint32_t)rowid : e, page >= 0);
+                }
+            }
+            copy_commit();
+            ++put;
+            put_slot = put_slot + 1 == RING ? 0 : put_slot + 1;
+        };
+        auto issue_values = [&]() {   // of the block whose keys were issued last
+            const int i = put >> 1;
+            if (i < nb) {
+                const uint32_t dst = ring_at + put_slot * ITEM;
+                const unsigned char *src = vbase + (size_t)(uint32_t)rowid * vw;
+                if (inside) {   // (columns past the last only reach outputs that are not written)
+                    const unsigned char *s1 = src + vw, *s8 = src + 8 * vw, *s9 = s8 + vw;
+                    each<VB>([&](auto b) {
+                        if (b < vb_n && 8 * VL * b + VL * row < a.dv) {
+                            copy16_at<(4 * b + 0) * 512, b * 128>(dst, src);
+                            copy16_at<(4 * b + 1) * 512, b * 128>(dst, s1);
+                            copy16_at<(4 * b + 2) * 512, b * 128>(dst, s8);
+                            copy16_at<(4 * b + 3) * 512, b * 128>(dst, s9);
+                        }
+                    });
                 } else {
-                    const C *src = pg_at(pv, a, max(page, 0), g, in, a.dv);
+                    const int p0 = (blk0 + RW * i) * 16;
+                    const bool page = present >> (i & 31) & 1;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int key = 2 * qd + (r & 1) + 8 * (r >> 1);
-                        const bool in_range = page >= 0 && p0 + key >= x.lo && p0 + key <= x.hi;
+                        const int key = (r & 1) + 8 * (r >> 1), p = p0 + 2 * qd + key;
+                        const bool in = page && p >= x.lo && p <= x.hi;
 #pragma unroll
                         for (int b = 0; b < VB; ++b)
                             if (b < vb_n) {
-                                const int c = 8 * VL * b + VL * row;
-                                const bool on = in_range && c < a.dv;
-                                copy16(dst + (b * 4 + r) * 512, on ? src + (size_t)key * a.dv + c : pv, on);
+                                const bool on = in && 8 * VL * b + VL * row < a.dv;
+                                copy16(dst + (b * 4 + r) * 512, on ? src + key * vw + 128 * b : a.v, on);
                             }
                     }
                 }
-                if (E4 && lane == 0) {
-                    const uint8_t *e = put & 1 ? a.ve : a.ke;
-                    copy16(&s_exp[(warp * RING + put_slot) * 16], page >= 0 ? pg_at(e, a, page, g, in, 1) : e, page >= 0);
-                }
-                if ((put & 1) && (i & 31) == 31) {
+                if ((i & 31) == 31) {
                     pages = pages_next;
                     pages_next = page_of(i + 33 + lane);
                 }
@@ -261,8 +340,13 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             ++put;
             put_slot = put_slot + 1 == RING ? 0 : put_slot + 1;
         };
+        // items alternate: the one RING - 1 further on, keys or values
+        auto issue_at = [&](bool keys) {
+            if (keys) issue_keys();
+            else issue_values();
+        };
         // the item to use next: all but the last RING - 1 groups are here (for
-        // the exponents, which one lane copied, at every lane)
+        // the exponents, which two lanes copied, at every lane)
         auto item = [&]() -> const unsigned char * {
             copy_wait<RING - 1>();
             if (E4) __syncwarp();
@@ -273,10 +357,10 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             get_slot = get_slot + 1 == RING ? 0 : get_slot + 1;
         };
 #pragma unroll 1
-        for (int i = 0; i < RING - 1; ++i) issue();
+        for (int i = 0; i < RING - 1; ++i) issue_at(!(i & 1));
 #pragma unroll 1
         for (int i = 0; i < nb; ++i) {
-            issue();
+            issue_at((RING - 1) % 2 == 0);
             const unsigned char *it = item();
             // ---- scores
             // the lower terms of q in a sum of their own: the MMA truncates at each
@@ -286,42 +370,48 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
 #pragma unroll
             for (int b = 0; b < KB; ++b)
                 if (b < kb_n) {
-                    uint4 kw[2];
+                    uint4 kw4[2];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) kw[n] = *(const uint4 *)(it + (n * KB + b) * 512);
+                    for (int n = 0; n < 2; ++n) kw4[n] = *(const uint4 *)(it + (n * KB + b) * 512);
 #pragma unroll
                     for (int st = 0; st < VL / 4; ++st) {
                         uint32_t b0[2], b1[2];
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             if (E4) {
-                                const uint32_t w = st == 0 ? kw[n].x : st == 1 ? kw[n].y : st == 2 ? kw[n].z : kw[n].w;
-                                b0[n] = bf16_of_e4m3(w, 0);
-                                b1[n] = bf16_of_e4m3(w, 1);
+                                const uint32_t w = st == 0 ? kw4[n].x : st == 1 ? kw4[n].y : st == 2 ? kw4[n].z : kw4[n].w;
+                                b0[n] = of_e4m3((const M *)nullptr, w, 0);
+                                b1[n] = of_e4m3((const M *)nullptr, w, 1);
                             } else {
-                                b0[n] = st == 0 ? kw[n].x : kw[n].z;
-                                b1[n] = st == 0 ? kw[n].y : kw[n].w;
+                                b0[n] = st == 0 ? kw4[n].x : kw4[n].z;
+                                b1[n] = st == 0 ? kw4[n].y : kw4[n].w;
                             }
                         }
 #pragma unroll
                         for (int t = TERMS - 1; t >= 0; --t) {
-                            const uint4 qa = *(const uint4 *)(sq + ((t * STEPS + b * (VL / 4) + st) * 32 + lane) * 4);
+                            const int step = b * (VL / 4) + st;
+                            const uint4 qa = Q_REGS ? qr[Q_REGS ? step : 0] : *(const uint4 *)(sq + ((t * STEPS + step) * 32 + lane) * 4);
 #pragma unroll
                             for (int n = 0; n < 2; ++n) mma16((const M *)nullptr, t ? low_s[n] : s[n], qa, b0[n], b1[n]);
                         }
                     }
                 }
             const int p0 = (blk0 + RW * i) * 16;
-            const uint8_t *ek = &s_exp[(warp * RING + get_slot) * 16];
-            float f[2][2];
+            uint32_t eb[2][2];   // this lane's columns' bytes, keys' and values': column c of tile n in byte c
+            if (E4) {
+                const uint8_t *e = &s_exp[(warp * RING + get_slot) * 32 + 2 * qd];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) eb[kv][n] = *(const uint16_t *)(e + 16 * kv + 8 * n);
+            }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) f[n][c] = E4 ? sc2 * pg_scale(ek[8 * n + 2 * qd + c]) : sc2;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[n][j] = (TERMS > 1 ? s[n][j] + low_s[n][j] : s[n][j]) * f[n][j & 1];
+                for (int j = 0; j < 4; ++j) {
+                    s[n][j] = (TERMS > 1 ? s[n][j] + low_s[n][j] : s[n][j]) * sc[j >> 1];
+                    if (E4) s[n][j] *= pg_scale(eb[0][n] >> (8 * (j & 1)) & 0xff);
+                }
             const bool there = present >> (i & 31) & 1;
             if (!(there && p0 >= plain_lo && p0 + 15 <= plain_hi)) {
 #pragma unroll
@@ -333,45 +423,61 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                     }
             }
             done();
-            issue();
+            issue_at((RING - 1) % 2 == 1);
             // ---- softmax: a reference within 2^8 of the running maximum
-            float top[2];
+            float top[2], topv[2], sv[2][4];
+            if (CODES) {   // score and the value's power of two together (-inf stays)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sv[n][j] = s[n][j] + (float)((int)(eb[1][n] >> (8 * (j & 1)) & 0xff) - 127);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
                 top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
                 top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                topv[h] = top[h];
+                if (CODES) {
+                    topv[h] = fmaxf(fmaxf(sv[0][2 * h], sv[0][2 * h + 1]), fmaxf(sv[1][2 * h], sv[1][2 * h + 1]));
+                    topv[h] = fmaxf(topv[h], __shfl_xor_sync(0xffffffffu, topv[h], 1));
+                    topv[h] = fmaxf(topv[h], __shfl_xor_sync(0xffffffffu, topv[h], 2));
+                }
             }
-            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f ||
+                                            (CODES && (topv[0] > mv[0] + 8.f || topv[1] > mv[1] + 8.f)))) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float mn = fmaxf(m[h], top[h]), r = m[h] > -INFINITY ? ex2(m[h] - mn) : 0.f;
                     m[h] = mn;
                     l[h] *= r;
+                    float rv = r;
+                    if (CODES) {
+                        const float mvn = fmaxf(mv[h], topv[h]);
+                        rv = mv[h] > -INFINITY ? ex2(mv[h] - mvn) : 0.f;
+                        mv[h] = mvn;
+                    }
 #pragma unroll
                     for (int j = 0; j < VB * VL; ++j) {
-                        acc[j][2 * h] *= r;
-                        acc[j][2 * h + 1] *= r;
+                        acc[j][2 * h] *= rv;
+                        acc[j][2 * h + 1] *= rv;
                     }
                 }
             }
             const float ref[2] = {m[0] > -INFINITY ? m[0] : 0.f, m[1] > -INFINITY ? m[1] : 0.f};
+            const float refv[2] = {mv[0] > -INFINITY ? mv[0] : 0.f, mv[1] > -INFINITY ? mv[1] : 0.f};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     s[n][j] = ex2(s[n][j] - ref[j >> 1]);
                     l[j >> 1] += s[n][j];
+                    if (CODES) s[n][j] = ex2(sv[n][j] - refv[j >> 1]);
+                    // fp32 rows: the value's power of two (a masked position's byte may be any)
+                    else if (E4) s[n][j] = s[n][j] > 0.f ? s[n][j] * pg_scale(eb[1][n] >> (8 * (j & 1)) & 0xff) : 0.f;
                 }
             // ---- weighted values
             it = item();
-            if (E4) {
-                const uint8_t *ev = &s_exp[(warp * RING + get_slot) * 16];
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[n][j] = s[n][j] > 0.f ? s[n][j] * pg_scale(ev[8 * n + 2 * qd + (j & 1)]) : 0.f;   // a masked position's byte may be any
-            }
             uint32_t w[4][TERMS];
             split_m<M, TERMS>(s[0][0], s[0][1], w[0]);
             split_m<M, TERMS>(s[0][2], s[0][3], w[1]);
@@ -380,25 +486,25 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
 #pragma unroll
             for (int b = 0; b < VB; ++b)
                 if (b < vb_n) {
-                    uint32_t vw[4][4];
+                    uint32_t vr[4][4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) *(uint4 *)vw[r] = *(const uint4 *)(it + (b * 4 + r) * 512);
+                    for (int r = 0; r < 4; ++r) *(uint4 *)vr[r] = *(const uint4 *)(it + (b * 4 + r) * 512);
 #pragma unroll
                     for (int j4 = 0; j4 < 4; ++j4) {
                         uint32_t b0[VL / 4], b1[VL / 4];   // of the columns in word j4
                         if (E4) {
-                            const uint32_t lo = __byte_perm(vw[0][j4], vw[1][j4], 0x5140), hi = __byte_perm(vw[0][j4], vw[1][j4], 0x7362);
-                            const uint32_t lo8 = __byte_perm(vw[2][j4], vw[3][j4], 0x5140), hi8 = __byte_perm(vw[2][j4], vw[3][j4], 0x7362);
+                            const uint32_t lo = __byte_perm(vr[0][j4], vr[1][j4], 0x5140), hi = __byte_perm(vr[0][j4], vr[1][j4], 0x7362);
+                            const uint32_t lo8 = __byte_perm(vr[2][j4], vr[3][j4], 0x5140), hi8 = __byte_perm(vr[2][j4], vr[3][j4], 0x7362);
 #pragma unroll
                             for (int c = 0; c < VL / 4; ++c) {
-                                b0[c] = bf16_of_e4m3(c < 2 ? lo : hi, c & 1);
-                                b1[c] = bf16_of_e4m3(c < 2 ? lo8 : hi8, c & 1);
+                                b0[c] = of_e4m3((const M *)nullptr, c < 2 ? lo : hi, c & 1);
+                                b1[c] = of_e4m3((const M *)nullptr, c < 2 ? lo8 : hi8, c & 1);
                             }
                         } else {
 #pragma unroll
                             for (int c = 0; c < VL / 4; ++c) {
-                                b0[c] = __byte_perm(vw[0][j4], vw[1][j4], c ? 0x7632 : 0x5410);
-                                b1[c] = __byte_perm(vw[2][j4], vw[3][j4], c ? 0x7632 : 0x5410);
+                                b0[c] = __byte_perm(vr[0][j4], vr[1][j4], c ? 0x7632 : 0x5410);
+                                b1[c] = __byte_perm(vr[2][j4], vr[3][j4], c ? 0x7632 : 0x5410);
                             }
                         }
 #pragma unroll
@@ -414,9 +520,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
 #pragma unroll
                                 for (int i2 = 0; i2 < 4; ++i2) o[i2] += y[i2];
                             } else {
-#pragma unroll
-                                for (int t = TERMS - 1; t >= 0; --t)
-                                    mma16((const M *)nullptr, o, make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]), b0[c], b1[c]);
+                                mma16((const M *)nullptr, o, make_uint4(w[0][0], w[1][0], w[2][0], w[3][0]), b0[c], b1[c]);
                             }
                         }
                     }
@@ -438,7 +542,8 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
         for (int h = 0; h < 2; ++h) {
             big[h] = -INFINITY;
             for (int w = 0; w < RW; ++w) big[h] = fmaxf(big[h], s_m[w][row + 8 * h]);
-            fac[h] = m[h] > -INFINITY ? ex2(m[h] - big[h]) : 0.f;
+            const float from = CODES ? mv[h] : m[h];   // what the sums are relative to
+            fac[h] = from > -INFINITY ? ex2(from - big[h]) : 0.f;
         }
         const int ld = a.dv + 4;
         float *so = (float *)ring;   // [RV][ld]: within this warp's ring

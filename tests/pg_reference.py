@@ -19,8 +19,13 @@ w_j = e^{s_j}, s_j = scale q.k_j, S_j = |scale| sum |q| |k_j|, p_j = w_j / sum w
  - The weights of the values are rounded to rho: bf16 has 8 significant bits, so
    a value in [1, 2) is off by at most half of 2^-7: 2^-8 relative for one bf16
    term, 2^-16 for two (the second takes what the first left, at most 2^-8, and
-   leaves 2^-8 of it), 2^-24 for three; fp16, 11 bits, 2^-11 (and 2^-25 below its
-   normal numbers, where a row's largest weight is at least 1).
+   leaves 2^-8 of it), 2^-24 for three; fp16, 11 bits, 2^-11, and 2^-25 below its
+   normal numbers. fp16 weights of an e4m3 cache are those of the codes v_j /
+   2^{e_j}, that is p_j 2^{e_j}, and are taken so that a row's largest is at least
+   1: 2^-25 max_i (p_i 2^{e_i}) sum_j |v_j| / 2^{e_j} (e = 0 for an fp16 cache).
+ - 16-bit rows over e4m3: q in fp16 times a power of two that brings its largest
+   value into [1, 2): 2^-25 of that value for each of q's below 2^-14, so 2^-25
+   |scale| max |q| sum |k_j| of a score.
  - The weighted sum is n / 8 + 400 accumulations or joins, n the keys, each off
    by at most 2u of the absolute sum.
 So with A = sum p_j |v_j|: |error| <= sum p_j delta_j (|v_j| + |out|)
@@ -63,9 +68,10 @@ def places(table, page, slot, a, b):
     return table[slot, p // page].long(), p % page
 
 
-def attend(q, k, v, table, page, n_pages, seqs, scale, window, dtype, terms, rho, f16_weights=False):
+def attend(q, k, v, table, page, n_pages, seqs, scale, window, dtype, terms, rho, f16_weights=False, v_exp=None):
     """-> out and its bound (double; rows of no sequence 0). k, v: held values
-    [pages, G, page, width]; seqs (row0, rows, slot, pos0)."""
+    [pages, G, page, width]; seqs (row0, rows, slot, pos0); v_exp: the values'
+    bytes of an e4m3 cache."""
     q = q.double()
     R, nh, d = q.shape
     G, dv = k.shape[1], v.shape[3]
@@ -96,10 +102,15 @@ def attend(q, k, v, table, page, n_pages, seqs, scale, window, dtype, terms, rho
         o = pr @ vv[:, None]
         A = pr @ vv[:, None].abs()
         delta = (2 * (d / 16 + 2) * terms + 2) * U * S + 8 * U * top + 2.0 ** -22
+        if v_exp is not None and dtype is not torch.float32:
+            far = abs(scale) * qq.abs().amax(-1, keepdim=True) * kk[:, None].abs().sum(-1)[..., None, :]
+            delta = delta + 2.0 ** -25 * torch.where(see, far, 0.0)
         b = 1.01 * ((pr * delta) @ vv[:, None].abs() + (pr * delta).sum(-1, keepdim=True) * o.abs()
                     + (rho + (j.numel() / 4 + 800) * U) * A)
         if f16_weights:
-            b = b + 2.0 ** -25 * (see.double() @ vv[:, None].abs())
+            size = pow2(v_exp[ids, :, at].int() - 127).T if v_exp is not None else torch.ones_like(vv[..., 0])   # [G, n]
+            most = (pr * size[:, None, None]).amax(-1, keepdim=True)
+            b = b + 2.0 ** -25 * most * (see.double() @ (vv.abs() / size[..., None])[:, None])
         out[row0:row0 + rows] = o.permute(2, 0, 1, 3).flatten(1, 2)
         bound[row0:row0 + rows] = b.permute(2, 0, 1, 3).flatten(1, 2)
     return out, bound + rounding(out, dtype)
@@ -109,6 +120,6 @@ def precision(dtype, cache_dtype):
     """Terms, rho and whether weights are fp16, of rows over a cache."""
     if dtype is torch.float32:
         return 3, 2.0 ** -24, False
-    if cache_dtype is E4M3:
-        return (1, 2.0 ** -8, False) if dtype is torch.bfloat16 else (2, 2.0 ** -16, False)
+    if cache_dtype is E4M3:   # in fp16 or, for many rows, in bf16
+        return 2, 2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -11, True
     return (1, 2.0 ** -8, False) if dtype is torch.bfloat16 else (1, 2.0 ** -11, True)

@@ -90,7 +90,7 @@ def check(o1, cache, q, seqs, out, what):
     k, v = cache.held()
     dt = q.dtype
     terms, rho, f16 = ref.precision(dt, cache.ct)
-    want, bound = ref.attend(q, k, v, cache.table, g.page, cache.n, seqs, g.scale, g.window, dt, terms, rho, f16)
+    want, bound = ref.attend(q, k, v, cache.table, g.page, cache.n, seqs, g.scale, g.window, dt, terms, rho, f16, cache.ve)
     live = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
     for r0, n, _, _ in seqs:
         live[r0:r0 + n] = True
@@ -409,8 +409,9 @@ def test_far_offsets(o1):
     o1.check(o1.o1_pg_chunk_attend(g, c, scratch, q, [(0, rows, 0, 0)], out), "chunk")
     o1.check(o1.o1_pg_token_attend(g, c, scratch, q[-1:], None, torch.tensor([rows - 1], device="cuda"), one), "token")
     near = lambda x: ref.quantise(x)[0].unflatten(0, (1, rows)).transpose(1, 2)   # one page of all the rows
+    exp = ref.quantise(vv)[1].unflatten(0, (1, rows)).transpose(1, 2)
     want, bound = ref.attend(q, near(kk), near(vv), torch.zeros(1, 1, dtype=torch.int32, device="cuda"), rows, 1, [(0, rows, 0, 0)],
-                             g.scale, 0, BF16, *ref.precision(BF16, E4))
+                             g.scale, 0, BF16, *ref.precision(BF16, E4), v_exp=exp)
     ref.assert_within(out, want.cpu(), bound.cpu(), "far chunk")
     ref.assert_within(one, want[-1:].cpu(), bound[-1:].cpu(), "far row")
 
@@ -583,7 +584,7 @@ def test_expired_waits_leave_nan_or_right_values(o1, dt, ct, d):
     cache = Cache(o1, g, [900, 100], 27)
     q = randn(torch.Generator().manual_seed(13), 400, 8, d, dtype=dt)
     k, v = cache.held()
-    want, bound = ref.attend(q, k, v, cache.table, 64, cache.n, seqs, g.scale, 0, dt, *ref.precision(dt, ct))
+    want, bound = ref.attend(q, k, v, cache.table, 64, cache.n, seqs, g.scale, 0, dt, *ref.precision(dt, ct), v_exp=cache.ve)
     assert o1.o1_pg_flags(clear=True) == 0
     raised = 0
     for limit in (1, 300, 1000, 2000, 3000, 5000, 8000, 20000):
