@@ -6,14 +6,17 @@
 //
 // A warp takes 16 of a tile's keys and keeps a softmax and an accumulator of
 // its own, so that nothing waits for another warp until the segment's end. Its
-// keys and values come by 16-byte asynchronous copies into a ring of items (16
-// keys, or 16 values); a lane copies exactly the bytes that it will use, so the
-// ring needs no barrier and no swizzle. That works since the order of a
-// contraction is free: the lane that holds key n's contraction indices 2q, 2q+1,
-// 2q + 8, 2q + 9 of every k16 step (q = lane % 4) takes them from 16 consecutive
-// bytes of the row, and the queries are laid out to match; likewise a lane takes
-// 16 consecutive bytes of the value columns, column j of it belonging to the
-// j-th n8 tile.
+// keys and values, 16 rows of a page and so contiguous, come by 16-byte
+// asynchronous copies, 512 bytes in a row an instruction, into a ring of items
+// of its own (16 keys, or 16 values). (A lane copying just the bytes that it
+// will use needs no exchange, but an instruction then touches 8 or 16 rows: 1024
+// bf16 heads of 9000 positions took 970 us.) The order of a contraction is free:
+// the lane that holds key n's contraction indices 2q, 2q + 1, 2q + 8, 2q + 9 of
+// every k16 step (q = lane % 4) takes them from 16 consecutive bytes of the row,
+// and the queries are laid out to match; likewise a lane takes 16 consecutive
+// bytes of the value columns, column j of it belonging to the j-th n8 tile. The
+// pieces of 16 bytes are permuted within 128 by their key, so that neither read
+// hits a bank twice.
 #include <math.h>
 
 #include <type_traits>
@@ -132,10 +135,17 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
     const int n = on ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-template <int D, int S>
-__device__ __forceinline__ void copy16_at(uint32_t dst, const void *src) {   // dst + D, src + S
-    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(D), "n"(S) : "memory");
+template <int O>
+__device__ __forceinline__ void copy16_at(uint32_t dst, const void *src) {   // dst + O, src + O
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(dst), "l"(src), "n"(O) : "memory");
 }
+// What the 16-byte pieces of a key's row are permuted by (piece p of each 128
+// bytes lies at p ^ turn). 8 lanes that read at once read 4 pieces of keys 2i and
+// 2i + 1, which differ in bit 2 of it, or 2 pieces of values 0, 2, 4, 6 or 1, 3,
+// 5, 7 (mod 8), which differ in bits 1 and 2.
+__device__ __forceinline__ constexpr int turn(int k) { return ((k >> 2 ^ k) & 1) << 2 | (k & 2); }
+// (rows of 128, 256 and 512 bytes; others lie as they come)
+__device__ __forceinline__ bool turned(int width) { return width >= 128 && !(width & (width - 1)); }
 // A loop of constants 0 .. N - 1.
 template <int N, typename F>
 __device__ __forceinline__ void each(F f) {
@@ -165,14 +175,14 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     constexpr int CB = Z::CB, VL = Z::VL, KB = Z::KB, VB = Z::VB, STEPS = Z::STEPS, RING = Z::RING, ITEM = Z::ITEM;
     constexpr bool E4 = CB == 1;
     constexpr bool Q_REGS = TERMS == 1 && N <= 2;   // the queries in registers
-    extern __shared__ __align__(16) unsigned char sm[];
+    extern __shared__ __align__(128) unsigned char sm[];
     __shared__ long long s_share[RW + 2];
     __shared__ float s_m[RW][RV], s_l[RW][RV];
     __shared__ int s_qe[RV];
     __shared__ __align__(16) uint8_t s_exp[E4 ? RW * RING * 32 : 16];   // of an item of keys: theirs, then the values'
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qd = lane & 3, row = lane >> 2;
     unsigned char *ring = sm + (size_t)warp * RING * ITEM;
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring) + 16 * lane;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     uint32_t *sq = (uint32_t *)(sm + (size_t)RW * RING * ITEM);   // [term][step][lane][4]
 
     PgShare share = pg_share<Plan, RT>(a, tab, units, s_share);
@@ -181,6 +191,12 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     const float sc2 = a.scale * 1.4426950408889634f;
     const int kb_n = (a.d * CB + 63) >> 6, vb_n = (a.dv * CB + 127) >> 7;
     const bool k_whole = (a.d * CB & 63) == 0;
+    const int kw = a.d * CB, vw = a.dv * CB;   // bytes of a cached row
+    // this lane's pieces of an item: of key `row` (block b: even and odd ones), of
+    // values 2 qd and 2 qd + 1; 8 rows further on the same
+    const int k_turn = turned(kw) ? turn(row) : 0, v_turn = turned(vw) ? turn(2 * qd) : 0, v_turn1 = turned(vw) ? turn(2 * qd + 1) : 0;
+    const int k_even = row * kw + 16 * (qd ^ k_turn), k_odd = row * kw + 16 * ((4 + qd) ^ k_turn);
+    const int v_even = 2 * qd * vw + 16 * (row ^ v_turn), v_odd = (2 * qd + 1) * vw + 16 * (row ^ v_turn1);
     bool first_seg = true;
     PgSegment seg;
     while (pg_next<Plan>(a, tab, units, share, seg)) {
@@ -255,11 +271,42 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
         int pages = page_of(lane), pages_next = page_of(32 + lane);
         uint32_t present = 0;   // bit i % 32: block i has a page
         int put = 0, put_slot = 0, get_slot = 0;   // next item to issue: block put / 2, keys then values
-        const unsigned char *kbase = (const unsigned char *)a.k + (size_t)(row * a.d + VL * qd) * CB;
-        const unsigned char *vbase = (const unsigned char *)a.v + (size_t)(2 * qd * a.dv + VL * row) * CB;
-        const int kw = a.d * CB, vw = a.dv * CB;   // bytes of a cached row
         int rowid = 0;          // of the block's first position in the pools
         bool inside = false;    // all of the block's positions are attended by some vector, and on a page
+        // 16 rows of `width` bytes from row `rowid` of a pool. Where not all of
+        // them are attended, the others are zeros.
+        auto copy_rows = [&](const void *pool, int width, int i) {
+            const uint32_t dst = ring_at + put_slot * ITEM;
+            const char *src = (const char *)pool + (size_t)(uint32_t)rowid * width + 16 * lane;
+            const bool sw = turned(width);
+            constexpr int MOST = ITEM / 512;
+            if (inside && sw) {
+                // 512 bytes: half a key, one, two or four; piece p of key k goes
+                // to p ^ turn(k), of which the lane's part stands in `at` and
+                // the instruction's is a constant
+                const int log = 31 - __clz(width);   // 7 to 9
+                const uint32_t at = dst + ((16 * lane) ^ (log == 7 ? 16 * turn(lane >> 3) : log == 8 ? 16 * turn(lane >> 4) : 0));
+                each<MOST>([&](auto n) {
+                    if (n * 512 < 16 * width) {
+                        const uint32_t x = log == 7 ? 16 * turn(4 * n) : log == 8 ? 16 * turn(2 * n) : 16 * turn(n);
+                        copy16_at<n * 512>(at ^ x, src);
+                    }
+                });
+            } else if (inside) {
+                each<MOST>([&](auto n) {
+                    if (n * 512 + 16 * lane < 16 * width) copy16_at<n * 512>(dst + 16 * lane, src);
+                });
+            } else {
+                const int p0 = (blk0 + RW * i) * 16;
+                const bool page = present >> (i & 31) & 1;
+#pragma unroll 1
+                for (int o = 16 * lane; o < 16 * width; o += 512) {
+                    const int key = o / width, p = p0 + key;
+                    const bool on = page && p >= x.lo && p <= x.hi;
+                    copy16(dst + (o ^ (sw ? 16 * turn(key) : 0)), on ? src + (o - 16 * lane) : pool, on);
+                }
+            }
+        };
         auto issue_keys = [&]() {
             const int i = put >> 1;
             if (i < nb) {
@@ -268,29 +315,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 present = (present & ~(1u << (i & 31))) | (page >= 0 ? 1u : 0u) << (i & 31);
                 rowid = ((max(page, 0) * a.G + g) << a.lpage) + (p0 & ((1 << a.lpage) - 1));
                 inside = page >= 0 && p0 >= x.lo && p0 + 15 <= x.hi;
-                const uint32_t dst = ring_at + put_slot * ITEM;
-                const unsigned char *src = kbase + (size_t)(uint32_t)rowid * kw;
-                if (inside && k_whole) {
-                    each<KB>([&](auto b) {
-                        if (b < kb_n) copy16_at<b * 512, b * 64>(dst, src);
-                    });
-                    src += 8 * kw;
-                    each<KB>([&](auto b) {
-                        if (b < kb_n) copy16_at<(KB + b) * 512, b * 64>(dst, src);
-                    });
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int p = p0 + 8 * n + row;
-                        const bool in = page >= 0 && p >= x.lo && p <= x.hi;
-#pragma unroll
-                        for (int b = 0; b < KB; ++b)
-                            if (b < kb_n) {
-                                const bool on = in && 4 * VL * b + VL * qd < a.d;
-                                copy16(dst + (n * KB + b) * 512, on ? src + 8 * n * kw + 64 * b : a.k, on);
-                            }
-                    }
-                }
+                copy_rows(a.k, kw, i);
                 if (E4 && lane < 2) {   // the 16 exponents of the keys, and of the values
                     const uint8_t *e = lane ? a.ve : a.ke;
                     copy16((uint32_t)__cvta_generic_to_shared(&s_exp[(warp * RING + put_slot) * 32 + 16 * lane]),
@@ -304,33 +329,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
         auto issue_values = [&]() {   // of the block whose keys were issued last
             const int i = put >> 1;
             if (i < nb) {
-                const uint32_t dst = ring_at + put_slot * ITEM;
-                const unsigned char *src = vbase + (size_t)(uint32_t)rowid * vw;
-                if (inside) {   // (columns past the last only reach outputs that are not written)
-                    const unsigned char *s1 = src + vw, *s8 = src + 8 * vw, *s9 = s8 + vw;
-                    each<VB>([&](auto b) {
-                        if (b < vb_n && 8 * VL * b + VL * row < a.dv) {
-                            copy16_at<(4 * b + 0) * 512, b * 128>(dst, src);
-                            copy16_at<(4 * b + 1) * 512, b * 128>(dst, s1);
-                            copy16_at<(4 * b + 2) * 512, b * 128>(dst, s8);
-                            copy16_at<(4 * b + 3) * 512, b * 128>(dst, s9);
-                        }
-                    });
-                } else {
-                    const int p0 = (blk0 + RW * i) * 16;
-                    const bool page = present >> (i & 31) & 1;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int key = (r & 1) + 8 * (r >> 1), p = p0 + 2 * qd + key;
-                        const bool in = page && p >= x.lo && p <= x.hi;
-#pragma unroll
-                        for (int b = 0; b < VB; ++b)
-                            if (b < vb_n) {
-                                const bool on = in && 8 * VL * b + VL * row < a.dv;
-                                copy16(dst + (b * 4 + r) * 512, on ? src + key * vw + 128 * b : a.v, on);
-                            }
-                    }
-                }
+                copy_rows(a.v, vw, i);
                 if ((i & 31) == 31) {
                     pages = pages_next;
                     pages_next = page_of(i + 33 + lane);
@@ -345,15 +344,14 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             if (keys) issue_keys();
             else issue_values();
         };
-        // the item to use next: all but the last RING - 1 groups are here (for
-        // the exponents, which two lanes copied, at every lane)
+        // the item to use next: all but the last RING - 1 groups of every lane are here
         auto item = [&]() -> const unsigned char * {
             copy_wait<RING - 1>();
-            if (E4) __syncwarp();
-            return ring + get_slot * ITEM + 16 * lane;
+            __syncwarp();
+            return ring + get_slot * ITEM;
         };
         auto done = [&]() {
-            if (E4) __syncwarp();
+            __syncwarp();
             get_slot = get_slot + 1 == RING ? 0 : get_slot + 1;
         };
 #pragma unroll 1
@@ -372,7 +370,10 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 if (b < kb_n) {
                     uint4 kw4[2];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) kw4[n] = *(const uint4 *)(it + (n * KB + b) * 512);
+                    for (int n = 0; n < 2; ++n) {
+                        kw4[n] = *(const uint4 *)(it + (b & 1 ? k_odd : k_even) + (b >> 1) * 128 + n * 8 * kw);
+                        if (!k_whole && b == kb_n - 1 && 4 * VL * b + VL * qd >= a.d) kw4[n] = make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
                     for (int st = 0; st < VL / 4; ++st) {
                         uint32_t b0[2], b1[2];
@@ -488,7 +489,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 if (b < vb_n) {
                     uint32_t vr[4][4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) *(uint4 *)vr[r] = *(const uint4 *)(it + (b * 4 + r) * 512);
+                    for (int r = 0; r < 4; ++r) *(uint4 *)vr[r] = *(const uint4 *)(it + (r & 1 ? v_odd : v_even) + b * 128 + (r >> 1) * 8 * vw);
 #pragma unroll
                     for (int j4 = 0; j4 < 4; ++j4) {
                         uint32_t b0[VL / 4], b1[VL / 4];   // of the columns in word j4
