@@ -2,8 +2,12 @@
 // way, and read back; and the C ABI of the cache and of the attention over it.
 //
 // Bound of both copies: HBM, each value read once and written once. A group of
-// lanes takes a head's row, 8 values a lane, four rows a group of lanes in
-// flight.
+// LPV lanes takes head rows, 8 values a lane: up to four heads of a position, all
+// in flight, while the next position's page is looked up. Of 16-bit rows a lane
+// takes 8 values in a row; of fp32 rows 4 and the 4 that lie 4 LPV further on, so
+// that an instruction of either side covers whole lines. 32749 fp32 rows of 4
+// heads of 128 to e4m3: 34 us, 4.9 TB/s (a head at a time, each with its own look
+// and addresses, took 43: instruction issue).
 #include <math.h>
 #include <stdint.h>
 
@@ -13,56 +17,98 @@
 
 namespace {
 
-constexpr int CP_THREADS = 256;
+constexpr int CP_THREADS = 256, CP_BLOCKS = 4;   // of a block; blocks an SM
 
 struct Vec8 {
     float x[8];
 };
-__device__ __forceinline__ Vec8 ld8(const float *p) {
-    const float4 a = o1_ld4(p), b = o1_ld4(p + 4);
-    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+__device__ __forceinline__ void put4(Vec8 &v, int i, float4 f) {
+    v.x[i] = f.x;
+    v.x[i + 1] = f.y;
+    v.x[i + 2] = f.z;
+    v.x[i + 3] = f.w;
 }
-template <typename T>
-__device__ __forceinline__ Vec8 ld8_16(const T *p) {
-    const uint4 u = *(const uint4 *)p;
-    const uint2 h[2] = {make_uint2(u.x, u.y), make_uint2(u.z, u.w)};
-    const float4 a = o1_ld4((const T *)&h[0]), b = o1_ld4((const T *)&h[1]);
-    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+__device__ __forceinline__ float4 get4(const Vec8 &v, int i) { return make_float4(v.x[i], v.x[i + 1], v.x[i + 2], v.x[i + 3]); }
+// 4 e4m3 codes
+__device__ __forceinline__ float4 codes4(uint32_t w) {
+    uint32_t h[2];
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"((uint16_t)w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"((uint16_t)(w >> 16)));
+    const float2 a = __half22float2(*(const __half2 *)&h[0]), b = __half22float2(*(const __half2 *)&h[1]);
+    return make_float4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ Vec8 ld8(const __nv_bfloat16 *p) { return ld8_16(p); }
-__device__ __forceinline__ Vec8 ld8(const __half *p) { return ld8_16(p); }
-// e4m3 codes
-__device__ __forceinline__ Vec8 ld8(const uint8_t *p) {
-    const uint2 u = *(const uint2 *)p;
-    Vec8 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint16_t two = (uint16_t)((i < 2 ? u.x : u.y) >> (16 * (i & 1)));
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-        const float2 f = __half22float2(*(const __half2 *)&h);
-        r.x[2 * i] = f.x;
-        r.x[2 * i + 1] = f.y;
-    }
-    return r;
-}
-__device__ __forceinline__ void st8(float *p, const Vec8 &v) {
-    o1_st4(p, make_float4(v.x[0], v.x[1], v.x[2], v.x[3]));
-    o1_st4(p + 4, make_float4(v.x[4], v.x[5], v.x[6], v.x[7]));
-}
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 *, float a, float b) {
+__device__ __forceinline__ uint32_t pack2(const __nv_bfloat16 *, float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *(const uint32_t *)&h;
 }
-__device__ __forceinline__ uint32_t pack2(__half *, float a, float b) {
+__device__ __forceinline__ uint32_t pack2(const __half *, float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *(const uint32_t *)&h;
 }
-template <typename T>
-__device__ __forceinline__ void st8(T *p, const Vec8 &v) {
-    *(uint4 *)p = make_uint4(pack2(p, v.x[0], v.x[1]), pack2(p, v.x[2], v.x[3]), pack2(p, v.x[4], v.x[5]),
-                             pack2(p, v.x[6], v.x[7]));
-}
+
+// A lane's 8 values of a head's row of `width`: how they lie for rows of T, as
+// loads and stores of a row of R (T, or the cache's type).
+template <typename T, int LPV>
+struct Lay {
+    static constexpr bool APART = sizeof(T) == 4;   // two runs of 4
+    static __device__ __forceinline__ int at(int lane, int half) { return APART ? 4 * lane + 4 * LPV * half : 8 * lane + 4 * half; }
+    static __device__ __forceinline__ bool on(int lane, int half, int width) { return at(lane, half) < width; }
+    static __device__ __forceinline__ Vec8 load(const float *p, int lane, int width) {
+        Vec8 v;
+        put4(v, 0, on(lane, 0, width) ? o1_ld4(p + at(lane, 0)) : make_float4(0.f, 0.f, 0.f, 0.f));
+        put4(v, 4, on(lane, 1, width) ? o1_ld4(p + at(lane, 1)) : make_float4(0.f, 0.f, 0.f, 0.f));
+        return v;
+    }
+    template <typename R>
+    static __device__ __forceinline__ Vec8 load(const R *p, int lane, int width) {   // 16 bits
+        Vec8 v;
+        if (APART) {
+            put4(v, 0, on(lane, 0, width) ? o1_ld4(p + at(lane, 0)) : make_float4(0.f, 0.f, 0.f, 0.f));
+            put4(v, 4, on(lane, 1, width) ? o1_ld4(p + at(lane, 1)) : make_float4(0.f, 0.f, 0.f, 0.f));
+        } else {
+            const uint4 u = on(lane, 0, width) ? *(const uint4 *)(p + 8 * lane) : make_uint4(0u, 0u, 0u, 0u);
+            const uint2 h[2] = {make_uint2(u.x, u.y), make_uint2(u.z, u.w)};
+            put4(v, 0, o1_ld4((const R *)&h[0]));
+            put4(v, 4, o1_ld4((const R *)&h[1]));
+        }
+        return v;
+    }
+    static __device__ __forceinline__ Vec8 load(const uint8_t *p, int lane, int width) {   // codes
+        Vec8 v;
+        uint2 u = make_uint2(0u, 0u);
+        if (APART) {
+            if (on(lane, 0, width)) u.x = *(const uint32_t *)(p + at(lane, 0));
+            if (on(lane, 1, width)) u.y = *(const uint32_t *)(p + at(lane, 1));
+        } else if (on(lane, 0, width)) {
+            u = *(const uint2 *)(p + 8 * lane);
+        }
+        put4(v, 0, codes4(u.x));
+        put4(v, 4, codes4(u.y));
+        return v;
+    }
+    static __device__ __forceinline__ void store(float *p, const Vec8 &v, int lane, int width) {
+        if (on(lane, 0, width)) o1_st4(p + at(lane, 0), get4(v, 0));
+        if (on(lane, 1, width)) o1_st4(p + at(lane, 1), get4(v, 4));
+    }
+    template <typename R>
+    static __device__ __forceinline__ void store(R *p, const Vec8 &v, int lane, int width) {
+        if (APART) {
+            if (on(lane, 0, width)) o1_st4(p + at(lane, 0), get4(v, 0));
+            if (on(lane, 1, width)) o1_st4(p + at(lane, 1), get4(v, 4));
+        } else if (on(lane, 0, width)) {
+            *(uint4 *)(p + 8 * lane) = make_uint4(pack2(p, v.x[0], v.x[1]), pack2(p, v.x[2], v.x[3]), pack2(p, v.x[4], v.x[5]),
+                                                  pack2(p, v.x[6], v.x[7]));
+        }
+    }
+    static __device__ __forceinline__ void store(uint8_t *p, uint2 codes, int lane, int width) {
+        if (APART) {
+            if (on(lane, 0, width)) *(uint32_t *)(p + at(lane, 0)) = codes.x;
+            if (on(lane, 1, width)) *(uint32_t *)(p + at(lane, 1)) = codes.y;
+        } else if (on(lane, 0, width)) {
+            *(uint2 *)(p + 8 * lane) = codes;
+        }
+    }
+};
 
 // A head's row, LPV lanes of 8 values, as e4m3 codes under a power of two:
 // returns the byte e + 127. With max |x| = 1.m 2^(E - 127) the least e has
@@ -71,53 +117,60 @@ __device__ __forceinline__ void st8(T *p, const Vec8 &v) {
 // subnormals. The factor 2^-e is a normal number and x 2^-e exact unless it
 // falls below fp32's range, far below e4m3's.
 template <int LPV>
-__device__ __forceinline__ uint32_t quantise8(const Vec8 &v, uint2 &codes) {
-    float top = 0.f;
+__device__ __forceinline__ uint32_t quantise8(Vec8 v, uint2 &codes) {
+    constexpr uint32_t INF = 0x7f800000u;
+    uint32_t top = 0;   // of |x| as bits, which are in its order
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = fabsf(v.x[i]);
-        top = fmaxf(top, x < INFINITY ? x : 0.f);
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v.x[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int m = 1; m < LPV; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+    if (__any_sync(0xffffffffu, top >= INF)) {   // infinities and NaN: apart from the maximum, and NaN
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t x = __float_as_uint(v.x[i]) & 0x7fffffffu;
+            if (x >= INF) v.x[i] = NAN;
+            else top = max(top, x);
+        }
+#pragma unroll
+        for (int m = 1; m < LPV; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
     }
-#pragma unroll
-    for (int m = 1; m < LPV; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const uint32_t bits = __float_as_uint(top);
-    const int e = max(1, (int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+    const int e = max(1, (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
     const float f = __uint_as_float((uint32_t)(254 - e) << 23);
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float a = v.x[2 * i] * f, b = v.x[2 * i + 1] * f;
-        if (!(fabsf(v.x[2 * i]) < INFINITY)) a = NAN;   // infinities would saturate
-        if (!(fabsf(v.x[2 * i + 1]) < INFINITY)) b = NAN;
         uint16_t two;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(v.x[2 * i + 1] * f), "f"(v.x[2 * i] * f));
         h[i] = two;
     }
     codes = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     return (uint32_t)e;
 }
 
-// A head's row into the cache at `at`; every lane of the group calls it.
-template <typename C, int LPV>
+// A head's row into the cache at `at` (null: nowhere); every lane of the group
+// calls it, with zeros past the row's end.
+template <typename L, typename C, int LPV>
 struct Store {
-    static __device__ __forceinline__ void row(C *at, uint8_t *, const Vec8 &v, int lane, bool on) {
-        if (on) st8(at + 8 * lane, v);
+    static __device__ __forceinline__ void row(C *at, uint8_t *, const Vec8 &v, int lane, int width) {
+        if (at) L::store(at, v, lane, width);
     }
 };
-template <int LPV>
-struct Store<uint8_t, LPV> {
-    static __device__ __forceinline__ void row(uint8_t *at, uint8_t *exp, const Vec8 &v, int lane, bool on) {
+template <typename L, int LPV>
+struct Store<L, uint8_t, LPV> {
+    static __device__ __forceinline__ void row(uint8_t *at, uint8_t *exp, const Vec8 &v, int lane, int width) {
         uint2 codes;
         const uint32_t e = quantise8<LPV>(v, codes);
-        if (on) *(uint2 *)(at + 8 * lane) = codes;
-        if (on && lane == 0) *exp = (uint8_t)e;
+        if (!at) return;
+        L::store(at, codes, lane, width);
+        if (lane == 0) *exp = (uint8_t)e;
     }
 };
-template <typename C>
-__device__ __forceinline__ Vec8 cached8(const C *at, const uint8_t *, int lane) { return ld8(at + 8 * lane); }
-template <>
-__device__ __forceinline__ Vec8 cached8<uint8_t>(const uint8_t *at, const uint8_t *exp, int lane) {
-    Vec8 v = ld8(at + 8 * lane);
+template <typename L, typename C>
+__device__ __forceinline__ Vec8 cached8(const C *at, const uint8_t *, int lane, int width) { return L::load(at, lane, width); }
+template <typename L>
+__device__ __forceinline__ Vec8 cached8(const uint8_t *at, const uint8_t *exp, int lane, int width) {
+    Vec8 v = L::load(at, lane, width);
     const float f = pg_scale(*exp);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.x[i] *= f;
@@ -139,69 +192,75 @@ __device__ __forceinline__ Side<T, C> side_of(const PgArgs &a, bool keys, bool w
     return {(T *)(write ? a.v_in : a.v_out), (C *)a.v, a.ve, a.vs, a.dv};
 }
 
-// Rows of the table's sequences to their places or back. Head rows are counted
-// i G + g over the live rows i; a block takes a run of them, a group of LPV
-// lanes every GROUPS-th of the run.
+// Rows of the table's sequences to their places or back. Work is counted in
+// (live row, four heads); a block takes a run of it, a group of LPV lanes every
+// GROUPS-th of the run.
 template <typename T, typename C, int LPV, bool WRITE>
 __device__ __forceinline__ void copy_run(const PgArgs &a, const PgTable &tab, bool keys) {
+    using L = Lay<T, LPV>;
     constexpr int GROUPS = CP_THREADS / LPV, U = 4;
     const Side<T, C> s = side_of<T, C>(a, keys, WRITE);
-    const int lane = threadIdx.x % LPV, grp = threadIdx.x / LPV;
-    const bool on = 8 * lane < s.width;
-    const int64_t all = (int64_t)tab.total * a.G, per = (all + gridDim.x - 1) / gridDim.x;
-    const int64_t run = (per + GROUPS * U - 1) / (GROUPS * U) * (GROUPS * U);
-    const int64_t v0 = run * blockIdx.x, v1 = min(all, v0 + run);
-    if (v0 >= v1) return;
-    int i = (int)((v0 + grp) / a.G), g = (int)(v0 + grp - (int64_t)i * a.G);
-    const int step_i = GROUPS / a.G, step_g = GROUPS - step_i * a.G;
+    const int lane = threadIdx.x % LPV, grp = threadIdx.x / LPV, four = (a.G + U - 1) / U;
+    const int64_t all = (int64_t)tab.total * four, turns = (all + GROUPS - 1) / GROUPS;
+    const int64_t v0 = turns * blockIdx.x / gridDim.x * GROUPS, v1 = min(all, turns * (blockIdx.x + 1) / gridDim.x * GROUPS);
+    int i = (int)((v0 + grp) / four), g = (int)(v0 + grp - (int64_t)i * four);   // of this group's next piece
+    const int step_i = GROUPS / four, step_g = GROUPS - step_i * four;
     int n = 0;
     for (int hi = tab.n - 1; n < hi;) {   // the last sequence that starts at or before row i
         const int mid = (n + hi + 1) >> 1;
         if (tab.s[mid].before <= i) n = mid;
         else hi = mid - 1;
     }
-    for (int64_t v = v0; v < v1; v += GROUPS * U) {
+    struct Piece {
+        int row, page, at, g;   // row of the tensors, page (-1: none), row in it, first head
+    };
+    auto piece = [&](int64_t v) {
+        Piece p = {0, -1, 0, U * g};
+        if (v < v1) {
+            while (n + 1 < tab.n && tab.s[n + 1].before <= i) ++n;
+            const int r = i - tab.s[n].before, pos = tab.s[n].pos0 + r;
+            p.row = tab.s[n].row0 + r;
+            p.page = pg_page(a, tab.s[n].slot, pos);
+            p.at = pos & ((1 << a.lpage) - 1);
+        }
+        g += step_g;
+        i += step_i;
+        if (g >= four) g -= four, ++i;
+        return p;
+    };
+    const size_t head = (size_t)s.width << a.lpage;   // from a group's rows of a page to the next one's
+    Piece p = piece(v0 + grp);
+    for (int64_t v = v0; v < v1; v += GROUPS) {
+        T *row = s.rows + (size_t)p.row * s.stride + (size_t)p.g * s.width;
+        const bool live = p.page >= 0;
+        const size_t place = (((size_t)max(p.page, 0) * a.G + p.g) << a.lpage) + p.at;
+        C *at = s.pool + place * s.width;
+        uint8_t *exp = sizeof(C) == 1 ? s.exp + place : nullptr;
+        const int heads = live ? min(U, a.G - p.g) : 0;
         Vec8 x[U];
-        C *at[U];
-        uint8_t *ex[U];
-        T *row[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            at[u] = nullptr;
-            if (v + grp + GROUPS * u < v1) {
-                while (n + 1 < tab.n && tab.s[n + 1].before <= i) ++n;
-                const int r = i - tab.s[n].before, p = tab.s[n].pos0 + r;
-                const int page = pg_page(a, tab.s[n].slot, p), w = p & ((1 << a.lpage) - 1);
-                row[u] = s.rows + (size_t)(tab.s[n].row0 + r) * s.stride + (size_t)g * s.width;
-                if (page >= 0) {
-                    at[u] = pg_at(s.pool, a, page, g, w, s.width);
-                    if (sizeof(C) == 1) ex[u] = pg_at(s.exp, a, page, g, w, 1);
-                }
-                if (WRITE && on) x[u] = ld8((const T *)row[u] + 8 * lane);
+            if (u < heads) {
+                if (WRITE) x[u] = L::load((const T *)row + (size_t)u * s.width, lane, s.width);
+                else x[u] = cached8<L>((const C *)at + u * head, exp + ((size_t)u << a.lpage), lane, s.width);
+            } else {
+                x[u] = {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
             }
-            g += step_g;
-            i += step_i;
-            if (g >= a.G) g -= a.G, ++i;
         }
-        if (WRITE) {
+        p = piece(v + GROUPS + grp);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!on || !at[u]) x[u] = {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
-                Store<C, LPV>::row(at[u], ex[u], x[u], lane, on && at[u]);
+        for (int u = 0; u < U; ++u) {
+            if (WRITE) {
+                if (u < a.G) Store<L, C, LPV>::row(u < heads ? at + u * head : nullptr, exp + ((size_t)u << a.lpage), x[u], lane, s.width);
+            } else if (u < heads) {
+                L::store(row + (size_t)u * s.width, x[u], lane, s.width);
             }
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (on && at[u]) x[u] = cached8(at[u], ex[u], lane);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (on && at[u]) st8(row[u] + 8 * lane, x[u]);
         }
     }
 }
 
 template <typename T, typename C, int LPV, bool WRITE>
-__global__ __launch_bounds__(CP_THREADS) void k_pg_copy(PgArgs a, const __grid_constant__ PgTable tab) {
+__global__ __launch_bounds__(CP_THREADS, CP_BLOCKS) void k_pg_copy(PgArgs a, const __grid_constant__ PgTable tab) {
     copy_run<T, C, LPV, WRITE>(a, tab, blockIdx.y == 0);
 }
 
@@ -209,17 +268,17 @@ __global__ __launch_bounds__(CP_THREADS) void k_pg_copy(PgArgs a, const __grid_c
 // place, then its head rows.
 template <typename T, typename C, int LPV>
 __device__ __forceinline__ void token_side(const PgArgs &a, const PgRow &pr, int page, bool keys) {
+    using L = Lay<T, LPV>;
     constexpr int GROUPS = CP_THREADS / LPV;
     const Side<T, C> s = side_of<T, C>(a, keys, true);
     const int lane = threadIdx.x % LPV, grp = threadIdx.x / LPV, w = pr.pos & ((1 << a.lpage) - 1);
-    const bool on = 8 * lane < s.width;
     for (int g0 = 0; g0 < a.G; g0 += GROUPS) {   // the same number of turns for every lane: shuffles inside
         const int g = min(g0 + grp, a.G - 1);
-        const bool live = on && g0 + grp < a.G;
+        const bool live = g0 + grp < a.G;
         Vec8 x = {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
-        if (live) x = ld8((const T *)s.rows + (size_t)blockIdx.x * s.stride + (size_t)g * s.width + 8 * lane);
-        Store<C, LPV>::row(pg_at(s.pool, a, page, g, w, s.width), sizeof(C) == 1 ? pg_at(s.exp, a, page, g, w, 1) : nullptr,
-                           x, lane, live);
+        if (live) x = L::load((const T *)s.rows + (size_t)blockIdx.x * s.stride + (size_t)g * s.width, lane, s.width);
+        Store<L, C, LPV>::row(live ? pg_at(s.pool, a, page, g, w, s.width) : nullptr, sizeof(C) == 1 ? pg_at(s.exp, a, page, g, w, 1) : nullptr,
+                              x, lane, s.width);
     }
 }
 template <typename T, typename C, int LPV>
@@ -245,8 +304,9 @@ void copy_launch_l(const PgArgs &a, const PgTable *tab, cudaStream_t st) {
         if (WRITE) k_pg_token_write<T, C, LPV><<<a.rows, CP_THREADS, 0, st>>>(a);
         return;
     }
-    // at most three blocks an SM and side, fewer where the rows do not fill them
-    const int64_t vecs = (int64_t)tab->total * a.G, turn = CP_THREADS / LPV * 4, want = (vecs + turn - 1) / turn, most = 152 * 3;
+    // one wave of blocks over both sides, fewer where the rows do not fill them
+    const int64_t work = (int64_t)tab->total * ((a.G + 3) / 4), turn = CP_THREADS / LPV, want = (work + turn - 1) / turn;
+    const int64_t most = 152 * CP_BLOCKS / 2;
     k_pg_copy<T, C, LPV, WRITE><<<dim3((unsigned)(want < most ? want : most), 2), CP_THREADS, 0, st>>>(a, *tab);
 }
 template <typename T, typename C, bool WRITE>

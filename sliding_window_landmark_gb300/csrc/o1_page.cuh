@@ -194,9 +194,10 @@ __device__ __forceinline__ bool pg_next(const PgArgs &a, const PgTable &tab, int
     return false;
 }
 
-// What a block leaves of the units that its borders cut: the values [V][dv] and
-// the statistics [V][2] (maximum in log2 units, sum) of its first segment and of
-// its last, and in its header the first one's unit.
+// What a block leaves of the units that its borders cut: the values [dv / 4][V][4]
+// (a warp's threads hold a vector each, and their 16 bytes lie in a row) and the
+// statistics [V][2] (maximum in log2 units, sum) of its first segment and of its
+// last, and in its header the first one's unit.
 struct PgHead {
     int last;       // the last block with a part of the unit; -1: none begins its tiles in the block before
     int row0, vec0, nv, g;
@@ -208,6 +209,10 @@ struct PgParts {
 };
 __host__ __device__ inline PgParts pg_parts(float *p, int blocks, int vecs) {
     return {(PgHead *)p, p + (size_t)blocks * 8, p + (size_t)blocks * 8 + (size_t)blocks * 2 * vecs * 2};
+}
+// Columns c .. c + 3 of vector v of partial result ps.
+__device__ __forceinline__ float4 *pg_val(const PgParts &p, size_t ps, int vecs, int dv, int v, int c) {
+    return (float4 *)p.val + (ps * (dv >> 2) + (c >> 2)) * vecs + v;
 }
 static inline size_t pg_parts_bytes(int blocks, int vecs, int dv) {
     return o1_al256(((size_t)blocks * 8 + (size_t)blocks * 2 * vecs * (2 + dv)) * 4);

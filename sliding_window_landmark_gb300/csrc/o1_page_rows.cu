@@ -578,7 +578,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 const float r = sum == 0.f ? 0.f : 1.f / sum;   // a NaN stays one
                 o1_st4((T *)a.out + pg_vec_at(a, x.row0, x.vec0 + v, g, a.os, a.dv) + c, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
             } else {
-                *(float4 *)(parts.val + (ps * RV + v) * a.dv + c) = o;
+                *pg_val(parts, ps, RV, a.dv, v, c) = o;
                 if (c == 0) *(float2 *)(parts.stat + (ps * RV + v) * 2) = make_float2(mx, sum);
             }
         }
@@ -588,10 +588,8 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
 }
 
 // The partial results of a unit that borders cut, added up by the blocks of the
-// first border inside it. TPV threads a vector, 4 columns each, and eight parts
-// in flight: what it takes is the latency of three loads one behind the other.
-// SPLIT: one vector a block, its parts dealt to JOIN / TPV groups of threads
-// (few vectors, many parts); otherwise JOIN / TPV vectors a block.
+// first border inside it, eight parts (four) in flight: what it takes is the
+// latency of three loads one behind the other.
 constexpr int JOIN = 256;
 struct Sum {
     float m, l;
@@ -606,57 +604,80 @@ struct Sum {
         o.z = o.z * f + y.z * h;
         o.w = o.w * f + y.w * h;
     }
-};
-template <typename T, int TPV, bool SPLIT>
-__global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs) {
-    constexpr int GROUPS = JOIN / TPV, U = 8;
-    __shared__ Sum part[SPLIT ? JOIN : 1];
-    o1_chain_wait();
-    const int c = blockIdx.x + 1, grp = threadIdx.x / TPV, col = 4 * (threadIdx.x % TPV);
-    const PgParts parts = pg_parts(a.part, blocks, vecs);
-    const PgHead h = parts.head[c];
-    const int v = SPLIT ? blockIdx.y : blockIdx.y * GROUPS + grp;
-    if (h.last < 0 || (SPLIT && v >= h.nv)) return;
-    const bool in = v < h.nv && col < a.dv;
-    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    constexpr int STEP = SPLIT ? GROUPS : 1;
-    if (in)
-        for (int i0 = c - 1 + (SPLIT ? grp : 0); i0 <= h.last; i0 += U * STEP) {
-            float2 st[U];
-            float4 y[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * STEP;
-                const size_t at = (size_t)(i == c - 1 ? 2 * i + 1 : 2 * i) * vecs + v;
-                if (i <= h.last) st[u] = *(const float2 *)(parts.stat + at * 2), y[u] = *(const float4 *)(parts.val + at * a.dv + col);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * STEP <= h.last) s.add(st[u], y[u]);
-        }
-    if (SPLIT) {
-        part[threadIdx.x] = s;
-        __syncthreads();
-        if (grp) return;
-        for (int g = 1; g < GROUPS; ++g) {
-            const Sum &o = part[g * TPV + threadIdx.x];
-            s.add(make_float2(o.m, o.l), o.o);
-        }
+    __device__ __forceinline__ float4 result() const {
+        const float r = l == 0.f ? 0.f : 1.f / l;   // a NaN stays one
+        return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
     }
-    if (!in) return;
-    const float r = s.l == 0.f ? 0.f : 1.f / s.l;   // a NaN stays one
-    o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + col, make_float4(s.o.x * r, s.o.y * r, s.o.z * r, s.o.w * r));
+};
+// Parts first, first + STEP, ... of columns c .. c + 3 of a vector.
+template <int U, int STEP>
+__device__ __forceinline__ Sum join_parts(const PgParts &parts, int border, int last, int first, int vecs, int dv, int v, int c) {
+    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int i0 = border - 1 + first; i0 <= last; i0 += U * STEP) {
+        float2 st[U];
+        float4 y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * STEP;
+            const size_t ps = i == border - 1 ? 2 * (size_t)i + 1 : 2 * (size_t)i;
+            if (i <= last) st[u] = *(const float2 *)(parts.stat + (ps * vecs + v) * 2), y[u] = *pg_val(parts, ps, vecs, dv, v, c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * STEP <= last) s.add(st[u], y[u]);
+    }
+    return s;
 }
+// Few vectors, maybe many parts: a vector a block, TPV threads its columns, the
+// parts dealt to JOIN / TPV groups of them.
 template <typename T, int TPV>
-void join_launch(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
-    if (vecs <= PG_ROWS_V) o1_launch_chained(true, k_pg_join<T, TPV, true>, dim3(blocks - 1, vecs), dim3(JOIN), 0, st, a, blocks, vecs);
-    else o1_launch_chained(true, k_pg_join<T, TPV, false>, dim3(blocks - 1, (vecs + JOIN / TPV - 1) / (JOIN / TPV)), dim3(JOIN), 0, st, a, blocks, vecs);
+__global__ __launch_bounds__(JOIN) void k_pg_join_few(PgArgs a, int blocks, int vecs) {
+    constexpr int GROUPS = JOIN / TPV;
+    __shared__ Sum part[JOIN];
+    o1_chain_wait();
+    const int border = blockIdx.x + 1, grp = threadIdx.x / TPV, c = 4 * (threadIdx.x % TPV), v = blockIdx.y;
+    const PgParts parts = pg_parts(a.part, blocks, vecs);
+    const PgHead h = parts.head[border];
+    if (h.last < 0 || v >= h.nv) return;
+    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (c < a.dv) s = join_parts<8, GROUPS>(parts, border, h.last, grp, vecs, a.dv, v, c);
+    part[threadIdx.x] = s;
+    __syncthreads();
+    if (grp || c >= a.dv) return;
+    for (int g = 1; g < GROUPS; ++g) {
+        const Sum &o = part[g * TPV + threadIdx.x];
+        s.add(make_float2(o.m, o.l), o.o);
+    }
+    o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + c, s.result());
+}
+// Many vectors, a few parts: 32 vectors a block, a lane one of them; their rows
+// go out through shared memory.
+template <typename T>
+__global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs) {
+    __shared__ float4 rows[32][O1_MAX_DV / 4 + 1];
+    o1_chain_wait();
+    const int border = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = 32 * blockIdx.y, v = v0 + lane;
+    const PgParts parts = pg_parts(a.part, blocks, vecs);
+    const PgHead h = parts.head[border];
+    if (h.last < 0 || v0 >= h.nv) return;
+    const int four = a.dv >> 2;
+    if (v < h.nv)
+        for (int c4 = warp; c4 < four; c4 += JOIN / 32)
+            rows[lane][c4] = join_parts<4, 1>(parts, border, h.last, 0, vecs, a.dv, v, 4 * c4).result();
+    __syncthreads();
+    const int nv = min(32, h.nv - v0);
+    for (int i = threadIdx.x; i < nv * four; i += JOIN) {
+        const int r = i / four, c4 = i - r * four;
+        o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v0 + r, h.g, a.os, a.dv) + 4 * c4, rows[r][c4]);
+    }
 }
 template <typename T>
-void join_launch_t(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
-    if (a.dv <= 64) join_launch<T, 16>(a, blocks, vecs, st);
-    else if (a.dv <= 128) join_launch<T, 32>(a, blocks, vecs, st);
-    else join_launch<T, 64>(a, blocks, vecs, st);
+void join_launch(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
+    const dim3 few(blocks - 1, vecs), many(blocks - 1, (vecs + 31) / 32);
+    if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN), 0, st, a, blocks, vecs);
+    else if (a.dv <= 64) o1_launch_chained(true, k_pg_join_few<T, 16>, few, dim3(JOIN), 0, st, a, blocks, vecs);
+    else if (a.dv <= 128) o1_launch_chained(true, k_pg_join_few<T, 32>, few, dim3(JOIN), 0, st, a, blocks, vecs);
+    else o1_launch_chained(true, k_pg_join_few<T, 64>, few, dim3(JOIN), 0, st, a, blocks, vecs);
 }
 
 template <typename T, typename C, int N>
@@ -692,9 +713,9 @@ cudaError_t rows_launch_c(const PgArgs &a, const PgTable *tab, int units, cudaSt
 size_t pg_rows_scratch(int dv) { return pg_parts_bytes(BLOCKS, RV, dv); }
 
 cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, cudaStream_t st) {
-    if (dtype == O1_F32) join_launch_t<float>(a, blocks, vecs, st);
-    else if (dtype == O1_BF16) join_launch_t<__nv_bfloat16>(a, blocks, vecs, st);
-    else join_launch_t<__half>(a, blocks, vecs, st);
+    if (dtype == O1_F32) join_launch<float>(a, blocks, vecs, st);
+    else if (dtype == O1_BF16) join_launch<__nv_bfloat16>(a, blocks, vecs, st);
+    else join_launch<__half>(a, blocks, vecs, st);
     return cudaGetLastError();
 }
 

@@ -82,7 +82,7 @@ struct Types<__half, uint8_t> {
 constexpr int REGS = 128;
 template <bool E4>
 struct Regs {
-    static constexpr int PRODUCER = E4 ? 104 : 88, ISSUER = 72, SOFTMAX = E4 ? 168 : 176;
+    static constexpr int PRODUCER = E4 ? 128 : 88, ISSUER = E4 ? 64 : 72, SOFTMAX = E4 ? 160 : 176;
     static_assert(2 * SOFTMAX + PRODUCER + ISSUER <= 4 * REGS, "no more than the block has");
 };
 template <int N>
@@ -400,7 +400,6 @@ struct Producer {
     __device__ __forceinline__ void item(const PgSegment &s, int j, int ids, int part, bool boxes) {
         if (!ok) return;
         wait_for(&sh.empty[put.slot], put.phase ^ 1);
-        if (E4 && !ok) return;
         const int width = KEYS ? a.d : a.dv, col0 = KEYS ? 128 * part : 0, key0 = KEYS ? 0 : z.v_keys * part;
         const int rows = KEYS ? 128 : z.v_keys, runs = rows / 16;
         const int cols = min(KEYS ? 128 : 256, (width + 15) / 16 * 16 - col0);   // to be filled
@@ -452,55 +451,122 @@ struct Producer {
                     }
                 }
             }
-        } else {
-            // 16 codes a thread, two pieces of a 64-column block; four threads
-            // cover a block, and the 8 of a row write their two pieces in
-            // opposite orders, so that no bank is hit twice
-            const uint8_t *exps = KEYS ? a.ke : a.ve;
-            const int halves = cols > 128 ? 2 : 1;
-#pragma unroll 1
-            for (int i0 = 0; i0 < runs; i0 += 4) {
-                uint4 w[4][2];
-                uint32_t e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int page = __shfl_sync(0xffffffffu, ids, key0 / 16 + i0 + i), p = p0 + 16 * (i0 + i) + r4;
-                    const bool in = page >= 0 && p >= s.x.lo && p <= s.x.hi;
-                    const int at = p & ((1 << a.lpage) - 1);
-                    const C *src = pg_at(pool, a, max(page, 0), s.g, at, width) + col0;
-                    e[i] = in ? *pg_at(exps, a, page, s.g, at, 1) : 0u;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = 128 * h + 16 * l8;
-                        w[i][h] = make_uint4(0u, 0u, 0u, 0u);
-                        if (h < halves && in && col0 + c < width) w[i][h] = *(const uint4 *)(src + c);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t f2 = e[i] * 0x00800080u;   // 2^(byte - 127) twice
-                    const __nv_bfloat162 f = *(const __nv_bfloat162 *)&f2;
-                    const int row = 16 * (i0 + i) + r4;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = 128 * h + 16 * l8;
-                        if (h >= halves || c >= cols) continue;
-                        const uint32_t at = dst + (c >> 6) * (rows * 128);
-                        const int p = (c & 63) >> 3, odd = (l8 >> 2) & 1;
-                        const uint4 lo = bf16_of_e4m3(make_uint2(w[i][h].x, w[i][h].y), f);
-                        const uint4 hi = bf16_of_e4m3(make_uint2(w[i][h].z, w[i][h].w), f);
-                        st16(at + piece(row, p + odd), odd ? hi : lo);
-                        st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
-                    }
-                }
-            }
         }
         announce(full);
         put.next(z.nslot);
         ++sent;
     }
 
+    // e4m3: an item's codes and powers of two in registers, 16 codes of eight
+    // rows a thread (of four rows and both halves of 256 columns), so that the
+    // next item's loads are under way while one is converted.
+    struct Codes {
+        uint4 w[8];
+        uint32_t e[8];
+    };
+    struct Item {
+        bool keys;
+        int j, part;
+    };
+    __device__ __forceinline__ void fetch(const PgSegment &s, const Item &x, int ids, Codes &r) {
+        const int width = x.keys ? a.d : a.dv, col0 = x.keys ? 128 * x.part : 0, key0 = x.keys ? 0 : z.v_keys * x.part;
+        const int p0 = (s.x.lo / KT + x.j) * KT + key0, halves = !x.keys && z.v_keys == 64 ? 2 : 1;
+        const C *pool = (const C *)(x.keys ? a.k : a.v);
+        const uint8_t *exps = x.keys ? a.ke : a.ve;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int run = halves == 2 ? i >> 1 : i, page = __shfl_sync(0xffffffffu, ids, key0 / 16 + run), p = p0 + 16 * run + r4;
+            const bool in = page >= 0 && p >= s.x.lo && p <= s.x.hi;
+            const uint32_t row = (uint32_t)((((page * a.G) + s.g) << a.lpage) + (p & ((1 << a.lpage) - 1)));
+            const int c = col0 + 16 * l8 + (halves == 2 ? 128 * (i & 1) : 0);
+            r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+            r.e[i] = 0;
+            if (in) r.e[i] = exps[row];
+            if (in && c < width) r.w[i] = *(const uint4 *)(pool + (size_t)row * width + c);
+        }
+    }
+    // Four threads cover the 64 columns of a block, and the 8 of a row write their
+    // two pieces in opposite orders, so that no bank is hit twice.
+    __device__ __forceinline__ void convert(const Item &x, const Codes &r) {
+        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles);
+        if (!ok) return;
+        const int width = x.keys ? a.d : a.dv, rows = x.keys ? 128 : z.v_keys, halves = !x.keys && z.v_keys == 64 ? 2 : 1;
+        const int cols = min(halves == 2 ? 256 : 128, (width + 15) / 16 * 16 - (x.keys ? 128 * x.part : 0));
+        const uint32_t dst = ring0 + put.slot * SLOT;
+        const int odd = (l8 >> 2) & 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 16 * (halves == 2 ? i >> 1 : i) + r4, c = 16 * l8 + (halves == 2 ? 128 * (i & 1) : 0);
+            const uint32_t f2 = r.e[i] * 0x00800080u;   // 2^(byte - 127) twice
+            const __nv_bfloat162 f = *(const __nv_bfloat162 *)&f2;
+            if (c < cols) {
+                const uint32_t at = dst + (c >> 6) * (rows * 128);
+                const int p = (c & 63) >> 3;
+                const uint4 lo = bf16_of_e4m3(make_uint2(r.w[i].x, r.w[i].y), f);
+                const uint4 hi = bf16_of_e4m3(make_uint2(r.w[i].z, r.w[i].w), f);
+                st16(at + piece(row, p + odd), odd ? hi : lo);
+                st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
+            }
+        }
+        announce(&sh.full[put.slot]);
+        put.next(z.nslot);
+    }
+    __device__ __forceinline__ void run_codes(const PgTable &tab, int units, PgShare share) {
+        PgSegment s;
+        while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
+            // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
+            Item x = {true, s.t0, 0};
+            auto next = [&](Item &i) -> bool {   // false after the last
+                if (++i.part < (i.keys ? z.k_items : z.v_items)) return true;
+                i.part = 0;
+                if (QT == 2) {
+                    if (!i.keys) ++i.j;
+                    i.keys = !i.keys;
+                } else if (i.keys) {
+                    if (i.j == s.t0 && i.j + 1 < s.t1) ++i.j;   // the second tile's keys
+                    else if (i.j == s.t0) i.keys = false;
+                    else i.keys = false, --i.j;
+                } else {
+                    i.j += 2;
+                    i.keys = i.j < s.t1;
+                    if (!i.keys) --i.j;                           // no keys are left: the next values
+                }
+                return i.j < s.t1;
+            };
+            // pages of tiles t and on, t the last one whose values are to come
+            int tile = s.t0, ids = pages(s, tile), ids1 = pages(s, tile + 1), ids2 = pages(s, tile + 2);
+            auto of = [&](int j) -> int {
+                while (tile + 1 < j || (tile < j && !x.keys)) {
+                    ++tile;
+                    ids = ids1;
+                    ids1 = ids2;
+                    ids2 = pages(s, tile + 2);   // looked up a tile ahead
+                }
+                return j == tile ? ids : ids1;
+            };
+            Codes now;
+            fetch(s, x, of(x.j), now);
+            ok = warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
+            if (!ok) return;
+            qp ^= 1;
+            queries(s);
+#pragma unroll 1
+            for (bool more = true; ok && more;) {
+                const Item was = x;
+                more = next(x);
+                Codes then;
+                if (more) fetch(s, x, of(x.j), then);
+                convert(was, now);
+                now = then;
+            }
+        }
+    }
+
     __device__ __forceinline__ void run(const PgTable &tab, int units, PgShare share) {
+        if constexpr (E4) run_codes(tab, units, share);
+        else run_rows(tab, units, share);
+    }
+    __device__ __forceinline__ void run_rows(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
         while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
             // a tile of a 16-bit cache comes in boxes where some row of the
@@ -786,6 +852,26 @@ __device__ __forceinline__ void st8(T *p, const float *x) {
     *(uint4 *)p = make_uint4(pack_m(p, x[0], x[1]), pack_m(p, x[2], x[3]), pack_m(p, x[4], x[5]), pack_m(p, x[6], x[7]));
 }
 
+// 32 bytes: 8 floats, or 16 values of T
+__device__ __forceinline__ void st32_words(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st32(float *p, const float *x) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    st32_words(p, w);
+}
+template <typename T>
+__device__ __forceinline__ void st32(T *p, const float *x) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_m(p, x[2 * i], x[2 * i + 1]);
+    st32_words(p, w);
+}
+
 template <typename T, typename C, int QT>
 __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape &z, uint32_t tmem, const PgTable &tab, int units,
                                         PgShare share, int vecs) {
@@ -1017,18 +1103,31 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
         const int v = v0 + row;
         const bool whole = s.whole(), in = v < x.nv;
         const float f = !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const size_t ps = (size_t)s.part() * vecs + v;
+        const size_t ps = s.part();
+        const bool wide = ((uintptr_t)a.out | a.os * sizeof(T) | a.dv * sizeof(T)) % 32 == 0;
         T *out = (T *)a.out + (in ? pg_vec_at(a, x.row0, x.vec0 + v, s.g, a.os, a.dv) : 0);
-        if (in && !whole && (QT == 2 || wg == 0)) *(float2 *)(parts.stat + ps * 2) = ok ? make_float2(m, l) : make_float2(0.f, NAN);
+        if (in && !whole && (QT == 2 || wg == 0)) *(float2 *)(parts.stat + (ps * vecs + v) * 2) = ok ? make_float2(m, l) : make_float2(0.f, NAN);
         auto write = [&](int c, float *y) {   // 32 columns
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = ok ? y[i] * f : NAN;
+            if (!in) return;
+            if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                if (in && c + i < a.dv) {
-                    if (whole) st8(out + c + i, y + i);
-                    else st8(parts.val + ps * a.dv + c + i, y + i);
-                }
+                for (int i = 0; i < 32; i += 4)
+                    if (c + i < a.dv) *pg_val(parts, ps, vecs, a.dv, v, c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                return;
+            }
+            // 32 bytes a store where the rows allow it: a lane writes a row of
+            // its own, so that a store costs a line a lane whatever its width
+            constexpr int W = 32 / sizeof(T);
+            if (wide && c + 32 <= a.dv) {
+#pragma unroll
+                for (int i = 0; i < 32; i += W) st32(out + c + i, y + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    if (c + i < a.dv) st8(out + c + i, y + i);
+            }
         };
         if constexpr (REG) {
             write(64 * wg, o);
