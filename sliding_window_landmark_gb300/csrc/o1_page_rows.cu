@@ -650,30 +650,31 @@ __global__ __launch_bounds__(JOIN) void k_pg_join_few(PgArgs a, int blocks, int 
     }
     o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + c, s.result());
 }
-// Many vectors, a few parts: 32 vectors a block, a lane one of them; their rows
-// go out through shared memory.
+// Many vectors: 32 vectors and 32 columns a turn, a lane a vector and a warp 4
+// columns; the rows go out through shared memory. A block takes 32 columns where
+// units are small and their parts many, all of them (fewer blocks) where not.
 template <typename T>
 __global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs) {
-    __shared__ float4 rows[32][O1_MAX_DV / 4 + 1];
+    constexpr int W = JOIN / 32;
+    __shared__ float4 rows[32][W + 1];
     o1_chain_wait();
     const int border = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = 32 * blockIdx.y, v = v0 + lane;
     const PgParts parts = pg_parts(a.part, blocks, vecs);
     const PgHead h = parts.head[border];
     if (h.last < 0 || v0 >= h.nv) return;
-    const int four = a.dv >> 2;
-    if (v < h.nv)
-        for (int c4 = warp; c4 < four; c4 += JOIN / 32)
-            rows[lane][c4] = join_parts<4, 1>(parts, border, h.last, 0, vecs, a.dv, v, 4 * c4).result();
-    __syncthreads();
-    const int nv = min(32, h.nv - v0);
-    for (int i = threadIdx.x; i < nv * four; i += JOIN) {
-        const int r = i / four, c4 = i - r * four;
-        o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v0 + r, h.g, a.os, a.dv) + 4 * c4, rows[r][c4]);
+    const int r = threadIdx.x / W, k = threadIdx.x % W;
+    for (int c0 = 4 * W * blockIdx.z; c0 < a.dv; c0 += 4 * W * gridDim.z) {
+        const int c = c0 + 4 * warp;
+        if (v < h.nv && c < a.dv) rows[lane][warp] = join_parts<8, 1>(parts, border, h.last, 0, vecs, a.dv, v, c).result();
+        __syncthreads();
+        if (v0 + r < h.nv && c0 + 4 * k < a.dv)
+            o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v0 + r, h.g, a.os, a.dv) + c0 + 4 * k, rows[r][k]);
+        __syncthreads();
     }
 }
 template <typename T>
 void join_launch(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
-    const dim3 few(blocks - 1, vecs), many(blocks - 1, (vecs + 31) / 32);
+    const dim3 few(blocks - 1, vecs), many(blocks - 1, (vecs + 31) / 32, vecs <= 128 ? (a.dv + 31) / 32 : 1);
     if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN), 0, st, a, blocks, vecs);
     else if (a.dv <= 64) o1_launch_chained(true, k_pg_join_few<T, 16>, few, dim3(JOIN), 0, st, a, blocks, vecs);
     else if (a.dv <= 128) o1_launch_chained(true, k_pg_join_few<T, 32>, few, dim3(JOIN), 0, st, a, blocks, vecs);

@@ -102,10 +102,11 @@ struct Cols {
     static constexpr uint32_t STRIDE = TERMS == 3 ? 192 : 128, OUT = 2 * STRIDE;
     static __device__ __forceinline__ uint32_t score(int b) { return STRIDE * b; }
     static __device__ __forceinline__ uint32_t out(int tile) { return OUT + 128 * tile; }
-    // A operand of 16 keys (step k of 8), term t: 64 keys' first and second
-    // terms lie over the scores of those keys
+    // A operand of 16 keys (step k of 8), term t. P lies over the scores of the
+    // same keys: 64 keys' first 32 columns or, of several terms, 32 keys' first
+    // and second 16; third terms behind the scores
     static __device__ __forceinline__ uint32_t p(int k, int t) {
-        return t < 2 ? 64 * (k >> 2) + 32 * t + 8 * (k & 3) : 128 + 8 * k;
+        return TERMS == 1 ? 64 * (k >> 2) + 8 * (k & 3) : t < 2 ? 32 * (k >> 1) + 16 * t + 8 * (k & 1) : 128 + 8 * k;
     }
 };
 
@@ -636,16 +637,17 @@ __device__ __forceinline__ void run_ss(bool e, uint32_t col, uint64_t qd, uint64
         }
     }
 }
-template <int TERMS>
+// N terms 16 columns apart; STEP: columns from an odd step of 16 keys to the next.
+template <int N, int STEP>
 __device__ __forceinline__ void run_ts(bool e, uint32_t out, uint32_t p, uint64_t vd, uint32_t id, uint32_t acc) {
 #pragma unroll 1
-    for (int x = 4; x > 0; --x) {
+    for (int x = 0; x < 4; ++x) {
 #pragma unroll
-        for (int m = TERMS - 1; m >= 0; --m) {
-            if (e) mma_ts(out, p + 32 * m, vd, id, acc);
+        for (int m = N - 1; m >= 0; --m) {
+            if (e) mma_ts(out, p + 16 * m, vd, id, acc);
             acc = 1;
         }
-        p += 8;
+        p += x & 1 ? STEP : 8;
         vd += 128;
     }
 }
@@ -703,12 +705,12 @@ __device__ __forceinline__ void issuer_of(int tile, const PgArgs &a, Shared &sh,
             ok = ok && warp_wait(&sh.p_full[2 * tile + 1], n & 1, &sh.abort, wl);
             if (!ok || !item()) break;
             const uint64_t vd = dv + (uint64_t)(get.slot * (SLOT / 16));
-            run_ts<1>(e, out, sc + 64, vd + 512, id_o, j > 0);
+            run_ts<1, 8>(e, out, sc + 64, vd + 512, id_o, j > 0);
             commit(&sh.pv_half[tile]);
             ok = warp_wait(&sh.p_full[2 * tile], n & 1, &sh.abort, wl);
             if (!ok) break;
             tc_after();
-            run_ts<1>(e, out, sc, vd, id_o, 1);
+            run_ts<1, 8>(e, out, sc, vd, id_o, 1);
             commit(&sh.pv_done[tile]);
             commit(&sh.empty[get.slot]);
             get.next(z.nslot);
@@ -786,16 +788,17 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
             tc_after();
             const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
             // lower terms first
-            for (int m = 2; m >= 0; --m)
-                for (int h = 0; h < 2; ++h) run_ts<1>(e, out, p + Col::p(4 * h, m), vd + 512 * h, id_o, m < 2 || h > 0);
+            for (int h = 0; h < 2; ++h) run_ts<1, 8>(e, out, p + Col::p(4 * h, 2), vd + 512 * h, id_o, h > 0);
+            for (int m = 1; m >= 0; --m)
+                for (int h = 0; h < 2; ++h) run_ts<1, 24>(e, out, p + Col::p(4 * h, m), vd + 512 * h, id_o, 1);
             commit(&sh.empty[r.slot]);
         } else {
             for (int i = 0; i < z.v_items; ++i) {
                 if (!filled(r)) return;
                 tc_after();
                 const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
-                run_ts<TERMS>(e, out, p + 64 * i, vd, id_o, acc || i > 0);
-                if (z.v_items == 1) run_ts<TERMS>(e, out, p + 64, vd + 512, id_o, 1);
+                run_ts<TERMS, TERMS == 1 ? 8 : 24>(e, out, p + 64 * i, vd, id_o, acc || i > 0);
+                if (z.v_items == 1) run_ts<TERMS, TERMS == 1 ? 8 : 24>(e, out, p + 64, vd + 512, id_o, 1);
                 commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
@@ -961,19 +964,30 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
 #pragma unroll 1
             for (int i = 0; i < QT; ++i) {
                 const int h = QT == 2 ? 1 - i : wg;
-                uint32_t r[64], w[TERMS == 1 ? 32 : 1];
-                float sum = 0.f;
-                if (ok && !idle) {   // raw scores, those not attended -inf
-                    TMEM_LD32(scol + 64 * h, (&r[0]));
-                    TMEM_LD32(scol + 64 * h + 32, (&r[32]));
+                // (several terms: 32 keys at a time, for their maximum and again
+                // for their weights)
+                constexpr int NR = TERMS == 1 ? 64 : 32;
+                uint32_t r[NR], w[TERMS == 1 ? 32 : 1];
+                float sum = 0.f, early = -INFINITY;
+                auto load = [&](int k0) {   // raw scores, those not attended -inf
+#pragma unroll
+                    for (int c = 0; c < NR; c += 32) TMEM_LD32(scol + 64 * h + k0 + c, (&r[c]));
                     tmem_ld_wait();
                     if (!plain) {
-                        const int b0 = low - x0 - 64 * h, b1 = pos - x0 - 64 * h;
-                        const uint32_t on = there >> (4 * h);
+                        const int b0 = low - x0 - 64 * h - k0, b1 = pos - x0 - 64 * h - k0;
+                        const uint32_t on = there >> (4 * h + k0 / 16);
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
+                        for (int c = 0; c < NR; ++c)
                             if (c < b0 || c > b1 || !(on >> (c / 16) & 1)) r[c] = 0xff800000u;
                     }
+                };
+                if (ok && !idle) {
+                    if constexpr (TERMS > 1) {
+                        load(32);
+#pragma unroll
+                        for (int c = 0; c < NR; c += 2) early = max3(early, r[c], r[c + 1]);
+                    }
+                    load(0);
                 }
 #pragma unroll 1
                 while (true) {
@@ -984,7 +998,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                         F2 part[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
+                        for (int c = 0; c < NR / 2; ++c) {
                             t[c & 3] = max3(t[c & 3], r[2 * c], r[2 * c + 1]);
                             if constexpr (TERMS == 1) {
                                 float x, y;
@@ -995,7 +1009,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                                 w[c] = pack_m((const M *)nullptr, x, y);
                             }
                         }
-                        top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * sc2;
+                        top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), early) * sc2;
                         if constexpr (TERMS == 1) {
                             float a0, a1;
                             f2_get(f2_add(part[0], part[1]), a0, a1);
@@ -1052,22 +1066,23 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                         TMEM_ST32(scol + 64 * h, w);
                     } else {
                         const float ref = m > -INFINITY ? m : 0.f;
-#pragma unroll
-                        for (int c0 = 0; c0 < 32; c0 += 16) {
+#pragma unroll 1
+                        for (int k0 = 0; k0 < 64; k0 += 32) {
+                            if (k0) load(k0);
                             uint32_t w0[16], w1[16], w2[16];
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
-                                float x = ex2(fmaf(__uint_as_float(r[2 * (c0 + c)]), sc2, -ref));
-                                float y = ex2(fmaf(__uint_as_float(r[2 * (c0 + c) + 1]), sc2, -ref));
+                                float x = ex2(fmaf(__uint_as_float(r[2 * c]), sc2, -ref));
+                                float y = ex2(fmaf(__uint_as_float(r[2 * c + 1]), sc2, -ref));
                                 l += x + y;
                                 w0[c] = take_m<M>(x, y);
                                 w1[c] = take_m<M>(x, y);
                                 if constexpr (TERMS > 2) w2[c] = pack_m((const M *)nullptr, x, y);
                             }
                             __syncwarp();
-                            TMEM_ST16(scol + 64 * h + c0, w0);
-                            TMEM_ST16(scol + 64 * h + 32 + c0, w1);
-                            if constexpr (TERMS > 2) TMEM_ST16(scol + 128 + 32 * h + c0, w2);
+                            TMEM_ST16(scol + 64 * h + k0, w0);
+                            TMEM_ST16(scol + 64 * h + k0 + 16, w1);
+                            if constexpr (TERMS > 2) TMEM_ST16(scol + 128 + 32 * h + k0 / 2, w2);
                         }
                     }
                 }
