@@ -80,9 +80,8 @@ struct Types<__half, uint8_t> {
 // Registers a thread. The block starts with 128, all of the SM's; each role's
 // warpgroups then trade them: softmax (two warpgroups), producers, issuer.
 constexpr int REGS = 128;
-template <bool E4>
 struct Regs {
-    static constexpr int PRODUCER = E4 ? 128 : 88, ISSUER = E4 ? 64 : 72, SOFTMAX = E4 ? 160 : 176;
+    static constexpr int PRODUCER = 88, ISSUER = 72, SOFTMAX = 176;
     static_assert(2 * SOFTMAX + PRODUCER + ISSUER <= 4 * REGS, "no more than the block has");
 };
 template <int N>
@@ -161,6 +160,17 @@ __device__ __forceinline__ void tma_3d_at(uint32_t dst, const CUtensorMap *map, 
         "l"((uint64_t)map), "r"(x), "r"(y), "r"(w), "r"(su32(bar))
         : "memory");
 }
+// `bytes` (a multiple of 16) from a 16-byte boundary to another.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, int bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(su32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld16(uint32_t src) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+    return v;
+}
 // Byte of 16-byte piece p (0 to 7) of row r in a panel of 128-byte rows.
 __device__ __forceinline__ uint32_t piece(int r, int p) { return (uint32_t)(128 * r + 16 * (p ^ (r & 7))); }
 
@@ -206,7 +216,7 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
 }
 
 struct Shared {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw[PR_WARPS][2];
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_full[4], pv_half[2], pv_done[2], o_free[2], fin;   // p_full: QT = 2, halves of keys of either tile
     long long share[THREADS / 32 + 2];
@@ -226,8 +236,10 @@ struct Shape {
     int v_items;
     int nv;        // value columns, rounded to 16
     int nslot;
+    int raw;       // bytes of the queries, behind which codes to be converted lie, and then the ring
 };
-template <int QT, int TERMS>
+constexpr int RAW_WARP = 4096, RAW_BYTES = 2 * RAW_WARP * PR_WARPS;
+template <int QT, int TERMS, bool E4>
 __device__ __forceinline__ Shape shape_of(int d, int dv) {
     Shape s;
     s.nqc = (d + 63) / 64;
@@ -236,7 +248,8 @@ __device__ __forceinline__ Shape shape_of(int d, int dv) {
     s.v_keys = dv > 128 ? 64 : 128;
     s.v_items = dv > 128 ? 2 : 1;
     s.nv = (dv + 15) / 16 * 16;
-    s.nslot = min(MAX_SLOTS, (int)((SMEM - 1024 - (size_t)TERMS * QT * s.nqc * 16384) / SLOT));   // 3 at least
+    s.raw = TERMS * QT * s.nqc * 16384;
+    s.nslot = min(MAX_SLOTS, (int)((SMEM - 1024 - s.raw - (E4 ? RAW_BYTES : 0)) / SLOT));   // 3 at least (fp16 over e4m3, d > 128: 2)
     return s;
 }
 
@@ -305,9 +318,11 @@ struct Producer {
         else if (master()) met = met && warp_wait(bar, parity, &sh.abort, a.wait_cycles);
     }
     // all warps' copies are in shared memory
-    __device__ __forceinline__ void announce(uint64_t *bar) {
-        copy_commit();
-        copy_wait<0>();
+    __device__ __forceinline__ void announce(uint64_t *bar, bool copies = !E4) {
+        if (copies) {
+            copy_commit();
+            copy_wait<0>();
+        }
         fence_async_smem();
         if (E4) __syncwarp();
         else sync();
@@ -321,7 +336,7 @@ struct Producer {
         const int tiles = QT == 2 && s.x.nv > 128 ? 2 : 1, pieces = 2 * z.ksteps;   // 16-byte pieces of a row
         if (Q_COPY && mq) {
             const int n = z.nqc * tiles;
-            if (master() && met) {
+            if (master() && (E4 ? ok : met)) {
                 if (lane == 0) mbar_expect_tx(&sh.q_full, 16384 * n);
                 __syncwarp();
                 if (lane < n) {
@@ -384,14 +399,17 @@ struct Producer {
                 }
             }
         }
-        announce(&sh.q_full);
+        announce(&sh.q_full, true);
     }
 
-    // The pages of a tile's eight runs of 16 positions, run i in lanes i, i + 8, ...
-    __device__ __forceinline__ int pages(const PgSegment &s, int j) const {
+    // The table's entries for a tile's eight runs of 16 positions, run i in lanes
+    // i, i + 8, ...; and an entry's page, or -1. They are apart, for an entry is
+    // looked up a tile ahead and would be waited for where it is first compared.
+    __device__ __forceinline__ int entries(const PgSegment &s, int j) const {
         const int p = (s.x.lo / KT + j) * KT + 16 * (lane & 7);
-        return j < s.t1 && p <= s.x.last && p + 15 >= s.x.first ? pg_page(a, s.x.slot, p) : -1;
+        return j < s.t1 && p <= s.x.last && p + 15 >= s.x.first ? a.table[(size_t)s.x.slot * a.width + (p >> a.lpage)] : -1;
     }
+    __device__ __forceinline__ int page_of(int entry) const { return entry >= 0 && entry < a.n_pages ? entry : -1; }
 
     // An item of the tile: keys (128 columns) or values (v_keys rows). 16 rows
     // at a time; a thread has the same row of each 16.
@@ -458,57 +476,95 @@ struct Producer {
         ++sent;
     }
 
-    // e4m3: an item's codes and powers of two in registers, 16 codes of eight
-    // rows a thread (of four rows and both halves of 256 columns), so that the
-    // next item's loads are under way while one is converted.
-    struct Codes {
-        uint4 w[8];
-        uint32_t e[8];
-    };
+    // e4m3. Each warp has a quarter of an item's rows, and brings their codes by
+    // bulk copies into a buffer of its own, an item ahead of the one it converts;
+    // the 128 bytes of exponents a word a lane.
     struct Item {
         bool keys;
         int j, part;
     };
-    __device__ __forceinline__ void fetch(const PgSegment &s, const Item &x, int ids, Codes &r) {
-        const int width = x.keys ? a.d : a.dv, col0 = x.keys ? 128 * x.part : 0, key0 = x.keys ? 0 : z.v_keys * x.part;
-        const int p0 = (s.x.lo / KT + x.j) * KT + key0, halves = !x.keys && z.v_keys == 64 ? 2 : 1;
-        const C *pool = (const C *)(x.keys ? a.k : a.v);
-        const uint8_t *exps = x.keys ? a.ke : a.ve;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int run = halves == 2 ? i >> 1 : i, page = __shfl_sync(0xffffffffu, ids, key0 / 16 + run), p = p0 + 16 * run + r4;
-            const bool in = page >= 0 && p >= s.x.lo && p <= s.x.hi;
-            const uint32_t row = (uint32_t)((((page * a.G) + s.g) << a.lpage) + (p & ((1 << a.lpage) - 1)));
-            const int c = col0 + 16 * l8 + (halves == 2 ? 128 * (i & 1) : 0);
-            r.w[i] = make_uint4(0u, 0u, 0u, 0u);
-            r.e[i] = 0;
-            if (in) r.e[i] = exps[row];
-            if (in && c < width) r.w[i] = *(const uint4 *)(pool + (size_t)row * width + c);
+    struct Bytes {       // of the tile's positions 4 lane .. 4 lane + 3
+        uint32_t exps, in;   // in: a bit each, whether it is attended by some row
+    };
+    uint32_t raw0;       // shared address of this warp's two buffers
+    uint32_t fetched, converted;   // items
+    __device__ __forceinline__ bool halves(const Item &x) const { return QT == 1 && !x.keys && z.v_keys == 64; }
+    __device__ __forceinline__ int rows_of(const Item &x) const { return halves(x) ? 16 : 32; }   // this warp's
+    // Keys of more than 128 values come row by row, all else 16 rows at once.
+    __device__ __forceinline__ bool by_row(const Item &x) const { return QT == 1 && x.keys && a.d > 128; }
+    __device__ __forceinline__ Bytes fetch(const PgSegment &s, const Item &x, int ids) {
+        const int width = x.keys ? a.d : a.dv, key0 = QT == 2 || x.keys ? 0 : z.v_keys * x.part, rowly = by_row(x);
+        const int p0 = (s.x.lo / KT + x.j) * KT, mask = (1 << a.lpage) - 1, col0 = QT == 1 && x.keys ? 128 * x.part : 0;
+        const int n = rowly ? 32 : rows_of(x) / 16, row0 = key0 + rows_of(x) * wid, run = rowly ? lane >> 4 : lane & 1;
+        const int bytes = rowly ? min(128, width - col0) : 16 * width;
+        uint64_t *bar = &sh.raw[wid][fetched & 1];
+        int page = __shfl_sync(0xffffffffu, ids, row0 / 16 + run & 7);
+        const bool on = lane < n && page >= 0;
+        const int count = __popc(__ballot_sync(0xffffffffu, on));
+        if (lane == 0) mbar_expect_tx(bar, count * bytes);
+        __syncwarp();
+        if (on) {
+            const int p = p0 + row0 + (rowly ? lane : 16 * run);
+            const uint32_t row = (uint32_t)(((page * a.G + s.g) << a.lpage) + (p & mask));
+            bulk_load(raw0 + (fetched & 1) * RAW_WARP + lane * (rowly ? 128 : 16 * width),
+                      (const C *)(x.keys ? a.k : a.v) + (size_t)row * width + col0, bytes, bar);
         }
+        __syncwarp();
+        ++fetched;
+        Bytes r = {0u, 0u};
+        page = __shfl_sync(0xffffffffu, ids, lane >> 2);
+        const int p = p0 + 4 * lane;
+        if (page >= 0) {
+            r.exps = *(const uint32_t *)((x.keys ? a.ke : a.ve) + (uint32_t)(((page * a.G + s.g) << a.lpage) + (p & mask)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.in |= (uint32_t)(p + i >= s.x.lo && p + i <= s.x.hi) << i;
+        }
+        return r;
     }
     // Four threads cover the 64 columns of a block, and the 8 of a row write their
     // two pieces in opposite orders, so that no bank is hit twice.
-    __device__ __forceinline__ void convert(const Item &x, const Codes &r) {
-        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles);
+    __device__ __forceinline__ void convert(const Item &x, const Bytes &y) {
+        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles) &&
+             warp_wait(&sh.raw[wid][converted & 1], (converted >> 1) & 1, &sh.abort, a.wait_cycles);
         if (!ok) return;
-        const int width = x.keys ? a.d : a.dv, rows = x.keys ? 128 : z.v_keys, halves = !x.keys && z.v_keys == 64 ? 2 : 1;
-        const int cols = min(halves == 2 ? 256 : 128, (width + 15) / 16 * 16 - (x.keys ? 128 * x.part : 0));
-        const uint32_t dst = ring0 + put.slot * SLOT;
-        const int odd = (l8 >> 2) & 1;
+        const int width = x.keys ? a.d : a.dv, rows = QT == 2 || x.keys ? 128 : z.v_keys, two = halves(x), key0 = QT == 2 || x.keys ? 0 : z.v_keys * x.part;
+        const int cols = min(two ? 256 : 128, (width + 15) / 16 * 16 - (QT == 1 && x.keys ? 128 * x.part : 0));
+        const int odd = (l8 >> 2) & 1, p = 2 * (l8 & 3), block = rows * 128, pitch = by_row(x) ? 128 : width;
+        const int row0 = rows_of(x) * wid, l4 = lane >> 3, from0 = (key0 + row0) / 4;
+        const uint32_t src = raw0 + (converted & 1) * RAW_WARP + l4 * pitch + 16 * l8, dst = ring0 + put.slot * SLOT;
+        const bool all = __all_sync(0xffffffffu, y.in == 15);
+        const uint32_t exps = all ? y.exps : y.exps & ((y.in & 1) * 0xffu | (y.in >> 1 & 1) * 0xff00u | (y.in >> 2 & 1) * 0xff0000u |
+                                                       (y.in >> 3) * 0xff000000u);   // (zero times 2^128 would be NaN)
+#pragma unroll 1
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 w[4];
+            __nv_bfloat162 f[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = 16 * (halves == 2 ? i >> 1 : i) + r4, c = 16 * l8 + (halves == 2 ? 128 * (i & 1) : 0);
-            const uint32_t f2 = r.e[i] * 0x00800080u;   // 2^(byte - 127) twice
-            const __nv_bfloat162 f = *(const __nv_bfloat162 *)&f2;
-            if (c < cols) {
-                const uint32_t at = dst + (c >> 6) * (rows * 128);
-                const int p = (c & 63) >> 3;
-                const uint4 lo = bf16_of_e4m3(make_uint2(r.w[i].x, r.w[i].y), f);
-                const uint4 hi = bf16_of_e4m3(make_uint2(r.w[i].z, r.w[i].w), f);
-                st16(at + piece(row, p + odd), odd ? hi : lo);
-                st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u;
+                const uint32_t e = __shfl_sync(0xffffffffu, exps, from0 + (i >> two)) >> (8 * l4) & 0xff;
+                const uint32_t f2 = e * 0x00800080u;   // 2^(byte - 127) twice
+                f[u] = *(const __nv_bfloat162 *)&f2;
+                w[u] = ld16(src + 4 * pitch * (i >> two) + (two ? 128 * (i & 1) : 0));
+            }
+            if (!all) {   // where no row attends it, memory may hold anything
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (!(__shfl_sync(0xffffffffu, y.in, from0 + ((i0 + u) >> two)) >> l4 & 1))
+                        w[u] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u, row = row0 + 4 * (i >> two) + l4, c = 16 * l8 + (two ? 128 * (i & 1) : 0);
+                if (c < cols) {
+                    const uint32_t at = dst + (c >> 6) * block;
+                    const uint4 lo = bf16_of_e4m3(make_uint2(w[u].x, w[u].y), f[u]), hi = bf16_of_e4m3(make_uint2(w[u].z, w[u].w), f[u]);
+                    st16(at + piece(row, p + odd), odd ? hi : lo);
+                    st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
+                }
             }
         }
+        ++converted;
         announce(&sh.full[put.slot]);
         put.next(z.nslot);
     }
@@ -518,7 +574,7 @@ struct Producer {
             // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
             Item x = {true, s.t0, 0};
             auto next = [&](Item &i) -> bool {   // false after the last
-                if (++i.part < (i.keys ? z.k_items : z.v_items)) return true;
+                if (QT == 1 && ++i.part < (i.keys ? z.k_items : z.v_items)) return true;
                 i.part = 0;
                 if (QT == 2) {
                     if (!i.keys) ++i.j;
@@ -535,32 +591,38 @@ struct Producer {
                 return i.j < s.t1;
             };
             // pages of tiles t and on, t the last one whose values are to come
-            int tile = s.t0, ids = pages(s, tile), ids1 = pages(s, tile + 1), ids2 = pages(s, tile + 2);
+            int tile = s.t0, ids = page_of(entries(s, tile)), ids1 = page_of(entries(s, tile + 1)), next2 = entries(s, tile + 2);
             auto of = [&](int j) -> int {
                 while (tile + 1 < j || (tile < j && !x.keys)) {
                     ++tile;
                     ids = ids1;
-                    ids1 = ids2;
-                    ids2 = pages(s, tile + 2);   // looked up a tile ahead
+                    ids1 = page_of(next2);
+                    next2 = entries(s, tile + 2);
                 }
                 return j == tile ? ids : ids1;
             };
-            Codes now;
-            fetch(s, x, of(x.j), now);
+            Bytes now = fetch(s, x, of(x.j));
             ok = warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
-            if (!ok) return;
+            if (!ok) break;
             qp ^= 1;
             queries(s);
 #pragma unroll 1
             for (bool more = true; ok && more;) {
                 const Item was = x;
+                Bytes then = {0u, 0u};
                 more = next(x);
-                Codes then;
-                if (more) fetch(s, x, of(x.j), then);
+                if (more) then = fetch(s, x, of(x.j));
                 convert(was, now);
                 now = then;
             }
         }
+        if (ok) return;
+        // after a wait that ran out: what is still being copied lands before the block ends
+        if (lane == 0) {
+            if (q_sent) mbar_drain(&sh.q_full, qp);
+            for (; converted != fetched; ++converted) mbar_drain(&sh.raw[wid][converted & 1], (converted >> 1) & 1);
+        }
+        __syncwarp();
     }
 
     __device__ __forceinline__ void run(const PgTable &tab, int units, PgShare share) {
@@ -585,7 +647,7 @@ struct Producer {
             auto values = [&](int j, int id, bool bx) {
                 for (int p = 0; ok && p < z.v_items; ++p) item<false>(s, j, id, p, bx);
             };
-            int ids = pages(s, s.t0), ids1 = pages(s, s.t0 + 1);
+            int ids = page_of(entries(s, s.t0)), ids1 = page_of(entries(s, s.t0 + 1));
             bool bx = boxes(s.t0, ids), bx1;
             keys(s.t0, ids, bx);   // before the queries, whose place the segment before may still hold
             wait_for(&sh.q_free, qp);
@@ -593,13 +655,13 @@ struct Producer {
             qp ^= 1;
             queries(s);
             for (int j = s.t0; ok && j < s.t1; ++j) {
-                const int ids2 = pages(s, j + 2);
+                const int next2 = entries(s, j + 2);
                 bx1 = boxes(j + 1, ids1);
                 if (QT == 1 && j + 1 < s.t1) keys(j + 1, ids1, bx1);
                 values(j, ids, bx);
                 if (QT == 2 && j + 1 < s.t1) keys(j + 1, ids1, bx1);
                 ids = ids1;
-                ids1 = ids2;
+                ids1 = page_of(next2);
                 bx = bx1;
             }
         }
@@ -1175,15 +1237,16 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     constexpr int TERMS = Types<T, C>::TERMS;
     extern __shared__ unsigned char smraw[];
     __shared__ Shared sh;
-    const Shape z = shape_of<QT, TERMS>(a.d, a.dv);
+    const Shape z = shape_of<QT, TERMS, sizeof(C) == 1>(a.d, a.dv);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t q0 = (su32(smraw) + 1023) & ~1023u, ring0 = q0 + (uint32_t)(TERMS * QT * z.nqc) * 16384;
+    const uint32_t q0 = (su32(smraw) + 1023) & ~1023u, ring0 = q0 + z.raw + (sizeof(C) == 1 ? RAW_BYTES : 0);
     if (tid == 0) {
         for (int i = 0; i < MAX_SLOTS; ++i) {
             mbar_init(&sh.full[i], sizeof(C) == 1 ? PR_WARPS : 1);
             mbar_init(&sh.empty[i], QT);   // QT issuers
         }
-        mbar_init(&sh.q_full, sizeof(C) == 1 ? PR_WARPS : 1);
+        mbar_init(&sh.q_full, sizeof(C) == 1 && !qrows ? PR_WARPS : 1);
+        for (int i = 0; i < 2 * PR_WARPS; ++i) mbar_init(&sh.raw[i >> 1][i & 1], 1);
         mbar_init(&sh.q_free, QT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -1205,7 +1268,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tslot;
-    using R = Regs<sizeof(C) == 1>;
+    using R = Regs;
     if (warp < SM_WARPS) {
         regs_more<R::SOFTMAX>();
         softmax<T, C, QT>(a, sh, z, tmem, tab, units, share, vecs);
@@ -1213,7 +1276,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
         regs_less<R::PRODUCER>();
         const int wid = warp - SM_WARPS;
         Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * wid + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
-                                wid, {0, 0}, true, true, 0, 1, false};
+                                wid, {0, 0}, true, true, 0, 1, false, q0 + z.raw + 2 * RAW_WARP * wid, 0, 0};
         p.run(tab, units, share);
     } else {
         regs_less<R::ISSUER>();
@@ -1269,14 +1332,15 @@ cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vec
         const uint32_t page = 1u << a.lpage, most = a.dv > 128 ? 64 : 128;
         if (!pool_map<C>(&mk, a.k, a.d, rows, page < 128 ? page : 128) || !pool_map<C>(&mv, a.v, a.dv, rows, page < most ? page : most))
             return cudaErrorInvalidValue;
-        if (sizeof(T) == 2 && 128 % a.hpg == 0) {
+    }
+    if constexpr (sizeof(T) == 2 && Types<T, C>::TERMS == 1)
+        if (128 % a.hpg == 0) {
             qrows = 128 / a.hpg;
             const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.G * a.hpg, (cuuint64_t)vectors / a.hpg};
             const cuuint64_t strides[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.qs * 2};
             const cuuint32_t box[3] = {64, (cuuint32_t)a.hpg, (cuuint32_t)qrows};
             if (!encode<T>(&mq, 3, a.q, dims, strides, box)) return cudaErrorInvalidValue;
         }
-    }
     k<<<BLOCKS, THREADS, SMEM, st>>>(a, tab, mq, mk, mv, qrows, tab.total, vecs);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, vecs, st) : e;
