@@ -30,7 +30,7 @@ constexpr int RV = PG_ROWS_V;         // query vectors of a unit
 constexpr int TILE = 16 * RW;         // keys of a tile
 constexpr int PER_SM = 2, BLOCKS = 152 * PER_SM;
 struct Plan {
-    static constexpr int V = RV, K = TILE, START = 2, LEAST = 4;
+    static constexpr int V = RV, K = TILE, START = 5, LEAST = 2;
 };
 
 // Rows of type T over a cache of type C: the MMA's type M, and the terms that q

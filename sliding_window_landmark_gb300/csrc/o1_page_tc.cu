@@ -48,7 +48,7 @@ constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside i
 
 template <int QT>
 struct Plan {
-    static constexpr int V = 128 * QT, K = KT, START = 2, LEAST = 4;
+    static constexpr int V = 128 * QT, K = KT, START = 3, LEAST = 1;
 };
 
 template <typename T, typename C>
@@ -216,11 +216,14 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
 }
 
 struct Shared {
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw[PR_WARPS][2];
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    uint64_t raw_full[2], raw_empty[2];   // e4m3: items of codes to be converted
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_full[4], pv_half[2], pv_done[2], o_free[2], fin;   // p_full: QT = 2, halves of keys of either tile
     long long share[THREADS / 32 + 2];
     uint64_t turn[2][4];   // QT = 2: the two tiles' warps of a scheduler form weights in turn
+    alignas(16) uint8_t raw_exps[2][KT];  // their exponents
+    uint32_t raw_there[2];                // their runs of 16 positions that have a page, a bit each
     uint32_t tslot;
     int abort;
     float half[2][128];   // QT = 1: the warpgroups' maxima, then sums
@@ -238,7 +241,7 @@ struct Shape {
     int nslot;
     int raw;       // bytes of the queries, behind which codes to be converted lie, and then the ring
 };
-constexpr int RAW_WARP = 4096, RAW_BYTES = 2 * RAW_WARP * PR_WARPS;
+constexpr int RAW_ITEM = 16384, RAW_BYTES = 2 * RAW_ITEM;
 template <int QT, int TERMS, bool E4>
 __device__ __forceinline__ Shape shape_of(int d, int dv) {
     Shape s;
@@ -476,152 +479,152 @@ struct Producer {
         ++sent;
     }
 
-    // e4m3. Each warp has a quarter of an item's rows, and brings their codes by
-    // bulk copies into a buffer of its own, an item ahead of the one it converts;
-    // the 128 bytes of exponents a word a lane.
+    // e4m3. A warp of its own, the loader, brings an item's codes and exponents by
+    // bulk copies, 16 rows a lane and two items ahead; each of the four producer
+    // warps converts a quarter of its rows.
     struct Item {
         bool keys;
         int j, part;
     };
-    struct Bytes {       // of the tile's positions 4 lane .. 4 lane + 3
-        uint32_t exps, in;   // in: a bit each, whether it is attended by some row
-    };
-    uint32_t raw0;       // shared address of this warp's two buffers
-    uint32_t fetched, converted;   // items
+    uint32_t raw0;   // shared address of the two buffers of codes
     __device__ __forceinline__ bool halves(const Item &x) const { return QT == 1 && !x.keys && z.v_keys == 64; }
-    __device__ __forceinline__ int rows_of(const Item &x) const { return halves(x) ? 16 : 32; }   // this warp's
-    // Keys of more than 128 values come row by row, all else 16 rows at once.
+    // Keys of more than 128 values come row by row.
     __device__ __forceinline__ bool by_row(const Item &x) const { return QT == 1 && x.keys && a.d > 128; }
-    __device__ __forceinline__ Bytes fetch(const PgSegment &s, const Item &x, int ids) {
-        const int width = x.keys ? a.d : a.dv, key0 = QT == 2 || x.keys ? 0 : z.v_keys * x.part, rowly = by_row(x);
-        const int p0 = (s.x.lo / KT + x.j) * KT, mask = (1 << a.lpage) - 1, col0 = QT == 1 && x.keys ? 128 * x.part : 0;
-        const int n = rowly ? 32 : rows_of(x) / 16, row0 = key0 + rows_of(x) * wid, run = rowly ? lane >> 4 : lane & 1;
-        const int bytes = rowly ? min(128, width - col0) : 16 * width;
-        uint64_t *bar = &sh.raw[wid][fetched & 1];
-        int page = __shfl_sync(0xffffffffu, ids, row0 / 16 + run & 7);
-        const bool on = lane < n && page >= 0;
-        const int count = __popc(__ballot_sync(0xffffffffu, on));
-        if (lane == 0) mbar_expect_tx(bar, count * bytes);
-        __syncwarp();
-        if (on) {
-            const int p = p0 + row0 + (rowly ? lane : 16 * run);
-            const uint32_t row = (uint32_t)(((page * a.G + s.g) << a.lpage) + (p & mask));
-            bulk_load(raw0 + (fetched & 1) * RAW_WARP + lane * (rowly ? 128 : 16 * width),
-                      (const C *)(x.keys ? a.k : a.v) + (size_t)row * width + col0, bytes, bar);
+    __device__ __forceinline__ int key0_of(const Item &x) const { return QT == 2 || x.keys ? 0 : z.v_keys * x.part; }
+    // in the MMA issuer's order: QT = 1 runs a tile's scores ahead; false after the last
+    __device__ __forceinline__ bool next(const PgSegment &s, Item &i) const {
+        if (QT == 1 && ++i.part < (i.keys ? z.k_items : z.v_items)) return true;
+        i.part = 0;
+        if (QT == 2) {
+            if (!i.keys) ++i.j;
+            i.keys = !i.keys;
+        } else if (i.keys) {
+            if (i.j == s.t0 && i.j + 1 < s.t1) ++i.j;   // the second tile's keys
+            else if (i.j == s.t0) i.keys = false;
+            else i.keys = false, --i.j;
+        } else {
+            i.j += 2;
+            i.keys = i.j < s.t1;
+            if (!i.keys) --i.j;                           // no keys are left: the next values
         }
-        __syncwarp();
-        ++fetched;
-        Bytes r = {0u, 0u};
-        page = __shfl_sync(0xffffffffu, ids, lane >> 2);
-        const int p = p0 + 4 * lane;
-        if (page >= 0) {
-            r.exps = *(const uint32_t *)((x.keys ? a.ke : a.ve) + (uint32_t)(((page * a.G + s.g) << a.lpage) + (p & mask)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r.in |= (uint32_t)(p + i >= s.x.lo && p + i <= s.x.hi) << i;
-        }
-        return r;
+        return i.j < s.t1;
     }
-    // Four threads cover the 64 columns of a block, and the 8 of a row write their
-    // two pieces in opposite orders, so that no bank is hit twice.
-    __device__ __forceinline__ void convert(const Item &x, const Bytes &y) {
-        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles) &&
-             warp_wait(&sh.raw[wid][converted & 1], (converted >> 1) & 1, &sh.abort, a.wait_cycles);
-        if (!ok) return;
-        const int width = x.keys ? a.d : a.dv, rows = QT == 2 || x.keys ? 128 : z.v_keys, two = halves(x), key0 = QT == 2 || x.keys ? 0 : z.v_keys * x.part;
-        const int cols = min(two ? 256 : 128, (width + 15) / 16 * 16 - (QT == 1 && x.keys ? 128 * x.part : 0));
-        const int odd = (l8 >> 2) & 1, p = 2 * (l8 & 3), block = rows * 128, pitch = by_row(x) ? 128 : width;
-        const int row0 = rows_of(x) * wid, l4 = lane >> 3, from0 = (key0 + row0) / 4;
-        const uint32_t src = raw0 + (converted & 1) * RAW_WARP + l4 * pitch + 16 * l8, dst = ring0 + put.slot * SLOT;
-        const bool all = __all_sync(0xffffffffu, y.in == 15);
-        const uint32_t exps = all ? y.exps : y.exps & ((y.in & 1) * 0xffu | (y.in >> 1 & 1) * 0xff00u | (y.in >> 2 & 1) * 0xff0000u |
-                                                       (y.in >> 3) * 0xff000000u);   // (zero times 2^128 would be NaN)
-#pragma unroll 1
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-            uint4 w[4];
-            __nv_bfloat162 f[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u;
-                const uint32_t e = __shfl_sync(0xffffffffu, exps, from0 + (i >> two)) >> (8 * l4) & 0xff;
-                const uint32_t f2 = e * 0x00800080u;   // 2^(byte - 127) twice
-                f[u] = *(const __nv_bfloat162 *)&f2;
-                w[u] = ld16(src + 4 * pitch * (i >> two) + (two ? 128 * (i & 1) : 0));
-            }
-            if (!all) {   // where no row attends it, memory may hold anything
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (!(__shfl_sync(0xffffffffu, y.in, from0 + ((i0 + u) >> two)) >> l4 & 1))
-                        w[u] = make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u, row = row0 + 4 * (i >> two) + l4, c = 16 * l8 + (two ? 128 * (i & 1) : 0);
-                if (c < cols) {
-                    const uint32_t at = dst + (c >> 6) * block;
-                    const uint4 lo = bf16_of_e4m3(make_uint2(w[u].x, w[u].y), f[u]), hi = bf16_of_e4m3(make_uint2(w[u].z, w[u].w), f[u]);
-                    st16(at + piece(row, p + odd), odd ? hi : lo);
-                    st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
-                }
-            }
-        }
-        ++converted;
-        announce(&sh.full[put.slot]);
-        put.next(z.nslot);
-    }
-    __device__ __forceinline__ void run_codes(const PgTable &tab, int units, PgShare share) {
+    __device__ __forceinline__ void load_codes(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
+        uint32_t n = 0;   // items
         while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
-            // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
-            Item x = {true, s.t0, 0};
-            auto next = [&](Item &i) -> bool {   // false after the last
-                if (QT == 1 && ++i.part < (i.keys ? z.k_items : z.v_items)) return true;
-                i.part = 0;
-                if (QT == 2) {
-                    if (!i.keys) ++i.j;
-                    i.keys = !i.keys;
-                } else if (i.keys) {
-                    if (i.j == s.t0 && i.j + 1 < s.t1) ++i.j;   // the second tile's keys
-                    else if (i.j == s.t0) i.keys = false;
-                    else i.keys = false, --i.j;
-                } else {
-                    i.j += 2;
-                    i.keys = i.j < s.t1;
-                    if (!i.keys) --i.j;                           // no keys are left: the next values
-                }
-                return i.j < s.t1;
-            };
             // pages of tiles t and on, t the last one whose values are to come
             int tile = s.t0, ids = page_of(entries(s, tile)), ids1 = page_of(entries(s, tile + 1)), next2 = entries(s, tile + 2);
-            auto of = [&](int j) -> int {
-                while (tile + 1 < j || (tile < j && !x.keys)) {
+            Item x = {true, s.t0, 0};
+            do {
+                while (tile + 1 < x.j || (tile < x.j && !x.keys)) {
                     ++tile;
                     ids = ids1;
                     ids1 = page_of(next2);
                     next2 = entries(s, tile + 2);
                 }
-                return j == tile ? ids : ids1;
-            };
-            Bytes now = fetch(s, x, of(x.j));
-            ok = warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
-            if (!ok) break;
-            qp ^= 1;
-            queries(s);
-#pragma unroll 1
-            for (bool more = true; ok && more;) {
-                const Item was = x;
-                Bytes then = {0u, 0u};
-                more = next(x);
-                if (more) then = fetch(s, x, of(x.j));
-                convert(was, now);
-                now = then;
-            }
+                const int b = n & 1;
+                ok = warp_wait(&sh.raw_empty[b], ((n >> 1) & 1) ^ 1, &sh.abort, a.wait_cycles);
+                if (!ok) break;
+                const bool rowly = by_row(x);
+                const int width = x.keys ? a.d : a.dv, key0 = key0_of(x), runs = halves(x) ? 4 : 8, mask = (1 << a.lpage) - 1;
+                const int p0 = (s.x.lo / KT + x.j) * KT, col0 = QT == 1 && x.keys ? 128 * x.part : 0;
+                const int bytes = rowly ? min(128, width - col0) : width, page = x.j == tile ? ids : ids1;   // bytes of a row
+                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) >> (key0 / 16) & ((1u << runs) - 1);
+                if (lane == 0) {
+                    sh.raw_there[b] = there;
+                    mbar_expect_tx(&sh.raw_full[b], __popc(there) * 16 * (bytes + 1));
+                }
+                __syncwarp();
+                const C *pool = (const C *)(x.keys ? a.k : a.v);
+                const uint32_t dst = raw0 + b * RAW_ITEM;
+                // lanes 0 to 7: 16 rows of codes each; 8 to 15: of exponents
+                const int run = lane & 7, id = __shfl_sync(0xffffffffu, page, key0 / 16 + run & 7);
+                const uint32_t row = (uint32_t)(((id * a.G + s.g) << a.lpage) + (p0 + key0 + 16 * run & mask));
+                if (lane < 16 && there >> run & 1) {
+                    if (lane >= 8) bulk_load(su32(sh.raw_exps[b]) + 16 * run, (x.keys ? a.ke : a.ve) + row, 16, &sh.raw_full[b]);
+                    else if (!rowly) bulk_load(dst + 16 * run * width, pool + (size_t)row * width, 16 * width, &sh.raw_full[b]);
+                }
+                __syncwarp();
+                if (rowly)
+                    for (int i = 0; i < 8; i += 2) {
+                        const int of = i + (lane >> 4);
+                        const uint32_t r = __shfl_sync(0xffffffffu, row, of) + (lane & 15);
+                        if (there >> of & 1)
+                            bulk_load(dst + 128 * (16 * of + (lane & 15)), pool + (size_t)r * width + col0, bytes, &sh.raw_full[b]);
+                        __syncwarp();
+                    }
+                ++n;
+            } while (next(s, x));
         }
         if (ok) return;
         // after a wait that ran out: what is still being copied lands before the block ends
-        if (lane == 0) {
-            if (q_sent) mbar_drain(&sh.q_full, qp);
-            for (; converted != fetched; ++converted) mbar_drain(&sh.raw[wid][converted & 1], (converted >> 1) & 1);
+        if (lane == 0)
+            for (uint32_t i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_drain(&sh.raw_full[i & 1], (i >> 1) & 1);
+        __syncwarp();
+    }
+    // Four threads cover the 64 columns of a block, and the 8 of a row write their
+    // two pieces in opposite orders, so that no bank is hit twice.
+    __device__ __forceinline__ void convert(const PgSegment &s, const Item &x, uint32_t n) {
+        const int b = n & 1;
+        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles) &&
+             warp_wait(&sh.raw_full[b], (n >> 1) & 1, &sh.abort, a.wait_cycles);
+        if (!ok) return;
+        const bool two = halves(x);
+        const int width = x.keys ? a.d : a.dv, rows = two ? 64 : 128, key0 = key0_of(x), pitch = by_row(x) ? 128 : width;
+        const int cols = min(two ? 256 : 128, (width + 15) / 16 * 16 - (QT == 1 && x.keys ? 128 * x.part : 0));
+        const int odd = (l8 >> 2) & 1, p = 2 * (l8 & 3), row0 = (two ? 16 : 32) * wid + (lane >> 3);
+        const int from = (s.x.lo / KT + x.j) * KT + key0;   // position of row 0
+        const uint32_t src = raw0 + b * RAW_ITEM + row0 * pitch + 16 * l8, dst = ring0 + put.slot * SLOT, there = sh.raw_there[b];
+        const bool all = there == (two ? 15 : 255) && from >= s.x.lo && from + rows - 1 <= s.x.hi;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 w[4];
+            uint32_t f[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u, row = row0 + 4 * (i >> two);
+                f[u] = sh.raw_exps[b][row];
+                w[u] = ld16(src + 4 * pitch * (i >> two) + (two ? 128 * (i & 1) : 0));
+            }
+            if (!all) {   // where no row attends it, memory may hold anything
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int row = row0 + 4 * ((i0 + u) >> two);
+                    if (!(there >> (row >> 4) & 1) || from + row < s.x.lo || from + row > s.x.hi) w[u] = make_uint4(0u, 0u, 0u, 0u), f[u] = 0;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u, row = row0 + 4 * (i >> two), c = 16 * l8 + (two ? 128 * (i & 1) : 0);
+                if (c < cols) {
+                    const uint32_t f2 = f[u] * 0x00800080u, at = dst + (c >> 6) * (rows * 128);   // 2^(byte - 127) twice
+                    const __nv_bfloat162 fb = *(const __nv_bfloat162 *)&f2;
+                    const uint4 lo = bf16_of_e4m3(make_uint2(w[u].x, w[u].y), fb), hi = bf16_of_e4m3(make_uint2(w[u].z, w[u].w), fb);
+                    st16(at + piece(row, p + odd), odd ? hi : lo);
+                    st16(at + piece(row, p + 1 - odd), odd ? lo : hi);
+                }
+            }
         }
+        announce(&sh.full[put.slot]);
+        if (lane == 0) mbar_arrive(&sh.raw_empty[b]);
+        put.next(z.nslot);
+    }
+    __device__ __forceinline__ void run_codes(const PgTable &tab, int units, PgShare share) {
+        PgSegment s;
+        uint32_t n = 0;   // items
+        while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
+            Item x = {true, s.t0, 0};
+            convert(s, x, n++);   // before the queries, whose place the segment before may still hold
+            ok = ok && warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
+            if (!ok) break;
+            qp ^= 1;
+            queries(s);
+            while (ok && next(s, x)) convert(s, x, n++);
+        }
+        if (ok) return;
+        // after a wait that ran out: what is still being copied lands before the block ends
+        if (lane == 0 && q_sent) mbar_drain(&sh.q_full, qp);
         __syncwarp();
     }
 
@@ -1246,7 +1249,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
             mbar_init(&sh.empty[i], QT);   // QT issuers
         }
         mbar_init(&sh.q_full, sizeof(C) == 1 && !qrows ? PR_WARPS : 1);
-        for (int i = 0; i < 2 * PR_WARPS; ++i) mbar_init(&sh.raw[i >> 1][i & 1], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], PR_WARPS);
         mbar_init(&sh.q_free, QT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
@@ -1272,19 +1275,22 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     if (warp < SM_WARPS) {
         regs_more<R::SOFTMAX>();
         softmax<T, C, QT>(a, sh, z, tmem, tab, units, share, vecs);
-    } else if (warp < SM_WARPS + PR_WARPS) {
-        regs_less<R::PRODUCER>();
-        const int wid = warp - SM_WARPS;
-        Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * wid + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
-                                wid, {0, 0}, true, true, 0, 1, false, q0 + z.raw + 2 * RAW_WARP * wid, 0, 0};
-        p.run(tab, units, share);
     } else {
-        regs_less<R::ISSUER>();
-        const int w = warp - SM_WARPS - PR_WARPS;
-        if constexpr (QT == 2) {
-            if (w < 2) issuer_of<T, C>(w, a, sh, z, q0, ring0, tmem, tab, units, share);
+        const int w = warp - SM_WARPS;   // the producers', then the issuers'
+        Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * w + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
+                                w, {0, 0}, true, true, 0, 1, false, q0 + z.raw};
+        if (w < PR_WARPS) {
+            regs_less<R::PRODUCER>();
+            p.run(tab, units, share);
         } else {
-            if (w == 0) issuer<T, C>(a, sh, z, q0, ring0, tmem, tab, units, share);
+            regs_less<R::ISSUER>();
+            const int i = w - PR_WARPS;
+            if (i < QT) {
+                if constexpr (QT == 2) issuer_of<T, C>(i, a, sh, z, q0, ring0, tmem, tab, units, share);
+                else issuer<T, C>(a, sh, z, q0, ring0, tmem, tab, units, share);
+            } else if (sizeof(C) == 1 && i == 2) {
+                p.load_codes(tab, units, share);
+            }
         }
     }
     tc_before();
