@@ -321,11 +321,9 @@ struct Producer {
         else if (master()) met = met && warp_wait(bar, parity, &sh.abort, a.wait_cycles);
     }
     // all warps' copies are in shared memory
-    __device__ __forceinline__ void announce(uint64_t *bar, bool copies = !E4) {
-        if (copies) {
-            copy_commit();
-            copy_wait<0>();
-        }
+    __device__ __forceinline__ void announce(uint64_t *bar) {
+        copy_commit();
+        copy_wait<0>();
         fence_async_smem();
         if (E4) __syncwarp();
         else sync();
@@ -402,7 +400,7 @@ struct Producer {
                 }
             }
         }
-        announce(&sh.q_full, true);
+        announce(&sh.q_full);
     }
 
     // The table's entries for a tile's eight runs of 16 positions, run i in lanes
@@ -479,18 +477,17 @@ struct Producer {
         ++sent;
     }
 
-    // e4m3. A warp of its own, the loader, brings an item's codes and exponents by
-    // bulk copies, 16 rows a lane and two items ahead; each of the four producer
-    // warps converts a quarter of its rows.
+    // e4m3. A warp of its own, the loader, brings codes and exponents by bulk
+    // copies, 16 rows a lane and two items ahead; each of the four producer warps
+    // converts a quarter of an item's rows. An item of codes is 128 rows of up to
+    // 128 values, or 64 of up to 256: two of such keys fill two slots together.
     struct Item {
         bool keys;
         int j, part;
     };
     uint32_t raw0;   // shared address of the two buffers of codes
-    __device__ __forceinline__ bool halves(const Item &x) const { return QT == 1 && !x.keys && z.v_keys == 64; }
-    // Keys of more than 128 values come row by row.
-    __device__ __forceinline__ bool by_row(const Item &x) const { return QT == 1 && x.keys && a.d > 128; }
-    __device__ __forceinline__ int key0_of(const Item &x) const { return QT == 2 || x.keys ? 0 : z.v_keys * x.part; }
+    __device__ __forceinline__ bool halves(const Item &x) const { return QT == 1 && (x.keys ? a.d : a.dv) > 128; }
+    __device__ __forceinline__ int key0_of(const Item &x) const { return QT == 2 ? 0 : 64 * x.part; }
     // in the MMA issuer's order: QT = 1 runs a tile's scores ahead; false after the last
     __device__ __forceinline__ bool next(const PgSegment &s, Item &i) const {
         if (QT == 1 && ++i.part < (i.keys ? z.k_items : z.v_items)) return true;
@@ -526,14 +523,12 @@ struct Producer {
                 const int b = n & 1;
                 ok = warp_wait(&sh.raw_empty[b], ((n >> 1) & 1) ^ 1, &sh.abort, a.wait_cycles);
                 if (!ok) break;
-                const bool rowly = by_row(x);
                 const int width = x.keys ? a.d : a.dv, key0 = key0_of(x), runs = halves(x) ? 4 : 8, mask = (1 << a.lpage) - 1;
-                const int p0 = (s.x.lo / KT + x.j) * KT, col0 = QT == 1 && x.keys ? 128 * x.part : 0;
-                const int bytes = rowly ? min(128, width - col0) : width, page = x.j == tile ? ids : ids1;   // bytes of a row
+                const int p0 = (s.x.lo / KT + x.j) * KT, page = x.j == tile ? ids : ids1;
                 const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) >> (key0 / 16) & ((1u << runs) - 1);
                 if (lane == 0) {
                     sh.raw_there[b] = there;
-                    mbar_expect_tx(&sh.raw_full[b], __popc(there) * 16 * (bytes + 1));
+                    mbar_expect_tx(&sh.raw_full[b], __popc(there) * 16 * (width + 1));
                 }
                 __syncwarp();
                 const C *pool = (const C *)(x.keys ? a.k : a.v);
@@ -542,18 +537,10 @@ struct Producer {
                 const int run = lane & 7, id = __shfl_sync(0xffffffffu, page, key0 / 16 + run & 7);
                 const uint32_t row = (uint32_t)(((id * a.G + s.g) << a.lpage) + (p0 + key0 + 16 * run & mask));
                 if (lane < 16 && there >> run & 1) {
-                    if (lane >= 8) bulk_load(su32(sh.raw_exps[b]) + 16 * run, (x.keys ? a.ke : a.ve) + row, 16, &sh.raw_full[b]);
-                    else if (!rowly) bulk_load(dst + 16 * run * width, pool + (size_t)row * width, 16 * width, &sh.raw_full[b]);
+                    if (lane < 8) bulk_load(dst + 16 * run * width, pool + (size_t)row * width, 16 * width, &sh.raw_full[b]);
+                    else bulk_load(su32(sh.raw_exps[b]) + 16 * run, (x.keys ? a.ke : a.ve) + row, 16, &sh.raw_full[b]);
                 }
                 __syncwarp();
-                if (rowly)
-                    for (int i = 0; i < 8; i += 2) {
-                        const int of = i + (lane >> 4);
-                        const uint32_t r = __shfl_sync(0xffffffffu, row, of) + (lane & 15);
-                        if (there >> of & 1)
-                            bulk_load(dst + 128 * (16 * of + (lane & 15)), pool + (size_t)r * width + col0, bytes, &sh.raw_full[b]);
-                        __syncwarp();
-                    }
                 ++n;
             } while (next(s, x));
         }
@@ -567,15 +554,20 @@ struct Producer {
     // two pieces in opposite orders, so that no bank is hit twice.
     __device__ __forceinline__ void convert(const PgSegment &s, const Item &x, uint32_t n) {
         const int b = n & 1;
-        ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles) &&
-             warp_wait(&sh.raw_full[b], (n >> 1) & 1, &sh.abort, a.wait_cycles);
+        const bool two = halves(x), pair = two && x.keys, open = !pair || x.part == 0, shut = !pair || x.part == 1;
+        Ring second = put;   // of a pair of slots
+        second.next(z.nslot);
+        if (open) ok = ok && warp_wait(&sh.empty[put.slot], put.phase ^ 1, &sh.abort, a.wait_cycles);
+        if (open && pair) ok = ok && warp_wait(&sh.empty[second.slot], second.phase ^ 1, &sh.abort, a.wait_cycles);
+        ok = ok && warp_wait(&sh.raw_full[b], (n >> 1) & 1, &sh.abort, a.wait_cycles);
         if (!ok) return;
-        const bool two = halves(x);
-        const int width = x.keys ? a.d : a.dv, rows = two ? 64 : 128, key0 = key0_of(x), pitch = by_row(x) ? 128 : width;
-        const int cols = min(two ? 256 : 128, (width + 15) / 16 * 16 - (QT == 1 && x.keys ? 128 * x.part : 0));
+        const int width = x.keys ? a.d : a.dv, rows = two ? 64 : 128, key0 = key0_of(x), cols = (width + 15) / 16 * 16;
         const int odd = (l8 >> 2) & 1, p = 2 * (l8 & 3), row0 = (two ? 16 : 32) * wid + (lane >> 3);
         const int from = (s.x.lo / KT + x.j) * KT + key0;   // position of row 0
-        const uint32_t src = raw0 + b * RAW_ITEM + row0 * pitch + 16 * l8, dst = ring0 + put.slot * SLOT, there = sh.raw_there[b];
+        const uint32_t src = raw0 + b * RAW_ITEM + row0 * width + 16 * l8, there = sh.raw_there[b];
+        const uint32_t dst = ring0 + put.slot * SLOT, block = (pair ? 128 : rows) * 128;
+        // columns of 128 and on: the same slot's next blocks, or a pair's second slot
+        const uint32_t dst1 = pair ? ring0 + second.slot * SLOT : dst + 2 * block;
         const bool all = there == (two ? 15 : 255) && from >= s.x.lo && from + rows - 1 <= s.x.hi;
 #pragma unroll 1
         for (int i0 = 0; i0 < 8; i0 += 4) {
@@ -585,7 +577,7 @@ struct Producer {
             for (int u = 0; u < 4; ++u) {
                 const int i = i0 + u, row = row0 + 4 * (i >> two);
                 f[u] = sh.raw_exps[b][row];
-                w[u] = ld16(src + 4 * pitch * (i >> two) + (two ? 128 * (i & 1) : 0));
+                w[u] = ld16(src + 4 * width * (i >> two) + (two ? 128 * (i & 1) : 0));
             }
             if (!all) {   // where no row attends it, memory may hold anything
 #pragma unroll
@@ -598,7 +590,8 @@ struct Producer {
             for (int u = 0; u < 4; ++u) {
                 const int i = i0 + u, row = row0 + 4 * (i >> two), c = 16 * l8 + (two ? 128 * (i & 1) : 0);
                 if (c < cols) {
-                    const uint32_t f2 = f[u] * 0x00800080u, at = dst + (c >> 6) * (rows * 128);   // 2^(byte - 127) twice
+                    const uint32_t f2 = f[u] * 0x00800080u;   // 2^(byte - 127) twice
+                    const uint32_t at = (c >= 128 ? dst1 : dst) + (c >> 6 & 1) * block + (pair ? 64 * 128 * x.part : 0);
                     const __nv_bfloat162 fb = *(const __nv_bfloat162 *)&f2;
                     const uint4 lo = bf16_of_e4m3(make_uint2(w[u].x, w[u].y), fb), hi = bf16_of_e4m3(make_uint2(w[u].z, w[u].w), fb);
                     st16(at + piece(row, p + odd), odd ? hi : lo);
@@ -606,9 +599,16 @@ struct Producer {
                 }
             }
         }
-        announce(&sh.full[put.slot]);
-        if (lane == 0) mbar_arrive(&sh.raw_empty[b]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sh.raw_empty[b]);
+            if (shut) mbar_arrive(&sh.full[put.slot]);
+            if (shut && pair) mbar_arrive(&sh.full[second.slot]);
+        }
+        if (!shut) return;
         put.next(z.nslot);
+        if (pair) put.next(z.nslot);
     }
     __device__ __forceinline__ void run_codes(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
