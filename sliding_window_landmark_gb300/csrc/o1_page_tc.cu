@@ -316,13 +316,13 @@ struct Producer {
     Ring put;             // slot of the next item
     bool ok;
 
-    // 16-bit caches: the first warp alone waits and issues boxes; where all four
-    // copy, a barrier before says whether its wait was met, and one after lets it
-    // announce. Its wait may run out between two such places, so it goes on to
-    // the next one, where all learn of it (`ok`). e4m3: every warp waits and
-    // arrives for itself.
-    bool met;             // the first warp: its waits were met so far
-    int sent;             // its items
+    // 16-bit caches: the warps take the items that come in boxes in turn, each
+    // waiting for its own (`met`: its waits were met so far); where all four copy,
+    // the first waits, a barrier before says whether any wait ran out (`ok`), and
+    // one after lets the first announce. e4m3: every warp waits and arrives for
+    // itself.
+    bool met;
+    uint32_t items, sent, sent_phase;   // items so far; slots this warp's boxes went to last, a bit each, and the phases
     uint32_t qp;          // phase of q_free
     bool q_sent;
     __device__ __forceinline__ bool master() const { return wid == 0; }
@@ -336,11 +336,8 @@ struct Producer {
             : "memory");
         return r != 0;
     }
-    __device__ __forceinline__ void agree() { ok = !any_of(master() && !met); }
-    __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity) {
-        if (E4) ok = ok && warp_wait(bar, parity, &sh.abort, a.wait_cycles);
-        else if (master()) met = met && warp_wait(bar, parity, &sh.abort, a.wait_cycles);
-    }
+    __device__ __forceinline__ void agree() { ok = !any_of(!met); }
+    __device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity) { met = met && warp_wait(bar, parity, &sh.abort, a.wait_cycles); }
     // all warps' copies are in shared memory
     __device__ __forceinline__ void announce(uint64_t *bar) {
         copy_commit();
@@ -457,21 +454,24 @@ struct Producer {
                 const int page = __shfl_sync(0xffffffffu, ids, (key0 + key) / 16 & 7);
                 const int y = ((page * a.G + s.g) << a.lpage) + (p0 + key & ((1 << a.lpage) - 1));
                 const uint32_t at = dst + (b * rows + key) * 128;
-                wait_for(&sh.empty[put.slot], put.phase ^ 1);
-                if (master() && met) {
-                    if (lane == 0) mbar_expect_tx(full, blocks * rows * 128);
-                    __syncwarp();
-                    if (on) {
-                        if constexpr (CT == 2) tma_2d_pair(at, KEYS ? mk : mv, x, y, full);
-                        else tma_2d_at(at, KEYS ? mk : mv, x, y, full);
+                if ((items++ & (PR_WARPS - 1)) == wid) {
+                    wait_for(&sh.empty[put.slot], put.phase ^ 1);
+                    if (met) {
+                        if (lane == 0) mbar_expect_tx(full, blocks * rows * 128);
+                        __syncwarp();
+                        if (on) {
+                            if constexpr (CT == 2) tma_2d_pair(at, KEYS ? mk : mv, x, y, full);
+                            else tma_2d_at(at, KEYS ? mk : mv, x, y, full);
+                        }
+                        __syncwarp();
+                        sent |= 1u << put.slot;
+                        sent_phase = sent_phase & ~(1u << put.slot) | put.phase << put.slot;
                     }
-                    __syncwarp();
-                    ++sent;
                 }
-                if (met) put.next(z.nslot);   // the first warp stays at the item it could not send
+                put.next(z.nslot);
                 return;
             }
-            wait_for(&sh.empty[put.slot], put.phase ^ 1);
+            if (master()) wait_for(&sh.empty[put.slot], put.phase ^ 1);
             agree();
             if (!ok) return;
             constexpr int U = 4;   // runs in flight
@@ -499,7 +499,6 @@ struct Producer {
         }
         announce(full);
         put.next(z.nslot);
-        ++sent;
     }
 
     // e4m3. A warp of its own, the loader, brings codes and exponents by bulk
@@ -678,7 +677,7 @@ struct Producer {
             int ids = page_of(entries(s, s.t0)), ids1 = page_of(entries(s, s.t0 + 1));
             bool bx = boxes(s.t0, ids), bx1;
             keys(s.t0, ids, bx);   // before the queries, whose place the segment before may still hold
-            wait_for(&sh.q_free, qp);
+            if (master()) wait_for(&sh.q_free, qp);
             if (!ok) break;
             qp ^= 1;
             queries(s);
@@ -698,16 +697,12 @@ struct Producer {
             Ring r = put;
             for (int i = 0; i < z.nslot; ++i, r.next(z.nslot)) wait_for(&sh.empty[r.slot], r.phase ^ 1);
         }
-        if (E4 || !master() || (ok && met)) return;
+        if (E4 || (ok && met)) return;
         // after a wait that ran out: what TMA still writes lands before the block ends
         if (lane == 0) {
             if (q_sent) mbar_drain(&sh.q_full, qp);
-            Ring r = put;
-            const int back = min(sent, z.nslot);
-            for (int i = 0; i < back; ++i) {
-                if (--r.slot < 0) r.slot = z.nslot - 1, r.phase ^= 1;
-                mbar_drain(&sh.full[r.slot], r.phase);
-            }
+            for (int i = 0; i < z.nslot; ++i)
+                if (sent >> i & 1) mbar_drain(&sh.full[i], sent_phase >> i & 1);
         }
         __syncwarp();
     }
@@ -1316,7 +1311,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     } else {
         const int w = warp - SM_WARPS;   // the producers', then the issuers'
         Producer<T, C, QT, CT> p = {a, sh, z, q0, ring0, lane, 4 * w + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
-                                w, {0, 0}, true, true, 0, 1, false, q0 + z.raw};
+                                w, {0, 0}, true, true, 0, 0, 0, 1, false, q0 + z.raw};
         if (w < PR_WARPS) {
             regs_less<R::PRODUCER>();
             p.run(tab, units, share);
