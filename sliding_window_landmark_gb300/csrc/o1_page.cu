@@ -535,11 +535,11 @@ int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *s
     // fit into its units, the tensor cores' where they do not
     int64_t most = 0;
     for (int i = 0; i < n_seq; ++i) most = std::max(most, (int64_t)seqs[i].rows * g.heads_per_group);
-    const int tc = most > PG_ROWS_V ? pg_tc_vectors(g, seqs, n_seq) : 0, unit = tc ? tc : PG_ROWS_V;
+    const int tc = most > PG_ROWS_V ? pg_tc_vectors(g) : 0, unit = tc ? tc : PG_ROWS_V;
     cudaStream_t st = (cudaStream_t)stream;
     bool ok = true;
     for_tables(seqs, n_seq, [&](int rows) { return ((int64_t)rows * g.heads_per_group + unit - 1) / unit; }, [&](const PgTable &t) {
-        const cudaError_t e = tc ? pg_launch_tc(a, g, t, unit, (int64_t)total_rows * g.heads_per_group, st)
+        const cudaError_t e = tc ? pg_launch_tc(a, g, t, (int64_t)total_rows * g.heads_per_group, st)
                                  : pg_launch_rows(a, g.dtype, g.cache_dtype, &t, st);
         ok = ok && e == cudaSuccess;
     });

@@ -62,8 +62,7 @@ __device__ __forceinline__ PgRow pg_token_row(const PgArgs &a, int r) {
 }
 
 // ---------------------------------------------------------------- attention
-// Work, for both kernels (a plan P: constants V, K, START, LEAST, CTAS: thread
-// blocks that work as one; "block" below means them). A unit is up
+// Work, for both kernels (a plan P: constants V, K, START, LEAST). A unit is up
 // to V query vectors of a sequence (vector i: row i / hpg of its rows, head i %
 // hpg of a group) and a group; its keys are tiles of K positions, and it costs
 // its tiles and START more (queries, filling the pipeline, outputs). The costs of
@@ -142,10 +141,9 @@ __device__ __forceinline__ PgShare pg_share(const PgArgs &a, const PgTable &tab,
     }
     PgShare s;
     s.total = total;
-    const int block = blockIdx.x / P::CTAS;
-    s.blocks = (int)min((long long)gridDim.x / P::CTAS, max(1ll, total / P::LEAST));
-    s.at = block < s.blocks ? s.border(block) : 0;
-    s.to = block < s.blocks ? s.border(block + 1) : 0;
+    s.blocks = (int)min((long long)gridDim.x, max(1ll, total / P::LEAST));
+    s.at = (int)blockIdx.x < s.blocks ? s.border(blockIdx.x) : 0;
+    s.to = (int)blockIdx.x < s.blocks ? s.border(blockIdx.x + 1) : 0;
     before += base - own;   // costs before this thread's units
     if (s.at < s.to && s.at >= before && s.at < before + own) {
         int u = u0;
@@ -171,10 +169,7 @@ struct PgSegment {
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
     // where its partial result goes: a segment that begins inside its unit is
     // its block's first, one that only ends inside it the block's last
-    template <typename P>
-    __device__ __forceinline__ int part() const {
-        return blockIdx.x / P::CTAS * 2 + (t0 > 0 ? 0 : 1);
-    }
+    __device__ __forceinline__ int part() const { return blockIdx.x * 2 + (t0 > 0 ? 0 : 1); }
 };
 template <typename P>
 __device__ __forceinline__ bool pg_next(const PgArgs &a, const PgTable &tab, int units, PgShare &s, PgSegment &o) {
@@ -226,7 +221,7 @@ static inline size_t pg_parts_bytes(int blocks, int vecs, int dv) {
 // block's own border is the first inside its tiles.
 template <typename P>
 __device__ __forceinline__ void pg_head(PgHead *head, const PgShare &sh, const PgSegment &s) {
-    if (s.t0 == 0 || sh.border(blockIdx.x / P::CTAS - 1) > s.start + P::START) return;
+    if (s.t0 == 0 || sh.border(blockIdx.x - 1) > s.start + P::START) return;
     const int64_t end = s.start + P::START + s.nt;   // last: border(last + 1) >= end
     *head = {(int)((end * sh.blocks + sh.total - 1) / sh.total) - 1, s.x.row0, s.x.vec0, s.x.nv, s.g, {0, 0, 0}};
 }
@@ -246,7 +241,7 @@ size_t pg_rows_scratch(int dv);
 cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, cudaStream_t st);
 // o1_page_tc.cu: many query vectors, on tcgen05. pg_tc_vectors: a unit's, 0
 // where it does not take the geometry.
-int pg_tc_vectors(const o1_pg_geom &g, const o1_pg_seq *seqs, int n);
-size_t pg_tc_scratch(const o1_pg_geom &g, int64_t vectors);   // whatever the unit
-cudaError_t pg_launch_tc(const PgArgs &a, const o1_pg_geom &g, const PgTable &tab, int unit, int64_t vectors, cudaStream_t st);
+int pg_tc_vectors(const o1_pg_geom &g);
+size_t pg_tc_scratch(const o1_pg_geom &g, int64_t vectors);
+cudaError_t pg_launch_tc(const PgArgs &a, const o1_pg_geom &g, const PgTable &tab, int64_t vectors, cudaStream_t st);
 int pg_flags(uint32_t *flags, int clear, cudaStream_t st);

@@ -30,7 +30,7 @@ constexpr int RV = PG_ROWS_V;         // query vectors of a unit
 constexpr int TILE = 16 * RW;         // keys of a tile
 constexpr int PER_SM = 2, BLOCKS = 152 * PER_SM;
 struct Plan {
-    static constexpr int V = RV, K = TILE, START = 5, LEAST = 2, CTAS = 1;
+    static constexpr int V = RV, K = TILE, START = 5, LEAST = 2;
 };
 
 // Rows of type T over a cache of type C: the MMA's type M, and the terms that q
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                 }
         __syncthreads();
         const bool whole = seg.whole();
-        const size_t ps = seg.part<Plan>();
+        const size_t ps = seg.part();
         for (int i = tid; i < x.nv * (a.dv >> 2); i += RT) {
             const int v = i / (a.dv >> 2), c = 4 * (i - v * (a.dv >> 2));
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -46,15 +46,10 @@ constexpr int BLOCKS = 152;
 constexpr float HEADROOM = 8.f;                // log2 units above the reference before it moves
 constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside it
 
-template <int QT, int CT>
+template <int QT>
 struct Plan {
-    static constexpr int V = 128 * QT * CT, K = KT, START = 3, LEAST = 1, CTAS = CT;
+    static constexpr int V = 128 * QT, K = KT, START = 3, LEAST = 1;
 };
-// this block's place in its pair (CT = 2)
-template <int CT>
-__device__ __forceinline__ int rank() {
-    return CT == 2 ? blockIdx.x & 1 : 0;
-}
 
 template <typename T, typename C>
 struct Types {   // 16-bit rows over their own type
@@ -158,22 +153,6 @@ __device__ __forceinline__ void tma_2d_at(uint32_t dst, const CUtensorMap *map, 
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"((uint64_t)map), "r"(x), "r"(y), "r"(su32(bar))
         : "memory");
-}
-// into both blocks of a pair, at the same place of either, whose barrier counts it
-__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"((uint64_t)map), "r"(x), "r"(y), "r"(su32(bar)), "h"((uint16_t)3)
-        : "memory");
-}
-// arrives at the barrier of either block once this block's MMAs are done
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(bar)),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-__device__ __forceinline__ void pair_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tma_3d_at(uint32_t dst, const CUtensorMap *map, int x, int y, int w, uint64_t *bar) {
     asm volatile(
@@ -300,7 +279,7 @@ __device__ __forceinline__ bool sm_or(bool p) {
 
 // ---------------------------------------------------------------- producers
 
-template <typename T, typename C, int QT, int CT>
+template <typename T, typename C, int QT>
 struct Producer {
     using M = typename Types<T, C>::M;
     static constexpr int TERMS = Types<T, C>::TERMS;
@@ -360,7 +339,7 @@ struct Producer {
                 __syncwarp();
                 if (lane < n) {
                     const int tile = lane / z.nqc, c = lane - tile * z.nqc;
-                    tma_3d_at(q0 + 16384 * lane, mq, 64 * c, s.g * a.hpg, s.x.row0 + s.x.vec0 / a.hpg + (tile + rank<CT>()) * qrows, &sh.q_full);
+                    tma_3d_at(q0 + 16384 * lane, mq, 64 * c, s.g * a.hpg, s.x.row0 + s.x.vec0 / a.hpg + tile * qrows, &sh.q_full);
                 }
                 __syncwarp();
                 q_sent = true;
@@ -378,7 +357,7 @@ struct Producer {
             bool in[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int v = r0 + 16 * u + r4 + 128 * rank<CT>();
+                const int v = r0 + 16 * u + r4;
                 in[u] = v < s.x.nv;
                 src[u] = (const T *)a.q + (in[u] ? pg_vec_at(a, s.x.row0, s.x.vec0 + v, s.g, a.qs, a.d) : 0) + 8 * l8;
             }
@@ -450,7 +429,7 @@ struct Producer {
                 // all but the wait and the copies is done before the slot is free
                 const int blocks = (cols + 63) / 64, lb = split ? 2 : 1, lrows = min(a.lpage, split ? 6 : 7);   // rows of a box
                 const int b = lane & ((1 << lb) - 1), key = (lane >> lb) << lrows, x = col0 + 64 * b;
-                const bool on = b < blocks && key < rows && (CT == 1 || (lane & 1) == rank<CT>());
+                const bool on = b < blocks && key < rows;
                 const int page = __shfl_sync(0xffffffffu, ids, (key0 + key) / 16 & 7);
                 const int y = ((page * a.G + s.g) << a.lpage) + (p0 + key & ((1 << a.lpage) - 1));
                 const uint32_t at = dst + (b * rows + key) * 128;
@@ -459,10 +438,7 @@ struct Producer {
                     if (met) {
                         if (lane == 0) mbar_expect_tx(full, blocks * rows * 128);
                         __syncwarp();
-                        if (on) {
-                            if constexpr (CT == 2) tma_2d_pair(at, KEYS ? mk : mv, x, y, full);
-                            else tma_2d_at(at, KEYS ? mk : mv, x, y, full);
-                        }
+                        if (on) tma_2d_at(at, KEYS ? mk : mv, x, y, full);
                         __syncwarp();
                         sent |= 1u << put.slot;
                         sent_phase = sent_phase & ~(1u << put.slot) | put.phase << put.slot;
@@ -533,7 +509,7 @@ struct Producer {
     __device__ __forceinline__ void load_codes(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
         uint32_t n = 0;   // items
-        while (ok && pg_next<Plan<QT, CT>>(a, tab, units, share, s)) {
+        while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
             // pages of tiles t and on, t the last one whose values are to come
             int tile = s.t0, ids = page_of(entries(s, tile)), ids1 = page_of(entries(s, tile + 1)), next2 = entries(s, tile + 2);
             Item x = {true, s.t0, 0};
@@ -637,7 +613,7 @@ struct Producer {
     __device__ __forceinline__ void run_codes(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
         uint32_t n = 0;   // items
-        while (ok && pg_next<Plan<QT, CT>>(a, tab, units, share, s)) {
+        while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
             Item x = {true, s.t0, 0};
             convert(s, x, n++);   // before the queries, whose place the segment before may still hold
             ok = ok && warp_wait(&sh.q_free, qp, &sh.abort, a.wait_cycles);
@@ -658,7 +634,7 @@ struct Producer {
     }
     __device__ __forceinline__ void run_rows(const PgTable &tab, int units, PgShare share) {
         PgSegment s;
-        while (ok && pg_next<Plan<QT, CT>>(a, tab, units, share, s)) {
+        while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
             // a tile of a 16-bit cache comes in boxes where some row of the
             // sequence attends every position of it (outside, memory may hold
             // anything); the warps decide together, whatever each read of the table
@@ -691,11 +667,6 @@ struct Producer {
                 ids1 = page_of(next2);
                 bx = bx1;
             }
-        }
-        // what the other block's MMAs still say to this one's barriers arrives before the block ends
-        if (CT == 2 && ok && master()) {
-            Ring r = put;
-            for (int i = 0; i < z.nslot; ++i, r.next(z.nslot)) wait_for(&sh.empty[r.slot], r.phase ^ 1);
         }
         if (E4 || (ok && met)) return;
         // after a wait that ran out: what TMA still writes lands before the block ends
@@ -774,7 +745,7 @@ __device__ __forceinline__ void issuer_of(int tile, const PgArgs &a, Shared &sh,
         commit(&sh.empty[get.slot]);
         get.next(z.nslot);
     };
-    while (ok && pg_next<Plan<2, 1>>(a, tab, units, share, s)) {
+    while (ok && pg_next<Plan<2>>(a, tab, units, share, s)) {
         ok = warp_wait(&sh.q_full, qp, &sh.abort, wl);
         if (!ok) break;
         qp ^= 1;
@@ -816,7 +787,7 @@ __device__ __forceinline__ void issuer_of(int tile, const PgArgs &a, Shared &sh,
     __syncwarp();
 }
 
-template <typename T, typename C, int CT>
+template <typename T, typename C>
 __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape &z, uint32_t q0, uint32_t ring0, uint32_t tmem,
                                        const PgTable &tab, int units, PgShare share) {
     using M = typename Types<T, C>::M;
@@ -835,13 +806,6 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
     auto commit = [&](uint64_t *bar) {
         if (e) mma_commit(bar);
     };
-    auto release = [&](int slot) {
-        if constexpr (CT == 2) {
-            if (e) mma_commit_pair(&sh.empty[slot]);
-        } else {
-            commit(&sh.empty[slot]);
-        }
-    };
     auto filled = [&](const Ring &r) -> bool {
         ok = ok && warp_wait(&sh.full[r.slot], r.phase, &sh.abort, wl);
         return ok;
@@ -855,7 +819,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 tc_after();
                 const uint64_t kd = dk + (uint64_t)(r.slot * (SLOT / 16)), qd = dq + (uint64_t)(2 * i * 1024);
                 run_ss(e, col, qd, kd, id_s, min(8, z.ksteps - 8 * i), i > 0);
-                release(r.slot);
+                commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
         } else {
@@ -873,7 +837,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 }
             }
             q = r;
-            for (int i = 0; i < z.k_items; ++i, q.next(z.nslot)) release(q.slot);
+            for (int i = 0; i < z.k_items; ++i, q.next(z.nslot)) commit(&sh.empty[q.slot]);
         }
         commit(&sh.s_full[buf]);
     };
@@ -888,7 +852,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
             for (int h = 0; h < 2; ++h) run_ts<1, 8>(e, out, p + Col::p(4 * h, 2), vd + 512 * h, id_o, h > 0);
             for (int m = 1; m >= 0; --m)
                 for (int h = 0; h < 2; ++h) run_ts<1, 24>(e, out, p + Col::p(4 * h, m), vd + 512 * h, id_o, 1);
-            release(r.slot);
+            commit(&sh.empty[r.slot]);
         } else {
             for (int i = 0; i < z.v_items; ++i) {
                 if (!filled(r)) return;
@@ -896,7 +860,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
                 const uint64_t vd = dv + (uint64_t)(r.slot * (SLOT / 16));
                 run_ts<TERMS, TERMS == 1 ? 8 : 24>(e, out, p + 64 * i, vd, id_o, acc || i > 0);
                 if (z.v_items == 1) run_ts<TERMS, TERMS == 1 ? 8 : 24>(e, out, p + 64, vd + 512, id_o, 1);
-                release(r.slot);
+                commit(&sh.empty[r.slot]);
                 r.next(z.nslot);
             }
         }
@@ -905,7 +869,7 @@ __device__ __forceinline__ void issuer(const PgArgs &a, Shared &sh, const Shape 
     auto advance = [&](int n) {
         for (int i = 0; i < n; ++i) get.next(z.nslot);
     };
-    while (ok && pg_next<Plan<1, CT>>(a, tab, units, share, s)) {
+    while (ok && pg_next<Plan<1>>(a, tab, units, share, s)) {
         ok = warp_wait(&sh.q_full, qp, &sh.abort, wl);
         if (!ok) break;
         qp ^= 1;
@@ -972,7 +936,7 @@ __device__ __forceinline__ void st32(T *p, const float *x) {
     st32_words(p, w);
 }
 
-template <typename T, typename C, int QT, int CT>
+template <typename T, typename C, int QT>
 __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape &z, uint32_t tmem, const PgTable &tab, int units,
                                         PgShare share, int vecs) {
     using M = typename Types<T, C>::M;
@@ -983,19 +947,19 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float sc2 = a.scale * 1.4426950408889634f;   // scores in log2 units; scale > 0
     const long long wl = a.wait_cycles;
-    if (tid == 0 && rank<CT>() == 0) {
-        PgHead *head = &pg_parts(a.part, BLOCKS / CT, vecs).head[blockIdx.x / CT];
+    if (tid == 0) {
+        PgHead *head = &pg_parts(a.part, BLOCKS, vecs).head[blockIdx.x];
         head->last = -1;
         PgShare first = share;
         PgSegment f;
-        if (pg_next<Plan<QT, CT>>(a, tab, units, first, f)) pg_head<Plan<QT, CT>>(head, share, f);
+        if (pg_next<Plan<QT>>(a, tab, units, first, f)) pg_head<Plan<QT>>(head, share, f);
     }
     __syncwarp();
     bool ok = true;
     uint32_t n = 0, turns = 0;   // tiles so far, of this warpgroup's query tile, and in turn with the other's
     PgSegment s;
-    while (pg_next<Plan<QT, CT>>(a, tab, units, share, s)) {
-        const int tile = QT == 2 ? wg : 0, v0 = 128 * (tile + rank<CT>());
+    while (pg_next<Plan<QT>>(a, tab, units, share, s)) {
+        const int tile = QT == 2 ? wg : 0, v0 = 128 * tile;
         if (QT == 2 && s.x.nv <= v0) continue;
         const int pos = s.x.pos(a, min(v0 + row, s.x.nv - 1)), low = a.window ? pos - a.window + 1 : 0;
         // positions that every row of the tile attends
@@ -1210,12 +1174,12 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
         // the unit again, not held in registers meanwhile
         int u = s.u;
         asm volatile("" : "+r"(u));
-        const PgUnit x = pg_unit<Plan<QT, CT>::V>(a, tab, u);
-        const PgParts parts = pg_parts(a.part, BLOCKS / CT, vecs);
+        const PgUnit x = pg_unit<Plan<QT>::V>(a, tab, u);
+        const PgParts parts = pg_parts(a.part, BLOCKS, vecs);
         const int v = v0 + row;
         const bool whole = s.whole(), in = v < x.nv;
         const float f = !ok ? NAN : !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const size_t ps = s.part<Plan<QT, CT>>();
+        const size_t ps = s.part();
         const bool wide = ((uintptr_t)a.out | a.os * sizeof(T) | a.dv * sizeof(T)) % 32 == 0;
         T *out = (T *)a.out + (in ? pg_vec_at(a, x.row0, x.vec0 + v, s.g, a.os, a.dv) : 0);
         if (in && !whole && (QT == 2 || wg == 0)) *(float2 *)(parts.stat + (ps * vecs + v) * 2) = ok ? make_float2(m, l) : make_float2(0.f, NAN);
@@ -1265,7 +1229,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
     if (!ok) tmem_st_wait();   // stores issued before a wait ran out are over before the TMEM is given back
 }
 
-template <typename T, typename C, int QT, int CT>
+template <typename T, typename C, int QT>
 __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_constant__ PgTable tab,
                                                       const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                                                       const __grid_constant__ CUtensorMap mv, int qrows, int units, int vecs) {
@@ -1278,7 +1242,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     if (tid == 0) {
         for (int i = 0; i < MAX_SLOTS; ++i) {
             mbar_init(&sh.full[i], sizeof(C) == 1 ? PR_WARPS : 1);
-            mbar_init(&sh.empty[i], QT * CT);   // issuers
+            mbar_init(&sh.empty[i], QT);   // QT issuers
         }
         mbar_init(&sh.q_full, sizeof(C) == 1 && !qrows ? PR_WARPS : 1);
         for (int i = 0; i < 2; ++i) mbar_init(&sh.raw_full[i], 1), mbar_init(&sh.raw_empty[i], PR_WARPS);
@@ -1299,18 +1263,17 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     __syncwarp();
     if (warp == SM_WARPS + PR_WARPS) tmem_alloc512(&sh.tslot);
     tc_before();
-    const PgShare share = pg_share<Plan<QT, CT>, THREADS>(a, tab, units, sh.share);
+    const PgShare share = pg_share<Plan<QT>, THREADS>(a, tab, units, sh.share);
     __syncthreads();
-    if constexpr (CT == 2) pair_sync();   // both have their barriers
     tc_after();
     const uint32_t tmem = sh.tslot;
     using R = Regs;
     if (warp < SM_WARPS) {
         regs_more<R::SOFTMAX>();
-        softmax<T, C, QT, CT>(a, sh, z, tmem, tab, units, share, vecs);
+        softmax<T, C, QT>(a, sh, z, tmem, tab, units, share, vecs);
     } else {
         const int w = warp - SM_WARPS;   // the producers', then the issuers'
-        Producer<T, C, QT, CT> p = {a, sh, z, q0, ring0, lane, 4 * w + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
+        Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * w + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
                                 w, {0, 0}, true, true, 0, 0, 0, 1, false, q0 + z.raw};
         if (w < PR_WARPS) {
             regs_less<R::PRODUCER>();
@@ -1320,7 +1283,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
             const int i = w - PR_WARPS;
             if (i < QT) {
                 if constexpr (QT == 2) issuer_of<T, C>(i, a, sh, z, q0, ring0, tmem, tab, units, share);
-                else issuer<T, C, CT>(a, sh, z, q0, ring0, tmem, tab, units, share);
+                else issuer<T, C>(a, sh, z, q0, ring0, tmem, tab, units, share);
             } else if (sizeof(C) == 1 && i == 2) {
                 p.load_codes(tab, units, share);
             }
@@ -1328,7 +1291,6 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     }
     tc_before();
     __syncthreads();
-    if constexpr (CT == 2) pair_sync();   // neither's copies or barriers are used any more
     tc_after();
     if (warp == SM_WARPS + PR_WARPS) tmem_free512(tmem);
     if (tid == 0 && sh.abort) atomicOr(&pg_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
@@ -1350,11 +1312,11 @@ bool pool_map(CUtensorMap *m, const void *base, int width, uint64_t rows, uint32
     return encode<M>(m, 2, base, dims, strides, box);
 }
 
-template <typename T, typename C, int QT, int CT>
+template <typename T, typename C, int QT>
 cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vectors, cudaStream_t st) {
     static unsigned long long done = 0;
     unsigned long long bit = 0;
-    auto *k = k_pg_tc<T, C, QT, CT>;
+    auto *k = k_pg_tc<T, C, QT>;
     if (o1_attrs_needed(&done, &bit)) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
         if (e != cudaSuccess) return e;
@@ -1364,7 +1326,7 @@ cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vec
         if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;
         o1_attrs_done(&done, bit);
     }
-    constexpr int V = Plan<QT, CT>::V;
+    constexpr int V = Plan<QT>::V;
     const int vecs = (int)(vectors < V ? vectors : V);
     CUtensorMap mq = {}, mk = {}, mv = {};
     int qrows = 0;
@@ -1382,66 +1344,42 @@ cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vec
             const cuuint32_t box[3] = {64, (cuuint32_t)a.hpg, (cuuint32_t)qrows};
             if (!encode<T>(&mq, 3, a.q, dims, strides, box)) return cudaErrorInvalidValue;
         }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = BLOCKS;
-    cfg.blockDim = THREADS;
-    cfg.dynamicSmemBytes = SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute pair = {};
-    pair.id = cudaLaunchAttributeClusterDimension;
-    pair.val.clusterDim.x = CT;
-    pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
-    cfg.attrs = &pair;
-    cfg.numAttrs = CT == 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a, tab, mq, mk, mv, qrows, (int)tab.total, vecs);
-    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS / CT, vecs, st) : e;
+    k<<<BLOCKS, THREADS, SMEM, st>>>(a, tab, mq, mk, mv, qrows, tab.total, vecs);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, vecs, st) : e;
 }
 // Two query tiles a block where both fit beside a ring of five slots: one term
 // and rows of up to 128 values.
 template <typename T, typename C>
-cudaError_t launch_t(const PgArgs &a, int dtype, const PgTable &tab, int unit, int64_t vectors, cudaStream_t st) {
-    if constexpr (Types<T, C>::TERMS == 1) {
-        if (a.d <= 128 && a.dv <= 128) return launch_q<T, C, 2, 1>(a, dtype, tab, vectors, st);
-        if constexpr (sizeof(C) == 2)
-            if (unit == 256) return launch_q<T, C, 1, 2>(a, dtype, tab, vectors, st);
-    }
-    return launch_q<T, C, 1, 1>(a, dtype, tab, vectors, st);
+cudaError_t launch_t(const PgArgs &a, int dtype, const PgTable &tab, int64_t vectors, cudaStream_t st) {
+    if constexpr (Types<T, C>::TERMS == 1)
+        if (a.d <= 128 && a.dv <= 128) return launch_q<T, C, 2>(a, dtype, tab, vectors, st);
+    return launch_q<T, C, 1>(a, dtype, tab, vectors, st);
 }
 
 }  // namespace
 
-// Wide rows over a 16-bit cache: pairs of blocks, a unit's 256 vectors between
-// them, where few of their tiles would be empty.
-int pg_tc_vectors(const o1_pg_geom &g, const o1_pg_seq *seqs, int n) {
+int pg_tc_vectors(const o1_pg_geom &g) {
     const bool wide = g.d > 128 || g.dv > 128;
     if (g.dtype == O1_F32) return wide ? 0 : 128;   // three terms of Q, and P's third
     if (g.dtype == O1_F16 && g.cache_dtype == O1_E4M3) return 128;
-    if (!wide) return 256;
-    if (g.cache_dtype == O1_E4M3) return 128;
-    int64_t one = 0, two = 0;   // tiles, and of pairs
-    for (int i = 0; i < n; ++i) {
-        const int64_t v = (int64_t)seqs[i].rows * g.heads_per_group;
-        one += (v + 127) / 128;
-        two += (v + 255) / 256 * 2;
-    }
-    return 4 * two <= 5 * one ? 256 : 128;
+    return wide ? 128 : 256;
 }
 
 size_t pg_tc_scratch(const o1_pg_geom &g, int64_t vectors) {
-    // (a pair's 256 vectors take no more than its blocks' 128 each)
-    const int v = pg_tc_vectors(g, nullptr, 0) ? g.d > 128 || g.dv > 128 || g.dtype == O1_F32 ? 128 : 256 : 0;
+    const int v = pg_tc_vectors(g);
     return v ? pg_parts_bytes(BLOCKS, (int)(vectors < v ? vectors : v), g.dv) : 0;
 }
 
-cudaError_t pg_launch_tc(const PgArgs &a, const o1_pg_geom &g, const PgTable &tab, int unit, int64_t vectors, cudaStream_t st) {
+cudaError_t pg_launch_tc(const PgArgs &a, const o1_pg_geom &g, const PgTable &tab, int64_t vectors, cudaStream_t st) {
     if (g.dtype == O1_F32)
-        return g.cache_dtype == O1_E4M3 ? launch_t<float, uint8_t>(a, g.dtype, tab, unit, vectors, st)
-                                        : launch_t<float, __nv_bfloat16>(a, g.dtype, tab, unit, vectors, st);
+        return g.cache_dtype == O1_E4M3 ? launch_t<float, uint8_t>(a, g.dtype, tab, vectors, st)
+                                        : launch_t<float, __nv_bfloat16>(a, g.dtype, tab, vectors, st);
     if (g.dtype == O1_BF16)
-        return g.cache_dtype == O1_E4M3 ? launch_t<__nv_bfloat16, uint8_t>(a, g.dtype, tab, unit, vectors, st)
-                                        : launch_t<__nv_bfloat16, __nv_bfloat16>(a, g.dtype, tab, unit, vectors, st);
-    return g.cache_dtype == O1_E4M3 ? launch_t<__half, uint8_t>(a, g.dtype, tab, unit, vectors, st)
-                                    : launch_t<__half, __half>(a, g.dtype, tab, unit, vectors, st);
+        return g.cache_dtype == O1_E4M3 ? launch_t<__nv_bfloat16, uint8_t>(a, g.dtype, tab, vectors, st)
+                                        : launch_t<__nv_bfloat16, __nv_bfloat16>(a, g.dtype, tab, vectors, st);
+    return g.cache_dtype == O1_E4M3 ? launch_t<__half, uint8_t>(a, g.dtype, tab, vectors, st)
+                                    : launch_t<__half, __half>(a, g.dtype, tab, vectors, st);
 }
 
 // As lin_flags: reset only where it was read as raised.
