@@ -1118,7 +1118,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                     if (QT == 1) sm_sync();   // the maxima are read before they are written again
                 }
                 if (!ok) break;
-                if (QT == 2 && paired && i == 1 && lane == 0) mbar_arrive(&sh.turn[wg ^ 1][warp & 3]);
+                if (QT == 2 && paired && i == 0 && lane == 0) mbar_arrive(&sh.turn[wg ^ 1][warp & 3]);
                 // P over the scores it comes from
                 if (!idle) {
                     __syncwarp();   // the warp is together for the stores
