@@ -48,7 +48,7 @@ constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside i
 
 template <int QT>
 struct Plan {
-    static constexpr int V = 128 * QT, K = KT, START = 3, LEAST = 1;
+    static constexpr int V = 128 * QT, K = KT, START = 2, LEAST = 1;
 };
 
 template <typename T, typename C>
@@ -936,6 +936,9 @@ __device__ __forceinline__ void st32(T *p, const float *x) {
     st32_words(p, w);
 }
 
+// ones from bit b on, of any b
+__device__ __forceinline__ uint32_t ones_from(int b) { return b <= 0 ? ~0u : b > 31 ? 0u : ~0u << b; }
+
 template <typename T, typename C, int QT>
 __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape &z, uint32_t tmem, const PgTable &tab, int units,
                                         PgShare share, int vecs) {
@@ -1038,8 +1041,13 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                         const int b0 = low - x0 - 64 * h - k0, b1 = pos - x0 - 64 * h - k0;
                         const uint32_t on = there >> (4 * h + k0 / 16);
 #pragma unroll
-                        for (int c = 0; c < NR; ++c)
-                            if (c < b0 || c > b1 || !(on >> (c / 16) & 1)) r[c] = 0xff800000u;
+                        for (int q = 0; q < NR; q += 32) {
+                            const uint32_t at = (on >> (q / 16) & 1) * 0xffffu | (on >> (q / 16 + 1) & 1) * 0xffff0000u;
+                            const uint32_t bits = at & ones_from(b0 - q) & ~ones_from(b1 - q + 1);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(bits >> c & 1)) r[q + c] = 0xff800000u;
+                        }
                     }
                 };
                 if (ok && !idle) {
