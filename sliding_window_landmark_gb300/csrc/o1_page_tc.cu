@@ -11,14 +11,28 @@
 //               one tile with two score buffers and a warpgroup on either half
 //               of its keys (QT = 1)
 //   warps 8-11  producers: queries, keys and values into shared memory, 128-byte
-//               swizzled, by 16-byte asynchronous copies (16-bit caches) or
-//               through registers, where e4m3 codes become bf16 values under
-//               their row's power of two (exact). Pages end anywhere on 16
-//               positions; a producer's 16 rows lie in one page. What no row
-//               attends is zero-filled, not read.
+//               swizzled. 16-bit caches: the tiles that lie wholly in a sequence
+//               and on pages in TMA boxes, the warps in turn; others by 16-byte
+//               asynchronous copies (pages end anywhere on 16 positions; what no
+//               row attends is zero-filled, not read). e4m3: codes, converted
+//               to bf16 values under their row's power of two (exact)
 //   warp 12     issues the MMAs (QT = 2: warps 12 and 13, a query tile each)
+//   warp 14     e4m3: brings the codes
 // Keys come as items of 128 keys x 128 columns, values as 128 keys x 128 columns
 // or 64 x 256: 32 KB slots of one ring, in the order of use.
+//
+// Bound: rows of 128, the weights' formation. Two tiles of 128 x 128 scores take
+// the tensor cores 2150 cycles and their softmax warps about 4000 (an element is
+// one exponential and three other operations; they are formed by the tiles'
+// warps half a turn apart, which took 9 % less than all at once). 8192 bf16 rows
+// of 4 groups of 4 heads of 128, cache empty before: 259 us, 1060 TFLOP/s. Rows of
+// 256 have twice the products to a weight, and the tensor cores are the bound:
+// 4096 bf16 rows of 2 groups of 4 heads behind 12288: 318 us, 1510 TFLOP/s.
+// Producers: a slot's wait, its arrival and its copies are a chain of single
+// instructions, and one warp that also formed the addresses there (453 us) was
+// the bound of the latter. (Pairs of blocks that load each key tile once for
+// both were no faster.) e4m3: the conversion. 2047 bf16 rows and eight shorter
+// sequences: 81 us; 2048 bf16 rows of 256: 87 us, of a bf16 cache 56.
 //
 // Terms. As in o1_page_rows.cu: one for 16-bit rows over their own type and bf16
 // over e4m3, two bf16 for fp16 over e4m3, three for fp32. For fp32 rows a tile's
@@ -40,12 +54,16 @@ namespace {
 
 constexpr int KT = 128;                        // keys of a tile
 constexpr int SM_WARPS = 8, PR_WARPS = 4;      // softmax and producer warps
-constexpr int THREADS = 32 * (SM_WARPS + PR_WARPS + 4), SM_THREADS = 32 * SM_WARPS;   // the issuer's warpgroup has three idle warps
+constexpr int THREADS = 32 * (SM_WARPS + PR_WARPS + 4), SM_THREADS = 32 * SM_WARPS;
 constexpr int SLOT = 32768, MAX_SLOTS = 6;
 constexpr int BLOCKS = 152;
 constexpr float HEADROOM = 8.f;                // log2 units above the reference before it moves
 constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside it
 
+// A segment costs about two tiles beside its own (8192 bf16 rows: 306 us with
+// START = 1, 259 with 2, 261 with 3, 263 with 4; the ragged e4m3 batch 90, 81, 82,
+// 83), and a tile alone is worth a block: 300 and 77 fp16 rows of odd widths and a
+// window took 21 us with LEAST = 1, 25 with 2, 28 with 4, 34 with 6.
 template <int QT>
 struct Plan {
     static constexpr int V = 128 * QT, K = KT, START = 2, LEAST = 1;
