@@ -594,13 +594,13 @@ O1_API size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows);
  * values are in the cache before (o1_pg_write). A row with no position left is 0.
  *   scratch  device, 256-byte aligned, o1_pg_scratch_bytes(geom, total_rows) at least
  *   q        device row tensor [total_rows][nh][d]
- *   seqs     as for o1_pg_read
+ *   seqs     as for o1_pg_read; rows * heads_per_group < 2^31 - 512 of each
  *   out      device row tensor [total_rows][nh][dv]; rows of no sequence are
  *            left as they were
  * q and what is attended are finite, and scores below 2^127 in fp32. A
  * non-finite key or value spoils rows of its own sequence only: from its
- * position on, and up to 127 before it. Positions that no row of the sequence
- * attends (past its end, before its window) may hold anything.
+ * position on, and less than 384 before it. Positions that no row of the
+ * sequence attends (past its end, before its window) may hold anything.
  * Scores, the softmax's maxima and sums and the outputs' sums are fp32. The
  * products run on the tensor cores with the cached values as they are; of the
  * other operand, q is exact (16-bit rows over e4m3: to 2^-25 of its largest

@@ -540,6 +540,7 @@ int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *s
     // 60), fp16 over e4m3, with two terms, later (5 rows: 53 and 66, 16: 90 and 68).
     int64_t most = 0;
     for (int i = 0; i < n_seq; ++i) most = std::max(most, (int64_t)seqs[i].rows * g.heads_per_group);
+    if (most >= INT32_MAX - 511) return O1_ERR_ARG;   // vectors are counted in 32 bits
     const int tc = most > PG_ROWS_V ? pg_tc_vectors(g) : 0, unit = tc ? tc : PG_ROWS_V;
     cudaStream_t st = (cudaStream_t)stream;
     bool ok = true;

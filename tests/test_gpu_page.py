@@ -361,6 +361,33 @@ def test_extreme_scores(o1, dt, ct):
     check(o1, cache, q, [(r, 1, 0, r) for r in range(700)], out, "rows")
 
 
+@pytest.mark.parametrize("dt,ct", TYPES)
+@pytest.mark.parametrize("hpg,d", [(1, 64), (2, 144)])
+def test_non_finite_rows_spoil_only_what_is_near(o1, dt, ct, hpg, d):
+    """A key that is infinite and a value that is NaN: rows 384 and more before
+    them and the other sequence are as if they were not there, rows from the
+    value's position on are NaN."""
+    at, lens = 700, [1000, 150]
+    g = o1.pg_geom(1, hpg, d, d, 64, dtype=dt, cache_dtype=ct)
+    cache = Cache(o1, g, lens, 31)
+    for pool, value in ((cache.v, NAN), (cache.k, float("inf"))):
+        ids, n = ref.places(cache.table, 64, 0, at, at + 1)
+        if ct is E4:
+            pool.view(torch.uint8)[ids, 0, n] = 0x7f
+        else:
+            pool[ids, 0, n] = value
+        q = randn(torch.Generator().manual_seed(6), sum(lens), hpg, d, dtype=dt)
+        out = torch.zeros(sum(lens), hpg, d, dtype=dt, device="cuda")
+        attend(o1, cache, q, [(0, lens[0], 0, 0), (lens[0], lens[1], 1, 0)], out)
+        seqs = [(0, at - 383, 0, 0), (lens[0], lens[1], 1, 0)]
+        k, v = cache.held()
+        terms, rho, f16 = ref.precision(dt, ct)
+        want, bound = ref.attend(q, k, v, cache.table, 64, cache.n, seqs, g.scale, 0, dt, terms, rho, f16, cache.ve)
+        for r0, n, _, _ in seqs:
+            ref.assert_within(out[r0:r0 + n], want[r0:r0 + n].cpu(), bound[r0:r0 + n].cpu(), f"rows {r0} on")
+        assert torch.isnan(out[at:lens[0]]).all()
+
+
 @pytest.mark.parametrize("dt,ct", [(F32, BF16), (BF16, E4)])
 def test_strides_and_slices(o1, dt, ct):
     """q, k, v as columns of one projection's rows; out as columns of a buffer;

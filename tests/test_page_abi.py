@@ -162,6 +162,14 @@ def test_chunk_refusals(o1):
     assert chunk(o1, g=geom(o1, cache_dtype=E4), out=160 * MB) == A
 
 
+def test_vectors_of_a_sequence(o1):
+    """A sequence's rows times its heads a group are counted in 32 bits."""
+    big = dict(g=geom(o1, G=1, hpg=16, d=8, dv=8, page=256), c=cache(o1, n_pages=1, width=1 << 22), q=1 << 44, qs=128, out=1 << 45,
+               os_=128, rows=1 << 28)
+    assert chunk(o1, seqs=((0, 1 << 27, 0, 0),), **big) == o1.O1_ERR_ARG
+    assert chunk(o1, seqs=((0, 0, 0, 0), (0, 1 << 28, 1, 0)), **big) == o1.O1_ERR_ARG
+
+
 def test_token_refusals(o1):
     A = o1.O1_ERR_ARG
     for call in (token, token_write):
