@@ -18,7 +18,9 @@
 // pieces of 16 bytes are permuted within 128 by their key, so that neither read
 // hits a bank twice.
 #include <math.h>
+#include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "o1_page.cuh"
@@ -678,8 +680,8 @@ __global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs
     }
 }
 template <typename T>
-void join_launch(const PgArgs &a, int blocks, int vecs, cudaStream_t st) {
-    const dim3 few(blocks - 1, vecs), many(blocks - 1, (vecs + 31) / 32, vecs <= 128 ? (a.dv + 31) / 32 : 1);
+void join_launch(const PgArgs &a, int blocks, int vecs, int most, cudaStream_t st) {
+    const dim3 few(blocks - 1, most), many(blocks - 1, (vecs + 31) / 32, vecs <= 128 ? (a.dv + 31) / 32 : 1);
     if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN), 0, st, a, blocks, vecs);
     else if (a.dv <= 64) o1_launch_chained(true, k_pg_join_few<T, 16>, few, dim3(JOIN), 0, st, a, blocks, vecs);
     else if (a.dv <= 128) o1_launch_chained(true, k_pg_join_few<T, 32>, few, dim3(JOIN), 0, st, a, blocks, vecs);
@@ -718,10 +720,10 @@ cudaError_t rows_launch_c(const PgArgs &a, const PgTable *tab, int units, cudaSt
 
 size_t pg_rows_scratch(int dv) { return pg_parts_bytes(BLOCKS, RV, dv); }
 
-cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, cudaStream_t st) {
-    if (dtype == O1_F32) join_launch<float>(a, blocks, vecs, st);
-    else if (dtype == O1_BF16) join_launch<__nv_bfloat16>(a, blocks, vecs, st);
-    else join_launch<__half>(a, blocks, vecs, st);
+cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, int most, cudaStream_t st) {
+    if (dtype == O1_F32) join_launch<float>(a, blocks, vecs, most, st);
+    else if (dtype == O1_BF16) join_launch<__nv_bfloat16>(a, blocks, vecs, most, st);
+    else join_launch<__half>(a, blocks, vecs, most, st);
     return cudaGetLastError();
 }
 
@@ -734,5 +736,8 @@ cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const Pg
     else if (dtype == O1_BF16) e = rows_launch_c<__nv_bfloat16, uint8_t>(a, tab, units, st);
     else if (cache_dtype == O1_F16) e = rows_launch_c<__half, __half>(a, tab, units, st);
     else e = rows_launch_c<__half, uint8_t>(a, tab, units, st);
-    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, RV, st) : e;   // partial results of RV vectors' room
+    int most = tab ? 1 : a.hpg;
+    if (tab)
+        for (int i = 0; i < tab->n && most < RV; ++i) most = (int)std::max<int64_t>(most, std::min<int64_t>(RV, (int64_t)tab->s[i].rows * a.hpg));
+    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, RV, most, st) : e;
 }
