@@ -415,6 +415,49 @@ def test_strides_and_slices(o1, dt, ct):
     assert all((x[i].view(torch.uint8) == 0).all() for x in pools for i in (0, 2))
 
 
+@pytest.mark.parametrize("dt,ct", [(BF16, BF16), (F16, E4)])
+def test_most_rows(o1, dt, ct):
+    """65536 decode rows, written and attended in a call each; some of them checked."""
+    n = 65536
+    g = o1.pg_geom(1, 2, 16, 16, 16, dtype=dt, cache_dtype=ct)
+    cache = Cache(o1, g, [2 + r % 40 for r in range(n)], 41)
+    gen = torch.Generator().manual_seed(42)
+    k, v, q = (randn(gen, n, h, 16, dtype=dt) for h in (1, 1, 2))
+    pos = torch.arange(n, device="cuda") % 40 + 1
+    o1.check(o1.o1_pg_token_write(g, cache.c, k, v, None, pos), "write")
+    out = torch.full((n, 2, 16), NAN, dtype=dt, device="cuda")
+    attend(o1, cache, q, None, out, token=(None, pos))
+    some = list(range(0, n, 409)) + [n - 2, n - 1]
+    held = ref.quantise(k)[0] if ct is E4 else k.double()
+    for r in some[::10]:
+        ids, at = ref.places(cache.table, 16, r, int(pos[r]), int(pos[r]) + 1)
+        assert torch.equal(ref.held(cache.k, cache.ke)[ids, :, at][0], held[r])
+    seqs = [(r, 1, r, int(pos[r])) for r in some]
+    terms, rho, f16 = ref.precision(dt, ct)
+    want, bound = ref.attend(q, *cache.held(), cache.table, 16, cache.n, seqs, g.scale, 0, dt, terms, rho, f16, cache.ve)
+    ref.assert_within(out[some], want[some].cpu(), bound[some].cpu(), "rows")
+    assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dt,ct", [(BF16, BF16), (BF16, E4), (F32, BF16)])
+@pytest.mark.parametrize("hpg", [4, 16])
+def test_most_sequences(o1, dt, ct, hpg):
+    """4096 sequences of 3 rows, in 32 launches over the same scratch."""
+    n = 4096
+    g = o1.pg_geom(1, hpg, 32, 32, 16, dtype=dt, cache_dtype=ct)
+    cache = Cache(o1, g, [3 + r % 60 for r in range(n)], 43)
+    q = randn(torch.Generator().manual_seed(44), 3 * n, hpg, 32, dtype=dt)
+    out = torch.full((3 * n, hpg, 32), NAN, dtype=dt, device="cuda")
+    seqs = [(3 * r, 3, r, r % 60) for r in range(n)]
+    attend(o1, cache, q, seqs, out)
+    some = seqs[::31] + seqs[-1:]
+    terms, rho, f16 = ref.precision(dt, ct)
+    want, bound = ref.attend(q, *cache.held(), cache.table, 16, cache.n, some, g.scale, 0, dt, terms, rho, f16, cache.ve)
+    rows = [r0 + i for r0, m, _, _ in some for i in range(m)]
+    ref.assert_within(out[rows], want[rows].cpu(), bound[rows].cpu(), "sequences")
+    assert torch.isfinite(out).all()
+
+
 def test_far_offsets(o1):
     """A cache whose offsets pass 2^31 values: its last pages, 2.3 GB in."""
     G, d, page = 2, 256, 256
