@@ -597,7 +597,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
 // The partial results of a unit that borders cut, added up by the blocks of the
 // first border inside it, eight parts (four) in flight: what it takes is the
 // latency of three loads one behind the other.
-constexpr int JOIN = 256;
+constexpr int JOIN = 256, JOIN_MANY = 128;   // threads, of few and of many vectors
 struct Sum {
     float m, l;
     float4 o;
@@ -657,12 +657,14 @@ __global__ __launch_bounds__(JOIN) void k_pg_join_few(PgArgs a, int blocks, int 
     }
     o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v, h.g, a.os, a.dv) + c, s.result());
 }
-// Many vectors: 32 vectors and 32 columns a turn, a lane a vector and a warp 4
-// columns; the rows go out through shared memory. A block takes 32 columns where
-// units are small and their parts many, all of them (fewer blocks) where not.
+// Many vectors: a block takes 32 vectors and 16 columns, a lane a vector and a warp
+// 4 columns; the rows go out through shared memory. (A block that took all
+// columns of its vectors left the sum of a few units' many parts to few of them:
+// 64 bf16 rows behind 16000, 4 groups of 4 heads of 128, 53 us; 35 with 32 columns,
+// 33 with 16, 37 with 8.)
 template <typename T>
-__global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs) {
-    constexpr int W = JOIN / 32;
+__global__ __launch_bounds__(JOIN_MANY) void k_pg_join(PgArgs a, int blocks, int vecs) {
+    constexpr int W = JOIN_MANY / 32;
     __shared__ float4 rows[32][W + 1];
     o1_chain_wait();
     const int border = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = 32 * blockIdx.y, v = v0 + lane;
@@ -670,19 +672,16 @@ __global__ __launch_bounds__(JOIN) void k_pg_join(PgArgs a, int blocks, int vecs
     const PgHead h = parts.head[border];
     if (h.last < 0 || v0 >= h.nv) return;
     const int r = threadIdx.x / W, k = threadIdx.x % W;
-    for (int c0 = 4 * W * blockIdx.z; c0 < a.dv; c0 += 4 * W * gridDim.z) {
-        const int c = c0 + 4 * warp;
-        if (v < h.nv && c < a.dv) rows[lane][warp] = join_parts<8, 1>(parts, border, h.last, 0, vecs, a.dv, v, c).result();
-        __syncthreads();
-        if (v0 + r < h.nv && c0 + 4 * k < a.dv)
-            o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v0 + r, h.g, a.os, a.dv) + c0 + 4 * k, rows[r][k]);
-        __syncthreads();
-    }
+    const int c0 = 4 * W * blockIdx.z, c = c0 + 4 * warp;
+    if (v < h.nv && c < a.dv) rows[lane][warp] = join_parts<8, 1>(parts, border, h.last, 0, vecs, a.dv, v, c).result();
+    __syncthreads();
+    if (v0 + r < h.nv && c0 + 4 * k < a.dv)
+        o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v0 + r, h.g, a.os, a.dv) + c0 + 4 * k, rows[r][k]);
 }
 template <typename T>
 void join_launch(const PgArgs &a, int blocks, int vecs, int most, cudaStream_t st) {
-    const dim3 few(blocks - 1, most), many(blocks - 1, (vecs + 31) / 32, vecs <= 128 ? (a.dv + 31) / 32 : 1);
-    if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN), 0, st, a, blocks, vecs);
+    const dim3 few(blocks - 1, most), many(blocks - 1, (vecs + 31) / 32, (a.dv + JOIN_MANY / 8 - 1) / (JOIN_MANY / 8));
+    if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN_MANY), 0, st, a, blocks, vecs);
     else if (a.dv <= 64) o1_launch_chained(true, k_pg_join_few<T, 16>, few, dim3(JOIN), 0, st, a, blocks, vecs);
     else if (a.dv <= 128) o1_launch_chained(true, k_pg_join_few<T, 32>, few, dim3(JOIN), 0, st, a, blocks, vecs);
     else o1_launch_chained(true, k_pg_join_few<T, 64>, few, dim3(JOIN), 0, st, a, blocks, vecs);
