@@ -535,9 +535,9 @@ int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *s
     // fit into its units of 16, the tensor cores' where they do not. 32 sequences
     // behind 2000 positions, 4 groups of 4 heads of 128: of 4 rows 44 us with
     // either (bf16; fp32: 49 with the first and 66 with the second, bf16 over e4m3:
-    // 37 and 48), of 5 rows 58 and 45 (72 and 67, 53 and 47), of 16 97 and 46 (124
-    // and 69, 90 and 49). Rows of 256 the tensor cores' has earlier (4 rows: 69 and
-    // 60), fp16 over e4m3, with two terms, later (5 rows: 53 and 66, 16: 90 and 68).
+    // 37 and 48), of 5 rows 57 and 45 (72 and 66, 53 and 48), of 16 96 and 46 (124
+    // and 68, 90 and 48). Rows of 256 the tensor cores' has earlier (4 rows: 69 and
+    // 60), fp16 over e4m3, with two terms, later (5 rows: 53 and 65, 16: 90 and 67).
     int64_t most = 0;
     for (int i = 0; i < n_seq; ++i) most = std::max(most, (int64_t)seqs[i].rows * g.heads_per_group);
     if (most >= INT32_MAX - 511) return O1_ERR_ARG;   // vectors are counted in 32 bits

@@ -25,14 +25,14 @@
 // the tensor cores 2150 cycles and their softmax warps about 4000 (an element is
 // one exponential and three other operations; they are formed by the tiles'
 // warps half a turn apart, which took 9 % less than all at once). 8192 bf16 rows
-// of 4 groups of 4 heads of 128, cache empty before: 259 us, 1060 TFLOP/s. Rows of
+// of 4 groups of 4 heads of 128, cache empty before: 256 us, 1070 TFLOP/s. Rows of
 // 256 have twice the products to a weight, and the tensor cores are the bound:
-// 4096 bf16 rows of 2 groups of 4 heads behind 12288: 318 us, 1510 TFLOP/s.
+// 4096 bf16 rows of 2 groups of 4 heads behind 12288: 317 us, 1520 TFLOP/s.
 // Producers: a slot's wait, its arrival and its copies are a chain of single
 // instructions, and one warp that also formed the addresses there (453 us) was
 // the bound of the latter. (Pairs of blocks that load each key tile once for
-// both were no faster.) e4m3: the conversion. 2047 bf16 rows and eight shorter
-// sequences: 81 us; 2048 bf16 rows of 256: 87 us, of a bf16 cache 56.
+// both were no faster.) e4m3: the conversion, 2100 cycles a 16 KB item of codes; 2047
+// bf16 rows and eight shorter sequences, 4 groups of 4 heads of 128: 80 us.
 //
 // Terms. As in o1_page_rows.cu: one for 16-bit rows over their own type and bf16
 // over e4m3, two bf16 for fp16 over e4m3, three for fp32. For fp32 rows a tile's
