@@ -32,7 +32,7 @@
 // instructions, and one warp that also formed the addresses there (453 us) was
 // the bound of the latter. (Pairs of blocks that load each key tile once for
 // both were no faster.) e4m3: the conversion, 2100 cycles a 16 KB item of codes; 2047
-// bf16 rows and eight shorter sequences, 4 groups of 4 heads of 128: 80 us.
+// bf16 rows and eight shorter sequences, 4 groups of 4 heads of 128: 79 us.
 //
 // Terms. As in o1_page_rows.cu: one for 16-bit rows over their own type and bf16
 // over e4m3, two bf16 for fp16 over e4m3, three for fp32. For fp32 rows a tile's
@@ -587,25 +587,28 @@ struct Producer {
         // columns of 128 and on: the same slot's next blocks, or a pair's second slot
         const uint32_t dst1 = pair ? ring0 + second.slot * SLOT : dst + 2 * block;
         const bool all = there == (two ? 15 : 255) && from >= s.x.lo && from + rows - 1 <= s.x.hi;
+        // pieces in flight: more of them make the loop too long for the instruction
+        // caches (the ragged batch took 89 us with 8, 80 with 4, 79 with 2, 81 with 1)
+        constexpr int U = 2;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-            uint4 w[4];
-            uint32_t f[4];
+        for (int i0 = 0; i0 < 8; i0 += U) {
+            uint4 w[U];
+            uint32_t f[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int i = i0 + u, row = row0 + 4 * (i >> two);
                 f[u] = sh.raw_exps[b][row];
                 w[u] = ld16(src + 4 * width * (i >> two) + (two ? 128 * (i & 1) : 0));
             }
             if (!all) {   // where no row attends it, memory may hold anything
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < U; ++u) {
                     const int row = row0 + 4 * ((i0 + u) >> two);
                     if (!(there >> (row >> 4) & 1) || from + row < s.x.lo || from + row > s.x.hi) w[u] = make_uint4(0u, 0u, 0u, 0u), f[u] = 0;
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int i = i0 + u, row = row0 + 4 * (i >> two), c = 16 * l8 + (two ? 128 * (i & 1) : 0);
                 if (c < cols) {
                     const uint32_t f2 = f[u] * 0x00800080u;   // 2^(byte - 127) twice
