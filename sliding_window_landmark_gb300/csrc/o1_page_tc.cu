@@ -242,11 +242,23 @@ struct Shared {
     uint64_t turn[2][4];   // QT = 2: the two tiles' warps of a scheduler form weights in turn
     alignas(16) uint8_t raw_exps[2][KT];  // their exponents
     uint32_t raw_there[2];                // their runs of 16 positions that have a page, a bit each
+    // for the block's end after a wait that ran out: where TMA writes or wrote
+    // last, 1 and the phase that this completes (0: nowhere): slots, queries, codes
+    uint32_t sent[MAX_SLOTS], sent_q, sent_raw[2];
     uint32_t tslot;
     int abort;
     float half[2][128];   // QT = 1: the warpgroups' maxima, then sums
 };
 static_assert(sizeof(Shared) <= 2048, "static and dynamic shared memory in 227 KB");
+// Announces `bytes` of TMA at a barrier, whose phase they complete.
+__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t &sent, uint32_t phase, int bytes) {
+    sent = 1 + phase;
+    mbar_expect_tx(bar, bytes);
+}
+// Waits until what TMA was last told to write is written.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t sent) {
+    if (sent) mbar_drain(bar, sent - 1);
+}
 
 // Sizes of a call, the same in every role.
 struct Shape {
@@ -319,9 +331,8 @@ struct Producer {
     // one after lets the first announce. e4m3: every warp waits and arrives for
     // itself.
     bool met;
-    uint32_t items, sent, sent_phase;   // items so far; slots this warp's boxes went to last, a bit each, and the phases
+    uint32_t items;       // items so far
     uint32_t qp;          // phase of q_free
-    bool q_sent;
     __device__ __forceinline__ bool master() const { return wid == 0; }
     __device__ __forceinline__ void sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * PR_WARPS) : "memory"); }
     __device__ __forceinline__ bool any_of(bool p) {   // of the producers' threads
@@ -353,14 +364,13 @@ struct Producer {
         if (Q_COPY && mq) {
             const int n = z.nqc * tiles;
             if (master() && (E4 ? ok : met)) {
-                if (lane == 0) mbar_expect_tx(&sh.q_full, 16384 * n);
+                if (lane == 0) expect_tx(&sh.q_full, sh.sent_q, qp, 16384 * n);
                 __syncwarp();
                 if (lane < n) {
                     const int tile = lane / z.nqc, c = lane - tile * z.nqc;
                     tma_3d_at(q0 + 16384 * lane, mq, 64 * c, s.g * a.hpg, s.x.row0 + s.x.vec0 / a.hpg + tile * qrows, &sh.q_full);
                 }
                 __syncwarp();
-                q_sent = true;
             }
             return;
         }
@@ -454,12 +464,10 @@ struct Producer {
                 if ((items++ & (PR_WARPS - 1)) == wid) {
                     wait_for(&sh.empty[put.slot], put.phase ^ 1);
                     if (met) {
-                        if (lane == 0) mbar_expect_tx(full, blocks * rows * 128);
+                        if (lane == 0) expect_tx(full, sh.sent[put.slot], put.phase, blocks * rows * 128);
                         __syncwarp();
                         if (on) tma_2d_at(at, KEYS ? mk : mv, x, y, full);
                         __syncwarp();
-                        sent |= 1u << put.slot;
-                        sent_phase = sent_phase & ~(1u << put.slot) | put.phase << put.slot;
                     }
                 }
                 put.next(z.nslot);
@@ -468,6 +476,7 @@ struct Producer {
             if (master()) wait_for(&sh.empty[put.slot], put.phase ^ 1);
             agree();
             if (!ok) return;
+            if (master() && lane == 0) sh.sent[put.slot] = 0;   // the boxes before were used
             constexpr int U = 4;   // runs in flight
 #pragma unroll 1
             for (int i0 = 0; i0 < runs; i0 += U) {
@@ -546,7 +555,7 @@ struct Producer {
                 const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) >> (key0 / 16) & ((1u << runs) - 1);
                 if (lane == 0) {
                     sh.raw_there[b] = there;
-                    mbar_expect_tx(&sh.raw_full[b], __popc(there) * 16 * (width + 1));
+                    expect_tx(&sh.raw_full[b], sh.sent_raw[b], (n >> 1) & 1, __popc(there) * 16 * (width + 1));
                 }
                 __syncwarp();
                 const C *pool = (const C *)(x.keys ? a.k : a.v);
@@ -562,11 +571,6 @@ struct Producer {
                 ++n;
             } while (next(s, x));
         }
-        if (ok) return;
-        // after a wait that ran out: what is still being copied lands before the block ends
-        if (lane == 0)
-            for (uint32_t i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_drain(&sh.raw_full[i & 1], (i >> 1) & 1);
-        __syncwarp();
     }
     // Four threads cover the 64 columns of a block, and the 8 of a row write their
     // two pieces in opposite orders, so that no bank is hit twice.
@@ -643,10 +647,6 @@ struct Producer {
             queries(s);
             while (ok && next(s, x)) convert(s, x, n++);
         }
-        if (ok) return;
-        // after a wait that ran out: what is still being copied lands before the block ends
-        if (lane == 0 && q_sent) mbar_drain(&sh.q_full, qp);
-        __syncwarp();
     }
 
     __device__ __forceinline__ void run(const PgTable &tab, int units, PgShare share) {
@@ -689,14 +689,6 @@ struct Producer {
                 bx = bx1;
             }
         }
-        if (E4 || (ok && met)) return;
-        // after a wait that ran out: what TMA still writes lands before the block ends
-        if (lane == 0) {
-            if (q_sent) mbar_drain(&sh.q_full, qp);
-            for (int i = 0; i < z.nslot; ++i)
-                if (sent >> i & 1) mbar_drain(&sh.full[i], sent_phase >> i & 1);
-        }
-        __syncwarp();
     }
 };
 
@@ -1286,6 +1278,8 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
         }
         mbar_init(&sh.fin, QT);
         for (int i = 0; i < 8; ++i) mbar_init(&sh.turn[i >> 2][i & 3], 1);
+        for (int i = 0; i < MAX_SLOTS; ++i) sh.sent[i] = 0;
+        sh.sent_q = sh.sent_raw[0] = sh.sent_raw[1] = 0;
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1303,7 +1297,7 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     } else {
         const int w = warp - SM_WARPS;   // the producers', then the issuers'
         Producer<T, C, QT> p = {a, sh, z, q0, ring0, lane, 4 * w + (lane >> 3), lane & 7, qrows ? &mq : nullptr, &mk, &mv, qrows,
-                                w, {0, 0}, true, true, 0, 0, 0, 1, false, q0 + z.raw};
+                                w, {0, 0}, true, true, 0, 1, q0 + z.raw};
         if (w < PR_WARPS) {
             regs_less<R::PRODUCER>();
             p.run(tab, units, share);
@@ -1322,7 +1316,15 @@ __global__ __launch_bounds__(THREADS, 1) void k_pg_tc(PgArgs a, const __grid_con
     __syncthreads();
     tc_after();
     if (warp == SM_WARPS + PR_WARPS) tmem_free512(tmem);
-    if (tid == 0 && sh.abort) atomicOr(&pg_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
+    // Where no wait ran out, the issuers met all that was sent. Where one did, what
+    // TMA still writes lands before the block ends, whichever role's wait it was:
+    // the senders' own may all have been met.
+    if (tid == 0 && sh.abort) {
+        for (int i = 0; i < MAX_SLOTS; ++i) drain(&sh.full[i], sh.sent[i]);
+        drain(&sh.q_full, sh.sent_q);
+        for (int i = 0; i < 2; ++i) drain(&sh.raw_full[i], sh.sent_raw[i]);
+        atomicOr(&pg_device_flags, (uint32_t)O1_FLAG_WAIT_EXPIRED);
+    }
 }
 
 template <typename M>

@@ -674,3 +674,33 @@ def test_expired_waits_leave_nan_or_right_values(o1, dt, ct, d):
     attend(o1, cache, q, seqs, out)
     check(o1, cache, q, seqs, out, "after expiry")
     assert o1.o1_pg_flags() == 0
+
+
+@pytest.mark.parametrize("dt,ct,d", [(BF16, BF16, 128), (F16, F16, 256), (BF16, E4, 128), (F32, E4, 64), (F32, BF16, 64)])
+def test_calls_behind_expired_waits_are_right(o1, dt, ct, d):
+    """Blocks whose waits ran out at once, with their first copies on the way and no
+    wait of the senders among them, keep their shared memory until the copies have
+    landed: calls directly behind them, whose blocks take that memory, are right,
+    and the same bit for bit."""
+    g = o1.pg_geom(2, 4, d, d, 64, dtype=dt, cache_dtype=ct)
+    seqs = [(0, 256, 0, 640), (256, 64, 1, 64)]
+    cache = Cache(o1, g, [896, 128], 29)
+    q = randn(torch.Generator().manual_seed(14), 320, 8, d, dtype=dt)
+    scratch = torch.empty(o1.o1_pg_scratch_bytes(g, 320), dtype=torch.uint8, device="cuda")
+    slots, pos = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([895, 127], device="cuda")
+    lost = torch.empty(320, 8, d, dtype=dt, device="cuda")
+    outs = [torch.full((322, 8, d), NAN, dtype=dt, device="cuda") for _ in range(24)]
+    o1.o1_pg_flags(clear=True)
+    for out in outs:
+        try:
+            o1.o1_set_wait_limit(1)
+            o1.check(o1.o1_pg_chunk_attend(g, cache.c, scratch, q, seqs, lost), "expired")
+        finally:
+            o1.o1_set_wait_limit(0)
+        o1.check(o1.o1_pg_token_attend(g, cache.c, scratch, q[255:320:64], slots, pos, out[320:]), "token")
+        o1.check(o1.o1_pg_chunk_attend(g, cache.c, scratch, q, seqs, out[:320]), "chunk")
+    assert o1.o1_pg_flags(clear=True) == o1.O1_FLAG_WAIT_EXPIRED
+    check(o1, cache, q, seqs, outs[0][:320], "chunk behind expired waits")
+    check(o1, cache, q[255:320:64], [(0, 1, 0, 895), (1, 1, 1, 127)], outs[0][320:], "rows behind expired waits")
+    for out in outs[1:]:
+        assert torch.equal(out.view(torch.uint8), outs[0].view(torch.uint8)), "results differ from call to call"
