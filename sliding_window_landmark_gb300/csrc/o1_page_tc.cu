@@ -658,11 +658,16 @@ struct Producer {
         while (ok && pg_next<Plan<QT>>(a, tab, units, share, s)) {
             // a tile of a 16-bit cache comes in boxes where some row of the
             // sequence attends every position of it (outside, memory may hold
-            // anything); the warps decide together, whatever each read of the table
+            // anything); the warps decide together, whatever each read of the table.
+            // Once a wait of any of them ran out no tile does, and its copies' wait
+            // says so to all: a warp that went on alone would come to a slot
+            // another one skipped, whose phases are then one behind and look free
+            // (three slots and four warps: the next look at a slot is another
+            // warp's, with no wait of its own between).
             auto boxes = [&](int j, int id) -> bool {
                 if (E4 || j >= s.t1) return false;
                 const int x0 = (s.x.lo / KT + j) * KT;
-                return !any_of(!(x0 >= s.x.first && x0 + KT - 1 <= s.x.last && __all_sync(0xffffffffu, id >= 0)));
+                return !any_of(!(met && x0 >= s.x.first && x0 + KT - 1 <= s.x.last && __all_sync(0xffffffffu, id >= 0)));
             };
             // in the MMA issuer's order: QT = 1 runs a tile's scores ahead
             auto keys = [&](int j, int id, bool bx) {

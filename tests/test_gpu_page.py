@@ -704,3 +704,51 @@ def test_calls_behind_expired_waits_are_right(o1, dt, ct, d):
     check(o1, cache, q[255:320:64], [(0, 1, 0, 895), (1, 1, 1, 127)], outs[0][320:], "rows behind expired waits")
     for out in outs[1:]:
         assert torch.equal(out.view(torch.uint8), outs[0].view(torch.uint8)), "results differ from call to call"
+
+
+@pytest.mark.parametrize("dt,ct,d", [(BF16, BF16, 128), (F16, F16, 256), (F32, BF16, 128), (F32, BF16, 64), (BF16, E4, 128), (F16, E4, 256)])
+def test_expired_waits_in_long_shares(o1, dt, ct, d):
+    """Waits that run out late: blocks of several units and many tiles, most of them
+    whole (boxes), of one and of two query tiles, whose rings are around more than
+    once. Every value is NaN or right, a call without the flag is right, and every
+    call ends soon: a block that waited for a phase that does not come would take
+    4e9 cycles, 1.9 s at the highest clock, where a call takes less than a millisecond."""
+    import time
+    g = o1.pg_geom(2, 4, d, d, 64, dtype=dt, cache_dtype=ct)
+    rows = [(64, 32, 300)[i % 3] for i in range(60)]
+    ends = [(1024, 896, 1280)[i % 3] + (i % 7 == 0) * 5 for i in range(60)]
+    seqs, at = [], 0
+    for i, (n, end) in enumerate(zip(rows, ends)):
+        seqs.append((at, n, i, end - n))
+        at += n
+    cache = Cache(o1, g, ends, 31)
+    q = randn(torch.Generator().manual_seed(15), at, 8, d, dtype=dt)
+    k, v = cache.held()
+    want, bound = ref.attend(q, k, v, cache.table, 64, cache.n, seqs, g.scale, 0, dt, *ref.precision(dt, ct), v_exp=cache.ve)
+    out = torch.full((at, 8, d), NAN, dtype=dt, device="cuda")
+    scratch = attend(o1, cache, q, seqs, out)
+    ref.assert_within(out, want.cpu(), bound.cpu(), "without limits")
+    assert o1.o1_pg_flags(clear=True) == 0
+    raised = []
+    for limit in (1, 500, 1000, 1500, 2000, 2500, 3000, 3500, 4000, 5000, 6000, 8000, 12000, 20000, 40000):
+        for _ in range(3):
+            out.fill_(77.0)
+            torch.cuda.synchronize()
+            start = time.perf_counter()
+            try:
+                o1.o1_set_wait_limit(limit)
+                o1.check(o1.o1_pg_chunk_attend(g, cache.c, scratch, q, seqs, out), "chunk")
+            finally:
+                o1.o1_set_wait_limit(0)
+            flags = o1.o1_pg_flags(clear=True)
+            took = time.perf_counter() - start
+            assert took < 0.5, f"limit {limit}: {took} s"
+            bad = ~torch.isnan(out) & ((out.double() - want).abs() > bound)
+            assert not bad.any(), f"limit {limit}: {int(bad.sum())} values neither NaN nor right"
+            assert flags or torch.isfinite(out).all()
+            raised.append((limit, flags, float(torch.isnan(out).double().mean())))
+    assert any(f == o1.O1_FLAG_WAIT_EXPIRED for _, f, _ in raised)
+    print("limit, flags and part of NaN:", raised)
+    attend(o1, cache, q, seqs, out)
+    ref.assert_within(out, want.cpu(), bound.cpu(), "after expiry")
+    assert o1.o1_pg_flags() == 0
