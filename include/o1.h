@@ -605,9 +605,14 @@ O1_API size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows);
  * products run on the tensor cores with the cached values as they are; of the
  * other operand, q is exact (16-bit rows over e4m3: to 2^-25 of its largest
  * value), and the softmax's weights are rounded to 2^-8 (bf16 rows), 2^-11 (fp16
- * rows) or 2^-24 (fp32 rows) of their value. Calls that
- * may overlap on the GPU (other streams, captured graphs) need a scratch each.
- * Asynchronous. */
+ * rows) or 2^-24 (fp32 rows) of their value. Some are held in fp16: those of fp16
+ * rows over fp16, and of 16-bit rows over e4m3 in token batches and in calls whose
+ * sequences all have rows * heads_per_group <= 16 (2^-11, of bf16 rows too). These
+ * are off by up to 2^-32 of the row's largest weight where that is more; over e4m3,
+ * where a weight is held times its value's power of two, of the largest such
+ * product.
+ * Calls that may overlap on the GPU (other streams, captured graphs) need a
+ * scratch each. Asynchronous. */
 O1_API int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
                               const void *q, int64_t q_stride, const o1_pg_seq *seqs, int32_t n_seq, void *out,
                               int64_t out_stride, int32_t total_rows, void *stream);

@@ -231,6 +231,15 @@ __device__ __forceinline__ size_t pg_vec_at(const PgArgs &a, int row0, int vec, 
     return (size_t)(row0 + r) * stride + (size_t)h * width;
 }
 
+// A softmax's weights are taken from a reference, which moves to `below` under the
+// row's maximum where that passes it by more than `above` (log2 units). Of weights
+// held in fp16 a row's largest is at least 2^7 and at most 2^15: they have their
+// 11 bits down to 2^-21 of the largest, and are off by 2^-32 of it below.
+struct PgReference {
+    float above, below;
+    constexpr explicit PgReference(bool f16) : above(f16 ? 15.f : 8.f), below(f16 ? 7.f : 0.f) {}
+};
+
 // Launches over the rows of a token batch (tab null) or the sequences of a
 // table, counted in units of the launched kernel's vectors.
 // o1_page_rows.cu: few query vectors a group, any geometry.

@@ -41,8 +41,8 @@ struct Plan {
 };
 
 // Rows of type T over a cache of type C: the MMA's type M, and the terms that q
-// and the weights are split into (a weight in [0, 2^8]): 16-bit rows over their
-// own type need one, fp32 rows three, which hold fp32.
+// and the weights are split into (a weight at most 2^8, in fp16 2^15): 16-bit rows
+// over their own type need one, fp32 rows three, which hold fp32.
 // 16-bit rows over e4m3 run in fp16, which holds the codes: a pair of codes is
 // one conversion (bf16 takes four). fp16's short range is met by powers of two:
 // a query vector is taken times the one that brings its largest value into [1,
@@ -182,6 +182,8 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     constexpr int CB = Z::CB, VL = Z::VL, KB = Z::KB, VB = Z::VB, STEPS = Z::STEPS, RING = Z::RING, ITEM = Z::ITEM;
     constexpr bool E4 = CB == 1;
     constexpr bool Q_REGS = TERMS == 1 && N <= 2;   // the queries in registers
+    // of the sum's weights, and of the values' (the same ones unless CODES)
+    constexpr PgReference REF(std::is_same<M, __half>::value && !CODES), REF_V(std::is_same<M, __half>::value);
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ long long s_share[RW + 2];
     __shared__ float s_m[RW][RV], s_l[RW][RV];
@@ -432,7 +434,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             }
             done();
             issue_at((RING - 1) % 2 == 1);
-            // ---- softmax: a reference within 2^8 of the running maximum
+            // ---- softmax: a reference near the running maximum
             float top[2], topv[2], sv[2][4];
             if (CODES) {   // score and the value's power of two together (-inf stays)
 #pragma unroll
@@ -452,16 +454,16 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
                     topv[h] = fmaxf(topv[h], __shfl_xor_sync(0xffffffffu, topv[h], 2));
                 }
             }
-            if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f ||
-                                            (CODES && (topv[0] > mv[0] + 8.f || topv[1] > mv[1] + 8.f)))) {
+            if (__any_sync(0xffffffffu, top[0] > m[0] + REF.above || top[1] > m[1] + REF.above ||
+                                            (CODES && (topv[0] > mv[0] + REF_V.above || topv[1] > mv[1] + REF_V.above)))) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float mn = fmaxf(m[h], top[h]), r = m[h] > -INFINITY ? ex2(m[h] - mn) : 0.f;
+                    const float mn = fmaxf(m[h], top[h] - REF.below), r = m[h] > -INFINITY ? ex2(m[h] - mn) : 0.f;
                     m[h] = mn;
                     l[h] *= r;
                     float rv = r;
                     if (CODES) {
-                        const float mvn = fmaxf(mv[h], topv[h]);
+                        const float mvn = fmaxf(mv[h], topv[h] - REF_V.below);
                         rv = mv[h] > -INFINITY ? ex2(mv[h] - mvn) : 0.f;
                         mv[h] = mvn;
                     }

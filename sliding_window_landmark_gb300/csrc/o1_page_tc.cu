@@ -2,8 +2,8 @@
 // (tcgen05, accumulators in TMEM). The query heads of a group share its keys, so
 // a tile is 128 query vectors (rows times heads of the group) against 128 keys:
 //   S = Q K^T, P = e^{S - m}, O += P V
-// with a running reference m a row within 2^8 of the row's maximum (O is
-// rescaled only when the maximum passes it), P written over S in TMEM.
+// with a running reference m a row near the row's maximum (O is rescaled only when
+// the maximum passes it by 2^8; see PgReference), P written over S in TMEM.
 //
 // A block takes segments of units (o1_page.cuh), one block an SM:
 //   warps 0-7   softmax: a thread a row; two query tiles (QT = 2: rows of up to
@@ -57,7 +57,6 @@ constexpr int SM_WARPS = 8, PR_WARPS = 4;      // softmax and producer warps
 constexpr int THREADS = 32 * (SM_WARPS + PR_WARPS + 4), SM_THREADS = 32 * SM_WARPS;
 constexpr int SLOT = 32768, MAX_SLOTS = 6;
 constexpr int BLOCKS = 152;
-constexpr float HEADROOM = 8.f;                // log2 units above the reference before it moves
 constexpr size_t SMEM = 225 * 1024;            // dynamic; static parts beside it
 
 // A segment costs about two tiles beside its own (8192 bf16 rows: 306 us with
@@ -963,6 +962,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
     using M = typename Types<T, C>::M;
     constexpr int TERMS = Types<T, C>::TERMS;
     constexpr bool REG = TERMS == 3;   // sums in registers
+    constexpr PgReference REF(std::is_same<M, __half>::value);
     using Col = Cols<TERMS>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -1105,7 +1105,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                     }
                     // QT = 1: the two halves of a row decide together, also to give
                     // up (a barrier that one of them left would never be met)
-                    bool move = top > m + HEADROOM;
+                    bool move = top > m + REF.above;
                     if (QT == 2) move = __any_sync(0xffffffffu, move);
                     else move = sm_or(move || !ok);
                     if (!move) break;
@@ -1115,7 +1115,7 @@ __device__ __forceinline__ void softmax(const PgArgs &a, Shared &sh, const Shape
                         if (!ok) break;
                         top = fmaxf(top, sh.half[wg ^ 1][row]);
                     }
-                    const float mn = fmaxf(m, top), f = m > -INFINITY ? ex2(m - mn) : 0.f;
+                    const float mn = fmaxf(m, top - REF.below), f = m > -INFINITY ? ex2(m - mn) : 0.f;
                     m = mn;
                     l *= f;
                     if (REG) {

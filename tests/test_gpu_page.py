@@ -752,3 +752,42 @@ def test_expired_waits_in_long_shares(o1, dt, ct, d):
     attend(o1, cache, q, seqs, out)
     ref.assert_within(out, want.cpu(), bound.cpu(), "after expiry")
     assert o1.o1_pg_flags() == 0
+
+
+@pytest.mark.parametrize("dt,ct,d,rows", [(F16, F16, 64, 1), (F16, F16, 128, 64), (F16, F16, 256, 40), (F16, F16, 256, 2), (BF16, E4, 64, 1),
+                                          (F16, E4, 128, 1), (BF16, E4, 256, 2), (F16, E4, 64, 64), (BF16, E4, 128, 64)])
+def test_small_weights_under_a_large_one(o1, dt, ct, d, rows):
+    """The output is the sum of a thousand small weights beside one large one that
+    adds nothing to it: a key 15.3 above the others in score (weights of 2^-22 of
+    the largest) whose value is 0, or, over e4m3, a value row 2^24 times as large
+    whose other columns are 0. Weights held in fp16 may be off by 2^-11 of their
+    value and 2^-32 of the largest (over e4m3, of weights times their values' powers
+    of two), as the header states; the reference's bound counts 2^-25 for the latter,
+    so that its part is taken 2^-7 times."""
+    G, hpg, page, past = 2, 4, 64, 1000
+    g = o1.pg_geom(G, hpg, d, d, page, dtype=dt, cache_dtype=ct)
+    n = past + rows
+    cache = Cache(o1, g, [n], 33, fill=False)
+    gen = torch.Generator().manual_seed(16)
+    q = randn(gen, rows, G * hpg, d) * 0.25
+    k = randn(gen, n, G, d) * 0.05
+    v = 500 + 500 * torch.rand(n, G, d, generator=gen).cuda()
+    q[..., 0], k[..., 0] = 4.0, 0.0
+    if ct is E4:
+        v *= 2.0 ** -19                      # under 2^-17, the large row under 2^7
+        k[3, :, 0], v[3] = 0.065 * d ** 0.5, 0.0
+        v[3, :, 5] = 440 * 2.0 ** 7
+    else:
+        k[3, :, 0], v[3] = 15.3 / 4 * d ** 0.5, 0.0
+    q, k, v = (x.to(dt) for x in (q, k, v))
+    o1.check(o1.o1_pg_write(g, cache.c, k, v, [(0, n, 0, 0)]), "write")
+    seqs = [(0, rows, 0, past)]
+    out = torch.full((rows, G * hpg, d), NAN, dtype=dt, device="cuda")
+    attend(o1, cache, q, seqs, out)
+    terms, rho, f16 = ref.precision(dt, ct)
+    if f16 and rows * hpg <= 16:
+        rho = 2.0 ** -11                     # few rows over e4m3: fp16 for bf16 rows too
+    args = (q, *cache.held(), cache.table, page, cache.n, seqs, g.scale, 0, dt, terms, rho)
+    want, bound = ref.attend(*args, False, cache.ve)
+    coarse = ref.attend(*args, True, cache.ve)[1]
+    ref.assert_within(out, want.cpu(), (bound + 2.0 ** -7 * (coarse - bound)).cpu(), "small weights")
