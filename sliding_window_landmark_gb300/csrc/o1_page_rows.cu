@@ -81,8 +81,16 @@ struct Sizes {
     static constexpr int VB = (N * CB + 1) / 2;          // 128-byte blocks of a value row
     static constexpr int STEPS = N * 4;                  // k16 steps of a key
     static constexpr int ITEM = (2 * KB > 4 * VB ? 2 * KB : 4 * VB) * 512;
-    // items of a warp's ring: what two blocks an SM hold beside the queries
-    static constexpr int RING = N == 4 ? (CB == 2 ? 3 : 6) : N == 2 && CB == 2 ? 6 : 8;
+    static constexpr int QUERIES = TERMS * STEPS * 512;  // bytes of the queries
+    // items of a warp's ring: what PER_SM blocks an SM hold beside the queries (wide
+    // fp32 rows over 16 bits: one in use and one in flight; 64 rows of 2 groups of 4
+    // heads of 256 at 8191 took 177 us, and 299 with three items and one block an SM;
+    // over e4m3 194 with five, 294 with six and one block)
+    static constexpr int RING = N == 4 ? (CB == 2 ? (TERMS == 3 ? 2 : 3) : TERMS == 3 ? 5 : 6) : N == 2 && CB == 2 ? 6 : 8;
+    static constexpr int RESULTS = RV * (64 * N + 4) * 4;   // a warp's, in its ring
+    static constexpr int WARP = RING * ITEM > RESULTS ? RING * ITEM : RESULTS, SMEM = RW * WARP + QUERIES;
+    // beside it: the block's static part, and what the SM keeps for itself a block
+    static_assert(PER_SM * (SMEM + 768 + (CB == 1 ? RW * RING * 32 : 0) + 1024) <= 228 * 1024, "one wave of blocks");
 };
 
 __device__ __forceinline__ uint32_t pack_m(const __nv_bfloat16 *, float a, float b) {
@@ -190,9 +198,9 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
     __shared__ int s_qe[RV];
     __shared__ __align__(16) uint8_t s_exp[E4 ? RW * RING * 32 : 16];   // of an item of keys: theirs, then the values'
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qd = lane & 3, row = lane >> 2;
-    unsigned char *ring = sm + (size_t)warp * RING * ITEM;
+    unsigned char *ring = sm + (size_t)warp * Z::WARP;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    uint32_t *sq = (uint32_t *)(sm + (size_t)RW * RING * ITEM);   // [term][step][lane][4]
+    uint32_t *sq = (uint32_t *)(sm + (size_t)RW * Z::WARP);   // [term][step][lane][4]
 
     PgShare share = pg_share<Plan, RT>(a, tab, units, s_share);
     const PgParts parts = pg_parts(a.part, BLOCKS, RV);
@@ -579,7 +587,7 @@ __global__ __launch_bounds__(RT, PER_SM) void k_pg_rows(PgArgs a, const __grid_c
             float sum = 0.f, mx = -INFINITY;
             for (int w = 0; w < RW; ++w) mx = fmaxf(mx, s_m[w][v]);
             for (int w = 0; w < RW; ++w) {
-                const float4 y = *(const float4 *)((const float *)(sm + (size_t)w * RING * ITEM) + v * ld + c);
+                const float4 y = *(const float4 *)((const float *)(sm + (size_t)w * Z::WARP) + v * ld + c);
                 o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
                 sum += s_m[w][v] > -INFINITY ? s_l[w][v] * ex2(s_m[w][v] - mx) : 0.f;
             }
@@ -691,22 +699,19 @@ void join_launch(const PgArgs &a, int blocks, int vecs, int most, cudaStream_t s
 
 template <typename T, typename C, int N>
 cudaError_t rows_launch_n(const PgArgs &a, const PgTable *tab, int units, cudaStream_t st) {
-    constexpr int TERMS = Types<T, C>::TERMS;
-    using Z = Sizes<C, N, TERMS>;
-    const size_t smem = (size_t)RW * Z::RING * Z::ITEM + (size_t)TERMS * Z::STEPS * 512;
-    static_assert((size_t)Z::RING * Z::ITEM >= RV * (64 * N + 4) * 4, "a warp's results in its ring");
+    using Z = Sizes<C, N, Types<T, C>::TERMS>;
     static_assert(sizeof(PgHead) == 32, "headers of 8 words");
     static unsigned long long done = 0;
     unsigned long long bit = 0;
     auto *k = k_pg_rows<T, C, N>;
     if (o1_attrs_needed(&done, &bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
         if (e != cudaSuccess) return e;
         o1_attrs_done(&done, bit);
     }
     PgTable none;
     none.n = 0;
-    k<<<BLOCKS, RT, smem, st>>>(a, tab ? *tab : none, units);
+    k<<<BLOCKS, RT, Z::SMEM, st>>>(a, tab ? *tab : none, units);
     return cudaGetLastError();
 }
 template <typename T, typename C>
