@@ -623,7 +623,8 @@ O1_API int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, 
  * step can be replayed as the sequences grow. A row whose slot or position is
  * out of range is padding: its output is left as it was. A slot may be named by
  * several rows (draft rows at successive positions). At most 65536 rows. The
- * keys of all rows are split evenly over the GPU. Two launches; asynchronous. */
+ * keys of all rows are split evenly over the GPU. Two launches at most;
+ * asynchronous. */
 O1_API int o1_pg_token_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,
                               const void *q, int64_t q_stride, const int32_t *slots, const int64_t *pos, void *out,
                               int64_t out_stride, int32_t rows, void *stream);

@@ -247,8 +247,8 @@ constexpr int PG_ROWS_V = 16;
 cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, cudaStream_t st);
 size_t pg_rows_scratch(int dv);
 // The partial results of a launch of `blocks` blocks, joined (chained behind it):
-// laid out for `vecs` vectors, of which a unit has `most` at most.
-cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, int most, cudaStream_t st);
+// laid out for `room` blocks and `vecs` vectors, of which a unit has `most` at most.
+cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int room, int vecs, int most, cudaStream_t st);
 // o1_page_tc.cu: many query vectors, on tcgen05. pg_tc_vectors: a unit's, 0
 // where it does not take the geometry.
 int pg_tc_vectors(const o1_pg_geom &g);

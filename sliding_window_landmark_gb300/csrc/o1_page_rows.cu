@@ -648,12 +648,12 @@ __device__ __forceinline__ Sum join_parts(const PgParts &parts, int border, int 
 // Few vectors, maybe many parts: a vector a block, TPV threads its columns, the
 // parts dealt to JOIN / TPV groups of them.
 template <typename T, int TPV>
-__global__ __launch_bounds__(JOIN) void k_pg_join_few(PgArgs a, int blocks, int vecs) {
+__global__ __launch_bounds__(JOIN) void k_pg_join_few(PgArgs a, int room, int vecs) {
     constexpr int GROUPS = JOIN / TPV;
     __shared__ Sum part[JOIN];
     o1_chain_wait();
     const int border = blockIdx.x + 1, grp = threadIdx.x / TPV, c = 4 * (threadIdx.x % TPV), v = blockIdx.y;
-    const PgParts parts = pg_parts(a.part, blocks, vecs);
+    const PgParts parts = pg_parts(a.part, room, vecs);
     const PgHead h = parts.head[border];
     if (h.last < 0 || v >= h.nv) return;
     Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -673,12 +673,12 @@ __global__ __launch_bounds__(JOIN) void k_pg_join_few(PgArgs a, int blocks, int 
 // 64 bf16 rows behind 16000, 4 groups of 4 heads of 128, 53 us; 35 with 32 columns,
 // 33 with 16, 37 with 8.)
 template <typename T>
-__global__ __launch_bounds__(JOIN_MANY) void k_pg_join(PgArgs a, int blocks, int vecs) {
+__global__ __launch_bounds__(JOIN_MANY) void k_pg_join(PgArgs a, int room, int vecs) {
     constexpr int W = JOIN_MANY / 32;
     __shared__ float4 rows[32][W + 1];
     o1_chain_wait();
     const int border = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, v0 = 32 * blockIdx.y, v = v0 + lane;
-    const PgParts parts = pg_parts(a.part, blocks, vecs);
+    const PgParts parts = pg_parts(a.part, room, vecs);
     const PgHead h = parts.head[border];
     if (h.last < 0 || v0 >= h.nv) return;
     const int r = threadIdx.x / W, k = threadIdx.x % W;
@@ -689,16 +689,16 @@ __global__ __launch_bounds__(JOIN_MANY) void k_pg_join(PgArgs a, int blocks, int
         o1_st4((T *)a.out + pg_vec_at(a, h.row0, h.vec0 + v0 + r, h.g, a.os, a.dv) + c0 + 4 * k, rows[r][k]);
 }
 template <typename T>
-void join_launch(const PgArgs &a, int blocks, int vecs, int most, cudaStream_t st) {
+void join_launch(const PgArgs &a, int blocks, int room, int vecs, int most, cudaStream_t st) {
     const dim3 few(blocks - 1, most), many(blocks - 1, (vecs + 31) / 32, (a.dv + JOIN_MANY / 8 - 1) / (JOIN_MANY / 8));
-    if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN_MANY), 0, st, a, blocks, vecs);
-    else if (a.dv <= 64) o1_launch_chained(true, k_pg_join_few<T, 16>, few, dim3(JOIN), 0, st, a, blocks, vecs);
-    else if (a.dv <= 128) o1_launch_chained(true, k_pg_join_few<T, 32>, few, dim3(JOIN), 0, st, a, blocks, vecs);
-    else o1_launch_chained(true, k_pg_join_few<T, 64>, few, dim3(JOIN), 0, st, a, blocks, vecs);
+    if (vecs > PG_ROWS_V) o1_launch_chained(true, k_pg_join<T>, many, dim3(JOIN_MANY), 0, st, a, room, vecs);
+    else if (a.dv <= 64) o1_launch_chained(true, k_pg_join_few<T, 16>, few, dim3(JOIN), 0, st, a, room, vecs);
+    else if (a.dv <= 128) o1_launch_chained(true, k_pg_join_few<T, 32>, few, dim3(JOIN), 0, st, a, room, vecs);
+    else o1_launch_chained(true, k_pg_join_few<T, 64>, few, dim3(JOIN), 0, st, a, room, vecs);
 }
 
 template <typename T, typename C, int N>
-cudaError_t rows_launch_n(const PgArgs &a, const PgTable *tab, int units, cudaStream_t st) {
+cudaError_t rows_launch_n(const PgArgs &a, int dtype, const PgTable *tab, int units, int most, int64_t cost, cudaStream_t st) {
     using Z = Sizes<C, N, Types<T, C>::TERMS>;
     static_assert(sizeof(PgHead) == 32, "headers of 8 words");
     static unsigned long long done = 0;
@@ -711,39 +711,55 @@ cudaError_t rows_launch_n(const PgArgs &a, const PgTable *tab, int units, cudaSt
     }
     PgTable none;
     none.n = 0;
-    k<<<BLOCKS, RT, Z::SMEM, st>>>(a, tab ? *tab : none, units);
-    return cudaGetLastError();
+    const int blocks = (int)std::min<int64_t>(BLOCKS, std::max<int64_t>(1, cost / Plan::LEAST));
+    k<<<blocks, RT, Z::SMEM, st>>>(a, tab ? *tab : none, units);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess && blocks > 1 ? pg_launch_join(a, dtype, blocks, BLOCKS, RV, most, st) : e;
 }
 template <typename T, typename C>
-cudaError_t rows_launch_c(const PgArgs &a, const PgTable *tab, int units, cudaStream_t st) {
+cudaError_t rows_launch_c(const PgArgs &a, int dtype, const PgTable *tab, int units, int most, int64_t cost, cudaStream_t st) {
     const int w = a.d > a.dv ? a.d : a.dv;
-    if (w <= 64) return rows_launch_n<T, C, 1>(a, tab, units, st);
-    if (w <= 128) return rows_launch_n<T, C, 2>(a, tab, units, st);
-    return rows_launch_n<T, C, 4>(a, tab, units, st);
+    if (w <= 64) return rows_launch_n<T, C, 1>(a, dtype, tab, units, most, cost, st);
+    if (w <= 128) return rows_launch_n<T, C, 2>(a, dtype, tab, units, most, cost, st);
+    return rows_launch_n<T, C, 4>(a, dtype, tab, units, most, cost, st);
 }
 
 }  // namespace
 
 size_t pg_rows_scratch(int dv) { return pg_parts_bytes(BLOCKS, RV, dv); }
 
-cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int vecs, int most, cudaStream_t st) {
-    if (dtype == O1_F32) join_launch<float>(a, blocks, vecs, most, st);
-    else if (dtype == O1_BF16) join_launch<__nv_bfloat16>(a, blocks, vecs, most, st);
-    else join_launch<__half>(a, blocks, vecs, most, st);
+cudaError_t pg_launch_join(const PgArgs &a, int dtype, int blocks, int room, int vecs, int most, cudaStream_t st) {
+    if (dtype == O1_F32) join_launch<float>(a, blocks, room, vecs, most, st);
+    else if (dtype == O1_BF16) join_launch<__nv_bfloat16>(a, blocks, room, vecs, most, st);
+    else join_launch<__half>(a, blocks, room, vecs, most, st);
     return cudaGetLastError();
 }
 
 cudaError_t pg_launch_rows(const PgArgs &a, int dtype, int cache_dtype, const PgTable *tab, cudaStream_t st) {
     const int units = tab ? tab->total : a.rows;
-    cudaError_t e;
-    if (dtype == O1_F32 && cache_dtype == O1_BF16) e = rows_launch_c<float, __nv_bfloat16>(a, tab, units, st);
-    else if (dtype == O1_F32) e = rows_launch_c<float, uint8_t>(a, tab, units, st);
-    else if (dtype == O1_BF16 && cache_dtype == O1_BF16) e = rows_launch_c<__nv_bfloat16, __nv_bfloat16>(a, tab, units, st);
-    else if (dtype == O1_BF16) e = rows_launch_c<__nv_bfloat16, uint8_t>(a, tab, units, st);
-    else if (cache_dtype == O1_F16) e = rows_launch_c<__half, __half>(a, tab, units, st);
-    else e = rows_launch_c<__half, uint8_t>(a, tab, units, st);
-    int most = tab ? 1 : a.hpg;
+    int most = tab ? 1 : a.hpg;   // vectors of a unit
     if (tab)
         for (int i = 0; i < tab->n && most < RV; ++i) most = (int)std::max<int64_t>(most, std::min<int64_t>(RV, (int64_t)tab->s[i].rows * a.hpg));
-    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, RV, most, st) : e;
+    // What the call can cost (pg_share): no more blocks than get a share of it.
+    // (Those without one are not free: one row at 8191 of the heads above, where 133 of
+    // 304 blocks have a share, took 19.7 us with all of them and 18.4 without; over
+    // e4m3 21.7 and 19.2.)
+    auto cost_of = [&](int64_t n, int lo, int hi) { return n * (hi / TILE - lo / TILE + 1 + Plan::START) * a.G; };
+    int64_t cost = 0;
+    if (tab) {
+        for (int i = 0; i < tab->n; ++i) {
+            const PgSeq &s = tab->s[i];
+            cost += cost_of((i + 1 < tab->n ? tab->s[i + 1].before : tab->total) - s.before, a.window ? std::max(0, s.pos0 - a.window + 1) : 0,
+                            s.pos0 + s.rows - 1);
+        }
+    } else {
+        const int64_t len = (int64_t)a.width << a.lpage;   // the window anywhere in it: a tile more
+        cost = cost_of(units, 0, (int)std::min<int64_t>(len - 1, a.window ? (int64_t)a.window - 1 + TILE : len - 1));
+    }
+    if (dtype == O1_F32 && cache_dtype == O1_BF16) return rows_launch_c<float, __nv_bfloat16>(a, dtype, tab, units, most, cost, st);
+    if (dtype == O1_F32) return rows_launch_c<float, uint8_t>(a, dtype, tab, units, most, cost, st);
+    if (dtype == O1_BF16 && cache_dtype == O1_BF16) return rows_launch_c<__nv_bfloat16, __nv_bfloat16>(a, dtype, tab, units, most, cost, st);
+    if (dtype == O1_BF16) return rows_launch_c<__nv_bfloat16, uint8_t>(a, dtype, tab, units, most, cost, st);
+    if (cache_dtype == O1_F16) return rows_launch_c<__half, __half>(a, dtype, tab, units, most, cost, st);
+    return rows_launch_c<__half, uint8_t>(a, dtype, tab, units, most, cost, st);
 }

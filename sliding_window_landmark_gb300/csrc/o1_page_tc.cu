@@ -1382,7 +1382,7 @@ cudaError_t launch_q(const PgArgs &a, int dtype, const PgTable &tab, int64_t vec
         }
     k<<<BLOCKS, THREADS, SMEM, st>>>(a, tab, mq, mk, mv, qrows, tab.total, vecs);
     const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, vecs, vecs, st) : e;
+    return e == cudaSuccess ? pg_launch_join(a, dtype, BLOCKS, BLOCKS, vecs, vecs, st) : e;
 }
 // Two query tiles a block where both fit beside a ring of five slots: one term
 // and rows of up to 128 values.

@@ -791,3 +791,34 @@ def test_small_weights_under_a_large_one(o1, dt, ct, d, rows):
     want, bound = ref.attend(*args, False, cache.ve)
     coarse = ref.attend(*args, True, cache.ve)[1]
     ref.assert_within(out, want.cpu(), (bound + 2.0 ** -7 * (coarse - bound)).cpu(), "small weights")
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("dt,ct,d", [(F32, BF16, 256), (F32, E4, 256), (BF16, E4, 128), (F16, F16, 64)])
+def test_launches_hold_what_a_table_admits(o1, dt, ct, d, window):
+    """A call launches the blocks that its table's width (or its sequences) can
+    give a share to. The split of the keys depends on the lengths alone, so that a
+    wide table and a narrow one, a chunk of one row and a token give the same bits; a
+    call of one block alone is right."""
+    G, hpg, page = 2, 4, 16
+    g = o1.pg_geom(G, hpg, d, d, page, dtype=dt, cache_dtype=ct, window=window)
+    ends = [1, 64, 65, 400, 799, 800]
+    cache = Cache(o1, g, ends, 35)
+    gen = torch.Generator().manual_seed(17)
+    wide = torch.full((len(ends), 4096), -1, dtype=torch.int32, device="cuda")
+    wide[:, :50] = cache.table[:, :50]
+    tables = {"narrow": wide[:, :50].contiguous(), "wide": wide}
+    for rows in ([0], [3], [5], list(range(6))):
+        q = randn(gen, len(rows), G * hpg, d, dtype=dt)
+        seqs = [(i, 1, s, ends[s] - 1) for i, s in enumerate(rows)]
+        slots = torch.tensor(rows, dtype=torch.int32, device="cuda")
+        pos = torch.tensor([ends[s] - 1 for s in rows], device="cuda")
+        outs = []
+        for table in tables.values():
+            cache.c = o1.pg_cache(g, cache.k, cache.v, table, cache.ke, cache.ve)
+            for token in ((slots, pos), None):
+                outs.append(torch.full((len(rows), G * hpg, d), NAN, dtype=dt, device="cuda"))
+                attend(o1, cache, q, seqs, outs[-1], token=token)
+        check(o1, cache, q, seqs, outs[0], f"rows {rows}")
+        for o in outs[1:]:
+            assert torch.equal(o.view(torch.uint8), outs[0].view(torch.uint8)), f"rows {rows}"
