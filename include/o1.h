@@ -564,8 +564,9 @@ O1_API int o1_pg_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const v
  * position pos[r] (device int64, also o1_head_prep's) of slot slots[r] (device
  * int32; NULL: slot r). A row whose slot or position is out of range is padding
  * and written nowhere. Of rows that name the same position of a slot the first
- * counts (with the slots' look of o1_lin_token_attend). At most 65536 rows. One
- * launch; asynchronous. */
+ * counts (with the slots' look of o1_lin_token_attend: each row is compared with all
+ * before it, work that grows with the square of the rows). At most 65536 rows.
+ * One launch; asynchronous. */
 O1_API int o1_pg_token_write(const o1_pg_geom *geom, const o1_pg_cache *cache, const void *k, int64_t k_stride,
                              const void *v, int64_t v_stride, const int32_t *slots, const int64_t *pos, int32_t rows,
                              void *stream);
@@ -611,6 +612,9 @@ O1_API size_t o1_pg_scratch_bytes(const o1_pg_geom *geom, int32_t rows);
  * are off by up to 2^-32 of the row's largest weight where that is more; over e4m3,
  * where a weight is held times its value's power of two, of the largest such
  * product.
+ * One kernel takes all sequences of a call (where some have rows * heads_per_group
+ * > 16, in tiles of 128 or 256 query vectors), so that single rows of long sequences
+ * beside a prompt's chunk are better attended by a call of their own.
  * Calls that may overlap on the GPU (other streams, captured graphs) need a
  * scratch each. Asynchronous. */
 O1_API int o1_pg_chunk_attend(const o1_pg_geom *geom, const o1_pg_cache *cache, void *scratch, size_t scratch_bytes,

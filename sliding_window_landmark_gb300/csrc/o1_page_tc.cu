@@ -27,7 +27,8 @@
 // warps half a turn apart, which took 9 % less than all at once). 8192 bf16 rows
 // of 4 groups of 4 heads of 128, cache empty before: 256 us, 1070 TFLOP/s. Rows of
 // 256 have twice the products to a weight, and the tensor cores are the bound:
-// 4096 bf16 rows of 2 groups of 4 heads behind 12288: 317 us, 1520 TFLOP/s.
+// 4096 bf16 rows of 2 groups of 4 heads behind 12288: 317 us, 1520 TFLOP/s. (All
+// times here are of replayed graphs; in a loop of calls these two take 256 and 338.)
 // Producers: a slot's wait, its arrival and its copies are a chain of single
 // instructions, and one warp that also formed the addresses there (453 us) was
 // the bound of the latter. (Pairs of blocks that load each key tile once for
@@ -40,7 +41,9 @@
 // the MMA's accumulation truncates, the same way each time.
 //
 // Every wait is bounded; where one runs out the block raises a flag, writes NaN
-// for what is left of its share, and ends once its copies and MMAs are over.
+// for what is left of its share, and ends once its copies and MMAs are over: the
+// issuers wait for their MMAs, one thread at the end for the last copy of each
+// barrier, as recorded where it was sent.
 #include <math.h>
 
 #include <type_traits>
