@@ -661,11 +661,12 @@ struct Producer {
             // a tile of a 16-bit cache comes in boxes where some row of the
             // sequence attends every position of it (outside, memory may hold
             // anything); the warps decide together, whatever each read of the table.
-            // Once a wait of any of them ran out no tile does, and its copies' wait
-            // says so to all: a warp that went on alone would come to a slot
-            // another one skipped, whose phases are then one behind and look free
-            // (three slots and four warps: the next look at a slot is another
-            // warp's, with no wait of its own between).
+            // Once a wait of any of them ran out no tile does, and the copies' vote
+            // on their wait ends the loops of all: none walks the rest of the share,
+            // past slots that another one skipped and whose phases are one behind.
+            // (Such a slot, a ring later, could look free to a warp that had met no
+            // wait between. Rings of 16-bit caches have four slots at least, so
+            // that every warp has a wait of its own between.)
             auto boxes = [&](int j, int id) -> bool {
                 if (E4 || j >= s.t1) return false;
                 const int x0 = (s.x.lo / KT + j) * KT;
